@@ -217,7 +217,8 @@ def _plain_norm(st):
 def _plain_norm_e4m3(s, w, rstd):
     t = s * w
     a = t.abs().amax(dim=1, keepdim=True).clamp_min(TINY)
-    return (t * (E4M3_MAX / a)).to(torch.float8_e4m3fn).float(), ((a / E4M3_MAX) * rstd).squeeze(1)
+    # a division of tensors rounds once; number / tensor would round a reciprocal first
+    return (t * (torch.full_like(a, E4M3_MAX) / a)).to(torch.float8_e4m3fn).float(), ((a / E4M3_MAX) * rstd).squeeze(1)
 
 
 def _run_plain(st):
