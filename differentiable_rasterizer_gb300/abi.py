@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -23,9 +24,14 @@ GS_MAX_VIEWS = 32
 GS_REC_FLOAT4 = 3
 GS_GRAD2D_STRIDE = 12
 
+GS_F32, GS_BF16, GS_F16, GS_E4M3 = range(4)
+GS_ACT_NONE, GS_ACT_RELU, GS_ACT_SILU, GS_ACT_GELU = range(4)
+GS_NORM_MAX_COLS = 16384
+
 EXPORTS = ("gs_project", "gs_bin_sort", "gs_raster_fused_fwd_bwd", "gs_grad_compact", "gs_adam_deferred",
            "gs_raster_forward_state", "gs_dssim_loss_grad", "gs_raster_backward_state", "gs_grad_compact_static",
            "gs_prune_tiles", "gs_split_ranges", "gs_compose", "gs_raster_work_counts", "gs_check_report",
+           "gs_rms_norm", "gs_rms_norm_bwd", "gs_quantize_rows", "gs_linear", "gs_linear_bwd", "gs_glu", "gs_glu_bwd",
            "gs_error_string", "gs_param_rows", "gs_param_stride", "gs_num_tiles", "gs_version")
 
 
@@ -96,6 +102,12 @@ def lib():
         for name in ("gs_project", "gs_bin_sort", "gs_raster_fused_fwd_bwd", "gs_grad_compact", "gs_adam_deferred",
                      "gs_raster_forward_state", "gs_dssim_loss_grad", "gs_raster_backward_state", "gs_prune_tiles",
                      "gs_split_ranges", "gs_compose", "gs_raster_work_counts"):
+            getattr(L, name).restype = ctypes.c_int
+        for name in ("gs_rms_norm", "gs_quantize_rows"):
+            getattr(L, name).argtypes = [ctypes.c_char_p, _P]
+            getattr(L, name).restype = ctypes.c_int
+        for name in ("gs_rms_norm_bwd", "gs_linear", "gs_linear_bwd", "gs_glu", "gs_glu_bwd"):
+            getattr(L, name).argtypes = [ctypes.c_char_p, _P, ctypes.POINTER(ctypes.c_size_t), _P]
             getattr(L, name).restype = ctypes.c_int
         L.gs_check_report.argtypes = [_P, ctypes.POINTER(ctypes.c_int32)]
         L.gs_check_report.restype = ctypes.c_int
@@ -302,3 +314,99 @@ def gs_grad_compact_static(grad2d, touched, params, n, sh_degree, cams, n_views,
         f.restype = ctypes.c_int
     _check("gs_grad_compact_static", f(grad2d, touched, params, n, sh_degree, cams, n_views, ctypes.byref(opts), idx,
                                        n_idx, grads, stream))
+
+
+# Decoder layers.  Each call's arguments are one C struct, packed here in the order of
+# its fields (64-bit sizes and pointers first, 32-bit fields last); pointers are ints, 0
+# for an absent array.
+_RMS_NORM = struct.Struct("=qq Qq Qq Q Qq Q Qq Q fiii")
+_RMS_NORM_BWD = struct.Struct("=qq Qq Qq Q Q Qq Qq Q iiii")
+_QUANTIZE_ROWS = struct.Struct("=qq Qq Qq Q ii")
+_LINEAR = struct.Struct("=qqq Qq Qq QQ Q Qq Qq Qq iiii")
+_LINEAR_BWD = struct.Struct("=qqq Qq Qq Qq Qq Qq Qq Q iiii ii")
+_GLU = struct.Struct("=qqq Qq Qq Qq QQQ Qq Qq Qq iiii")
+_GLU_BWD = struct.Struct("=qqq Qq Qq Qq Qq Qq Qq Qq Qq Qq iiii")
+
+
+def _ws_call(name, packed, ws, ws_bytes, stream):
+    """ws_bytes None: a call that needs no scratch."""
+    f = getattr(_lib or lib(), name)
+    st = f(packed, ws, None if ws_bytes is None else ctypes.byref(ctypes.c_size_t(ws_bytes)), stream)
+    if st != GS_OK:
+        _check(name, st)
+
+
+def _ws_query(name, packed) -> int:
+    sz = ctypes.c_size_t(0)
+    st = getattr(_lib or lib(), name)(packed, None, ctypes.byref(sz), None)
+    if st != GS_OK:
+        _check(name, st)
+    return sz.value
+
+
+def gs_rms_norm(rows, cols, x, ldx, residual, ldr, weight, y, ldy, y_scale, sum_, lds, rstd, eps, type_, weight_type,
+                y_type, stream):
+    _check("gs_rms_norm", lib().gs_rms_norm(
+        _RMS_NORM.pack(rows, cols, x, ldx, residual, ldr, weight, y, ldy, y_scale, sum_, lds, rstd, eps, type_,
+                       weight_type, y_type), stream))
+
+
+def gs_quantize_rows(rows, cols, x, ldx, q, ldq, scale, type_, stream):
+    _check("gs_quantize_rows", lib().gs_quantize_rows(
+        _QUANTIZE_ROWS.pack(rows, cols, x, ldx, q, ldq, scale, type_, 0), stream))
+
+
+def rms_norm_bwd_args(rows, cols, dy, lddy, sum_, lds, weight, rstd, dsum, ldds, dx, lddx, dweight, type_, dy_type,
+                      weight_type) -> bytes:
+    return _RMS_NORM_BWD.pack(rows, cols, dy, lddy, sum_, lds, weight, rstd, dsum, ldds, dx, lddx, dweight, type_,
+                              dy_type, weight_type, 0)
+
+
+def linear_args(rows, in_features, out_features, x, ldx, w, ldw, x_scale, w_scale, bias, residual, ldr, y, ldy, z, ldz,
+                type_, bias_type, out_type, act) -> bytes:
+    return _LINEAR.pack(rows, in_features, out_features, x, ldx, w, ldw, x_scale, w_scale, bias, residual, ldr, y, ldy,
+                        z, ldz, type_, bias_type, out_type, act)
+
+
+def linear_bwd_args(rows, in_features, out_features, dy, lddy, x, ldx, w, ldw, z, ldz, dx, lddx, dw, lddw, db, type_,
+                    dy_type, dw_type, db_type, act) -> bytes:
+    return _LINEAR_BWD.pack(rows, in_features, out_features, dy, lddy, x, ldx, w, ldw, z, ldz, dx, lddx, dw, lddw, db,
+                            type_, dy_type, dw_type, db_type, act, 0)
+
+
+def glu_args(rows, in_features, hidden, x, ldx, w_gate, ldwg, w_up, ldwu, x_scale, gate_scale, up_scale, h, ldh, g, ldg,
+             u, ldu, type_, out_type, act) -> bytes:
+    return _GLU.pack(rows, in_features, hidden, x, ldx, w_gate, ldwg, w_up, ldwu, x_scale, gate_scale, up_scale, h, ldh,
+                     g, ldg, u, ldu, type_, out_type, act, 0)
+
+
+def glu_bwd_args(rows, in_features, hidden, dh, lddh, x, ldx, w_gate, ldwg, w_up, ldwu, g, ldg, u, ldu, dx, lddx,
+                 dw_gate, lddwg, dw_up, lddwu, type_, dw_type, act) -> bytes:
+    return _GLU_BWD.pack(rows, in_features, hidden, dh, lddh, x, ldx, w_gate, ldwg, w_up, ldwu, g, ldg, u, ldu, dx,
+                         lddx, dw_gate, lddwg, dw_up, lddwu, type_, dw_type, act, 0)
+
+
+def gs_rms_norm_bwd(args: bytes, ws, ws_bytes, stream):
+    """args: rms_norm_bwd_args(...); ws: device pointer of ws_bytes, or None and None where none is needed."""
+    _ws_call("gs_rms_norm_bwd", args, ws, ws_bytes, stream)
+
+
+def gs_linear(args: bytes, ws, ws_bytes, stream):
+    _ws_call("gs_linear", args, ws, ws_bytes, stream)
+
+
+def gs_linear_bwd(args: bytes, ws, ws_bytes, stream):
+    _ws_call("gs_linear_bwd", args, ws, ws_bytes, stream)
+
+
+def gs_glu(args: bytes, ws, ws_bytes, stream):
+    _ws_call("gs_glu", args, ws, ws_bytes, stream)
+
+
+def gs_glu_bwd(args: bytes, ws, ws_bytes, stream):
+    _ws_call("gs_glu_bwd", args, ws, ws_bytes, stream)
+
+
+def layer_ws_bytes(name: str, args: bytes) -> int:
+    """Scratch that the named layer call (gs_linear, gs_linear_bwd, ...) needs for these arguments."""
+    return _ws_query(name, args)

@@ -1,0 +1,180 @@
+// layers_common.cuh -- element types, conversions and activations shared by the
+// decoder layers (norm.cu, linear.cu, gemm.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "gs_common.cuh"
+
+namespace gs {
+
+__host__ __device__ constexpr int type_bytes(int t) { return t == GS_F32 ? 4 : (t == GS_E4M3 ? 1 : 2); }
+
+inline bool type_float(int t) { return t == GS_F32 || t == GS_BF16 || t == GS_F16; }
+inline bool type_half(int t) { return t == GS_BF16 || t == GS_F16; }
+inline bool act_ok(int a) { return a >= GS_ACT_NONE && a <= GS_ACT_GELU; }
+
+// A matrix of the given columns and leading dimension: present, wide enough and
+// aligned to its elements.
+inline bool mat_ok(const void* p, int64_t ld, int64_t cols, int type)
+{
+    return p && ld >= cols && ld <= 0x7fffffffll && ((uintptr_t)p % (uintptr_t)type_bytes(type)) == 0;
+}
+inline bool vec_ok(const void* p, int type) { return ((uintptr_t)p % (uintptr_t)type_bytes(type)) == 0; }
+inline bool size_ok(int64_t v, int64_t lo) { return v >= lo && v <= 0x7fffffffll; }
+
+// Rows that 16-byte accesses and tensor copies can take as they lie.
+inline bool rows16(const void* p, int64_t ld, int type)
+{
+    return aligned16(p) && (ld * type_bytes(type)) % 16 == 0;
+}
+
+inline int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+
+// The host-side workspace convention: ws == NULL with ws_bytes reports the size;
+// ws_bytes == NULL runs a call that needs none; otherwise the size must suffice.
+enum class WsCheck { kRun, kQuery, kBad };
+inline WsCheck ws_check(void* ws, size_t* ws_bytes, size_t need)
+{
+    if (!ws_bytes) return need == 0 ? WsCheck::kRun : WsCheck::kBad;
+    if (!ws) {
+        *ws_bytes = need;
+        return WsCheck::kQuery;
+    }
+    return *ws_bytes < need || ((uintptr_t)ws & 255u) ? WsCheck::kBad : WsCheck::kRun;
+}
+
+// ------------------------------------------------------------------ elements
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+
+__device__ __forceinline__ float load_elem(const void* p, int64_t i, int type)
+{
+    if (type == GS_F32) return ((const float*)p)[i];
+    if (type == GS_BF16) return __bfloat162float(((const __nv_bfloat16*)p)[i]);
+    if (type == GS_F16) return __half2float(((const __half*)p)[i]);
+    __nv_fp8_e4m3 q;
+    q.__x = ((const __nv_fp8_storage_t*)p)[i];
+    return (float)q;
+}
+
+// fp32 -> e4m3: nearest even, saturating at 448, NaN kept.
+__device__ __forceinline__ uint8_t e4m3_bits(float v)
+{
+    return (uint8_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+}
+
+__device__ __forceinline__ void store_elem(void* p, int64_t i, int type, float v)
+{
+    if (type == GS_F32) ((float*)p)[i] = v;
+    else if (type == GS_BF16) ((__nv_bfloat16*)p)[i] = __float2bfloat16_rn(v);
+    else if (type == GS_F16) ((__half*)p)[i] = __float2half_rn(v);
+    else ((uint8_t*)p)[i] = e4m3_bits(v);
+}
+
+// Two values in 16 bits each, the first in the low half.
+__device__ __forceinline__ uint32_t pack_half2(float a, float b, int type)
+{
+    if (type == GS_BF16) {
+        __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<uint32_t*>(&h);
+    }
+    __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float2 unpack_half2(uint32_t v, int type)
+{
+    if (type == GS_BF16)   // a bfloat16 is the upper half of the float of the same value
+        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+    return __half22float2(*reinterpret_cast<__half2*>(&v));
+}
+
+// Eight consecutive elements, 16-byte aligned (f32: two accesses).
+__device__ __forceinline__ void load8(const void* p, int64_t i, int type, float v[8])
+{
+    if (type == GS_F32) {
+        const float4 a = *reinterpret_cast<const float4*>((const float*)p + i);
+        const float4 b = *reinterpret_cast<const float4*>((const float*)p + i + 4);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        return;
+    }
+    const uint4 a = *reinterpret_cast<const uint4*>((const uint16_t*)p + i);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack_half2(w[j], type);
+        v[2 * j] = f.x, v[2 * j + 1] = f.y;
+    }
+}
+
+__device__ __forceinline__ void store8(void* p, int64_t i, int type, const float v[8])
+{
+    if (type == GS_F32) {
+        *reinterpret_cast<float4*>((float*)p + i) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>((float*)p + i + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    } else if (type == GS_E4M3) {
+        uint32_t w[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * j], v[4 * j + 1]), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * j + 2], v[4 * j + 3]), __NV_SATFINITE,
+                                                         __NV_E4M3);
+            w[j] = lo | (hi << 16);
+        }
+        *reinterpret_cast<uint2*>((uint8_t*)p + i) = make_uint2(w[0], w[1]);
+    } else {
+        *reinterpret_cast<uint4*>((uint16_t*)p + i) =
+            make_uint4(pack_half2(v[0], v[1], type), pack_half2(v[2], v[3], type), pack_half2(v[4], v[5], type),
+                       pack_half2(v[6], v[7], type));
+    }
+}
+
+// ------------------------------------------------------------------ activations
+// sigma(v) by the hardware exponential: relative error below 2^-20 (two roundings
+// of |v| log2 e and the exponential's 2 ulp), far inside the 16-bit results.
+__device__ __forceinline__ float sigmoid_fast(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
+
+// v sigma(v).  For v below about -88 the exponential overflows to infinity and
+// the quotient is -0, as it should be (__fdividef by infinity gives 0).
+__device__ __forceinline__ float act_value(float v, int act)
+{
+    if (act == GS_ACT_RELU) return v < 0.0f ? 0.0f : v;   // NaN stays NaN
+    if (act == GS_ACT_SILU) return v * sigmoid_fast(v);
+    if (act == GS_ACT_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+    return v;
+}
+
+__device__ __forceinline__ float act_slope(float v, int act)
+{
+    if (act == GS_ACT_RELU) return v > 0.0f ? 1.0f : (v != v ? v : 0.0f);
+    if (act == GS_ACT_SILU) {
+        const float p = sigmoid_fast(v);
+        return p * __fmaf_rn(v, 1.0f - p, 1.0f);
+    }
+    if (act == GS_ACT_GELU)
+        return 0.5f * (1.0f + erff(v * 0.70710678118654752f)) + v * (0.39894228040143268f * __expf(-0.5f * v * v));
+    return 1.0f;
+}
+
+// Both at once, from one sigma (or one erf).
+__device__ __forceinline__ void act_both(float v, int act, float& value, float& slope)
+{
+    if (act == GS_ACT_SILU) {
+        const float p = sigmoid_fast(v);
+        value = v * p;
+        slope = p * __fmaf_rn(v, 1.0f - p, 1.0f);
+    } else if (act == GS_ACT_GELU) {
+        const float c = 0.5f * (1.0f + erff(v * 0.70710678118654752f));
+        value = v * c;
+        slope = c + v * (0.39894228040143268f * __expf(-0.5f * v * v));
+    } else {
+        value = act_value(v, act);
+        slope = act_slope(v, act);
+    }
+}
+
+}  // namespace gs

@@ -1,0 +1,407 @@
+// linear.cu -- entry points of gs_linear, gs_glu and their gradients: argument
+// checks, the elementwise passes in front of the gradients' products, and the
+// fixed-order joins of partial sums.  The products are in gemm.cu.
+#include "gemm.cuh"
+
+namespace gs {
+namespace {
+
+// Gradient in front of the products: dz = dy * act'(z) rounded to the operands'
+// type, and (DB) its column sums unrounded.  HBM bound: every value is read and
+// written once.  A block owns kCols columns and every gridDim.y-th slab of
+// kRows rows; a thread keeps its columns' sums in registers over all its rows,
+// the block joins them in row order and writes one partial row.
+constexpr int kElemThreads = 256;
+
+template <int VEC>
+__device__ __forceinline__ void load_cols(const void* p, int64_t i, int type, float (&v)[VEC])
+{
+    if constexpr (VEC == 8) load8(p, i, type, v);
+    else v[0] = load_elem(p, i, type);
+}
+template <int VEC>
+__device__ __forceinline__ void store_cols(void* p, int64_t i, int type, const float (&v)[VEC])
+{
+    if constexpr (VEC == 8) store8(p, i, type, v);
+    else store_elem(p, i, type, v[0]);
+}
+
+struct DzParams {
+    const void* dy;
+    const void* z;
+    void* dz;         // NULL: column sums only
+    float* partial;   // [gridDim.y][n] or NULL
+    int64_t m, n, lddy, ldz, lddz;
+    int dy_type, type, act;
+};
+
+template <int VEC>
+__global__ void __launch_bounds__(kElemThreads) dz_kernel(const DzParams p, int tx)
+{
+    __shared__ float part[kElemThreads * VEC];
+    const int ty = kElemThreads / tx;                 // rows a block takes at a time
+    const int x = threadIdx.x % tx, y = threadIdx.x / tx;
+    const int64_t col = ((int64_t)blockIdx.x * tx + x) * VEC;
+    float sum[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) sum[e] = 0.0f;
+    if (col < p.n) {
+        const int64_t step = (int64_t)gridDim.y * ty;
+#pragma unroll 2
+        for (int64_t row = (int64_t)blockIdx.y * ty + y; row < p.m; row += step) {
+            float g[VEC];
+            load_cols<VEC>(p.dy, row * p.lddy + col, p.dy_type, g);
+            if (p.act != GS_ACT_NONE) {
+                float z[VEC];
+                load_cols<VEC>(p.z, row * p.ldz + col, p.type, z);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) g[e] *= act_slope(z[e], p.act);
+            }
+            if (p.dz) store_cols<VEC>(p.dz, row * p.lddz + col, p.type, g);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) sum[e] += g[e];
+        }
+    }
+    if (!p.partial) return;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) part[(y * tx + x) * VEC + e] = sum[e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < tx * VEC; i += kElemThreads) {
+        const int64_t c = (int64_t)blockIdx.x * tx * VEC + i;
+        if (c >= p.n) continue;
+        float t = 0.0f;
+        for (int r = 0; r < ty; ++r) t += part[r * tx * VEC + i];
+        p.partial[(int64_t)blockIdx.y * p.n + c] = t;
+    }
+}
+
+struct GluGradParams {
+    const void *dh, *g, *u;
+    void *dg, *du;
+    int64_t m, n, lddh, ldg, ldu, ldd;
+    int type, act;
+};
+
+// dg = dh * u * act'(g), du = dh * act(g).  HBM bound: three reads, two writes.
+template <int VEC>
+__global__ void __launch_bounds__(kElemThreads) glu_grad_kernel(const GluGradParams p, int tx)
+{
+    const int ty = kElemThreads / tx;
+    const int64_t col = ((int64_t)blockIdx.x * tx + threadIdx.x % tx) * VEC;
+    if (col >= p.n) return;
+    const int64_t step = (int64_t)gridDim.y * ty;
+    for (int64_t row = (int64_t)blockIdx.y * ty + threadIdx.x / tx; row < p.m; row += step) {
+        float d[VEC], g[VEC], u[VEC];
+        load_cols<VEC>(p.dh, row * p.lddh + col, p.type, d);
+        load_cols<VEC>(p.g, row * p.ldg + col, p.type, g);
+        load_cols<VEC>(p.u, row * p.ldu + col, p.type, u);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            float value, slope;
+            act_both(g[e], p.act, value, slope);
+            g[e] = d[e] * u[e] * slope;
+            u[e] = d[e] * value;
+        }
+        store_cols<VEC>(p.dg, row * p.ldd + col, p.type, g);
+        store_cols<VEC>(p.du, row * p.ldd + col, p.type, u);
+    }
+}
+
+// 32 columns x 8 slices of the parts a block: slice y sums parts y, y + 8, ...,
+// then the slices are added in order.
+__global__ void __launch_bounds__(256) join_partials_kernel(const float* partial, int64_t parts, int64_t count, void* out,
+                                                            int64_t cols, int64_t ld, int type)
+{
+    __shared__ float sm[8][33];
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const int64_t i = (int64_t)blockIdx.x * 32 + x;
+    float t = 0.0f;
+    if (i < count)
+        for (int64_t p = y; p < parts; p += 8) t += partial[p * count + i];
+    sm[y][x] = t;
+    __syncthreads();
+    if (y == 0 && i < count) {
+        for (int k = 1; k < 8; ++k) t += sm[k][x];
+        store_elem(out, (i / cols) * ld + i % cols, type, t);
+    }
+}
+
+// Thread columns of an elementwise block: a power of two that covers the row
+// when it is narrow, a block's width at most.
+int thread_cols(int64_t n, int vec)
+{
+    int tx = 1;
+    while (tx < 64 && (int64_t)tx * vec < n) tx *= 2;
+    return tx;
+}
+
+constexpr int64_t kSlabs = 608;   // about four blocks an SM over the column blocks
+
+int64_t slabs_for(int64_t m, int64_t n, int vec)
+{
+    const int tx = thread_cols(n, vec), ty = kElemThreads / tx;
+    const int64_t cb = (n + (int64_t)tx * vec - 1) / ((int64_t)tx * vec);
+    int64_t s = (kSlabs + cb - 1) / cb;
+    const int64_t most = (m + ty - 1) / ty;
+    return s < most ? s : (most > 0 ? most : 1);
+}
+
+gs_status check_sizes(int64_t rows, int64_t in, int64_t out)
+{
+    return size_ok(rows, 0) && size_ok(in, 1) && size_ok(out, 1) ? GS_OK : GS_ERR_INVALID_ARG;
+}
+
+gs_status zero_rows(void* p, int64_t ld, int64_t rows, int64_t cols, int type, cudaStream_t st)
+{
+    const size_t e = type_bytes(type);
+    GS_CUDA_TRY(cudaMemset2DAsync(p, (size_t)ld * e, 0, (size_t)cols * e, (size_t)rows, st));
+    return GS_OK;
+}
+
+// Offsets of the parts of a workspace.
+struct Scratch {
+    size_t used = 0;
+    size_t take(size_t bytes)
+    {
+        const size_t at = used;
+        used += (size_t)round_up((int64_t)bytes, 256);
+        return at;
+    }
+};
+
+}  // namespace
+
+gs_status join_partials(const float* partial, int64_t parts, int64_t count, void* out, int64_t cols, int64_t ld, int type,
+                        cudaStream_t st)
+{
+    const int64_t blocks = (count + 31) / 32;
+    if (blocks > 0x7fffffffll) return GS_ERR_INVALID_ARG;
+    join_partials_kernel<<<(unsigned)blocks, 256, 0, st>>>(partial, parts, count, out, cols, ld, type);
+    GS_LAUNCH_CHECK();
+    return GS_OK;
+}
+
+}  // namespace gs
+
+using namespace gs;
+
+extern "C" gs_status gs_linear(const gs_linear_args* args, void* ws, size_t* ws_bytes, void* stream)
+{
+    GS_NVTX_RANGE("gs_linear");
+    if (!args) return GS_ERR_INVALID_ARG;
+    const gs_linear_args& a = *args;
+    if (check_sizes(a.rows, a.in_features, a.out_features) != GS_OK) return GS_ERR_INVALID_ARG;
+    if (!(type_half(a.type) || a.type == GS_E4M3) || !type_float(a.out_type) || !act_ok(a.act)) return GS_ERR_INVALID_ARG;
+    if (a.type != GS_E4M3 && (a.x_scale || a.w_scale)) return GS_ERR_INVALID_ARG;
+    if (a.bias && (!type_float(a.bias_type) || !vec_ok(a.bias, a.bias_type))) return GS_ERR_INVALID_ARG;
+    if (!vec_ok(a.x_scale, GS_F32) || !vec_ok(a.w_scale, GS_F32)) return GS_ERR_INVALID_ARG;
+    if (!mat_ok(a.w, a.ldw, a.in_features, a.type)) return GS_ERR_INVALID_ARG;
+    if (a.rows > 0) {
+        if (!mat_ok(a.x, a.ldx, a.in_features, a.type) || !mat_ok(a.y, a.ldy, a.out_features, a.out_type))
+            return GS_ERR_INVALID_ARG;
+        if (a.residual && !mat_ok(a.residual, a.ldr, a.out_features, a.out_type)) return GS_ERR_INVALID_ARG;
+        if (a.z && (!type_half(a.type) || !mat_ok(a.z, a.ldz, a.out_features, a.type))) return GS_ERR_INVALID_ARG;
+    }
+    GemmCall c = {};
+    c.kind = GemmKind::kLinear;
+    c.m = a.rows, c.n = a.out_features, c.k = a.in_features, c.type = a.type;
+    c.a[0] = {a.x, a.ldx, true}, c.b[0] = {a.w, a.ldw, true};
+    c.x_scale = a.x_scale, c.w_scale[0] = a.w_scale;
+    c.bias = a.bias, c.bias_type = a.bias_type, c.act = a.act;
+    c.residual = a.residual, c.ldr = a.ldr;
+    c.y = a.y, c.ldy = a.ldy, c.out_type = a.out_type;
+    c.z = a.z, c.ldz = a.ldz, c.z_type = a.type;
+    size_t need = 0;
+    gs_status s = a.rows > 0 ? gemm_ws_bytes(c, &need) : GS_OK;
+    if (s != GS_OK) return s;
+    const WsCheck wc = ws_check(ws, ws_bytes, need);
+    if (wc == WsCheck::kBad) return GS_ERR_INVALID_ARG;
+    if (wc == WsCheck::kQuery || a.rows == 0) return GS_OK;
+    return gemm_run(c, ws, (cudaStream_t)stream);
+}
+
+extern "C" gs_status gs_linear_bwd(const gs_linear_bwd_args* args, void* ws, size_t* ws_bytes, void* stream)
+{
+    GS_NVTX_RANGE("gs_linear_bwd");
+    if (!args) return GS_ERR_INVALID_ARG;
+    const gs_linear_bwd_args& a = *args;
+    const int64_t m = a.rows, k = a.in_features, n = a.out_features;
+    if (check_sizes(m, k, n) != GS_OK) return GS_ERR_INVALID_ARG;
+    if (!type_half(a.type) || !type_float(a.dy_type) || !act_ok(a.act)) return GS_ERR_INVALID_ARG;
+    if (a.dw && ((a.dw_type != a.type && a.dw_type != GS_F32) || !mat_ok(a.dw, a.lddw, k, a.dw_type)))
+        return GS_ERR_INVALID_ARG;
+    if (a.db && (!type_float(a.db_type) || !vec_ok(a.db, a.db_type))) return GS_ERR_INVALID_ARG;
+    if (m > 0) {
+        if (!mat_ok(a.dy, a.lddy, n, a.dy_type)) return GS_ERR_INVALID_ARG;
+        if (a.act != GS_ACT_NONE && !mat_ok(a.z, a.ldz, n, a.type)) return GS_ERR_INVALID_ARG;
+        if (a.dx && (!mat_ok(a.dx, a.lddx, k, a.type) || !mat_ok(a.w, a.ldw, k, a.type))) return GS_ERR_INVALID_ARG;
+        if (a.dw && !mat_ok(a.x, a.ldx, k, a.type)) return GS_ERR_INVALID_ARG;
+    }
+    const bool plain = a.act == GS_ACT_NONE && a.dy_type == a.type;   // dz is dy
+    const bool products = a.dx || a.dw;
+    const bool make_dz = !plain && products;
+    const int64_t lddz = round_up(n, 8);
+    const bool vec = n % 8 == 0 && rows16(a.dy, a.lddy, a.dy_type) &&
+                     (a.act == GS_ACT_NONE || rows16(a.z, a.ldz, a.type));
+    Scratch sc;
+    const size_t at_dz = make_dz ? sc.take((size_t)m * lddz * 2) : 0;
+    const size_t at_db = a.db ? sc.take((size_t)slabs_for(m, n, vec ? 8 : 1) * n * 4) : 0;
+    GemmCall cx = {}, cw = {};
+    cx.kind = cw.kind = GemmKind::kLinear;
+    cx.type = cw.type = a.type;
+    const GemmFactor dz_k = {make_dz ? (void*)256 : a.dy, make_dz ? lddz : a.lddy, true};
+    cx.m = m, cx.n = k, cx.k = n;
+    cx.a[0] = dz_k, cx.b[0] = {a.w, a.ldw, false};
+    cx.y = a.dx, cx.ldy = a.lddx, cx.out_type = a.type;
+    cw.m = n, cw.n = k, cw.k = m;
+    cw.a[0] = {dz_k.p, dz_k.ld, false}, cw.b[0] = {a.x, a.ldx, false};
+    cw.y = a.dw, cw.ldy = a.lddw, cw.out_type = a.dw_type;
+    size_t need_x = 0, need_w = 0;
+    if (m > 0 && a.dx && gemm_ws_bytes(cx, &need_x) != GS_OK) return GS_ERR_INVALID_ARG;
+    if (m > 0 && a.dw && gemm_ws_bytes(cw, &need_w) != GS_OK) return GS_ERR_INVALID_ARG;
+    const size_t at_gemm = sc.take(need_x > need_w ? need_x : need_w);   // one after the other
+    const WsCheck wc = ws_check(ws, ws_bytes, sc.used);
+    if (wc == WsCheck::kBad) return GS_ERR_INVALID_ARG;
+    if (wc == WsCheck::kQuery) return GS_OK;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (m == 0) {
+        if (a.dw && zero_rows(a.dw, a.lddw, n, k, a.dw_type, st) != GS_OK) return GS_ERR_CUDA;
+        if (a.db && zero_rows(a.db, n, 1, n, a.db_type, st) != GS_OK) return GS_ERR_CUDA;
+        return GS_OK;
+    }
+    char* base = (char*)ws;
+    if (make_dz || a.db) {
+        DzParams p = {};
+        p.dy = a.dy, p.z = a.z, p.dz = make_dz ? base + at_dz : nullptr;
+        p.partial = a.db ? (float*)(base + at_db) : nullptr;
+        p.m = m, p.n = n, p.lddy = a.lddy, p.ldz = a.ldz, p.lddz = lddz;
+        p.dy_type = a.dy_type, p.type = a.type, p.act = a.act;
+        const int v = vec ? 8 : 1, tx = thread_cols(n, v);
+        const int64_t slabs = slabs_for(m, n, v);
+        const dim3 grid((unsigned)((n + (int64_t)tx * v - 1) / ((int64_t)tx * v)), (unsigned)slabs);
+        if (vec) dz_kernel<8><<<grid, kElemThreads, 0, st>>>(p, tx);
+        else dz_kernel<1><<<grid, kElemThreads, 0, st>>>(p, tx);
+        GS_LAUNCH_CHECK();
+        if (a.db) {
+            const gs_status s = join_partials(p.partial, slabs, n, a.db, n, n, a.db_type, st);
+            if (s != GS_OK) return s;
+        }
+        if (make_dz) cx.a[0].p = cw.a[0].p = base + at_dz;
+    }
+    if (a.dx) {
+        const gs_status s = gemm_run(cx, base + at_gemm, st);
+        if (s != GS_OK) return s;
+    }
+    if (a.dw) return gemm_run(cw, base + at_gemm, st);
+    return GS_OK;
+}
+
+extern "C" gs_status gs_glu(const gs_glu_args* args, void* ws, size_t* ws_bytes, void* stream)
+{
+    GS_NVTX_RANGE("gs_glu");
+    if (!args) return GS_ERR_INVALID_ARG;
+    const gs_glu_args& a = *args;
+    if (check_sizes(a.rows, a.in_features, a.hidden) != GS_OK) return GS_ERR_INVALID_ARG;
+    if (!(type_half(a.type) || a.type == GS_E4M3) || !type_half(a.out_type) || !act_ok(a.act)) return GS_ERR_INVALID_ARG;
+    if (a.type != GS_E4M3 && (a.out_type != a.type || a.x_scale || a.gate_scale || a.up_scale)) return GS_ERR_INVALID_ARG;
+    if (!vec_ok(a.x_scale, GS_F32) || !vec_ok(a.gate_scale, GS_F32) || !vec_ok(a.up_scale, GS_F32))
+        return GS_ERR_INVALID_ARG;
+    if (!mat_ok(a.w_gate, a.ldwg, a.in_features, a.type) || !mat_ok(a.w_up, a.ldwu, a.in_features, a.type))
+        return GS_ERR_INVALID_ARG;
+    if (!a.g != !a.u) return GS_ERR_INVALID_ARG;
+    if (a.rows > 0) {
+        if (!mat_ok(a.x, a.ldx, a.in_features, a.type) || !mat_ok(a.h, a.ldh, a.hidden, a.out_type))
+            return GS_ERR_INVALID_ARG;
+        if (a.g && (!mat_ok(a.g, a.ldg, a.hidden, a.out_type) || !mat_ok(a.u, a.ldu, a.hidden, a.out_type)))
+            return GS_ERR_INVALID_ARG;
+    }
+    GemmCall c = {};
+    c.kind = GemmKind::kGlu;
+    c.m = a.rows, c.n = a.hidden, c.k = a.in_features, c.type = a.type;
+    c.a[0] = {a.x, a.ldx, true};
+    c.b[0] = {a.w_gate, a.ldwg, true}, c.b[1] = {a.w_up, a.ldwu, true};
+    c.x_scale = a.x_scale, c.w_scale[0] = a.gate_scale, c.w_scale[1] = a.up_scale;
+    c.act = a.act;
+    c.y = a.h, c.ldy = a.ldh, c.out_type = c.z_type = a.out_type;
+    c.z = a.g, c.ldz = a.ldg, c.z2 = a.u, c.ldz2 = a.ldu;
+    size_t need = 0;
+    gs_status s = a.rows > 0 ? gemm_ws_bytes(c, &need) : GS_OK;
+    if (s != GS_OK) return s;
+    const WsCheck wc = ws_check(ws, ws_bytes, need);
+    if (wc == WsCheck::kBad) return GS_ERR_INVALID_ARG;
+    if (wc == WsCheck::kQuery || a.rows == 0) return GS_OK;
+    return gemm_run(c, ws, (cudaStream_t)stream);
+}
+
+extern "C" gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* ws_bytes, void* stream)
+{
+    GS_NVTX_RANGE("gs_glu_bwd");
+    if (!args) return GS_ERR_INVALID_ARG;
+    const gs_glu_bwd_args& a = *args;
+    const int64_t m = a.rows, k = a.in_features, f = a.hidden;
+    if (check_sizes(m, k, f) != GS_OK) return GS_ERR_INVALID_ARG;
+    if (!type_half(a.type) || !act_ok(a.act) || !a.dw_gate != !a.dw_up) return GS_ERR_INVALID_ARG;
+    if (a.dw_gate && ((a.dw_type != a.type && a.dw_type != GS_F32) || !mat_ok(a.dw_gate, a.lddwg, k, a.dw_type) ||
+                      !mat_ok(a.dw_up, a.lddwu, k, a.dw_type)))
+        return GS_ERR_INVALID_ARG;
+    if (m > 0) {
+        if (!mat_ok(a.dh, a.lddh, f, a.type) || !mat_ok(a.g, a.ldg, f, a.type) || !mat_ok(a.u, a.ldu, f, a.type))
+            return GS_ERR_INVALID_ARG;
+        if (a.dx && (!mat_ok(a.dx, a.lddx, k, a.type) || !mat_ok(a.w_gate, a.ldwg, k, a.type) ||
+                     !mat_ok(a.w_up, a.ldwu, k, a.type)))
+            return GS_ERR_INVALID_ARG;
+        if (a.dw_gate && !mat_ok(a.x, a.ldx, k, a.type)) return GS_ERR_INVALID_ARG;
+    }
+    const int64_t ldd = round_up(f, 8);
+    Scratch sc;
+    const size_t at_dg = sc.take((size_t)m * ldd * 2), at_du = sc.take((size_t)m * ldd * 2);
+    GemmCall cx = {}, cw = {};
+    cx.kind = GemmKind::kSum, cw.kind = GemmKind::kTwo;
+    cx.type = cw.type = a.type;
+    void* const aligned = (void*)256;   // where the workspace's parts lie is not known yet; that they are aligned is
+    cx.m = m, cx.n = k, cx.k = f;
+    cx.a[0] = cx.a[1] = {aligned, ldd, true};
+    cx.b[0] = {a.w_gate, a.ldwg, false}, cx.b[1] = {a.w_up, a.ldwu, false};
+    cx.y = a.dx, cx.ldy = a.lddx, cx.out_type = a.type;
+    cw.m = f, cw.n = k, cw.k = m;
+    cw.a[0] = cw.a[1] = {aligned, ldd, false};
+    cw.b[0] = cw.b[1] = {a.x, a.ldx, false};
+    cw.y = a.dw_gate, cw.ldy = a.lddwg, cw.y2 = a.dw_up, cw.ldy2 = a.lddwu, cw.out_type = a.dw_type;
+    size_t need_x = 0, need_w = 0;
+    if (m > 0 && a.dx && gemm_ws_bytes(cx, &need_x) != GS_OK) return GS_ERR_INVALID_ARG;
+    if (m > 0 && a.dw_gate && gemm_ws_bytes(cw, &need_w) != GS_OK) return GS_ERR_INVALID_ARG;
+    const size_t at_gemm = sc.take(need_x > need_w ? need_x : need_w);
+    const WsCheck wc = ws_check(ws, ws_bytes, sc.used);
+    if (wc == WsCheck::kBad) return GS_ERR_INVALID_ARG;
+    if (wc == WsCheck::kQuery) return GS_OK;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (m == 0) {
+        if (a.dw_gate && (zero_rows(a.dw_gate, a.lddwg, f, k, a.dw_type, st) != GS_OK ||
+                          zero_rows(a.dw_up, a.lddwu, f, k, a.dw_type, st) != GS_OK))
+            return GS_ERR_CUDA;
+        return GS_OK;
+    }
+    if (!a.dx && !a.dw_gate) return GS_OK;
+    char* base = (char*)ws;
+    GluGradParams p = {};
+    p.dh = a.dh, p.g = a.g, p.u = a.u, p.dg = base + at_dg, p.du = base + at_du;
+    p.m = m, p.n = f, p.lddh = a.lddh, p.ldg = a.ldg, p.ldu = a.ldu, p.ldd = ldd;
+    p.type = a.type, p.act = a.act;
+    const bool vec = f % 8 == 0 && rows16(a.dh, a.lddh, a.type) && rows16(a.g, a.ldg, a.type) &&
+                     rows16(a.u, a.ldu, a.type);
+    const int v = vec ? 8 : 1, tx = thread_cols(f, v), ty = kElemThreads / tx;
+    int64_t gy = (m + ty - 1) / ty;
+    if (gy > 65535) gy = 65535;
+    const dim3 grid((unsigned)((f + (int64_t)tx * v - 1) / ((int64_t)tx * v)), (unsigned)gy);
+    if (vec) glu_grad_kernel<8><<<grid, kElemThreads, 0, st>>>(p, tx);
+    else glu_grad_kernel<1><<<grid, kElemThreads, 0, st>>>(p, tx);
+    GS_LAUNCH_CHECK();
+    cx.a[0].p = cw.a[0].p = p.dg;
+    cx.a[1].p = cw.a[1].p = p.du;
+    if (a.dx) {
+        const gs_status s = gemm_run(cx, base + at_gemm, st);
+        if (s != GS_OK) return s;
+    }
+    if (a.dw_gate) return gemm_run(cw, base + at_gemm, st);
+    return GS_OK;
+}

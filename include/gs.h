@@ -78,7 +78,7 @@ typedef enum gs_status {
     GS_ERR_INVALID_ARG = 1, /* a pointer, size or option is out of range          */
     GS_ERR_CAPACITY = 2,    /* instance buffers too small; needed count reported  */
     GS_ERR_CUDA = 3,        /* a CUDA runtime call or kernel launch failed        */
-    GS_ERR_TIMEOUT = 4,     /* reserved: no call waits on the device              */
+    GS_ERR_TIMEOUT = 4,     /* a kernel's bounded wait ran out (gs_wait_report)   */
     GS_ERR_DEVICE = 5       /* a kernel reported an error through the device word */
 } gs_status;
 
@@ -439,6 +439,222 @@ typedef enum gs_check_site {
  * Errors: INVALID_ARG for NULL pointers; DEVICE when a check failed; CUDA when a
  * copy of the records fails. */
 GS_API gs_status gs_check_report(uint64_t* report, int32_t* checked);
+
+/* ---- Decoder layers: the network in front of the rasterizer ----
+ * Rows are Gaussians (or tokens of a reconstruction model), features are
+ * columns; the last layer may write the [n][stride] parameter buffer itself.
+ * Three operators and their gradients:
+ *   gs_rms_norm   s = x + residual, y = s / rms(s) * weight, also in e4m3 with scales
+ *   gs_linear     y = act(x w^T + bias) + residual
+ *   gs_glu        h = act(x Wg^T) * (x Wu^T)   (gs_linear is the down projection)
+ * Conventions, besides those at the top of this file:
+ *   - Matrices are row-major: element (r, c) of a matrix with leading dimension
+ *     ld (in elements, >= its columns) is p[r * ld + c].  Any ld and any
+ *     element-aligned base is accepted; rows whose base and pitch are
+ *     multiples of 16 bytes are read and written in place by the tensor copies,
+ *     other operands are first copied to aligned rows in the workspace.
+ *   - rows = 0 is valid (gradients of weights are then zero); features >= 1.
+ *     Sizes are below 2^31; products of sizes and offsets are 64-bit.
+ *   - Sums, norms and products are accumulated in fp32; each output is rounded
+ *     to its type once, to nearest even.  Results do not depend on the run:
+ *     there are no atomics on values, split sums are joined in a fixed order.
+ *   - NULL marks an optional array that is absent.  Scale vectors are fp32.
+ *   - ws / ws_bytes: scratch of 256-byte alignment; ws == NULL queries the size
+ *     into *ws_bytes and does nothing else; where that size is 0, both may be
+ *     NULL in the call.  Contents on entry are ignored.
+ *   - y may be the same array as residual (same ld), sum the same as x or
+ *     residual, dx the same as dsum; other outputs overlap nothing.
+ *   - Structs are read on the host during the call. */
+typedef enum gs_type { GS_F32 = 0, GS_BF16 = 1, GS_F16 = 2, GS_E4M3 = 3 } gs_type;
+typedef enum gs_act { GS_ACT_NONE = 0, GS_ACT_RELU = 1, GS_ACT_SILU = 2, GS_ACT_GELU = 3 } gs_act;
+
+#define GS_NORM_MAX_COLS 16384 /* columns of a normalised or quantised row          */
+
+/* Root-mean-square norm with the residual's addition.
+ *   s = x + residual (fp32; s = x without one);  rstd = 1 / sqrt(mean(s^2) + eps)
+ *   y = s * rstd * weight
+ * With y_type GS_E4M3:  t = s * weight, a = max(max_row |t|, 2^-100),
+ *   y = e4m3(t * (448 / a)), y_scale = (a / 448) * rstd, so that y * y_scale is
+ *   the norm: rstd cancels out of the 8-bit values.  A NaN in a row makes its
+ *   y and y_scale NaN.
+ * The norm is taken of the fp32 sum; `sum` receives it rounded to `type`.
+ * x, residual, sum: [rows][cols] of `type` (F32, BF16, F16).  weight: [cols] of
+ * weight_type (F32, BF16, F16).  y: y_type (F32, BF16, F16, E4M3).  y_scale:
+ * [rows], with E4M3 only.  rstd: [rows] or NULL.
+ * Errors: INVALID_ARG for bad pointers, sizes (cols outside 1..GS_NORM_MAX_COLS),
+ * types, or eps not finite or negative; CUDA on launch failure. */
+typedef struct gs_rms_norm_args {
+    int64_t rows, cols;
+    const void* x;
+    int64_t ldx;
+    const void* residual;
+    int64_t ldr;
+    const void* weight;
+    void* y;
+    int64_t ldy;
+    float* y_scale;
+    void* sum;
+    int64_t lds;
+    float* rstd;
+    float eps;
+    int32_t type, weight_type, y_type;
+} gs_rms_norm_args;
+GS_API gs_status gs_rms_norm(const gs_rms_norm_args* args, void* stream);
+
+/* Gradients of gs_rms_norm (16- or 32-bit y).
+ *   dx = rstd * (dy * weight - s * rstd^2 * mean(dy * weight * s)) + dsum
+ *   dweight = sum over rows of dy * s * rstd
+ * dx is the gradient of x and of residual alike.  sum, rstd: the forward's.
+ * dsum: gradient that reaches the sum from elsewhere (the residual stream), or
+ * NULL.  dy: dy_type; sum, dsum, dx: `type`; weight, dweight: weight_type (all
+ * F32, BF16 or F16).  dx or dweight may be NULL (not computed).
+ * Errors: as gs_rms_norm, and a too small workspace. */
+typedef struct gs_rms_norm_bwd_args {
+    int64_t rows, cols;
+    const void* dy;
+    int64_t lddy;
+    const void* sum;
+    int64_t lds;
+    const void* weight;
+    const float* rstd;
+    const void* dsum;
+    int64_t ldds;
+    void* dx;
+    int64_t lddx;
+    void* dweight;
+    int32_t type, dy_type, weight_type, reserved;
+} gs_rms_norm_bwd_args;
+GS_API gs_status gs_rms_norm_bwd(const gs_rms_norm_bwd_args* args, void* ws, size_t* ws_bytes, void* stream);
+
+/* Rows to 8 bits: a = max(max_row |x|, 2^-100), q = e4m3(x * (448 / a)),
+ * scale = a / 448.  x: [rows][cols] of `type` (F32, BF16, F16).
+ * Errors: as gs_rms_norm. */
+typedef struct gs_quantize_rows_args {
+    int64_t rows, cols;
+    const void* x;
+    int64_t ldx;
+    void* q;
+    int64_t ldq;
+    float* scale;
+    int32_t type, reserved;
+} gs_quantize_rows_args;
+GS_API gs_status gs_quantize_rows(const gs_quantize_rows_args* args, void* stream);
+
+/* Matrix product with bias, activation and residual in its epilogue:
+ *   z = (x w^T) * x_scale[row] * w_scale[column] + bias;  y = act(z) + residual
+ * x: [rows][in], w: [out][in], both of `type` (BF16, F16 or E4M3); x_scale
+ * [rows] and w_scale [out]: with E4M3 only (NULL: 1).  bias: [out] of bias_type
+ * (F32, BF16, F16) or NULL.  residual (or NULL), y: [rows][out] of out_type
+ * (F32, BF16, F16).  z: NULL, or [rows][out] of `type` (16 bits): the
+ * pre-activations rounded to 16 bits, which gs_linear_bwd takes.
+ * act: gs_act; GELU is the exact one, v * Phi(v).
+ * Errors: INVALID_ARG for bad pointers, sizes, types or a too small workspace;
+ * CUDA on launch failure. */
+typedef struct gs_linear_args {
+    int64_t rows, in_features, out_features;
+    const void* x;
+    int64_t ldx;
+    const void* w;
+    int64_t ldw;
+    const float* x_scale;
+    const float* w_scale;
+    const void* bias;
+    const void* residual;
+    int64_t ldr;
+    void* y;
+    int64_t ldy;
+    void* z;
+    int64_t ldz;
+    int32_t type, bias_type, out_type, act;
+} gs_linear_args;
+GS_API gs_status gs_linear(const gs_linear_args* args, void* ws, size_t* ws_bytes, void* stream);
+
+/* Gradients of gs_linear (16-bit operands).
+ *   dz = dy * act'(z);  dx = dz w;  dw = dz^T x;  db = sum over rows of dz
+ * (the residual's gradient is dy itself).  dz enters the two products rounded
+ * to `type`, the operands' 16 bits; db sums it unrounded.  With act NONE and dy
+ * of `type`, dz is dy and z is not read (may be NULL).
+ * dy: [rows][out] of dy_type (F32, BF16, F16).  dx: [rows][in] of `type`.
+ * dw: [out][in] of dw_type (F32 or `type`).  db: [out] of db_type (F32, BF16,
+ * F16).  dx, dw and db may each be NULL (not computed).
+ * Errors: as gs_linear. */
+typedef struct gs_linear_bwd_args {
+    int64_t rows, in_features, out_features;
+    const void* dy;
+    int64_t lddy;
+    const void* x;
+    int64_t ldx;
+    const void* w;
+    int64_t ldw;
+    const void* z;
+    int64_t ldz;
+    void* dx;
+    int64_t lddx;
+    void* dw;
+    int64_t lddw;
+    void* db;
+    int32_t type, dy_type, dw_type, db_type, act, reserved;
+} gs_linear_bwd_args;
+GS_API gs_status gs_linear_bwd(const gs_linear_bwd_args* args, void* ws, size_t* ws_bytes, void* stream);
+
+/* Gated feed-forward, both projections, the activation and the product in one
+ * kernel:  g = (x w_gate^T) * x_scale[row] * gate_scale[column],
+ *          u = (x w_up^T) * x_scale[row] * up_scale[column],  h = act(g) * u
+ * x: [rows][in], w_gate, w_up: [hidden][in], all of `type` (BF16, F16 or E4M3);
+ * scales as for gs_linear.  h: [rows][hidden] of out_type (BF16 or F16; `type`
+ * when that is 16 bits).  g, u: both NULL, or [rows][hidden] of out_type: the
+ * projections rounded to 16 bits, which gs_glu_bwd takes.
+ * Errors: as gs_linear. */
+typedef struct gs_glu_args {
+    int64_t rows, in_features, hidden;
+    const void* x;
+    int64_t ldx;
+    const void* w_gate;
+    int64_t ldwg;
+    const void* w_up;
+    int64_t ldwu;
+    const float* x_scale;
+    const float* gate_scale;
+    const float* up_scale;
+    void* h;
+    int64_t ldh;
+    void* g;
+    int64_t ldg;
+    void* u;
+    int64_t ldu;
+    int32_t type, out_type, act, reserved;
+} gs_glu_args;
+GS_API gs_status gs_glu(const gs_glu_args* args, void* ws, size_t* ws_bytes, void* stream);
+
+/* Gradients of gs_glu (16-bit operands).
+ *   dg = dh * u * act'(g);  du = dh * act(g)   (rounded to `type` for the products)
+ *   dx = dg w_gate + du w_up;  dw_gate = dg^T x;  dw_up = du^T x
+ * dh, g, u: [rows][hidden] of `type`.  dx: [rows][in] of `type`.  dw_gate,
+ * dw_up: [hidden][in] of dw_type (F32 or `type`), both or neither; dx may be NULL.
+ * Errors: as gs_linear. */
+typedef struct gs_glu_bwd_args {
+    int64_t rows, in_features, hidden;
+    const void* dh;
+    int64_t lddh;
+    const void* x;
+    int64_t ldx;
+    const void* w_gate;
+    int64_t ldwg;
+    const void* w_up;
+    int64_t ldwu;
+    const void* g;
+    int64_t ldg;
+    const void* u;
+    int64_t ldu;
+    void* dx;
+    int64_t lddx;
+    void* dw_gate;
+    int64_t lddwg;
+    void* dw_up;
+    int64_t lddwu;
+    int32_t type, dw_type, act, reserved;
+} gs_glu_bwd_args;
+GS_API gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* ws_bytes, void* stream);
 
 /* Static helpers (no device work). */
 GS_API const char* gs_error_string(gs_status s);
