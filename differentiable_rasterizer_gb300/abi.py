@@ -32,6 +32,7 @@ EXPORTS = ("gs_project", "gs_bin_sort", "gs_raster_fused_fwd_bwd", "gs_grad_comp
            "gs_raster_forward_state", "gs_dssim_loss_grad", "gs_raster_backward_state", "gs_grad_compact_static",
            "gs_prune_tiles", "gs_split_ranges", "gs_compose", "gs_raster_work_counts", "gs_check_report",
            "gs_rms_norm", "gs_rms_norm_bwd", "gs_quantize_rows", "gs_linear", "gs_linear_bwd", "gs_glu", "gs_glu_bwd",
+           "gs_wait_report",
            "gs_error_string", "gs_param_rows", "gs_param_stride", "gs_num_tiles", "gs_version")
 
 
@@ -109,6 +110,8 @@ def lib():
         for name in ("gs_rms_norm_bwd", "gs_linear", "gs_linear_bwd", "gs_glu", "gs_glu_bwd"):
             getattr(L, name).argtypes = [ctypes.c_char_p, _P, ctypes.POINTER(ctypes.c_size_t), _P]
             getattr(L, name).restype = ctypes.c_int
+        L.gs_wait_report.argtypes = [ctypes.POINTER(ctypes.c_int32)]
+        L.gs_wait_report.restype = ctypes.c_int
         L.gs_check_report.argtypes = [_P, ctypes.POINTER(ctypes.c_int32)]
         L.gs_check_report.restype = ctypes.c_int
         L.gs_error_string.argtypes = [ctypes.c_int]
@@ -410,3 +413,13 @@ def gs_glu_bwd(args: bytes, ws, ws_bytes, stream):
 def layer_ws_bytes(name: str, args: bytes) -> int:
     """Scratch that the named layer call (gs_linear, gs_linear_bwd, ...) needs for these arguments."""
     return _ws_query(name, args)
+
+
+def gs_wait_report() -> bool:
+    """True if a layer kernel's bounded wait ran out since the last report (then cleared);
+    synchronises the device."""
+    expired = ctypes.c_int32(0)
+    st = lib().gs_wait_report(ctypes.byref(expired))
+    if st not in (GS_OK, GS_ERR_TIMEOUT):
+        _check("gs_wait_report", st)
+    return bool(expired.value)

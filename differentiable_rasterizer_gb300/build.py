@@ -29,7 +29,7 @@ CHECKED_LIB = os.path.join(OUT_DIR, "libgs_gb300_checked.so")
 VARIANTS = ((LIB, OUT_DIR, []), (CHECKED_LIB, os.path.join(OUT_DIR, "checked"), ["-DGS_CHECKED"]))
 SOURCES = ["abi.cu", "project.cu", "binsort.cu", "prune.cu", "raster.cu", "dssim.cu", "compose.cu", "compact.cu", "adam.cu",
            "norm.cu", "linear.cu", "gemm.cu"]
-HEADERS = ["gs_common.cuh", "project_math.cuh", "scan.cuh", "layers_common.cuh", "gemm.cuh"]
+HEADERS = ["gs_common.cuh", "project_math.cuh", "scan.cuh", "layers_common.cuh", "gemm.cuh", "tc_common.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-fmad=false", "-prec-div=true", "-prec-sqrt=true", "-ftz=false",

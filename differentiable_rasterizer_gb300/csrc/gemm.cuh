@@ -42,13 +42,12 @@ struct GemmCall {
     int out_type, z_type, act;
 };
 
-// Scratch that a call needs; it depends on sizes, types and presence, and on the
-// alignment of the factors.
+// Scratch that a call needs; it depends on sizes, types, presence and alignment.
 gs_status gemm_ws_bytes(const GemmCall& c, size_t* bytes);
 gs_status gemm_run(const GemmCall& c, void* ws, cudaStream_t st);
 
-// out[i / cols][i % cols] = sum over parts, in order, of partial[part][i].
-gs_status join_partials(const float* partial, int64_t parts, int64_t count, void* out, int64_t cols, int64_t ld, int type,
-                        cudaStream_t st);
+// out[r * ld + c] = sum over parts, in order, of partial[part][r][c] (rows of `pitch`).
+gs_status join_partials(const float* partial, int64_t parts, int64_t rows, int64_t cols, int64_t pitch, void* out,
+                        int64_t ld, int type, cudaStream_t st);
 
 }  // namespace gs

@@ -107,22 +107,24 @@ __global__ void __launch_bounds__(kElemThreads) glu_grad_kernel(const GluGradPar
     }
 }
 
-// 32 columns x 8 slices of the parts a block: slice y sums parts y, y + 8, ...,
+// 32 values x 8 slices of the parts a block: slice y sums parts y, y + 8, ...,
 // then the slices are added in order.
-__global__ void __launch_bounds__(256) join_partials_kernel(const float* partial, int64_t parts, int64_t count, void* out,
-                                                            int64_t cols, int64_t ld, int type)
+__global__ void __launch_bounds__(256) join_partials_kernel(const float* partial, int64_t parts, int64_t rows,
+                                                            int64_t cols, int64_t pitch, void* out, int64_t ld, int type)
 {
     __shared__ float sm[8][33];
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int64_t i = (int64_t)blockIdx.x * 32 + x;
+    const int64_t i = (int64_t)blockIdx.x * 32 + x, count = rows * pitch;
+    const int64_t r = i / pitch, c = i % pitch;
+    const bool live = i < count && c < cols;
     float t = 0.0f;
-    if (i < count)
+    if (live)
         for (int64_t p = y; p < parts; p += 8) t += partial[p * count + i];
     sm[y][x] = t;
     __syncthreads();
-    if (y == 0 && i < count) {
+    if (y == 0 && live) {
         for (int k = 1; k < 8; ++k) t += sm[k][x];
-        store_elem(out, (i / cols) * ld + i % cols, type, t);
+        store_elem(out, r * ld + c, type, t);
     }
 }
 
@@ -171,12 +173,12 @@ struct Scratch {
 
 }  // namespace
 
-gs_status join_partials(const float* partial, int64_t parts, int64_t count, void* out, int64_t cols, int64_t ld, int type,
-                        cudaStream_t st)
+gs_status join_partials(const float* partial, int64_t parts, int64_t rows, int64_t cols, int64_t pitch, void* out,
+                        int64_t ld, int type, cudaStream_t st)
 {
-    const int64_t blocks = (count + 31) / 32;
+    const int64_t blocks = (rows * pitch + 31) / 32;
     if (blocks > 0x7fffffffll) return GS_ERR_INVALID_ARG;
-    join_partials_kernel<<<(unsigned)blocks, 256, 0, st>>>(partial, parts, count, out, cols, ld, type);
+    join_partials_kernel<<<(unsigned)blocks, 256, 0, st>>>(partial, parts, rows, cols, pitch, out, ld, type);
     GS_LAUNCH_CHECK();
     return GS_OK;
 }
@@ -283,7 +285,7 @@ extern "C" gs_status gs_linear_bwd(const gs_linear_bwd_args* args, void* ws, siz
         else dz_kernel<1><<<grid, kElemThreads, 0, st>>>(p, tx);
         GS_LAUNCH_CHECK();
         if (a.db) {
-            const gs_status s = join_partials(p.partial, slabs, n, a.db, n, n, a.db_type, st);
+            const gs_status s = join_partials(p.partial, slabs, 1, n, n, a.db, n, a.db_type, st);
             if (s != GS_OK) return s;
         }
         if (make_dz) cx.a[0].p = cw.a[0].p = base + at_dz;

@@ -7,7 +7,7 @@
 // smallest power of two of threads that covers the row at kVec elements a
 // thread (16-byte accesses where every row allows them, single elements
 // otherwise), so narrow rows share a warp and wide ones take a block.
-#include "layers_common.cuh"
+#include "gemm.cuh"
 
 namespace gs {
 namespace {
@@ -286,10 +286,6 @@ gs_status run_fwd(const gs_rms_norm_args& a, cudaStream_t st)
 }
 
 }  // namespace
-
-gs_status join_partials(const float* partial, int64_t parts, int64_t count, void* out, int64_t cols, int64_t ld, int type,
-                        cudaStream_t st);   // linear.cu
-
 }  // namespace gs
 
 using namespace gs;
@@ -379,6 +375,6 @@ extern "C" gs_status gs_rms_norm_bwd(const gs_rms_norm_bwd_args* args, void* ws,
     else GS_BWD(1, 16);
 #undef GS_BWD
     GS_LAUNCH_CHECK();
-    if (a.dweight) return join_partials(part, grid, a.cols, a.dweight, a.cols, a.cols, a.weight_type, st);
+    if (a.dweight) return join_partials(part, grid, 1, a.cols, a.cols, a.dweight, a.cols, a.weight_type, st);
     return GS_OK;
 }

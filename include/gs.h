@@ -656,6 +656,14 @@ typedef struct gs_glu_bwd_args {
 } gs_glu_bwd_args;
 GS_API gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* ws_bytes, void* stream);
 
+/* The layers' products wait on their own copies and tensor-core work, each wait
+ * bounded to about two seconds; a kernel whose wait runs out (a device fault; it
+ * cannot happen otherwise) drains, returns with its outputs undefined, and
+ * leaves a mark that this call reports and clears.  Synchronises the device.
+ * expired: HOST int32 out, 1 if a wait ran out since the last report.
+ * Errors: INVALID_ARG for NULL; TIMEOUT when a wait ran out; CUDA. */
+GS_API gs_status gs_wait_report(int32_t* expired);
+
 /* Static helpers (no device work). */
 GS_API const char* gs_error_string(gs_status s);
 GS_API int32_t gs_param_rows(int32_t sh_degree);                     /* P: 14, 59, or -1 */

@@ -36,8 +36,10 @@ def layers():
 
 @pytest.fixture(autouse=True)
 def no_wait_expired():
+    """No bounded wait of a layer kernel may run out."""
     yield
-    torch.cuda.synchronize()
+    from differentiable_rasterizer_gb300 import abi
+    assert not abi.gs_wait_report()
 
 
 def rnd(shape, seed, dtype, std=1.0, pitch=None, offset=0):
