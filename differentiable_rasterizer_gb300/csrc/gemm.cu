@@ -117,17 +117,37 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t a)
     return v;
 }
 
-// A row's 32 values into a slot, rounded to the output's type.
+// A row's 32 values into a slot, rounded to the output's type, and a slot's row added.
+template <int T>
+__device__ __forceinline__ void slot_write_half(uint32_t slot, int row, const float (&v)[kChunk])
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        st_shared16(slot + slot_piece<2>(row, j),
+                    make_uint4(pack_half2(v[8 * j], v[8 * j + 1], T), pack_half2(v[8 * j + 2], v[8 * j + 3], T),
+                               pack_half2(v[8 * j + 4], v[8 * j + 5], T), pack_half2(v[8 * j + 6], v[8 * j + 7], T)));
+}
+template <int T>
+__device__ __forceinline__ void slot_add_half(uint32_t slot, int row, float (&v)[kChunk])
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint4 q = ld_shared16(slot + slot_piece<2>(row, j));
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = unpack_half2(w[i], T);
+            v[8 * j + 2 * i] += f.x;
+            v[8 * j + 2 * i + 1] += f.y;
+        }
+    }
+}
 template <int ESZ>
 __device__ __forceinline__ void slot_write(uint32_t slot, int row, const float (&v)[kChunk], int type)
 {
     if constexpr (ESZ == 2) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            st_shared16(slot + slot_piece<2>(row, j),
-                        make_uint4(pack_half2(v[8 * j], v[8 * j + 1], type), pack_half2(v[8 * j + 2], v[8 * j + 3], type),
-                                   pack_half2(v[8 * j + 4], v[8 * j + 5], type),
-                                   pack_half2(v[8 * j + 6], v[8 * j + 7], type)));
+        if (type == GS_BF16) slot_write_half<GS_BF16>(slot, row, v);
+        else slot_write_half<GS_F16>(slot, row, v);
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -140,17 +160,8 @@ template <int ESZ>
 __device__ __forceinline__ void slot_add(uint32_t slot, int row, float (&v)[kChunk], int type)
 {
     if constexpr (ESZ == 2) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint4 q = ld_shared16(slot + slot_piece<2>(row, j));
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = unpack_half2(w[i], type);
-                v[8 * j + 2 * i] += f.x;
-                v[8 * j + 2 * i + 1] += f.y;
-            }
-        }
+        if (type == GS_BF16) slot_add_half<GS_BF16>(slot, row, v);
+        else slot_add_half<GS_F16>(slot, row, v);
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -384,6 +395,16 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 fetch(chunk_no, 0);
             }
             const float xs = p.x_scale && row0 + lane < p.m ? p.x_scale[row0 + lane] : 1.0f;
+            // column factors of the warp's chunks, one a lane, fetched before the accumulator is waited for
+            float ca[kChunks], cb[kChunks];
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                const int64_t col = base_col + c * kChunk + lane;
+                const bool live = c < chunks && col < p.n;
+                ca[c] = p.w_scale[0] && live ? p.w_scale[0][col] : 1.0f;
+                if constexpr (GLU) cb[c] = p.w_scale[1] && live ? p.w_scale[1][col] : 1.0f;
+                else cb[c] = p.bias && live ? load_elem(p.bias, col, p.bias_type) : 0.0f;
+            }
             if (!__all_sync(0xffffffffu, mbar_wait(bar_acc + 8 * acc, (tile >> 1) & 1, gave_up))) {
                 ok = false;
                 // a residual chunk may be in flight: let it land
@@ -396,22 +417,20 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             __syncwarp();
             tc_fence_after();
             const uint32_t d = tmem + ((uint32_t)(quarter * 32) << 16) + acc * BN + half * (kOutCols / 2);
-            for (int c = 0; c < chunks; ++c, ++chunk_no) {
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                if (c >= chunks) break;
                 const int64_t col0 = base_col + c * kChunk;
                 const uint32_t b = chunk_no % bufs, ys = slot + b * buf_bytes;
                 const uint32_t zs = slot + z_at + (bufs == 2 ? b * 2048 : 0);
                 uint32_t raw[kChunk], raw2[GLU ? kChunk : 1];
                 tmem_ld32(d + c * kChunk, raw);
                 if constexpr (GLU) tmem_ld32(d + BN / 2 + c * kChunk, raw2);
-                // column factors of the chunk, one a lane, then read by all
-                const bool col_live = col0 + lane < p.n;
-                const float ca = p.w_scale[0] && col_live ? p.w_scale[0][col0 + lane] : 1.0f;
-                float cb;
-                if constexpr (GLU) cb = p.w_scale[1] && col_live ? p.w_scale[1][col0 + lane] : 1.0f;
-                else cb = p.bias && col_live ? load_elem(p.bias, col0 + lane, p.bias_type) : 0.0f;
-                __syncwarp();   // the last chunk's readers are done
-                col_a[lane] = ca;
-                col_b[lane] = cb;
+                if (p.e4m3 || p.bias) {
+                    __syncwarp();   // the last chunk's readers are done
+                    col_a[lane] = ca[c];
+                    col_b[lane] = cb[c];
+                }
                 if (has_res && !p.r_tma) {
                     if (lane == 0) bulk_wait_read<0>();
                     __syncwarp();
@@ -520,6 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     slot_to_rows<2>(GLU ? slot + z_at : zs, p.zp, p.ldz, row0, col0, p.m, p.n, lane);
                     if constexpr (GLU) slot_to_rows<2>(slot + z_at + 2048, p.z2p, p.ldz2, row0, col0, p.m, p.n, lane);
                 }
+                ++chunk_no;
             }
             tc_fence_before();
             __syncwarp();

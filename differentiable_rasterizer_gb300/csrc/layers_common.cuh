@@ -133,34 +133,126 @@ __device__ __forceinline__ void store8(void* p, int64_t i, int type, const float
     }
 }
 
+// Elements as they lie in memory, and their values.  The type is a template argument
+// (GS_F32, GS_BF16, GS_F16, or kAnyType with the type at run time): a branch on the
+// type between a load and its conversion makes every load wait for the one before
+// (the norm's forward over 1,000,000 x 256 took 479 us with such branches).
+constexpr int kAnyType = -1;
+
+template <int T, int VEC>
+struct Raw {
+    uint4 q[T == GS_F32 || T == kAnyType ? 2 : 1];
+};
+template <>
+struct Raw<GS_F32, 1> {
+    float f;
+};
+template <>
+struct Raw<GS_BF16, 1> {
+    uint16_t h;
+};
+template <>
+struct Raw<GS_F16, 1> {
+    uint16_t h;
+};
+template <>
+struct Raw<kAnyType, 1> {
+    float f;
+};
+
+template <int T, int VEC>
+__device__ __forceinline__ void raw_load(Raw<T, VEC>& r, const void* p, int64_t i, int type)
+{
+    if constexpr (VEC == 8) {
+        if (T == GS_F32 || (T == kAnyType && type == GS_F32)) {
+            r.q[0] = *reinterpret_cast<const uint4*>((const float*)p + i);
+            if constexpr (T == GS_F32 || T == kAnyType) r.q[1] = *reinterpret_cast<const uint4*>((const float*)p + i + 4);
+        } else r.q[0] = *reinterpret_cast<const uint4*>((const uint16_t*)p + i);
+    } else if constexpr (T == GS_F32) r.f = ((const float*)p)[i];
+    else if constexpr (T == kAnyType) r.f = load_elem(p, i, type);
+    else r.h = ((const uint16_t*)p)[i];
+}
+
+template <int T, int VEC>
+__device__ __forceinline__ void raw_zero(Raw<T, VEC>& r)
+{
+    if constexpr (VEC == 8) {
+        r.q[0] = make_uint4(0, 0, 0, 0);
+        if constexpr (T == GS_F32 || T == kAnyType) r.q[1] = make_uint4(0, 0, 0, 0);
+    } else if constexpr (T == GS_F32 || T == kAnyType) r.f = 0.0f;
+    else r.h = 0;
+}
+
+template <int T, int VEC>
+__device__ __forceinline__ void raw_values(const Raw<T, VEC>& r, int type, float (&v)[VEC])
+{
+    if constexpr (VEC == 8) {
+        if (T == GS_F32 || (T == kAnyType && type == GS_F32)) {
+            constexpr int hi = T == GS_F32 || T == kAnyType ? 1 : 0;
+            const uint32_t w[8] = {r.q[0].x, r.q[0].y, r.q[0].z, r.q[0].w, r.q[hi].x, r.q[hi].y, r.q[hi].z, r.q[hi].w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
+        } else {
+            const uint32_t w[4] = {r.q[0].x, r.q[0].y, r.q[0].z, r.q[0].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = unpack_half2(w[j], T == kAnyType ? type : T);
+                v[2 * j] = f.x, v[2 * j + 1] = f.y;
+            }
+        }
+    } else if constexpr (T == GS_F32 || T == kAnyType) v[0] = r.f;
+    else v[0] = unpack_half2(r.h, T).x;
+}
+
+template <int VEC>
+__device__ __forceinline__ void load_vec(const void* p, int64_t i, int type, float (&v)[VEC])
+{
+    if constexpr (VEC == 8) load8(p, i, type, v);
+    else v[0] = load_elem(p, i, type);
+}
+template <int VEC>
+__device__ __forceinline__ void store_vec(void* p, int64_t i, int type, const float (&v)[VEC])
+{
+    if constexpr (VEC == 8) store8(p, i, type, v);
+    else store_elem(p, i, type, v[0]);
+}
+
 // ------------------------------------------------------------------ activations
 // sigma(v) by the hardware exponential: relative error below 2^-20 (two roundings
-// of |v| log2 e and the exponential's 2 ulp), far inside the 16-bit results.
+// of |v| log2 e and the exponential's 2 ulp), far inside the 16-bit results.  For v
+// below about -88 the exponential is infinite and the quotient 0, as it should be.
 __device__ __forceinline__ float sigmoid_fast(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
 
-// v sigma(v).  For v below about -88 the exponential overflows to infinity and
-// the quotient is -0, as it should be (__fdividef by infinity gives 0).
+// Phi(v), the normal distribution function, and e = exp(-v^2 / 2), which its slope
+// shares:  Phi(-|v|) = (a1 t + ... + a5 t^5) e / 2,  t = 1 / (1 + p |v| / sqrt 2)
+// (Abramowitz & Stegun, Handbook of Mathematical Functions, 7.1.26: |error| of erf
+// below 1.5e-7).  Taken on the negative side, so that small tails do not cancel.
+// An erff and a second exponential cost three times as many instructions, which
+// is what bounded the epilogues (100,000 x 256 -> 256 GELU step: 224 us with them).
+__device__ __forceinline__ float normal_cdf(float v, float& e)
+{
+    const float t = __fdividef(1.0f, __fmaf_rn(fabsf(v), 0.3275911f * 0.70710678f, 1.0f));
+    e = __expf(-0.5f * v * v);
+    float q = __fmaf_rn(t, 1.061405429f, -1.453152027f);
+    q = __fmaf_rn(t, q, 1.421413741f);
+    q = __fmaf_rn(t, q, -0.284496736f);
+    q = __fmaf_rn(t, q, 0.254829592f);
+    q = q * t * (0.5f * e);
+    return v < 0.0f ? q : 1.0f - q;
+}
+
 __device__ __forceinline__ float act_value(float v, int act)
 {
     if (act == GS_ACT_RELU) return v < 0.0f ? 0.0f : v;   // NaN stays NaN
     if (act == GS_ACT_SILU) return v * sigmoid_fast(v);
-    if (act == GS_ACT_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+    if (act == GS_ACT_GELU) {
+        float e;
+        return v * normal_cdf(v, e);
+    }
     return v;
 }
 
-__device__ __forceinline__ float act_slope(float v, int act)
-{
-    if (act == GS_ACT_RELU) return v > 0.0f ? 1.0f : (v != v ? v : 0.0f);
-    if (act == GS_ACT_SILU) {
-        const float p = sigmoid_fast(v);
-        return p * __fmaf_rn(v, 1.0f - p, 1.0f);
-    }
-    if (act == GS_ACT_GELU)
-        return 0.5f * (1.0f + erff(v * 0.70710678118654752f)) + v * (0.39894228040143268f * __expf(-0.5f * v * v));
-    return 1.0f;
-}
-
-// Both at once, from one sigma (or one erf).
+// act(v) and act'(v), from one sigma or one Phi.
 __device__ __forceinline__ void act_both(float v, int act, float& value, float& slope)
 {
     if (act == GS_ACT_SILU) {
@@ -168,13 +260,24 @@ __device__ __forceinline__ void act_both(float v, int act, float& value, float& 
         value = v * p;
         slope = p * __fmaf_rn(v, 1.0f - p, 1.0f);
     } else if (act == GS_ACT_GELU) {
-        const float c = 0.5f * (1.0f + erff(v * 0.70710678118654752f));
+        float e;
+        const float c = normal_cdf(v, e);
         value = v * c;
-        slope = c + v * (0.39894228040143268f * __expf(-0.5f * v * v));
+        slope = __fmaf_rn(v * 0.39894228040143268f, e, c);
+    } else if (act == GS_ACT_RELU) {
+        value = v < 0.0f ? 0.0f : v;
+        slope = v > 0.0f ? 1.0f : (v != v ? v : 0.0f);
     } else {
-        value = act_value(v, act);
-        slope = act_slope(v, act);
+        value = v;
+        slope = 1.0f;
     }
+}
+
+__device__ __forceinline__ float act_slope(float v, int act)
+{
+    float value, slope;
+    act_both(v, act, value, slope);
+    return slope;
 }
 
 }  // namespace gs

@@ -1,6 +1,8 @@
 // linear.cu -- entry points of gs_linear, gs_glu and their gradients: argument
 // checks, the elementwise passes in front of the gradients' products, and the
 // fixed-order joins of partial sums.  The products are in gemm.cu.
+#include <type_traits>
+
 #include "gemm.cuh"
 
 namespace gs {
@@ -12,19 +14,7 @@ namespace {
 // kRows rows; a thread keeps its columns' sums in registers over all its rows,
 // the block joins them in row order and writes one partial row.
 constexpr int kElemThreads = 256;
-
-template <int VEC>
-__device__ __forceinline__ void load_cols(const void* p, int64_t i, int type, float (&v)[VEC])
-{
-    if constexpr (VEC == 8) load8(p, i, type, v);
-    else v[0] = load_elem(p, i, type);
-}
-template <int VEC>
-__device__ __forceinline__ void store_cols(void* p, int64_t i, int type, const float (&v)[VEC])
-{
-    if constexpr (VEC == 8) store8(p, i, type, v);
-    else store_elem(p, i, type, v[0]);
-}
+constexpr int kElemRows = 4;   // rows of a thread in flight
 
 struct DzParams {
     const void* dy;
@@ -35,7 +25,7 @@ struct DzParams {
     int dy_type, type, act;
 };
 
-template <int VEC>
+template <int T, int TDY, int VEC, int ACT>
 __global__ void __launch_bounds__(kElemThreads) dz_kernel(const DzParams p, int tx)
 {
     __shared__ float part[kElemThreads * VEC];
@@ -47,19 +37,31 @@ __global__ void __launch_bounds__(kElemThreads) dz_kernel(const DzParams p, int 
     for (int e = 0; e < VEC; ++e) sum[e] = 0.0f;
     if (col < p.n) {
         const int64_t step = (int64_t)gridDim.y * ty;
-#pragma unroll 2
-        for (int64_t row = (int64_t)blockIdx.y * ty + y; row < p.m; row += step) {
-            float g[VEC];
-            load_cols<VEC>(p.dy, row * p.lddy + col, p.dy_type, g);
-            if (p.act != GS_ACT_NONE) {
-                float z[VEC];
-                load_cols<VEC>(p.z, row * p.ldz + col, p.type, z);
+        for (int64_t row = (int64_t)blockIdx.y * ty + y; row < p.m; row += kElemRows * step) {
+            Raw<TDY, VEC> gr[kElemRows];
+            Raw<T, VEC> zr[kElemRows];
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) g[e] *= act_slope(z[e], p.act);
+            for (int i = 0; i < kElemRows; ++i) {
+                raw_zero(gr[i]);
+                raw_zero(zr[i]);
+                if (row + i * step < p.m) {
+                    raw_load(gr[i], p.dy, (row + i * step) * p.lddy + col, p.dy_type);
+                    if (ACT != GS_ACT_NONE) raw_load(zr[i], p.z, (row + i * step) * p.ldz + col, T);
+                }
             }
-            if (p.dz) store_cols<VEC>(p.dz, row * p.lddz + col, p.type, g);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) sum[e] += g[e];
+            for (int i = 0; i < kElemRows; ++i) {
+                float g[VEC], z[VEC];
+                raw_values(gr[i], p.dy_type, g);
+                if (ACT != GS_ACT_NONE) {
+                    raw_values(zr[i], T, z);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) g[e] *= act_slope(z[e], ACT);
+                }
+                if (p.dz && row + i * step < p.m) store_vec<VEC>(p.dz, (row + i * step) * p.lddz + col, T, g);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) sum[e] += g[e];
+            }
         }
     }
     if (!p.partial) return;
@@ -83,27 +85,41 @@ struct GluGradParams {
 };
 
 // dg = dh * u * act'(g), du = dh * act(g).  HBM bound: three reads, two writes.
-template <int VEC>
+template <int T, int VEC, int ACT>
 __global__ void __launch_bounds__(kElemThreads) glu_grad_kernel(const GluGradParams p, int tx)
 {
     const int ty = kElemThreads / tx;
     const int64_t col = ((int64_t)blockIdx.x * tx + threadIdx.x % tx) * VEC;
     if (col >= p.n) return;
     const int64_t step = (int64_t)gridDim.y * ty;
-    for (int64_t row = (int64_t)blockIdx.y * ty + threadIdx.x / tx; row < p.m; row += step) {
-        float d[VEC], g[VEC], u[VEC];
-        load_cols<VEC>(p.dh, row * p.lddh + col, p.type, d);
-        load_cols<VEC>(p.g, row * p.ldg + col, p.type, g);
-        load_cols<VEC>(p.u, row * p.ldu + col, p.type, u);
+    for (int64_t row = (int64_t)blockIdx.y * ty + threadIdx.x / tx; row < p.m; row += 2 * step) {
+        Raw<T, VEC> dr[2], gr[2], ur[2];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            float value, slope;
-            act_both(g[e], p.act, value, slope);
-            g[e] = d[e] * u[e] * slope;
-            u[e] = d[e] * value;
+        for (int i = 0; i < 2; ++i) {
+            const int64_t r = row + i * step;
+            if (r >= p.m) continue;
+            raw_load(dr[i], p.dh, r * p.lddh + col, T);
+            raw_load(gr[i], p.g, r * p.ldg + col, T);
+            raw_load(ur[i], p.u, r * p.ldu + col, T);
         }
-        store_cols<VEC>(p.dg, row * p.ldd + col, p.type, g);
-        store_cols<VEC>(p.du, row * p.ldd + col, p.type, u);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int64_t r = row + i * step;
+            if (r >= p.m) continue;
+            float d[VEC], g[VEC], u[VEC];
+            raw_values(dr[i], T, d);
+            raw_values(gr[i], T, g);
+            raw_values(ur[i], T, u);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                float value, slope;
+                act_both(g[e], ACT, value, slope);
+                g[e] = d[e] * u[e] * slope;
+                u[e] = d[e] * value;
+            }
+            store_vec<VEC>(p.dg, r * p.ldd + col, T, g);
+            store_vec<VEC>(p.du, r * p.ldd + col, T, u);
+        }
     }
 }
 
@@ -126,6 +142,20 @@ __global__ void __launch_bounds__(256) join_partials_kernel(const float* partial
         for (int k = 1; k < 8; ++k) t += sm[k][x];
         store_elem(out, r * ld + c, type, t);
     }
+}
+
+// Calls f with the 16-bit type and the activation as constants.
+template <class F>
+void for_type_act(int type, int act, F f)
+{
+    const auto with_type = [&](auto t) {
+        if (act == GS_ACT_SILU) f(t, std::integral_constant<int, GS_ACT_SILU>());
+        else if (act == GS_ACT_GELU) f(t, std::integral_constant<int, GS_ACT_GELU>());
+        else if (act == GS_ACT_RELU) f(t, std::integral_constant<int, GS_ACT_RELU>());
+        else f(t, std::integral_constant<int, GS_ACT_NONE>());
+    };
+    if (type == GS_BF16) with_type(std::integral_constant<int, GS_BF16>());
+    else with_type(std::integral_constant<int, GS_F16>());
 }
 
 // Thread columns of an elementwise block: a power of two that covers the row
@@ -281,8 +311,16 @@ extern "C" gs_status gs_linear_bwd(const gs_linear_bwd_args* args, void* ws, siz
         const int v = vec ? 8 : 1, tx = thread_cols(n, v);
         const int64_t slabs = slabs_for(m, n, v);
         const dim3 grid((unsigned)((n + (int64_t)tx * v - 1) / ((int64_t)tx * v)), (unsigned)slabs);
-        if (vec) dz_kernel<8><<<grid, kElemThreads, 0, st>>>(p, tx);
-        else dz_kernel<1><<<grid, kElemThreads, 0, st>>>(p, tx);
+        for_type_act(a.type, a.act, [&](auto t, auto act) {
+            constexpr int T = decltype(t)::value, ACT = decltype(act)::value;
+            if (a.dy_type == a.type) {
+                if (vec) dz_kernel<T, T, 8, ACT><<<grid, kElemThreads, 0, st>>>(p, tx);
+                else dz_kernel<T, T, 1, ACT><<<grid, kElemThreads, 0, st>>>(p, tx);
+            } else {
+                if (vec) dz_kernel<T, kAnyType, 8, ACT><<<grid, kElemThreads, 0, st>>>(p, tx);
+                else dz_kernel<T, kAnyType, 1, ACT><<<grid, kElemThreads, 0, st>>>(p, tx);
+            }
+        });
         GS_LAUNCH_CHECK();
         if (a.db) {
             const gs_status s = join_partials(p.partial, slabs, 1, n, n, a.db, n, a.db_type, st);
@@ -392,11 +430,14 @@ extern "C" gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* w
     const bool vec = f % 8 == 0 && rows16(a.dh, a.lddh, a.type) && rows16(a.g, a.ldg, a.type) &&
                      rows16(a.u, a.ldu, a.type);
     const int v = vec ? 8 : 1, tx = thread_cols(f, v), ty = kElemThreads / tx;
-    int64_t gy = (m + ty - 1) / ty;
+    int64_t gy = (m + 2 * ty - 1) / (2 * ty);
     if (gy > 65535) gy = 65535;
     const dim3 grid((unsigned)((f + (int64_t)tx * v - 1) / ((int64_t)tx * v)), (unsigned)gy);
-    if (vec) glu_grad_kernel<8><<<grid, kElemThreads, 0, st>>>(p, tx);
-    else glu_grad_kernel<1><<<grid, kElemThreads, 0, st>>>(p, tx);
+    for_type_act(a.type, a.act, [&](auto t, auto act) {
+        constexpr int T = decltype(t)::value, ACT = decltype(act)::value;
+        if (vec) glu_grad_kernel<T, 8, ACT><<<grid, kElemThreads, 0, st>>>(p, tx);
+        else glu_grad_kernel<T, 1, ACT><<<grid, kElemThreads, 0, st>>>(p, tx);
+    });
     GS_LAUNCH_CHECK();
     cx.a[0].p = cw.a[0].p = p.dg;
     cx.a[1].p = cw.a[1].p = p.du;

@@ -7,6 +7,8 @@
 // smallest power of two of threads that covers the row at kVec elements a
 // thread (16-byte accesses where every row allows them, single elements
 // otherwise), so narrow rows share a warp and wide ones take a block.
+#include <type_traits>
+
 #include "gemm.cuh"
 
 namespace gs {
@@ -47,113 +49,131 @@ __device__ __forceinline__ float group_reduce(float v, int group, float* sm)
     return r;
 }
 
-template <int VEC>
-__device__ __forceinline__ void load_vec(const void* p, int64_t i, int type, float (&v)[VEC])
-{
-    if constexpr (VEC == 8) load8(p, i, type, v);
-    else v[0] = load_elem(p, i, type);
-}
-template <int VEC>
-__device__ __forceinline__ void store_vec(void* p, int64_t i, int type, const float (&v)[VEC])
-{
-    if constexpr (VEC == 8) store8(p, i, type, v);
-    else store_elem(p, i, type, v[0]);
-}
-
 // NORM: gs_rms_norm; otherwise gs_quantize_rows (weight 1, no rstd).
-// A block takes blockDim / group rows at a time.
-template <int VEC, int NV, bool NORM>
-__global__ void __launch_bounds__(1024) norm_fwd_kernel(gs_rms_norm_args a, int group)
+// A group takes R rows at a time, all their loads in flight together; with R rows
+// the lanes share out the rows' scalar work (root, quotients), which otherwise
+// costs every lane as many instructions as the row's elements.
+template <int T, int VEC, int NV, int R, bool NORM>
+__global__ void __launch_bounds__(R > 1 ? 256 : 1024) norm_fwd_kernel(gs_rms_norm_args a, int group)
 {
     __shared__ float sm[32];
     const int lane = threadIdx.x % group;
-    const int rows_per_block = blockDim.x / group;
+    const int64_t rows_per_block = (int64_t)(blockDim.x / group) * R;
     const int nvec = (int)((a.cols + VEC - 1) / VEC);
     const float inv_cols = 1.0f / (float)a.cols;
     const bool q8 = a.y_type == GS_E4M3;
     const int64_t step = (int64_t)gridDim.x * rows_per_block;
-    // every thread of a warp runs the same number of rounds (the reductions use whole warps)
-    for (int64_t row0 = (int64_t)blockIdx.x * rows_per_block; row0 < a.rows; row0 += step) {
-        const int64_t row = row0 + threadIdx.x / group;
-        const bool live = row < a.rows;
-        float s[NV][VEC];
-        float ss = 0.0f;
+    float w[NV][VEC];
+    if (NORM) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = lane + j * group;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) s[j][e] = 0.0f;
-            if (live && c < nvec) {
-                load_vec<VEC>(a.x, row * a.ldx + (int64_t)c * VEC, a.type, s[j]);
-                if (NORM && a.residual) {
-                    float r[VEC];
-                    load_vec<VEC>(a.residual, row * a.ldr + (int64_t)c * VEC, a.type, r);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) s[j][e] += r[e];
-                }
-            }
+            for (int e = 0; e < VEC; ++e) w[j][e] = 0.0f;
+            if (lane + j * group < nvec) load_vec<VEC>(a.weight, (int64_t)(lane + j * group) * VEC, a.weight_type, w[j]);
         }
-        float rstd = 1.0f;
-        if (NORM) {
+    }
+    // every thread of a warp runs the same number of rounds (the reductions use whole warps)
+    for (int64_t row0 = (int64_t)blockIdx.x * rows_per_block; row0 < a.rows; row0 += step) {
+        const int64_t row = row0 + (int64_t)(threadIdx.x / group) * R;
+        float s[R][NV][VEC];
+        Raw<T, VEC> xr[R][NV], rr[R][NV];
+#pragma unroll
+        for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int c = lane + j * group;
-                if (a.sum && live && c < nvec) store_vec<VEC>(a.sum, row * a.lds + (int64_t)c * VEC, a.type, s[j]);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) ss = __fmaf_rn(s[j][e], s[j][e], ss);
+                raw_zero(xr[i][j]);
+                raw_zero(rr[i][j]);
+                if (row + i < a.rows && c < nvec) {
+                    raw_load(xr[i][j], a.x, (row + i) * a.ldx + (int64_t)c * VEC, T);
+                    if (NORM && a.residual) raw_load(rr[i][j], a.residual, (row + i) * a.ldr + (int64_t)c * VEC, T);
+                }
             }
-            ss = group_reduce<Sum>(ss, group, sm);
-            rstd = 1.0f / sqrtf(ss * inv_cols + a.eps);
-            if (a.rstd && live && lane == 0) a.rstd[row] = rstd;
-        }
-        float top = 0.0f;
+        float ss[R], top[R];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = lane + j * group;
-            if (c < nvec) {
+        for (int i = 0; i < R; ++i) {
+            ss[i] = top[i] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = lane + j * group;
+                raw_values(xr[i][j], T, s[i][j]);
                 if (NORM) {
-                    float w[VEC];
-                    load_vec<VEC>(a.weight, (int64_t)c * VEC, a.weight_type, w);
+                    float r[VEC];
+                    raw_values(rr[i][j], T, r);
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) s[j][e] = q8 ? s[j][e] * w[e] : (s[j][e] * rstd) * w[e];
+                    for (int e = 0; e < VEC; ++e) {
+                        s[i][j][e] += r[e];
+                        ss[i] = __fmaf_rn(s[i][j][e], s[i][j][e], ss[i]);
+                    }
+                    if (a.sum && row + i < a.rows && c < nvec)
+                        store_vec<VEC>(a.sum, (row + i) * a.lds + (int64_t)c * VEC, T, s[i][j]);
+                    if (q8) {
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) s[i][j][e] *= w[j][e];
+                    }
                 }
                 if (q8) {
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) top = max_nan(top, fabsf(s[j][e]));
+                    for (int e = 0; e < VEC; ++e) top[i] = max_nan(top[i], fabsf(s[i][j][e]));
                 }
             }
         }
-        if (q8) {
-            // e4m3 keeps 4 significant bits; the row's largest magnitude goes to 448
-            top = max_nan(group_reduce<Max>(top, group, sm), kTiny);
-            const float to8 = kE4m3Max / top;
-            if (live && lane == 0) a.y_scale[row] = (top / kE4m3Max) * rstd;
+        // scalar work: every lane for R == 1, lane i (mod R) for row i otherwise
+        float rstd[R], to8[R];
+        if (NORM) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j)
+            for (int i = 0; i < R; ++i) ss[i] = group_reduce<Sum>(ss[i], group, sm);
+        }
+        if (q8) {   // e4m3 keeps 4 significant bits; the row's largest magnitude goes to 448
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) s[j][e] *= to8;
+            for (int i = 0; i < R; ++i) top[i] = max_nan(group_reduce<Max>(top[i], group, sm), kTiny);
+        }
+        const int mine = R == 1 ? 0 : lane % R;
+        float my_ss = ss[0], my_top = top[0];
+#pragma unroll
+        for (int i = 1; i < R; ++i)
+            if (mine == i) my_ss = ss[i], my_top = top[i];
+        const float my_rstd = NORM ? 1.0f / sqrtf(my_ss * inv_cols + a.eps) : 1.0f;
+        const float my_to8 = q8 ? kE4m3Max / my_top : 1.0f;
+        if (lane < R && row + mine < a.rows) {
+            if (NORM && a.rstd) a.rstd[row + mine] = my_rstd;
+            if (q8) a.y_scale[row + mine] = (my_top / kE4m3Max) * my_rstd;
         }
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = lane + j * group;
-            if (live && c < nvec) store_vec<VEC>(a.y, row * a.ldy + (int64_t)c * VEC, a.y_type, s[j]);
+        for (int i = 0; i < R; ++i) {
+            const float factor = q8 ? my_to8 : my_rstd;
+            rstd[i] = to8[i] = R == 1 ? factor : __shfl_sync(0xffffffffu, factor, (threadIdx.x & 31) / group * group + i);
         }
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = lane + j * group;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    if (q8) s[i][j][e] *= to8[i];
+                    else s[i][j][e] = (s[i][j][e] * rstd[i]) * w[j][e];
+                }
+                if (row + i < a.rows && c < nvec)
+                    store_vec<VEC>(a.y, (row + i) * a.ldy + (int64_t)c * VEC, a.y_type, s[i][j]);
+            }
     }
 }
 
 // Gradients.  dweight: every thread keeps its columns' sums over the rows it
 // visits; a block joins its groups in order and writes one partial row, and
 // join_partials_kernel (linear.cu) adds the blocks' rows in order.
-template <int VEC, int NV>
-__global__ void __launch_bounds__(1024) norm_bwd_kernel(gs_rms_norm_bwd_args a, int group, float* partial)
+// R rows a group at a time, their loads in flight together.
+template <int T, int TDY, int VEC, int NV, int R>
+__global__ void __launch_bounds__(R > 1 ? 256 : 1024) norm_bwd_kernel(gs_rms_norm_bwd_args a, int group, float* partial)
 {
-    extern __shared__ float part[];   // [rows_per_block][cols rounded up] when a block holds several groups
+    extern __shared__ float part[];   // [groups][columns rounded up] when a block holds several groups
     __shared__ float sm[32];
     const int lane = threadIdx.x % group;
-    const int rows_per_block = blockDim.x / group;
+    const int groups = blockDim.x / group;
     const int nvec = (int)((a.cols + VEC - 1) / VEC);
     const float inv_cols = 1.0f / (float)a.cols;
-    const int64_t step = (int64_t)gridDim.x * rows_per_block;
+    const int64_t step = (int64_t)gridDim.x * groups * R;
     float w[NV][VEC], acc[NV][VEC];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -162,51 +182,64 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(gs_rms_norm_bwd_args a, 
         for (int e = 0; e < VEC; ++e) w[j][e] = acc[j][e] = 0.0f;
         if (c < nvec) load_vec<VEC>(a.weight, (int64_t)c * VEC, a.weight_type, w[j]);
     }
-    for (int64_t row0 = (int64_t)blockIdx.x * rows_per_block; row0 < a.rows; row0 += step) {
-        const int64_t row = row0 + threadIdx.x / group;
-        const bool live = row < a.rows;
-        float s[NV][VEC], g[NV][VEC];
-        float dot = 0.0f;
+    for (int64_t row0 = (int64_t)blockIdx.x * groups * R; row0 < a.rows; row0 += step) {
+        const int64_t row = row0 + (int64_t)(threadIdx.x / group) * R;
+        float s[R][NV][VEC], g[R][NV][VEC], rstd[R];
+        Raw<T, VEC> sr[R][NV], dr[R][NV];
+        Raw<TDY, VEC> gr[R][NV];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = lane + j * group;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) s[j][e] = g[j][e] = 0.0f;
-            if (live && c < nvec) {
-                load_vec<VEC>(a.sum, row * a.lds + (int64_t)c * VEC, a.type, s[j]);
-                load_vec<VEC>(a.dy, row * a.lddy + (int64_t)c * VEC, a.dy_type, g[j]);
-            }
-        }
-        const float rstd = live ? a.rstd[row] : 0.0f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                acc[j][e] = __fmaf_rn(g[j][e], s[j][e] * rstd, acc[j][e]);
-                g[j][e] *= w[j][e];
-                dot = __fmaf_rn(g[j][e], s[j][e], dot);
-            }
-        if (a.dx) {
-            dot = group_reduce<Sum>(dot, group, sm);
-            const float c2 = dot * inv_cols * rstd * rstd;
+        for (int i = 0; i < R; ++i) {
+            rstd[i] = row + i < a.rows ? a.rstd[row + i] : 0.0f;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int c = lane + j * group;
-                if (live && c < nvec) {
-                    float d[VEC];
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) d[e] = 0.0f;
-                    if (a.dsum) load_vec<VEC>(a.dsum, row * a.ldds + (int64_t)c * VEC, a.type, d);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) d[e] = __fmaf_rn(rstd, __fmaf_rn(-s[j][e], c2, g[j][e]), d[e]);
-                    store_vec<VEC>(a.dx, row * a.lddx + (int64_t)c * VEC, a.type, d);
+                raw_zero(sr[i][j]);
+                raw_zero(gr[i][j]);
+                raw_zero(dr[i][j]);
+                if (row + i < a.rows && c < nvec) {
+                    raw_load(sr[i][j], a.sum, (row + i) * a.lds + (int64_t)c * VEC, T);
+                    raw_load(gr[i][j], a.dy, (row + i) * a.lddy + (int64_t)c * VEC, a.dy_type);
+                    if (a.dx && a.dsum) raw_load(dr[i][j], a.dsum, (row + i) * a.ldds + (int64_t)c * VEC, T);
                 }
+            }
+        }
+        float dot[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            dot[i] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                raw_values(sr[i][j], T, s[i][j]);
+                raw_values(gr[i][j], a.dy_type, g[i][j]);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    acc[j][e] = __fmaf_rn(g[i][j][e], s[i][j][e] * rstd[i], acc[j][e]);
+                    g[i][j][e] *= w[j][e];
+                    dot[i] = __fmaf_rn(g[i][j][e], s[i][j][e], dot[i]);
+                }
+            }
+        }
+        if (!a.dx) continue;
+#pragma unroll
+        for (int i = 0; i < R; ++i) dot[i] = group_reduce<Sum>(dot[i], group, sm);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const float c2 = dot[i] * inv_cols * rstd[i] * rstd[i];
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = lane + j * group;
+                float d[VEC];
+                raw_values(dr[i][j], T, d);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) d[e] = __fmaf_rn(rstd[i], __fmaf_rn(-s[i][j][e], c2, g[i][j][e]), d[e]);
+                if (row + i < a.rows && c < nvec)
+                    store_vec<VEC>(a.dx, (row + i) * a.lddx + (int64_t)c * VEC, T, d);
             }
         }
     }
     if (!a.dweight) return;
     float* out = partial + (int64_t)blockIdx.x * a.cols;
-    if (rows_per_block == 1) {
+    if (groups == 1) {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -225,10 +258,13 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(gs_rms_norm_bwd_args a, 
     __syncthreads();
     for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
         float t = 0.0f;
-        for (int r = 0; r < rows_per_block; ++r) t += part[r * width + c];
+        for (int r = 0; r < groups; ++r) t += part[r * width + c];
         out[c] = t;
     }
 }
+
+template <int V>
+using Type = std::integral_constant<int, V>;
 
 struct Shape {
     int nv, group, threads;
@@ -245,7 +281,7 @@ Shape shape_for(int64_t cols, int vec)
     if (vec == 1)
         while (s.group < 1024 && nvec > 8 * (int64_t)s.group) s.group *= 2;
     s.nv = 1;
-    while ((int64_t)s.nv * s.group < nvec) s.nv *= 2;
+    while ((int64_t)s.nv * s.group < nvec) s.nv *= vec == 8 ? 2 : 4;
     s.threads = s.group < 256 ? 256 : s.group;
     return s;
 }
@@ -266,21 +302,29 @@ gs_status run_fwd(const gs_rms_norm_args& a, cudaStream_t st)
                      (!NORM || aligned16(a.weight)) &&
                      (a.y_type == GS_E4M3 ? ((uintptr_t)a.y & 7u) == 0 && a.ldy % 8 == 0 : rows16(a.y, a.ldy, a.y_type));
     const Shape s = shape_for(a.cols, vec ? 8 : 1);
-    const int rpb = s.threads / s.group;
     const int sms = sm_count();
     if (sms <= 0) return GS_ERR_CUDA;
-    const int64_t want = (a.rows + rpb - 1) / rpb, most = (int64_t)sms * (2048 / s.threads);
+    // four rows a group where a group is within a warp, holds one vector a lane and
+    // there are rows enough to fill the SMs all the same
+    const bool four = vec && s.group >= 4 && s.group <= 32 && s.nv == 1 && a.rows >= (int64_t)sms * 4 * (s.threads / s.group) * 4;
+    const int rpb = s.threads / s.group * (four ? 4 : 1);
+    const int64_t want = (a.rows + rpb - 1) / rpb, most = (int64_t)sms * (four ? 2 : 2048 / s.threads);
     const int grid = (int)(want < most ? want : most);
-#define GS_FWD(V, N) norm_fwd_kernel<V, N, NORM><<<grid, s.threads, 0, st>>>(a, s.group)
-    if (vec) {
-        if (s.nv == 1) GS_FWD(8, 1);
-        else GS_FWD(8, 2);
-    } else if (s.nv <= 1) GS_FWD(1, 1);
-    else if (s.nv == 2) GS_FWD(1, 2);
-    else if (s.nv == 4) GS_FWD(1, 4);
-    else if (s.nv == 8) GS_FWD(1, 8);
-    else GS_FWD(1, 16);
+    const auto run = [&](auto t) {
+        constexpr int T = decltype(t)::value;
+#define GS_FWD(V, N, R) norm_fwd_kernel<T, V, N, R, NORM><<<grid, s.threads, 0, st>>>(a, s.group)
+        if (vec) {
+            if (four) GS_FWD(8, 1, 4);
+            else if (s.nv == 1) GS_FWD(8, 1, 1);
+            else GS_FWD(8, 2, 1);
+        } else if (s.nv <= 1) GS_FWD(1, 1, 1);
+        else if (s.nv <= 4) GS_FWD(1, 4, 1);
+        else GS_FWD(1, 16, 1);
 #undef GS_FWD
+    };
+    if (a.type == GS_F32) run(Type<GS_F32>());
+    else if (a.type == GS_BF16) run(Type<GS_BF16>());
+    else run(Type<GS_F16>());
     GS_LAUNCH_CHECK();
     return GS_OK;
 }
@@ -335,7 +379,7 @@ extern "C" gs_status gs_rms_norm_bwd(const gs_rms_norm_bwd_args* args, void* ws,
     if (!type_float(a.type) || !type_float(a.dy_type) || !type_float(a.weight_type)) return GS_ERR_INVALID_ARG;
     const int sms = sm_count();
     // one partial row per block; the size is the same whatever the alignment of the arrays
-    const int64_t blocks = 2 * (sms > 0 ? sms : 152);
+    const int64_t blocks = 3 * (sms > 0 ? sms : 152);
     const size_t need = a.dweight ? (size_t)round_up(blocks * a.cols * 4, 256) : 0;
     const WsCheck wc = ws_check(ws, ws_bytes, need);
     if (wc == WsCheck::kBad) return GS_ERR_INVALID_ARG;
@@ -357,23 +401,32 @@ extern "C" gs_status gs_rms_norm_bwd(const gs_rms_norm_bwd_args* args, void* ws,
                      (!a.dsum || rows16(a.dsum, a.ldds, a.type)) && (!a.dx || rows16(a.dx, a.lddx, a.type)) &&
                      aligned16(a.weight);
     const int v = vec ? 8 : 1;
-    Shape s = shape_for(a.cols, v);
-    if (s.threads < 512) s.threads = 512;
-    const int rpb = s.threads / s.group;
-    const int64_t want = (a.rows + rpb - 1) / rpb;
+    const Shape s = shape_for(a.cols, v);
+    const int groups = s.threads / s.group;
+    const bool two = vec && s.threads == 256 && s.nv == 1 && a.rows >= blocks * groups * 2;   // rows enough to fill the SMs
+    const int64_t rpb = groups * (two ? 2 : 1), want = (a.rows + rpb - 1) / rpb;
     const int grid = (int)(want < blocks ? want : blocks);
-    const size_t smem = rpb > 1 && a.dweight ? (size_t)rpb * s.nv * s.group * v * 4 : 0;   // at most 32 KB
+    const size_t smem = groups > 1 && a.dweight ? (size_t)groups * s.nv * s.group * v * 4 : 0;   // at most 16 KB
     float* part = (float*)ws;
-#define GS_BWD(V, N) norm_bwd_kernel<V, N><<<grid, s.threads, smem, st>>>(a, s.group, part)
-    if (vec) {
-        if (s.nv == 1) GS_BWD(8, 1);
-        else GS_BWD(8, 2);
-    } else if (s.nv <= 1) GS_BWD(1, 1);
-    else if (s.nv == 2) GS_BWD(1, 2);
-    else if (s.nv == 4) GS_BWD(1, 4);
-    else if (s.nv == 8) GS_BWD(1, 8);
-    else GS_BWD(1, 16);
+    const auto run = [&](auto t, auto tdy) {
+        constexpr int T = decltype(t)::value, TDY = decltype(tdy)::value;
+#define GS_BWD(V, N, R) norm_bwd_kernel<T, TDY, V, N, R><<<grid, s.threads, smem, st>>>(a, s.group, part)
+        if (vec) {
+            if (two) GS_BWD(8, 1, 2);
+            else if (s.nv == 1) GS_BWD(8, 1, 1);
+            else GS_BWD(8, 2, 1);
+        } else if (s.nv <= 1) GS_BWD(1, 1, 1);
+        else if (s.nv <= 4) GS_BWD(1, 4, 1);
+        else GS_BWD(1, 16, 1);
 #undef GS_BWD
+    };
+    const auto pick = [&](auto t) {
+        if (a.dy_type == a.type) run(t, t);
+        else run(t, Type<kAnyType>());
+    };
+    if (a.type == GS_F32) pick(Type<GS_F32>());
+    else if (a.type == GS_BF16) pick(Type<GS_BF16>());
+    else pick(Type<GS_F16>());
     GS_LAUNCH_CHECK();
     if (a.dweight) return join_partials(part, grid, 1, a.cols, a.cols, a.dweight, a.cols, a.weight_type, st);
     return GS_OK;

@@ -67,29 +67,37 @@ def _bad(what):
     raise ValueError(what)
 
 
-def _matrix(t, name, dtypes, device, cols=None, rows=None):
-    """(pointer, leading dimension, rows, columns) of a tensor seen as rows."""
+def _wrong(t, name, dtypes, device):
+    """Raises for a tensor of another type or device (the slow path of the checks)."""
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
         _bad(f"{name}: expected a tensor of {[str(d) for d in dtypes]}, got {getattr(t, 'dtype', type(t))}")
-    if t.device != device:
-        _bad(f"{name}: on {t.device}, expected {device}")
-    if t.dim() == 0:
-        _bad(f"{name}: needs at least one dimension")
-    if t.dim() != 2:
+    _bad(f"{name}: on {t.device}, expected {device}")
+
+
+def _matrix(t, name, dtypes, device, cols=None, rows=None):
+    """(pointer, leading dimension, rows, columns) of a tensor seen as rows."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.device != device:
+        _wrong(t, name, dtypes, device)
+    shape = t.shape
+    if len(shape) != 2:
+        if not shape:
+            _bad(f"{name}: needs at least one dimension")
         try:
-            t = t.view(-1, t.shape[-1]) if t.shape[-1] else t.reshape(0, 0)
+            t = t.view(-1, shape[-1]) if shape[-1] else t.reshape(0, 0)
         except RuntimeError:
             _bad(f"{name}: leading dimensions do not merge into one stride {tuple(t.shape)} {t.stride()}")
-    n, c = t.shape
+        shape = t.shape
+    n, c = shape
     if cols is not None and c != cols:
         _bad(f"{name}: {c} columns, expected {cols}")
     if rows is not None and n != rows:
         _bad(f"{name}: {n} rows, expected {rows}")
-    if c > 1 and t.stride(1) != 1:
+    ld, unit = t.stride()
+    if unit != 1 and c > 1:
         _bad(f"{name}: the last dimension is not contiguous {t.stride()}")
-    # the pitch of a single row is never used: one that keeps the row aligned
-    ld = t.stride(0) if n > 1 else (c + 15) // 16 * 16
-    if ld < c:
+    if n <= 1:   # the pitch of a single row is never used: one that keeps the row aligned
+        ld = (c + 15) & ~15
+    elif ld < c:
         _bad(f"{name}: rows overlap (stride {ld}, {c} columns)")
     return t.data_ptr(), ld, n, c
 
@@ -97,63 +105,81 @@ def _matrix(t, name, dtypes, device, cols=None, rows=None):
 def _vector(t, name, dtypes, device, size):
     if t is None:
         return 0
-    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
-        _bad(f"{name}: expected a tensor of {[str(d) for d in dtypes]}, got {getattr(t, 'dtype', type(t))}")
-    if t.device != device:
-        _bad(f"{name}: on {t.device}, expected {device}")
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.device != device:
+        _wrong(t, name, dtypes, device)
     if t.numel() != size or (size > 1 and not t.is_contiguous()):
         _bad(f"{name}: expected {size} contiguous values, got {tuple(t.shape)} {t.stride()}")
     return t.data_ptr()
 
 
 def _device(t, name):
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         _bad(f"{name}: expected a CUDA tensor, got {t.device if isinstance(t, torch.Tensor) else type(t)}")
     return t.device
 
 
 def _act(act):
-    if act not in _ACTS:
+    code = _ACTS.get(act)
+    if code is None:
         _bad(f"act: {act!r} is not one of {[a for a in _ACTS if a]}")
-    return _ACTS[act]
+    return code
 
 
-def _padded(shape, cols, dtype, device):
-    """An uninitialised output [*shape, cols] whose rows are 16-byte aligned."""
-    per = 16 // torch.empty((), dtype=dtype).element_size() if cols % 8 else 0
-    if not per or cols % per == 0:
-        return torch.empty((*shape, cols), dtype=dtype, device=device)
-    return torch.empty((*shape, (cols + per - 1) // per * per), dtype=dtype, device=device)[..., :cols]
+_PER_16 = {torch.float32: 4, torch.bfloat16: 8, torch.float16: 8, torch.float8_e4m3fn: 16}
+
+
+def _output(lead, rows, cols, dtype, device):
+    """An uninitialised [*lead, cols] whose rows are 16-byte aligned, its pointer and leading dimension."""
+    per = _PER_16[dtype]
+    ld = (cols + per - 1) // per * per
+    t = torch.empty((*lead, ld), dtype=dtype, device=device)
+    p = t.data_ptr()
+    return (t if ld == cols else t[..., :cols]), p, ld
 
 
 class _On:
-    """Makes the tensors' device current around a call when it is not."""
+    """Makes the tensors' device current around a call."""
 
     def __init__(self, device):
-        self.guard = torch.cuda.device(device) if device.index != torch.cuda.current_device() else None
+        self.guard = torch.cuda.device(device)
 
     def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
+        self.guard.__enter__()
 
     def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+        self.guard.__exit__(*exc)
 
 
 def _stream(device):
     return torch.cuda.current_stream(device).cuda_stream
 
 
-def _call(name, args, device):
+def _run(f, device, *args):
+    """f(*args, stream) with the tensors' device current."""
+    if device.index == torch.cuda.current_device():
+        f(*args, _stream(device))
+    else:
+        with _On(device):
+            f(*args, _stream(device))
+
+
+def _scratch(f, name, device, args):
     """A layer call with the scratch it asks for, on the current stream."""
-    with _On(device):
-        n = abi.layer_ws_bytes(name, args)
-        if n:
-            ws = torch.empty(n, dtype=torch.uint8, device=device)
-            getattr(abi, name)(args, ws.data_ptr(), n, _stream(device))
-        else:
-            getattr(abi, name)(args, None, None, _stream(device))
+    n = abi.layer_ws_bytes(name, args)
+    if n:
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        _run(f, device, args, ws.data_ptr(), n)
+    else:
+        _run(f, device, args, None, None)
+
+
+def _call(name, args, device):
+    f = getattr(abi, name)
+    if device.index == torch.cuda.current_device():
+        _scratch(f, name, device, args)
+    else:
+        with _On(device):
+            _scratch(f, name, device, args)
 
 
 # ------------------------------------------------------------------ norm
@@ -176,10 +202,8 @@ def rms_norm(x, weight, *, residual=None, eps=1e-6, out_dtype=None, need_backwar
     s = x
     if residual is not None:
         pr, ldr, _, _ = _matrix(residual, "residual", (x.dtype,), dev, cols, rows)
-        s = _padded(lead, cols, x.dtype, dev)
-        ps, lds, _, _ = _matrix(s, "s", (x.dtype,), dev, cols, rows)
-    y = _padded(lead, cols, out_dtype, dev)
-    py, ldy, _, _ = _matrix(y, "y", (out_dtype,), dev, cols, rows)
+        s, ps, lds = _output(lead, rows, cols, x.dtype, dev)
+    y, py, ldy = _output(lead, rows, cols, out_dtype, dev)
     scale = rstd = None
     if out_dtype == torch.float8_e4m3fn:
         scale = torch.empty(lead, dtype=torch.float32, device=dev)
@@ -188,9 +212,8 @@ def rms_norm(x, weight, *, residual=None, eps=1e-6, out_dtype=None, need_backwar
         rstd = torch.empty(lead, dtype=torch.float32, device=dev)
         prstd = rstd.data_ptr()
     if rows:
-        with _On(dev):
-            abi.gs_rms_norm(rows, cols, px, ldx, pr, ldr, pw, py, ldy, pscale, ps, lds, prstd, eps, _TYPES[x.dtype],
-                            _TYPES[weight.dtype], _TYPES[out_dtype], _stream(dev))
+        _run(abi.gs_rms_norm, dev, rows, cols, px, ldx, pr, ldr, pw, py, ldy, pscale, ps, lds, prstd, eps,
+             _TYPES[x.dtype], _TYPES[weight.dtype], _TYPES[out_dtype])
     return NormOut(y, scale, s, rstd)
 
 
@@ -208,8 +231,7 @@ def rms_norm_backward(dy, s, weight, rstd, *, ds=None):
     pds = ldds = 0
     if ds is not None:
         pds, ldds, _, _ = _matrix(ds, "ds", (s.dtype,), dev, cols, rows)
-    dx = _padded(s.shape[:-1], cols, s.dtype, dev)
-    pdx, lddx, _, _ = _matrix(dx, "dx", (s.dtype,), dev)
+    dx, pdx, lddx = _output(s.shape[:-1], rows, cols, s.dtype, dev)
     dw = torch.empty(weight.shape, dtype=weight.dtype, device=dev)
     _call("gs_rms_norm_bwd", abi.rms_norm_bwd_args(rows, cols, pdy, lddy, ps, lds, pw, prstd, pds, ldds, pdx, lddx,
                                                    dw.data_ptr(), _TYPES[s.dtype], _TYPES[dy.dtype],
@@ -222,12 +244,10 @@ def quantize_rows(x):
     the float32 scale that restores it: x ~ q * scale[..., None]."""
     dev = _device(x, "x")
     px, ldx, rows, cols = _matrix(x, "x", _FLOAT, dev)
-    q = _padded(x.shape[:-1], cols, torch.float8_e4m3fn, dev)
-    pq, ldq, _, _ = _matrix(q, "q", (torch.float8_e4m3fn,), dev)
+    q, pq, ldq = _output(x.shape[:-1], rows, cols, torch.float8_e4m3fn, dev)
     scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
     if rows:
-        with _On(dev):
-            abi.gs_quantize_rows(rows, cols, px, ldx, pq, ldq, scale.data_ptr(), _TYPES[x.dtype], _stream(dev))
+        _run(abi.gs_quantize_rows, dev, rows, cols, px, ldx, pq, ldq, scale.data_ptr(), _TYPES[x.dtype])
     return q, scale
 
 
@@ -257,14 +277,16 @@ def linear(x, w, bias=None, *, x_scale=None, w_scale=None, act=None, residual=No
     pr = ldr = pz = ldz = 0
     if residual is not None:
         pr, ldr, _, _ = _matrix(residual, "residual", (out_dtype,), dev, n, rows)
-    y = _padded(lead, n, out_dtype, dev) if out is None else out
-    py, ldy, _, _ = _matrix(y, "out", (out_dtype,), dev, n, rows)
+    if out is None:
+        y, py, ldy = _output(lead, rows, n, out_dtype, dev)
+    else:
+        y = out
+        py, ldy, _, _ = _matrix(y, "out", (out_dtype,), dev, n, rows)
     z = None
     if need_backward and code != abi.GS_ACT_NONE:
         if x.dtype not in _HALF:
             _bad("need_backward: 8-bit operands have no gradients")
-        z = _padded(lead, n, x.dtype, dev)
-        pz, ldz, _, _ = _matrix(z, "z", (x.dtype,), dev)
+        z, pz, ldz = _output(lead, rows, n, x.dtype, dev)
     _call("gs_linear", abi.linear_args(rows, k, n, px, ldx, pw, ldw, pxs, pws, pb, pr, ldr, py, ldy, pz, ldz,
                                        _TYPES[x.dtype], _TYPES[bias.dtype] if bias is not None else 0,
                                        _TYPES[out_dtype], code), dev)
@@ -294,11 +316,10 @@ def linear_backward(dy, x, w, *, z=None, act=None, bias=False, need_dx=True, nee
         _bad(f"db_dtype: {db_dtype}")
     dx = dw = db = None
     if need_dx:
-        dx = _padded(x.shape[:-1], k, x.dtype, dev)
-        pdx, lddx, _, _ = _matrix(dx, "dx", (x.dtype,), dev)
+        dx, pdx, lddx = _output(x.shape[:-1], rows, k, x.dtype, dev)
     if need_dw:
         dw = torch.empty((n, k), dtype=dw_dtype, device=dev)
-        pdw, lddw, _, _ = _matrix(dw, "dw", (dw_dtype,), dev)
+        pdw, lddw = dw.data_ptr(), k
     if bias:
         db = torch.empty(n, dtype=db_dtype, device=dev)
         pdb = db.data_ptr()
@@ -328,16 +349,14 @@ def glu(x, w_gate, w_up, *, x_scale=None, gate_scale=None, up_scale=None, act="s
     if out_dtype not in _HALF:
         _bad(f"out_dtype: {out_dtype}")
     lead = x.shape[:-1]
-    h = _padded(lead, f, out_dtype, dev)
-    ph, ldh, _, _ = _matrix(h, "h", (out_dtype,), dev)
+    h, ph, ldh = _output(lead, rows, f, out_dtype, dev)
     g = u = None
     pg = ldg = pu = ldu = 0
     if need_backward:
         if x.dtype not in _HALF:
             _bad("need_backward: 8-bit operands have no gradients")
-        g, u = _padded(lead, f, out_dtype, dev), _padded(lead, f, out_dtype, dev)
-        pg, ldg, _, _ = _matrix(g, "g", (out_dtype,), dev)
-        pu, ldu, _, _ = _matrix(u, "u", (out_dtype,), dev)
+        g, pg, ldg = _output(lead, rows, f, out_dtype, dev)
+        u, pu, ldu = _output(lead, rows, f, out_dtype, dev)
     _call("gs_glu", abi.glu_args(rows, k, f, px, ldx, pg_, ldwg, pu_, ldwu, pxs, pgs, pus, ph, ldh, pg, ldg, pu, ldu,
                                  _TYPES[x.dtype], _TYPES[out_dtype], _act(act)), dev)
     return GluOut(h, g, u)
@@ -358,12 +377,10 @@ def glu_backward(dh, x, w_gate, w_up, g, u, *, act="silu", need_dx=True, need_dw
     dx = dwg = dwu = None
     pdx = lddx = pdwg = lddwg = pdwu = lddwu = 0
     if need_dx:
-        dx = _padded(x.shape[:-1], k, x.dtype, dev)
-        pdx, lddx, _, _ = _matrix(dx, "dx", (x.dtype,), dev)
+        dx, pdx, lddx = _output(x.shape[:-1], rows, k, x.dtype, dev)
     if need_dw:
         dwg, dwu = (torch.empty((f, k), dtype=dw_dtype, device=dev) for _ in range(2))
-        pdwg, lddwg, _, _ = _matrix(dwg, "dw_gate", (dw_dtype,), dev)
-        pdwu, lddwu, _, _ = _matrix(dwu, "dw_up", (dw_dtype,), dev)
+        pdwg, lddwg, pdwu, lddwu = dwg.data_ptr(), k, dwu.data_ptr(), k
     _call("gs_glu_bwd", abi.glu_bwd_args(rows, k, f, pdh, lddh, px, ldx, pwg, ldwg, pwu, ldwu, pg, ldg, pu, ldu, pdx,
                                          lddx, pdwg, lddwg, pdwu, lddwu, _TYPES[x.dtype], _TYPES[dw_dtype], _act(act)),
           dev)
