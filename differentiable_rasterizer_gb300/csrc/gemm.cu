@@ -2,11 +2,15 @@
 //
 //   D[m][n] = sum_k A[m][k] B[n][k], fp32 accumulators, epilogue on the way out
 //
-// One persistent CTA an SM (or a pair of CTAs on two SMs), 10 warps with fixed roles:
+// One persistent CTA an SM (or a pair of CTAs on two SMs), 18 warps with fixed roles:
 //   warp 0      TMA producer: tiles of A and B into a ring of 128-byte-swizzled stages
-//   warp 1      issues tcgen05.mma into one of two TMEM accumulators
-//   warps 2-9   epilogue: accumulator -> registers -> scale, bias, activation, gate,
-//               residual -> shared memory -> TMA store, while the next tile accumulates
+//   warp 1      issues tcgen05.mma into one of two to four TMEM accumulators
+//   warps 2-17  epilogue: accumulator -> registers -> scale, bias, activation, gate ->
+//               shared memory -> residual, row stores, while the next tiles accumulate.
+//               Sixteen warps of few registers and short rolled loops: eight warps with
+//               a whole row of 32 columns each in registers issued one instruction in
+//               three cycles, waiting for instruction fetches and for each other
+//               (1,000,000 x 64 -> 128 gated layer: 289 us)
 // Either factor may have k as its fast or its slow index (the gradients contract over
 // rows and over output features), so no operand is ever transposed in memory.
 //
@@ -23,17 +27,17 @@ namespace {
 
 using namespace tc;
 
-constexpr int kWarps = 10;
+constexpr int kWarps = 18;
 constexpr int kThreads = kWarps * 32;
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;
 constexpr int kRowsA = 128;                      // accumulator rows of a CTA
 constexpr int kStageRow = 128;                   // bytes of k a stage holds per row
-constexpr int kSlotBytes = 8192;                 // staging of one epilogue warp
-constexpr int kChunk = 32;                       // columns an epilogue warp handles at a time
+constexpr int kSlot = 4096;                      // staging of one epilogue warp: 32 rows of 128 bytes
+constexpr int kGroupCols = 64;                   // output columns of a group of four epilogue warps
 constexpr int kGroupM = 8;                       // m-tiles that run together (L2 reuse of B)
 
 struct Params {
-    CUtensorMap a[2], b[2], y[2], r, z, z2;
+    CUtensorMap a[2], b[2];
     int64_t m, n;
     const float* x_scale;
     const float* w_scale[2];
@@ -43,19 +47,20 @@ struct Params {
     void* zp;
     void* z2p;
     int64_t ldr, ldy[2], ldz, ldz2;
-    int64_t k_blocks;         // of one term
-    int64_t tiles_m, tiles_n, units;
-    int splits, terms, probs; // k ranges; products summed; independent products
+    int64_t part;             // elements of one partial sum
+    uint32_t k_blocks;        // of one term
+    uint32_t tiles_m, tiles_n, units;
+    uint32_t splits, terms, probs;   // k ranges; products summed; independent products
     int k_elems;              // k of a stage
     int a_fast, b_fast, e4m3;
     uint32_t idesc;
     int bias_type, out_type, z_type, act;
-    int y_tma, r_tma, z_tma, partial;
+    int y_vec, r_vec, z_vec, partial;
 };
 
 __device__ int g_wait_expired;
 
-template <int BN, bool PAIR>
+template <int BN, bool PAIR, bool GLU>
 struct Shape {
     static constexpr int kTileM = PAIR ? 256 : 128;
     static constexpr int kRowsB = PAIR ? BN / 2 : BN;                  // rows of B a CTA holds
@@ -63,49 +68,55 @@ struct Shape {
     static constexpr int kBytesB = kRowsB * kStageRow;
     static constexpr int kStageBytes = kBytesA + kBytesB;
     static constexpr int kStages = BN == 64 ? 6 : 5;
-    static constexpr int kTmemCols = 2 * BN;
-    static constexpr int kBars = kStages * 2 + 4 + kEpiWarps * 4 + 2;   // even: what follows is 16-byte aligned
-    static constexpr int kSmem = kStages * kStageBytes + kEpiWarps * kSlotBytes + kBars * 8 + 16 +
-                                 kEpiWarps * 2 * kChunk * 4;
+    // Four groups of epilogue warps, 64 output columns each: all on one tile, or tiles in turn.
+    static constexpr int kOutCols = GLU ? BN / 2 : BN;
+    static constexpr int kGroupsTile = kOutCols / kGroupCols;
+    static constexpr int kTurns = 4 / kGroupsTile;
+    static constexpr int kAccs = kTurns > 2 ? kTurns : 2;              // accumulators in TMEM
+    static constexpr int kTmemCols = kAccs * BN;
+    static_assert(kTmemCols <= 512, "TMEM of an SM");
+    static constexpr int kBars = kStages * 2 + kAccs * 2 + 2;          // even: what follows is 16-byte aligned
+    static constexpr int kSmem = kStages * kStageBytes + kEpiWarps * kSlot + kBars * 8 + 16 + kEpiWarps * 32 * 4;
 };
 
 struct Unit {
-    int prob, split;
-    int64_t tm, tn, kb0, kb1;
+    uint32_t prob, split, tm, tn, kb0, kb1;
 };
 
-__device__ __forceinline__ Unit decode(const Params& p, int64_t u)
+__device__ __forceinline__ Unit decode(const Params& p, uint32_t u)
 {
     Unit r;
-    const int64_t tiles = p.tiles_m * p.tiles_n, per_split = tiles * p.probs;
-    r.split = (int)(u / per_split);
-    const int64_t rest = u % per_split;
-    r.prob = (int)(rest % p.probs);
-    const int64_t t = rest / p.probs;
-    const int64_t per_group = kGroupM * p.tiles_n, first = t / per_group * kGroupM, in = t % per_group;
-    const int64_t rows = p.tiles_m - first < kGroupM ? p.tiles_m - first : kGroupM;
-    r.tm = first + in % rows;
+    const uint32_t kb = p.k_blocks * p.terms;
+    r.split = r.prob = 0;
+    r.kb0 = 0;
+    r.kb1 = kb;
+    if (p.splits > 1) {
+        const uint32_t per_split = p.tiles_m * p.tiles_n * p.probs;
+        r.split = u / per_split;
+        u -= r.split * per_split;
+        r.kb0 = (uint32_t)((uint64_t)kb * r.split / p.splits);
+        r.kb1 = (uint32_t)((uint64_t)kb * (r.split + 1) / p.splits);
+    }
+    if (p.probs > 1) {
+        r.prob = u & 1;
+        u >>= 1;
+    }
+    if (p.tiles_n == 1) {
+        r.tm = u;
+        r.tn = 0;
+        return r;
+    }
+    const uint32_t per_group = kGroupM * p.tiles_n, first = u / per_group * kGroupM, in = u % per_group;
+    const uint32_t rows = p.tiles_m - first < kGroupM ? p.tiles_m - first : kGroupM;
     r.tn = in / rows;
-    const int64_t kb = p.k_blocks * p.terms;
-    r.kb0 = kb * r.split / p.splits;
-    r.kb1 = kb * (r.split + 1) / p.splits;
+    r.tm = first + (in - r.tn * rows);
     return r;
 }
 
-// Byte of 16-byte piece j of row r in a staging slot: 64-byte rows under the 64-byte
-// swizzle (16-bit elements), 128-byte rows under the 128-byte swizzle (32-bit ones).
-template <int ESZ>
-__device__ __forceinline__ uint32_t slot_piece(int r, int j)
-{
-    return ESZ == 2 ? r * 64 + ((j ^ ((r >> 1) & 3)) << 4) : r * 128 + ((j ^ (r & 7)) << 4);
-}
-// Byte of element c of row r.
-template <int ESZ>
-__device__ __forceinline__ uint32_t slot_elem(int r, int c)
-{
-    return slot_piece<ESZ>(r, c * ESZ >> 4) + ((c * ESZ) & 15);
-}
-
+// Byte of 16-byte piece j of row r in a staging slot: 32 rows of 128 bytes (64 columns
+// in 16 bits, 32 in 32) under the 128-byte swizzle, so that a thread's row and a
+// group of eight threads' row are both free of bank conflicts.
+__device__ __forceinline__ uint32_t slot_piece(int r, int j) { return r * 128 + ((j ^ (r & 7)) << 4); }
 __device__ __forceinline__ void st_shared16(uint32_t a, uint4 v)
 {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -117,102 +128,152 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t a)
     return v;
 }
 
-// A row's 32 values into a slot, rounded to the output's type, and a slot's row added.
+__device__ __forceinline__ uint16_t ld_shared_u16(uint32_t a)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t a)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// 16 values of a thread's row into a slot: in 16 bits (pieces 2 step, 2 step + 1 of
+// 64 columns) or in fp32 (four pieces of 32 columns).
 template <int T>
-__device__ __forceinline__ void slot_write_half(uint32_t slot, int row, const float (&v)[kChunk])
+__device__ __forceinline__ void slot_put_half(uint32_t slot, int row, int step, const float (&v)[16])
 {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        st_shared16(slot + slot_piece<2>(row, j),
+    for (int j = 0; j < 2; ++j)
+        st_shared16(slot + slot_piece(row, 2 * step + j),
                     make_uint4(pack_half2(v[8 * j], v[8 * j + 1], T), pack_half2(v[8 * j + 2], v[8 * j + 3], T),
                                pack_half2(v[8 * j + 4], v[8 * j + 5], T), pack_half2(v[8 * j + 6], v[8 * j + 7], T)));
 }
-template <int T>
-__device__ __forceinline__ void slot_add_half(uint32_t slot, int row, float (&v)[kChunk])
+__device__ __forceinline__ void slot_put(uint32_t slot, int row, int step, const float (&v)[16])
 {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint4 q = ld_shared16(slot + slot_piece<2>(row, j));
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    for (int j = 0; j < 4; ++j)
+        st_shared16(slot + slot_piece(row, 4 * step + j),
+                    make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
+                               __float_as_uint(v[4 * j + 3])));
+}
+
+// A slot of 64 16-bit columns to memory: eight threads a row, 16 bytes each, where the
+// rows are aligned (vec); single elements otherwise and where a row ends inside a
+// piece.  Plain stores: they need no proxy fence and no wait before the slot is used
+// again, and write nothing beside the matrix (a TMA store writes whole 16-byte pieces).
+__device__ __forceinline__ void store_half(uint32_t slot, void* p, int64_t ld, int64_t row0, int64_t col0, int64_t m,
+                                           int64_t n, bool vec, int lane)
+{
+    const int rows = m - row0 < 32 ? (int)(m - row0) : 32, cols = n - col0 < 64 ? (int)(n - col0) : 64;
+    if (vec) {
+        const int j = lane & 7, r0 = lane >> 3, left = cols - 8 * j;
+        uint16_t* at = (uint16_t*)p + (row0 + r0) * ld + col0 + 8 * j;
+        if (left >= 8) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = unpack_half2(w[i], T);
-            v[8 * j + 2 * i] += f.x;
-            v[8 * j + 2 * i + 1] += f.y;
+            for (int i = 0; i < 8; ++i)
+                if (r0 + 4 * i < rows)
+                    *reinterpret_cast<uint4*>(at + 4 * i * ld) = ld_shared16(slot + slot_piece(r0 + 4 * i, j));
+        } else {
+            for (int r = r0; r < rows; r += 4, at += 4 * ld)
+                for (int e = 0; e < left; ++e) at[e] = ld_shared_u16(slot + slot_piece(r, j) + 2 * e);
         }
+    } else {
+        for (int c = lane; c < cols; c += 32)
+            for (int r = 0; r < rows; ++r)
+                ((uint16_t*)p)[(row0 + r) * ld + col0 + c] = ld_shared_u16(slot + slot_piece(r, c >> 3) + 2 * (c & 7));
     }
 }
-template <int ESZ>
-__device__ __forceinline__ void slot_write(uint32_t slot, int row, const float (&v)[kChunk], int type)
+
+// The residual's part of a 32 x 32 chunk, in the layout in which store_chunk writes:
+// fetched before the accumulator is read.
+template <int OSZ>
+struct Residual {
+    uint4 q[32 * OSZ / 16];
+};
+template <int OSZ>
+__device__ __forceinline__ void fetch_residual(Residual<OSZ>& res, const void* p, int64_t ld, int64_t row0, int64_t col0,
+                                               int64_t m, int64_t n, int lane)
 {
-    if constexpr (ESZ == 2) {
-        if (type == GS_BF16) slot_write_half<GS_BF16>(slot, row, v);
-        else slot_write_half<GS_F16>(slot, row, v);
-    } else {
+    constexpr int kPer = 16 / OSZ, kPieces = 32 / kPer, kRows = 32 / kPieces;
+    const int j = lane % kPieces, r0 = lane / kPieces;
+    const char* at = (const char*)p + ((row0 + r0) * ld + col0 + kPer * j) * OSZ;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            st_shared16(slot + slot_piece<4>(row, j),
-                        make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
-                                   __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
+    for (int i = 0; i < 32 / kRows; ++i) {
+        res.q[i] = make_uint4(0, 0, 0, 0);
+        if (row0 + r0 + i * kRows < m && col0 + kPer * (j + 1) <= n)
+            res.q[i] = *reinterpret_cast<const uint4*>(at + (int64_t)i * kRows * ld * OSZ);
     }
 }
-template <int ESZ>
-__device__ __forceinline__ void slot_add(uint32_t slot, int row, float (&v)[kChunk], int type)
+
+// A slot of 32 fp32 columns to memory, the residual added and rounded once: 16 bytes a
+// thread where the rows are aligned, single elements otherwise.
+template <int OSZ, int T>
+__device__ __forceinline__ void store_chunk(uint32_t slot, const Residual<OSZ>& res, const void* resp, int64_t ldr, void* p,
+                                            int64_t ld, int64_t row0, int64_t col0, int64_t m, int64_t n, bool y_vec,
+                                            bool r_vec, int lane)
 {
-    if constexpr (ESZ == 2) {
-        if (type == GS_BF16) slot_add_half<GS_BF16>(slot, row, v);
-        else slot_add_half<GS_F16>(slot, row, v);
-    } else {
+    constexpr int kPer = 16 / OSZ, kPieces = 32 / kPer, kRows = 32 / kPieces;
+    const int rows = m - row0 < 32 ? (int)(m - row0) : 32, cols = n - col0 < 32 ? (int)(n - col0) : 32;
+    const bool vec = y_vec && (r_vec || !resp);
+    const int j = lane % kPieces, r0 = lane / kPieces, left = cols - kPer * j;
+    if (vec && left >= kPer) {
+        char* at = (char*)p + ((row0 + r0) * ld + col0 + kPer * j) * OSZ;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint4 q = ld_shared16(slot + slot_piece<4>(row, j));
-            v[4 * j] += __uint_as_float(q.x);
-            v[4 * j + 1] += __uint_as_float(q.y);
-            v[4 * j + 2] += __uint_as_float(q.z);
-            v[4 * j + 3] += __uint_as_float(q.w);
+        for (int i = 0; i < 32 / kRows; ++i) {
+            const int r = r0 + i * kRows;
+            if (r < rows) {
+                uint4 out = ld_shared16(slot + slot_piece(r, OSZ == 4 ? j : 2 * j));
+                if constexpr (OSZ == 4) {
+                    if (resp) {
+                        out.x = __float_as_uint(__uint_as_float(out.x) + __uint_as_float(res.q[i].x));
+                        out.y = __float_as_uint(__uint_as_float(out.y) + __uint_as_float(res.q[i].y));
+                        out.z = __float_as_uint(__uint_as_float(out.z) + __uint_as_float(res.q[i].z));
+                        out.w = __float_as_uint(__uint_as_float(out.w) + __uint_as_float(res.q[i].w));
+                    }
+                } else {
+                    const uint4 hi = ld_shared16(slot + slot_piece(r, 2 * j + 1));
+                    const float2 a = unpack_half2(res.q[i].x, T), b = unpack_half2(res.q[i].y, T),
+                                 c = unpack_half2(res.q[i].z, T), d = unpack_half2(res.q[i].w, T);
+                    out = make_uint4(pack_half2(__uint_as_float(out.x) + a.x, __uint_as_float(out.y) + a.y, T),
+                                     pack_half2(__uint_as_float(out.z) + b.x, __uint_as_float(out.w) + b.y, T),
+                                     pack_half2(__uint_as_float(hi.x) + c.x, __uint_as_float(hi.y) + c.y, T),
+                                     pack_half2(__uint_as_float(hi.z) + d.x, __uint_as_float(hi.w) + d.y, T));
+                }
+                *reinterpret_cast<uint4*>(at + (int64_t)i * kRows * ld * OSZ) = out;
+            }
+        }
+    } else if (vec) {   // the row ends inside this thread's piece
+        for (int r = r0; r < rows; r += kRows)
+            for (int e = 0; e < left; ++e) {
+                const int c = kPer * j + e;
+                float v = ld_shared_f32(slot + slot_piece(r, c >> 2) + 4 * (c & 3));
+                if (resp) v += load_elem(resp, (row0 + r) * ldr + col0 + c, T);
+                store_elem(p, (row0 + r) * ld + col0 + c, T, v);
+            }
+    } else if (lane < cols) {
+        for (int r = 0; r < rows; ++r) {
+            float v = ld_shared_f32(slot + slot_piece(r, lane >> 2) + 4 * (lane & 3));
+            if (resp) v += load_elem(resp, (row0 + r) * ldr + col0 + lane, T);
+            store_elem(p, (row0 + r) * ld + col0 + lane, T, v);
         }
     }
 }
 
-// Rows of any alignment: the warp moves a chunk between a slot and memory, one row
-// of consecutive columns at a time.
-template <int ESZ>
-__device__ __forceinline__ void slot_to_rows(uint32_t slot, void* p, int64_t ld, int64_t row0, int64_t col0, int64_t m,
-                                             int64_t n, int lane)
+template <int ACT>
+__device__ __forceinline__ void activate(float (&v)[16])
 {
-    const int64_t col = col0 + lane;
-    if (col >= n) return;
-    const int rows = m - row0 < 32 ? (int)(m - row0) : 32;
-    for (int r = 0; r < rows; ++r) {
-        const uint32_t a = slot + slot_elem<ESZ>(r, lane);
-        if constexpr (ESZ == 2) {
-            uint16_t v;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
-            ((uint16_t*)p)[(row0 + r) * ld + col] = v;
-        } else {
-            uint32_t v;
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-            ((uint32_t*)p)[(row0 + r) * ld + col] = v;
-        }
-    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = act_value(v[j], ACT);
 }
-template <int ESZ>
-__device__ __forceinline__ void rows_to_slot(uint32_t slot, const void* p, int64_t ld, int64_t row0, int64_t col0,
-                                             int64_t m, int64_t n, int lane)
+__device__ __forceinline__ void activate(float (&v)[16], int act)
 {
-    const int64_t col = col0 + lane;
-#pragma unroll 8
-    for (int r = 0; r < 32; ++r) {
-        const uint32_t a = slot + slot_elem<ESZ>(r, lane);
-        const bool live = col < n && row0 + r < m;
-        if constexpr (ESZ == 2) {
-            const uint16_t v = live ? ((const uint16_t*)p)[(row0 + r) * ld + col] : (uint16_t)0;
-            asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(v) : "memory");
-        } else {
-            const uint32_t v = live ? ((const uint32_t*)p)[(row0 + r) * ld + col] : 0u;
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-        }
-    }
+    if (act == GS_ACT_SILU) activate<GS_ACT_SILU>(v);
+    else if (act == GS_ACT_GELU) activate<GS_ACT_GELU>(v);
+    else if (act == GS_ACT_RELU) activate<GS_ACT_RELU>(v);
 }
 
 // GLU: B's rows are half gate, half up; the epilogue joins column c with c + BN/2.
@@ -220,7 +281,7 @@ __device__ __forceinline__ void rows_to_slot(uint32_t slot, const void* p, int64
 template <int BN, bool PAIR, bool GLU, int OSZ>
 __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ Params p)
 {
-    using S = Shape<BN, PAIR>;
+    using S = Shape<BN, PAIR, GLU>;
     extern __shared__ __align__(1024) char smem_raw[];   // the swizzle patterns repeat every 1024 bytes
     const uint32_t base = smem_addr(smem_raw);
     if (base & 1023u) {   // every thread sees the same address; there is no padding to move within
@@ -228,28 +289,27 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         return;
     }
     const uint32_t stages = base, slots = base + S::kStages * S::kStageBytes;
-    const uint32_t bars = slots + kEpiWarps * kSlotBytes;
+    const uint32_t bars = slots + kEpiWarps * kSlot;
     const uint32_t bar_full = bars, bar_empty = bars + S::kStages * 8, bar_acc = bar_empty + S::kStages * 8,
-                   bar_free = bar_acc + 16, bar_res = bar_free + 16, bar_drain = bar_res + kEpiWarps * 32;
+                   bar_free = bar_acc + S::kAccs * 8, bar_drain = bar_free + S::kAccs * 8;
     char* tail = smem_raw + (bars + S::kBars * 8 - base);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail);
     volatile int* gave_up = reinterpret_cast<volatile int*>(tail + 4);
-    float* columns = reinterpret_cast<float*>(tail + 16);   // [warp][2][chunk]: scale, bias (or the second scale)
+    float* columns = reinterpret_cast<float*>(tail + 16);   // [warp][2][16]: scale, bias (or the second scale)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? cluster_rank() : 0;
-    const int64_t first = PAIR ? blockIdx.x >> 1 : blockIdx.x, step = PAIR ? gridDim.x >> 1 : gridDim.x;
+    const uint32_t first = PAIR ? blockIdx.x >> 1 : blockIdx.x, step = PAIR ? gridDim.x >> 1 : gridDim.x;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(bar_full + 8 * i, 1);
             mbar_init(bar_empty + 8 * i, 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < S::kAccs; ++i) {
             mbar_init(bar_acc + 8 * i, 1);
-            mbar_init(bar_free + 8 * i, kEpiWarps * (PAIR ? 2 : 1));
+            mbar_init(bar_free + 8 * i, 4 * S::kGroupsTile * (PAIR ? 2 : 1));
         }
-        for (int i = 0; i < kEpiWarps * 4; ++i) mbar_init(bar_res + 8 * i, 1);
         mbar_init(bar_drain, 1);
         *gave_up = 0;
         mbar_init_fence();
@@ -269,11 +329,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             const uint32_t full0 = PAIR ? map_rank(bar_full, 0) : bar_full;   // the pair counts at its first CTA
             uint32_t it = 0;
             bool ok = true;
-            for (int64_t u = first; u < p.units && ok; u += step) {
+            for (uint32_t u = first; u < p.units && ok; u += step) {
                 const Unit q = decode(p, u);
                 const int row_a = (int)(q.tm * S::kTileM + rank * kRowsA);
                 const int row_b = GLU ? (int)(q.tn * (BN / 2)) : (int)(q.tn * BN + rank * S::kRowsB);
-                for (int64_t kb = q.kb0; kb < q.kb1; ++kb, ++it) {
+                for (uint32_t kb = q.kb0; kb < q.kb1; ++kb, ++it) {
                     const int s = it % S::kStages;
                     if (!mbar_wait(bar_empty + 8 * s, ((it / S::kStages) & 1) ^ 1, gave_up)) {
                         ok = false;
@@ -316,13 +376,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             const uint32_t step_a = k_step(p.a_fast), step_b = k_step(p.b_fast);
             uint32_t it = 0, tile = 0;
             bool ok = true;
-            for (int64_t u = first; u < p.units && ok; u += step, ++tile) {
+            for (uint32_t u = first; u < p.units && ok; u += step, ++tile) {
                 const Unit q = decode(p, u);
-                const uint32_t acc = tile & 1;
-                if (!mbar_wait(bar_free + 8 * acc, ((tile >> 1) & 1) ^ 1, gave_up)) break;
+                const uint32_t acc = tile % S::kAccs;
+                if (!mbar_wait(bar_free + 8 * acc, ((tile / S::kAccs) & 1) ^ 1, gave_up)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + acc * BN;
-                for (int64_t kb = q.kb0; kb < q.kb1; ++kb, ++it) {
+                for (uint32_t kb = q.kb0; kb < q.kb1; ++kb, ++it) {
                     const int s = it % S::kStages;
                     if (!mbar_wait(bar_full + 8 * s, (it / S::kStages) & 1, gave_up)) {
                         ok = false;
@@ -351,195 +411,123 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         }
     } else {
         // -------------------------------------------------------------- epilogue
-        const int ew = warp - 2, quarter = warp & 3, half = ew >> 2;
-        constexpr int kOutCols = GLU ? BN / 2 : BN;
-        constexpr int kChunks = kOutCols / 2 / kChunk > 0 ? kOutCols / 2 / kChunk : 1;
-        static_assert(kChunks * kChunk * 2 == kOutCols, "two halves of whole chunks");
-        const uint32_t slot = slots + ew * kSlotBytes;
-        const uint32_t res = bar_res + ew * 32;
+        const int quarter = warp & 3, group = (warp - 2) >> 2;
+        const int turn = group / S::kGroupsTile, col_group = group % S::kGroupsTile;
+        const uint32_t slot = slots + (warp - 2) * kSlot;
         const uint32_t free0 = PAIR ? map_rank(bar_free, 0) : bar_free;
-        float* col_a = columns + ew * 2 * kChunk;
-        float* col_b = col_a + kChunk;
-        // staging: buffers of y and where the saved projections go
-        const bool save = p.zp != nullptr;
-        const int bufs = OSZ == 4 ? (save ? 1 : 2) : (GLU ? (save ? 1 : 4) : (save ? 2 : 4));
-        const uint32_t buf_bytes = kChunk * 32 * OSZ;
-        const uint32_t z_at = OSZ == 4 ? 4096 : (GLU ? 2048 : 4096);
-        const bool has_res = !GLU && p.residual != nullptr;
-        uint32_t chunk_no = 0, tile = 0;
-        bool ok = true;
-        for (int64_t u = first; u < p.units && ok; u += step, ++tile) {
+        float* const factors = columns + (warp - 2) * 32;
+        const bool has_factors = p.e4m3 || p.bias;
+        const int passes = p.zp ? (GLU ? 3 : 2) : 1;
+        uint32_t tile = 0;
+        for (uint32_t u = first; u < p.units; u += step, ++tile) {
+            if (S::kTurns > 1 && (int)(tile % S::kTurns) != turn) continue;
+            const uint32_t acc = tile % S::kAccs;
             const Unit q = decode(p, u);
-            const uint32_t acc = tile & 1;
-            const int64_t row0 = q.tm * S::kTileM + rank * kRowsA + quarter * 32;
-            const int64_t base_col = q.tn * kOutCols + half * (kOutCols / 2);
-            const bool rows_live = row0 < p.m;
-            const int chunks = !rows_live || base_col >= p.n
-                                   ? 0
-                                   : (int)((p.n - base_col + kChunk - 1) / kChunk < kChunks
-                                               ? (p.n - base_col + kChunk - 1) / kChunk
-                                               : kChunks);
-            // residual chunks are fetched one ahead; the first before the accumulator is waited for
-            auto fetch = [&](uint32_t no, int c) {
-                const uint32_t b = no % bufs;
-                if (lane == 0) {
-                    mbar_expect(res + 8 * b, buf_bytes);
-                    tma_load_2d<false>(slot + b * buf_bytes, &p.r, (int)(base_col + c * kChunk), (int)row0, res + 8 * b);
+            const int64_t row0 = (int64_t)q.tm * S::kTileM + rank * kRowsA + quarter * 32;
+            const int64_t col0 = (int64_t)q.tn * S::kOutCols + col_group * kGroupCols;
+            const bool live = row0 < p.m && col0 < p.n;
+            const float xs = p.x_scale && row0 + lane < p.m ? p.x_scale[row0 + lane] : 1.0f;
+            if (!__all_sync(0xffffffffu, mbar_wait(bar_acc + 8 * acc, (tile / S::kAccs) & 1, gave_up))) break;
+            tc_fence_after();
+            const uint32_t d = tmem + ((uint32_t)(quarter * 32) << 16) + acc * BN + col_group * kGroupCols;
+
+            // 16 columns from c on, as pass `pass` of `passes` wants them: gate, up, product
+            // (pass 0, 1, last of a gated layer); pre-activation, activation (pass 0, last)
+            const auto columns16 = [&](int c, int pass, float (&v)[16]) {
+                const bool last = pass == passes - 1;
+                if (has_factors) {   // the columns' factors: lanes 0-15 the first, 16-31 the second
+                    const int64_t col = col0 + c + (lane & 15);
+                    float f = lane < 16 || GLU ? 1.0f : 0.0f;
+                    if (col < p.n) {
+                        if (lane < 16) f = p.w_scale[0] ? p.w_scale[0][col] : 1.0f;
+                        else if constexpr (GLU) f = p.w_scale[1] ? p.w_scale[1][col] : 1.0f;
+                        else f = p.bias ? load_elem(p.bias, col, p.bias_type) : 0.0f;
+                    }
+                    __syncwarp();   // the last readers are done
+                    factors[lane] = f;
+                    __syncwarp();
+                }
+                uint32_t raw[16];
+                tmem_ld16(d + c + (GLU && !last && pass == 1 ? BN / 2 : 0), raw);
+                if constexpr (GLU) {
+                    if (last) {
+                        uint32_t up[16];
+                        tmem_ld16(d + c + BN / 2, up);
+                        tmem_ld_wait(raw);
+                        tmem_ld_wait(up);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            v[j] = __uint_as_float(raw[j]) * (p.e4m3 ? xs * factors[j] : 1.0f);
+                        activate(v, p.act);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            v[j] *= __uint_as_float(up[j]) * (p.e4m3 ? xs * factors[16 + j] : 1.0f);
+                        return;
+                    }
+                    tmem_ld_wait(raw);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        v[j] = __uint_as_float(raw[j]) * (p.e4m3 ? xs * factors[pass * 16 + j] : 1.0f);
+                } else {
+                    tmem_ld_wait(raw);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(raw[j]);
+                    if (has_factors) {
+                        if (p.e4m3) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) v[j] *= xs * factors[j];
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] += factors[16 + j];
+                    }
+                    if (last) activate(v, p.act);
                 }
             };
-            if (has_res && p.r_tma && chunks > 0 && bufs > 1) {
-                if (lane == 0) {   // the buffer's last store has been read
-                    if (bufs == 2) bulk_wait_read<1>();
-                    else bulk_wait_read<3>();
-                }
-                fetch(chunk_no, 0);
-            }
-            const float xs = p.x_scale && row0 + lane < p.m ? p.x_scale[row0 + lane] : 1.0f;
-            // column factors of the warp's chunks, one a lane, fetched before the accumulator is waited for
-            float ca[kChunks], cb[kChunks];
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                const int64_t col = base_col + c * kChunk + lane;
-                const bool live = c < chunks && col < p.n;
-                ca[c] = p.w_scale[0] && live ? p.w_scale[0][col] : 1.0f;
-                if constexpr (GLU) cb[c] = p.w_scale[1] && live ? p.w_scale[1][col] : 1.0f;
-                else cb[c] = p.bias && live ? load_elem(p.bias, col, p.bias_type) : 0.0f;
-            }
-            if (!__all_sync(0xffffffffu, mbar_wait(bar_acc + 8 * acc, (tile >> 1) & 1, gave_up))) {
-                ok = false;
-                // a residual chunk may be in flight: let it land
-                if (has_res && p.r_tma && chunks > 0 && bufs > 1) {
-                    volatile int still = 0;
-                    mbar_wait(res + 8 * (chunk_no % bufs), (chunk_no / bufs) & 1, &still);
-                }
-                break;
-            }
-            __syncwarp();
-            tc_fence_after();
-            const uint32_t d = tmem + ((uint32_t)(quarter * 32) << 16) + acc * BN + half * (kOutCols / 2);
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                if (c >= chunks) break;
-                const int64_t col0 = base_col + c * kChunk;
-                const uint32_t b = chunk_no % bufs, ys = slot + b * buf_bytes;
-                const uint32_t zs = slot + z_at + (bufs == 2 ? b * 2048 : 0);
-                uint32_t raw[kChunk], raw2[GLU ? kChunk : 1];
-                tmem_ld32(d + c * kChunk, raw);
-                if constexpr (GLU) tmem_ld32(d + BN / 2 + c * kChunk, raw2);
-                if (p.e4m3 || p.bias) {
-                    __syncwarp();   // the last chunk's readers are done
-                    col_a[lane] = ca[c];
-                    col_b[lane] = cb[c];
-                }
-                if (has_res && !p.r_tma) {
-                    if (lane == 0) bulk_wait_read<0>();
+
+            for (int pass = 0; live && pass < passes; ++pass) {
+                const bool last = pass == passes - 1;
+                if (!last || (OSZ == 2 && !p.residual)) {   // 64 columns in 16 bits
+                    const int type = last ? p.out_type : p.z_type;
+                    __syncwarp();   // the slot's last readers are done
+#pragma unroll 1
+                    for (int s = 0; s < 4; ++s) {
+                        float v[16];
+                        columns16(16 * s, pass, v);
+                        if (type == GS_BF16) slot_put_half<GS_BF16>(slot, lane, s, v);
+                        else slot_put_half<GS_F16>(slot, lane, s, v);
+                    }
                     __syncwarp();
-                    rows_to_slot<OSZ>(ys, p.residual, p.ldr, row0, col0, p.m, p.n, lane);
-                }
-                if (has_res && p.r_tma) {
-                    if (bufs == 1) {
-                        if (lane == 0) bulk_wait_read<0>();
-                        fetch(chunk_no, c);
-                    } else if (c + 1 < chunks) {
-                        if (lane == 0) {
-                            if (bufs == 2) bulk_wait_read<0>();
-                            else bulk_wait_read<2>();
+                    void* const to = last ? p.yp[q.prob] : (GLU && pass == 1 ? p.z2p : p.zp);
+                    const int64_t ld = last ? p.ldy[q.prob] : (GLU && pass == 1 ? p.ldz2 : p.ldz);
+                    store_half(slot, to, ld, row0, col0, p.m, p.n, last ? p.y_vec : p.z_vec, lane);
+                } else {   // twice 32 columns in fp32, the residual added on the way out
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        const int64_t at = col0 + 32 * h;
+                        if (at >= p.n) break;
+                        Residual<OSZ> res;
+                        if (p.residual && p.r_vec) fetch_residual(res, p.residual, p.ldr, row0, at, p.m, p.n, lane);
+                        __syncwarp();
+#pragma unroll 1
+                        for (int s = 0; s < 2; ++s) {
+                            float v[16];
+                            columns16(32 * h + 16 * s, pass, v);
+                            slot_put(slot, lane, s, v);
                         }
-                        fetch(chunk_no + 1, c + 1);
-                    }
-                } else if (lane == 0) {
-                    if (bufs == 1) bulk_wait_read<0>();
-                    else if (bufs == 2) bulk_wait_read<1>();
-                    else bulk_wait_read<3>();
-                }
-                __syncwarp();
-                float v[kChunk];
-                tmem_ld_wait(raw);
-                if constexpr (GLU) {
-                    tmem_ld_wait(raw2);
-                    float g[kChunk];
-#pragma unroll
-                    for (int j = 0; j < kChunk; ++j) {
-                        g[j] = __uint_as_float(raw[j]);
-                        v[j] = __uint_as_float(raw2[j]);
-                    }
-                    if (p.e4m3) {
-#pragma unroll
-                        for (int j = 0; j < kChunk; ++j) {
-                            g[j] *= xs * col_a[j];
-                            v[j] *= xs * col_b[j];
-                        }
-                    }
-                    if (save) {
-                        slot_write<2>(slot + z_at, lane, g, p.z_type);
-                        slot_write<2>(slot + z_at + 2048, lane, v, p.z_type);
-                    }
-                    if (p.act == GS_ACT_SILU) {
-#pragma unroll
-                        for (int j = 0; j < kChunk; ++j) v[j] *= act_value(g[j], GS_ACT_SILU);
-                    } else if (p.act == GS_ACT_GELU) {
-#pragma unroll
-                        for (int j = 0; j < kChunk; ++j) v[j] *= act_value(g[j], GS_ACT_GELU);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < kChunk; ++j) v[j] *= act_value(g[j], p.act);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < kChunk; ++j) v[j] = __uint_as_float(raw[j]);
-                    if (p.e4m3) {
-#pragma unroll
-                        for (int j = 0; j < kChunk; ++j) v[j] *= xs * col_a[j];
-                    }
-                    if (p.bias) {
-#pragma unroll
-                        for (int j = 0; j < kChunk; ++j) v[j] += col_b[j];
-                    }
-                    if (save) slot_write<2>(zs, lane, v, p.z_type);
-                    if (p.act == GS_ACT_SILU) {
-#pragma unroll
-                        for (int j = 0; j < kChunk; ++j) v[j] = act_value(v[j], GS_ACT_SILU);
-                    } else if (p.act == GS_ACT_GELU) {
-#pragma unroll
-                        for (int j = 0; j < kChunk; ++j) v[j] = act_value(v[j], GS_ACT_GELU);
-                    } else if (p.act == GS_ACT_RELU) {
-#pragma unroll
-                        for (int j = 0; j < kChunk; ++j) v[j] = act_value(v[j], GS_ACT_RELU);
-                    }
-                    if (has_res) {
-                        if (p.r_tma && !__all_sync(0xffffffffu, mbar_wait(res + 8 * b, (chunk_no / bufs) & 1, gave_up))) {
-                            ok = false;
-                            break;
-                        }
-                        slot_add<OSZ>(ys, lane, v, p.out_type);
+                        __syncwarp();
+                        if constexpr (OSZ == 4) {
+                            float* const to = (float*)p.yp[p.partial ? 0 : q.prob] +
+                                              (p.partial ? (int64_t)(q.prob * p.splits + q.split) * p.part : 0);
+                            store_chunk<4, GS_F32>(slot, res, p.residual, p.ldr, to, p.ldy[p.partial ? 0 : q.prob], row0, at,
+                                                   p.m, p.n, p.y_vec, p.r_vec, lane);
+                        } else if (p.out_type == GS_BF16)
+                            store_chunk<2, GS_BF16>(slot, res, p.residual, p.ldr, p.yp[0], p.ldy[0], row0, at, p.m, p.n,
+                                                    p.y_vec, p.r_vec, lane);
+                        else
+                            store_chunk<2, GS_F16>(slot, res, p.residual, p.ldr, p.yp[0], p.ldy[0], row0, at, p.m, p.n,
+                                                   p.y_vec, p.r_vec, lane);
                     }
                 }
-                slot_write<OSZ>(ys, lane, v, p.out_type);
-                fence_async_smem();
-                __syncwarp();
-                // a TMA store writes whole 16-byte pieces: the last chunk of a row that ends
-                // inside a piece goes by plain stores, which touch nothing beside it
-                const bool ragged = col0 + kChunk > p.n;
-                const bool y_tma = p.y_tma && (p.partial || !(ragged && (p.n * OSZ & 15)));
-                const bool z_tma = p.z_tma && !(ragged && (p.n & 7));
-                if (lane == 0) {
-                    if (y_tma)
-                        tma_store_3d(&p.y[p.partial ? 0 : q.prob], ys, (int)col0, (int)row0,
-                                     p.partial ? q.prob * p.splits + q.split : 0);
-                    if (save && z_tma) {
-                        tma_store_3d(&p.z, GLU ? slot + z_at : zs, (int)col0, (int)row0, 0);
-                        if constexpr (GLU) tma_store_3d(&p.z2, slot + z_at + 2048, (int)col0, (int)row0, 0);
-                    }
-                    bulk_commit();
-                }
-                if (!y_tma)
-                    slot_to_rows<OSZ>(ys, q.prob ? p.yp[1] : p.yp[0], q.prob ? p.ldy[1] : p.ldy[0], row0, col0, p.m, p.n,
-                                      lane);
-                if (save && !z_tma) {
-                    slot_to_rows<2>(GLU ? slot + z_at : zs, p.zp, p.ldz, row0, col0, p.m, p.n, lane);
-                    if constexpr (GLU) slot_to_rows<2>(slot + z_at + 2048, p.z2p, p.ldz2, row0, col0, p.m, p.n, lane);
-                }
-                ++chunk_no;
             }
             tc_fence_before();
             __syncwarp();
@@ -548,7 +536,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 else mbar_arrive(bar_free + 8 * acc);
             }
         }
-        if (lane == 0) bulk_wait_all();
     }
     __syncthreads();
     if (threadIdx.x == 0 && *gave_up) atomicExch(&g_wait_expired, 1);
@@ -678,7 +665,7 @@ using Kernel = void (*)(const Params);
 template <int BN, bool PAIR, bool GLU, int OSZ>
 gs_status launch(const Params& p, int grid, cudaStream_t st)
 {
-    using S = Shape<BN, PAIR>;
+    using S = Shape<BN, PAIR, GLU>;
     static_assert(S::kSmem <= 232448, "shared memory of an SM");
     auto* kernel = gemm_kernel<BN, PAIR, GLU, OSZ>;
     GS_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem));
@@ -702,7 +689,7 @@ gs_status launch(const Params& p, int grid, cudaStream_t st)
 namespace tc {
 
 gs_status make_map(CUtensorMap* map, const void* p, int type, int64_t rows, int64_t cols, int64_t ld, int box_rows,
-                   int box_cols, int64_t depth)
+                   int box_cols)
 {
     using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -722,14 +709,13 @@ gs_status make_map(CUtensorMap* map, const void* p, int type, int64_t rows, int6
                                    : type == GS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                    : type == GS_F16  ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                      : CU_TENSOR_MAP_DATA_TYPE_UINT8;
-    const int dims = depth > 0 ? 3 : 2;
-    const cuuint64_t size[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)(depth > 0 ? depth : 1)};
-    const cuuint64_t pitch[2] = {(cuuint64_t)(ld * esz), (cuuint64_t)(ld * esz) * (cuuint64_t)rows};
-    const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
-    const cuuint32_t unit[3] = {1, 1, 1};
-    const CUresult r = encode(map, dt, dims, const_cast<void*>(p), size, pitch, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              box_cols * esz == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const cuuint64_t size[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t pitch[1] = {(cuuint64_t)(ld * esz)};
+    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+    const cuuint32_t unit[2] = {1, 1};
+    const CUresult r = encode(map, dt, 2, const_cast<void*>(p), size, pitch, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? GS_OK : GS_ERR_CUDA;
 }
 
@@ -783,36 +769,21 @@ gs_status gemm_run(const GemmCall& c, void* ws, cudaStream_t st)
     void* y[2] = {c.y, c.y2};
     const int64_t ldy[2] = {c.ldy, c.ldy2};
     if (p.partial) {
-        p.y_tma = 1;
-        const gs_status s = tc::make_map(&p.y[0], base + plan.partial_at, GS_F32, c.m, plan.pitch, plan.pitch, 32, kChunk,
-                                         (int64_t)plan.splits * plan.probs);
-        if (s != GS_OK) return s;
+        p.yp[0] = base + plan.partial_at;
+        p.ldy[0] = plan.pitch;
+        p.part = c.m * plan.pitch;
+        p.y_vec = 1;
     } else {
-        p.y_tma = rows16(c.y, c.ldy, c.out_type) && (plan.probs == 1 || rows16(c.y2, c.ldy2, c.out_type));
-        for (int i = 0; i < plan.probs; ++i) {
-            p.yp[i] = y[i];
-            p.ldy[i] = ldy[i];
-            if (!p.y_tma) continue;
-            const gs_status s = tc::make_map(&p.y[i], y[i], out_type, c.m, c.n, ldy[i], 32, kChunk, 1);
-            if (s != GS_OK) return s;
-        }
+        for (int i = 0; i < plan.probs; ++i) p.yp[i] = y[i], p.ldy[i] = ldy[i];
+        p.y_vec = rows16(c.y, c.ldy, c.out_type) && (plan.probs == 1 || rows16(c.y2, c.ldy2, c.out_type));
         if (c.residual) {
             p.residual = c.residual;
             p.ldr = c.ldr;
-            p.r_tma = rows16(c.residual, c.ldr, c.out_type);
-            if (p.r_tma) {
-                const gs_status s = tc::make_map(&p.r, c.residual, c.out_type, c.m, c.n, c.ldr, 32, kChunk);
-                if (s != GS_OK) return s;
-            }
+            p.r_vec = rows16(c.residual, c.ldr, c.out_type);
         }
         if (c.z) {
             p.zp = c.z, p.ldz = c.ldz, p.z2p = c.z2, p.ldz2 = c.ldz2;
-            p.z_tma = rows16(c.z, c.ldz, c.z_type) && (!glu || rows16(c.z2, c.ldz2, c.z_type));
-            if (p.z_tma) {
-                gs_status s = tc::make_map(&p.z, c.z, c.z_type, c.m, c.n, c.ldz, 32, kChunk, 1);
-                if (s == GS_OK && glu) s = tc::make_map(&p.z2, c.z2, c.z_type, c.m, c.n, c.ldz2, 32, kChunk, 1);
-                if (s != GS_OK) return s;
-            }
+            p.z_vec = rows16(c.z, c.ldz, c.z_type) && (!glu || rows16(c.z2, c.ldz2, c.z_type));
         }
         p.x_scale = c.x_scale;
         p.w_scale[0] = c.w_scale[0], p.w_scale[1] = c.w_scale[1];
@@ -820,7 +791,8 @@ gs_status gemm_run(const GemmCall& c, void* ws, cudaStream_t st)
     }
     p.m = c.m, p.n = c.n;
     p.out_type = out_type, p.z_type = c.z_type;
-    p.k_blocks = plan.k_blocks, p.tiles_m = plan.tiles_m, p.tiles_n = plan.tiles_n, p.units = plan.units;
+    p.k_blocks = (uint32_t)plan.k_blocks, p.tiles_m = (uint32_t)plan.tiles_m, p.tiles_n = (uint32_t)plan.tiles_n;
+    p.units = (uint32_t)plan.units;
     p.splits = plan.splits, p.terms = plan.terms, p.probs = plan.probs, p.k_elems = plan.k_elems;
     p.a_fast = c.a[0].k_fast, p.b_fast = c.b[0].k_fast;
     p.e4m3 = c.type == GS_E4M3;
