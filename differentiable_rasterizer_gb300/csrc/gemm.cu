@@ -182,22 +182,44 @@ __device__ __forceinline__ void store_half(uint32_t slot, void* p, int64_t ld, i
                 for (int e = 0; e < left; ++e) at[e] = ld_shared_u16(slot + slot_piece(r, j) + 2 * e);
         }
     } else {
-        for (int c = lane; c < cols; c += 32)
-            for (int r = 0; r < rows; ++r)
-                ((uint16_t*)p)[(row0 + r) * ld + col0 + c] = ld_shared_u16(slot + slot_piece(r, c >> 3) + 2 * (c & 7));
+        for (int c = lane; c < cols; c += 32) {
+            uint16_t* at = (uint16_t*)p + row0 * ld + col0 + c;
+#pragma unroll 8
+            for (int r = 0; r < 32; ++r, at += ld) {
+                const uint16_t v = ld_shared_u16(slot + slot_piece(r, c >> 3) + 2 * (c & 7));
+                if (r < rows) *at = v;
+            }
+        }
     }
 }
 
-// The residual's part of a 32 x 32 chunk, in the layout in which store_chunk writes:
-// fetched before the accumulator is read.
+// The residual's part of a 32 x 32 chunk, in the layout in which store_chunk writes
+// (16-byte pieces of rows, or a column a thread): fetched before the accumulator is read.
 template <int OSZ>
 struct Residual {
     uint4 q[32 * OSZ / 16];
 };
 template <int OSZ>
 __device__ __forceinline__ void fetch_residual(Residual<OSZ>& res, const void* p, int64_t ld, int64_t row0, int64_t col0,
-                                               int64_t m, int64_t n, int lane)
+                                               int64_t m, int64_t n, bool vec, int lane)
 {
+    if (!vec) {
+        uint32_t w[32 * OSZ / 4];
+#pragma unroll
+        for (int i = 0; i < 32 * OSZ / 4; ++i) w[i] = 0;
+        if (col0 + lane < n) {
+            const char* at = (const char*)p + (row0 * ld + col0 + lane) * OSZ;
+#pragma unroll
+            for (int r = 0; r < 32; ++r, at += ld * OSZ) {
+                if (row0 + r >= m) continue;
+                if constexpr (OSZ == 4) w[r] = *(const uint32_t*)at;
+                else w[r >> 1] |= (uint32_t)(*(const uint16_t*)at) << (16 * (r & 1));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 32 * OSZ / 16; ++i) res.q[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        return;
+    }
     constexpr int kPer = 16 / OSZ, kPieces = 32 / kPer, kRows = 32 / kPieces;
     const int j = lane % kPieces, r0 = lane / kPieces;
     const char* at = (const char*)p + ((row0 + r0) * ld + col0 + kPer * j) * OSZ;
@@ -213,12 +235,11 @@ __device__ __forceinline__ void fetch_residual(Residual<OSZ>& res, const void* p
 // thread where the rows are aligned, single elements otherwise.
 template <int OSZ, int T>
 __device__ __forceinline__ void store_chunk(uint32_t slot, const Residual<OSZ>& res, const void* resp, int64_t ldr, void* p,
-                                            int64_t ld, int64_t row0, int64_t col0, int64_t m, int64_t n, bool y_vec,
-                                            bool r_vec, int lane)
+                                            int64_t ld, int64_t row0, int64_t col0, int64_t m, int64_t n, bool vec,
+                                            int lane)
 {
     constexpr int kPer = 16 / OSZ, kPieces = 32 / kPer, kRows = 32 / kPieces;
     const int rows = m - row0 < 32 ? (int)(m - row0) : 32, cols = n - col0 < 32 ? (int)(n - col0) : 32;
-    const bool vec = y_vec && (r_vec || !resp);
     const int j = lane % kPieces, r0 = lane / kPieces, left = cols - kPer * j;
     if (vec && left >= kPer) {
         char* at = (char*)p + ((row0 + r0) * ld + col0 + kPer * j) * OSZ;
@@ -255,10 +276,15 @@ __device__ __forceinline__ void store_chunk(uint32_t slot, const Residual<OSZ>& 
                 store_elem(p, (row0 + r) * ld + col0 + c, T, v);
             }
     } else if (lane < cols) {
-        for (int r = 0; r < rows; ++r) {
+        char* at = (char*)p + (row0 * ld + col0 + lane) * OSZ;
+#pragma unroll
+        for (int r = 0; r < 32; ++r, at += ld * OSZ) {
             float v = ld_shared_f32(slot + slot_piece(r, lane >> 2) + 4 * (lane & 3));
-            if (resp) v += load_elem(resp, (row0 + r) * ldr + col0 + lane, T);
-            store_elem(p, (row0 + r) * ld + col0 + lane, T, v);
+            const uint4 q = res.q[OSZ == 4 ? r >> 2 : r >> 3];
+            const int w = OSZ == 4 ? r & 3 : (r >> 1) & 3;
+            const uint32_t word = w == 0 ? q.x : (w == 1 ? q.y : (w == 2 ? q.z : q.w));
+            if (resp) v += OSZ == 4 ? __uint_as_float(word) : (r & 1 ? unpack_half2(word, T).y : unpack_half2(word, T).x);
+            if (r < rows) store_elem(at, 0, T, v);
         }
     }
 }
@@ -418,6 +444,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         float* const factors = columns + (warp - 2) * 32;
         const bool has_factors = p.e4m3 || p.bias;
         const int passes = p.zp ? (GLU ? 3 : 2) : 1;
+        const auto factor = [&](int64_t col) -> float {
+            if (lane < 16) return p.w_scale[0] && col < p.n ? p.w_scale[0][col] : 1.0f;
+            if constexpr (GLU) return p.w_scale[1] && col < p.n ? p.w_scale[1][col] : 1.0f;
+            else return p.bias && col < p.n ? load_elem(p.bias, col, p.bias_type) : 0.0f;
+        };
         uint32_t tile = 0;
         for (uint32_t u = first; u < p.units; u += step, ++tile) {
             if (S::kTurns > 1 && (int)(tile % S::kTurns) != turn) continue;
@@ -427,6 +458,18 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             const int64_t col0 = (int64_t)q.tn * S::kOutCols + col_group * kGroupCols;
             const bool live = row0 < p.m && col0 < p.n;
             const float xs = p.x_scale && row0 + lane < p.m ? p.x_scale[row0 + lane] : 1.0f;
+            // the columns' factors, 16 columns at a time: lanes 0-15 the first, 16-31 the
+            // second; they and the residual's way into L2 start before the accumulator is waited for
+            float f0 = 1.0f, f1 = 1.0f, f2 = 1.0f, f3 = 1.0f;
+            if (has_factors && live) {
+                const int64_t col = col0 + (lane & 15);
+                f0 = factor(col), f1 = factor(col + 16), f2 = factor(col + 32), f3 = factor(col + 48);
+            }
+            if (!GLU && p.residual && live && row0 + lane < p.m) {
+                const char* at = (const char*)p.residual + ((row0 + lane) * p.ldr + col0) * OSZ;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+                if (OSZ == 4 && col0 + 32 < p.n) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 128));
+            }
             if (!__all_sync(0xffffffffu, mbar_wait(bar_acc + 8 * acc, (tile / S::kAccs) & 1, gave_up))) break;
             tc_fence_after();
             const uint32_t d = tmem + ((uint32_t)(quarter * 32) << 16) + acc * BN + col_group * kGroupCols;
@@ -435,14 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             // (pass 0, 1, last of a gated layer); pre-activation, activation (pass 0, last)
             const auto columns16 = [&](int c, int pass, float (&v)[16]) {
                 const bool last = pass == passes - 1;
-                if (has_factors) {   // the columns' factors: lanes 0-15 the first, 16-31 the second
-                    const int64_t col = col0 + c + (lane & 15);
-                    float f = lane < 16 || GLU ? 1.0f : 0.0f;
-                    if (col < p.n) {
-                        if (lane < 16) f = p.w_scale[0] ? p.w_scale[0][col] : 1.0f;
-                        else if constexpr (GLU) f = p.w_scale[1] ? p.w_scale[1][col] : 1.0f;
-                        else f = p.bias ? load_elem(p.bias, col, p.bias_type) : 0.0f;
-                    }
+                if (has_factors) {
+                    const float f = c < 32 ? (c == 0 ? f0 : f1) : (c == 32 ? f2 : f3);
                     __syncwarp();   // the last readers are done
                     factors[lane] = f;
                     __syncwarp();
@@ -456,18 +493,26 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                         tmem_ld_wait(raw);
                         tmem_ld_wait(up);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            v[j] = __uint_as_float(raw[j]) * (p.e4m3 ? xs * factors[j] : 1.0f);
+                        for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(raw[j]);
+                        if (p.e4m3) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                v[j] *= xs * factors[j];
+                                up[j] = __float_as_uint(__uint_as_float(up[j]) * (xs * factors[16 + j]));
+                            }
+                        }
                         activate(v, p.act);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            v[j] *= __uint_as_float(up[j]) * (p.e4m3 ? xs * factors[16 + j] : 1.0f);
+                        for (int j = 0; j < 16; ++j) v[j] *= __uint_as_float(up[j]);
                         return;
                     }
                     tmem_ld_wait(raw);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        v[j] = __uint_as_float(raw[j]) * (p.e4m3 ? xs * factors[pass * 16 + j] : 1.0f);
+                    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(raw[j]);
+                    if (p.e4m3) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] *= xs * factors[pass * 16 + j];
+                    }
                 } else {
                     tmem_ld_wait(raw);
 #pragma unroll
@@ -505,8 +550,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     for (int h = 0; h < 2; ++h) {
                         const int64_t at = col0 + 32 * h;
                         if (at >= p.n) break;
+                        const bool vec = p.y_vec && (p.r_vec || !p.residual);
                         Residual<OSZ> res;
-                        if (p.residual && p.r_vec) fetch_residual(res, p.residual, p.ldr, row0, at, p.m, p.n, lane);
+                        if (p.residual) fetch_residual(res, p.residual, p.ldr, row0, at, p.m, p.n, vec, lane);
                         __syncwarp();
 #pragma unroll 1
                         for (int s = 0; s < 2; ++s) {
@@ -519,13 +565,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                             float* const to = (float*)p.yp[p.partial ? 0 : q.prob] +
                                               (p.partial ? (int64_t)(q.prob * p.splits + q.split) * p.part : 0);
                             store_chunk<4, GS_F32>(slot, res, p.residual, p.ldr, to, p.ldy[p.partial ? 0 : q.prob], row0, at,
-                                                   p.m, p.n, p.y_vec, p.r_vec, lane);
+                                                   p.m, p.n, vec, lane);
                         } else if (p.out_type == GS_BF16)
                             store_chunk<2, GS_BF16>(slot, res, p.residual, p.ldr, p.yp[0], p.ldy[0], row0, at, p.m, p.n,
-                                                    p.y_vec, p.r_vec, lane);
+                                                    vec, lane);
                         else
                             store_chunk<2, GS_F16>(slot, res, p.residual, p.ldr, p.yp[0], p.ldy[0], row0, at, p.m, p.n,
-                                                   p.y_vec, p.r_vec, lane);
+                                                   vec, lane);
                     }
                 }
             }
