@@ -34,6 +34,7 @@ constexpr int kRowsA = 128;                      // accumulator rows of a CTA
 constexpr int kStageRow = 128;                   // bytes of k a stage holds per row
 constexpr int kSlot = 4096;                      // staging of one epilogue warp: 32 rows of 128 bytes
 constexpr int kGroupCols = 64;                   // output columns of a group of four epilogue warps
+constexpr int kFewRows = 64;                     // up to here the weights' bytes are what a product costs
 constexpr int kGroupM = 8;                       // m-tiles that run together (L2 reuse of B)
 
 struct Params {
@@ -593,6 +594,179 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     }
 }
 
+// ------------------------------------------------------------------ few rows
+// With few rows (single tokens, small batches) the weights' bytes are the floor, so
+// the roles are turned: a CTA holds 128 rows of the weights as the MMA's M side
+// (64 of gate and 64 of up for a gated layer) and at most NB rows of x as its N
+// side, and the CTAs of a cluster split k, so that enough SMs stream the weights
+// (4096 x 1024: 32 tiles x 4).  Their partial sums meet in shared memory across the
+// cluster, added in rank order, and every CTA finishes its share of the outputs:
+// one launch, no workspace, no atomics.
+struct RowsParams {
+    CUtensorMap x, w[2];
+    int64_t m, n;
+    const float* x_scale;
+    const float* w_scale[2];
+    const void* bias;
+    const void* residual;
+    void *y, *z, *z2;
+    int64_t ldr, ldy, ldz, ldz2;
+    uint32_t k_blocks, tiles_n, idesc;
+    int k_elems, e4m3, bias_type, out_type, z_type, act;
+};
+
+constexpr int kRowsThreads = 256;
+
+template <int NB, bool GLU>
+struct RowsShape {
+    static constexpr int kBytesW = 128 * kStageRow, kBytesX = NB * kStageRow, kStageBytes = kBytesW + kBytesX;
+    static constexpr int kStages = NB == 64 ? 8 : 10;
+    static constexpr int kSmem = kStages * kStageBytes + kStages * 16 + 32;
+    static constexpr int kTmemCols = NB < 32 ? 32 : NB;
+};
+
+template <int NB, bool GLU>
+__global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_constant__ RowsParams p)
+{
+    using S = RowsShape<NB, GLU>;
+    extern __shared__ __align__(1024) char smem_raw[];
+    const uint32_t stages = smem_addr(smem_raw);
+    if (stages & 1023u) {
+        g_wait_expired = 1;
+        return;
+    }
+    const uint32_t bar_full = stages + S::kStages * S::kStageBytes, bar_empty = bar_full + S::kStages * 8,
+                   bar_acc = bar_empty + S::kStages * 8;
+    char* tail = smem_raw + (bar_acc + 8 - stages);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail);
+    volatile int* gave_up = reinterpret_cast<volatile int*>(tail + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t ranks;
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ranks));
+    const uint32_t rank = cluster_rank();
+    const uint32_t tile = blockIdx.x / ranks, tn = tile % p.tiles_n, tm = tile / p.tiles_n;
+    constexpr int kFeatures = GLU ? 64 : 128;
+    const int64_t n0 = (int64_t)tn * kFeatures, m0 = (int64_t)tm * NB;
+    const uint32_t kb0 = (uint32_t)((uint64_t)p.k_blocks * rank / ranks),
+                   kb1 = (uint32_t)((uint64_t)p.k_blocks * (rank + 1) / ranks);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(bar_full + 8 * i, 1);
+            mbar_init(bar_empty + 8 * i, 1);
+        }
+        mbar_init(bar_acc, 1);
+        *gave_up = 0;
+        mbar_init_fence();
+    }
+    if (warp == 1) tmem_alloc<false>(smem_addr(tmem_slot), S::kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (threadIdx.x == 0) {
+        uint32_t it = 0;
+        for (uint32_t kb = kb0; kb < kb1; ++kb, ++it) {
+            const int s = it % S::kStages;
+            if (!mbar_wait(bar_empty + 8 * s, ((it / S::kStages) & 1) ^ 1, gave_up)) break;
+            const int k = (int)kb * p.k_elems;
+            const uint32_t sw = stages + s * S::kStageBytes, full = bar_full + 8 * s;
+            mbar_expect(full, S::kStageBytes);
+            if constexpr (GLU) {
+                tma_load_2d<false>(sw, &p.w[0], k, (int)n0, full);
+                tma_load_2d<false>(sw + S::kBytesW / 2, &p.w[1], k, (int)n0, full);
+            } else tma_load_2d<false>(sw, &p.w[0], k, (int)n0, full);
+            tma_load_2d<false>(sw + S::kBytesW, &p.x, k, (int)m0, full);
+        }
+        if (*gave_up) {   // let the copies in flight land
+            volatile int still = 0;
+            for (uint32_t i = it > S::kStages ? it - S::kStages : 0; i < it; ++i)
+                mbar_wait(bar_full + 8 * (i % S::kStages), (i / S::kStages) & 1, &still);
+        }
+    } else if (threadIdx.x == 32) {
+        const uint64_t desc = smem_desc(0, true);
+        uint32_t it = 0;
+        for (uint32_t kb = kb0; kb < kb1; ++kb, ++it) {
+            const int s = it % S::kStages;
+            if (!mbar_wait(bar_full + 8 * s, (it / S::kStages) & 1, gave_up)) break;
+            tc_fence_after();
+            const uint32_t sw = stages + s * S::kStageBytes;
+            uint64_t dw = desc | (sw >> 4), dx = desc | ((sw + S::kBytesW) >> 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool add = kb > kb0 || i > 0;
+                if (p.e4m3) mma<false, true>(tmem, dw, dx, p.idesc, add);
+                else mma<false, false>(tmem, dw, dx, p.idesc, add);
+                dw += k_step(true);
+                dx += k_step(true);
+            }
+            mma_commit<false>(bar_empty + 8 * s);
+        }
+        mma_commit<false>(bar_acc);   // every product so far, also after giving up
+    }
+    __syncwarp();
+    mbar_wait(bar_acc, 0, gave_up);
+    __syncthreads();   // every wait of the block has ended; the ring is free for the partial sums
+    tc_fence_after();
+    // partial[row][feature]: 128 features a row
+    if (warp < 4) {
+        const uint32_t d = tmem + ((uint32_t)(warp * 32) << 16);
+#pragma unroll
+        for (int c = 0; c < NB; c += 16) {
+            uint32_t raw[16];
+            tmem_ld16(d + c, raw);
+            tmem_ld_wait(raw);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const float v = kb1 > kb0 ? __uint_as_float(raw[j]) : 0.0f;   // a rank without k adds nothing
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(stages + (uint32_t)(((c + j) * 128 + warp * 32 + lane) * 4)),
+                             "f"(v)
+                             : "memory");
+            }
+        }
+    }
+    cluster_sync();
+    const int rows = p.m - m0 < NB ? (int)(p.m - m0) : NB;
+    const int64_t left = p.n - n0;
+    uint32_t peer[8];
+#pragma unroll
+    for (uint32_t r = 0; r < 8; ++r) peer[r] = map_rank(stages, r < ranks ? r : 0);
+    for (int i = (int)(rank * kRowsThreads + threadIdx.x); i < rows * kFeatures; i += (int)(ranks * kRowsThreads)) {
+        const int r = i / kFeatures, f = i % kFeatures;
+        if (f >= left) continue;
+        const int64_t row = m0 + r, col = n0 + f;
+        float v = 0.0f, u = 0.0f;
+#pragma unroll
+        for (uint32_t q = 0; q < 8; ++q) {
+            if (q >= ranks) break;
+            v += ld_cluster_f32(peer[q] + (uint32_t)((r * 128 + f) * 4));
+            if constexpr (GLU) u += ld_cluster_f32(peer[q] + (uint32_t)((r * 128 + 64 + f) * 4));
+        }
+        const float xs = p.x_scale ? p.x_scale[row] : 1.0f;
+        if (p.e4m3) {
+            v *= xs * (p.w_scale[0] ? p.w_scale[0][col] : 1.0f);
+            if constexpr (GLU) u *= xs * (p.w_scale[1] ? p.w_scale[1][col] : 1.0f);
+        }
+        if (!GLU && p.bias) v += load_elem(p.bias, col, p.bias_type);
+        if (p.z) {
+            store_elem(p.z, row * p.ldz + col, p.z_type, v);
+            if constexpr (GLU) store_elem(p.z2, row * p.ldz2 + col, p.z_type, u);
+        }
+        v = act_value(v, p.act);
+        if constexpr (GLU) v *= u;
+        else if (p.residual) v += load_elem(p.residual, row * p.ldr + col, p.out_type);
+        store_elem(p.y, row * p.ldy + col, p.out_type, v);
+    }
+    if (threadIdx.x == 0 && *gave_up) atomicExch(&g_wait_expired, 1);
+    tc_fence_before();
+    cluster_sync();   // the peers have read this CTA's sums
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_free<false>(tmem, S::kTmemCols);
+    }
+}
+
 // Rows of any alignment to rows of 16-byte pitch (the TMA needs both): eight
 // 2-byte or sixteen 1-byte elements a thread, one 16-byte store.
 template <typename E>
@@ -615,6 +789,7 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const E* src, int64_t ld
 
 // ------------------------------------------------------------------ host
 struct Plan {
+    int nb, ranks;   // the few-rows kernel: rows of x a CTA takes (0: not used), CTAs that split k
     bool pair;
     int bn;
     int64_t tile_m, out_cols, tiles_m, tiles_n, units, k_blocks;
@@ -686,6 +861,14 @@ Plan make_plan(const GemmCall& c)
         }
     }
     p = best;
+    p.nb = 0;
+    if ((c.kind == GemmKind::kLinear || glu) && c.a[0].k_fast && c.b[0].k_fast && c.m <= kFewRows) {
+        p.nb = c.m <= 16 ? 16 : (c.m <= 32 ? 32 : 64);
+        const int64_t tiles = ((c.n + (glu ? 63 : 127)) / (glu ? 64 : 128)) * ((c.m + p.nb - 1) / p.nb);
+        p.ranks = 1;
+        while (p.ranks < 8 && tiles * p.ranks * 2 <= sms && p.k_blocks >= 2 * p.ranks) p.ranks *= 2;
+        p.splits = 1;
+    }
     size_t used = 0;
     const GemmFactor* f[4] = {&c.a[0], &c.a[1], &c.b[0], &c.b[1]};
     for (int i = 0; i < 4; ++i) {
@@ -706,7 +889,27 @@ Plan make_plan(const GemmCall& c)
     return p;
 }
 
-using Kernel = void (*)(const Params);
+template <int NB, bool GLU>
+gs_status launch_rows(const RowsParams& p, unsigned grid, int ranks, cudaStream_t st)
+{
+    using S = RowsShape<NB, GLU>;
+    static_assert(S::kSmem <= 232448, "shared memory of an SM");
+    auto* kernel = rows_kernel<NB, GLU>;
+    GS_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kRowsThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ranks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    GS_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, p));
+    return GS_OK;
+}
 
 template <int BN, bool PAIR, bool GLU, int OSZ>
 gs_status launch(const Params& p, int grid, cudaStream_t st)
@@ -798,8 +1001,35 @@ gs_status gemm_run(const GemmCall& c, void* ws, cudaStream_t st)
         f[i].ld = pieces * 16 / plan.esz;
     }
 
-    Params p = {};
     const bool glu = c.kind == GemmKind::kGlu;
+    if (plan.nb) {
+        RowsParams r = {};
+        gs_status s = tc::make_map(&r.x, f[0].p, c.type, c.m, c.k, f[0].ld, plan.nb, plan.k_elems);
+        if (s == GS_OK) s = tc::make_map(&r.w[0], f[2].p, c.type, c.n, c.k, f[2].ld, glu ? 64 : 128, plan.k_elems);
+        if (s == GS_OK && glu) s = tc::make_map(&r.w[1], f[3].p, c.type, c.n, c.k, f[3].ld, 64, plan.k_elems);
+        if (s != GS_OK) return s;
+        r.m = c.m, r.n = c.n;
+        r.x_scale = c.x_scale, r.w_scale[0] = c.w_scale[0], r.w_scale[1] = c.w_scale[1];
+        r.bias = c.bias, r.bias_type = c.bias_type, r.act = c.act;
+        r.residual = c.residual, r.ldr = c.ldr;
+        r.y = c.y, r.ldy = c.ldy, r.out_type = c.out_type;
+        r.z = c.z, r.ldz = c.ldz, r.z2 = c.z2, r.ldz2 = c.ldz2, r.z_type = c.z_type;
+        r.k_blocks = (uint32_t)plan.k_blocks, r.k_elems = plan.k_elems, r.e4m3 = c.type == GS_E4M3;
+        const int64_t tiles_n = (c.n + (glu ? 63 : 127)) / (glu ? 64 : 128), tiles_m = (c.m + plan.nb - 1) / plan.nb;
+        if (tiles_n * tiles_m * plan.ranks > 0x7fffffffll) return GS_ERR_INVALID_ARG;
+        r.tiles_n = (uint32_t)tiles_n;
+        r.idesc = tc::instr_desc(c.type, true, true, plan.nb, 128);
+        const unsigned grid = (unsigned)(tiles_n * tiles_m * plan.ranks);
+        if (glu)
+            return plan.nb == 16   ? launch_rows<16, true>(r, grid, plan.ranks, st)
+                   : plan.nb == 32 ? launch_rows<32, true>(r, grid, plan.ranks, st)
+                                   : launch_rows<64, true>(r, grid, plan.ranks, st);
+        return plan.nb == 16   ? launch_rows<16, false>(r, grid, plan.ranks, st)
+               : plan.nb == 32 ? launch_rows<32, false>(r, grid, plan.ranks, st)
+                               : launch_rows<64, false>(r, grid, plan.ranks, st);
+    }
+
+    Params p = {};
     const int rows_b = plan.pair || glu ? plan.bn / 2 : plan.bn;
     for (int i = 0; i < 4; ++i) {
         if (!f[i].p) continue;
