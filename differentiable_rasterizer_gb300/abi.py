@@ -339,6 +339,15 @@ def _ws_call(name, packed, ws, ws_bytes, stream):
         _check(name, st)
 
 
+def layer_call(name, args, stream) -> bool:
+    """The named layer call without scratch; False if it needs some or refuses its arguments
+    (layer_ws_bytes tells which)."""
+    st = getattr(_lib or lib(), name)(args, None, None, stream)
+    if st not in (GS_OK, GS_ERR_INVALID_ARG):
+        _check(name, st)
+    return st == GS_OK
+
+
 def _ws_query(name, packed) -> int:
     sz = ctypes.c_size_t(0)
     st = getattr(_lib or lib(), name)(packed, None, ctypes.byref(sz), None)
@@ -349,9 +358,11 @@ def _ws_query(name, packed) -> int:
 
 def gs_rms_norm(rows, cols, x, ldx, residual, ldr, weight, y, ldy, y_scale, sum_, lds, rstd, eps, type_, weight_type,
                 y_type, stream):
-    _check("gs_rms_norm", lib().gs_rms_norm(
+    st = (_lib or lib()).gs_rms_norm(
         _RMS_NORM.pack(rows, cols, x, ldx, residual, ldr, weight, y, ldy, y_scale, sum_, lds, rstd, eps, type_,
-                       weight_type, y_type), stream))
+                       weight_type, y_type), stream)
+    if st != GS_OK:
+        _check("gs_rms_norm", st)
 
 
 def gs_quantize_rows(rows, cols, x, ldx, q, ldq, scale, type_, stream):

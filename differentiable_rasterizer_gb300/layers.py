@@ -67,17 +67,17 @@ def _bad(what):
     raise ValueError(what)
 
 
-def _wrong(t, name, dtypes, device):
+def _wrong(t, name, dtypes, dev):
     """Raises for a tensor of another type or device (the slow path of the checks)."""
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
         _bad(f"{name}: expected a tensor of {[str(d) for d in dtypes]}, got {getattr(t, 'dtype', type(t))}")
-    _bad(f"{name}: on {t.device}, expected {device}")
+    _bad(f"{name}: on {t.device}, expected cuda:{dev}")
 
 
-def _matrix(t, name, dtypes, device, cols=None, rows=None):
+def _matrix(t, name, dtypes, dev, cols=None, rows=None):
     """(pointer, leading dimension, rows, columns) of a tensor seen as rows."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.device != device:
-        _wrong(t, name, dtypes, device)
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.get_device() != dev:
+        _wrong(t, name, dtypes, dev)
     shape = t.shape
     if len(shape) != 2:
         if not shape:
@@ -102,20 +102,21 @@ def _matrix(t, name, dtypes, device, cols=None, rows=None):
     return t.data_ptr(), ld, n, c
 
 
-def _vector(t, name, dtypes, device, size):
+def _vector(t, name, dtypes, dev, size):
     if t is None:
         return 0
-    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.device != device:
-        _wrong(t, name, dtypes, device)
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.get_device() != dev:
+        _wrong(t, name, dtypes, dev)
     if t.numel() != size or (size > 1 and not t.is_contiguous()):
         _bad(f"{name}: expected {size} contiguous values, got {tuple(t.shape)} {t.stride()}")
     return t.data_ptr()
 
 
 def _device(t, name):
+    """Index of the CUDA device that a call's first tensor is on."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         _bad(f"{name}: expected a CUDA tensor, got {t.device if isinstance(t, torch.Tensor) else type(t)}")
-    return t.device
+    return t.get_device()
 
 
 def _act(act):
@@ -128,58 +129,41 @@ def _act(act):
 _PER_16 = {torch.float32: 4, torch.bfloat16: 8, torch.float16: 8, torch.float8_e4m3fn: 16}
 
 
-def _output(lead, rows, cols, dtype, device):
-    """An uninitialised [*lead, cols] whose rows are 16-byte aligned, its pointer and leading dimension."""
+def _output(like, lead, cols, dtype):
+    """An uninitialised [*lead, cols] on like's device whose rows are 16-byte aligned, its pointer
+    and leading dimension."""
     per = _PER_16[dtype]
     ld = (cols + per - 1) // per * per
-    t = torch.empty((*lead, ld), dtype=dtype, device=device)
+    t = like.new_empty((*lead, ld), dtype=dtype)
     p = t.data_ptr()
     return (t if ld == cols else t[..., :cols]), p, ld
 
 
-class _On:
-    """Makes the tensors' device current around a call."""
-
-    def __init__(self, device):
-        self.guard = torch.cuda.device(device)
-
-    def __enter__(self):
-        self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        self.guard.__exit__(*exc)
+_current_device = torch._C._cuda_getDevice              # torch.cuda.current_device without its checks
+_stream = torch._C._cuda_getCurrentRawStream            # torch.cuda.current_stream(dev).cuda_stream
 
 
-def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-def _run(f, device, *args):
+def _run(f, dev, *args):
     """f(*args, stream) with the tensors' device current."""
-    if device.index == torch.cuda.current_device():
-        f(*args, _stream(device))
+    if dev == _current_device():
+        f(*args, _stream(dev))
     else:
-        with _On(device):
-            f(*args, _stream(device))
+        with torch.cuda.device(dev):
+            f(*args, _stream(dev))
 
 
-def _scratch(f, name, device, args):
-    """A layer call with the scratch it asks for, on the current stream."""
-    n = abi.layer_ws_bytes(name, args)
-    if n:
-        ws = torch.empty(n, dtype=torch.uint8, device=device)
-        _run(f, device, args, ws.data_ptr(), n)
-    else:
-        _run(f, device, args, None, None)
-
-
-def _call(name, args, device):
-    f = getattr(abi, name)
-    if device.index == torch.cuda.current_device():
-        _scratch(f, name, device, args)
-    else:
-        with _On(device):
-            _scratch(f, name, device, args)
+def _call(name, args, like, dev):
+    """A layer call with the scratch that it asks for, on the current stream."""
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return _call(name, args, like, dev)
+    stream = _stream(dev)
+    if not abi.layer_call(name, args, stream):
+        n = abi.layer_ws_bytes(name, args)
+        if n == 0:
+            raise abi.GsError(name, abi.GS_ERR_INVALID_ARG)
+        ws = like.new_empty(n, dtype=torch.uint8)
+        getattr(abi, name)(args, ws.data_ptr(), n, stream)
 
 
 # ------------------------------------------------------------------ norm
@@ -202,14 +186,14 @@ def rms_norm(x, weight, *, residual=None, eps=1e-6, out_dtype=None, need_backwar
     s = x
     if residual is not None:
         pr, ldr, _, _ = _matrix(residual, "residual", (x.dtype,), dev, cols, rows)
-        s, ps, lds = _output(lead, rows, cols, x.dtype, dev)
-    y, py, ldy = _output(lead, rows, cols, out_dtype, dev)
+        s, ps, lds = _output(x, lead, cols, x.dtype)
+    y, py, ldy = _output(x, lead, cols, out_dtype)
     scale = rstd = None
     if out_dtype == torch.float8_e4m3fn:
-        scale = torch.empty(lead, dtype=torch.float32, device=dev)
+        scale = x.new_empty(lead, dtype=torch.float32)
         pscale = scale.data_ptr()
     if need_backward:
-        rstd = torch.empty(lead, dtype=torch.float32, device=dev)
+        rstd = x.new_empty(lead, dtype=torch.float32)
         prstd = rstd.data_ptr()
     if rows:
         _run(abi.gs_rms_norm, dev, rows, cols, px, ldx, pr, ldr, pw, py, ldy, pscale, ps, lds, prstd, eps,
@@ -231,11 +215,11 @@ def rms_norm_backward(dy, s, weight, rstd, *, ds=None):
     pds = ldds = 0
     if ds is not None:
         pds, ldds, _, _ = _matrix(ds, "ds", (s.dtype,), dev, cols, rows)
-    dx, pdx, lddx = _output(s.shape[:-1], rows, cols, s.dtype, dev)
-    dw = torch.empty(weight.shape, dtype=weight.dtype, device=dev)
+    dx, pdx, lddx = _output(s, s.shape[:-1], cols, s.dtype)
+    dw = s.new_empty(weight.shape, dtype=weight.dtype)
     _call("gs_rms_norm_bwd", abi.rms_norm_bwd_args(rows, cols, pdy, lddy, ps, lds, pw, prstd, pds, ldds, pdx, lddx,
                                                    dw.data_ptr(), _TYPES[s.dtype], _TYPES[dy.dtype],
-                                                   _TYPES[weight.dtype]), dev)
+                                                   _TYPES[weight.dtype]), s, dev)
     return dx, dw
 
 
@@ -244,8 +228,8 @@ def quantize_rows(x):
     the float32 scale that restores it: x ~ q * scale[..., None]."""
     dev = _device(x, "x")
     px, ldx, rows, cols = _matrix(x, "x", _FLOAT, dev)
-    q, pq, ldq = _output(x.shape[:-1], rows, cols, torch.float8_e4m3fn, dev)
-    scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    q, pq, ldq = _output(x, x.shape[:-1], cols, torch.float8_e4m3fn)
+    scale = x.new_empty(x.shape[:-1], dtype=torch.float32)
     if rows:
         _run(abi.gs_quantize_rows, dev, rows, cols, px, ldx, pq, ldq, scale.data_ptr(), _TYPES[x.dtype])
     return q, scale
@@ -278,7 +262,7 @@ def linear(x, w, bias=None, *, x_scale=None, w_scale=None, act=None, residual=No
     if residual is not None:
         pr, ldr, _, _ = _matrix(residual, "residual", (out_dtype,), dev, n, rows)
     if out is None:
-        y, py, ldy = _output(lead, rows, n, out_dtype, dev)
+        y, py, ldy = _output(x, lead, n, out_dtype)
     else:
         y = out
         py, ldy, _, _ = _matrix(y, "out", (out_dtype,), dev, n, rows)
@@ -286,10 +270,10 @@ def linear(x, w, bias=None, *, x_scale=None, w_scale=None, act=None, residual=No
     if need_backward and code != abi.GS_ACT_NONE:
         if x.dtype not in _HALF:
             _bad("need_backward: 8-bit operands have no gradients")
-        z, pz, ldz = _output(lead, rows, n, x.dtype, dev)
+        z, pz, ldz = _output(x, lead, n, x.dtype)
     _call("gs_linear", abi.linear_args(rows, k, n, px, ldx, pw, ldw, pxs, pws, pb, pr, ldr, py, ldy, pz, ldz,
                                        _TYPES[x.dtype], _TYPES[bias.dtype] if bias is not None else 0,
-                                       _TYPES[out_dtype], code), dev)
+                                       _TYPES[out_dtype], code), x, dev)
     return LinearOut(y, z)
 
 
@@ -316,16 +300,16 @@ def linear_backward(dy, x, w, *, z=None, act=None, bias=False, need_dx=True, nee
         _bad(f"db_dtype: {db_dtype}")
     dx = dw = db = None
     if need_dx:
-        dx, pdx, lddx = _output(x.shape[:-1], rows, k, x.dtype, dev)
+        dx, pdx, lddx = _output(x, x.shape[:-1], k, x.dtype)
     if need_dw:
-        dw = torch.empty((n, k), dtype=dw_dtype, device=dev)
+        dw = x.new_empty((n, k), dtype=dw_dtype)
         pdw, lddw = dw.data_ptr(), k
     if bias:
-        db = torch.empty(n, dtype=db_dtype, device=dev)
+        db = x.new_empty(n, dtype=db_dtype)
         pdb = db.data_ptr()
     _call("gs_linear_bwd", abi.linear_bwd_args(rows, k, n, pdy, lddy, px, ldx, pw, ldw, pz, ldz, pdx, lddx, pdw, lddw,
                                                pdb, _TYPES[x.dtype], _TYPES[dy.dtype], _TYPES[dw_dtype],
-                                               _TYPES[db_dtype], code), dev)
+                                               _TYPES[db_dtype], code), x, dev)
     return LinearGrads(dx, dw, db)
 
 
@@ -349,16 +333,16 @@ def glu(x, w_gate, w_up, *, x_scale=None, gate_scale=None, up_scale=None, act="s
     if out_dtype not in _HALF:
         _bad(f"out_dtype: {out_dtype}")
     lead = x.shape[:-1]
-    h, ph, ldh = _output(lead, rows, f, out_dtype, dev)
+    h, ph, ldh = _output(x, lead, f, out_dtype)
     g = u = None
     pg = ldg = pu = ldu = 0
     if need_backward:
         if x.dtype not in _HALF:
             _bad("need_backward: 8-bit operands have no gradients")
-        g, pg, ldg = _output(lead, rows, f, out_dtype, dev)
-        u, pu, ldu = _output(lead, rows, f, out_dtype, dev)
+        g, pg, ldg = _output(x, lead, f, out_dtype)
+        u, pu, ldu = _output(x, lead, f, out_dtype)
     _call("gs_glu", abi.glu_args(rows, k, f, px, ldx, pg_, ldwg, pu_, ldwu, pxs, pgs, pus, ph, ldh, pg, ldg, pu, ldu,
-                                 _TYPES[x.dtype], _TYPES[out_dtype], _act(act)), dev)
+                                 _TYPES[x.dtype], _TYPES[out_dtype], _act(act)), x, dev)
     return GluOut(h, g, u)
 
 
@@ -377,11 +361,11 @@ def glu_backward(dh, x, w_gate, w_up, g, u, *, act="silu", need_dx=True, need_dw
     dx = dwg = dwu = None
     pdx = lddx = pdwg = lddwg = pdwu = lddwu = 0
     if need_dx:
-        dx, pdx, lddx = _output(x.shape[:-1], rows, k, x.dtype, dev)
+        dx, pdx, lddx = _output(x, x.shape[:-1], k, x.dtype)
     if need_dw:
-        dwg, dwu = (torch.empty((f, k), dtype=dw_dtype, device=dev) for _ in range(2))
+        dwg, dwu = (x.new_empty((f, k), dtype=dw_dtype) for _ in range(2))
         pdwg, lddwg, pdwu, lddwu = dwg.data_ptr(), k, dwu.data_ptr(), k
     _call("gs_glu_bwd", abi.glu_bwd_args(rows, k, f, pdh, lddh, px, ldx, pwg, ldwg, pwu, ldwu, pg, ldg, pu, ldu, pdx,
                                          lddx, pdwg, lddwg, pdwu, lddwu, _TYPES[x.dtype], _TYPES[dw_dtype], _act(act)),
-          dev)
+          x, dev)
     return GluGrads(dx, dwg, dwu)

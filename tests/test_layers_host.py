@@ -110,7 +110,7 @@ def test_tensor_refusals():
                  lambda: layers.linear(None, w)):
         with pytest.raises(ValueError, match="CUDA tensor"):
             call()
-    dev = torch.device("cpu")
+    dev = -1   # the index of a CPU tensor's device
     with pytest.raises(ValueError, match="overlap"):
         layers._matrix(torch.zeros(8).expand(3, 8), "t", (torch.float32,), dev)
     with pytest.raises(ValueError, match="not contiguous"):
