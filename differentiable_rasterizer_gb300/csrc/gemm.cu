@@ -303,6 +303,39 @@ __device__ __forceinline__ void activate(float (&v)[16], int act)
     else if (act == GS_ACT_RELU) activate<GS_ACT_RELU>(v);
 }
 
+// The MMA warp's loop: the warp waits together, one lane issues.
+template <int BN, bool PAIR, bool GLU, bool E4M3>
+__device__ __forceinline__ void issue_products(const Params& p, uint32_t first, uint32_t step, uint32_t stages,
+                                               uint32_t bar_full, uint32_t bar_empty, uint32_t bar_acc, uint32_t bar_free,
+                                               uint32_t tmem, volatile int* gave_up)
+{
+    using S = Shape<BN, PAIR, GLU>;
+    const uint64_t desc_a = smem_desc(stages, p.a_fast), desc_b = smem_desc(stages + S::kBytesA, p.b_fast);
+    const uint32_t step_a = k_step(p.a_fast), step_b = k_step(p.b_fast);
+    uint32_t it = 0, tile = 0;
+    for (uint32_t u = first; u < p.units; u += step, ++tile) {
+        const Unit q = decode(p, u);
+        const uint32_t acc = tile % S::kAccs;
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_free + 8 * acc, ((tile / S::kAccs) & 1) ^ 1, gave_up))) return;
+        tc_fence_after();
+        const uint32_t d = tmem + acc * BN;
+        for (uint32_t kb = q.kb0; kb < q.kb1; ++kb, ++it) {
+            const uint32_t s = it % S::kStages;
+            if (!__all_sync(0xffffffffu, mbar_wait(bar_full + 8 * s, (it / S::kStages) & 1, gave_up))) return;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t da = desc_a + s * (S::kStageBytes >> 4), db = desc_b + s * (S::kStageBytes >> 4);
+#pragma unroll
+                for (uint32_t i = 0; i < 4; ++i)
+                    mma<PAIR, E4M3>(d, da + i * step_a, db + i * step_b, p.idesc, kb > q.kb0 || i > 0);
+                mma_commit<PAIR>(bar_empty + 8 * s);   // the stage is free once these are done
+                if (kb + 1 == q.kb1) mma_commit<PAIR>(bar_acc + 8 * acc);
+            }
+            __syncwarp();
+        }
+    }
+}
+
 // GLU: B's rows are half gate, half up; the epilogue joins column c with c + BN/2.
 // OSZ: bytes of an output element.
 template <int BN, bool PAIR, bool GLU, int OSZ>
@@ -349,26 +382,26 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     const uint32_t tmem = *tmem_slot;
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ---------------------------------------------------------- producer
+        // -------------------------------------------------------------- producer
+        if (elect_one()) {
             prefetch_map(&p.a[0]);
             prefetch_map(&p.b[0]);
-            const uint32_t full0 = PAIR ? map_rank(bar_full, 0) : bar_full;   // the pair counts at its first CTA
-            uint32_t it = 0;
-            bool ok = true;
-            for (uint32_t u = first; u < p.units && ok; u += step) {
-                const Unit q = decode(p, u);
-                const int row_a = (int)(q.tm * S::kTileM + rank * kRowsA);
-                const int row_b = GLU ? (int)(q.tn * (BN / 2)) : (int)(q.tn * BN + rank * S::kRowsB);
-                for (uint32_t kb = q.kb0; kb < q.kb1; ++kb, ++it) {
-                    const int s = it % S::kStages;
-                    if (!mbar_wait(bar_empty + 8 * s, ((it / S::kStages) & 1) ^ 1, gave_up)) {
-                        ok = false;
-                        break;
-                    }
-                    const int term = kb >= p.k_blocks ? 1 : 0;
-                    const int k = (int)((kb - term * p.k_blocks) * p.k_elems);
-                    const int which = p.probs > 1 ? q.prob : term;
+        }
+        const uint32_t full0 = PAIR ? map_rank(bar_full, 0) : bar_full;   // the pair counts at its first CTA
+        uint32_t it = 0;
+        bool ok = true;
+        for (uint32_t u = first; u < p.units && ok; u += step) {
+            const Unit q = decode(p, u);
+            const int row_a = (int)(q.tm * S::kTileM + rank * kRowsA);
+            const int row_b = GLU ? (int)(q.tn * (BN / 2)) : (int)(q.tn * BN + rank * S::kRowsB);
+            for (uint32_t kb = q.kb0; kb < q.kb1; ++kb, ++it) {
+                const int s = it % S::kStages;
+                ok = __all_sync(0xffffffffu, mbar_wait(bar_empty + 8 * s, ((it / S::kStages) & 1) ^ 1, gave_up));
+                if (!ok) break;
+                const int term = kb >= p.k_blocks ? 1 : 0;
+                const int k = (int)(kb - term * p.k_blocks) * p.k_elems;
+                const int which = p.probs > 1 ? q.prob : term;
+                if (elect_one()) {
                     if (rank == 0) mbar_expect(bar_full + 8 * s, S::kStageBytes * (PAIR ? 2 : 1));
                     const uint32_t full = full0 + 8 * s, sa = stages + s * S::kStageBytes, sb = sa + S::kBytesA;
                     if (p.a_fast) tma_load_2d<PAIR>(sa, &p.a[which], k, row_a, full);
@@ -388,51 +421,24 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                         for (int i = 0; i < S::kRowsB / 64; ++i)
                             tma_load_2d<PAIR>(sb + i * 8192, &p.b[which], row_b + 64 * i, k, full);
                 }
-            }
-            if (!ok && rank == 0) {   // given up: let the copies in flight land before the block leaves
-                volatile int still = 0;
-                const uint32_t from = it > S::kStages ? it - S::kStages : 0;
-                for (uint32_t i = from; i < it; ++i)
-                    mbar_wait(bar_full + 8 * (i % S::kStages), (i / S::kStages) & 1, &still);
+                __syncwarp();
             }
         }
+        if (!ok && rank == 0) {   // given up: let the copies in flight land before the block leaves
+            volatile int still = 0;
+            const uint32_t from = it > S::kStages ? it - S::kStages : 0;
+            for (uint32_t i = from; i < it; ++i)
+                mbar_wait(bar_full + 8 * (i % S::kStages), (i / S::kStages) & 1, &still);
+        }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             // ---------------------------------------------------------- tensor cores
-            const uint64_t desc_a = smem_desc(0, p.a_fast), desc_b = smem_desc(0, p.b_fast);
-            const uint32_t step_a = k_step(p.a_fast), step_b = k_step(p.b_fast);
-            uint32_t it = 0, tile = 0;
-            bool ok = true;
-            for (uint32_t u = first; u < p.units && ok; u += step, ++tile) {
-                const Unit q = decode(p, u);
-                const uint32_t acc = tile % S::kAccs;
-                if (!mbar_wait(bar_free + 8 * acc, ((tile / S::kAccs) & 1) ^ 1, gave_up)) break;
-                tc_fence_after();
-                const uint32_t d = tmem + acc * BN;
-                for (uint32_t kb = q.kb0; kb < q.kb1; ++kb, ++it) {
-                    const int s = it % S::kStages;
-                    if (!mbar_wait(bar_full + 8 * s, (it / S::kStages) & 1, gave_up)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t sa = stages + s * S::kStageBytes, sb = sa + S::kBytesA;
-                    uint64_t da = desc_a | (sa >> 4), db = desc_b | (sb >> 4);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const bool add = kb > q.kb0 || i > 0;
-                        if (p.e4m3) mma<PAIR, true>(d, da, db, p.idesc, add);
-                        else mma<PAIR, false>(d, da, db, p.idesc, add);
-                        da += step_a;
-                        db += step_b;
-                    }
-                    mma_commit<PAIR>(bar_empty + 8 * s);   // the stage is free once these are done
-                }
-                if (ok) mma_commit<PAIR>(bar_acc + 8 * acc);
-            }
+            if (p.e4m3) issue_products<BN, PAIR, GLU, true>(p, first, step, stages, bar_full, bar_empty, bar_acc, bar_free, tmem, gave_up);
+            else issue_products<BN, PAIR, GLU, false>(p, first, step, stages, bar_full, bar_empty, bar_acc, bar_free, tmem, gave_up);
             if (*gave_up) {
                 volatile int still = 0;
-                mma_commit<PAIR>(bar_drain);
+                if (elect_one()) mma_commit<PAIR>(bar_drain);
+                __syncwarp();
                 mbar_wait(bar_drain, 0, &still);
             }
         }
@@ -665,45 +671,49 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (threadIdx.x == 0) {
+    if (warp == 0) {
         uint32_t it = 0;
+        bool ok = true;
         for (uint32_t kb = kb0; kb < kb1; ++kb, ++it) {
             const int s = it % S::kStages;
-            if (!mbar_wait(bar_empty + 8 * s, ((it / S::kStages) & 1) ^ 1, gave_up)) break;
-            const int k = (int)kb * p.k_elems;
-            const uint32_t sw = stages + s * S::kStageBytes, full = bar_full + 8 * s;
-            mbar_expect(full, S::kStageBytes);
-            if constexpr (GLU) {
-                tma_load_2d<false>(sw, &p.w[0], k, (int)n0, full);
-                tma_load_2d<false>(sw + S::kBytesW / 2, &p.w[1], k, (int)n0, full);
-            } else tma_load_2d<false>(sw, &p.w[0], k, (int)n0, full);
-            tma_load_2d<false>(sw + S::kBytesW, &p.x, k, (int)m0, full);
+            ok = __all_sync(0xffffffffu, mbar_wait(bar_empty + 8 * s, ((it / S::kStages) & 1) ^ 1, gave_up));
+            if (!ok) break;
+            if (elect_one()) {
+                const int k = (int)kb * p.k_elems;
+                const uint32_t sw = stages + s * S::kStageBytes, full = bar_full + 8 * s;
+                mbar_expect(full, S::kStageBytes);
+                if constexpr (GLU) {
+                    tma_load_2d<false>(sw, &p.w[0], k, (int)n0, full);
+                    tma_load_2d<false>(sw + S::kBytesW / 2, &p.w[1], k, (int)n0, full);
+                } else tma_load_2d<false>(sw, &p.w[0], k, (int)n0, full);
+                tma_load_2d<false>(sw + S::kBytesW, &p.x, k, (int)m0, full);
+            }
+            __syncwarp();
         }
-        if (*gave_up) {   // let the copies in flight land
+        if (!ok) {   // let the copies in flight land
             volatile int still = 0;
             for (uint32_t i = it > S::kStages ? it - S::kStages : 0; i < it; ++i)
                 mbar_wait(bar_full + 8 * (i % S::kStages), (i / S::kStages) & 1, &still);
         }
-    } else if (threadIdx.x == 32) {
-        const uint64_t desc = smem_desc(0, true);
+    } else if (warp == 1) {
+        const uint64_t desc_w = smem_desc(stages, true), desc_x = smem_desc(stages + S::kBytesW, true);
         uint32_t it = 0;
         for (uint32_t kb = kb0; kb < kb1; ++kb, ++it) {
-            const int s = it % S::kStages;
-            if (!mbar_wait(bar_full + 8 * s, (it / S::kStages) & 1, gave_up)) break;
+            const uint32_t s = it % S::kStages;
+            if (!__all_sync(0xffffffffu, mbar_wait(bar_full + 8 * s, (it / S::kStages) & 1, gave_up))) break;
             tc_fence_after();
-            const uint32_t sw = stages + s * S::kStageBytes;
-            uint64_t dw = desc | (sw >> 4), dx = desc | ((sw + S::kBytesW) >> 4);
+            if (elect_one()) {
+                const uint64_t dw = desc_w + s * (S::kStageBytes >> 4), dx = desc_x + s * (S::kStageBytes >> 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bool add = kb > kb0 || i > 0;
-                if (p.e4m3) mma<false, true>(tmem, dw, dx, p.idesc, add);
-                else mma<false, false>(tmem, dw, dx, p.idesc, add);
-                dw += k_step(true);
-                dx += k_step(true);
+                for (uint32_t i = 0; i < 4; ++i) {
+                    if (p.e4m3) mma<false, true>(tmem, dw + i * k_step(true), dx + i * k_step(true), p.idesc, kb > kb0 || i > 0);
+                    else mma<false, false>(tmem, dw + i * k_step(true), dx + i * k_step(true), p.idesc, kb > kb0 || i > 0);
+                }
+                mma_commit<false>(bar_empty + 8 * s);
             }
-            mma_commit<false>(bar_empty + 8 * s);
+            __syncwarp();
         }
-        mma_commit<false>(bar_acc);   // every product so far, also after giving up
+        if (elect_one()) mma_commit<false>(bar_acc);   // every product so far, also after giving up
     }
     __syncwarp();
     mbar_wait(bar_acc, 0, gave_up);

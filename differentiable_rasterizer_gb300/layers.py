@@ -132,11 +132,10 @@ _PER_16 = {torch.float32: 4, torch.bfloat16: 8, torch.float16: 8, torch.float8_e
 def _output(like, lead, cols, dtype):
     """An uninitialised [*lead, cols] on like's device whose rows are 16-byte aligned, its pointer
     and leading dimension."""
-    per = _PER_16[dtype]
-    ld = (cols + per - 1) // per * per
-    t = like.new_empty((*lead, ld), dtype=dtype)
+    pad = -cols % _PER_16[dtype]
+    t = torch.empty(lead + (cols + pad,), dtype=dtype, device=like.device)
     p = t.data_ptr()
-    return (t if ld == cols else t[..., :cols]), p, ld
+    return (t[..., :cols] if pad else t), p, cols + pad
 
 
 _current_device = torch._C._cuda_getDevice              # torch.cuda.current_device without its checks
@@ -162,7 +161,7 @@ def _call(name, args, like, dev):
         n = abi.layer_ws_bytes(name, args)
         if n == 0:
             raise abi.GsError(name, abi.GS_ERR_INVALID_ARG)
-        ws = like.new_empty(n, dtype=torch.uint8)
+        ws = torch.empty(n, dtype=torch.uint8, device=like.device)
         getattr(abi, name)(args, ws.data_ptr(), n, stream)
 
 
@@ -190,10 +189,10 @@ def rms_norm(x, weight, *, residual=None, eps=1e-6, out_dtype=None, need_backwar
     y, py, ldy = _output(x, lead, cols, out_dtype)
     scale = rstd = None
     if out_dtype == torch.float8_e4m3fn:
-        scale = x.new_empty(lead, dtype=torch.float32)
+        scale = torch.empty(lead, dtype=torch.float32, device=x.device)
         pscale = scale.data_ptr()
     if need_backward:
-        rstd = x.new_empty(lead, dtype=torch.float32)
+        rstd = torch.empty(lead, dtype=torch.float32, device=x.device)
         prstd = rstd.data_ptr()
     if rows:
         _run(abi.gs_rms_norm, dev, rows, cols, px, ldx, pr, ldr, pw, py, ldy, pscale, ps, lds, prstd, eps,
@@ -216,7 +215,7 @@ def rms_norm_backward(dy, s, weight, rstd, *, ds=None):
     if ds is not None:
         pds, ldds, _, _ = _matrix(ds, "ds", (s.dtype,), dev, cols, rows)
     dx, pdx, lddx = _output(s, s.shape[:-1], cols, s.dtype)
-    dw = s.new_empty(weight.shape, dtype=weight.dtype)
+    dw = torch.empty(weight.shape, dtype=weight.dtype, device=s.device)
     _call("gs_rms_norm_bwd", abi.rms_norm_bwd_args(rows, cols, pdy, lddy, ps, lds, pw, prstd, pds, ldds, pdx, lddx,
                                                    dw.data_ptr(), _TYPES[s.dtype], _TYPES[dy.dtype],
                                                    _TYPES[weight.dtype]), s, dev)
@@ -229,7 +228,7 @@ def quantize_rows(x):
     dev = _device(x, "x")
     px, ldx, rows, cols = _matrix(x, "x", _FLOAT, dev)
     q, pq, ldq = _output(x, x.shape[:-1], cols, torch.float8_e4m3fn)
-    scale = x.new_empty(x.shape[:-1], dtype=torch.float32)
+    scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
     if rows:
         _run(abi.gs_quantize_rows, dev, rows, cols, px, ldx, pq, ldq, scale.data_ptr(), _TYPES[x.dtype])
     return q, scale
@@ -302,10 +301,10 @@ def linear_backward(dy, x, w, *, z=None, act=None, bias=False, need_dx=True, nee
     if need_dx:
         dx, pdx, lddx = _output(x, x.shape[:-1], k, x.dtype)
     if need_dw:
-        dw = x.new_empty((n, k), dtype=dw_dtype)
+        dw = torch.empty((n, k), dtype=dw_dtype, device=x.device)
         pdw, lddw = dw.data_ptr(), k
     if bias:
-        db = x.new_empty(n, dtype=db_dtype)
+        db = torch.empty(n, dtype=db_dtype, device=x.device)
         pdb = db.data_ptr()
     _call("gs_linear_bwd", abi.linear_bwd_args(rows, k, n, pdy, lddy, px, ldx, pw, ldw, pz, ldz, pdx, lddx, pdw, lddw,
                                                pdb, _TYPES[x.dtype], _TYPES[dy.dtype], _TYPES[dw_dtype],
@@ -363,7 +362,7 @@ def glu_backward(dh, x, w_gate, w_up, g, u, *, act="silu", need_dx=True, need_dw
     if need_dx:
         dx, pdx, lddx = _output(x, x.shape[:-1], k, x.dtype)
     if need_dw:
-        dwg, dwu = (x.new_empty((f, k), dtype=dw_dtype) for _ in range(2))
+        dwg, dwu = (torch.empty((f, k), dtype=dw_dtype, device=x.device) for _ in range(2))
         pdwg, lddwg, pdwu, lddwu = dwg.data_ptr(), k, dwu.data_ptr(), k
     _call("gs_glu_bwd", abi.glu_bwd_args(rows, k, f, pdh, lddh, px, ldx, pwg, ldwg, pwu, ldwu, pg, ldg, pu, ldu, pdx,
                                          lddx, pdwg, lddwg, pdwu, lddwu, _TYPES[x.dtype], _TYPES[dw_dtype], _act(act)),
