@@ -32,7 +32,6 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kEpiWarps = 16;
 constexpr int kRowsA = 128;                      // accumulator rows of a CTA
 constexpr int kStageRow = 128;                   // bytes of k a stage holds per row
-constexpr int kSlot = 4096;                      // staging of one epilogue warp: 32 rows of 128 bytes
 constexpr int kGroupCols = 64;                   // output columns of a group of four epilogue warps
 constexpr int kFewRows = 64;                     // up to here the weights' bytes are what a product costs
 constexpr int kGroupM = 8;                       // m-tiles that run together (L2 reuse of B)
@@ -68,7 +67,11 @@ struct Shape {
     static constexpr int kBytesA = kRowsA * kStageRow;
     static constexpr int kBytesB = kRowsB * kStageRow;
     static constexpr int kStageBytes = kBytesA + kBytesB;
-    static constexpr int kStages = BN == 64 ? 6 : 5;
+    // Staging of an epilogue warp: 32 rows of 128 bytes, or of 64 in a pair, whose sixth
+    // stage is worth more (32768 x 1024 -> 4096: 4, 5 stages 167, 162 us).
+    static constexpr int kSlotRow = PAIR ? 64 : 128;
+    static constexpr int kSlot = 32 * kSlotRow;
+    static constexpr int kStages = BN == 64 || PAIR ? 6 : 5;
     // Four groups of epilogue warps, 64 output columns each: all on one tile, or tiles in turn.
     static constexpr int kOutCols = GLU ? BN / 2 : BN;
     static constexpr int kGroupsTile = kOutCols / kGroupCols;
@@ -114,10 +117,14 @@ __device__ __forceinline__ Unit decode(const Params& p, uint32_t u)
     return r;
 }
 
-// Byte of 16-byte piece j of row r in a staging slot: 32 rows of 128 bytes (64 columns
-// in 16 bits, 32 in 32) under the 128-byte swizzle, so that a thread's row and a
-// group of eight threads' row are both free of bank conflicts.
-__device__ __forceinline__ uint32_t slot_piece(int r, int j) { return r * 128 + ((j ^ (r & 7)) << 4); }
+// Byte of 16-byte piece j of row r in a staging slot of 32 rows of ROW bytes, swizzled
+// so that neither a piece of eight rows nor the pieces of 128 bytes share a bank.
+template <int ROW>
+__device__ __forceinline__ uint32_t slot_piece(int r, int j)
+{
+    return ROW == 128 ? r * 128 + ((j ^ (r & 7)) << 4) : r * 64 + ((j ^ ((r >> 1) & 3)) << 4);
+}
+
 __device__ __forceinline__ void st_shared16(uint32_t a, uint4 v)
 {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -143,112 +150,124 @@ __device__ __forceinline__ float ld_shared_f32(uint32_t a)
 }
 
 // 16 values of a thread's row into a slot: in 16 bits (pieces 2 step, 2 step + 1 of
-// 64 columns) or in fp32 (four pieces of 32 columns).
-template <int T>
+// ROW / 2 columns) or in fp32 (four pieces of ROW / 4 columns).
+template <int ROW, int T>
 __device__ __forceinline__ void slot_put_half(uint32_t slot, int row, int step, const float (&v)[16])
 {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-        st_shared16(slot + slot_piece(row, 2 * step + j),
+        st_shared16(slot + slot_piece<ROW>(row, 2 * step + j),
                     make_uint4(pack_half2(v[8 * j], v[8 * j + 1], T), pack_half2(v[8 * j + 2], v[8 * j + 3], T),
                                pack_half2(v[8 * j + 4], v[8 * j + 5], T), pack_half2(v[8 * j + 6], v[8 * j + 7], T)));
 }
+template <int ROW>
 __device__ __forceinline__ void slot_put(uint32_t slot, int row, int step, const float (&v)[16])
 {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        st_shared16(slot + slot_piece(row, 4 * step + j),
+        st_shared16(slot + slot_piece<ROW>(row, 4 * step + j),
                     make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
                                __float_as_uint(v[4 * j + 3])));
 }
 
-// A slot of 64 16-bit columns to memory: eight threads a row, 16 bytes each, where the
-// rows are aligned (vec); single elements otherwise and where a row ends inside a
-// piece.  Plain stores: they need no proxy fence and no wait before the slot is used
-// again, and write nothing beside the matrix (a TMA store writes whole 16-byte pieces).
+// A slot of ROW / 2 16-bit columns to memory: 16 bytes a thread where the rows are
+// aligned (vec); single elements otherwise and where a row ends inside a piece.
+// Plain stores: they need no proxy fence and no wait before the slot is used again,
+// and write nothing beside the matrix (a TMA store writes whole 16-byte pieces).
+template <int ROW>
 __device__ __forceinline__ void store_half(uint32_t slot, void* p, int64_t ld, int64_t row0, int64_t col0, int64_t m,
                                            int64_t n, bool vec, int lane)
 {
-    const int rows = m - row0 < 32 ? (int)(m - row0) : 32, cols = n - col0 < 64 ? (int)(n - col0) : 64;
+    constexpr int kCols = ROW / 2, kPieces = ROW / 16, kRows = 32 / kPieces;
+    const int rows = m - row0 < 32 ? (int)(m - row0) : 32, cols = n - col0 < kCols ? (int)(n - col0) : kCols;
     if (vec) {
-        const int j = lane & 7, r0 = lane >> 3, left = cols - 8 * j;
+        const int j = lane % kPieces, r0 = lane / kPieces, left = cols - 8 * j;
         uint16_t* at = (uint16_t*)p + (row0 + r0) * ld + col0 + 8 * j;
         if (left >= 8) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (r0 + 4 * i < rows)
-                    *reinterpret_cast<uint4*>(at + 4 * i * ld) = ld_shared16(slot + slot_piece(r0 + 4 * i, j));
+            for (int i = 0; i < 32 / kRows; ++i)
+                if (r0 + kRows * i < rows)
+                    *reinterpret_cast<uint4*>(at + kRows * i * ld) = ld_shared16(slot + slot_piece<ROW>(r0 + kRows * i, j));
         } else {
-            for (int r = r0; r < rows; r += 4, at += 4 * ld)
-                for (int e = 0; e < left; ++e) at[e] = ld_shared_u16(slot + slot_piece(r, j) + 2 * e);
+            for (int r = r0; r < rows; r += kRows, at += kRows * ld)
+                for (int e = 0; e < left; ++e) at[e] = ld_shared_u16(slot + slot_piece<ROW>(r, j) + 2 * e);
         }
     } else {
         for (int c = lane; c < cols; c += 32) {
             uint16_t* at = (uint16_t*)p + row0 * ld + col0 + c;
 #pragma unroll 8
             for (int r = 0; r < 32; ++r, at += ld) {
-                const uint16_t v = ld_shared_u16(slot + slot_piece(r, c >> 3) + 2 * (c & 7));
+                const uint16_t v = ld_shared_u16(slot + slot_piece<ROW>(r, c >> 3) + 2 * (c & 7));
                 if (r < rows) *at = v;
             }
         }
     }
 }
 
-// The residual's part of a 32 x 32 chunk, in the layout in which store_chunk writes
-// (16-byte pieces of rows, or a column a thread): fetched before the accumulator is read.
-template <int OSZ>
-struct Residual {
-    uint4 q[32 * OSZ / 16];
+// A chunk of 32 rows of ROW / 4 columns on its way out: 16 bytes of a row a thread
+// where y's and the residual's rows are aligned, a column a thread otherwise.
+template <int ROW, int OSZ>
+struct Chunk {
+    static constexpr int kCols = ROW / 4, kPer = 16 / OSZ, kPieces = kCols / kPer, kRows = 32 / kPieces, kSteps = 32 / kRows;
+    static constexpr int kColThreads = 32 / kCols;             // threads that share a column, rows in turn
+    static constexpr int kWords = 32 / kColThreads * OSZ / 4;  // a thread's rows of a column, packed
+    static_assert(kWords <= 4 * kSteps, "the residual's registers hold either layout");
 };
-template <int OSZ>
-__device__ __forceinline__ void fetch_residual(Residual<OSZ>& res, const void* p, int64_t ld, int64_t row0, int64_t col0,
-                                               int64_t m, int64_t n, bool vec, int lane)
+
+// The residual's part of a chunk in that layout, fetched before the accumulator is read.
+template <int ROW, int OSZ>
+struct Residual {
+    uint4 q[Chunk<ROW, OSZ>::kSteps];
+};
+template <int ROW, int OSZ>
+__device__ __forceinline__ void fetch_residual(Residual<ROW, OSZ>& res, const void* p, int64_t ld, int64_t row0,
+                                               int64_t col0, int64_t m, int64_t n, bool vec, int lane)
 {
+    using C = Chunk<ROW, OSZ>;
     if (!vec) {
-        uint32_t w[32 * OSZ / 4];
+        uint32_t w[4 * C::kSteps];
 #pragma unroll
-        for (int i = 0; i < 32 * OSZ / 4; ++i) w[i] = 0;
-        if (col0 + lane < n) {
-            const char* at = (const char*)p + (row0 * ld + col0 + lane) * OSZ;
+        for (int i = 0; i < 4 * C::kSteps; ++i) w[i] = 0;
+        const int c = lane % C::kCols, r0 = lane / C::kCols;
+        if (col0 + c < n) {
+            const char* at = (const char*)p + ((row0 + r0) * ld + col0 + c) * OSZ;
 #pragma unroll
-            for (int r = 0; r < 32; ++r, at += ld * OSZ) {
-                if (row0 + r >= m) continue;
-                if constexpr (OSZ == 4) w[r] = *(const uint32_t*)at;
-                else w[r >> 1] |= (uint32_t)(*(const uint16_t*)at) << (16 * (r & 1));
+            for (int i = 0; i < 32 / C::kColThreads; ++i, at += C::kColThreads * ld * OSZ) {
+                if (row0 + r0 + i * C::kColThreads >= m) continue;
+                if constexpr (OSZ == 4) w[i] = *(const uint32_t*)at;
+                else w[i >> 1] |= (uint32_t)(*(const uint16_t*)at) << (16 * (i & 1));
             }
         }
 #pragma unroll
-        for (int i = 0; i < 32 * OSZ / 16; ++i) res.q[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        for (int i = 0; i < C::kSteps; ++i) res.q[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         return;
     }
-    constexpr int kPer = 16 / OSZ, kPieces = 32 / kPer, kRows = 32 / kPieces;
-    const int j = lane % kPieces, r0 = lane / kPieces;
-    const char* at = (const char*)p + ((row0 + r0) * ld + col0 + kPer * j) * OSZ;
+    const int j = lane % C::kPieces, r0 = lane / C::kPieces;
+    const char* at = (const char*)p + ((row0 + r0) * ld + col0 + C::kPer * j) * OSZ;
 #pragma unroll
-    for (int i = 0; i < 32 / kRows; ++i) {
+    for (int i = 0; i < C::kSteps; ++i) {
         res.q[i] = make_uint4(0, 0, 0, 0);
-        if (row0 + r0 + i * kRows < m && col0 + kPer * (j + 1) <= n)
-            res.q[i] = *reinterpret_cast<const uint4*>(at + (int64_t)i * kRows * ld * OSZ);
+        if (row0 + r0 + i * C::kRows < m && col0 + C::kPer * (j + 1) <= n)
+            res.q[i] = *reinterpret_cast<const uint4*>(at + (int64_t)i * C::kRows * ld * OSZ);
     }
 }
 
-// A slot of 32 fp32 columns to memory, the residual added and rounded once: 16 bytes a
-// thread where the rows are aligned, single elements otherwise.
-template <int OSZ, int T>
-__device__ __forceinline__ void store_chunk(uint32_t slot, const Residual<OSZ>& res, const void* resp, int64_t ldr, void* p,
-                                            int64_t ld, int64_t row0, int64_t col0, int64_t m, int64_t n, bool vec,
+// A slot of fp32 columns to memory, the residual added and rounded once.
+template <int ROW, int OSZ, int T>
+__device__ __forceinline__ void store_chunk(uint32_t slot, const Residual<ROW, OSZ>& res, const void* resp, int64_t ldr,
+                                            void* p, int64_t ld, int64_t row0, int64_t col0, int64_t m, int64_t n, bool vec,
                                             int lane)
 {
-    constexpr int kPer = 16 / OSZ, kPieces = 32 / kPer, kRows = 32 / kPieces;
-    const int rows = m - row0 < 32 ? (int)(m - row0) : 32, cols = n - col0 < 32 ? (int)(n - col0) : 32;
-    const int j = lane % kPieces, r0 = lane / kPieces, left = cols - kPer * j;
-    if (vec && left >= kPer) {
-        char* at = (char*)p + ((row0 + r0) * ld + col0 + kPer * j) * OSZ;
+    using C = Chunk<ROW, OSZ>;
+    const int rows = m - row0 < 32 ? (int)(m - row0) : 32, cols = n - col0 < C::kCols ? (int)(n - col0) : C::kCols;
+    const int j = lane % C::kPieces, r0 = lane / C::kPieces, left = cols - C::kPer * j;
+    if (vec && left >= C::kPer) {
+        char* at = (char*)p + ((row0 + r0) * ld + col0 + C::kPer * j) * OSZ;
 #pragma unroll
-        for (int i = 0; i < 32 / kRows; ++i) {
-            const int r = r0 + i * kRows;
+        for (int i = 0; i < C::kSteps; ++i) {
+            const int r = r0 + i * C::kRows;
             if (r < rows) {
-                uint4 out = ld_shared16(slot + slot_piece(r, OSZ == 4 ? j : 2 * j));
+                uint4 out = ld_shared16(slot + slot_piece<ROW>(r, OSZ == 4 ? j : 2 * j));
                 if constexpr (OSZ == 4) {
                     if (resp) {
                         out.x = __float_as_uint(__uint_as_float(out.x) + __uint_as_float(res.q[i].x));
@@ -257,7 +276,7 @@ __device__ __forceinline__ void store_chunk(uint32_t slot, const Residual<OSZ>& 
                         out.w = __float_as_uint(__uint_as_float(out.w) + __uint_as_float(res.q[i].w));
                     }
                 } else {
-                    const uint4 hi = ld_shared16(slot + slot_piece(r, 2 * j + 1));
+                    const uint4 hi = ld_shared16(slot + slot_piece<ROW>(r, 2 * j + 1));
                     const float2 a = unpack_half2(res.q[i].x, T), b = unpack_half2(res.q[i].y, T),
                                  c = unpack_half2(res.q[i].z, T), d = unpack_half2(res.q[i].w, T);
                     out = make_uint4(pack_half2(__uint_as_float(out.x) + a.x, __uint_as_float(out.y) + a.y, T),
@@ -265,26 +284,28 @@ __device__ __forceinline__ void store_chunk(uint32_t slot, const Residual<OSZ>& 
                                      pack_half2(__uint_as_float(hi.x) + c.x, __uint_as_float(hi.y) + c.y, T),
                                      pack_half2(__uint_as_float(hi.z) + d.x, __uint_as_float(hi.w) + d.y, T));
                 }
-                *reinterpret_cast<uint4*>(at + (int64_t)i * kRows * ld * OSZ) = out;
+                *reinterpret_cast<uint4*>(at + (int64_t)i * C::kRows * ld * OSZ) = out;
             }
         }
     } else if (vec) {   // the row ends inside this thread's piece
-        for (int r = r0; r < rows; r += kRows)
+        for (int r = r0; r < rows; r += C::kRows)
             for (int e = 0; e < left; ++e) {
-                const int c = kPer * j + e;
-                float v = ld_shared_f32(slot + slot_piece(r, c >> 2) + 4 * (c & 3));
+                const int c = C::kPer * j + e;
+                float v = ld_shared_f32(slot + slot_piece<ROW>(r, c >> 2) + 4 * (c & 3));
                 if (resp) v += load_elem(resp, (row0 + r) * ldr + col0 + c, T);
                 store_elem(p, (row0 + r) * ld + col0 + c, T, v);
             }
-    } else if (lane < cols) {
-        char* at = (char*)p + (row0 * ld + col0 + lane) * OSZ;
+    } else if (lane % C::kCols < cols) {
+        const int c = lane % C::kCols, rr = lane / C::kCols;
+        char* at = (char*)p + ((row0 + rr) * ld + col0 + c) * OSZ;
 #pragma unroll
-        for (int r = 0; r < 32; ++r, at += ld * OSZ) {
-            float v = ld_shared_f32(slot + slot_piece(r, lane >> 2) + 4 * (lane & 3));
-            const uint4 q = res.q[OSZ == 4 ? r >> 2 : r >> 3];
-            const int w = OSZ == 4 ? r & 3 : (r >> 1) & 3;
-            const uint32_t word = w == 0 ? q.x : (w == 1 ? q.y : (w == 2 ? q.z : q.w));
-            if (resp) v += OSZ == 4 ? __uint_as_float(word) : (r & 1 ? unpack_half2(word, T).y : unpack_half2(word, T).x);
+        for (int i = 0; i < 32 / C::kColThreads; ++i, at += C::kColThreads * ld * OSZ) {
+            const int r = rr + i * C::kColThreads;
+            float v = ld_shared_f32(slot + slot_piece<ROW>(r, c >> 2) + 4 * (c & 3));
+            const int word = OSZ == 4 ? i : i >> 1;
+            const uint4 q = res.q[word >> 2];
+            const uint32_t w = (word & 3) == 0 ? q.x : ((word & 3) == 1 ? q.y : ((word & 3) == 2 ? q.z : q.w));
+            if (resp) v += OSZ == 4 ? __uint_as_float(w) : (i & 1 ? unpack_half2(w, T).y : unpack_half2(w, T).x);
             if (r < rows) store_elem(at, 0, T, v);
         }
     }
@@ -349,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         return;
     }
     const uint32_t stages = base, slots = base + S::kStages * S::kStageBytes;
-    const uint32_t bars = slots + kEpiWarps * kSlot;
+    const uint32_t bars = slots + kEpiWarps * S::kSlot;
     const uint32_t bar_full = bars, bar_empty = bars + S::kStages * 8, bar_acc = bar_empty + S::kStages * 8,
                    bar_free = bar_acc + S::kAccs * 8, bar_drain = bar_free + S::kAccs * 8;
     char* tail = smem_raw + (bars + S::kBars * 8 - base);
@@ -446,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         // -------------------------------------------------------------- epilogue
         const int quarter = warp & 3, group = (warp - 2) >> 2;
         const int turn = group / S::kGroupsTile, col_group = group % S::kGroupsTile;
-        const uint32_t slot = slots + (warp - 2) * kSlot;
+        const uint32_t slot = slots + (warp - 2) * S::kSlot;
         const uint32_t free0 = PAIR ? map_rank(bar_free, 0) : bar_free;
         float* const factors = columns + (warp - 2) * 32;
         const bool has_factors = p.e4m3 || p.bias;
@@ -538,47 +559,54 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
 
             for (int pass = 0; live && pass < passes; ++pass) {
                 const bool last = pass == passes - 1;
-                if (!last || (OSZ == 2 && !p.residual)) {   // 64 columns in 16 bits
+                if (!last || (OSZ == 2 && !p.residual)) {   // in 16 bits
+                    constexpr int kCols = S::kSlotRow / 2;
                     const int type = last ? p.out_type : p.z_type;
-                    __syncwarp();   // the slot's last readers are done
-#pragma unroll 1
-                    for (int s = 0; s < 4; ++s) {
-                        float v[16];
-                        columns16(16 * s, pass, v);
-                        if (type == GS_BF16) slot_put_half<GS_BF16>(slot, lane, s, v);
-                        else slot_put_half<GS_F16>(slot, lane, s, v);
-                    }
-                    __syncwarp();
                     void* const to = last ? p.yp[q.prob] : (GLU && pass == 1 ? p.z2p : p.zp);
                     const int64_t ld = last ? p.ldy[q.prob] : (GLU && pass == 1 ? p.ldz2 : p.ldz);
-                    store_half(slot, to, ld, row0, col0, p.m, p.n, last ? p.y_vec : p.z_vec, lane);
-                } else {   // twice 32 columns in fp32, the residual added on the way out
 #pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        const int64_t at = col0 + 32 * h;
+                    for (int h = 0; h < kGroupCols / kCols; ++h) {
+                        const int64_t at = col0 + kCols * h;
                         if (at >= p.n) break;
-                        const bool vec = p.y_vec && (p.r_vec || !p.residual);
-                        Residual<OSZ> res;
+                        __syncwarp();   // the slot's last readers are done
+#pragma unroll 1
+                        for (int s = 0; s < kCols / 16; ++s) {
+                            float v[16];
+                            columns16(kCols * h + 16 * s, pass, v);
+                            if (type == GS_BF16) slot_put_half<S::kSlotRow, GS_BF16>(slot, lane, s, v);
+                            else slot_put_half<S::kSlotRow, GS_F16>(slot, lane, s, v);
+                        }
+                        __syncwarp();
+                        store_half<S::kSlotRow>(slot, to, ld, row0, at, p.m, p.n, last ? p.y_vec : p.z_vec, lane);
+                    }
+                } else {   // in fp32, the residual added on the way out
+                    constexpr int kCols = S::kSlotRow / 4;
+                    const bool vec = p.y_vec && (p.r_vec || !p.residual);
+#pragma unroll 1
+                    for (int h = 0; h < kGroupCols / kCols; ++h) {
+                        const int64_t at = col0 + kCols * h;
+                        if (at >= p.n) break;
+                        Residual<S::kSlotRow, OSZ> res;
                         if (p.residual) fetch_residual(res, p.residual, p.ldr, row0, at, p.m, p.n, vec, lane);
                         __syncwarp();
 #pragma unroll 1
-                        for (int s = 0; s < 2; ++s) {
+                        for (int s = 0; s < kCols / 16; ++s) {
                             float v[16];
-                            columns16(32 * h + 16 * s, pass, v);
-                            slot_put(slot, lane, s, v);
+                            columns16(kCols * h + 16 * s, pass, v);
+                            slot_put<S::kSlotRow>(slot, lane, s, v);
                         }
                         __syncwarp();
                         if constexpr (OSZ == 4) {
                             float* const to = (float*)p.yp[p.partial ? 0 : q.prob] +
                                               (p.partial ? (int64_t)(q.prob * p.splits + q.split) * p.part : 0);
-                            store_chunk<4, GS_F32>(slot, res, p.residual, p.ldr, to, p.ldy[p.partial ? 0 : q.prob], row0, at,
-                                                   p.m, p.n, vec, lane);
+                            store_chunk<S::kSlotRow, 4, GS_F32>(slot, res, p.residual, p.ldr, to,
+                                                                p.ldy[p.partial ? 0 : q.prob], row0, at, p.m, p.n, vec, lane);
                         } else if (p.out_type == GS_BF16)
-                            store_chunk<2, GS_BF16>(slot, res, p.residual, p.ldr, p.yp[0], p.ldy[0], row0, at, p.m, p.n,
-                                                    vec, lane);
+                            store_chunk<S::kSlotRow, 2, GS_BF16>(slot, res, p.residual, p.ldr, p.yp[0], p.ldy[0], row0, at,
+                                                                 p.m, p.n, vec, lane);
                         else
-                            store_chunk<2, GS_F16>(slot, res, p.residual, p.ldr, p.yp[0], p.ldy[0], row0, at, p.m, p.n,
-                                                   vec, lane);
+                            store_chunk<S::kSlotRow, 2, GS_F16>(slot, res, p.residual, p.ldr, p.yp[0], p.ldy[0], row0, at,
+                                                                p.m, p.n, vec, lane);
                     }
                 }
             }
