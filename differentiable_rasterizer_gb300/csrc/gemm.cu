@@ -150,51 +150,68 @@ __device__ __forceinline__ float ld_shared_f32(uint32_t a)
 }
 
 // 16 values of a thread's row into a slot: in 16 bits (pieces 2 step, 2 step + 1 of
-// ROW / 2 columns) or in fp32 (four pieces of ROW / 4 columns).
-template <int ROW, int T>
-__device__ __forceinline__ void slot_put_half(uint32_t slot, int row, int step, const float (&v)[16])
+// ROW / 2 columns) or in fp32 (four pieces of ROW / 4 columns).  mine: the address of
+// piece 0 of the thread's row, which the swizzle makes the others' but for an xor.
+template <int T>
+__device__ __forceinline__ void slot_put_half(uint32_t mine, int step, const float (&v)[16])
 {
+    const uint32_t at = mine ^ (step << 5);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-        st_shared16(slot + slot_piece<ROW>(row, 2 * step + j),
+        st_shared16(at ^ (j << 4),
                     make_uint4(pack_half2(v[8 * j], v[8 * j + 1], T), pack_half2(v[8 * j + 2], v[8 * j + 3], T),
                                pack_half2(v[8 * j + 4], v[8 * j + 5], T), pack_half2(v[8 * j + 6], v[8 * j + 7], T)));
 }
-template <int ROW>
-__device__ __forceinline__ void slot_put(uint32_t slot, int row, int step, const float (&v)[16])
+__device__ __forceinline__ void slot_put(uint32_t mine, int step, const float (&v)[16])
 {
+    const uint32_t at = mine ^ (step << 6);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        st_shared16(slot + slot_piece<ROW>(row, 4 * step + j),
-                    make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
-                               __float_as_uint(v[4 * j + 3])));
+        st_shared16(at ^ (j << 4), make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                              __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
 }
 
-// A slot of ROW / 2 16-bit columns to memory: 16 bytes a thread where the rows are
-// aligned (vec); single elements otherwise and where a row ends inside a piece.
-// Plain stores: they need no proxy fence and no wait before the slot is used again,
-// and write nothing beside the matrix (a TMA store writes whole 16-byte pieces).
+// Address of piece j of row r0 + R i of a slot, for the i-th of the rows a thread visits
+// R apart (R 4 only under 128-byte rows): a constant away from the first but for the
+// swizzle's third bit.
+template <int ROW, int R>
+__device__ __forceinline__ uint32_t slot_walk(uint32_t first, int i)
+{
+    return (ROW == 128 && R == 4 ? first ^ ((i & 1) << 6) : first) + i * R * ROW;
+}
+
+// A slot of ROW / 2 16-bit columns to memory (base: the chunk's first element): 16 bytes
+// a thread where the rows are aligned (vec); single elements otherwise and where a row
+// ends inside a piece.  Plain stores: they need no proxy fence and no wait before the
+// slot is used again, and write nothing beside the matrix (a TMA store writes whole
+// 16-byte pieces).
 template <int ROW>
-__device__ __forceinline__ void store_half(uint32_t slot, void* p, int64_t ld, int64_t row0, int64_t col0, int64_t m,
-                                           int64_t n, bool vec, int lane)
+__device__ __forceinline__ void store_half(uint32_t slot, uint16_t* base, int64_t ld, int rows, int cols, bool vec, int lane)
 {
     constexpr int kCols = ROW / 2, kPieces = ROW / 16, kRows = 32 / kPieces;
-    const int rows = m - row0 < 32 ? (int)(m - row0) : 32, cols = n - col0 < kCols ? (int)(n - col0) : kCols;
     if (vec) {
         const int j = lane % kPieces, r0 = lane / kPieces, left = cols - 8 * j;
-        uint16_t* at = (uint16_t*)p + (row0 + r0) * ld + col0 + 8 * j;
+        const uint32_t from = slot + slot_piece<ROW>(r0, j);
+        uint16_t* at = base + r0 * ld + 8 * j;
+        const int64_t step = kRows * ld;
         if (left >= 8) {
 #pragma unroll
-            for (int i = 0; i < 32 / kRows; ++i)
-                if (r0 + kRows * i < rows)
-                    *reinterpret_cast<uint4*>(at + kRows * i * ld) = ld_shared16(slot + slot_piece<ROW>(r0 + kRows * i, j));
-        } else {
-            for (int r = r0; r < rows; r += kRows, at += kRows * ld)
-                for (int e = 0; e < left; ++e) at[e] = ld_shared_u16(slot + slot_piece<ROW>(r, j) + 2 * e);
+            for (int i = 0; i < 32 / kRows; ++i, at += step)
+                if (r0 + kRows * i < rows) *reinterpret_cast<uint4*>(at) = ld_shared16(slot_walk<ROW, kRows>(from, i));
+        } else if (left > 0) {
+#pragma unroll 2
+            for (int i = 0; i < 32 / kRows; ++i, at += step) {
+                if (r0 + kRows * i >= rows) break;
+                const uint4 q = ld_shared16(slot_walk<ROW, kRows>(from, i));
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int e = 0; e < 7; ++e)
+                    if (e < left) at[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+            }
         }
     } else {
         for (int c = lane; c < cols; c += 32) {
-            uint16_t* at = (uint16_t*)p + row0 * ld + col0 + c;
+            uint16_t* at = base + c;
 #pragma unroll 8
             for (int r = 0; r < 32; ++r, at += ld) {
                 const uint16_t v = ld_shared_u16(slot + slot_piece<ROW>(r, c >> 3) + 2 * (c & 7));
@@ -214,99 +231,122 @@ struct Chunk {
     static_assert(kWords <= 4 * kSteps, "the residual's registers hold either layout");
 };
 
-// The residual's part of a chunk in that layout, fetched before the accumulator is read.
+// The residual's part of kSteps / PARTS of a chunk's steps in that layout.  In 16 bits
+// a whole chunk is fetched before the accumulator is read; in 32 its registers would
+// spill, and it is fetched in parts on the way out.
 template <int ROW, int OSZ>
 struct Residual {
-    uint4 q[Chunk<ROW, OSZ>::kSteps];
+    static constexpr int kParts = OSZ == 4 ? 2 : 1, kSteps = Chunk<ROW, OSZ>::kSteps / kParts;
+    uint4 q[kSteps];
 };
 template <int ROW, int OSZ>
-__device__ __forceinline__ void fetch_residual(Residual<ROW, OSZ>& res, const void* p, int64_t ld, int64_t row0,
-                                               int64_t col0, int64_t m, int64_t n, bool vec, int lane)
+__device__ __forceinline__ void fetch_residual(Residual<ROW, OSZ>& res, int part, const char* base, int64_t ld, int rows,
+                                               int cols, bool vec, int lane)
 {
     using C = Chunk<ROW, OSZ>;
+    using R = Residual<ROW, OSZ>;
     if (!vec) {
-        uint32_t w[4 * C::kSteps];
+        constexpr int kVisits = 32 / C::kColThreads / R::kParts;
+        uint32_t w[4 * R::kSteps];
 #pragma unroll
-        for (int i = 0; i < 4 * C::kSteps; ++i) w[i] = 0;
-        const int c = lane % C::kCols, r0 = lane / C::kCols;
-        if (col0 + c < n) {
-            const char* at = (const char*)p + ((row0 + r0) * ld + col0 + c) * OSZ;
+        for (int i = 0; i < 4 * R::kSteps; ++i) w[i] = 0;
+        const int c = lane % C::kCols, r0 = lane / C::kCols + part * kVisits * C::kColThreads;
+        const char* at = base + (r0 * ld + c) * OSZ;
 #pragma unroll
-            for (int i = 0; i < 32 / C::kColThreads; ++i, at += C::kColThreads * ld * OSZ) {
-                if (row0 + r0 + i * C::kColThreads >= m) continue;
-                if constexpr (OSZ == 4) w[i] = *(const uint32_t*)at;
-                else w[i >> 1] |= (uint32_t)(*(const uint16_t*)at) << (16 * (i & 1));
-            }
+        for (int i = 0; i < kVisits; ++i, at += C::kColThreads * ld * OSZ) {
+            if (c >= cols || r0 + i * C::kColThreads >= rows) continue;
+            if constexpr (OSZ == 4) w[i] = *(const uint32_t*)at;
+            else w[i >> 1] |= (uint32_t)(*(const uint16_t*)at) << (16 * (i & 1));
         }
 #pragma unroll
-        for (int i = 0; i < C::kSteps; ++i) res.q[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        for (int i = 0; i < R::kSteps; ++i) res.q[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         return;
     }
-    const int j = lane % C::kPieces, r0 = lane / C::kPieces;
-    const char* at = (const char*)p + ((row0 + r0) * ld + col0 + C::kPer * j) * OSZ;
+    const int j = lane % C::kPieces, r0 = lane / C::kPieces + part * R::kSteps * C::kRows, left = cols - C::kPer * j;
+    const char* at = base + (r0 * ld + C::kPer * j) * OSZ;
+    const int64_t step = C::kRows * ld * OSZ;
 #pragma unroll
-    for (int i = 0; i < C::kSteps; ++i) {
+    for (int i = 0; i < R::kSteps; ++i, at += step) {
         res.q[i] = make_uint4(0, 0, 0, 0);
-        if (row0 + r0 + i * C::kRows < m && col0 + C::kPer * (j + 1) <= n)
-            res.q[i] = *reinterpret_cast<const uint4*>(at + (int64_t)i * C::kRows * ld * OSZ);
+        if (r0 + i * C::kRows >= rows) continue;
+        if (left >= C::kPer) res.q[i] = *reinterpret_cast<const uint4*>(at);
+        else if (left > 0) {   // the row ends inside this piece
+            uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int e = 0; e < C::kPer - 1; ++e) {
+                if (e >= left) continue;
+                if constexpr (OSZ == 4) w[e] = ((const uint32_t*)at)[e];
+                else w[e >> 1] |= (uint32_t)((const uint16_t*)at)[e] << (16 * (e & 1));
+            }
+            res.q[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
     }
 }
 
-// A slot of fp32 columns to memory, the residual added and rounded once.
+// A slot of fp32 columns to memory, the residual (from, or the 16-bit one in res) added
+// and rounded once.
 template <int ROW, int OSZ, int T>
-__device__ __forceinline__ void store_chunk(uint32_t slot, const Residual<ROW, OSZ>& res, const void* resp, int64_t ldr,
-                                            void* p, int64_t ld, int64_t row0, int64_t col0, int64_t m, int64_t n, bool vec,
-                                            int lane)
+__device__ __forceinline__ void store_chunk(uint32_t slot, Residual<ROW, OSZ>& res, const char* from, int64_t ldr, char* base,
+                                            int64_t ld, int rows, int cols, bool vec, int lane)
 {
     using C = Chunk<ROW, OSZ>;
-    const int rows = m - row0 < 32 ? (int)(m - row0) : 32, cols = n - col0 < C::kCols ? (int)(n - col0) : C::kCols;
-    const int j = lane % C::kPieces, r0 = lane / C::kPieces, left = cols - C::kPer * j;
-    if (vec && left >= C::kPer) {
-        char* at = (char*)p + ((row0 + r0) * ld + col0 + C::kPer * j) * OSZ;
+    using R = Residual<ROW, OSZ>;
+    const bool add = from != nullptr;
+#pragma unroll 1
+    for (int part = 0; part < R::kParts; ++part) {
+        if (R::kParts > 1 && add) fetch_residual(res, part, from, ldr, rows, cols, vec, lane);
+        if (vec) {
+            const int j = lane % C::kPieces, r0 = lane / C::kPieces + part * R::kSteps * C::kRows, left = cols - C::kPer * j;
+            if (left <= 0) continue;
+            const uint32_t first = slot + slot_piece<ROW>(r0, OSZ == 4 ? j : 2 * j);
+            char* at = base + (r0 * ld + C::kPer * j) * OSZ;
+            const int64_t step = C::kRows * ld * OSZ;
 #pragma unroll
-        for (int i = 0; i < C::kSteps; ++i) {
-            const int r = r0 + i * C::kRows;
-            if (r < rows) {
-                uint4 out = ld_shared16(slot + slot_piece<ROW>(r, OSZ == 4 ? j : 2 * j));
+            for (int i = 0; i < R::kSteps; ++i, at += step) {
+                if (r0 + i * C::kRows >= rows) break;
+                const uint32_t a = slot_walk<ROW, C::kRows>(first, i);
+                uint4 out = ld_shared16(a);
                 if constexpr (OSZ == 4) {
-                    if (resp) {
+                    if (add) {
                         out.x = __float_as_uint(__uint_as_float(out.x) + __uint_as_float(res.q[i].x));
                         out.y = __float_as_uint(__uint_as_float(out.y) + __uint_as_float(res.q[i].y));
                         out.z = __float_as_uint(__uint_as_float(out.z) + __uint_as_float(res.q[i].z));
                         out.w = __float_as_uint(__uint_as_float(out.w) + __uint_as_float(res.q[i].w));
                     }
                 } else {
-                    const uint4 hi = ld_shared16(slot + slot_piece<ROW>(r, 2 * j + 1));
-                    const float2 a = unpack_half2(res.q[i].x, T), b = unpack_half2(res.q[i].y, T),
-                                 c = unpack_half2(res.q[i].z, T), d = unpack_half2(res.q[i].w, T);
-                    out = make_uint4(pack_half2(__uint_as_float(out.x) + a.x, __uint_as_float(out.y) + a.y, T),
-                                     pack_half2(__uint_as_float(out.z) + b.x, __uint_as_float(out.w) + b.y, T),
-                                     pack_half2(__uint_as_float(hi.x) + c.x, __uint_as_float(hi.y) + c.y, T),
+                    const uint4 hi = ld_shared16(a ^ 16);   // piece 2 j + 1
+                    const float2 r = unpack_half2(res.q[i].x, T), g = unpack_half2(res.q[i].y, T),
+                                 b = unpack_half2(res.q[i].z, T), d = unpack_half2(res.q[i].w, T);
+                    out = make_uint4(pack_half2(__uint_as_float(out.x) + r.x, __uint_as_float(out.y) + r.y, T),
+                                     pack_half2(__uint_as_float(out.z) + g.x, __uint_as_float(out.w) + g.y, T),
+                                     pack_half2(__uint_as_float(hi.x) + b.x, __uint_as_float(hi.y) + b.y, T),
                                      pack_half2(__uint_as_float(hi.z) + d.x, __uint_as_float(hi.w) + d.y, T));
                 }
-                *reinterpret_cast<uint4*>(at + (int64_t)i * C::kRows * ld * OSZ) = out;
-            }
-        }
-    } else if (vec) {   // the row ends inside this thread's piece
-        for (int r = r0; r < rows; r += C::kRows)
-            for (int e = 0; e < left; ++e) {
-                const int c = C::kPer * j + e;
-                float v = ld_shared_f32(slot + slot_piece<ROW>(r, c >> 2) + 4 * (c & 3));
-                if (resp) v += load_elem(resp, (row0 + r) * ldr + col0 + c, T);
-                store_elem(p, (row0 + r) * ld + col0 + c, T, v);
-            }
-    } else if (lane % C::kCols < cols) {
-        const int c = lane % C::kCols, rr = lane / C::kCols;
-        char* at = (char*)p + ((row0 + rr) * ld + col0 + c) * OSZ;
+                if (left >= C::kPer) *reinterpret_cast<uint4*>(at) = out;
+                else {   // the row ends inside this piece
+                    const uint32_t w[4] = {out.x, out.y, out.z, out.w};
 #pragma unroll
-        for (int i = 0; i < 32 / C::kColThreads; ++i, at += C::kColThreads * ld * OSZ) {
-            const int r = rr + i * C::kColThreads;
-            float v = ld_shared_f32(slot + slot_piece<ROW>(r, c >> 2) + 4 * (c & 3));
-            const int word = OSZ == 4 ? i : i >> 1;
-            const uint4 q = res.q[word >> 2];
-            const uint32_t w = (word & 3) == 0 ? q.x : ((word & 3) == 1 ? q.y : ((word & 3) == 2 ? q.z : q.w));
-            if (resp) v += OSZ == 4 ? __uint_as_float(w) : (i & 1 ? unpack_half2(w, T).y : unpack_half2(w, T).x);
-            if (r < rows) store_elem(at, 0, T, v);
+                    for (int e = 0; e < C::kPer - 1; ++e) {
+                        if (e >= left) continue;
+                        if constexpr (OSZ == 4) ((uint32_t*)at)[e] = w[e];
+                        else ((uint16_t*)at)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                    }
+                }
+            }
+        } else if (lane % C::kCols < cols) {
+            constexpr int kVisits = 32 / C::kColThreads / R::kParts;
+            const int c = lane % C::kCols, rr = lane / C::kCols + part * kVisits * C::kColThreads;
+            char* at = base + (rr * ld + c) * OSZ;
+#pragma unroll
+            for (int i = 0; i < kVisits; ++i, at += C::kColThreads * ld * OSZ) {
+                const int r = rr + i * C::kColThreads;
+                float v = ld_shared_f32(slot + slot_piece<ROW>(r, c >> 2) + 4 * (c & 3));
+                const int word = OSZ == 4 ? i : i >> 1;
+                const uint4 q = res.q[word >> 2];
+                const uint32_t w = (word & 3) == 0 ? q.x : ((word & 3) == 1 ? q.y : ((word & 3) == 2 ? q.z : q.w));
+                if (add) v += OSZ == 4 ? __uint_as_float(w) : (i & 1 ? unpack_half2(w, T).y : unpack_half2(w, T).x);
+                if (r < rows) store_elem(at, 0, T, v);
+            }
         }
     }
 }
@@ -472,31 +512,34 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         float* const factors = columns + (warp - 2) * 32;
         const bool has_factors = p.e4m3 || p.bias;
         const int passes = p.zp ? (GLU ? 3 : 2) : 1;
-        const auto factor = [&](int64_t col) -> float {
-            if (lane < 16) return p.w_scale[0] && col < p.n ? p.w_scale[0][col] : 1.0f;
-            if constexpr (GLU) return p.w_scale[1] && col < p.n ? p.w_scale[1][col] : 1.0f;
-            else return p.bias && col < p.n ? load_elem(p.bias, col, p.bias_type) : 0.0f;
+        const uint32_t mine = slot + slot_piece<S::kSlotRow>(lane, 0);
+        const uint32_t m = (uint32_t)p.m, n = (uint32_t)p.n;
+        const auto factor = [&](uint32_t col) -> float {
+            if (lane < 16) return p.w_scale[0] && col < n ? p.w_scale[0][col] : 1.0f;
+            if constexpr (GLU) return p.w_scale[1] && col < n ? p.w_scale[1][col] : 1.0f;
+            else return p.bias && col < n ? load_elem(p.bias, col, p.bias_type) : 0.0f;
         };
         uint32_t tile = 0;
         for (uint32_t u = first; u < p.units; u += step, ++tile) {
             if (S::kTurns > 1 && (int)(tile % S::kTurns) != turn) continue;
             const uint32_t acc = tile % S::kAccs;
             const Unit q = decode(p, u);
-            const int64_t row0 = (int64_t)q.tm * S::kTileM + rank * kRowsA + quarter * 32;
-            const int64_t col0 = (int64_t)q.tn * S::kOutCols + col_group * kGroupCols;
-            const bool live = row0 < p.m && col0 < p.n;
-            const float xs = p.x_scale && row0 + lane < p.m ? p.x_scale[row0 + lane] : 1.0f;
+            const uint32_t row0 = q.tm * S::kTileM + rank * kRowsA + quarter * 32;
+            const uint32_t col0 = q.tn * S::kOutCols + col_group * kGroupCols;
+            const bool live = row0 < m && col0 < n;
+            const int rows = live ? (int)(m - row0 < 32 ? m - row0 : 32) : 0, cols = live ? (int)(n - col0) : 0;
+            const float xs = p.x_scale && lane < rows ? p.x_scale[row0 + lane] : 1.0f;
             // the columns' factors, 16 columns at a time: lanes 0-15 the first, 16-31 the
             // second; they and the residual's way into L2 start before the accumulator is waited for
             float f0 = 1.0f, f1 = 1.0f, f2 = 1.0f, f3 = 1.0f;
             if (has_factors && live) {
-                const int64_t col = col0 + (lane & 15);
+                const uint32_t col = col0 + (lane & 15);
                 f0 = factor(col), f1 = factor(col + 16), f2 = factor(col + 32), f3 = factor(col + 48);
             }
-            if (!GLU && p.residual && live && row0 + lane < p.m) {
-                const char* at = (const char*)p.residual + ((row0 + lane) * p.ldr + col0) * OSZ;
+            if (!GLU && p.residual && lane < rows) {
+                const char* at = (const char*)p.residual + ((int64_t)(row0 + lane) * p.ldr + col0) * OSZ;
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
-                if (OSZ == 4 && col0 + 32 < p.n) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 128));
+                if (OSZ == 4 && cols > 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 128));
             }
             if (!__all_sync(0xffffffffu, mbar_wait(bar_acc + 8 * acc, (tile / S::kAccs) & 1, gave_up))) break;
             tc_fence_after();
@@ -559,54 +602,51 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
 
             for (int pass = 0; live && pass < passes; ++pass) {
                 const bool last = pass == passes - 1;
-                if (!last || (OSZ == 2 && !p.residual)) {   // in 16 bits
+                if (GLU || !last || (OSZ == 2 && !p.residual)) {   // in 16 bits
                     constexpr int kCols = S::kSlotRow / 2;
                     const int type = last ? p.out_type : p.z_type;
-                    void* const to = last ? p.yp[q.prob] : (GLU && pass == 1 ? p.z2p : p.zp);
                     const int64_t ld = last ? p.ldy[q.prob] : (GLU && pass == 1 ? p.ldz2 : p.ldz);
+                    uint16_t* to = (uint16_t*)(last ? p.yp[q.prob] : (GLU && pass == 1 ? p.z2p : p.zp)) + row0 * ld + col0;
 #pragma unroll 1
-                    for (int h = 0; h < kGroupCols / kCols; ++h) {
-                        const int64_t at = col0 + kCols * h;
-                        if (at >= p.n) break;
+                    for (int c = 0; c < kGroupCols && c < cols; c += kCols, to += kCols) {
                         __syncwarp();   // the slot's last readers are done
 #pragma unroll 1
                         for (int s = 0; s < kCols / 16; ++s) {
                             float v[16];
-                            columns16(kCols * h + 16 * s, pass, v);
-                            if (type == GS_BF16) slot_put_half<S::kSlotRow, GS_BF16>(slot, lane, s, v);
-                            else slot_put_half<S::kSlotRow, GS_F16>(slot, lane, s, v);
+                            columns16(c + 16 * s, pass, v);
+                            if (type == GS_BF16) slot_put_half<GS_BF16>(mine, s, v);
+                            else slot_put_half<GS_F16>(mine, s, v);
                         }
                         __syncwarp();
-                        store_half<S::kSlotRow>(slot, to, ld, row0, at, p.m, p.n, last ? p.y_vec : p.z_vec, lane);
+                        store_half<S::kSlotRow>(slot, to, ld, rows, cols - c < kCols ? cols - c : kCols,
+                                                last ? p.y_vec : p.z_vec, lane);
                     }
-                } else {   // in fp32, the residual added on the way out
+                } else if constexpr (!GLU) {   // in fp32, the residual added on the way out
                     constexpr int kCols = S::kSlotRow / 4;
-                    const bool vec = p.y_vec && (p.r_vec || !p.residual);
+                    const bool add = p.residual != nullptr, vec = p.y_vec && (p.r_vec || !add);
+                    const int64_t ld = p.ldy[p.partial ? 0 : q.prob];
+                    char* to = (char*)p.yp[p.partial ? 0 : q.prob] + (row0 * ld + col0) * OSZ;
+                    if (p.partial) to += (int64_t)(q.prob * p.splits + q.split) * p.part * OSZ;
+                    const char* from = add ? (const char*)p.residual + (row0 * p.ldr + col0) * OSZ : nullptr;
 #pragma unroll 1
-                    for (int h = 0; h < kGroupCols / kCols; ++h) {
-                        const int64_t at = col0 + kCols * h;
-                        if (at >= p.n) break;
+                    for (int c = 0; c < kGroupCols && c < cols; c += kCols, to += kCols * OSZ) {
+                        const int part = cols - c < kCols ? cols - c : kCols;
                         Residual<S::kSlotRow, OSZ> res;
-                        if (p.residual) fetch_residual(res, p.residual, p.ldr, row0, at, p.m, p.n, vec, lane);
+                        if (OSZ == 2) fetch_residual(res, 0, from, p.ldr, rows, part, vec, lane);
                         __syncwarp();
 #pragma unroll 1
                         for (int s = 0; s < kCols / 16; ++s) {
                             float v[16];
-                            columns16(kCols * h + 16 * s, pass, v);
-                            slot_put<S::kSlotRow>(slot, lane, s, v);
+                            columns16(c + 16 * s, pass, v);
+                            slot_put(mine, s, v);
                         }
                         __syncwarp();
-                        if constexpr (OSZ == 4) {
-                            float* const to = (float*)p.yp[p.partial ? 0 : q.prob] +
-                                              (p.partial ? (int64_t)(q.prob * p.splits + q.split) * p.part : 0);
-                            store_chunk<S::kSlotRow, 4, GS_F32>(slot, res, p.residual, p.ldr, to,
-                                                                p.ldy[p.partial ? 0 : q.prob], row0, at, p.m, p.n, vec, lane);
-                        } else if (p.out_type == GS_BF16)
-                            store_chunk<S::kSlotRow, 2, GS_BF16>(slot, res, p.residual, p.ldr, p.yp[0], p.ldy[0], row0, at,
-                                                                 p.m, p.n, vec, lane);
-                        else
-                            store_chunk<S::kSlotRow, 2, GS_F16>(slot, res, p.residual, p.ldr, p.yp[0], p.ldy[0], row0, at,
-                                                                p.m, p.n, vec, lane);
+                        if constexpr (OSZ == 4)
+                            store_chunk<S::kSlotRow, 4, GS_F32>(slot, res, from, p.ldr, to, ld, rows, part, vec, lane);
+                        else if (p.out_type == GS_BF16)
+                            store_chunk<S::kSlotRow, 2, GS_BF16>(slot, res, from, p.ldr, to, ld, rows, part, vec, lane);
+                        else store_chunk<S::kSlotRow, 2, GS_F16>(slot, res, from, p.ldr, to, ld, rows, part, vec, lane);
+                        if (add) from += kCols * OSZ;
                     }
                 }
             }
