@@ -19,6 +19,8 @@
 // shared memory delivers, so wide problems use the pair: 256 x 256 over two SMs, each
 // holding half of B, half the shared-memory bytes a product.  With small k (a
 // Gaussian decoder's layers) HBM, through the epilogue's stores.
+#include <type_traits>
+
 #include "gemm.cuh"
 #include "tc_common.cuh"
 
@@ -67,11 +69,11 @@ struct Shape {
     static constexpr int kBytesA = kRowsA * kStageRow;
     static constexpr int kBytesB = kRowsB * kStageRow;
     static constexpr int kStageBytes = kBytesA + kBytesB;
-    // Staging of an epilogue warp: 32 rows of 128 bytes, or of 64 in a pair, whose sixth
-    // stage is worth more (32768 x 1024 -> 4096: 4, 5 stages 167, 162 us).
-    static constexpr int kSlotRow = PAIR ? 64 : 128;
+    // Staging of an epilogue warp: 32 rows of 128 bytes, or of 64 in the wide pair, whose
+    // sixth stage is worth more (32768 x 1024 -> 4096: 4, 5 stages 167, 162 us).
+    static constexpr int kSlotRow = BN == 256 ? 64 : 128;
     static constexpr int kSlot = 32 * kSlotRow;
-    static constexpr int kStages = BN == 64 || PAIR ? 6 : 5;
+    static constexpr int kStages = BN == 128 && !PAIR ? 5 : 6;
     // Four groups of epilogue warps, 64 output columns each: all on one tile, or tiles in turn.
     static constexpr int kOutCols = GLU ? BN / 2 : BN;
     static constexpr int kGroupsTile = kOutCols / kGroupCols;
@@ -884,16 +886,26 @@ int device_sms()
     return sms;
 }
 
-// Cycles of a configuration: waves of tiles, each bound by its products, the shared
-// memory and TMA traffic that feeds them, or its epilogue, and a start-up.
-double cost(const GemmCall& c, int bn, bool pair, int sms, Plan* out)
+// Tile shapes: B's columns and whether two SMs share a tile.
+struct Tile {
+    int bn;
+    bool pair;
+    double per_kb;   // cycles a k-block (128 bytes of k) takes, measured
+};
+// An SM takes in 64 bytes a cycle: 24, 32, 24 and 32 KB a k-block, against 128, 256,
+// 256 and 512 cycles of products.  So the wide pair alone keeps the tensor cores fed.
+constexpr Tile kTiles[4] = {{64, false, 480}, {128, false, 570}, {128, true, 430}, {256, true, 600}};
+
+// Cycles of a call with a tile shape: waves of tiles, each bound by its k-blocks or by
+// its epilogue's traffic (about 16 bytes a cycle and SM), and a start-up.
+double cost(const GemmCall& c, const Tile& t, int sms, Plan* out)
 {
     Plan& p = *out;
     const bool glu = c.kind == GemmKind::kGlu;
-    p.pair = pair;
-    p.bn = bn;
-    p.tile_m = pair ? 256 : 128;
-    p.out_cols = glu ? bn / 2 : bn;
+    p.pair = t.pair;
+    p.bn = t.bn;
+    p.tile_m = t.pair ? 256 : 128;
+    p.out_cols = glu ? t.bn / 2 : t.bn;
     p.tiles_m = (c.m + p.tile_m - 1) / p.tile_m;
     p.tiles_n = (c.n + p.out_cols - 1) / p.out_cols;
     p.esz = type_bytes(c.type);
@@ -901,24 +913,28 @@ double cost(const GemmCall& c, int bn, bool pair, int sms, Plan* out)
     p.k_blocks = (c.k + p.k_elems - 1) / p.k_elems;
     p.terms = c.kind == GemmKind::kSum ? 2 : 1;
     p.probs = c.kind == GemmKind::kTwo ? 2 : 1;
-    const int64_t tiles = p.tiles_m * p.tiles_n * p.probs, slots = pair ? sms / 2 : sms, kb = p.k_blocks * p.terms;
+    const int64_t tiles = p.tiles_m * p.tiles_n * p.probs, slots = t.pair ? sms / 2 : sms, kb = p.k_blocks * p.terms;
     // Few tiles: split k over the idle SMs, at least four k-blocks each, where nothing
     // but the sum is asked for (the gradients): the partial sums are joined in order.
     const bool sum_only = c.kind != GemmKind::kGlu && !c.bias && !c.residual && !c.z && c.act == GS_ACT_NONE &&
                           !c.x_scale && !c.w_scale[0];
-    int64_t splits = 1;
-    if (sum_only && tiles < slots) {
-        splits = slots / tiles;
-        if (splits > kb / 4) splits = kb / 4;
-        if (splits < 1) splits = 1;
+    const double live = (double)(c.n < p.out_cols ? c.n : p.out_cols);
+    const int bytes = type_bytes(c.out_type) * (c.residual ? 2 : 1) + (c.z ? (glu ? 4 : 2) : 0);
+    double best = 0;
+    for (int64_t s = 1; s == 1 || (sum_only && s * tiles <= slots && s * 4 <= kb); ++s) {
+        const double main = t.per_kb * (double)((kb + s - 1) / s);
+        const double epi = 500 + 128.0 * live * (s > 1 ? 4 : bytes) / (t.bn == 256 ? 14 : 16);
+        const double waves = (double)((tiles * s + slots - 1) / slots);
+        // the join: a launch, and every partial sum read once at about 20 bytes a cycle and SM
+        const double join = s > 1 ? 3500 + (double)s * c.m * c.n * p.probs * 4 / (sms * 20.0) : 0;
+        const double v = 3000 + waves * (main > epi ? main : epi) + (main > epi ? epi : main) + join;
+        if (s == 1 || v < best) {
+            best = v;
+            p.splits = (int)s;
+        }
     }
-    p.splits = (int)splits;
-    p.units = tiles * splits;
-    const double per_kb = bn == 64 ? 200 : (bn == 128 ? 330 : 520);
-    const double main = per_kb * (double)((kb + splits - 1) / splits), epi = 10.0 * bn + 300;
-    const double waves = (double)((p.units + slots - 1) / slots);
-    const double join = splits > 1 ? 4000 + (double)splits * c.m * c.n * p.probs * 8 / (sms * 20.0) : 0;
-    return 2500 + waves * (main > epi ? main : epi) + (main > epi ? epi : main) + join;
+    p.units = tiles * p.splits;
+    return best;
 }
 
 int64_t stored_rows(const GemmFactor& f, int64_t rows, int64_t k) { return f.k_fast ? rows : k; }
@@ -930,9 +946,8 @@ Plan make_plan(const GemmCall& c)
     Plan best, p;
     double at = 0;
     const bool glu = c.kind == GemmKind::kGlu;
-    const int bns[3] = {64, 128, 256};
-    for (int i = glu ? 1 : 0; i < 3; ++i) {
-        const double v = cost(c, bns[i], bns[i] == 256, sms, &p);
+    for (int i = glu ? 1 : 0; i < 4; ++i) {
+        const double v = cost(c, kTiles[i], sms, &p);
         if (i == (glu ? 1 : 0) || v < at) {
             at = v;
             best = p;
@@ -1155,15 +1170,17 @@ gs_status gemm_run(const GemmCall& c, void* ws, cudaStream_t st)
     const int64_t most = plan.pair ? sms / 2 : sms;
     const int grid = (int)(plan.units < most ? plan.units : most) * (plan.pair ? 2 : 1);
     gs_status s;
-    if (glu) s = plan.pair ? launch<256, true, true, 2>(p, grid, st) : launch<128, false, true, 2>(p, grid, st);
-    else if (out_type == GS_F32)
-        s = plan.pair         ? launch<256, true, false, 4>(p, grid, st)
-            : plan.bn == 128 ? launch<128, false, false, 4>(p, grid, st)
-                             : launch<64, false, false, 4>(p, grid, st);
-    else
-        s = plan.pair         ? launch<256, true, false, 2>(p, grid, st)
-            : plan.bn == 128 ? launch<128, false, false, 2>(p, grid, st)
-                             : launch<64, false, false, 2>(p, grid, st);
+    const auto pick = [&](auto osz) {
+        constexpr int OSZ = decltype(osz)::value;
+        if (plan.pair) return plan.bn == 256 ? launch<256, true, false, OSZ>(p, grid, st) : launch<128, true, false, OSZ>(p, grid, st);
+        return plan.bn == 128 ? launch<128, false, false, OSZ>(p, grid, st) : launch<64, false, false, OSZ>(p, grid, st);
+    };
+    if (glu)
+        s = !plan.pair         ? launch<128, false, true, 2>(p, grid, st)
+            : plan.bn == 256 ? launch<256, true, true, 2>(p, grid, st)
+                             : launch<128, true, true, 2>(p, grid, st);
+    else if (out_type == GS_F32) s = pick(std::integral_constant<int, 4>());
+    else s = pick(std::integral_constant<int, 2>());
     if (s != GS_OK || !p.partial) return s;
     const float* partial = (const float*)(base + plan.partial_at);
     for (int i = 0; i < plan.probs; ++i) {

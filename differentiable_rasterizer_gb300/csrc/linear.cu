@@ -123,25 +123,54 @@ __global__ void __launch_bounds__(kElemThreads) glu_grad_kernel(const GluGradPar
     }
 }
 
-// 32 values x 8 slices of the parts a block: slice y sums parts y, y + 8, ...,
-// then the slices are added in order.
-__global__ void __launch_bounds__(256) join_partials_kernel(const float* partial, int64_t parts, int64_t rows,
-                                                            int64_t cols, int64_t pitch, void* out, int64_t ld, int type)
+// Sums of partial rows, in the order of the parts.  A thread takes VEC columns of one
+// row; with SLICES > 1 it takes every SLICES-th part, and the block adds the slices in
+// order.  Few parts of a large result: SLICES 1, one pass at the reads' bandwidth; many
+// parts of a small one (a decoder's weights over a million rows): SLICES 8.
+template <int VEC, int SLICES>
+__global__ void __launch_bounds__(256) join_partials_kernel(const float* partial, int parts, int64_t count, uint32_t rows,
+                                                            uint32_t cols, uint32_t pitch, void* out, int64_t ld, int type)
 {
-    __shared__ float sm[8][33];
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int64_t i = (int64_t)blockIdx.x * 32 + x, count = rows * pitch;
-    const int64_t r = i / pitch, c = i % pitch;
-    const bool live = i < count && c < cols;
-    float t = 0.0f;
-    if (live)
-        for (int64_t p = y; p < parts; p += 8) t += partial[p * count + i];
-    sm[y][x] = t;
-    __syncthreads();
-    if (y == 0 && live) {
-        for (int k = 1; k < 8; ++k) t += sm[k][x];
-        store_elem(out, r * ld + c, type, t);
+    constexpr int kWide = 256 / SLICES;
+    __shared__ float sm[SLICES > 1 ? SLICES : 1][kWide * VEC + 1];
+    const int x = threadIdx.x % kWide, y = threadIdx.x / kWide;
+    const uint32_t per_row = (cols + VEC - 1) / VEC;
+    const uint32_t i = blockIdx.x * kWide + x, r = i / per_row, c = (i - r * per_row) * VEC;
+    const bool live = r < rows;
+    float t[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) t[e] = 0.0f;
+    if (live) {
+        const float* at = partial + (int64_t)r * pitch + c;
+#pragma unroll 4
+        for (int p = y; p < parts; p += SLICES) {
+            if constexpr (VEC == 4) {
+                const float4 f = *reinterpret_cast<const float4*>(at + p * count);
+                t[0] += f.x, t[1] += f.y, t[2] += f.z, t[3] += f.w;
+            } else t[0] += at[p * count];
+        }
     }
+    if constexpr (SLICES > 1) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) sm[y][x * VEC + e] = t[e];
+        __syncthreads();
+        if (y > 0) return;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            for (int k = 1; k < SLICES; ++k) t[e] += sm[k][x * VEC + e];
+    }
+    if (!live) return;
+    const int64_t to = (int64_t)r * ld + c;
+    const size_t whole = VEC * (type == GS_F32 ? 4 : 2);
+    if (VEC == 4 && c + 4 <= cols && (((uintptr_t)out + (size_t)to * (whole / VEC)) & (whole - 1)) == 0) {
+        if (type == GS_F32) *reinterpret_cast<float4*>((float*)out + to) = make_float4(t[0], t[VEC > 1 ? 1 : 0], t[VEC > 1 ? 2 : 0], t[VEC > 1 ? 3 : 0]);
+        else *reinterpret_cast<uint2*>((uint16_t*)out + to) =
+                 make_uint2(pack_half2(t[0], t[VEC > 1 ? 1 : 0], type), pack_half2(t[VEC > 1 ? 2 : 0], t[VEC > 1 ? 3 : 0], type));
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+        if (c + e < cols) store_elem(out, to + e, type, t[e]);
 }
 
 // Calls f with the 16-bit type and the activation as constants.
@@ -206,9 +235,18 @@ struct Scratch {
 gs_status join_partials(const float* partial, int64_t parts, int64_t rows, int64_t cols, int64_t pitch, void* out,
                         int64_t ld, int type, cudaStream_t st)
 {
-    const int64_t blocks = (rows * pitch + 31) / 32;
-    if (blocks > 0x7fffffffll) return GS_ERR_INVALID_ARG;
-    join_partials_kernel<<<(unsigned)blocks, 256, 0, st>>>(partial, parts, rows, cols, pitch, out, ld, type);
+    const bool vec = pitch % 4 == 0 && aligned16(partial);
+    const int64_t threads = rows * (vec ? (cols + 3) / 4 : cols), count = rows * pitch;
+    const bool sliced = threads < 152 * 512;   // too few threads to fill the SMs, one a result
+    const int64_t wide = sliced ? 32 : 256, blocks = (threads + wide - 1) / wide;
+    if (blocks > 0x7fffffll || threads > 0x7fffffffll) return GS_ERR_INVALID_ARG;
+    const unsigned grid = (unsigned)blocks;
+    const uint32_t r = (uint32_t)rows, c = (uint32_t)cols, q = (uint32_t)pitch;
+    const int n = (int)parts;
+    if (vec && sliced) join_partials_kernel<4, 8><<<grid, 256, 0, st>>>(partial, n, count, r, c, q, out, ld, type);
+    else if (vec) join_partials_kernel<4, 1><<<grid, 256, 0, st>>>(partial, n, count, r, c, q, out, ld, type);
+    else if (sliced) join_partials_kernel<1, 8><<<grid, 256, 0, st>>>(partial, n, count, r, c, q, out, ld, type);
+    else join_partials_kernel<1, 1><<<grid, 256, 0, st>>>(partial, n, count, r, c, q, out, ld, type);
     GS_LAUNCH_CHECK();
     return GS_OK;
 }
