@@ -366,36 +366,91 @@ __device__ __forceinline__ void activate(float (&v)[16], int act)
     else if (act == GS_ACT_RELU) activate<GS_ACT_RELU>(v);
 }
 
-// The MMA warp's loop: the warp waits together, one lane issues.
-template <int BN, bool PAIR, bool GLU, bool E4M3>
+// The loops of the producer's and the MMA warp's elected lanes.  One thread's
+// instructions come five or more cycles apart, so a k-block must cost few of them:
+// the factors' orders are constants, the ring is stepped, addresses are added to
+// (with all of that in the loop a k-block took 500 cycles whatever its products:
+// 2048 x 4096 -> 1024 19 us).
+template <int BN, bool PAIR, bool GLU, bool A_FAST, bool B_FAST>
+__device__ __forceinline__ void load_tiles(const Params& p, uint32_t first, uint32_t step, uint32_t rank, uint32_t stages,
+                                           uint32_t bar_full, uint32_t bar_empty, volatile int* gave_up)
+{
+    using S = Shape<BN, PAIR, GLU>;
+    const uint32_t full0 = PAIR ? map_rank(bar_full, 0) : bar_full;   // the pair counts at its first CTA
+    const int k_elems = p.k_elems;
+    const uint32_t k_blocks = p.k_blocks, units = p.units;
+    Ring<S::kStages> ring;
+    uint32_t issued = 0;
+    for (uint32_t u = first; u < units; u += step) {
+        const Unit q = decode(p, u);
+        const int row_a = (int)(q.tm * S::kTileM + rank * kRowsA);
+        const int row_b = GLU ? (int)(q.tn * (BN / 2)) : (int)(q.tn * BN + rank * S::kRowsB);
+        uint32_t kb = q.kb0;
+        while (kb < q.kb1) {   // the k-blocks of one term
+            const uint32_t term = kb >= k_blocks ? 1 : 0, which = p.probs > 1 ? q.prob : term;
+            const uint32_t end = term == 0 && q.kb1 > k_blocks ? k_blocks : q.kb1;
+            const CUtensorMap *a = &p.a[which], *b = &p.b[GLU && PAIR ? rank : which];
+            int k = (int)(kb - term * k_blocks) * k_elems;
+            for (; kb < end; ++kb, k += k_elems, ++issued) {
+                if (!mbar_wait(bar_empty + 8 * ring.s, ring.parity ^ 1, gave_up)) {
+                    // given up: let the copies in flight land before the block leaves
+                    volatile int still = 0;
+                    for (int i = 0; rank == 0 && i < S::kStages && (uint32_t)i < issued; ++i) {
+                        const uint32_t s = (ring.s + S::kStages - 1 - i) % S::kStages;
+                        mbar_wait(bar_full + 8 * s, s < ring.s ? ring.parity : ring.parity ^ 1, &still);
+                    }
+                    return;
+                }
+                const uint32_t full = full0 + 8 * ring.s, sa = stages + ring.s * S::kStageBytes, sb = sa + S::kBytesA;
+                if (rank == 0) mbar_expect(bar_full + 8 * ring.s, S::kStageBytes * (PAIR ? 2 : 1));
+                if constexpr (A_FAST) tma_load_2d<PAIR>(sa, a, k, row_a, full);
+                else
+#pragma unroll
+                    for (int i = 0; i < kRowsA / 64; ++i) tma_load_2d<PAIR>(sa + i * 8192, a, row_a + 64 * i, k, full);
+                if constexpr (GLU && !PAIR) {
+                    tma_load_2d<PAIR>(sb, &p.b[0], k, row_b, full);
+                    tma_load_2d<PAIR>(sb + S::kBytesB / 2, &p.b[1], k, row_b, full);
+                } else if constexpr (B_FAST) tma_load_2d<PAIR>(sb, b, k, row_b, full);
+                else
+#pragma unroll
+                    for (int i = 0; i < S::kRowsB / 64; ++i) tma_load_2d<PAIR>(sb + i * 8192, b, row_b + 64 * i, k, full);
+                ring.next();
+            }
+        }
+    }
+}
+
+template <int BN, bool PAIR, bool GLU, bool A_FAST, bool B_FAST, bool E4M3>
 __device__ __forceinline__ void issue_products(const Params& p, uint32_t first, uint32_t step, uint32_t stages,
                                                uint32_t bar_full, uint32_t bar_empty, uint32_t bar_acc, uint32_t bar_free,
                                                uint32_t tmem, volatile int* gave_up)
 {
     using S = Shape<BN, PAIR, GLU>;
-    const uint64_t desc_a = smem_desc(stages, p.a_fast), desc_b = smem_desc(stages + S::kBytesA, p.b_fast);
-    const uint32_t step_a = k_step(p.a_fast), step_b = k_step(p.b_fast);
-    uint32_t it = 0, tile = 0;
-    for (uint32_t u = first; u < p.units; u += step, ++tile) {
+    constexpr uint32_t kStepA = k_step(A_FAST), kStepB = k_step(B_FAST);
+    const uint32_t lo_a = desc_lo(stages, A_FAST), lo_b = desc_lo(stages + S::kBytesA, B_FAST), idesc = p.idesc;
+    const uint32_t units = p.units;
+    Ring<S::kStages> ring;
+    Ring<S::kAccs> acc;
+    for (uint32_t u = first; u < units; u += step) {
         const Unit q = decode(p, u);
-        const uint32_t acc = tile % S::kAccs;
-        if (!__all_sync(0xffffffffu, mbar_wait(bar_free + 8 * acc, ((tile / S::kAccs) & 1) ^ 1, gave_up))) return;
+        if (!mbar_wait(bar_free + 8 * acc.s, acc.parity ^ 1, gave_up)) return;
         tc_fence_after();
-        const uint32_t d = tmem + acc * BN;
-        for (uint32_t kb = q.kb0; kb < q.kb1; ++kb, ++it) {
-            const uint32_t s = it % S::kStages;
-            if (!__all_sync(0xffffffffu, mbar_wait(bar_full + 8 * s, (it / S::kStages) & 1, gave_up))) return;
+        const uint32_t d = tmem + acc.s * BN;
+        uint32_t add = 0;
+        for (uint32_t kb = q.kb1 - q.kb0; kb > 0; --kb) {
+            if (!mbar_wait(bar_full + 8 * ring.s, ring.parity, gave_up)) return;
             tc_fence_after();
-            if (elect_one()) {
-                const uint64_t da = desc_a + s * (S::kStageBytes >> 4), db = desc_b + s * (S::kStageBytes >> 4);
+            const uint32_t a = lo_a + ring.s * (S::kStageBytes >> 4), b = lo_b + ring.s * (S::kStageBytes >> 4);
+            mma<PAIR, E4M3>(d, a, kDescHi, b, kDescHi, idesc, add);
 #pragma unroll
-                for (uint32_t i = 0; i < 4; ++i)
-                    mma<PAIR, E4M3>(d, da + i * step_a, db + i * step_b, p.idesc, kb > q.kb0 || i > 0);
-                mma_commit<PAIR>(bar_empty + 8 * s);   // the stage is free once these are done
-                if (kb + 1 == q.kb1) mma_commit<PAIR>(bar_acc + 8 * acc);
-            }
-            __syncwarp();
+            for (uint32_t i = 1; i < 4; ++i)
+                mma<PAIR, E4M3>(d, a + i * kStepA, kDescHi, b + i * kStepB, kDescHi, idesc, 1);
+            add = 1;
+            mma_commit<PAIR>(bar_empty + 8 * ring.s);   // the stage is free once these are done
+            ring.next();
         }
+        mma_commit<PAIR>(bar_acc + 8 * acc.s);
+        acc.next();
     }
 }
 
@@ -445,63 +500,32 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     const uint32_t tmem = *tmem_slot;
 
     if (warp == 0) {
-        // -------------------------------------------------------------- producer
         if (elect_one()) {
             prefetch_map(&p.a[0]);
             prefetch_map(&p.b[0]);
-        }
-        const uint32_t full0 = PAIR ? map_rank(bar_full, 0) : bar_full;   // the pair counts at its first CTA
-        uint32_t it = 0;
-        bool ok = true;
-        for (uint32_t u = first; u < p.units && ok; u += step) {
-            const Unit q = decode(p, u);
-            const int row_a = (int)(q.tm * S::kTileM + rank * kRowsA);
-            const int row_b = GLU ? (int)(q.tn * (BN / 2)) : (int)(q.tn * BN + rank * S::kRowsB);
-            for (uint32_t kb = q.kb0; kb < q.kb1; ++kb, ++it) {
-                const int s = it % S::kStages;
-                ok = __all_sync(0xffffffffu, mbar_wait(bar_empty + 8 * s, ((it / S::kStages) & 1) ^ 1, gave_up));
-                if (!ok) break;
-                const int term = kb >= p.k_blocks ? 1 : 0;
-                const int k = (int)(kb - term * p.k_blocks) * p.k_elems;
-                const int which = p.probs > 1 ? q.prob : term;
-                if (elect_one()) {
-                    if (rank == 0) mbar_expect(bar_full + 8 * s, S::kStageBytes * (PAIR ? 2 : 1));
-                    const uint32_t full = full0 + 8 * s, sa = stages + s * S::kStageBytes, sb = sa + S::kBytesA;
-                    if (p.a_fast) tma_load_2d<PAIR>(sa, &p.a[which], k, row_a, full);
-                    else
-#pragma unroll
-                        for (int i = 0; i < kRowsA / 64; ++i)
-                            tma_load_2d<PAIR>(sa + i * 8192, &p.a[which], row_a + 64 * i, k, full);
-                    if constexpr (GLU) {
-                        if constexpr (PAIR) tma_load_2d<PAIR>(sb, &p.b[rank], k, row_b, full);
-                        else {
-                            tma_load_2d<PAIR>(sb, &p.b[0], k, row_b, full);
-                            tma_load_2d<PAIR>(sb + S::kBytesB / 2, &p.b[1], k, row_b, full);
-                        }
-                    } else if (p.b_fast) tma_load_2d<PAIR>(sb, &p.b[which], k, row_b, full);
-                    else
-#pragma unroll
-                        for (int i = 0; i < S::kRowsB / 64; ++i)
-                            tma_load_2d<PAIR>(sb + i * 8192, &p.b[which], row_b + 64 * i, k, full);
-                }
-                __syncwarp();
+            if (p.b_fast) load_tiles<BN, PAIR, GLU, true, true>(p, first, step, rank, stages, bar_full, bar_empty, gave_up);
+            else if constexpr (!GLU) {
+                if (p.a_fast) load_tiles<BN, PAIR, GLU, true, false>(p, first, step, rank, stages, bar_full, bar_empty, gave_up);
+                else load_tiles<BN, PAIR, GLU, false, false>(p, first, step, rank, stages, bar_full, bar_empty, gave_up);
             }
         }
-        if (!ok && rank == 0) {   // given up: let the copies in flight land before the block leaves
-            volatile int still = 0;
-            const uint32_t from = it > S::kStages ? it - S::kStages : 0;
-            for (uint32_t i = from; i < it; ++i)
-                mbar_wait(bar_full + 8 * (i % S::kStages), (i / S::kStages) & 1, &still);
-        }
     } else if (warp == 1) {
-        if (rank == 0) {
-            // ---------------------------------------------------------- tensor cores
-            if (p.e4m3) issue_products<BN, PAIR, GLU, true>(p, first, step, stages, bar_full, bar_empty, bar_acc, bar_free, tmem, gave_up);
-            else issue_products<BN, PAIR, GLU, false>(p, first, step, stages, bar_full, bar_empty, bar_acc, bar_free, tmem, gave_up);
+        if (rank == 0 && elect_one()) {
+            const auto issue = [&](auto a_fast, auto b_fast, auto e4m3) {
+                issue_products<BN, PAIR, GLU, decltype(a_fast)::value, decltype(b_fast)::value, decltype(e4m3)::value>(
+                    p, first, step, stages, bar_full, bar_empty, bar_acc, bar_free, tmem, gave_up);
+            };
+            const std::true_type yes;
+            const std::false_type no;
+            if (p.e4m3) issue(yes, yes, yes);
+            else if (p.b_fast) issue(yes, yes, no);
+            else if constexpr (!GLU) {
+                if (p.a_fast) issue(yes, no, no);
+                else issue(no, no, no);
+            }
             if (*gave_up) {
                 volatile int still = 0;
-                if (elect_one()) mma_commit<PAIR>(bar_drain);
-                __syncwarp();
+                mma_commit<PAIR>(bar_drain);
                 mbar_wait(bar_drain, 0, &still);
             }
         }
@@ -742,48 +766,50 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
     const uint32_t tmem = *tmem_slot;
 
     if (warp == 0) {
-        uint32_t it = 0;
-        bool ok = true;
-        for (uint32_t kb = kb0; kb < kb1; ++kb, ++it) {
-            const int s = it % S::kStages;
-            ok = __all_sync(0xffffffffu, mbar_wait(bar_empty + 8 * s, ((it / S::kStages) & 1) ^ 1, gave_up));
-            if (!ok) break;
-            if (elect_one()) {
-                const int k = (int)kb * p.k_elems;
-                const uint32_t sw = stages + s * S::kStageBytes, full = bar_full + 8 * s;
+        if (elect_one()) {
+            Ring<S::kStages> ring;
+            int k = (int)kb0 * p.k_elems;
+            const int k_elems = p.k_elems;
+            uint32_t issued = 0;
+            for (uint32_t kb = kb0; kb < kb1; ++kb, k += k_elems, ++issued) {
+                if (!mbar_wait(bar_empty + 8 * ring.s, ring.parity ^ 1, gave_up)) {
+                    volatile int still = 0;   // given up: let the copies in flight land
+                    for (int i = 0; i < S::kStages && (uint32_t)i < issued; ++i) {
+                        const uint32_t s = (ring.s + S::kStages - 1 - i) % S::kStages;
+                        mbar_wait(bar_full + 8 * s, s < ring.s ? ring.parity : ring.parity ^ 1, &still);
+                    }
+                    break;
+                }
+                const uint32_t sw = stages + ring.s * S::kStageBytes, full = bar_full + 8 * ring.s;
                 mbar_expect(full, S::kStageBytes);
                 if constexpr (GLU) {
                     tma_load_2d<false>(sw, &p.w[0], k, (int)n0, full);
                     tma_load_2d<false>(sw + S::kBytesW / 2, &p.w[1], k, (int)n0, full);
                 } else tma_load_2d<false>(sw, &p.w[0], k, (int)n0, full);
                 tma_load_2d<false>(sw + S::kBytesW, &p.x, k, (int)m0, full);
+                ring.next();
             }
-            __syncwarp();
-        }
-        if (!ok) {   // let the copies in flight land
-            volatile int still = 0;
-            for (uint32_t i = it > S::kStages ? it - S::kStages : 0; i < it; ++i)
-                mbar_wait(bar_full + 8 * (i % S::kStages), (i / S::kStages) & 1, &still);
         }
     } else if (warp == 1) {
-        const uint64_t desc_w = smem_desc(stages, true), desc_x = smem_desc(stages + S::kBytesW, true);
-        uint32_t it = 0;
-        for (uint32_t kb = kb0; kb < kb1; ++kb, ++it) {
-            const uint32_t s = it % S::kStages;
-            if (!__all_sync(0xffffffffu, mbar_wait(bar_full + 8 * s, (it / S::kStages) & 1, gave_up))) break;
-            tc_fence_after();
-            if (elect_one()) {
-                const uint64_t dw = desc_w + s * (S::kStageBytes >> 4), dx = desc_x + s * (S::kStageBytes >> 4);
+        if (elect_one()) {
+            const uint32_t lo_w = desc_lo(stages, true), lo_x = desc_lo(stages + S::kBytesW, true), idesc = p.idesc;
+            Ring<S::kStages> ring;
+            uint32_t add = 0;
+            for (uint32_t kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait(bar_full + 8 * ring.s, ring.parity, gave_up)) break;
+                tc_fence_after();
+                const uint32_t w = lo_w + ring.s * (S::kStageBytes >> 4), x = lo_x + ring.s * (S::kStageBytes >> 4);
 #pragma unroll
                 for (uint32_t i = 0; i < 4; ++i) {
-                    if (p.e4m3) mma<false, true>(tmem, dw + i * k_step(true), dx + i * k_step(true), p.idesc, kb > kb0 || i > 0);
-                    else mma<false, false>(tmem, dw + i * k_step(true), dx + i * k_step(true), p.idesc, kb > kb0 || i > 0);
+                    if (p.e4m3) mma<false, true>(tmem, w + i * k_step(true), kDescHi, x + i * k_step(true), kDescHi, idesc, add);
+                    else mma<false, false>(tmem, w + i * k_step(true), kDescHi, x + i * k_step(true), kDescHi, idesc, add);
+                    add = 1;
                 }
-                mma_commit<false>(bar_empty + 8 * s);
+                mma_commit<false>(bar_empty + 8 * ring.s);
+                ring.next();
             }
-            __syncwarp();
+            mma_commit<false>(bar_acc);   // every product so far, also after giving up
         }
-        if (elect_one()) mma_commit<false>(bar_acc);   // every product so far, also after giving up
     }
     __syncwarp();
     mbar_wait(bar_acc, 0, gave_up);
@@ -894,7 +920,7 @@ struct Tile {
 };
 // An SM takes in 64 bytes a cycle: 24, 32, 24 and 32 KB a k-block, against 128, 256,
 // 256 and 512 cycles of products.  So the wide pair alone keeps the tensor cores fed.
-constexpr Tile kTiles[4] = {{64, false, 480}, {128, false, 570}, {128, true, 430}, {256, true, 600}};
+constexpr Tile kTiles[4] = {{64, false, 400}, {128, false, 480}, {128, true, 420}, {256, true, 590}};
 
 // Cycles of a call with a tile shape: waves of tiles, each bound by its k-blocks or by
 // its epilogue's traffic (about 16 bytes a cycle and SM), and a start-up.

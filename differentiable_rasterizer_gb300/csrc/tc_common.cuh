@@ -81,16 +81,19 @@ constexpr long long kWaitCycles = 4000000000ll;
 
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up)
 {
-    if (mbar_try(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (!mbar_try(bar, parity)) {
+    long long t0 = 0;
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)   // nothing but the barrier between two tries
+            if (mbar_try(bar, parity)) return true;
+        const long long t = clock64();
+        if (t0 == 0) t0 = t;
         if (*gave_up) return false;
-        if (clock64() - t0 > kWaitCycles) {
+        if (t - t0 > kWaitCycles) {
             *gave_up = 1;
             return false;
         }
     }
-    return true;
 }
 
 // ------------------------------------------------------------------ TMA
@@ -145,15 +148,17 @@ __device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols)
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// D[tmem] (+)= A B^T, both factors in shared memory.  E4M3: 32 k a call, else 16.
+// D[tmem] (+)= A B^T, both factors in shared memory, their descriptors in halves (the
+// low one holds the address).  E4M3: 32 k a call, else 16.
 template <bool PAIR, bool E4M3>
-__device__ __forceinline__ void mma(uint32_t tmem, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+__device__ __forceinline__ void mma(uint32_t tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                    uint32_t add)
 {
-    const uint32_t p = add ? 1u : 0u;
-#define GS_MMA(GROUP, KIND)                                                                        \
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                                  \
-                 "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem), \
-                 "l"(a), "l"(b), "r"(idesc), "r"(p)                                                \
+#define GS_MMA(GROUP, KIND)                                                                                  \
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t" \
+                 "setp.ne.b32 p, %6, 0;\n\t"                                                                 \
+                 "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], a, b, %5, p;\n\t}" ::"r"(tmem),     \
+                 "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(add)                             \
                  : "memory")
     if constexpr (PAIR && E4M3) GS_MMA("2", "f8f6f4");
     else if constexpr (PAIR) GS_MMA("2", "f16");
@@ -201,14 +206,25 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[16])
 // Shared-memory descriptor of a factor's tile under the 128-byte swizzle (rows of
 // 128 bytes, eight rows a repeat): k fast -- a row is 128 bytes of one row's k, the
 // next eight rows 1024 bytes on; k slow -- a row is 64 of the factor's rows at one
-// k, eight k 1024 bytes on, the next 64 rows 64 k (8192 bytes) on.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, bool k_fast)
+// k, eight k 1024 bytes on, the next 64 rows 64 k (8192 bytes) on.  Low half: the
+// address and the leading offset, in units of 16 bytes; high half constant.
+__device__ __forceinline__ constexpr uint32_t desc_lo(uint32_t addr, bool k_fast)
 {
-    const uint64_t lead = k_fast ? 1 : 8192 >> 4;
-    return (uint64_t)((addr >> 4) & 0x3fff) | (lead << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+    return (addr >> 4) | ((k_fast ? 1u : 8192u >> 4) << 16);
 }
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 // Steps of one MMA (32 bytes of k, or 16 k) within the tile, in descriptor units.
-__device__ __forceinline__ uint32_t k_step(bool k_fast) { return k_fast ? 32 >> 4 : 2048 >> 4; }
+__host__ __device__ constexpr uint32_t k_step(bool k_fast) { return k_fast ? 32 >> 4 : 2048 >> 4; }
+
+// Position in a ring of N stages and the parity of its current round.
+template <int N>
+struct Ring {
+    uint32_t s = 0, parity = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++s == N) s = 0, parity ^= 1;
+    }
+};
 
 // Instruction descriptor: fp32 accumulator, both factors of `type`, slow-k flags, N, M.
 __host__ __device__ constexpr uint32_t instr_desc(int type, bool a_k_fast, bool b_k_fast, int n, int m)
