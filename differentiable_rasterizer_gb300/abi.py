@@ -331,8 +331,8 @@ _GLU = struct.Struct("=qqq Qq Qq Qq QQQ Qq Qq Qq iiii")
 _GLU_BWD = struct.Struct("=qqq Qq Qq Qq Qq Qq Qq Qq Qq Qq iiii")
 
 
-def _ws_call(name, packed, ws, ws_bytes, stream):
-    """ws_bytes None: a call that needs no scratch."""
+def layer_run(name, packed, ws, ws_bytes, stream):
+    """The named layer call; ws_bytes None: one that needs no scratch."""
     f = getattr(_lib or lib(), name)
     st = f(packed, ws, None if ws_bytes is None else ctypes.byref(ctypes.c_size_t(ws_bytes)), stream)
     if st != GS_OK:
@@ -402,23 +402,23 @@ def glu_bwd_args(rows, in_features, hidden, dh, lddh, x, ldx, w_gate, ldwg, w_up
 
 def gs_rms_norm_bwd(args: bytes, ws, ws_bytes, stream):
     """args: rms_norm_bwd_args(...); ws: device pointer of ws_bytes, or None and None where none is needed."""
-    _ws_call("gs_rms_norm_bwd", args, ws, ws_bytes, stream)
+    layer_run("gs_rms_norm_bwd", args, ws, ws_bytes, stream)
 
 
 def gs_linear(args: bytes, ws, ws_bytes, stream):
-    _ws_call("gs_linear", args, ws, ws_bytes, stream)
+    layer_run("gs_linear", args, ws, ws_bytes, stream)
 
 
 def gs_linear_bwd(args: bytes, ws, ws_bytes, stream):
-    _ws_call("gs_linear_bwd", args, ws, ws_bytes, stream)
+    layer_run("gs_linear_bwd", args, ws, ws_bytes, stream)
 
 
 def gs_glu(args: bytes, ws, ws_bytes, stream):
-    _ws_call("gs_glu", args, ws, ws_bytes, stream)
+    layer_run("gs_glu", args, ws, ws_bytes, stream)
 
 
 def gs_glu_bwd(args: bytes, ws, ws_bytes, stream):
-    _ws_call("gs_glu_bwd", args, ws, ws_bytes, stream)
+    layer_run("gs_glu_bwd", args, ws, ws_bytes, stream)
 
 
 def layer_ws_bytes(name: str, args: bytes) -> int:

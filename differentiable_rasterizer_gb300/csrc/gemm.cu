@@ -19,6 +19,7 @@
 // shared memory delivers, so wide problems use the pair: 256 x 256 over two SMs, each
 // holding half of B, half the shared-memory bytes a product.  With small k (a
 // Gaussian decoder's layers) HBM, through the epilogue's stores.
+#include <atomic>
 #include <type_traits>
 
 #include "gemm.cuh"
@@ -750,7 +751,17 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
     const uint32_t kb0 = (uint32_t)((uint64_t)p.k_blocks * rank / ranks),
                    kb1 = (uint32_t)((uint64_t)p.k_blocks * (rank + 1) / ranks);
 
-    if (threadIdx.x == 0) {
+    // One lane makes the barriers and starts the first copies before the block has met.
+    const uint32_t kb_first = kb1 - kb0 < S::kStages ? kb1 : kb0 + S::kStages;   // end of the ring's first round
+    const auto send = [&](uint32_t s, uint32_t kb) {
+        const int k = (int)kb * p.k_elems;
+        const uint32_t sw = stages + s * S::kStageBytes, full = bar_full + 8 * s;
+        mbar_expect(full, S::kStageBytes);
+        tma_load_2d<false>(sw, &p.w[0], k, (int)n0, full);
+        if constexpr (GLU) tma_load_2d<false>(sw + S::kBytesW / 2, &p.w[1], k, (int)n0, full);
+        tma_load_2d<false>(sw + S::kBytesW, &p.x, k, (int)m0, full);
+    };
+    if (warp == 0 && elect_one()) {
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(bar_full + 8 * i, 1);
             mbar_init(bar_empty + 8 * i, 1);
@@ -758,6 +769,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
         mbar_init(bar_acc, 1);
         *gave_up = 0;
         mbar_init_fence();
+        for (uint32_t kb = kb0; kb < kb_first; ++kb) send(kb - kb0, kb);
     }
     if (warp == 1) tmem_alloc<false>(smem_addr(tmem_slot), S::kTmemCols);
     tc_fence_before();
@@ -767,26 +779,15 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
 
     if (warp == 0) {
         if (elect_one()) {
-            Ring<S::kStages> ring;
-            int k = (int)kb0 * p.k_elems;
-            const int k_elems = p.k_elems;
-            uint32_t issued = 0;
-            for (uint32_t kb = kb0; kb < kb1; ++kb, k += k_elems, ++issued) {
-                if (!mbar_wait(bar_empty + 8 * ring.s, ring.parity ^ 1, gave_up)) {
+            Ring<S::kStages> ring;   // round 1 on: a stage is sent again once its products are done
+            for (uint32_t kb = kb_first; kb < kb1; ++kb) {
+                if (!mbar_wait(bar_empty + 8 * ring.s, ring.parity, gave_up)) {
                     volatile int still = 0;   // given up: let the copies in flight land
-                    for (int i = 0; i < S::kStages && (uint32_t)i < issued; ++i) {
-                        const uint32_t s = (ring.s + S::kStages - 1 - i) % S::kStages;
-                        mbar_wait(bar_full + 8 * s, s < ring.s ? ring.parity : ring.parity ^ 1, &still);
-                    }
+                    for (uint32_t s = 0; s < S::kStages; ++s)
+                        mbar_wait(bar_full + 8 * s, s < ring.s ? ring.parity ^ 1 : ring.parity, &still);
                     break;
                 }
-                const uint32_t sw = stages + ring.s * S::kStageBytes, full = bar_full + 8 * ring.s;
-                mbar_expect(full, S::kStageBytes);
-                if constexpr (GLU) {
-                    tma_load_2d<false>(sw, &p.w[0], k, (int)n0, full);
-                    tma_load_2d<false>(sw + S::kBytesW / 2, &p.w[1], k, (int)n0, full);
-                } else tma_load_2d<false>(sw, &p.w[0], k, (int)n0, full);
-                tma_load_2d<false>(sw + S::kBytesW, &p.x, k, (int)m0, full);
+                send(ring.s, kb);
                 ring.next();
             }
         }
@@ -834,35 +835,54 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
     }
     cluster_sync();
     const int rows = p.m - m0 < NB ? (int)(p.m - m0) : NB;
-    const int64_t left = p.n - n0;
+    const int left = p.n - n0 < kFeatures ? (int)(p.n - n0) : kFeatures;
     uint32_t peer[8];
 #pragma unroll
     for (uint32_t r = 0; r < 8; ++r) peer[r] = map_rank(stages, r < ranks ? r : 0);
-    for (int i = (int)(rank * kRowsThreads + threadIdx.x); i < rows * kFeatures; i += (int)(ranks * kRowsThreads)) {
-        const int r = i / kFeatures, f = i % kFeatures;
+    // four features of a row a thread
+    for (int i = (int)(rank * kRowsThreads + threadIdx.x); i < rows * (kFeatures / 4); i += (int)(ranks * kRowsThreads)) {
+        const int r = i / (kFeatures / 4), f = i % (kFeatures / 4) * 4;
         if (f >= left) continue;
-        const int64_t row = m0 + r, col = n0 + f;
-        float v = 0.0f, u = 0.0f;
+        const int64_t row = m0 + r;
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (uint32_t q = 0; q < 8; ++q) {
             if (q >= ranks) break;
-            v += ld_cluster_f32(peer[q] + (uint32_t)((r * 128 + f) * 4));
-            if constexpr (GLU) u += ld_cluster_f32(peer[q] + (uint32_t)((r * 128 + 64 + f) * 4));
+            const float4 a = ld_cluster_f32x4(peer[q] + (uint32_t)((r * 128 + f) * 4));
+            v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+            if constexpr (GLU) {
+                const float4 b = ld_cluster_f32x4(peer[q] + (uint32_t)((r * 128 + 64 + f) * 4));
+                u[0] += b.x, u[1] += b.y, u[2] += b.z, u[3] += b.w;
+            }
         }
         const float xs = p.x_scale ? p.x_scale[row] : 1.0f;
-        if (p.e4m3) {
-            v *= xs * (p.w_scale[0] ? p.w_scale[0][col] : 1.0f);
-            if constexpr (GLU) u *= xs * (p.w_scale[1] ? p.w_scale[1][col] : 1.0f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (f + e >= left) break;
+            const int64_t col = n0 + f + e;
+            float o = v[e];
+            if (p.e4m3) {
+                o *= xs * (p.w_scale[0] ? p.w_scale[0][col] : 1.0f);
+                if constexpr (GLU) u[e] *= xs * (p.w_scale[1] ? p.w_scale[1][col] : 1.0f);
+            }
+            if (!GLU && p.bias) o += load_elem(p.bias, col, p.bias_type);
+            if (p.z) {
+                store_elem(p.z, row * p.ldz + col, p.z_type, o);
+                if constexpr (GLU) store_elem(p.z2, row * p.ldz2 + col, p.z_type, u[e]);
+            }
+            o = act_value(o, p.act);
+            if constexpr (GLU) o *= u[e];
+            else if (p.residual) o += load_elem(p.residual, row * p.ldr + col, p.out_type);
+            v[e] = o;
         }
-        if (!GLU && p.bias) v += load_elem(p.bias, col, p.bias_type);
-        if (p.z) {
-            store_elem(p.z, row * p.ldz + col, p.z_type, v);
-            if constexpr (GLU) store_elem(p.z2, row * p.ldz2 + col, p.z_type, u);
-        }
-        v = act_value(v, p.act);
-        if constexpr (GLU) v *= u;
-        else if (p.residual) v += load_elem(p.residual, row * p.ldr + col, p.out_type);
-        store_elem(p.y, row * p.ldy + col, p.out_type, v);
+        const int64_t at = row * p.ldy + n0 + f;
+        if (f + 4 <= left && p.out_type != GS_F32 && ((uintptr_t)((uint16_t*)p.y + at) & 7u) == 0)
+            *reinterpret_cast<uint2*>((uint16_t*)p.y + at) =
+                make_uint2(pack_half2(v[0], v[1], p.out_type), pack_half2(v[2], v[3], p.out_type));
+        else
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (f + e < left) store_elem(p.y, at + e, p.out_type, v[e]);
     }
     if (threadIdx.x == 0 && *gave_up) atomicExch(&g_wait_expired, 1);
     tc_fence_before();
@@ -874,42 +894,51 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
 }
 
 // Rows of any alignment to rows of 16-byte pitch (the TMA needs both): eight
-// 2-byte or sixteen 1-byte elements a thread, one 16-byte store.
+// 2-byte or sixteen 1-byte elements a thread, one 16-byte store.  All factors of a
+// call in one launch.
+struct PackJobs {
+    struct {
+        const void* src;
+        uint4* dst;
+        int64_t ld, rows, cols, pieces;
+        unsigned first;   // block
+    } job[4];
+    int jobs;
+};
 template <typename E>
-__global__ void __launch_bounds__(256) pack_rows_kernel(const E* src, int64_t ld, int64_t rows, int64_t cols, uint4* dst,
-                                                        int64_t pieces)
+__global__ void __launch_bounds__(256) pack_rows_kernel(const PackJobs p)
 {
     constexpr int kPer = 16 / sizeof(E);
-    const int64_t total = rows * pieces, step = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += step) {
-        const int64_t r = i / pieces, c0 = i % pieces * kPer;
+    int j = 0;
+    while (j + 1 < p.jobs && blockIdx.x >= p.job[j + 1].first) ++j;
+    const unsigned end = j + 1 < p.jobs ? p.job[j + 1].first : gridDim.x;
+    const auto& q = p.job[j];
+    const E* src = (const E*)q.src;
+    const int64_t total = q.rows * q.pieces, step = (int64_t)(end - q.first) * blockDim.x;
+    for (int64_t i = (int64_t)(blockIdx.x - q.first) * blockDim.x + threadIdx.x; i < total; i += step) {
+        const int64_t r = i / q.pieces, c0 = i % q.pieces * kPer;
         union {
-            uint4 q;
+            uint4 v;
             E e[kPer];
         } v;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) v.e[j] = c0 + j < cols ? src[r * ld + c0 + j] : (E)0;
-        dst[i] = v.q;
+        for (int e = 0; e < kPer; ++e) v.e[e] = c0 + e < q.cols ? src[r * q.ld + c0 + e] : (E)0;
+        q.dst[i] = v.v;
     }
 }
 
 // ------------------------------------------------------------------ host
-struct Plan {
-    int nb, ranks;   // the few-rows kernel: rows of x a CTA takes (0: not used), CTAs that split k
-    bool pair;
-    int bn;
-    int64_t tile_m, out_cols, tiles_m, tiles_n, units, k_blocks;
-    int splits, terms, probs, k_elems, esz;
-    size_t pack_at[4], partial_at, bytes;   // a0, a1, b0, b1: offset + 1, 0 where used in place
-    int64_t pitch;                          // of the partial sums
-};
-
-int device_sms()
+// Sets a kernel's shared memory once on each device.
+template <class K>
+gs_status allow_smem(K* kernel, int bytes, std::atomic<uint64_t>& done)
 {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) return 152;
-    return sms;
+    int dev = 0;
+    GS_CUDA_TRY(cudaGetDevice(&dev));
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return GS_OK;
+    GS_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    if (dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+    return GS_OK;
 }
 
 // Tile shapes: B's columns and whether two SMs share a tile.
@@ -924,9 +953,9 @@ constexpr Tile kTiles[4] = {{64, false, 400}, {128, false, 480}, {128, true, 420
 
 // Cycles of a call with a tile shape: waves of tiles, each bound by its k-blocks or by
 // its epilogue's traffic (about 16 bytes a cycle and SM), and a start-up.
-double cost(const GemmCall& c, const Tile& t, int sms, Plan* out)
+double cost(const GemmCall& c, const Tile& t, int sms, GemmPlan* out)
 {
-    Plan& p = *out;
+    GemmPlan& p = *out;
     const bool glu = c.kind == GemmKind::kGlu;
     p.pair = t.pair;
     p.bn = t.bn;
@@ -947,7 +976,10 @@ double cost(const GemmCall& c, const Tile& t, int sms, Plan* out)
     const double live = (double)(c.n < p.out_cols ? c.n : p.out_cols);
     const int bytes = type_bytes(c.out_type) * (c.residual ? 2 : 1) + (c.z ? (glu ? 4 : 2) : 0);
     double best = 0;
-    for (int64_t s = 1; s == 1 || (sum_only && s * tiles <= slots && s * 4 <= kb); ++s) {
+    int64_t most = sum_only ? slots / tiles : 1;
+    if (most > kb / 4) most = kb / 4;
+    if (most < 1) most = 1;
+    for (int64_t s = 1; s <= most; s = s == most ? most + 1 : (s + s / 2 + 1 < most ? s + s / 2 + 1 : most)) {
         const double main = t.per_kb * (double)((kb + s - 1) / s);
         const double epi = 500 + 128.0 * live * (s > 1 ? 4 : bytes) / (t.bn == 256 ? 14 : 16);
         const double waves = (double)((tiles * s + slots - 1) / slots);
@@ -966,55 +998,15 @@ double cost(const GemmCall& c, const Tile& t, int sms, Plan* out)
 int64_t stored_rows(const GemmFactor& f, int64_t rows, int64_t k) { return f.k_fast ? rows : k; }
 int64_t stored_cols(const GemmFactor& f, int64_t rows, int64_t k) { return f.k_fast ? k : rows; }
 
-Plan make_plan(const GemmCall& c)
-{
-    const int sms = device_sms();
-    Plan best, p;
-    double at = 0;
-    const bool glu = c.kind == GemmKind::kGlu;
-    for (int i = glu ? 1 : 0; i < 4; ++i) {
-        const double v = cost(c, kTiles[i], sms, &p);
-        if (i == (glu ? 1 : 0) || v < at) {
-            at = v;
-            best = p;
-        }
-    }
-    p = best;
-    p.nb = 0;
-    if ((c.kind == GemmKind::kLinear || glu) && c.a[0].k_fast && c.b[0].k_fast && c.m <= kFewRows) {
-        p.nb = c.m <= 16 ? 16 : (c.m <= 32 ? 32 : 64);
-        const int64_t tiles = ((c.n + (glu ? 63 : 127)) / (glu ? 64 : 128)) * ((c.m + p.nb - 1) / p.nb);
-        p.ranks = 1;
-        while (p.ranks < 8 && tiles * p.ranks * 2 <= sms && p.k_blocks >= 2 * p.ranks) p.ranks *= 2;
-        p.splits = 1;
-    }
-    size_t used = 0;
-    const GemmFactor* f[4] = {&c.a[0], &c.a[1], &c.b[0], &c.b[1]};
-    for (int i = 0; i < 4; ++i) {
-        p.pack_at[i] = 0;
-        if (!f[i]->p || rows16(f[i]->p, f[i]->ld, c.type)) continue;
-        if (i & 1 && f[i]->p == f[i - 1]->p) {   // kTwo: both products read the same factor
-            p.pack_at[i] = p.pack_at[i - 1];
-            continue;
-        }
-        const int64_t rows = i < 2 ? c.m : c.n;
-        p.pack_at[i] = used + 1;
-        used += (size_t)round_up(stored_rows(*f[i], rows, c.k) * round_up(stored_cols(*f[i], rows, c.k) * p.esz, 16), 256);
-    }
-    p.partial_at = used;
-    p.pitch = round_up(c.n, 4);
-    if (p.splits > 1) used += (size_t)round_up((int64_t)p.splits * p.probs * c.m * p.pitch * 4, 256);
-    p.bytes = used;
-    return p;
-}
-
 template <int NB, bool GLU>
 gs_status launch_rows(const RowsParams& p, unsigned grid, int ranks, cudaStream_t st)
 {
     using S = RowsShape<NB, GLU>;
     static_assert(S::kSmem <= 232448, "shared memory of an SM");
     auto* kernel = rows_kernel<NB, GLU>;
-    GS_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem));
+    static std::atomic<uint64_t> done{0};
+    const gs_status s = allow_smem(kernel, S::kSmem, done);
+    if (s != GS_OK) return s;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kRowsThreads);
@@ -1036,7 +1028,9 @@ gs_status launch(const Params& p, int grid, cudaStream_t st)
     using S = Shape<BN, PAIR, GLU>;
     static_assert(S::kSmem <= 232448, "shared memory of an SM");
     auto* kernel = gemm_kernel<BN, PAIR, GLU, OSZ>;
-    GS_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem));
+    static std::atomic<uint64_t> done{0};
+    const gs_status s = allow_smem(kernel, S::kSmem, done);
+    if (s != GS_OK) return s;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kThreads);
@@ -1053,6 +1047,18 @@ gs_status launch(const Params& p, int grid, cudaStream_t st)
 }
 
 }  // namespace
+
+// Read once a device: the count does not change while a process runs.
+int device_sms()
+{
+    static std::atomic<int> known[64];
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
+    return sms;
+}
 
 namespace tc {
 
@@ -1089,35 +1095,77 @@ gs_status make_map(CUtensorMap* map, const void* p, int type, int64_t rows, int6
 
 }  // namespace tc
 
-gs_status gemm_ws_bytes(const GemmCall& c, size_t* bytes)
+GemmPlan gemm_plan(const GemmCall& c)
 {
-    *bytes = make_plan(c).bytes;
-    return GS_OK;
+    const int known = device_sms(), sms = known > 0 ? known : 152;
+    GemmPlan best, p;
+    double at = 0;
+    const bool glu = c.kind == GemmKind::kGlu;
+    for (int i = glu ? 1 : 0; i < 4; ++i) {
+        const double v = cost(c, kTiles[i], sms, &p);
+        if (i == (glu ? 1 : 0) || v < at) {
+            at = v;
+            best = p;
+        }
+    }
+    p = best;
+    p.sms = sms;
+    p.nb = 0;
+    if ((c.kind == GemmKind::kLinear || glu) && c.a[0].k_fast && c.b[0].k_fast && c.m <= kFewRows) {
+        p.nb = c.m <= 16 ? 16 : (c.m <= 32 ? 32 : 64);
+        const int64_t tiles = ((c.n + (glu ? 63 : 127)) / (glu ? 64 : 128)) * ((c.m + p.nb - 1) / p.nb);
+        p.ranks = 1;
+        while (p.ranks < 8 && tiles * p.ranks * 2 <= sms && p.k_blocks >= 2 * p.ranks) p.ranks *= 2;
+        p.splits = 1;
+    }
+    size_t used = 0;
+    const GemmFactor* f[4] = {&c.a[0], &c.a[1], &c.b[0], &c.b[1]};
+    for (int i = 0; i < 4; ++i) {
+        p.pack_at[i] = 0;
+        if (!f[i]->p || rows16(f[i]->p, f[i]->ld, c.type)) continue;
+        if (i & 1 && f[i]->p == f[i - 1]->p) {   // kTwo: both products read the same factor
+            p.pack_at[i] = p.pack_at[i - 1];
+            continue;
+        }
+        const int64_t rows = i < 2 ? c.m : c.n;
+        p.pack_at[i] = used + 1;
+        used += (size_t)round_up(stored_rows(*f[i], rows, c.k) * round_up(stored_cols(*f[i], rows, c.k) * p.esz, 16), 256);
+    }
+    p.partial_at = used;
+    p.pitch = round_up(c.n, 4);
+    if (p.splits > 1) used += (size_t)round_up((int64_t)p.splits * p.probs * c.m * p.pitch * 4, 256);
+    p.bytes = used;
+    return p;
 }
 
-gs_status gemm_run(const GemmCall& c, void* ws, cudaStream_t st)
+gs_status gemm_run(const GemmCall& c, const GemmPlan& plan, void* ws, cudaStream_t st)
 {
-    const Plan plan = make_plan(c);
     if (plan.units > 0x7fffffffll || c.m > 0x7fffff00ll || c.n > 0x7fffff00ll || c.k > 0x7fffff00ll)
         return GS_ERR_INVALID_ARG;
     char* base = (char*)ws;
     GemmFactor f[4] = {c.a[0], c.a[1], c.b[0], c.b[1]};
+    PackJobs pack = {};
+    unsigned blocks = 0;
     for (int i = 0; i < 4; ++i) {
         if (!plan.pack_at[i]) continue;
         const int64_t rows = stored_rows(f[i], i < 2 ? c.m : c.n, c.k), cols = stored_cols(f[i], i < 2 ? c.m : c.n, c.k);
         const int64_t pieces = round_up(cols * plan.esz, 16) / 16;
         uint4* dst = (uint4*)(base + plan.pack_at[i] - 1);
         if (!(i & 1 && plan.pack_at[i] == plan.pack_at[i - 1])) {
-            const int64_t blocks = (rows * pieces + 255) / 256;
-            const unsigned grid = (unsigned)(blocks < 152 * 16 ? blocks : 152 * 16);
-            if (plan.esz == 2)
-                pack_rows_kernel<uint16_t><<<grid, 256, 0, st>>>((const uint16_t*)f[i].p, f[i].ld, rows, cols, dst, pieces);
-            else
-                pack_rows_kernel<uint8_t><<<grid, 256, 0, st>>>((const uint8_t*)f[i].p, f[i].ld, rows, cols, dst, pieces);
-            GS_LAUNCH_CHECK();
+            const int64_t want = (rows * pieces + 255) / 256, most = 16ll * plan.sms;
+            auto& job = pack.job[pack.jobs++];
+            job.src = f[i].p, job.dst = dst;
+            job.ld = f[i].ld, job.rows = rows, job.cols = cols, job.pieces = pieces;
+            job.first = blocks;
+            blocks += (unsigned)(want < most ? want : most);
         }
         f[i].p = dst;
         f[i].ld = pieces * 16 / plan.esz;
+    }
+    if (blocks) {
+        if (plan.esz == 2) pack_rows_kernel<uint16_t><<<blocks, 256, 0, st>>>(pack);
+        else pack_rows_kernel<uint8_t><<<blocks, 256, 0, st>>>(pack);
+        GS_LAUNCH_CHECK();
     }
 
     const bool glu = c.kind == GemmKind::kGlu;
@@ -1192,8 +1240,7 @@ gs_status gemm_run(const GemmCall& c, void* ws, cudaStream_t st)
     p.a_fast = c.a[0].k_fast, p.b_fast = c.b[0].k_fast;
     p.e4m3 = c.type == GS_E4M3;
     p.idesc = tc::instr_desc(c.type, c.a[0].k_fast, c.b[0].k_fast, plan.bn, (int)plan.tile_m);
-    const int sms = device_sms();
-    const int64_t most = plan.pair ? sms / 2 : sms;
+    const int64_t most = plan.pair ? plan.sms / 2 : plan.sms;
     const int grid = (int)(plan.units < most ? plan.units : most) * (plan.pair ? 2 : 1);
     gs_status s;
     const auto pick = [&](auto osz) {

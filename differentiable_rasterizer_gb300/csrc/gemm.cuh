@@ -42,9 +42,22 @@ struct GemmCall {
     int out_type, z_type, act;
 };
 
-// Scratch that a call needs; it depends on sizes, types, presence and alignment.
-gs_status gemm_ws_bytes(const GemmCall& c, size_t* bytes);
-gs_status gemm_run(const GemmCall& c, void* ws, cudaStream_t st);
+// How a call runs: kernel, tile shape, splits of k, and where the workspace's parts lie.
+// It depends on sizes, types, presence and alignment (of the pointers, not their values).
+struct GemmPlan {
+    int nb, ranks;   // the few-rows kernel: rows of x a CTA takes (0: not used), CTAs that split k
+    bool pair;
+    int bn, sms;
+    int64_t tile_m, out_cols, tiles_m, tiles_n, units, k_blocks;
+    int splits, terms, probs, k_elems, esz;
+    size_t pack_at[4], partial_at, bytes;   // a0, a1, b0, b1: offset + 1, 0 where used in place; scratch in all
+    int64_t pitch;                          // of the partial sums
+};
+GemmPlan gemm_plan(const GemmCall& c);
+gs_status gemm_run(const GemmCall& c, const GemmPlan& plan, void* ws, cudaStream_t st);
+
+// Multiprocessors of the current device (0 if there is none).
+int device_sms();
 
 // out[r * ld + c] = sum over parts, in order, of partial[part][r][c] (rows of `pitch`).
 gs_status join_partials(const float* partial, int64_t parts, int64_t rows, int64_t cols, int64_t pitch, void* out,

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kElemThreads) glu_grad_kernel(const GluGradPar
 // Sums of partial rows, in the order of the parts.  A thread takes VEC columns of one
 // row; with SLICES > 1 it takes every SLICES-th part, and the block adds the slices in
 // order.  Few parts of a large result: SLICES 1, one pass at the reads' bandwidth; many
-// parts of a small one (a decoder's weights over a million rows): SLICES 8.
+// parts of a small one (a decoder's weights over a million rows): SLICES 8 or 32.
 template <int VEC, int SLICES>
 __global__ void __launch_bounds__(256) join_partials_kernel(const float* partial, int parts, int64_t count, uint32_t rows,
                                                             uint32_t cols, uint32_t pitch, void* out, int64_t ld, int type)
@@ -237,16 +237,24 @@ gs_status join_partials(const float* partial, int64_t parts, int64_t rows, int64
 {
     const bool vec = pitch % 4 == 0 && aligned16(partial);
     const int64_t threads = rows * (vec ? (cols + 3) / 4 : cols), count = rows * pitch;
-    const bool sliced = threads < 152 * 512;   // too few threads to fill the SMs, one a result
-    const int64_t wide = sliced ? 32 : 256, blocks = (threads + wide - 1) / wide;
+    // one thread a result where they fill the SMs; else 8, or 32 for vectors' worth of results
+    const int slices = threads >= 152 * 512 || parts < 8 ? 1 : (threads >= 152 * 32 || parts < 32 ? 8 : 32);
+    const int64_t wide = 256 / slices, blocks = (threads + wide - 1) / wide;
     if (blocks > 0x7fffffll || threads > 0x7fffffffll) return GS_ERR_INVALID_ARG;
     const unsigned grid = (unsigned)blocks;
     const uint32_t r = (uint32_t)rows, c = (uint32_t)cols, q = (uint32_t)pitch;
     const int n = (int)parts;
-    if (vec && sliced) join_partials_kernel<4, 8><<<grid, 256, 0, st>>>(partial, n, count, r, c, q, out, ld, type);
-    else if (vec) join_partials_kernel<4, 1><<<grid, 256, 0, st>>>(partial, n, count, r, c, q, out, ld, type);
-    else if (sliced) join_partials_kernel<1, 8><<<grid, 256, 0, st>>>(partial, n, count, r, c, q, out, ld, type);
-    else join_partials_kernel<1, 1><<<grid, 256, 0, st>>>(partial, n, count, r, c, q, out, ld, type);
+    const auto run = [&](auto v, auto sl) {
+        join_partials_kernel<decltype(v)::value, decltype(sl)::value><<<grid, 256, 0, st>>>(partial, n, count, r, c, q, out,
+                                                                                          ld, type);
+    };
+    const auto pick = [&](auto v) {
+        if (slices == 1) run(v, std::integral_constant<int, 1>());
+        else if (slices == 8) run(v, std::integral_constant<int, 8>());
+        else run(v, std::integral_constant<int, 32>());
+    };
+    if (vec) pick(std::integral_constant<int, 4>());
+    else pick(std::integral_constant<int, 1>());
     GS_LAUNCH_CHECK();
     return GS_OK;
 }
@@ -281,13 +289,12 @@ extern "C" gs_status gs_linear(const gs_linear_args* args, void* ws, size_t* ws_
     c.residual = a.residual, c.ldr = a.ldr;
     c.y = a.y, c.ldy = a.ldy, c.out_type = a.out_type;
     c.z = a.z, c.ldz = a.ldz, c.z_type = a.type;
-    size_t need = 0;
-    gs_status s = a.rows > 0 ? gemm_ws_bytes(c, &need) : GS_OK;
-    if (s != GS_OK) return s;
-    const WsCheck wc = ws_check(ws, ws_bytes, need);
+    GemmPlan plan = {};
+    if (a.rows > 0) plan = gemm_plan(c);
+    const WsCheck wc = ws_check(ws, ws_bytes, plan.bytes);
     if (wc == WsCheck::kBad) return GS_ERR_INVALID_ARG;
     if (wc == WsCheck::kQuery || a.rows == 0) return GS_OK;
-    return gemm_run(c, ws, (cudaStream_t)stream);
+    return gemm_run(c, plan, ws, (cudaStream_t)stream);
 }
 
 extern "C" gs_status gs_linear_bwd(const gs_linear_bwd_args* args, void* ws, size_t* ws_bytes, void* stream)
@@ -326,10 +333,10 @@ extern "C" gs_status gs_linear_bwd(const gs_linear_bwd_args* args, void* ws, siz
     cw.m = n, cw.n = k, cw.k = m;
     cw.a[0] = {dz_k.p, dz_k.ld, false}, cw.b[0] = {a.x, a.ldx, false};
     cw.y = a.dw, cw.ldy = a.lddw, cw.out_type = a.dw_type;
-    size_t need_x = 0, need_w = 0;
-    if (m > 0 && a.dx && gemm_ws_bytes(cx, &need_x) != GS_OK) return GS_ERR_INVALID_ARG;
-    if (m > 0 && a.dw && gemm_ws_bytes(cw, &need_w) != GS_OK) return GS_ERR_INVALID_ARG;
-    const size_t at_gemm = sc.take(need_x > need_w ? need_x : need_w);   // one after the other
+    GemmPlan px = {}, pw = {};
+    if (m > 0 && a.dx) px = gemm_plan(cx);
+    if (m > 0 && a.dw) pw = gemm_plan(cw);
+    const size_t at_gemm = sc.take(px.bytes > pw.bytes ? px.bytes : pw.bytes);   // one after the other
     const WsCheck wc = ws_check(ws, ws_bytes, sc.used);
     if (wc == WsCheck::kBad) return GS_ERR_INVALID_ARG;
     if (wc == WsCheck::kQuery) return GS_OK;
@@ -367,10 +374,10 @@ extern "C" gs_status gs_linear_bwd(const gs_linear_bwd_args* args, void* ws, siz
         if (make_dz) cx.a[0].p = cw.a[0].p = base + at_dz;
     }
     if (a.dx) {
-        const gs_status s = gemm_run(cx, base + at_gemm, st);
+        const gs_status s = gemm_run(cx, px, base + at_gemm, st);
         if (s != GS_OK) return s;
     }
-    if (a.dw) return gemm_run(cw, base + at_gemm, st);
+    if (a.dw) return gemm_run(cw, pw, base + at_gemm, st);
     return GS_OK;
 }
 
@@ -402,13 +409,12 @@ extern "C" gs_status gs_glu(const gs_glu_args* args, void* ws, size_t* ws_bytes,
     c.act = a.act;
     c.y = a.h, c.ldy = a.ldh, c.out_type = c.z_type = a.out_type;
     c.z = a.g, c.ldz = a.ldg, c.z2 = a.u, c.ldz2 = a.ldu;
-    size_t need = 0;
-    gs_status s = a.rows > 0 ? gemm_ws_bytes(c, &need) : GS_OK;
-    if (s != GS_OK) return s;
-    const WsCheck wc = ws_check(ws, ws_bytes, need);
+    GemmPlan plan = {};
+    if (a.rows > 0) plan = gemm_plan(c);
+    const WsCheck wc = ws_check(ws, ws_bytes, plan.bytes);
     if (wc == WsCheck::kBad) return GS_ERR_INVALID_ARG;
     if (wc == WsCheck::kQuery || a.rows == 0) return GS_OK;
-    return gemm_run(c, ws, (cudaStream_t)stream);
+    return gemm_run(c, plan, ws, (cudaStream_t)stream);
 }
 
 extern "C" gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* ws_bytes, void* stream)
@@ -445,10 +451,10 @@ extern "C" gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* w
     cw.a[0] = cw.a[1] = {aligned, ldd, false};
     cw.b[0] = cw.b[1] = {a.x, a.ldx, false};
     cw.y = a.dw_gate, cw.ldy = a.lddwg, cw.y2 = a.dw_up, cw.ldy2 = a.lddwu, cw.out_type = a.dw_type;
-    size_t need_x = 0, need_w = 0;
-    if (m > 0 && a.dx && gemm_ws_bytes(cx, &need_x) != GS_OK) return GS_ERR_INVALID_ARG;
-    if (m > 0 && a.dw_gate && gemm_ws_bytes(cw, &need_w) != GS_OK) return GS_ERR_INVALID_ARG;
-    const size_t at_gemm = sc.take(need_x > need_w ? need_x : need_w);
+    GemmPlan px = {}, pw = {};
+    if (m > 0 && a.dx) px = gemm_plan(cx);
+    if (m > 0 && a.dw_gate) pw = gemm_plan(cw);
+    const size_t at_gemm = sc.take(px.bytes > pw.bytes ? px.bytes : pw.bytes);
     const WsCheck wc = ws_check(ws, ws_bytes, sc.used);
     if (wc == WsCheck::kBad) return GS_ERR_INVALID_ARG;
     if (wc == WsCheck::kQuery) return GS_OK;
@@ -480,9 +486,9 @@ extern "C" gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* w
     cx.a[0].p = cw.a[0].p = p.dg;
     cx.a[1].p = cw.a[1].p = p.du;
     if (a.dx) {
-        const gs_status s = gemm_run(cx, base + at_gemm, st);
+        const gs_status s = gemm_run(cx, px, base + at_gemm, st);
         if (s != GS_OK) return s;
     }
-    if (a.dw_gate) return gemm_run(cw, base + at_gemm, st);
+    if (a.dw_gate) return gemm_run(cw, pw, base + at_gemm, st);
     return GS_OK;
 }

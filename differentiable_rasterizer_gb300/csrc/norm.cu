@@ -286,14 +286,6 @@ Shape shape_for(int64_t cols, int vec)
     return s;
 }
 
-int sm_count()
-{
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    return sms;
-}
-
 template <bool NORM>
 gs_status run_fwd(const gs_rms_norm_args& a, cudaStream_t st)
 {
@@ -302,7 +294,7 @@ gs_status run_fwd(const gs_rms_norm_args& a, cudaStream_t st)
                      (!NORM || aligned16(a.weight)) &&
                      (a.y_type == GS_E4M3 ? ((uintptr_t)a.y & 7u) == 0 && a.ldy % 8 == 0 : rows16(a.y, a.ldy, a.y_type));
     const Shape s = shape_for(a.cols, vec ? 8 : 1);
-    const int sms = sm_count();
+    const int sms = device_sms();
     if (sms <= 0) return GS_ERR_CUDA;
     // four rows a group where a group is within a warp, holds one vector a lane and
     // there are rows enough to fill the SMs all the same
@@ -377,7 +369,7 @@ extern "C" gs_status gs_rms_norm_bwd(const gs_rms_norm_bwd_args* args, void* ws,
     const gs_rms_norm_bwd_args& a = *args;
     if (!size_ok(a.rows, 0) || !size_ok(a.cols, 1) || a.cols > GS_NORM_MAX_COLS) return GS_ERR_INVALID_ARG;
     if (!type_float(a.type) || !type_float(a.dy_type) || !type_float(a.weight_type)) return GS_ERR_INVALID_ARG;
-    const int sms = sm_count();
+    const int sms = device_sms();
     // one partial row per block; the size is the same whatever the alignment of the arrays
     const int64_t blocks = 3 * (sms > 0 ? sms : 152);
     const size_t need = a.dweight ? (size_t)round_up(blocks * a.cols * 4, 256) : 0;

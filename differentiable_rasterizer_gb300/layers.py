@@ -151,18 +151,21 @@ def _run(f, dev, *args):
             f(*args, _stream(dev))
 
 
-def _call(name, args, like, dev):
-    """A layer call with the scratch that it asks for, on the current stream."""
+def _call(name, args, like, dev, try_first=False):
+    """A layer call with the scratch that it asks for, on the current stream; try_first: it
+    mostly needs none."""
     if dev != _current_device():
         with torch.cuda.device(dev):
-            return _call(name, args, like, dev)
+            return _call(name, args, like, dev, try_first)
     stream = _stream(dev)
-    if not abi.layer_call(name, args, stream):
-        n = abi.layer_ws_bytes(name, args)
-        if n == 0:
-            raise abi.GsError(name, abi.GS_ERR_INVALID_ARG)
+    if try_first and abi.layer_call(name, args, stream):
+        return
+    n = abi.layer_ws_bytes(name, args)
+    if n:
         ws = torch.empty(n, dtype=torch.uint8, device=like.device)
-        getattr(abi, name)(args, ws.data_ptr(), n, stream)
+        abi.layer_run(name, args, ws.data_ptr(), n, stream)
+    else:
+        abi.layer_run(name, args, None, None, stream)
 
 
 # ------------------------------------------------------------------ norm
@@ -272,7 +275,7 @@ def linear(x, w, bias=None, *, x_scale=None, w_scale=None, act=None, residual=No
         z, pz, ldz = _output(x, lead, n, x.dtype)
     _call("gs_linear", abi.linear_args(rows, k, n, px, ldx, pw, ldw, pxs, pws, pb, pr, ldr, py, ldy, pz, ldz,
                                        _TYPES[x.dtype], _TYPES[bias.dtype] if bias is not None else 0,
-                                       _TYPES[out_dtype], code), x, dev)
+                                       _TYPES[out_dtype], code), x, dev, True)
     return LinearOut(y, z)
 
 
@@ -341,7 +344,7 @@ def glu(x, w_gate, w_up, *, x_scale=None, gate_scale=None, up_scale=None, act="s
         g, pg, ldg = _output(x, lead, f, out_dtype)
         u, pu, ldu = _output(x, lead, f, out_dtype)
     _call("gs_glu", abi.glu_args(rows, k, f, px, ldx, pg_, ldwg, pu_, ldwu, pxs, pgs, pus, ph, ldh, pg, ldg, pu, ldu,
-                                 _TYPES[x.dtype], _TYPES[out_dtype], _act(act)), x, dev)
+                                 _TYPES[x.dtype], _TYPES[out_dtype], _act(act)), x, dev, True)
     return GluOut(h, g, u)
 
 
