@@ -455,9 +455,57 @@ __device__ __forceinline__ void issue_products(const Params& p, uint32_t first, 
     }
 }
 
+// A thread's row of dh: kC columns from `base`, 16 bits.
+template <int C>
+__device__ __forceinline__ void load_row_half(uint32_t (&w)[C / 2], const uint16_t* base, int cols, bool vec)
+{
+    if (vec) {
+#pragma unroll
+        for (int j = 0; j < C / 8; ++j) {
+            uint4 q = make_uint4(0, 0, 0, 0);
+            if (8 * j + 8 <= cols) q = *reinterpret_cast<const uint4*>(base + 8 * j);
+            else {
+                uint32_t t[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int e = 0; e < 7; ++e)
+                    if (8 * j + e < cols) t[e >> 1] |= (uint32_t)base[8 * j + e] << (16 * (e & 1));
+                q = make_uint4(t[0], t[1], t[2], t[3]);
+            }
+            w[4 * j] = q.x, w[4 * j + 1] = q.y, w[4 * j + 2] = q.z, w[4 * j + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < C / 2; ++j) w[j] = 0;
+#pragma unroll
+        for (int e = 0; e < C; ++e)
+            if (e < cols) w[e >> 1] |= (uint32_t)base[e] << (16 * (e & 1));
+    }
+}
+
+// 16 columns of the gated layer's gradient: dg = dh u act'(g), du = dh act(g).
+template <int ACT>
+__device__ __forceinline__ void glu_gradient(float (&g)[16], float (&u)[16], const float (&dh)[16])
+{
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        float value, slope;
+        act_both(g[j], ACT, value, slope);
+        g[j] = dh[j] * u[j] * slope;
+        u[j] = dh[j] * value;
+    }
+}
+__device__ __forceinline__ void glu_gradient(float (&g)[16], float (&u)[16], const float (&dh)[16], int act)
+{
+    if (act == GS_ACT_SILU) glu_gradient<GS_ACT_SILU>(g, u, dh);
+    else if (act == GS_ACT_GELU) glu_gradient<GS_ACT_GELU>(g, u, dh);
+    else if (act == GS_ACT_RELU) glu_gradient<GS_ACT_RELU>(g, u, dh);
+    else glu_gradient<GS_ACT_NONE>(g, u, dh);
+}
+
 // GLU: B's rows are half gate, half up; the epilogue joins column c with c + BN/2.
+// GRAD: it takes dh where a residual would be and gives dg and du.
 // OSZ: bytes of an output element.
-template <int BN, bool PAIR, bool GLU, int OSZ>
+template <int BN, bool PAIR, bool GLU, int OSZ, bool GRAD = false>
 __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ Params p)
 {
     using S = Shape<BN, PAIR, GLU>;
@@ -627,7 +675,55 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 }
             };
 
-            for (int pass = 0; live && pass < passes; ++pass) {
+            if constexpr (GRAD) {   // a slot's row: dg, then du, of a quarter of its bytes' columns
+                constexpr int kCols = S::kSlotRow / 4, kHalf = S::kSlotRow / 32;   // pieces of dg
+                const uint16_t* from = (const uint16_t*)p.residual + (int64_t)(row0 + lane) * p.ldr + col0;
+                const int j = lane % (2 * kHalf);
+                // lanes whose piece is du's see its rows kHalf pieces to the left
+                uint16_t* to = (uint16_t*)p.yp[j < kHalf ? 0 : 1] + (int64_t)row0 * p.ldy[0] + col0 - (j < kHalf ? 0 : 8 * kHalf);
+#pragma unroll 1
+                for (int c = 0; c < kGroupCols && c < cols; c += kCols, to += kCols, from += kCols) {
+                    const int part = cols - c < kCols ? cols - c : kCols;
+                    uint32_t dh[kCols / 2];
+                    load_row_half<kCols>(dh, from, lane < rows ? part : 0, p.r_vec);
+                    __syncwarp();   // the slot's last readers are done
+#pragma unroll
+                    for (int s = 0; s < kCols / 16; ++s) {
+                        uint32_t raw[16], up[16];
+                        tmem_ld16(d + c + 16 * s, raw);
+                        tmem_ld16(d + c + 16 * s + BN / 2, up);
+                        float g[16], u[16], v[16];
+                        if (p.out_type == GS_BF16) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float2 f = unpack_half2(dh[8 * s + e], GS_BF16);
+                                v[2 * e] = f.x, v[2 * e + 1] = f.y;
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float2 f = unpack_half2(dh[8 * s + e], GS_F16);
+                                v[2 * e] = f.x, v[2 * e + 1] = f.y;
+                            }
+                        }
+                        tmem_ld_wait(raw);
+                        tmem_ld_wait(up);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) g[e] = __uint_as_float(raw[e]), u[e] = __uint_as_float(up[e]);
+                        glu_gradient(g, u, v, p.act);
+                        if (p.out_type == GS_BF16) {
+                            slot_put_half<GS_BF16>(mine, s, g);
+                            slot_put_half<GS_BF16>(mine ^ (kHalf << 4), s, u);
+                        } else {
+                            slot_put_half<GS_F16>(mine, s, g);
+                            slot_put_half<GS_F16>(mine ^ (kHalf << 4), s, u);
+                        }
+                    }
+                    __syncwarp();
+                    store_half<S::kSlotRow>(slot, to, p.ldy[0], rows, j < kHalf ? part : part + 8 * kHalf, true, lane);
+                }
+            }
+            for (int pass = 0; !GRAD && live && pass < passes; ++pass) {
                 const bool last = pass == passes - 1;
                 if (GLU || !last || (OSZ == 2 && !p.residual)) {   // in 16 bits
                     constexpr int kCols = S::kSlotRow / 2;
@@ -839,15 +935,21 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
     uint32_t peer[8];
 #pragma unroll
     for (uint32_t r = 0; r < 8; ++r) peer[r] = map_rank(stages, r < ranks ? r : 0);
-    // four features of a row a thread
-    for (int i = (int)(rank * kRowsThreads + threadIdx.x); i < rows * (kFeatures / 4); i += (int)(ranks * kRowsThreads)) {
-        const int r = i / (kFeatures / 4), f = i % (kFeatures / 4) * 4;
+    // four features of a row a thread, or one where that gives every thread at most one
+    const int width = rows * kFeatures <= (int)(ranks * kRowsThreads) ? 1 : 4;
+    for (int i = (int)(rank * kRowsThreads + threadIdx.x); i < rows * (kFeatures / width); i += (int)(ranks * kRowsThreads)) {
+        const int r = i / (kFeatures / width), f = i % (kFeatures / width) * width;
         if (f >= left) continue;
         const int64_t row = m0 + r;
         float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (uint32_t q = 0; q < 8; ++q) {
             if (q >= ranks) break;
+            if (width == 1) {
+                v[0] += ld_cluster_f32(peer[q] + (uint32_t)((r * 128 + f) * 4));
+                if constexpr (GLU) u[0] += ld_cluster_f32(peer[q] + (uint32_t)((r * 128 + 64 + f) * 4));
+                continue;
+            }
             const float4 a = ld_cluster_f32x4(peer[q] + (uint32_t)((r * 128 + f) * 4));
             v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
             if constexpr (GLU) {
@@ -858,7 +960,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
         const float xs = p.x_scale ? p.x_scale[row] : 1.0f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            if (f + e >= left) break;
+            if (e >= width || f + e >= left) break;
             const int64_t col = n0 + f + e;
             float o = v[e];
             if (p.e4m3) {
@@ -876,13 +978,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
             v[e] = o;
         }
         const int64_t at = row * p.ldy + n0 + f;
-        if (f + 4 <= left && p.out_type != GS_F32 && ((uintptr_t)((uint16_t*)p.y + at) & 7u) == 0)
+        if (width == 4 && f + 4 <= left && p.out_type != GS_F32 && ((uintptr_t)((uint16_t*)p.y + at) & 7u) == 0)
             *reinterpret_cast<uint2*>((uint16_t*)p.y + at) =
                 make_uint2(pack_half2(v[0], v[1], p.out_type), pack_half2(v[2], v[3], p.out_type));
         else
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (f + e < left) store_elem(p.y, at + e, p.out_type, v[e]);
+                if (e < width && f + e < left) store_elem(p.y, at + e, p.out_type, v[e]);
     }
     if (threadIdx.x == 0 && *gave_up) atomicExch(&g_wait_expired, 1);
     tc_fence_before();
@@ -956,7 +1058,7 @@ constexpr Tile kTiles[4] = {{64, false, 400}, {128, false, 480}, {128, true, 420
 double cost(const GemmCall& c, const Tile& t, int sms, GemmPlan* out)
 {
     GemmPlan& p = *out;
-    const bool glu = c.kind == GemmKind::kGlu;
+    const bool glu = c.kind == GemmKind::kGlu || c.kind == GemmKind::kGluGrad;
     p.pair = t.pair;
     p.bn = t.bn;
     p.tile_m = t.pair ? 256 : 128;
@@ -971,7 +1073,7 @@ double cost(const GemmCall& c, const Tile& t, int sms, GemmPlan* out)
     const int64_t tiles = p.tiles_m * p.tiles_n * p.probs, slots = t.pair ? sms / 2 : sms, kb = p.k_blocks * p.terms;
     // Few tiles: split k over the idle SMs, at least four k-blocks each, where nothing
     // but the sum is asked for (the gradients): the partial sums are joined in order.
-    const bool sum_only = c.kind != GemmKind::kGlu && !c.bias && !c.residual && !c.z && c.act == GS_ACT_NONE &&
+    const bool sum_only = !glu && !c.bias && !c.residual && !c.z && c.act == GS_ACT_NONE &&
                           !c.x_scale && !c.w_scale[0];
     const double live = (double)(c.n < p.out_cols ? c.n : p.out_cols);
     const int bytes = type_bytes(c.out_type) * (c.residual ? 2 : 1) + (c.z ? (glu ? 4 : 2) : 0);
@@ -1022,12 +1124,12 @@ gs_status launch_rows(const RowsParams& p, unsigned grid, int ranks, cudaStream_
     return GS_OK;
 }
 
-template <int BN, bool PAIR, bool GLU, int OSZ>
+template <int BN, bool PAIR, bool GLU, int OSZ, bool GRAD = false>
 gs_status launch(const Params& p, int grid, cudaStream_t st)
 {
     using S = Shape<BN, PAIR, GLU>;
     static_assert(S::kSmem <= 232448, "shared memory of an SM");
-    auto* kernel = gemm_kernel<BN, PAIR, GLU, OSZ>;
+    auto* kernel = gemm_kernel<BN, PAIR, GLU, OSZ, GRAD>;
     static std::atomic<uint64_t> done{0};
     const gs_status s = allow_smem(kernel, S::kSmem, done);
     if (s != GS_OK) return s;
@@ -1100,7 +1202,7 @@ GemmPlan gemm_plan(const GemmCall& c)
     const int known = device_sms(), sms = known > 0 ? known : 152;
     GemmPlan best, p;
     double at = 0;
-    const bool glu = c.kind == GemmKind::kGlu;
+    const bool glu = c.kind == GemmKind::kGlu || c.kind == GemmKind::kGluGrad;
     for (int i = glu ? 1 : 0; i < 4; ++i) {
         const double v = cost(c, kTiles[i], sms, &p);
         if (i == (glu ? 1 : 0) || v < at) {
@@ -1111,7 +1213,7 @@ GemmPlan gemm_plan(const GemmCall& c)
     p = best;
     p.sms = sms;
     p.nb = 0;
-    if ((c.kind == GemmKind::kLinear || glu) && c.a[0].k_fast && c.b[0].k_fast && c.m <= kFewRows) {
+    if ((c.kind == GemmKind::kLinear || c.kind == GemmKind::kGlu) && c.a[0].k_fast && c.b[0].k_fast && c.m <= kFewRows) {
         p.nb = c.m <= 16 ? 16 : (c.m <= 32 ? 32 : 64);
         const int64_t tiles = ((c.n + (glu ? 63 : 127)) / (glu ? 64 : 128)) * ((c.m + p.nb - 1) / p.nb);
         p.ranks = 1;
@@ -1168,7 +1270,7 @@ gs_status gemm_run(const GemmCall& c, const GemmPlan& plan, void* ws, cudaStream
         GS_LAUNCH_CHECK();
     }
 
-    const bool glu = c.kind == GemmKind::kGlu;
+    const bool glu = c.kind == GemmKind::kGlu || c.kind == GemmKind::kGluGrad;
     if (plan.nb) {
         RowsParams r = {};
         gs_status s = tc::make_map(&r.x, f[0].p, c.type, c.m, c.k, f[0].ld, plan.nb, plan.k_elems);
@@ -1217,7 +1319,7 @@ gs_status gemm_run(const GemmCall& c, const GemmPlan& plan, void* ws, cudaStream
         p.part = c.m * plan.pitch;
         p.y_vec = 1;
     } else {
-        for (int i = 0; i < plan.probs; ++i) p.yp[i] = y[i], p.ldy[i] = ldy[i];
+        for (int i = 0; i < 2; ++i) p.yp[i] = y[i], p.ldy[i] = ldy[i];
         p.y_vec = rows16(c.y, c.ldy, c.out_type) && (plan.probs == 1 || rows16(c.y2, c.ldy2, c.out_type));
         if (c.residual) {
             p.residual = c.residual;
@@ -1248,7 +1350,11 @@ gs_status gemm_run(const GemmCall& c, const GemmPlan& plan, void* ws, cudaStream
         if (plan.pair) return plan.bn == 256 ? launch<256, true, false, OSZ>(p, grid, st) : launch<128, true, false, OSZ>(p, grid, st);
         return plan.bn == 128 ? launch<128, false, false, OSZ>(p, grid, st) : launch<64, false, false, OSZ>(p, grid, st);
     };
-    if (glu)
+    if (c.kind == GemmKind::kGluGrad)
+        s = !plan.pair         ? launch<128, false, true, 2, true>(p, grid, st)
+            : plan.bn == 256 ? launch<256, true, true, 2, true>(p, grid, st)
+                             : launch<128, true, true, 2, true>(p, grid, st);
+    else if (glu)
         s = !plan.pair         ? launch<128, false, true, 2>(p, grid, st)
             : plan.bn == 256 ? launch<256, true, true, 2>(p, grid, st)
                              : launch<128, true, true, 2>(p, grid, st);

@@ -16,6 +16,7 @@ struct GemmFactor {
 enum class GemmKind {
     kLinear,   // y = act(sum * x_scale * w_scale + bias) + residual, z before act
     kGlu,      // b[0] gate, b[1] up: y = act(g) * u, z = g, z2 = u
+    kGluGrad,  // b[0] gate, b[1] up, residual dh: y = dh * u * act'(g), y2 = dh * act(g) (16-byte rows, one ld)
     kSum,      // y = a[0] b[0]^T + a[1] b[1]^T
     kTwo       // y = a[0] b[0]^T, y2 = a[1] b[1]^T
 };

@@ -424,18 +424,19 @@ extern "C" gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* w
     const gs_glu_bwd_args& a = *args;
     const int64_t m = a.rows, k = a.in_features, f = a.hidden;
     if (check_sizes(m, k, f) != GS_OK) return GS_ERR_INVALID_ARG;
-    if (!type_half(a.type) || !act_ok(a.act) || !a.dw_gate != !a.dw_up) return GS_ERR_INVALID_ARG;
+    if (!type_half(a.type) || !act_ok(a.act) || !a.dw_gate != !a.dw_up || !a.g != !a.u) return GS_ERR_INVALID_ARG;
     if (a.dw_gate && ((a.dw_type != a.type && a.dw_type != GS_F32) || !mat_ok(a.dw_gate, a.lddwg, k, a.dw_type) ||
                       !mat_ok(a.dw_up, a.lddwu, k, a.dw_type)))
         return GS_ERR_INVALID_ARG;
     if (m > 0) {
-        if (!mat_ok(a.dh, a.lddh, f, a.type) || !mat_ok(a.g, a.ldg, f, a.type) || !mat_ok(a.u, a.ldu, f, a.type))
+        if (!mat_ok(a.dh, a.lddh, f, a.type)) return GS_ERR_INVALID_ARG;
+        if (a.g && (!mat_ok(a.g, a.ldg, f, a.type) || !mat_ok(a.u, a.ldu, f, a.type))) return GS_ERR_INVALID_ARG;
+        if (a.dx && !mat_ok(a.dx, a.lddx, k, a.type)) return GS_ERR_INVALID_ARG;
+        if ((a.dx || !a.g) && (!mat_ok(a.w_gate, a.ldwg, k, a.type) || !mat_ok(a.w_up, a.ldwu, k, a.type)))
             return GS_ERR_INVALID_ARG;
-        if (a.dx && (!mat_ok(a.dx, a.lddx, k, a.type) || !mat_ok(a.w_gate, a.ldwg, k, a.type) ||
-                     !mat_ok(a.w_up, a.ldwu, k, a.type)))
-            return GS_ERR_INVALID_ARG;
-        if (a.dw_gate && !mat_ok(a.x, a.ldx, k, a.type)) return GS_ERR_INVALID_ARG;
+        if ((a.dw_gate || !a.g) && !mat_ok(a.x, a.ldx, k, a.type)) return GS_ERR_INVALID_ARG;
     }
+    const bool again = !a.g;   // the projections are computed again
     const int64_t ldd = round_up(f, 8);
     Scratch sc;
     const size_t at_dg = sc.take((size_t)m * ldd * 2), at_du = sc.take((size_t)m * ldd * 2);
@@ -451,10 +452,19 @@ extern "C" gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* w
     cw.a[0] = cw.a[1] = {aligned, ldd, false};
     cw.b[0] = cw.b[1] = {a.x, a.ldx, false};
     cw.y = a.dw_gate, cw.ldy = a.lddwg, cw.y2 = a.dw_up, cw.ldy2 = a.lddwu, cw.out_type = a.dw_type;
-    GemmPlan px = {}, pw = {};
+    GemmCall cg = {};
+    cg.kind = GemmKind::kGluGrad;
+    cg.m = m, cg.n = f, cg.k = k, cg.type = a.type;
+    cg.a[0] = {a.x, a.ldx, true}, cg.b[0] = {a.w_gate, a.ldwg, true}, cg.b[1] = {a.w_up, a.ldwu, true};
+    cg.residual = a.dh, cg.ldr = a.lddh, cg.act = a.act, cg.out_type = a.type;
+    cg.y = cg.y2 = aligned, cg.ldy = cg.ldy2 = ldd;
+    GemmPlan px = {}, pw = {}, pg = {};
     if (m > 0 && a.dx) px = gemm_plan(cx);
     if (m > 0 && a.dw_gate) pw = gemm_plan(cw);
-    const size_t at_gemm = sc.take(px.bytes > pw.bytes ? px.bytes : pw.bytes);
+    if (m > 0 && again) pg = gemm_plan(cg);
+    size_t most = px.bytes > pw.bytes ? px.bytes : pw.bytes;
+    if (pg.bytes > most) most = pg.bytes;
+    const size_t at_gemm = sc.take(most);
     const WsCheck wc = ws_check(ws, ws_bytes, sc.used);
     if (wc == WsCheck::kBad) return GS_ERR_INVALID_ARG;
     if (wc == WsCheck::kQuery) return GS_OK;
@@ -467,6 +477,11 @@ extern "C" gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* w
     }
     if (!a.dx && !a.dw_gate) return GS_OK;
     char* base = (char*)ws;
+    if (again) {
+        cg.y = base + at_dg, cg.y2 = base + at_du;
+        const gs_status s = gemm_run(cg, pg, base + at_gemm, st);
+        if (s != GS_OK) return s;
+    }
     GluGradParams p = {};
     p.dh = a.dh, p.g = a.g, p.u = a.u, p.dg = base + at_dg, p.du = base + at_du;
     p.m = m, p.n = f, p.lddh = a.lddh, p.ldg = a.ldg, p.ldu = a.ldu, p.ldd = ldd;
@@ -477,7 +492,7 @@ extern "C" gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* w
     int64_t gy = (m + 2 * ty - 1) / (2 * ty);
     if (gy > 65535) gy = 65535;
     const dim3 grid((unsigned)((f + (int64_t)tx * v - 1) / ((int64_t)tx * v)), (unsigned)gy);
-    for_type_act(a.type, a.act, [&](auto t, auto act) {
+    if (!again) for_type_act(a.type, a.act, [&](auto t, auto act) {
         constexpr int T = decltype(t)::value, ACT = decltype(act)::value;
         if (vec) glu_grad_kernel<T, 8, ACT><<<grid, kElemThreads, 0, st>>>(p, tx);
         else glu_grad_kernel<T, 1, ACT><<<grid, kElemThreads, 0, st>>>(p, tx);

@@ -316,13 +316,19 @@ def linear_backward(dy, x, w, *, z=None, act=None, bias=False, need_dx=True, nee
 
 
 # ------------------------------------------------------------------ gated feed-forward
+# Up to this many input features glu's gradients compute the projections again rather than
+# read them: two more products of that depth against 8 bytes a value written and read.
+_AGAIN_FEATURES = 512
+
+
 def glu(x, w_gate, w_up, *, x_scale=None, gate_scale=None, up_scale=None, act="silu", out_dtype=None,
-        need_backward=False) -> GluOut:
+        need_backward=False, save=None) -> GluOut:
     """h = act(x Wg^T) * (x Wu^T), both projections in one kernel.
 
     x [..., in], w_gate, w_up [hidden, in]: bfloat16, float16, or float8_e4m3fn with
     float32 scales per row.  h: x's type, or out_dtype (16 bits, default bfloat16) for
-    8-bit x.  need_backward also returns the projections g and u."""
+    8-bit x.  need_backward also returns the projections g and u where glu_backward is
+    better off reading them (wide inputs; save=True or False decides instead), else None."""
     dev = _device(x, "x")
     px, ldx, rows, k = _matrix(x, "x", (*_HALF, torch.float8_e4m3fn), dev)
     pg_, ldwg, f, _ = _matrix(w_gate, "w_gate", (x.dtype,), dev, k)
@@ -341,22 +347,26 @@ def glu(x, w_gate, w_up, *, x_scale=None, gate_scale=None, up_scale=None, act="s
     if need_backward:
         if x.dtype not in _HALF:
             _bad("need_backward: 8-bit operands have no gradients")
-        g, pg, ldg = _output(x, lead, f, out_dtype)
-        u, pu, ldu = _output(x, lead, f, out_dtype)
+        if k > _AGAIN_FEATURES if save is None else save:
+            g, pg, ldg = _output(x, lead, f, out_dtype)
+            u, pu, ldu = _output(x, lead, f, out_dtype)
     _call("gs_glu", abi.glu_args(rows, k, f, px, ldx, pg_, ldwg, pu_, ldwu, pxs, pgs, pus, ph, ldh, pg, ldg, pu, ldu,
                                  _TYPES[x.dtype], _TYPES[out_dtype], _act(act)), x, dev, True)
     return GluOut(h, g, u)
 
 
-def glu_backward(dh, x, w_gate, w_up, g, u, *, act="silu", need_dx=True, need_dw=True, dw_dtype=None) -> GluGrads:
-    """Gradients of glu from dh and the projections g, u of glu with need_backward."""
+def glu_backward(dh, x, w_gate, w_up, g=None, u=None, *, act="silu", need_dx=True, need_dw=True,
+                 dw_dtype=None) -> GluGrads:
+    """Gradients of glu from dh; g, u: glu's with need_backward (None: computed again)."""
     dev = _device(x, "x")
     px, ldx, rows, k = _matrix(x, "x", _HALF, dev)
     pwg, ldwg, f, _ = _matrix(w_gate, "w_gate", (x.dtype,), dev, k)
     pwu, ldwu, _, _ = _matrix(w_up, "w_up", (x.dtype,), dev, k, f)
     pdh, lddh, _, _ = _matrix(dh, "dh", (x.dtype,), dev, f, rows)
-    pg, ldg, _, _ = _matrix(g, "g", (x.dtype,), dev, f, rows)
-    pu, ldu, _, _ = _matrix(u, "u", (x.dtype,), dev, f, rows)
+    pg = ldg = pu = ldu = 0
+    if g is not None or u is not None:
+        pg, ldg, _, _ = _matrix(g, "g", (x.dtype,), dev, f, rows)
+        pu, ldu, _, _ = _matrix(u, "u", (x.dtype,), dev, f, rows)
     dw_dtype = x.dtype if dw_dtype is None else dw_dtype
     if dw_dtype not in (x.dtype, torch.float32):
         _bad(f"dw_dtype: {dw_dtype}")

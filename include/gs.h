@@ -603,7 +603,8 @@ GS_API gs_status gs_linear_bwd(const gs_linear_bwd_args* args, void* ws, size_t*
  * x: [rows][in], w_gate, w_up: [hidden][in], all of `type` (BF16, F16 or E4M3);
  * scales as for gs_linear.  h: [rows][hidden] of out_type (BF16 or F16; `type`
  * when that is 16 bits).  g, u: both NULL, or [rows][hidden] of out_type: the
- * projections rounded to 16 bits, which gs_glu_bwd takes.
+ * projections rounded to 16 bits, which gs_glu_bwd takes where it need not
+ * compute them again.
  * Errors: as gs_linear. */
 typedef struct gs_glu_args {
     int64_t rows, in_features, hidden;
@@ -629,8 +630,10 @@ GS_API gs_status gs_glu(const gs_glu_args* args, void* ws, size_t* ws_bytes, voi
 /* Gradients of gs_glu (16-bit operands).
  *   dg = dh * u * act'(g);  du = dh * act(g)   (rounded to `type` for the products)
  *   dx = dg w_gate + du w_up;  dw_gate = dg^T x;  dw_up = du^T x
- * dh, g, u: [rows][hidden] of `type`.  dx: [rows][in] of `type`.  dw_gate,
- * dw_up: [hidden][in] of dw_type (F32 or `type`), both or neither; dx may be NULL.
+ * dh, g, u: [rows][hidden] of `type`; g and u both NULL: the projections are
+ * computed again from x and the weights, in fp32 (less traffic, and closer; the
+ * quicker way for narrow inputs).  dx: [rows][in] of `type`.  dw_gate, dw_up:
+ * [hidden][in] of dw_type (F32 or `type`), both or neither; dx may be NULL.
  * Errors: as gs_linear. */
 typedef struct gs_glu_bwd_args {
     int64_t rows, in_features, hidden;

@@ -308,7 +308,7 @@ def test_glu_and_gradients(layers, m, k, f, dt, act):
     wg, wu = rnd((f, k), 1, dt, k ** -0.5), rnd((f, k), 2, dt, k ** -0.5)
     g, mg = pre64(x, wg)
     u, mu = pre64(x, wu)
-    o = layers.glu(x, wg, wu, act=act, need_backward=True)
+    o = layers.glu(x, wg, wu, act=act, need_backward=True, save=True)
     a = act64(g, act)
     ea = 1.13 * mg + 2.0 ** -20 * a.abs()
     check(o.h, a * u, ea * u.abs() + mu * a.abs() + ea * mu + 2.0 ** -23 * (a * u).abs(), "h")
@@ -335,6 +335,36 @@ def test_glu_and_gradients(layers, m, k, f, dt, act):
     assert only.dw_up is None and torch.equal(only.dx, gr.dx)
 
 
+@pytest.mark.parametrize("m,k,f", [(1, 8, 8), (2, 31, 45), (33, 64, 129), (64, 72, 128), (130, 96, 72), (257, 331, 200),
+                                   (1025, 64, 344), (5000, 40, 24), (700, 600, 520)])
+@pytest.mark.parametrize("dt,act", [(BF, "silu"), (HF, "gelu"), (BF, "relu"), (HF, "none"), (BF, "gelu")])
+def test_glu_gradients_again(layers, m, k, f, dt, act):
+    """The gradients that compute the projections again, against the formula's at the exact ones."""
+    x = rnd((m, k), 0, dt)
+    wg, wu = rnd((f, k), 1, dt, k ** -0.5), rnd((f, k), 2, dt, k ** -0.5)
+    g, mg = pre64(x, wg)
+    u, mu = pre64(x, wu)
+    dh = rnd((m, f), 7, dt)
+    gr = layers.glu_backward(dh, x, wg, wu, act=act)
+    d, s, a, ut = dh.double(), slope64(g, act), act64(g, act), U[dt]
+    dg, du = d * u * s, d * a
+    # act' is at most 1.13 and its slope at most 0.8 (relu's jumps at 0: where |g| is within its sum's error)
+    jump = (g.abs() <= mg).double() if act == "relu" else 0.0
+    eg = ut * dg.abs() + 2.0 ** -18 * (d * u).abs() + LEAST[dt] + d.abs() * (1.13 * mu + (0.8 * mg + jump) * (u.abs() + mu))
+    eu = ut * du.abs() + 2.0 ** -18 * (d * g).abs() + LEAST[dt] + 1.13 * d.abs() * mg
+    x64, wg64, wu64 = x.double(), wg.double(), wu.double()
+    mag = dg.abs() @ wg64.abs() + du.abs() @ wu64.abs()
+    check(gr.dx, dg @ wg64 + du @ wu64, eg @ wg64.abs() + eu @ wu64.abs() + (2 * f + 4) * 2.0 ** -23 * mag, "dx")
+    for got, dd, ee, name in ((gr.dw_gate, dg, eg, "dw_gate"), (gr.dw_up, du, eu, "dw_up")):
+        check(got, dd.t() @ x64, ee.t() @ x64.abs() + (m + 4) * 2.0 ** -23 * (dd.abs().t() @ x64.abs()), name)
+
+
+def test_glu_saves_for_wide_inputs_only(layers):
+    for k, saved in ((512, False), (520, True)):
+        o = layers.glu(rnd((3, k), 0, BF), rnd((16, k), 1, BF), rnd((16, k), 2, BF), need_backward=True)
+        assert (o.g is not None) == (o.u is not None) == saved
+
+
 @pytest.mark.parametrize("m,k,f", [(1, 512, 256), (5, 100, 59), (200, 1040, 136), (600, 96, 300)])
 @pytest.mark.parametrize("out", [BF, HF])
 def test_glu_e4m3(layers, m, k, f, out):
@@ -355,8 +385,8 @@ def test_glu_strides(layers, pitch, off):
     mats = [rnd((r, c), i, BF, c ** -0.5 if i else 1.0, pitch=pitch, offset=off)
             for i, (r, c) in enumerate(((m, k), (f, k), (f, k)))]
     dense = [t.contiguous() for t in mats]
-    a = layers.glu(*mats, need_backward=True)
-    b = layers.glu(*dense, need_backward=True)
+    a = layers.glu(*mats, need_backward=True, save=True)
+    b = layers.glu(*dense, need_backward=True, save=True)
     for p, q in zip(a, b):
         assert torch.equal(p, q)
     dh = rnd((m, f), 7, BF)
@@ -368,6 +398,8 @@ def test_glu_strides(layers, pitch, off):
     p = layers.glu_backward(wide[0], *mats, wide[1], wide[2])
     q = layers.glu_backward(dh, *dense, b.g, b.u)
     for s, t in zip(p, q):
+        assert torch.equal(s, t)
+    for s, t in zip(layers.glu_backward(wide[0], *mats), layers.glu_backward(dh, *dense)):
         assert torch.equal(s, t)
 
 
@@ -556,7 +588,8 @@ def test_runs_are_bit_identical(layers):
         h = layers.glu_backward(dy, x, w, w, u.g, u.u)
         nrm = layers.rms_norm(x, rnd((k,), 7, BF), need_backward=True)
         d = layers.rms_norm_backward(x, nrm.s, rnd((k,), 7, BF), nrm.rstd)
-        runs.append([*o, *g, *u, *h, nrm.y, *d])
+        s = layers.glu(x, w, w, need_backward=True, save=True)
+        runs.append([*o, *g, u.h, *s, *h, *layers.glu_backward(dy, x, w, w, s.g, s.u), nrm.y, *d])
     for other in runs[1:]:
         for a, b_ in zip(runs[0], other):
             assert torch.equal(a, b_)

@@ -40,6 +40,7 @@ BAD = {
                dict(ldwu=31), dict(type_=0), dict(out_type=0), dict(out_type=2), dict(gate_scale=4096), dict(act=7),
                dict(g=4096, ldg=16), dict(u=4096, ldu=16), dict(g=4096, ldg=15, u=4096, ldu=16)],
     "gs_glu_bwd": [dict(rows=-1), dict(dh=0), dict(g=0), dict(u=0), dict(x=0), dict(w_gate=0), dict(w_up=0),
+                   dict(g=0, u=0, x=0, dw_gate=0, dw_up=0), dict(g=0, u=0, w_up=0, dx=0),
                    dict(dw_gate=0), dict(dw_type=2), dict(type_=3), dict(lddwu=31), dict(lddx=31), dict(ldg=15),
                    dict(act=4)],
     "gs_rms_norm_bwd": [dict(rows=-1), dict(cols=0), dict(cols=16385), dict(dy=0), dict(sum_=0), dict(weight=0),
