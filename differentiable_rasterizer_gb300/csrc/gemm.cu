@@ -455,31 +455,33 @@ __device__ __forceinline__ void issue_products(const Params& p, uint32_t first, 
     }
 }
 
-// A thread's row of dh: kC columns from `base`, 16 bits.
-template <int C>
-__device__ __forceinline__ void load_row_half(uint32_t (&w)[C / 2], const uint16_t* base, int cols, bool vec)
+// dh's part of a chunk (C 16-bit columns) into the first half of a slot's rows, 16 bytes a
+// thread, several threads a row (a thread a row instead kept the L1 at 71 %: 200 us a
+// million rows of 64 -> 128); then each thread takes its own row.
+template <int ROW>
+__device__ __forceinline__ void stage_rows(uint32_t slot, const uint16_t* base, int64_t ld, int rows, int cols, bool vec,
+                                           int lane)
 {
-    if (vec) {
+    constexpr int kPieces = ROW / 32, kRows = 32 / kPieces;   // of a half row
+    const int j = lane % kPieces, r0 = lane / kPieces, left = cols - 8 * j;
+    const uint16_t* at = base + r0 * ld + 8 * j;
+    const int64_t step = kRows * ld;
+    uint4 q[32 / kRows];
 #pragma unroll
-        for (int j = 0; j < C / 8; ++j) {
-            uint4 q = make_uint4(0, 0, 0, 0);
-            if (8 * j + 8 <= cols) q = *reinterpret_cast<const uint4*>(base + 8 * j);
-            else {
-                uint32_t t[4] = {0, 0, 0, 0};
+    for (int i = 0; i < 32 / kRows; ++i, at += step) {
+        q[i] = make_uint4(0, 0, 0, 0);
+        if (r0 + i * kRows >= rows) continue;
+        if (vec && left >= 8) q[i] = *reinterpret_cast<const uint4*>(at);
+        else {
+            uint32_t t[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int e = 0; e < 7; ++e)
-                    if (8 * j + e < cols) t[e >> 1] |= (uint32_t)base[8 * j + e] << (16 * (e & 1));
-                q = make_uint4(t[0], t[1], t[2], t[3]);
-            }
-            w[4 * j] = q.x, w[4 * j + 1] = q.y, w[4 * j + 2] = q.z, w[4 * j + 3] = q.w;
+            for (int e = 0; e < 8; ++e)
+                if (e < left) t[e >> 1] |= (uint32_t)at[e] << (16 * (e & 1));
+            q[i] = make_uint4(t[0], t[1], t[2], t[3]);
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < C / 2; ++j) w[j] = 0;
-#pragma unroll
-        for (int e = 0; e < C; ++e)
-            if (e < cols) w[e >> 1] |= (uint32_t)base[e] << (16 * (e & 1));
     }
+#pragma unroll
+    for (int i = 0; i < 32 / kRows; ++i) st_shared16(slot + slot_piece<ROW>(r0 + i * kRows, j), q[i]);
 }
 
 // 16 columns of the gated layer's gradient: dg = dh u act'(g), du = dh act(g).
@@ -611,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 const uint32_t col = col0 + (lane & 15);
                 f0 = factor(col), f1 = factor(col + 16), f2 = factor(col + 32), f3 = factor(col + 48);
             }
-            if (!GLU && p.residual && lane < rows) {
+            if ((!GLU || GRAD) && p.residual && lane < rows) {
                 const char* at = (const char*)p.residual + ((int64_t)(row0 + lane) * p.ldr + col0) * OSZ;
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
                 if (OSZ == 4 && cols > 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 128));
@@ -677,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
 
             if constexpr (GRAD) {   // a slot's row: dg, then du, of a quarter of its bytes' columns
                 constexpr int kCols = S::kSlotRow / 4, kHalf = S::kSlotRow / 32;   // pieces of dg
-                const uint16_t* from = (const uint16_t*)p.residual + (int64_t)(row0 + lane) * p.ldr + col0;
+                const uint16_t* from = (const uint16_t*)p.residual + (int64_t)row0 * p.ldr + col0;
                 const int j = lane % (2 * kHalf);
                 // lanes whose piece is du's see its rows kHalf pieces to the left
                 uint16_t* to = (uint16_t*)p.yp[j < kHalf ? 0 : 1] + (int64_t)row0 * p.ldy[0] + col0 - (j < kHalf ? 0 : 8 * kHalf);
@@ -685,8 +687,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 for (int c = 0; c < kGroupCols && c < cols; c += kCols, to += kCols, from += kCols) {
                     const int part = cols - c < kCols ? cols - c : kCols;
                     uint32_t dh[kCols / 2];
-                    load_row_half<kCols>(dh, from, lane < rows ? part : 0, p.r_vec);
                     __syncwarp();   // the slot's last readers are done
+                    stage_rows<S::kSlotRow>(slot, from, p.ldr, rows, part, p.r_vec, lane);
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < kCols / 8; ++e) {
+                        const uint4 q = ld_shared16(mine ^ (e << 4));
+                        dh[4 * e] = q.x, dh[4 * e + 1] = q.y, dh[4 * e + 2] = q.z, dh[4 * e + 3] = q.w;
+                    }
 #pragma unroll
                     for (int s = 0; s < kCols / 16; ++s) {
                         uint32_t raw[16], up[16];
@@ -1054,7 +1062,7 @@ struct Tile {
 constexpr Tile kTiles[4] = {{64, false, 400}, {128, false, 480}, {128, true, 420}, {256, true, 590}};
 
 // Cycles of a call with a tile shape: waves of tiles, each bound by its k-blocks or by
-// its epilogue's traffic (about 16 bytes a cycle and SM), and a start-up.
+// its epilogue's arithmetic and traffic (14 to 22 bytes a cycle and SM), and a start-up.
 double cost(const GemmCall& c, const Tile& t, int sms, GemmPlan* out)
 {
     GemmPlan& p = *out;
@@ -1083,7 +1091,7 @@ double cost(const GemmCall& c, const Tile& t, int sms, GemmPlan* out)
     if (most < 1) most = 1;
     for (int64_t s = 1; s <= most; s = s == most ? most + 1 : (s + s / 2 + 1 < most ? s + s / 2 + 1 : most)) {
         const double main = t.per_kb * (double)((kb + s - 1) / s);
-        const double epi = 500 + 128.0 * live * (s > 1 ? 4 : bytes) / (t.bn == 256 ? 14 : 16);
+        const double epi = 300 + 128.0 * live * ((glu ? 0.14 : 0.02) + (s > 1 ? 4 : bytes) / (t.bn == 256 ? 14.0 : 22.0));
         const double waves = (double)((tiles * s + slots - 1) / slots);
         // the join: a launch, and every partial sum read once at about 20 bytes a cycle and SM
         const double join = s > 1 ? 3500 + (double)s * c.m * c.n * p.probs * 4 / (sms * 20.0) : 0;

@@ -54,7 +54,7 @@ __device__ __forceinline__ float group_reduce(float v, int group, float* sm)
 // the lanes share out the rows' scalar work (root, quotients), which otherwise
 // costs every lane as many instructions as the row's elements.
 template <int T, int VEC, int NV, int R, bool NORM>
-__global__ void __launch_bounds__(R > 1 ? 256 : 1024) norm_fwd_kernel(gs_rms_norm_args a, int group)
+__global__ void __launch_bounds__(R > 1 || NV * VEC == 32 ? 256 : 1024) norm_fwd_kernel(gs_rms_norm_args a, int group)
 {
     __shared__ float sm[32];
     const int lane = threadIdx.x % group;
@@ -293,9 +293,16 @@ gs_status run_fwd(const gs_rms_norm_args& a, cudaStream_t st)
                      (!a.residual || rows16(a.residual, a.ldr, a.type)) && (!a.sum || rows16(a.sum, a.lds, a.type)) &&
                      (!NORM || aligned16(a.weight)) &&
                      (a.y_type == GS_E4M3 ? ((uintptr_t)a.y & 7u) == 0 && a.ldy % 8 == 0 : rows16(a.y, a.ldy, a.y_type));
-    const Shape s = shape_for(a.cols, vec ? 8 : 1);
+    Shape s = shape_for(a.cols, vec ? 8 : 1);
     const int sms = device_sms();
     if (sms <= 0) return GS_ERR_CUDA;
+    // rows of 257 to 1024 in a warp, four vectors a lane, once there are warps enough: no
+    // barrier of the block between the two reductions
+    if (vec && s.group > 32 && a.cols <= 1024 && a.rows >= 4ll * sms) {
+        s.group = 32;
+        s.nv = 4;
+        s.threads = 256;
+    }
     // four rows a group where a group is within a warp, holds one vector a lane and
     // there are rows enough to fill the SMs all the same
     const bool four = vec && s.group >= 4 && s.group <= 32 && s.nv == 1 && a.rows >= (int64_t)sms * 4 * (s.threads / s.group) * 4;
@@ -308,6 +315,7 @@ gs_status run_fwd(const gs_rms_norm_args& a, cudaStream_t st)
         if (vec) {
             if (four) GS_FWD(8, 1, 4);
             else if (s.nv == 1) GS_FWD(8, 1, 1);
+            else if (s.nv == 4) GS_FWD(8, 4, 1);
             else GS_FWD(8, 2, 1);
         } else if (s.nv <= 1) GS_FWD(1, 1, 1);
         else if (s.nv <= 4) GS_FWD(1, 4, 1);
