@@ -1084,7 +1084,8 @@ double cost(const GemmCall& c, const Tile& t, int sms, GemmPlan* out)
     const bool sum_only = !glu && !c.bias && !c.residual && !c.z && c.act == GS_ACT_NONE &&
                           !c.x_scale && !c.w_scale[0];
     const double live = (double)(c.n < p.out_cols ? c.n : p.out_cols);
-    const int bytes = type_bytes(c.out_type) * (c.residual ? 2 : 1) + (c.z ? (glu ? 4 : 2) : 0);
+    // a plain sum's plan, and so its order, does not depend on the type it is rounded to
+    const int bytes = (sum_only ? 4 : type_bytes(c.out_type)) * (c.residual ? 2 : 1) + (c.z ? (glu ? 4 : 2) : 0);
     double best = 0;
     int64_t most = sum_only ? slots / tiles : 1;
     if (most > kb / 4) most = kb / 4;
@@ -1094,7 +1095,7 @@ double cost(const GemmCall& c, const Tile& t, int sms, GemmPlan* out)
         const double epi = 300 + 128.0 * live * ((glu ? 0.14 : 0.02) + (s > 1 ? 4 : bytes) / (t.bn == 256 ? 14.0 : 22.0));
         const double waves = (double)((tiles * s + slots - 1) / slots);
         // the join: a launch, and every partial sum read once at about 20 bytes a cycle and SM
-        const double join = s > 1 ? 3500 + (double)s * c.m * c.n * p.probs * 4 / (sms * 20.0) : 0;
+        const double join = s > 1 ? 4500 + (double)s * c.m * c.n * p.probs * 4 / (sms * 20.0) : 0;
         const double v = 3000 + waves * (main > epi ? main : epi) + (main > epi ? epi : main) + join;
         if (s == 1 || v < best) {
             best = v;
@@ -1248,7 +1249,7 @@ GemmPlan gemm_plan(const GemmCall& c)
     return p;
 }
 
-gs_status gemm_run(const GemmCall& c, const GemmPlan& plan, void* ws, cudaStream_t st)
+gs_status gemm_run(const GemmCall& c, const GemmPlan& plan, void* ws, JoinJobs* joins, cudaStream_t st)
 {
     if (plan.units > 0x7fffffffll || c.m > 0x7fffff00ll || c.n > 0x7fffff00ll || c.k > 0x7fffff00ll)
         return GS_ERR_INVALID_ARG;
@@ -1371,8 +1372,8 @@ gs_status gemm_run(const GemmCall& c, const GemmPlan& plan, void* ws, cudaStream
     if (s != GS_OK || !p.partial) return s;
     const float* partial = (const float*)(base + plan.partial_at);
     for (int i = 0; i < plan.probs; ++i) {
-        s = join_partials(partial + (int64_t)i * plan.splits * c.m * plan.pitch, plan.splits, c.m, c.n, plan.pitch, y[i],
-                          ldy[i], c.out_type, st);
+        s = joins->add(partial + (int64_t)i * plan.splits * c.m * plan.pitch, plan.splits, c.m, c.n, plan.pitch, y[i], ldy[i],
+                       c.out_type);
         if (s != GS_OK) return s;
     }
     return GS_OK;

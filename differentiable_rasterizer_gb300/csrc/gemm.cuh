@@ -55,13 +55,29 @@ struct GemmPlan {
     int64_t pitch;                          // of the partial sums
 };
 GemmPlan gemm_plan(const GemmCall& c);
-gs_status gemm_run(const GemmCall& c, const GemmPlan& plan, void* ws, cudaStream_t st);
 
 // Multiprocessors of the current device (0 if there is none).
 int device_sms();
 
-// out[r * ld + c] = sum over parts, in order, of partial[part][r][c] (rows of `pitch`).
-gs_status join_partials(const float* partial, int64_t parts, int64_t rows, int64_t cols, int64_t pitch, void* out,
-                        int64_t ld, int type, cudaStream_t st);
+// Sums of partial rows, up to four of them in one launch (a launch costs the host more
+// than a small sum the GPU):  out[r * ld + c] = sum over parts, in order, of
+// partial[part][r][c], rows of `pitch` floats.
+struct JoinJobs {
+    struct Job {
+        const float* partial;
+        void* out;
+        int64_t count, ld;          // floats of a part; of out
+        uint32_t rows, cols, pitch, first;   // first: block
+        int parts, type, vec, slices;
+    } job[4];
+    int jobs = 0;
+    unsigned blocks = 0;
+    gs_status add(const float* partial, int64_t parts, int64_t rows, int64_t cols, int64_t pitch, void* out, int64_t ld,
+                  int type);
+    gs_status run(cudaStream_t st) const;   // nothing to do without jobs
+};
+
+// The partial sums of a call whose plan splits k are joined by `joins`, run later.
+gs_status gemm_run(const GemmCall& c, const GemmPlan& plan, void* ws, JoinJobs* joins, cudaStream_t st);
 
 }  // namespace gs

@@ -123,54 +123,64 @@ __global__ void __launch_bounds__(kElemThreads) glu_grad_kernel(const GluGradPar
     }
 }
 
-// Sums of partial rows, in the order of the parts.  A thread takes VEC columns of one
-// row; with SLICES > 1 it takes every SLICES-th part, and the block adds the slices in
-// order.  Few parts of a large result: SLICES 1, one pass at the reads' bandwidth; many
-// parts of a small one (a decoder's weights over a million rows): SLICES 8 or 32.
-template <int VEC, int SLICES>
-__global__ void __launch_bounds__(256) join_partials_kernel(const float* partial, int parts, int64_t count, uint32_t rows,
-                                                            uint32_t cols, uint32_t pitch, void* out, int64_t ld, int type)
+// Sums of partial rows, in the order of the parts.  A thread takes four columns of one
+// row (one where rows are not aligned); with slices > 1 it takes every slices-th part,
+// and the block adds the slices in order.  Few parts of a large result: one slice, one
+// pass at the reads' bandwidth; many parts of a small one (a decoder's weights over a
+// million rows): 8 or 32.
+template <int VEC>
+__device__ __forceinline__ void join_job(const JoinJobs::Job& q, float* sm)
 {
-    constexpr int kWide = 256 / SLICES;
-    __shared__ float sm[SLICES > 1 ? SLICES : 1][kWide * VEC + 1];
-    const int x = threadIdx.x % kWide, y = threadIdx.x / kWide;
-    const uint32_t per_row = (cols + VEC - 1) / VEC;
-    const uint32_t i = blockIdx.x * kWide + x, r = i / per_row, c = (i - r * per_row) * VEC;
-    const bool live = r < rows;
+    const int wide = 256 / q.slices, x = threadIdx.x % wide, y = threadIdx.x / wide;
+    const uint32_t per_row = (q.cols + VEC - 1) / VEC;
+    const uint32_t i = (blockIdx.x - q.first) * wide + x, r = i / per_row, c = (i - r * per_row) * VEC;
+    const bool live = r < q.rows;
     float t[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) t[e] = 0.0f;
     if (live) {
-        const float* at = partial + (int64_t)r * pitch + c;
+        const float* at = q.partial + (int64_t)r * q.pitch + c;
 #pragma unroll 4
-        for (int p = y; p < parts; p += SLICES) {
+        for (int p = y; p < q.parts; p += q.slices) {
             if constexpr (VEC == 4) {
-                const float4 f = *reinterpret_cast<const float4*>(at + p * count);
+                const float4 f = *reinterpret_cast<const float4*>(at + p * q.count);
                 t[0] += f.x, t[1] += f.y, t[2] += f.z, t[3] += f.w;
-            } else t[0] += at[p * count];
+            } else t[0] += at[p * q.count];
         }
     }
-    if constexpr (SLICES > 1) {
+    if (q.slices > 1) {   // the same for the whole block
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) sm[y][x * VEC + e] = t[e];
+        for (int e = 0; e < VEC; ++e) sm[(y * wide + x) * VEC + e] = t[e];
         __syncthreads();
         if (y > 0) return;
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
-            for (int k = 1; k < SLICES; ++k) t[e] += sm[k][x * VEC + e];
+            for (int k = 1; k < q.slices; ++k) t[e] += sm[(k * wide + x) * VEC + e];
     }
     if (!live) return;
-    const int64_t to = (int64_t)r * ld + c;
-    const size_t whole = VEC * (type == GS_F32 ? 4 : 2);
-    if (VEC == 4 && c + 4 <= cols && (((uintptr_t)out + (size_t)to * (whole / VEC)) & (whole - 1)) == 0) {
-        if (type == GS_F32) *reinterpret_cast<float4*>((float*)out + to) = make_float4(t[0], t[VEC > 1 ? 1 : 0], t[VEC > 1 ? 2 : 0], t[VEC > 1 ? 3 : 0]);
-        else *reinterpret_cast<uint2*>((uint16_t*)out + to) =
-                 make_uint2(pack_half2(t[0], t[VEC > 1 ? 1 : 0], type), pack_half2(t[VEC > 1 ? 2 : 0], t[VEC > 1 ? 3 : 0], type));
-        return;
+    const int64_t to = (int64_t)r * q.ld + c;
+    if constexpr (VEC == 4) {
+        const size_t bytes = q.type == GS_F32 ? 4 : 2;
+        if (c + 4 <= q.cols && (((uintptr_t)q.out + (size_t)to * bytes) & (4 * bytes - 1)) == 0) {
+            if (q.type == GS_F32) *reinterpret_cast<float4*>((float*)q.out + to) = make_float4(t[0], t[1], t[2], t[3]);
+            else
+                *reinterpret_cast<uint2*>((uint16_t*)q.out + to) =
+                    make_uint2(pack_half2(t[0], t[1], q.type), pack_half2(t[2], t[3], q.type));
+            return;
+        }
     }
 #pragma unroll
     for (int e = 0; e < VEC; ++e)
-        if (c + e < cols) store_elem(out, to + e, type, t[e]);
+        if (c + e < q.cols) store_elem(q.out, to + e, q.type, t[e]);
+}
+
+__global__ void __launch_bounds__(256) join_kernel(const JoinJobs p)
+{
+    __shared__ float sm[256 * 4];
+    int j = 0;
+    while (j + 1 < p.jobs && blockIdx.x >= p.job[j + 1].first) ++j;
+    if (p.job[j].vec) join_job<4>(p.job[j], sm);
+    else join_job<1>(p.job[j], sm);
 }
 
 // Calls f with the 16-bit type and the activation as constants.
@@ -232,29 +242,28 @@ struct Scratch {
 
 }  // namespace
 
-gs_status join_partials(const float* partial, int64_t parts, int64_t rows, int64_t cols, int64_t pitch, void* out,
-                        int64_t ld, int type, cudaStream_t st)
+gs_status JoinJobs::add(const float* partial, int64_t parts, int64_t rows, int64_t cols, int64_t pitch, void* out, int64_t ld,
+                        int type)
 {
-    const bool vec = pitch % 4 == 0 && aligned16(partial);
-    const int64_t threads = rows * (vec ? (cols + 3) / 4 : cols), count = rows * pitch;
-    // one thread a result where they fill the SMs; else 8, or 32 for vectors' worth of results
-    const int slices = threads >= 152 * 512 || parts < 8 ? 1 : (threads >= 152 * 32 || parts < 32 ? 8 : 32);
-    const int64_t wide = 256 / slices, blocks = (threads + wide - 1) / wide;
-    if (blocks > 0x7fffffll || threads > 0x7fffffffll) return GS_ERR_INVALID_ARG;
-    const unsigned grid = (unsigned)blocks;
-    const uint32_t r = (uint32_t)rows, c = (uint32_t)cols, q = (uint32_t)pitch;
-    const int n = (int)parts;
-    const auto run = [&](auto v, auto sl) {
-        join_partials_kernel<decltype(v)::value, decltype(sl)::value><<<grid, 256, 0, st>>>(partial, n, count, r, c, q, out,
-                                                                                          ld, type);
-    };
-    const auto pick = [&](auto v) {
-        if (slices == 1) run(v, std::integral_constant<int, 1>());
-        else if (slices == 8) run(v, std::integral_constant<int, 8>());
-        else run(v, std::integral_constant<int, 32>());
-    };
-    if (vec) pick(std::integral_constant<int, 4>());
-    else pick(std::integral_constant<int, 1>());
+    if (jobs == 4) return GS_ERR_INVALID_ARG;
+    Job& q = job[jobs++];
+    q.vec = pitch % 4 == 0 && aligned16(partial);
+    const int64_t threads = rows * (q.vec ? (cols + 3) / 4 : cols);
+    // one thread a result where they fill the SMs; else 8, or 32 for few results
+    q.slices = threads >= 152 * 512 || parts < 8 ? 1 : (threads >= 152 * 32 || parts < 32 ? 8 : 32);
+    const int64_t wide = 256 / q.slices, n = (threads + wide - 1) / wide;
+    if (n + blocks > 0x7fffffll || threads > 0x7fffffffll) return GS_ERR_INVALID_ARG;
+    q.partial = partial, q.out = out, q.count = rows * pitch, q.ld = ld;
+    q.rows = (uint32_t)rows, q.cols = (uint32_t)cols, q.pitch = (uint32_t)pitch, q.first = blocks;
+    q.parts = (int)parts, q.type = type;
+    blocks += (unsigned)n;
+    return GS_OK;
+}
+
+gs_status JoinJobs::run(cudaStream_t st) const
+{
+    if (!jobs) return GS_OK;
+    join_kernel<<<blocks, 256, 0, st>>>(*this);
     GS_LAUNCH_CHECK();
     return GS_OK;
 }
@@ -294,7 +303,9 @@ extern "C" gs_status gs_linear(const gs_linear_args* args, void* ws, size_t* ws_
     const WsCheck wc = ws_check(ws, ws_bytes, plan.bytes);
     if (wc == WsCheck::kBad) return GS_ERR_INVALID_ARG;
     if (wc == WsCheck::kQuery || a.rows == 0) return GS_OK;
-    return gemm_run(c, plan, ws, (cudaStream_t)stream);
+    JoinJobs joins;
+    const gs_status s = gemm_run(c, plan, ws, &joins, (cudaStream_t)stream);
+    return s != GS_OK ? s : joins.run((cudaStream_t)stream);
 }
 
 extern "C" gs_status gs_linear_bwd(const gs_linear_bwd_args* args, void* ws, size_t* ws_bytes, void* stream)
@@ -336,7 +347,7 @@ extern "C" gs_status gs_linear_bwd(const gs_linear_bwd_args* args, void* ws, siz
     GemmPlan px = {}, pw = {};
     if (m > 0 && a.dx) px = gemm_plan(cx);
     if (m > 0 && a.dw) pw = gemm_plan(cw);
-    const size_t at_gemm = sc.take(px.bytes > pw.bytes ? px.bytes : pw.bytes);   // one after the other
+    const size_t at_x = sc.take(px.bytes), at_w = sc.take(pw.bytes);
     const WsCheck wc = ws_check(ws, ws_bytes, sc.used);
     if (wc == WsCheck::kBad) return GS_ERR_INVALID_ARG;
     if (wc == WsCheck::kQuery) return GS_OK;
@@ -347,6 +358,7 @@ extern "C" gs_status gs_linear_bwd(const gs_linear_bwd_args* args, void* ws, siz
         return GS_OK;
     }
     char* base = (char*)ws;
+    JoinJobs joins;
     if (make_dz || a.db) {
         DzParams p = {};
         p.dy = a.dy, p.z = a.z, p.dz = make_dz ? base + at_dz : nullptr;
@@ -368,17 +380,20 @@ extern "C" gs_status gs_linear_bwd(const gs_linear_bwd_args* args, void* ws, siz
         });
         GS_LAUNCH_CHECK();
         if (a.db) {
-            const gs_status s = join_partials(p.partial, slabs, 1, n, n, a.db, n, a.db_type, st);
+            const gs_status s = joins.add(p.partial, slabs, 1, n, n, a.db, n, a.db_type);
             if (s != GS_OK) return s;
         }
         if (make_dz) cx.a[0].p = cw.a[0].p = base + at_dz;
     }
     if (a.dx) {
-        const gs_status s = gemm_run(cx, px, base + at_gemm, st);
+        const gs_status s = gemm_run(cx, px, base + at_x, &joins, st);
         if (s != GS_OK) return s;
     }
-    if (a.dw) return gemm_run(cw, pw, base + at_gemm, st);
-    return GS_OK;
+    if (a.dw) {
+        const gs_status s = gemm_run(cw, pw, base + at_w, &joins, st);
+        if (s != GS_OK) return s;
+    }
+    return joins.run(st);
 }
 
 extern "C" gs_status gs_glu(const gs_glu_args* args, void* ws, size_t* ws_bytes, void* stream)
@@ -414,7 +429,9 @@ extern "C" gs_status gs_glu(const gs_glu_args* args, void* ws, size_t* ws_bytes,
     const WsCheck wc = ws_check(ws, ws_bytes, plan.bytes);
     if (wc == WsCheck::kBad) return GS_ERR_INVALID_ARG;
     if (wc == WsCheck::kQuery || a.rows == 0) return GS_OK;
-    return gemm_run(c, plan, ws, (cudaStream_t)stream);
+    JoinJobs joins;
+    const gs_status s = gemm_run(c, plan, ws, &joins, (cudaStream_t)stream);
+    return s != GS_OK ? s : joins.run((cudaStream_t)stream);
 }
 
 extern "C" gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* ws_bytes, void* stream)
@@ -462,9 +479,7 @@ extern "C" gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* w
     if (m > 0 && a.dx) px = gemm_plan(cx);
     if (m > 0 && a.dw_gate) pw = gemm_plan(cw);
     if (m > 0 && again) pg = gemm_plan(cg);
-    size_t most = px.bytes > pw.bytes ? px.bytes : pw.bytes;
-    if (pg.bytes > most) most = pg.bytes;
-    const size_t at_gemm = sc.take(most);
+    const size_t at_x = sc.take(px.bytes > pg.bytes ? px.bytes : pg.bytes), at_w = sc.take(pw.bytes);
     const WsCheck wc = ws_check(ws, ws_bytes, sc.used);
     if (wc == WsCheck::kBad) return GS_ERR_INVALID_ARG;
     if (wc == WsCheck::kQuery) return GS_OK;
@@ -477,9 +492,10 @@ extern "C" gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* w
     }
     if (!a.dx && !a.dw_gate) return GS_OK;
     char* base = (char*)ws;
+    JoinJobs joins;
     if (again) {
         cg.y = base + at_dg, cg.y2 = base + at_du;
-        const gs_status s = gemm_run(cg, pg, base + at_gemm, st);
+        const gs_status s = gemm_run(cg, pg, base + at_x, &joins, st);
         if (s != GS_OK) return s;
     }
     GluGradParams p = {};
@@ -501,9 +517,12 @@ extern "C" gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* w
     cx.a[0].p = cw.a[0].p = p.dg;
     cx.a[1].p = cw.a[1].p = p.du;
     if (a.dx) {
-        const gs_status s = gemm_run(cx, px, base + at_gemm, st);
+        const gs_status s = gemm_run(cx, px, base + at_x, &joins, st);
         if (s != GS_OK) return s;
     }
-    if (a.dw_gate) return gemm_run(cw, pw, base + at_gemm, st);
-    return GS_OK;
+    if (a.dw_gate) {
+        const gs_status s = gemm_run(cw, pw, base + at_w, &joins, st);
+        if (s != GS_OK) return s;
+    }
+    return joins.run(st);
 }

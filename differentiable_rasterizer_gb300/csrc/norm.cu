@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(R > 1 || NV * VEC == 32 ? 256 : 1024) norm_fwd
 
 // Gradients.  dweight: every thread keeps its columns' sums over the rows it
 // visits; a block joins its groups in order and writes one partial row, and
-// join_partials_kernel (linear.cu) adds the blocks' rows in order.
+// JoinJobs (linear.cu) adds the blocks' rows in order.
 // R rows a group at a time, their loads in flight together.
 template <int T, int TDY, int VEC, int NV, int R>
 __global__ void __launch_bounds__(R > 1 ? 256 : 1024) norm_bwd_kernel(gs_rms_norm_bwd_args a, int group, float* partial)
@@ -429,6 +429,10 @@ extern "C" gs_status gs_rms_norm_bwd(const gs_rms_norm_bwd_args* args, void* ws,
     else if (a.type == GS_BF16) pick(Type<GS_BF16>());
     else pick(Type<GS_F16>());
     GS_LAUNCH_CHECK();
-    if (a.dweight) return join_partials(part, grid, 1, a.cols, a.cols, a.dweight, a.cols, a.weight_type, st);
-    return GS_OK;
+    JoinJobs joins;
+    if (a.dweight) {
+        const gs_status s = joins.add(part, grid, 1, a.cols, a.cols, a.dweight, a.cols, a.weight_type);
+        if (s != GS_OK) return s;
+    }
+    return joins.run(st);
 }
