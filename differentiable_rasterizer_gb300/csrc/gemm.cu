@@ -1003,40 +1003,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
     }
 }
 
-// Rows of any alignment to rows of 16-byte pitch (the TMA needs both): eight
-// 2-byte or sixteen 1-byte elements a thread, one 16-byte store.  All factors of a
-// call in one launch.
-struct PackJobs {
-    struct {
-        const void* src;
-        uint4* dst;
-        int64_t ld, rows, cols, pieces;
-        unsigned first;   // block
-    } job[4];
-    int jobs;
-};
-template <typename E>
-__global__ void __launch_bounds__(256) pack_rows_kernel(const PackJobs p)
-{
-    constexpr int kPer = 16 / sizeof(E);
-    int j = 0;
-    while (j + 1 < p.jobs && blockIdx.x >= p.job[j + 1].first) ++j;
-    const unsigned end = j + 1 < p.jobs ? p.job[j + 1].first : gridDim.x;
-    const auto& q = p.job[j];
-    const E* src = (const E*)q.src;
-    const int64_t total = q.rows * q.pieces, step = (int64_t)(end - q.first) * blockDim.x;
-    for (int64_t i = (int64_t)(blockIdx.x - q.first) * blockDim.x + threadIdx.x; i < total; i += step) {
-        const int64_t r = i / q.pieces, c0 = i % q.pieces * kPer;
-        union {
-            uint4 v;
-            E e[kPer];
-        } v;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) v.e[e] = c0 + e < q.cols ? src[r * q.ld + c0 + e] : (E)0;
-        q.dst[i] = v.v;
-    }
-}
-
 // ------------------------------------------------------------------ host
 // Sets a kernel's shared memory once on each device.
 template <class K>
@@ -1229,23 +1195,8 @@ GemmPlan gemm_plan(const GemmCall& c)
         while (p.ranks < 8 && tiles * p.ranks * 2 <= sms && p.k_blocks >= 2 * p.ranks) p.ranks *= 2;
         p.splits = 1;
     }
-    size_t used = 0;
-    const GemmFactor* f[4] = {&c.a[0], &c.a[1], &c.b[0], &c.b[1]};
-    for (int i = 0; i < 4; ++i) {
-        p.pack_at[i] = 0;
-        if (!f[i]->p || rows16(f[i]->p, f[i]->ld, c.type)) continue;
-        if (i & 1 && f[i]->p == f[i - 1]->p) {   // kTwo: both products read the same factor
-            p.pack_at[i] = p.pack_at[i - 1];
-            continue;
-        }
-        const int64_t rows = i < 2 ? c.m : c.n;
-        p.pack_at[i] = used + 1;
-        used += (size_t)round_up(stored_rows(*f[i], rows, c.k) * round_up(stored_cols(*f[i], rows, c.k) * p.esz, 16), 256);
-    }
-    p.partial_at = used;
     p.pitch = round_up(c.n, 4);
-    if (p.splits > 1) used += (size_t)round_up((int64_t)p.splits * p.probs * c.m * p.pitch * 4, 256);
-    p.bytes = used;
+    p.bytes = p.splits > 1 ? (size_t)round_up((int64_t)p.splits * p.probs * c.m * p.pitch * 4, 256) : 0;
     return p;
 }
 
@@ -1253,32 +1204,7 @@ gs_status gemm_run(const GemmCall& c, const GemmPlan& plan, void* ws, JoinJobs* 
 {
     if (plan.units > 0x7fffffffll || c.m > 0x7fffff00ll || c.n > 0x7fffff00ll || c.k > 0x7fffff00ll)
         return GS_ERR_INVALID_ARG;
-    char* base = (char*)ws;
-    GemmFactor f[4] = {c.a[0], c.a[1], c.b[0], c.b[1]};
-    PackJobs pack = {};
-    unsigned blocks = 0;
-    for (int i = 0; i < 4; ++i) {
-        if (!plan.pack_at[i]) continue;
-        const int64_t rows = stored_rows(f[i], i < 2 ? c.m : c.n, c.k), cols = stored_cols(f[i], i < 2 ? c.m : c.n, c.k);
-        const int64_t pieces = round_up(cols * plan.esz, 16) / 16;
-        uint4* dst = (uint4*)(base + plan.pack_at[i] - 1);
-        if (!(i & 1 && plan.pack_at[i] == plan.pack_at[i - 1])) {
-            const int64_t want = (rows * pieces + 255) / 256, most = 16ll * plan.sms;
-            auto& job = pack.job[pack.jobs++];
-            job.src = f[i].p, job.dst = dst;
-            job.ld = f[i].ld, job.rows = rows, job.cols = cols, job.pieces = pieces;
-            job.first = blocks;
-            blocks += (unsigned)(want < most ? want : most);
-        }
-        f[i].p = dst;
-        f[i].ld = pieces * 16 / plan.esz;
-    }
-    if (blocks) {
-        if (plan.esz == 2) pack_rows_kernel<uint16_t><<<blocks, 256, 0, st>>>(pack);
-        else pack_rows_kernel<uint8_t><<<blocks, 256, 0, st>>>(pack);
-        GS_LAUNCH_CHECK();
-    }
-
+    const GemmFactor f[4] = {c.a[0], c.a[1], c.b[0], c.b[1]};
     const bool glu = c.kind == GemmKind::kGlu || c.kind == GemmKind::kGluGrad;
     if (plan.nb) {
         RowsParams r = {};
@@ -1323,7 +1249,7 @@ gs_status gemm_run(const GemmCall& c, const GemmPlan& plan, void* ws, JoinJobs* 
     void* y[2] = {c.y, c.y2};
     const int64_t ldy[2] = {c.ldy, c.ldy2};
     if (p.partial) {
-        p.yp[0] = base + plan.partial_at;
+        p.yp[0] = ws;
         p.ldy[0] = plan.pitch;
         p.part = c.m * plan.pitch;
         p.y_vec = 1;
@@ -1370,7 +1296,7 @@ gs_status gemm_run(const GemmCall& c, const GemmPlan& plan, void* ws, JoinJobs* 
     else if (out_type == GS_F32) s = pick(std::integral_constant<int, 4>());
     else s = pick(std::integral_constant<int, 2>());
     if (s != GS_OK || !p.partial) return s;
-    const float* partial = (const float*)(base + plan.partial_at);
+    const float* partial = (const float*)ws;
     for (int i = 0; i < plan.probs; ++i) {
         s = joins->add(partial + (int64_t)i * plan.splits * c.m * plan.pitch, plan.splits, c.m, c.n, plan.pitch, y[i], ldy[i],
                        c.out_type);

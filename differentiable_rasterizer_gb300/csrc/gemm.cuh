@@ -6,7 +6,8 @@
 namespace gs {
 
 // A factor of the product over the contracted index k: element (row, k) lies at
-// p[row * ld + k] when k is the fast index, at p[k * ld + row] otherwise.
+// p[row * ld + k] when k is the fast index, at p[k * ld + row] otherwise.  Base and
+// pitch are multiples of 16 bytes (the TMA needs both).
 struct GemmFactor {
     const void* p;
     int64_t ld;
@@ -43,16 +44,16 @@ struct GemmCall {
     int out_type, z_type, act;
 };
 
-// How a call runs: kernel, tile shape, splits of k, and where the workspace's parts lie.
-// It depends on sizes, types, presence and alignment (of the pointers, not their values).
+// How a call runs: kernel, tile shape, splits of k.  It depends on sizes, types and on
+// which arrays are there, not on where.
 struct GemmPlan {
     int nb, ranks;   // the few-rows kernel: rows of x a CTA takes (0: not used), CTAs that split k
     bool pair;
     int bn, sms;
     int64_t tile_m, out_cols, tiles_m, tiles_n, units, k_blocks;
     int splits, terms, probs, k_elems, esz;
-    size_t pack_at[4], partial_at, bytes;   // a0, a1, b0, b1: offset + 1, 0 where used in place; scratch in all
-    int64_t pitch;                          // of the partial sums
+    int64_t pitch;   // of the partial sums
+    size_t bytes;    // of the partial sums: the call's scratch
 };
 GemmPlan gemm_plan(const GemmCall& c);
 

@@ -240,6 +240,85 @@ struct Scratch {
     }
 };
 
+// Rows of any alignment to rows of 16-byte base and pitch: eight 2-byte or sixteen
+// 1-byte elements a thread, one 16-byte store.  All factors of a call in one launch.
+struct PackJobs {
+    struct {
+        const void* src;
+        uint4* dst;
+        int64_t ld, rows, cols, pieces;
+        unsigned first;   // block
+    } job[4];
+    int jobs = 0;
+};
+template <typename E>
+__global__ void __launch_bounds__(256) pack_rows_kernel(const PackJobs p)
+{
+    constexpr int kPer = 16 / sizeof(E);
+    int j = 0;
+    while (j + 1 < p.jobs && blockIdx.x >= p.job[j + 1].first) ++j;
+    const unsigned end = j + 1 < p.jobs ? p.job[j + 1].first : gridDim.x;
+    const auto& q = p.job[j];
+    const E* src = (const E*)q.src;
+    const int64_t total = q.rows * q.pieces, step = (int64_t)(end - q.first) * blockDim.x;
+    for (int64_t i = (int64_t)(blockIdx.x - q.first) * blockDim.x + threadIdx.x; i < total; i += step) {
+        const int64_t r = i / q.pieces, c0 = i % q.pieces * kPer;
+        union {
+            uint4 v;
+            E e[kPer];
+        } v;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) v.e[e] = c0 + e < q.cols ? src[r * q.ld + c0 + e] : (E)0;
+        q.dst[i] = v.v;
+    }
+}
+
+// A call's factor as the products take it: where it lies if its rows are aligned, else
+// a copy in the workspace, made by pack_all.
+struct Rows {
+    const void* p = nullptr;
+    int64_t ld = 0;
+    const void* src = nullptr;   // set where a copy is made
+    int64_t src_ld = 0, rows = 0, cols = 0;
+    size_t at = 0;
+};
+
+Rows aligned_rows(Scratch& sc, bool used, const void* p, int64_t ld, int64_t rows, int64_t cols, int type)
+{
+    Rows r;
+    r.p = p, r.ld = ld;
+    if (!used || rows16(p, ld, type)) return r;
+    const int64_t esz = type_bytes(type);
+    r.src = p, r.src_ld = ld, r.rows = rows, r.cols = cols;
+    r.ld = round_up(cols * esz, 16) / esz;
+    r.at = sc.take((size_t)(rows * r.ld * esz));
+    r.p = nullptr;
+    return r;
+}
+
+gs_status pack_all(Rows* const* list, int n, char* base, int type, cudaStream_t st)
+{
+    PackJobs jobs;
+    unsigned blocks = 0;
+    const int64_t esz = type_bytes(type), most = 16ll * (device_sms() > 0 ? device_sms() : 152);
+    for (int i = 0; i < n; ++i) {
+        Rows& r = *list[i];
+        if (!r.src) continue;
+        r.p = base + r.at;
+        auto& job = jobs.job[jobs.jobs++];
+        job.src = r.src, job.dst = (uint4*)r.p;
+        job.ld = r.src_ld, job.rows = r.rows, job.cols = r.cols, job.pieces = r.ld * esz / 16;
+        job.first = blocks;
+        const int64_t want = (job.rows * job.pieces + 255) / 256;
+        blocks += (unsigned)(want < most ? want : most);
+    }
+    if (!blocks) return GS_OK;
+    if (esz == 2) pack_rows_kernel<uint16_t><<<blocks, 256, 0, st>>>(jobs);
+    else pack_rows_kernel<uint8_t><<<blocks, 256, 0, st>>>(jobs);
+    GS_LAUNCH_CHECK();
+    return GS_OK;
+}
+
 }  // namespace
 
 gs_status JoinJobs::add(const float* partial, int64_t parts, int64_t rows, int64_t cols, int64_t pitch, void* out, int64_t ld,
@@ -292,20 +371,33 @@ extern "C" gs_status gs_linear(const gs_linear_args* args, void* ws, size_t* ws_
     GemmCall c = {};
     c.kind = GemmKind::kLinear;
     c.m = a.rows, c.n = a.out_features, c.k = a.in_features, c.type = a.type;
-    c.a[0] = {a.x, a.ldx, true}, c.b[0] = {a.w, a.ldw, true};
     c.x_scale = a.x_scale, c.w_scale[0] = a.w_scale;
     c.bias = a.bias, c.bias_type = a.bias_type, c.act = a.act;
     c.residual = a.residual, c.ldr = a.ldr;
     c.y = a.y, c.ldy = a.ldy, c.out_type = a.out_type;
     c.z = a.z, c.ldz = a.ldz, c.z_type = a.type;
+    c.a[0].k_fast = c.b[0].k_fast = true;
     GemmPlan plan = {};
-    if (a.rows > 0) plan = gemm_plan(c);
-    const WsCheck wc = ws_check(ws, ws_bytes, plan.bytes);
+    Scratch sc;
+    Rows x, w;
+    size_t at = 0;
+    if (a.rows > 0) {
+        plan = gemm_plan(c);
+        x = aligned_rows(sc, true, a.x, a.ldx, c.m, c.k, a.type);
+        w = aligned_rows(sc, true, a.w, a.ldw, c.n, c.k, a.type);
+        at = sc.take(plan.bytes);
+    }
+    const WsCheck wc = ws_check(ws, ws_bytes, sc.used);
     if (wc == WsCheck::kBad) return GS_ERR_INVALID_ARG;
     if (wc == WsCheck::kQuery || a.rows == 0) return GS_OK;
+    cudaStream_t st = (cudaStream_t)stream;
+    Rows* const list[] = {&x, &w};
+    gs_status s = pack_all(list, 2, (char*)ws, a.type, st);
+    if (s != GS_OK) return s;
+    c.a[0] = {x.p, x.ld, true}, c.b[0] = {w.p, w.ld, true};
     JoinJobs joins;
-    const gs_status s = gemm_run(c, plan, ws, &joins, (cudaStream_t)stream);
-    return s != GS_OK ? s : joins.run((cudaStream_t)stream);
+    s = gemm_run(c, plan, (char*)ws + at, &joins, st);
+    return s != GS_OK ? s : joins.run(st);
 }
 
 extern "C" gs_status gs_linear_bwd(const gs_linear_bwd_args* args, void* ws, size_t* ws_bytes, void* stream)
@@ -337,16 +429,17 @@ extern "C" gs_status gs_linear_bwd(const gs_linear_bwd_args* args, void* ws, siz
     GemmCall cx = {}, cw = {};
     cx.kind = cw.kind = GemmKind::kLinear;
     cx.type = cw.type = a.type;
-    const GemmFactor dz_k = {make_dz ? (void*)256 : a.dy, make_dz ? lddz : a.lddy, true};
+    cx.a[0].k_fast = true;   // the others' fast index is not the contracted one
     cx.m = m, cx.n = k, cx.k = n;
-    cx.a[0] = dz_k, cx.b[0] = {a.w, a.ldw, false};
     cx.y = a.dx, cx.ldy = a.lddx, cx.out_type = a.type;
     cw.m = n, cw.n = k, cw.k = m;
-    cw.a[0] = {dz_k.p, dz_k.ld, false}, cw.b[0] = {a.x, a.ldx, false};
     cw.y = a.dw, cw.ldy = a.lddw, cw.out_type = a.dw_type;
     GemmPlan px = {}, pw = {};
     if (m > 0 && a.dx) px = gemm_plan(cx);
     if (m > 0 && a.dw) pw = gemm_plan(cw);
+    Rows dz = aligned_rows(sc, m > 0 && products && !make_dz, a.dy, a.lddy, m, n, a.type);
+    Rows w = aligned_rows(sc, m > 0 && a.dx, a.w, a.ldw, n, k, a.type);
+    Rows x = aligned_rows(sc, m > 0 && a.dw, a.x, a.ldx, m, k, a.type);
     const size_t at_x = sc.take(px.bytes), at_w = sc.take(pw.bytes);
     const WsCheck wc = ws_check(ws, ws_bytes, sc.used);
     if (wc == WsCheck::kBad) return GS_ERR_INVALID_ARG;
@@ -383,8 +476,13 @@ extern "C" gs_status gs_linear_bwd(const gs_linear_bwd_args* args, void* ws, siz
             const gs_status s = joins.add(p.partial, slabs, 1, n, n, a.db, n, a.db_type);
             if (s != GS_OK) return s;
         }
-        if (make_dz) cx.a[0].p = cw.a[0].p = base + at_dz;
+        if (make_dz) dz.p = base + at_dz, dz.ld = lddz;
     }
+    Rows* const list[] = {&dz, &w, &x};
+    const gs_status packed = pack_all(list, 3, base, a.type, st);
+    if (packed != GS_OK) return packed;
+    cx.a[0] = {dz.p, dz.ld, true}, cx.b[0] = {w.p, w.ld, false};
+    cw.a[0] = {dz.p, dz.ld, false}, cw.b[0] = {x.p, x.ld, false};
     if (a.dx) {
         const gs_status s = gemm_run(cx, px, base + at_x, &joins, st);
         if (s != GS_OK) return s;
@@ -418,20 +516,30 @@ extern "C" gs_status gs_glu(const gs_glu_args* args, void* ws, size_t* ws_bytes,
     GemmCall c = {};
     c.kind = GemmKind::kGlu;
     c.m = a.rows, c.n = a.hidden, c.k = a.in_features, c.type = a.type;
-    c.a[0] = {a.x, a.ldx, true};
-    c.b[0] = {a.w_gate, a.ldwg, true}, c.b[1] = {a.w_up, a.ldwu, true};
     c.x_scale = a.x_scale, c.w_scale[0] = a.gate_scale, c.w_scale[1] = a.up_scale;
     c.act = a.act;
     c.y = a.h, c.ldy = a.ldh, c.out_type = c.z_type = a.out_type;
     c.z = a.g, c.ldz = a.ldg, c.z2 = a.u, c.ldz2 = a.ldu;
+    c.a[0].k_fast = c.b[0].k_fast = true;
     GemmPlan plan = {};
-    if (a.rows > 0) plan = gemm_plan(c);
-    const WsCheck wc = ws_check(ws, ws_bytes, plan.bytes);
+    Scratch sc;
+    Rows x, wg, wu;
+    if (a.rows > 0) {
+        plan = gemm_plan(c);
+        x = aligned_rows(sc, true, a.x, a.ldx, c.m, c.k, a.type);
+        wg = aligned_rows(sc, true, a.w_gate, a.ldwg, c.n, c.k, a.type);
+        wu = aligned_rows(sc, true, a.w_up, a.ldwu, c.n, c.k, a.type);
+    }
+    const WsCheck wc = ws_check(ws, ws_bytes, sc.used);
     if (wc == WsCheck::kBad) return GS_ERR_INVALID_ARG;
     if (wc == WsCheck::kQuery || a.rows == 0) return GS_OK;
-    JoinJobs joins;
-    const gs_status s = gemm_run(c, plan, ws, &joins, (cudaStream_t)stream);
-    return s != GS_OK ? s : joins.run((cudaStream_t)stream);
+    cudaStream_t st = (cudaStream_t)stream;
+    Rows* const list[] = {&x, &wg, &wu};
+    const gs_status s = pack_all(list, 3, (char*)ws, a.type, st);
+    if (s != GS_OK) return s;
+    c.a[0] = {x.p, x.ld, true};
+    c.b[0] = {wg.p, wg.ld, true}, c.b[1] = {wu.p, wu.ld, true};
+    return gemm_run(c, plan, nullptr, nullptr, st);   // a gated layer never splits k
 }
 
 extern "C" gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* ws_bytes, void* stream)
@@ -460,26 +568,25 @@ extern "C" gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* w
     GemmCall cx = {}, cw = {};
     cx.kind = GemmKind::kSum, cw.kind = GemmKind::kTwo;
     cx.type = cw.type = a.type;
-    void* const aligned = (void*)256;   // where the workspace's parts lie is not known yet; that they are aligned is
     cx.m = m, cx.n = k, cx.k = f;
-    cx.a[0] = cx.a[1] = {aligned, ldd, true};
-    cx.b[0] = {a.w_gate, a.ldwg, false}, cx.b[1] = {a.w_up, a.ldwu, false};
+    cx.a[0].k_fast = cx.a[1].k_fast = true;
     cx.y = a.dx, cx.ldy = a.lddx, cx.out_type = a.type;
     cw.m = f, cw.n = k, cw.k = m;
-    cw.a[0] = cw.a[1] = {aligned, ldd, false};
-    cw.b[0] = cw.b[1] = {a.x, a.ldx, false};
     cw.y = a.dw_gate, cw.ldy = a.lddwg, cw.y2 = a.dw_up, cw.ldy2 = a.lddwu, cw.out_type = a.dw_type;
     GemmCall cg = {};
     cg.kind = GemmKind::kGluGrad;
     cg.m = m, cg.n = f, cg.k = k, cg.type = a.type;
-    cg.a[0] = {a.x, a.ldx, true}, cg.b[0] = {a.w_gate, a.ldwg, true}, cg.b[1] = {a.w_up, a.ldwu, true};
+    cg.a[0].k_fast = cg.b[0].k_fast = cg.b[1].k_fast = true;
     cg.residual = a.dh, cg.ldr = a.lddh, cg.act = a.act, cg.out_type = a.type;
-    cg.y = cg.y2 = aligned, cg.ldy = cg.ldy2 = ldd;
+    cg.ldy = cg.ldy2 = ldd;
     GemmPlan px = {}, pw = {}, pg = {};
     if (m > 0 && a.dx) px = gemm_plan(cx);
     if (m > 0 && a.dw_gate) pw = gemm_plan(cw);
     if (m > 0 && again) pg = gemm_plan(cg);
-    const size_t at_x = sc.take(px.bytes > pg.bytes ? px.bytes : pg.bytes), at_w = sc.take(pw.bytes);
+    Rows x = aligned_rows(sc, m > 0 && (again || a.dw_gate), a.x, a.ldx, m, k, a.type);
+    Rows wg = aligned_rows(sc, m > 0 && (again || a.dx), a.w_gate, a.ldwg, f, k, a.type);
+    Rows wu = aligned_rows(sc, m > 0 && (again || a.dx), a.w_up, a.ldwu, f, k, a.type);
+    const size_t at_x = sc.take(px.bytes), at_w = sc.take(pw.bytes);
     const WsCheck wc = ws_check(ws, ws_bytes, sc.used);
     if (wc == WsCheck::kBad) return GS_ERR_INVALID_ARG;
     if (wc == WsCheck::kQuery) return GS_OK;
@@ -493,9 +600,14 @@ extern "C" gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* w
     if (!a.dx && !a.dw_gate) return GS_OK;
     char* base = (char*)ws;
     JoinJobs joins;
+    Rows* const list[] = {&x, &wg, &wu};
+    const gs_status packed = pack_all(list, 3, base, a.type, st);
+    if (packed != GS_OK) return packed;
     if (again) {
+        cg.a[0] = {x.p, x.ld, true};
+        cg.b[0] = {wg.p, wg.ld, true}, cg.b[1] = {wu.p, wu.ld, true};
         cg.y = base + at_dg, cg.y2 = base + at_du;
-        const gs_status s = gemm_run(cg, pg, base + at_x, &joins, st);
+        const gs_status s = gemm_run(cg, pg, nullptr, nullptr, st);
         if (s != GS_OK) return s;
     }
     GluGradParams p = {};
@@ -514,8 +626,10 @@ extern "C" gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* w
         else glu_grad_kernel<T, 1, ACT><<<grid, kElemThreads, 0, st>>>(p, tx);
     });
     GS_LAUNCH_CHECK();
-    cx.a[0].p = cw.a[0].p = p.dg;
-    cx.a[1].p = cw.a[1].p = p.du;
+    cx.a[0] = {p.dg, ldd, true}, cx.a[1] = {p.du, ldd, true};
+    cx.b[0] = {wg.p, wg.ld, false}, cx.b[1] = {wu.p, wu.ld, false};
+    cw.a[0] = {p.dg, ldd, false}, cw.a[1] = {p.du, ldd, false};
+    cw.b[0] = cw.b[1] = {x.p, x.ld, false};
     if (a.dx) {
         const gs_status s = gemm_run(cx, px, base + at_x, &joins, st);
         if (s != GS_OK) return s;
