@@ -358,7 +358,10 @@ template <int ACT>
 __device__ __forceinline__ void activate(float (&v)[16])
 {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = act_value(v[j], ACT);
+    for (int j = 0; j < 16; j += 2) {
+        const float2 f = unpair(act_value2<ACT>(pair(v[j], v[j + 1])));
+        v[j] = f.x, v[j + 1] = f.y;
+    }
 }
 __device__ __forceinline__ void activate(float (&v)[16], int act)
 {
@@ -489,11 +492,13 @@ template <int ACT>
 __device__ __forceinline__ void glu_gradient(float (&g)[16], float (&u)[16], const float (&dh)[16])
 {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        float value, slope;
-        act_both(g[j], ACT, value, slope);
-        g[j] = dh[j] * u[j] * slope;
-        u[j] = dh[j] * value;
+    for (int j = 0; j < 16; j += 2) {
+        uint64_t value, slope;
+        act_both2<ACT>(pair(g[j], g[j + 1]), value, slope);
+        const uint64_t d = pair(dh[j], dh[j + 1]);
+        const float2 a = unpair(mul2(mul2(d, pair(u[j], u[j + 1])), slope)), b = unpair(mul2(d, value));
+        g[j] = a.x, g[j + 1] = a.y;
+        u[j] = b.x, u[j + 1] = b.y;
     }
 }
 __device__ __forceinline__ void glu_gradient(float (&g)[16], float (&u)[16], const float (&dh)[16], int act)
@@ -671,7 +676,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                             for (int j = 0; j < 16; ++j) v[j] *= xs * factors[j];
                         }
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] += factors[16 + j];
+                        for (int j = 0; j < 16; j += 2) {
+                            const float2 f = unpair(add2(pair(v[j], v[j + 1]), pair(factors[16 + j], factors[17 + j])));
+                            v[j] = f.x, v[j + 1] = f.y;
+                        }
                     }
                     if (last) activate(v, p.act);
                 }

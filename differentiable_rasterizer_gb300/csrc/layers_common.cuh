@@ -267,6 +267,75 @@ __device__ __forceinline__ float act_value(float v, int act)
     return v;
 }
 
+// Two floats in one 64-bit register: sm_103a adds, multiplies and fuses them in one
+// instruction, rounding each as the single one does.
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// Phi of two values as normal_cdf computes it, but 1/2 + sign(v) (1/2 - q): in pairs that
+// is cheaper than a choice, and off by half a unit of 1/2 more.
+__device__ __forceinline__ uint64_t normal_cdf2(uint64_t v, uint64_t& e)
+{
+    const float2 f = unpair(v);
+    const float2 d = unpair(fma2(pair(fabsf(f.x), fabsf(f.y)), pair(0.3275911f * 0.70710678f, 0.3275911f * 0.70710678f),
+                                 pair(1.0f, 1.0f)));
+    const uint64_t t = pair(rcp_fast(d.x), rcp_fast(d.y));
+    const float kE = -0.5f * 1.4426950408889634f;
+    const float2 x = unpair(mul2(mul2(v, v), pair(kE, kE)));
+    e = pair(exp2_fast(x.x), exp2_fast(x.y));
+    const auto both = [](float c) { return pair(c, c); };
+    uint64_t q = fma2(t, both(0.5f * 1.061405429f), both(0.5f * -1.453152027f));
+    q = fma2(t, q, both(0.5f * 1.421413741f));
+    q = fma2(t, q, both(0.5f * -0.284496736f));
+    q = fma2(t, q, both(0.5f * 0.254829592f));
+    const float2 h = unpair(fma2(mul2(q, t), mul2(e, both(-1.0f)), both(0.5f)));
+    return add2(pair(copysignf(h.x, f.x), copysignf(h.y, f.y)), both(0.5f));
+}
+
+template <int ACT>
+__device__ __forceinline__ uint64_t act_value2(uint64_t v)
+{
+    if constexpr (ACT == GS_ACT_SILU) {
+        const float2 x = unpair(mul2(v, pair(-1.4426950408889634f, -1.4426950408889634f)));
+        const float2 d = unpair(add2(pair(exp2_fast(x.x), exp2_fast(x.y)), pair(1.0f, 1.0f)));
+        return mul2(v, pair(rcp_fast(d.x), rcp_fast(d.y)));
+    } else if constexpr (ACT == GS_ACT_GELU) {
+        uint64_t e;
+        return mul2(v, normal_cdf2(v, e));
+    } else {
+        const float2 f = unpair(v);
+        return pair(act_value(f.x, ACT), act_value(f.y, ACT));
+    }
+}
+
 // act(v) and act'(v), from one sigma or one Phi.
 __device__ __forceinline__ void act_both(float v, int act, float& value, float& slope)
 {
@@ -285,6 +354,31 @@ __device__ __forceinline__ void act_both(float v, int act, float& value, float& 
     } else {
         value = v;
         slope = 1.0f;
+    }
+}
+
+template <int ACT>
+__device__ __forceinline__ void act_both2(uint64_t v, uint64_t& value, uint64_t& slope)
+{
+    const auto both = [](float c) { return pair(c, c); };
+    if constexpr (ACT == GS_ACT_SILU) {
+        const float2 x = unpair(mul2(v, both(-1.4426950408889634f)));
+        const float2 d = unpair(add2(pair(exp2_fast(x.x), exp2_fast(x.y)), both(1.0f)));
+        const uint64_t p = pair(rcp_fast(d.x), rcp_fast(d.y));
+        value = mul2(v, p);
+        slope = mul2(p, fma2(v, fma2(p, both(-1.0f), both(1.0f)), both(1.0f)));
+    } else if constexpr (ACT == GS_ACT_GELU) {
+        uint64_t e;
+        const uint64_t c = normal_cdf2(v, e);
+        value = mul2(v, c);
+        slope = fma2(mul2(v, both(0.39894228040143268f)), e, c);
+    } else {
+        const float2 f = unpair(v);
+        float2 a, b;
+        act_both(f.x, ACT, a.x, b.x);
+        act_both(f.y, ACT, a.y, b.y);
+        value = pair(a.x, a.y);
+        slope = pair(b.x, b.y);
     }
 }
 

@@ -55,8 +55,15 @@ __global__ void __launch_bounds__(kElemThreads) dz_kernel(const DzParams p, int 
                 raw_values(gr[i], p.dy_type, g);
                 if (ACT != GS_ACT_NONE) {
                     raw_values(zr[i], T, z);
+                    if constexpr (VEC == 8) {
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) g[e] *= act_slope(z[e], ACT);
+                        for (int e = 0; e < 8; e += 2) {
+                            uint64_t value, slope;
+                            act_both2<ACT>(pair(z[e], z[e + 1]), value, slope);
+                            const float2 f = unpair(mul2(pair(g[e], g[e + 1]), slope));
+                            g[e] = f.x, g[e + 1] = f.y;
+                        }
+                    } else g[0] *= act_slope(z[0], ACT);
                 }
                 if (p.dz && row + i * step < p.m) store_vec<VEC>(p.dz, (row + i * step) * p.lddz + col, T, g);
 #pragma unroll
@@ -110,12 +117,21 @@ __global__ void __launch_bounds__(kElemThreads) glu_grad_kernel(const GluGradPar
             raw_values(dr[i], T, d);
             raw_values(gr[i], T, g);
             raw_values(ur[i], T, u);
+            if constexpr (VEC == 8) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
+                for (int e = 0; e < 8; e += 2) {
+                    uint64_t value, slope;
+                    act_both2<ACT>(pair(g[e], g[e + 1]), value, slope);
+                    const uint64_t q = pair(d[e], d[e + 1]);
+                    const float2 a = unpair(mul2(mul2(q, pair(u[e], u[e + 1])), slope)), b = unpair(mul2(q, value));
+                    g[e] = a.x, g[e + 1] = a.y;
+                    u[e] = b.x, u[e + 1] = b.y;
+                }
+            } else {
                 float value, slope;
-                act_both(g[e], ACT, value, slope);
-                g[e] = d[e] * u[e] * slope;
-                u[e] = d[e] * value;
+                act_both(g[0], ACT, value, slope);
+                g[0] = d[0] * u[0] * slope;
+                u[0] = d[0] * value;
             }
             store_vec<VEC>(p.dg, r * p.ldd + col, T, g);
             store_vec<VEC>(p.du, r * p.ldd + col, T, u);
@@ -174,7 +190,7 @@ __device__ __forceinline__ void join_job(const JoinJobs::Job& q, float* sm)
         if (c + e < q.cols) store_elem(q.out, to + e, q.type, t[e]);
 }
 
-__global__ void __launch_bounds__(256) join_kernel(const JoinJobs p)
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinJobs p)
 {
     __shared__ float sm[256 * 4];
     int j = 0;
@@ -252,7 +268,7 @@ struct PackJobs {
     int jobs = 0;
 };
 template <typename E>
-__global__ void __launch_bounds__(256) pack_rows_kernel(const PackJobs p)
+__global__ void __launch_bounds__(256) pack_rows_kernel(const __grid_constant__ PackJobs p)
 {
     constexpr int kPer = 16 / sizeof(E);
     int j = 0;
