@@ -773,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                         Residual<S::kSlotRow, OSZ> res;
                         if (OSZ == 2) fetch_residual(res, 0, from, p.ldr, rows, part, vec, lane);
                         __syncwarp();
-#pragma unroll 1
+#pragma unroll   // both steps' TMEM reads in flight
                         for (int s = 0; s < kCols / 16; ++s) {
                             float v[16];
                             columns16(c + 16 * s, pass, v);

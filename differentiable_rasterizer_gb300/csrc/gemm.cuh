@@ -61,7 +61,7 @@ GemmPlan gemm_plan(const GemmCall& c);
 int device_sms();
 
 // Sums of partial rows, up to four of them in one launch (a launch costs the host more
-// than a small sum the GPU):  out[r * ld + c] = sum over parts, in order, of
+// than a small sum the GPU):  out[r * ld + c] = sum over parts, in a fixed order, of
 // partial[part][r][c], rows of `pitch` floats.
 struct JoinJobs {
     struct Job {

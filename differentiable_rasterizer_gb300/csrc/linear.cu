@@ -141,11 +141,11 @@ __global__ void __launch_bounds__(kElemThreads) glu_grad_kernel(const GluGradPar
 
 // Sums of partial rows, in the order of the parts.  A thread takes four columns of one
 // row (one where rows are not aligned); with slices > 1 it takes every slices-th part,
-// and the block adds the slices in order.  Few parts of a large result: one slice, one
+// and the block adds the slices in a tree.  Few parts of a large result: one slice, one
 // pass at the reads' bandwidth; many parts of a small one (a decoder's weights over a
-// million rows): 8 or 32.
+// million rows): up to 64.
 template <int VEC>
-__device__ __forceinline__ void join_job(const JoinJobs::Job& q, float* sm)
+__device__ __forceinline__ void join_job(const JoinJobs::Job& q, float4* sm)
 {
     const int wide = 256 / q.slices, x = threadIdx.x % wide, y = threadIdx.x / wide;
     const uint32_t per_row = (q.cols + VEC - 1) / VEC;
@@ -164,14 +164,19 @@ __device__ __forceinline__ void join_job(const JoinJobs::Job& q, float* sm)
             } else t[0] += at[p * q.count];
         }
     }
-    if (q.slices > 1) {   // the same for the whole block
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) sm[(y * wide + x) * VEC + e] = t[e];
-        __syncthreads();
+    if (q.slices > 1) {   // the same for the whole block: halves added to halves, a fixed tree
+        float4* const mine = sm + threadIdx.x;
+        *mine = make_float4(t[0], t[VEC > 1 ? 1 : 0], t[VEC > 1 ? 2 : 0], t[VEC > 1 ? 3 : 0]);
+        for (int half = q.slices / 2; half > 0; half /= 2) {
+            __syncthreads();
+            if (y < half) {
+                const float4 o = mine[half * wide], m = *mine;
+                *mine = make_float4(m.x + o.x, m.y + o.y, m.z + o.z, m.w + o.w);
+            }
+        }
         if (y > 0) return;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-            for (int k = 1; k < q.slices; ++k) t[e] += sm[(k * wide + x) * VEC + e];
+        t[0] = mine->x;
+        if constexpr (VEC > 1) t[1] = mine->y, t[2] = mine->z, t[3] = mine->w;
     }
     if (!live) return;
     const int64_t to = (int64_t)r * q.ld + c;
@@ -192,7 +197,7 @@ __device__ __forceinline__ void join_job(const JoinJobs::Job& q, float* sm)
 
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinJobs p)
 {
-    __shared__ float sm[256 * 4];
+    __shared__ float4 sm[256];
     int j = 0;
     while (j + 1 < p.jobs && blockIdx.x >= p.job[j + 1].first) ++j;
     if (p.job[j].vec) join_job<4>(p.job[j], sm);
@@ -344,8 +349,9 @@ gs_status JoinJobs::add(const float* partial, int64_t parts, int64_t rows, int64
     Job& q = job[jobs++];
     q.vec = pitch % 4 == 0 && aligned16(partial);
     const int64_t threads = rows * (q.vec ? (cols + 3) / 4 : cols);
-    // one thread a result where they fill the SMs; else 8, or 32 for few results
-    q.slices = threads >= 152 * 512 || parts < 8 ? 1 : (threads >= 152 * 32 || parts < 32 ? 8 : 32);
+    // one thread a result where they fill the SMs; else so many that they do, eight parts each at least
+    q.slices = 1;
+    while (q.slices < 64 && threads * q.slices < 152 * 512 && parts >= 8 * q.slices) q.slices *= 2;
     const int64_t wide = 256 / q.slices, n = (threads + wide - 1) / wide;
     if (n + blocks > 0x7fffffll || threads > 0x7fffffffll) return GS_ERR_INVALID_ARG;
     q.partial = partial, q.out = out, q.count = rows * pitch, q.ld = ld;
