@@ -554,6 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     if constexpr (PAIR) cluster_sync();   // both CTAs' barriers exist before any copy or commit reaches them
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    wait_for_predecessor();
 
     if (warp == 0) {
         if (elect_one()) {
@@ -881,9 +882,11 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
         mbar_init(bar_acc, 1);
         *gave_up = 0;
         mbar_init_fence();
+        wait_for_predecessor();
         for (uint32_t kb = kb0; kb < kb_first; ++kb) send(kb - kb0, kb);
     }
     if (warp == 1) tmem_alloc<false>(smem_addr(tmem_slot), S::kTmemCols);
+    wait_for_predecessor();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1092,19 +1095,7 @@ gs_status launch_rows(const RowsParams& p, unsigned grid, int ranks, cudaStream_
     static std::atomic<uint64_t> done{0};
     const gs_status s = allow_smem(kernel, S::kSmem, done);
     if (s != GS_OK) return s;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kRowsThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ranks;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    GS_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, p));
-    return GS_OK;
+    return launch_after(kernel, dim3(grid), kRowsThreads, S::kSmem, (unsigned)ranks, st, p);
 }
 
 template <int BN, bool PAIR, bool GLU, int OSZ, bool GRAD = false>
@@ -1116,19 +1107,7 @@ gs_status launch(const Params& p, int grid, cudaStream_t st)
     static std::atomic<uint64_t> done{0};
     const gs_status s = allow_smem(kernel, S::kSmem, done);
     if (s != GS_OK) return s;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = PAIR ? 2 : 1;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = PAIR ? 1 : 0;
-    GS_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, p));
-    return GS_OK;
+    return launch_after(kernel, dim3((unsigned)grid), kThreads, S::kSmem, PAIR ? 2 : 1, st, p);
 }
 
 }  // namespace

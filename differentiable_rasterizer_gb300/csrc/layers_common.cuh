@@ -46,6 +46,38 @@ inline WsCheck ws_check(void* ws, size_t* ws_bytes, size_t need)
     return *ws_bytes < need || ((uintptr_t)ws & 255u) ? WsCheck::kBad : WsCheck::kRun;
 }
 
+// ------------------------------------------------------------------ launches
+// The layers' kernels follow one another closely (a training step of a layer is four to
+// eight), so each is launched as a dependent of the one before: its blocks may be set up
+// while that one still runs, and wait for its end, with all its writes visible, in
+// wait_for_predecessor, which every thread calls before it touches memory.
+__device__ __forceinline__ void wait_for_predecessor()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+}
+
+template <class... P, class... A>
+gs_status launch_after(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, unsigned cluster, cudaStream_t st,
+                       const A&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    GS_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, args...));
+    return GS_OK;
+}
+
 // ------------------------------------------------------------------ elements
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }

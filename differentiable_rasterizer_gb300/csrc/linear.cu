@@ -26,8 +26,9 @@ struct DzParams {
 };
 
 template <int T, int TDY, int VEC, int ACT>
-__global__ void __launch_bounds__(kElemThreads) dz_kernel(const DzParams p, int tx)
+__global__ void __launch_bounds__(kElemThreads) dz_kernel(const __grid_constant__ DzParams p, int tx)
 {
+    wait_for_predecessor();
     __shared__ float part[kElemThreads * VEC];
     const int ty = kElemThreads / tx;                 // rows a block takes at a time
     const int x = threadIdx.x % tx, y = threadIdx.x / tx;
@@ -93,8 +94,9 @@ struct GluGradParams {
 
 // dg = dh * u * act'(g), du = dh * act(g).  HBM bound: three reads, two writes.
 template <int T, int VEC, int ACT>
-__global__ void __launch_bounds__(kElemThreads) glu_grad_kernel(const GluGradParams p, int tx)
+__global__ void __launch_bounds__(kElemThreads) glu_grad_kernel(const __grid_constant__ GluGradParams p, int tx)
 {
+    wait_for_predecessor();
     const int ty = kElemThreads / tx;
     const int64_t col = ((int64_t)blockIdx.x * tx + threadIdx.x % tx) * VEC;
     if (col >= p.n) return;
@@ -197,6 +199,7 @@ __device__ __forceinline__ void join_job(const JoinJobs::Job& q, float4* sm)
 
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinJobs p)
 {
+    wait_for_predecessor();
     __shared__ float4 sm[256];
     int j = 0;
     while (j + 1 < p.jobs && blockIdx.x >= p.job[j + 1].first) ++j;
@@ -206,16 +209,16 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinJ
 
 // Calls f with the 16-bit type and the activation as constants.
 template <class F>
-void for_type_act(int type, int act, F f)
+gs_status for_type_act(int type, int act, F f)
 {
-    const auto with_type = [&](auto t) {
-        if (act == GS_ACT_SILU) f(t, std::integral_constant<int, GS_ACT_SILU>());
-        else if (act == GS_ACT_GELU) f(t, std::integral_constant<int, GS_ACT_GELU>());
-        else if (act == GS_ACT_RELU) f(t, std::integral_constant<int, GS_ACT_RELU>());
-        else f(t, std::integral_constant<int, GS_ACT_NONE>());
+    const auto with_type = [&](auto t) -> gs_status {
+        if (act == GS_ACT_SILU) return f(t, std::integral_constant<int, GS_ACT_SILU>());
+        if (act == GS_ACT_GELU) return f(t, std::integral_constant<int, GS_ACT_GELU>());
+        if (act == GS_ACT_RELU) return f(t, std::integral_constant<int, GS_ACT_RELU>());
+        return f(t, std::integral_constant<int, GS_ACT_NONE>());
     };
-    if (type == GS_BF16) with_type(std::integral_constant<int, GS_BF16>());
-    else with_type(std::integral_constant<int, GS_F16>());
+    return type == GS_BF16 ? with_type(std::integral_constant<int, GS_BF16>())
+                           : with_type(std::integral_constant<int, GS_F16>());
 }
 
 // Thread columns of an elementwise block: a power of two that covers the row
@@ -275,6 +278,7 @@ struct PackJobs {
 template <typename E>
 __global__ void __launch_bounds__(256) pack_rows_kernel(const __grid_constant__ PackJobs p)
 {
+    wait_for_predecessor();
     constexpr int kPer = 16 / sizeof(E);
     int j = 0;
     while (j + 1 < p.jobs && blockIdx.x >= p.job[j + 1].first) ++j;
@@ -334,10 +338,7 @@ gs_status pack_all(Rows* const* list, int n, char* base, int type, cudaStream_t 
         blocks += (unsigned)(want < most ? want : most);
     }
     if (!blocks) return GS_OK;
-    if (esz == 2) pack_rows_kernel<uint16_t><<<blocks, 256, 0, st>>>(jobs);
-    else pack_rows_kernel<uint8_t><<<blocks, 256, 0, st>>>(jobs);
-    GS_LAUNCH_CHECK();
-    return GS_OK;
+    return launch_after(esz == 2 ? pack_rows_kernel<uint16_t> : pack_rows_kernel<uint8_t>, dim3(blocks), 256, 0, 1, st, jobs);
 }
 
 }  // namespace
@@ -364,9 +365,7 @@ gs_status JoinJobs::add(const float* partial, int64_t parts, int64_t rows, int64
 gs_status JoinJobs::run(cudaStream_t st) const
 {
     if (!jobs) return GS_OK;
-    join_kernel<<<blocks, 256, 0, st>>>(*this);
-    GS_LAUNCH_CHECK();
-    return GS_OK;
+    return launch_after(join_kernel, dim3(blocks), 256, 0, 1, st, *this);
 }
 
 }  // namespace gs
@@ -483,17 +482,14 @@ extern "C" gs_status gs_linear_bwd(const gs_linear_bwd_args* args, void* ws, siz
         const int v = vec ? 8 : 1, tx = thread_cols(n, v);
         const int64_t slabs = slabs_for(m, n, v);
         const dim3 grid((unsigned)((n + (int64_t)tx * v - 1) / ((int64_t)tx * v)), (unsigned)slabs);
-        for_type_act(a.type, a.act, [&](auto t, auto act) {
+        const gs_status launched = for_type_act(a.type, a.act, [&](auto t, auto act) {
             constexpr int T = decltype(t)::value, ACT = decltype(act)::value;
-            if (a.dy_type == a.type) {
-                if (vec) dz_kernel<T, T, 8, ACT><<<grid, kElemThreads, 0, st>>>(p, tx);
-                else dz_kernel<T, T, 1, ACT><<<grid, kElemThreads, 0, st>>>(p, tx);
-            } else {
-                if (vec) dz_kernel<T, kAnyType, 8, ACT><<<grid, kElemThreads, 0, st>>>(p, tx);
-                else dz_kernel<T, kAnyType, 1, ACT><<<grid, kElemThreads, 0, st>>>(p, tx);
-            }
+            const bool same = a.dy_type == a.type;
+            return launch_after(vec ? (same ? dz_kernel<T, T, 8, ACT> : dz_kernel<T, kAnyType, 8, ACT>)
+                                    : (same ? dz_kernel<T, T, 1, ACT> : dz_kernel<T, kAnyType, 1, ACT>),
+                                grid, kElemThreads, 0, 1, st, p, tx);
         });
-        GS_LAUNCH_CHECK();
+        if (launched != GS_OK) return launched;
         if (a.db) {
             const gs_status s = joins.add(p.partial, slabs, 1, n, n, a.db, n, a.db_type);
             if (s != GS_OK) return s;
@@ -642,12 +638,14 @@ extern "C" gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* w
     int64_t gy = (m + 2 * ty - 1) / (2 * ty);
     if (gy > 65535) gy = 65535;
     const dim3 grid((unsigned)((f + (int64_t)tx * v - 1) / ((int64_t)tx * v)), (unsigned)gy);
-    if (!again) for_type_act(a.type, a.act, [&](auto t, auto act) {
-        constexpr int T = decltype(t)::value, ACT = decltype(act)::value;
-        if (vec) glu_grad_kernel<T, 8, ACT><<<grid, kElemThreads, 0, st>>>(p, tx);
-        else glu_grad_kernel<T, 1, ACT><<<grid, kElemThreads, 0, st>>>(p, tx);
-    });
-    GS_LAUNCH_CHECK();
+    if (!again) {
+        const gs_status launched = for_type_act(a.type, a.act, [&](auto t, auto act) {
+            constexpr int T = decltype(t)::value, ACT = decltype(act)::value;
+            return launch_after(vec ? glu_grad_kernel<T, 8, ACT> : glu_grad_kernel<T, 1, ACT>, grid, kElemThreads, 0, 1, st, p,
+                                tx);
+        });
+        if (launched != GS_OK) return launched;
+    }
     cx.a[0] = {p.dg, ldd, true}, cx.a[1] = {p.du, ldd, true};
     cx.b[0] = {wg.p, wg.ld, false}, cx.b[1] = {wu.p, wu.ld, false};
     cw.a[0] = {p.dg, ldd, false}, cw.a[1] = {p.du, ldd, false};

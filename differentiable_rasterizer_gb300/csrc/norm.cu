@@ -54,9 +54,10 @@ __device__ __forceinline__ float group_reduce(float v, int group, float* sm)
 // the lanes share out the rows' scalar work (root, quotients), which otherwise
 // costs every lane as many instructions as the row's elements.
 template <int T, int VEC, int NV, int R, bool NORM>
-__global__ void __launch_bounds__(R > 1 || NV * VEC == 32 ? 256 : 1024) norm_fwd_kernel(gs_rms_norm_args a, int group)
+__global__ void __launch_bounds__(R > 1 || NV * VEC == 32 ? 256 : 1024) norm_fwd_kernel(const __grid_constant__ gs_rms_norm_args a, int group)
 {
     __shared__ float sm[32];
+    wait_for_predecessor();
     const int lane = threadIdx.x % group;
     const int64_t rows_per_block = (int64_t)(blockDim.x / group) * R;
     const int nvec = (int)((a.cols + VEC - 1) / VEC);
@@ -165,10 +166,11 @@ __global__ void __launch_bounds__(R > 1 || NV * VEC == 32 ? 256 : 1024) norm_fwd
 // JoinJobs (linear.cu) adds the blocks' rows in order.
 // R rows a group at a time, their loads in flight together.
 template <int T, int TDY, int VEC, int NV, int R>
-__global__ void __launch_bounds__(R > 1 ? 256 : 1024) norm_bwd_kernel(gs_rms_norm_bwd_args a, int group, float* partial)
+__global__ void __launch_bounds__(R > 1 ? 256 : 1024) norm_bwd_kernel(const __grid_constant__ gs_rms_norm_bwd_args a, int group, float* partial)
 {
     extern __shared__ float part[];   // [groups][columns rounded up] when a block holds several groups
     __shared__ float sm[32];
+    wait_for_predecessor();
     const int lane = threadIdx.x % group;
     const int groups = blockDim.x / group;
     const int nvec = (int)((a.cols + VEC - 1) / VEC);
@@ -310,9 +312,9 @@ gs_status run_fwd(const gs_rms_norm_args& a, cudaStream_t st)
     const int rpb = s.threads / s.group * (two ? 2 : 1);
     const int64_t want = (a.rows + rpb - 1) / rpb, most = (int64_t)sms * (two ? 4 : 2048 / s.threads);
     const int grid = (int)(want < most ? want : most);
-    const auto run = [&](auto t) {
+    const auto run = [&](auto t) -> gs_status {
         constexpr int T = decltype(t)::value;
-#define GS_FWD(V, N, R) norm_fwd_kernel<T, V, N, R, NORM><<<grid, s.threads, 0, st>>>(a, s.group)
+#define GS_FWD(V, N, R) return launch_after(norm_fwd_kernel<T, V, N, R, NORM>, dim3(grid), s.threads, 0, 1, st, a, s.group)
         if (vec) {
             if (two) GS_FWD(8, 1, 2);
             else if (s.nv == 1) GS_FWD(8, 1, 1);
@@ -323,11 +325,9 @@ gs_status run_fwd(const gs_rms_norm_args& a, cudaStream_t st)
         else GS_FWD(1, 16, 1);
 #undef GS_FWD
     };
-    if (a.type == GS_F32) run(Type<GS_F32>());
-    else if (a.type == GS_BF16) run(Type<GS_BF16>());
-    else run(Type<GS_F16>());
-    GS_LAUNCH_CHECK();
-    return GS_OK;
+    if (a.type == GS_F32) return run(Type<GS_F32>());
+    if (a.type == GS_BF16) return run(Type<GS_BF16>());
+    return run(Type<GS_F16>());
 }
 
 }  // namespace
@@ -409,9 +409,9 @@ extern "C" gs_status gs_rms_norm_bwd(const gs_rms_norm_bwd_args* args, void* ws,
     const int grid = (int)(want < blocks ? want : blocks);
     const size_t smem = groups > 1 && a.dweight ? (size_t)groups * s.nv * s.group * v * 4 : 0;   // at most 16 KB
     float* part = (float*)ws;
-    const auto run = [&](auto t, auto tdy) {
+    const auto run = [&](auto t, auto tdy) -> gs_status {
         constexpr int T = decltype(t)::value, TDY = decltype(tdy)::value;
-#define GS_BWD(V, N, R) norm_bwd_kernel<T, TDY, V, N, R><<<grid, s.threads, smem, st>>>(a, s.group, part)
+#define GS_BWD(V, N, R) return launch_after(norm_bwd_kernel<T, TDY, V, N, R>, dim3(grid), s.threads, smem, 1, st, a, s.group, part)
         if (vec) {
             if (two) GS_BWD(8, 1, 2);
             else if (s.nv == 1) GS_BWD(8, 1, 1);
@@ -421,18 +421,16 @@ extern "C" gs_status gs_rms_norm_bwd(const gs_rms_norm_bwd_args* args, void* ws,
         else GS_BWD(1, 16, 1);
 #undef GS_BWD
     };
-    const auto pick = [&](auto t) {
-        if (a.dy_type == a.type) run(t, t);
-        else run(t, Type<kAnyType>());
+    const auto pick = [&](auto t) -> gs_status {
+        if (a.dy_type == a.type) return run(t, t);
+        return run(t, Type<kAnyType>());
     };
-    if (a.type == GS_F32) pick(Type<GS_F32>());
-    else if (a.type == GS_BF16) pick(Type<GS_BF16>());
-    else pick(Type<GS_F16>());
-    GS_LAUNCH_CHECK();
+    gs_status status = a.type == GS_F32 ? pick(Type<GS_F32>()) : (a.type == GS_BF16 ? pick(Type<GS_BF16>()) : pick(Type<GS_F16>()));
+    if (status != GS_OK) return status;
     JoinJobs joins;
     if (a.dweight) {
-        const gs_status s = joins.add(part, grid, 1, a.cols, a.cols, a.dweight, a.cols, a.weight_type);
-        if (s != GS_OK) return s;
+        status = joins.add(part, grid, 1, a.cols, a.cols, a.dweight, a.cols, a.weight_type);
+        if (status != GS_OK) return status;
     }
     return joins.run(st);
 }
