@@ -1,7 +1,8 @@
 """Builds libgs_gb300.so (the C-ABI CUDA library) in-tree for sm_103a, and its
 bounds-checked twin libgs_gb300_checked.so (the same sources with -DGS_CHECKED:
 every index read from memory is tested before use, failures are counted and
-the access skipped, gs_check_report returns the count).
+the access skipped, gs_check_report returns the count).  Also the Python extension
+module that calls the decoder layers on torch tensors (layers_torch.cpp, g++).
 
 Each translation unit of both libraries is compiled by nvcc in parallel, then
 each library is linked with the shared CUDA runtime.  Forward-decision code
@@ -31,6 +32,10 @@ SOURCES = ["abi.cu", "project.cu", "binsort.cu", "prune.cu", "raster.cu", "dssim
            "norm.cu", "linear.cu", "gemm.cu"]
 HEADERS = ["gs_common.cuh", "project_math.cuh", "scan.cuh", "layers_common.cuh", "gemm.cuh", "tc_common.cuh"]
 
+# The layers on torch tensors: a Python extension module against the installed torch's headers.
+TORCH_SRC = os.path.join(CSRC, "layers_torch.cpp")
+TORCH_MODULE = os.path.join(OUT_DIR, "_layers_torch.so")
+
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-fmad=false", "-prec-div=true", "-prec-sqrt=true", "-ftz=false",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "-I", os.path.join(ROOT, "include")]
@@ -48,8 +53,21 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch_module_command(out):
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{i}" for i in inc], TORCH_SRC, "-o", out,
+            "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+
+
 def build(verbose: bool = False, force: bool = False) -> str:
-    """Build both libraries (only what is stale); returns the plain library's path."""
+    """Build both libraries and the torch module (only what is stale); returns the plain library's path."""
     nvcc = _nvcc()
     hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(ROOT, "include", "gs.h")]
     jobs, links = [], []
@@ -68,6 +86,11 @@ def build(verbose: bool = False, force: bool = False) -> str:
                 fresh = True
         links.append((lib, objs, fresh))
 
+    tmp_module = TORCH_MODULE + ".tmp%d" % os.getpid()
+    torch_stale = force or _stale(TORCH_MODULE, [TORCH_SRC, os.path.join(ROOT, "include", "gs.h")])
+    if torch_stale:
+        jobs.insert(0, _torch_module_command(tmp_module))   # the longest of the jobs
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
@@ -78,7 +101,9 @@ def build(verbose: bool = False, force: bool = False) -> str:
             if verbose or r.returncode != 0:
                 sys.stderr.write(r.stdout + r.stderr)
             if r.returncode != 0:
-                raise RuntimeError("nvcc failed: " + " ".join(cmd))
+                raise RuntimeError("compiler failed: " + " ".join(cmd))
+    if torch_stale:
+        os.replace(tmp_module, TORCH_MODULE)
     for lib, objs, fresh in links:
         if force or fresh or _stale(lib, objs):
             tmp = lib + ".tmp%d" % os.getpid()

@@ -79,10 +79,6 @@ gs_status launch_after(void (*kernel)(P...), dim3 grid, unsigned block, size_t s
 }
 
 // ------------------------------------------------------------------ elements
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-
 __device__ __forceinline__ float load_elem(const void* p, int64_t i, int type)
 {
     if (type == GS_F32) return ((const float*)p)[i];

@@ -633,3 +633,43 @@ def test_graph_capture(layers):
     assert torch.equal(oc.y, o.y)
     for a, b in zip(gc, ref):
         assert torch.equal(a, b)
+
+
+def test_refusals(layers):
+    """What the torch layer cannot take, named; the device stays usable."""
+    from differentiable_rasterizer_gb300 import abi
+    z = lambda *s, dt=BF: torch.zeros(s, dtype=dt, device="cuda")   # noqa: E731
+    x, w, b = z(6, 16), z(8, 16), z(8)
+    lin, back = layers.linear, layers.linear_backward
+    cases = [
+        ("expected BFloat16", lambda: lin(x, w.half())), ("expected", lambda: lin(x.float(), w)),
+        ("expected", lambda: lin(x.to(torch.int32), w)), ("columns", lambda: lin(x, z(8, 15))),
+        ("on cpu", lambda: lin(x, w.cpu())), ("not contiguous", lambda: lin(z(16, 6).t(), w)),
+        ("overlap", lambda: lin(z(16).expand(6, 16), w)), ("do not merge", lambda: lin(z(2, 3, 16).transpose(0, 1), w)),
+        ("one dimension", lambda: lin(z(), w)), ("contiguous values", lambda: lin(x, w, z(16)[::2])),
+        ("contiguous values", lambda: lin(x, w, z(9))), ("rows, expected", lambda: lin(x, w, residual=z(5, 8))),
+        ("expected", lambda: lin(x, w, residual=z(6, 8), out_dtype=F32)), ("out_dtype", lambda: lin(x, w, out_dtype=E4)),
+        ("torch.dtype", lambda: lin(x, w, out_dtype="bfloat16")), ("rows, expected", lambda: lin(x, w, out=z(7, 8))),
+        ("8-bit", lambda: lin(x.to(E4), w.to(E4), act="silu", need_backward=True)),
+        ("x_scale", lambda: lin(x.to(E4), w.to(E4), x_scale=z(5, dt=F32))), ("x_scale", lambda: lin(x, w, x_scale=z(6))),
+        ("z: required", lambda: back(z(6, 8), x, w, act="silu")), ("dw_dtype", lambda: back(z(6, 8), x, w, dw_dtype=HF)),
+        ("db_dtype", lambda: back(z(6, 8), x, w, db_dtype=E4)), ("columns", lambda: back(z(6, 9), x, w)),
+        ("rows, expected", lambda: layers.glu(x, w, z(9, 16))), ("out_dtype", lambda: layers.glu(x, w, w, out_dtype=HF)),
+        ("8-bit", lambda: layers.glu(x.to(E4), w.to(E4), w.to(E4), need_backward=True)),
+        ("u: expected a tensor", lambda: layers.glu_backward(z(6, 8), x, w, w, z(6, 8))),
+        ("weight: required", lambda: layers.rms_norm(x, None)), ("contiguous values", lambda: layers.rms_norm(x, z(15))),
+        ("residual", lambda: layers.rms_norm(x, z(16), residual=x.float())),
+        ("rstd", lambda: layers.rms_norm_backward(x, x, z(16), None)),
+        ("expected", lambda: layers.quantize_rows(x.to(E4))),
+    ]
+    for what, call in cases:
+        with pytest.raises(ValueError, match=what):
+            call()
+    with pytest.raises(abi.GsError) as e:   # the library's own refusals: scales without 8-bit operands, too wide rows
+        lin(x, w, x_scale=z(6, dt=F32))
+    assert e.value.status == abi.GS_ERR_INVALID_ARG
+    with pytest.raises(abi.GsError):
+        layers.rms_norm(z(1, 16385), z(16385))
+    with pytest.raises(abi.GsError):
+        layers.rms_norm(x, z(16), eps=-1.0)
+    assert (lin(x, w, b).y == 0).all()

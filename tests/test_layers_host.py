@@ -103,28 +103,24 @@ def test_zero_rows_do_no_device_work(abi):
     assert abi.gs_glu(_pack(abi, "gs_glu", dict(GLU, rows=0, x=0, h=0)), None, None, None) is None
 
 
-def test_tensor_refusals():
+def test_tensor_refusals(abi):
     from differentiable_rasterizer_gb300 import layers
     x, w = torch.zeros((2, 8), dtype=torch.bfloat16), torch.zeros((4, 8), dtype=torch.bfloat16)
     for call in (lambda: layers.linear(x, w), lambda: layers.glu(x, w, w), lambda: layers.rms_norm(x, w[0]),
                  lambda: layers.quantize_rows(x), lambda: layers.linear_backward(x, x, w),
-                 lambda: layers.linear(None, w)):
+                 lambda: layers.glu_backward(x, x, w, w), lambda: layers.rms_norm_backward(x, x, w[0], w[0])):
         with pytest.raises(ValueError, match="CUDA tensor"):
             call()
-    dev = -1   # the index of a CPU tensor's device
-    with pytest.raises(ValueError, match="overlap"):
-        layers._matrix(torch.zeros(8).expand(3, 8), "t", (torch.float32,), dev)
-    with pytest.raises(ValueError, match="not contiguous"):
-        layers._matrix(torch.zeros(8, 4).t(), "t", (torch.float32,), dev)
-    with pytest.raises(ValueError, match="do not merge"):
-        layers._matrix(torch.zeros(2, 3, 4).transpose(0, 1), "t", (torch.float32,), dev)
-    with pytest.raises(ValueError, match="columns"):
-        layers._matrix(torch.zeros(2, 3), "t", (torch.float32,), dev, cols=4)
-    with pytest.raises(ValueError, match="rows"):
-        layers._matrix(torch.zeros(2, 3), "t", (torch.float32,), dev, rows=4)
-    with pytest.raises(ValueError, match="expected a tensor"):
-        layers._matrix(torch.zeros(2, 3, dtype=torch.int32), "t", (torch.float32,), dev)
-    with pytest.raises(ValueError, match="contiguous values"):
-        layers._vector(torch.zeros(8)[::2], "t", (torch.float32,), dev, 4)
+    with pytest.raises(ValueError, match="expected a tensor, got NoneType"):
+        layers.linear(None, w)
+    with pytest.raises(ValueError, match="expected a tensor, got list"):
+        layers.rms_norm([1.0], w[0])
     with pytest.raises(ValueError, match="not one of"):
-        layers._act("tanh")
+        layers.linear(x, w, act="tanh")
+
+
+def test_missing_module_raises(abi, tmp_path, monkeypatch):
+    from differentiable_rasterizer_gb300 import layers
+    monkeypatch.setattr(abi, "LIB_PATH", str(tmp_path / "missing.so"))
+    with pytest.raises(RuntimeError, match="layer module missing"):
+        layers._Native().linear
