@@ -1032,14 +1032,19 @@ gs_status allow_smem(K* kernel, int bytes, std::atomic<uint64_t>& done)
 struct Tile {
     int bn;
     bool pair;
-    double per_kb;   // cycles a k-block (128 bytes of k) takes, measured
+    double per_kb;   // cycles a k-block (128 bytes of k) takes
+    double per_clk;  // bytes a cycle its epilogue moves
 };
 // An SM takes in 64 bytes a cycle: 24, 32, 24 and 32 KB a k-block, against 128, 256,
 // 256 and 512 cycles of products.  So the wide pair alone keeps the tensor cores fed.
-constexpr Tile kTiles[4] = {{64, false, 400}, {128, false, 480}, {128, true, 420}, {256, true, 590}};
+// These rates and the cycles below are fitted to the times of all four shapes at 44
+// sizes (500 to 1,000,000 rows, k 64 to 4096, plain, with activation, gated, 8 bits,
+// gradients): the choice is within 6 % of the best shape, 20 % at 5 us (100,000 x 256 ->
+// 1024: 61 us with the narrow pair, 54 with the wide one).
+constexpr Tile kTiles[4] = {{64, false, 450, 22}, {128, false, 440, 21}, {128, true, 430, 19}, {256, true, 690, 21}};
 
 // Cycles of a call with a tile shape: waves of tiles, each bound by its k-blocks or by
-// its epilogue's arithmetic and traffic (14 to 22 bytes a cycle and SM), and a start-up.
+// its epilogue's arithmetic and traffic, and a start-up.
 double cost(const GemmCall& c, const Tile& t, int sms, GemmPlan* out)
 {
     GemmPlan& p = *out;
@@ -1061,19 +1066,20 @@ double cost(const GemmCall& c, const Tile& t, int sms, GemmPlan* out)
     const bool sum_only = !glu && !c.bias && !c.residual && !c.z && c.act == GS_ACT_NONE &&
                           !c.x_scale && !c.w_scale[0];
     const double live = (double)(c.n < p.out_cols ? c.n : p.out_cols);
-    // a plain sum's plan, and so its order, does not depend on the type it is rounded to
-    const int bytes = (sum_only ? 4 : type_bytes(c.out_type)) * (c.residual ? 2 : 1) + (c.z ? (glu ? 4 : 2) : 0);
+    // the weights' gradients: a plan, and so an order, that does not depend on the type they are rounded to
+    const int bytes = (c.a[0].k_fast ? type_bytes(c.out_type) : 4) * (c.residual ? 2 : 1) + (c.z ? (glu ? 4 : 2) : 0);
+    const double per_value = glu ? 0.13 : (c.act != GS_ACT_NONE ? 0.17 : (c.type == GS_E4M3 ? 0.04 : 0.02));
     double best = 0;
     int64_t most = sum_only ? slots / tiles : 1;
     if (most > kb / 4) most = kb / 4;
     if (most < 1) most = 1;
     for (int64_t s = 1; s <= most; s = s == most ? most + 1 : (s + s / 2 + 1 < most ? s + s / 2 + 1 : most)) {
         const double main = t.per_kb * (double)((kb + s - 1) / s);
-        const double epi = 300 + 128.0 * live * ((glu ? 0.14 : 0.02) + (s > 1 ? 4 : bytes) / (t.bn == 256 ? 14.0 : 22.0));
+        const double epi = 650 + 128.0 * live * (per_value + (s > 1 ? 4 : bytes) / t.per_clk);
         const double waves = (double)((tiles * s + slots - 1) / slots);
         // the join: a launch, and every partial sum read once at about 20 bytes a cycle and SM
         const double join = s > 1 ? 4500 + (double)s * c.m * c.n * p.probs * 4 / (sms * 20.0) : 0;
-        const double v = 3000 + waves * (main > epi ? main : epi) + (main > epi ? epi : main) + join;
+        const double v = 5700 + waves * (main > epi ? main : epi) + (main > epi ? epi : main) + join;
         if (s == 1 || v < best) {
             best = v;
             p.splits = (int)s;
