@@ -128,17 +128,6 @@ __device__ __forceinline__ uint32_t slot_piece(int r, int j)
     return ROW == 128 ? r * 128 + ((j ^ (r & 7)) << 4) : r * 64 + ((j ^ ((r >> 1) & 3)) << 4);
 }
 
-__device__ __forceinline__ void st_shared16(uint32_t a, uint4 v)
-{
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-__device__ __forceinline__ uint4 ld_shared16(uint32_t a)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-    return v;
-}
-
 __device__ __forceinline__ uint16_t ld_shared_u16(uint32_t a)
 {
     uint16_t v;
@@ -487,21 +476,8 @@ __device__ __forceinline__ void stage_rows(uint32_t slot, const uint16_t* base, 
     for (int i = 0; i < 32 / kRows; ++i) st_shared16(slot + slot_piece<ROW>(r0 + i * kRows, j), q[i]);
 }
 
-// 16 columns of the gated layer's gradient: dg = dh u act'(g), du = dh act(g).
-template <int ACT>
-__device__ __forceinline__ void glu_gradient(float (&g)[16], float (&u)[16], const float (&dh)[16])
-{
-#pragma unroll
-    for (int j = 0; j < 16; j += 2) {
-        uint64_t value, slope;
-        act_both2<ACT>(pair(g[j], g[j + 1]), value, slope);
-        const uint64_t d = pair(dh[j], dh[j + 1]);
-        const float2 a = unpair(mul2(mul2(d, pair(u[j], u[j + 1])), slope)), b = unpair(mul2(d, value));
-        g[j] = a.x, g[j + 1] = a.y;
-        u[j] = b.x, u[j + 1] = b.y;
-    }
-}
-__device__ __forceinline__ void glu_gradient(float (&g)[16], float (&u)[16], const float (&dh)[16], int act)
+// The activation at run time.
+__device__ __forceinline__ void glu_gradient_by(float (&g)[16], float (&u)[16], const float (&dh)[16], int act)
 {
     if (act == GS_ACT_SILU) glu_gradient<GS_ACT_SILU>(g, u, dh);
     else if (act == GS_ACT_GELU) glu_gradient<GS_ACT_GELU>(g, u, dh);
@@ -727,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                         tmem_ld_wait(up);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) g[e] = __uint_as_float(raw[e]), u[e] = __uint_as_float(up[e]);
-                        glu_gradient(g, u, v, p.act);
+                        glu_gradient_by(g, u, v, p.act);
                         if (p.out_type == GS_BF16) {
                             slot_put_half<GS_BF16>(mine, s, g);
                             slot_put_half<GS_BF16>(mine ^ (kHalf << 4), s, u);
@@ -1015,19 +991,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
 }
 
 // ------------------------------------------------------------------ host
-// Sets a kernel's shared memory once on each device.
-template <class K>
-gs_status allow_smem(K* kernel, int bytes, std::atomic<uint64_t>& done)
-{
-    int dev = 0;
-    GS_CUDA_TRY(cudaGetDevice(&dev));
-    const uint64_t bit = 1ull << (dev & 63);
-    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return GS_OK;
-    GS_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
-    if (dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
-    return GS_OK;
-}
-
 // Tile shapes: B's columns and whether two SMs share a tile.
 struct Tile {
     int bn;
@@ -1307,11 +1270,14 @@ extern "C" gs_status gs_wait_report(int32_t* expired)
     GS_NVTX_RANGE("gs_wait_report");
     if (!expired) return GS_ERR_INVALID_ARG;
     *expired = 0;
-    int v = 0;
+    int v = 0, narrow = 0;
     const int zero = 0;
     GS_CUDA_TRY(cudaDeviceSynchronize());
     GS_CUDA_TRY(cudaMemcpyFromSymbol(&v, g_wait_expired, sizeof v));
     if (v) GS_CUDA_TRY(cudaMemcpyToSymbol(g_wait_expired, &zero, sizeof zero));
+    const gs_status s = glu_narrow_wait_report(&narrow);
+    if (s != GS_OK) return s;
+    v |= narrow;
     *expired = v;
     return v ? GS_ERR_TIMEOUT : GS_OK;
 }

@@ -81,4 +81,23 @@ struct JoinJobs {
 // The partial sums of a call whose plan splits k are joined by `joins`, run later.
 gs_status gemm_run(const GemmCall& c, const GemmPlan& plan, void* ws, JoinJobs* joins, cudaStream_t st);
 
+// The gradients of a narrow gated layer (glu_narrow.cu), from x, dh and the weights: rows
+// of 16-byte base and pitch but for dx, which may be NULL; dw: NULL, or glu_narrow_blocks
+// partial sums [hidden][pitch] each.
+struct GluNarrowCall {
+    int64_t rows, features, hidden;
+    int type, act;
+    const void *x, *dh, *w_gate, *w_up;
+    int64_t ldx, lddh, ldwg, ldwu;
+    void* dx;
+    int64_t lddx;
+    float *dw_gate, *dw_up;
+    int64_t pitch;
+};
+bool glu_narrow_fits(int64_t features, int64_t hidden);
+int64_t glu_narrow_blocks(int64_t rows);
+gs_status glu_narrow_grad(const GluNarrowCall& c, cudaStream_t st);
+// Whether a wait of that kernel ran out; clears the mark.  The device is idle.
+gs_status glu_narrow_wait_report(int* expired);
+
 }  // namespace gs

@@ -1,0 +1,352 @@
+// glu_narrow.cu -- gradients of a narrow gated layer in one pass over its rows.
+//
+//   g = x Wg^T, u = x Wu^T            (computed again: features are few)
+//   dg = dh u act'(g), du = dh act(g) (rounded to 16 bits, factors of the products below)
+//   dx = dg Wg + du Wu,  dWg = dg^T x, dWu = du^T x
+//
+// for at most 64 features and 128 hidden columns (a per-Gaussian decoder's layer), where
+// both weights, a tile of 128 rows with its dg and du, and all accumulators fit on one SM:
+// only x and dh are read and dx is written, 2 (2 features + hidden) bytes a row.  As three
+// products dg and du cross HBM three times (1,000,000 x 64 -> 128: 1.5 GB of 2.0): 160 us
+// against 411 there, 26 against 56 for 100,000 rows, 10 against 15.5 for one.
+//
+// A persistent CTA an SM, 18 warps: a TMA producer, an MMA issuer, 16 epilogue warps.
+// TMEM, fp32: two buffers of 64 gate and 64 up columns (a half of the hidden columns
+// each, refilled while the other is read), dx, and dWg and dWu, which stay for all of the
+// CTA's rows and end as its partial sum.  dg takes dh's place in shared memory; the same
+// tiles are k-fast factors of dx and k-slow factors of the weights' gradients, and the
+// weights are k-fast for g and u and k-slow for dx.
+#include <atomic>
+
+#include "gemm.cuh"
+#include "tc_common.cuh"
+
+namespace gs {
+namespace {
+
+using namespace tc;
+
+constexpr int kWarps = 18, kThreads = kWarps * 32, kEpiWarps = 16;
+constexpr int kTileRows = 128, kHalf = 64;             // rows of a tile; hidden columns of a half
+constexpr uint32_t kBox = kTileRows * 128;             // bytes of 128 rows of 64 columns
+constexpr uint32_t kWeights = 2 * kBox;                // per half: 64 rows of Wg, 64 of Wu
+constexpr uint32_t kAtDg = kBox, kAtDu = 3 * kBox;     // in a stage: x, dh (then dg) of both halves, du of both
+constexpr uint32_t kStage = 5 * kBox;
+constexpr int kStages = 2;
+constexpr uint32_t kTmemDx = 256, kTmemDw = 320, kTmemCols = 512;   // columns: dx; dWg, dWu
+
+enum Bar { kWFull = 0, kFull = 1, kEmpty = 3, kGuFull = 5, kGuFree = 7, kGradFull = 9, kDxFull = 11, kDxFree, kDone, kDrain, kBars };
+constexpr int kSmem = kWeights + kStages * kStage + ((kBars * 8 + 15) & ~15) + 16;
+static_assert(kSmem <= 232448, "shared memory of an SM");
+
+struct Params {
+    CUtensorMap x, dh, wg, wu;
+    void* dx;          // NULL: not asked for
+    float* dw[2];      // NULL, or a partial sum [hidden][pitch] a CTA
+    int64_t lddx;
+    uint32_t m, tiles, idesc_gu, idesc_dx, idesc_dw;
+    int features, hidden, pitch, dx_vec;
+};
+
+__device__ int g_narrow_wait_expired;
+
+__device__ __forceinline__ void prefetch_2d(const CUtensorMap* map, int x, int y)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
+}
+
+// Stage addresses and phases of the CTA's i-th tile.
+__device__ __forceinline__ uint32_t stage_at(uint32_t stages, uint32_t i) { return stages + (i & 1) * kStage; }
+
+__device__ __forceinline__ void load_rows(const Params& p, uint32_t weights, uint32_t stages, uint32_t bars, volatile int* gave_up)
+{
+    const int halves = p.hidden > kHalf ? 2 : 1;
+    mbar_expect(bars + 8 * kWFull, halves * kBox);
+    for (int h = 0; h < halves; ++h) {
+        tma_load_2d<false>(weights + h * kBox, &p.wg, 0, h * kHalf, bars + 8 * kWFull);
+        tma_load_2d<false>(weights + h * kBox + kBox / 2, &p.wu, 0, h * kHalf, bars + 8 * kWFull);
+    }
+    uint32_t i = 0;
+    for (uint32_t t = blockIdx.x; t < p.tiles; t += gridDim.x, ++i) {
+        if (!mbar_wait(bars + 8 * (kEmpty + (i & 1)), ((i >> 1) & 1) ^ 1, gave_up)) break;
+        const uint32_t full = bars + 8 * (kFull + (i & 1)), at = stage_at(stages, i);
+        mbar_expect(full, (1 + halves) * kBox);
+        tma_load_2d<false>(at, &p.x, 0, (int)(t * kTileRows), full);
+        for (int h = 0; h < halves; ++h) tma_load_2d<false>(at + kAtDg + h * kBox, &p.dh, h * kHalf, (int)(t * kTileRows), full);
+        // a stage is empty for a short time only: the tile after the next is on its way into L2 by then
+        const uint64_t ahead = (uint64_t)t + 2ull * gridDim.x;
+        if (ahead < p.tiles) {
+            prefetch_2d(&p.x, 0, (int)(ahead * kTileRows));
+            for (int h = 0; h < halves; ++h) prefetch_2d(&p.dh, h * kHalf, (int)(ahead * kTileRows));
+        }
+    }
+    // the block does not leave before its copies have landed
+    volatile int still = 0;
+    mbar_wait(bars + 8 * kWFull, 0, &still);
+    for (uint32_t j = i > kStages ? i - kStages : 0; j < i; ++j) mbar_wait(bars + 8 * (kFull + (j & 1)), (j >> 1) & 1, &still);
+}
+
+__device__ __forceinline__ void issue_products(const Params& p, uint32_t weights, uint32_t stages, uint32_t bars, uint32_t tmem,
+                                               volatile int* gave_up)
+{
+    const uint32_t halves = p.hidden > kHalf ? 2 : 1, steps_x = (uint32_t)(p.features + 15) / 16;
+    uint32_t unit = 0;
+    const auto gate_up = [&](uint32_t i, uint32_t h) -> bool {
+        const uint32_t b = unit & 1;
+        if (!mbar_wait(bars + 8 * (kGuFree + b), ((unit >> 1) & 1) ^ 1, gave_up)) return false;
+        tc_fence_after();
+        const uint32_t x = desc_lo(stage_at(stages, i), true), w = desc_lo(weights + h * kBox, true);
+        for (uint32_t j = 0; j < steps_x; ++j)
+            mma<false, false>(tmem + b * 128, x + j * k_step(true), kDescHi, w + j * k_step(true), kDescHi, p.idesc_gu, j > 0);
+        mma_commit<false>(bars + 8 * (kGuFull + b));
+        ++unit;
+        return true;
+    };
+    if (!mbar_wait(bars + 8 * kWFull, 0, gave_up) || !mbar_wait(bars + 8 * kFull, 0, gave_up)) return;
+    tc_fence_after();
+    for (uint32_t h = 0; h < halves; ++h)
+        if (!gate_up(0, h)) return;
+    uint32_t i = 0;
+    for (uint32_t t = blockIdx.x; t < p.tiles; t += gridDim.x, ++i) {
+        if ((uint64_t)t + gridDim.x < p.tiles) {   // the next tile's g and u, as their buffers are read
+            if (!mbar_wait(bars + 8 * (kFull + ((i + 1) & 1)), ((i + 1) >> 1) & 1, gave_up)) return;
+            tc_fence_after();
+            for (uint32_t h = 0; h < halves; ++h)
+                if (!gate_up(i + 1, h)) return;
+        }
+        if (!mbar_wait(bars + 8 * (kGradFull + (i & 1)), (i >> 1) & 1, gave_up)) return;
+        tc_fence_after();
+        const uint32_t at = stage_at(stages, i);
+        if (p.dx) {
+            if (!mbar_wait(bars + 8 * kDxFree, (i & 1) ^ 1, gave_up)) return;
+            tc_fence_after();
+            uint32_t add = 0;
+            for (uint32_t h = 0; h < halves; ++h)
+                for (uint32_t w = 0; w < 2; ++w) {   // dg Wg, du Wu
+                    const uint32_t a = desc_lo(at + (w ? kAtDu : kAtDg) + h * kBox, true);
+                    const uint32_t b = desc_lo(weights + h * kBox + w * (kBox / 2), false);
+#pragma unroll
+                    for (uint32_t j = 0; j < 4; ++j, add = 1)
+                        mma<false, false>(tmem + kTmemDx, a + j * k_step(true), kDescHi, b + j * k_step(false), kDescHi,
+                                          p.idesc_dx, add);
+                }
+            mma_commit<false>(bars + 8 * kDxFull);
+        }
+        if (p.dw[0]) {
+            const uint32_t b = desc_lo(at, false);
+            for (uint32_t w = 0; w < 2; ++w) {
+                // k is the row: 64 columns a group, the next group a box on
+                const uint32_t a = ((at + (w ? kAtDu : kAtDg)) >> 4) | ((kBox >> 4) << 16);
+#pragma unroll
+                for (uint32_t j = 0; j < kTileRows / 16; ++j)
+                    mma<false, false>(tmem + kTmemDw + w * 64, a + j * k_step(false), kDescHi, b + j * k_step(false), kDescHi,
+                                      p.idesc_dw, i > 0 || j > 0);
+            }
+        }
+        mma_commit<false>(bars + 8 * (kEmpty + (i & 1)));
+    }
+    mma_commit<false>(bars + 8 * kDone);
+}
+
+// 16 columns of dx of the CTA's i-th tile to memory: a thread has its row's 32 bytes.
+template <int T>
+__device__ __forceinline__ bool store_dx(const Params& p, uint32_t i, uint32_t row, int col, uint32_t tmem, uint32_t bars, int lane,
+                                         volatile int* gave_up)
+{
+    if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * kDxFull, i & 1, gave_up))) return false;
+    tc_fence_after();
+    uint32_t v[16];
+    tmem_ld16(tmem + kTmemDx + col, v);
+    tmem_ld_wait(v);
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + 8 * kDxFree);
+    const int left = row < p.m ? p.features - col : 0;
+    uint16_t* to = (uint16_t*)p.dx + (int64_t)row * p.lddx + col;
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = pack_half2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]), T);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        if (p.dx_vec && left >= 8 * e + 8) *reinterpret_cast<uint4*>(to + 8 * e) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+        else
+#pragma unroll
+            for (int j = 8 * e; j < 8 * e + 8; ++j)
+                if (j < left) to[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+    }
+    return true;
+}
+
+template <int T, int ACT>
+__global__ void __launch_bounds__(kThreads, 1) glu_narrow_kernel(const __grid_constant__ Params p)
+{
+    extern __shared__ __align__(1024) char smem_raw[];
+    const uint32_t weights = smem_addr(smem_raw);
+    if (weights & 1023u) {   // every thread sees the same address; there is no padding to move within
+        g_narrow_wait_expired = 1;
+        return;
+    }
+    const uint32_t stages = weights + kWeights, bars = stages + kStages * kStage;
+    char* tail = smem_raw + (bars - weights) + ((kBars * 8 + 15) & ~15);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail);
+    volatile int* gave_up = reinterpret_cast<volatile int*>(tail + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kBars; ++i) {
+            const bool warps = i == kGuFree || i == kGuFree + 1 || i == kGradFull || i == kGradFull + 1 || i == kDxFree;
+            mbar_init(bars + 8 * i, warps ? kEpiWarps : 1);
+        }
+        *gave_up = 0;
+        mbar_init_fence();
+    }
+    if (warp == 1) tmem_alloc<false>(smem_addr(tmem_slot), kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    wait_for_predecessor();
+
+    if (warp == 0) {
+        if (elect_one()) load_rows(p, weights, stages, bars, gave_up);
+    } else if (warp == 1) {
+        if (elect_one()) {
+            issue_products(p, weights, stages, bars, tmem, gave_up);
+            if (*gave_up) {
+                volatile int still = 0;
+                mma_commit<false>(bars + 8 * kDrain);
+                mbar_wait(bars + 8 * kDrain, 0, &still);
+            }
+        }
+    } else {
+        const int quarter = warp & 3, col = ((warp - 2) >> 2) * 16;   // 32 rows, 16 columns of a half
+        const uint32_t row = quarter * 32 + lane, mine = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t piece = row * 128 + (((uint32_t)(col >> 3) ^ (row & 7)) << 4);   // its columns' first 16 bytes in a box
+        const int halves = p.hidden > kHalf ? 2 : 1;
+        uint32_t unit = 0, i = 0;
+        bool ok = true;
+        for (uint32_t t = blockIdx.x; ok && t < p.tiles; t += gridDim.x, ++i) {
+            const uint32_t at = stage_at(stages, i) + kAtDg + piece;
+            ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (kFull + (i & 1)), (i >> 1) & 1, gave_up));
+#pragma unroll 1
+            for (int h = 0; ok && h < halves; ++h, ++unit) {
+                const uint32_t b = unit & 1;
+                ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (kGuFull + b), (unit >> 1) & 1, gave_up));
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t raw[16], up[16];
+                tmem_ld16(mine + b * 128 + col, raw);
+                tmem_ld16(mine + b * 128 + 64 + col, up);
+                const uint32_t a = at + h * kBox;
+                const uint4 d0 = ld_shared16(a), d1 = ld_shared16(a ^ 16);
+                tmem_ld_wait(raw);
+                tmem_ld_wait(up);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars + 8 * (kGuFree + b));
+                const uint32_t dh[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+                float g[16], u[16], d[16];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float2 f = unpack_half2(dh[e], T);
+                    d[2 * e] = f.x, d[2 * e + 1] = f.y;
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) g[e] = __uint_as_float(raw[e]), u[e] = __uint_as_float(up[e]);
+                glu_gradient<ACT>(g, u, d);
+                const int left = p.hidden - h * kHalf - col;
+                if (left < 16) {   // beyond the layer: zeros, though an infinite x times no weight were none
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (e >= left) g[e] = u[e] = 0.0f;
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    st_shared16(a ^ (e << 4), make_uint4(pack_half2(g[8 * e], g[8 * e + 1], T), pack_half2(g[8 * e + 2], g[8 * e + 3], T),
+                                                         pack_half2(g[8 * e + 4], g[8 * e + 5], T), pack_half2(g[8 * e + 6], g[8 * e + 7], T)));
+                    st_shared16((a ^ (e << 4)) + (kAtDu - kAtDg),
+                                make_uint4(pack_half2(u[8 * e], u[8 * e + 1], T), pack_half2(u[8 * e + 2], u[8 * e + 3], T),
+                                           pack_half2(u[8 * e + 4], u[8 * e + 5], T), pack_half2(u[8 * e + 6], u[8 * e + 7], T)));
+                }
+                if (h == halves - 1) {
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the products read what was just written
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bars + 8 * (kGradFull + (i & 1)));
+                }
+                // the dx of the tile before is ready by now
+                if (h == 0 && i > 0 && p.dx) ok = store_dx<T>(p, i - 1, (t - gridDim.x) * kTileRows + row, col, mine, bars, lane, gave_up);
+            }
+        }
+        if (ok && p.dx) ok = store_dx<T>(p, i - 1, (blockIdx.x + (i - 1) * gridDim.x) * kTileRows + row, col, mine, bars, lane, gave_up);
+        if (ok && p.dw[0] && __all_sync(0xffffffffu, mbar_wait(bars + 8 * kDone, 0, gave_up))) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int w = 0; w < 2; ++w) {
+                uint32_t v[16];
+                tmem_ld16(mine + kTmemDw + w * 64 + col, v);
+                tmem_ld_wait(v);
+                float* to = p.dw[w] + ((int64_t)blockIdx.x * p.hidden + row) * p.pitch + col;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if ((int)row < p.hidden && col + 4 * e < p.pitch)
+                        *reinterpret_cast<uint4*>(to + 4 * e) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            }
+            tc_fence_before();
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && *gave_up) atomicExch(&g_narrow_wait_expired, 1);
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_free<false>(tmem, kTmemCols);
+    }
+}
+
+template <int T, int ACT>
+gs_status launch(const Params& p, unsigned grid, cudaStream_t st)
+{
+    static std::atomic<uint64_t> done{0};
+    const gs_status s = allow_smem(glu_narrow_kernel<T, ACT>, kSmem, done);
+    if (s != GS_OK) return s;
+    return launch_after(glu_narrow_kernel<T, ACT>, dim3(grid), kThreads, kSmem, 1, st, p);
+}
+
+}  // namespace
+
+bool glu_narrow_fits(int64_t features, int64_t hidden) { return features <= 64 && hidden <= 2 * kHalf; }
+
+int64_t glu_narrow_blocks(int64_t rows)
+{
+    const int64_t tiles = (rows + kTileRows - 1) / kTileRows, sms = device_sms() > 0 ? device_sms() : 152;
+    return tiles < sms ? tiles : sms;
+}
+
+gs_status glu_narrow_grad(const GluNarrowCall& c, cudaStream_t st)
+{
+    if (c.rows > 0x7fffff00ll) return GS_ERR_INVALID_ARG;
+    Params p = {};
+    gs_status s = make_map(&p.x, c.x, c.type, c.rows, c.features, c.ldx, kTileRows, kHalf);
+    if (s == GS_OK) s = make_map(&p.dh, c.dh, c.type, c.rows, c.hidden, c.lddh, kTileRows, kHalf);
+    if (s == GS_OK) s = make_map(&p.wg, c.w_gate, c.type, c.hidden, c.features, c.ldwg, kHalf, kHalf);
+    if (s == GS_OK) s = make_map(&p.wu, c.w_up, c.type, c.hidden, c.features, c.ldwu, kHalf, kHalf);
+    if (s != GS_OK) return s;
+    p.dx = c.dx, p.lddx = c.lddx, p.dx_vec = c.dx && rows16(c.dx, c.lddx, c.type);
+    p.dw[0] = c.dw_gate, p.dw[1] = c.dw_up, p.pitch = (int)c.pitch;
+    p.m = (uint32_t)c.rows, p.tiles = (uint32_t)((c.rows + kTileRows - 1) / kTileRows);
+    p.features = (int)c.features, p.hidden = (int)c.hidden;
+    p.idesc_gu = instr_desc(c.type, true, true, 2 * kHalf, kTileRows);
+    p.idesc_dx = instr_desc(c.type, true, false, 64, kTileRows);
+    p.idesc_dw = instr_desc(c.type, false, false, 64, 2 * kHalf);
+    const unsigned grid = (unsigned)glu_narrow_blocks(c.rows);
+    return for_type_act(c.type, c.act, [&](auto t, auto act) { return launch<decltype(t)::value, decltype(act)::value>(p, grid, st); });
+}
+
+gs_status glu_narrow_wait_report(int* expired)
+{
+    const int zero = 0;
+    GS_CUDA_TRY(cudaMemcpyFromSymbol(expired, g_narrow_wait_expired, sizeof *expired));
+    if (*expired) GS_CUDA_TRY(cudaMemcpyToSymbol(g_narrow_wait_expired, &zero, sizeof zero));
+    return GS_OK;
+}
+
+}  // namespace gs

@@ -1,6 +1,9 @@
 // layers_common.cuh -- element types, conversions and activations shared by the
-// decoder layers (norm.cu, linear.cu, gemm.cu).
+// decoder layers (norm.cu, linear.cu, gemm.cu, glu_narrow.cu).
 #pragma once
+
+#include <atomic>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -76,6 +79,33 @@ gs_status launch_after(void (*kernel)(P...), dim3 grid, unsigned block, size_t s
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     GS_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, args...));
     return GS_OK;
+}
+
+// Sets a kernel's shared memory once on each device.
+template <class K>
+inline gs_status allow_smem(K* kernel, int bytes, std::atomic<uint64_t>& done)
+{
+    int dev = 0;
+    GS_CUDA_TRY(cudaGetDevice(&dev));
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return GS_OK;
+    GS_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    if (dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+    return GS_OK;
+}
+
+// Calls f with the 16-bit type and the activation as constants.
+template <class F>
+gs_status for_type_act(int type, int act, F f)
+{
+    const auto with_type = [&](auto t) -> gs_status {
+        if (act == GS_ACT_SILU) return f(t, std::integral_constant<int, GS_ACT_SILU>());
+        if (act == GS_ACT_GELU) return f(t, std::integral_constant<int, GS_ACT_GELU>());
+        if (act == GS_ACT_RELU) return f(t, std::integral_constant<int, GS_ACT_RELU>());
+        return f(t, std::integral_constant<int, GS_ACT_NONE>());
+    };
+    return type == GS_BF16 ? with_type(std::integral_constant<int, GS_BF16>())
+                           : with_type(std::integral_constant<int, GS_F16>());
 }
 
 // ------------------------------------------------------------------ elements
@@ -415,6 +445,21 @@ __device__ __forceinline__ float act_slope(float v, int act)
     float value, slope;
     act_both(v, act, value, slope);
     return slope;
+}
+
+// 16 columns of the gated layer's gradient: dg = dh u act'(g), du = dh act(g).
+template <int ACT>
+__device__ __forceinline__ void glu_gradient(float (&g)[16], float (&u)[16], const float (&dh)[16])
+{
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+        uint64_t value, slope;
+        act_both2<ACT>(pair(g[j], g[j + 1]), value, slope);
+        const uint64_t d = pair(dh[j], dh[j + 1]);
+        const float2 a = unpair(mul2(mul2(d, pair(u[j], u[j + 1])), slope)), b = unpair(mul2(d, value));
+        g[j] = a.x, g[j + 1] = a.y;
+        u[j] = b.x, u[j + 1] = b.y;
+    }
 }
 
 }  // namespace gs

@@ -207,20 +207,6 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinJ
     else join_job<1>(p.job[j], sm);
 }
 
-// Calls f with the 16-bit type and the activation as constants.
-template <class F>
-gs_status for_type_act(int type, int act, F f)
-{
-    const auto with_type = [&](auto t) -> gs_status {
-        if (act == GS_ACT_SILU) return f(t, std::integral_constant<int, GS_ACT_SILU>());
-        if (act == GS_ACT_GELU) return f(t, std::integral_constant<int, GS_ACT_GELU>());
-        if (act == GS_ACT_RELU) return f(t, std::integral_constant<int, GS_ACT_RELU>());
-        return f(t, std::integral_constant<int, GS_ACT_NONE>());
-    };
-    return type == GS_BF16 ? with_type(std::integral_constant<int, GS_BF16>())
-                           : with_type(std::integral_constant<int, GS_F16>());
-}
-
 // Thread columns of an elementwise block: a power of two that covers the row
 // when it is narrow, a block's width at most.
 int thread_cols(int64_t n, int vec)
@@ -560,6 +546,38 @@ extern "C" gs_status gs_glu(const gs_glu_args* args, void* ws, size_t* ws_bytes,
     return gemm_run(c, plan, nullptr, nullptr, st);   // a gated layer never splits k
 }
 
+// Checked arguments, at least one row.
+static gs_status narrow_glu_bwd(const gs_glu_bwd_args& a, void* ws, size_t* ws_bytes, cudaStream_t st)
+{
+    Scratch sc;
+    Rows x = aligned_rows(sc, true, a.x, a.ldx, a.rows, a.in_features, a.type);
+    Rows dh = aligned_rows(sc, true, a.dh, a.lddh, a.rows, a.hidden, a.type);
+    Rows wg = aligned_rows(sc, true, a.w_gate, a.ldwg, a.hidden, a.in_features, a.type);
+    Rows wu = aligned_rows(sc, true, a.w_up, a.ldwu, a.hidden, a.in_features, a.type);
+    const int64_t pitch = round_up(a.in_features, 4), blocks = glu_narrow_blocks(a.rows);
+    const size_t bytes = a.dw_gate ? (size_t)(blocks * a.hidden * pitch) * 4 : 0;
+    const size_t at_g = sc.take(bytes), at_u = sc.take(bytes);
+    const WsCheck wc = ws_check(ws, ws_bytes, sc.used);
+    if (wc == WsCheck::kBad) return GS_ERR_INVALID_ARG;
+    if (wc == WsCheck::kQuery) return GS_OK;
+    char* base = (char*)ws;
+    Rows* const list[] = {&x, &dh, &wg, &wu};
+    gs_status s = pack_all(list, 4, base, a.type, st);
+    if (s != GS_OK) return s;
+    GluNarrowCall c = {};
+    c.rows = a.rows, c.features = a.in_features, c.hidden = a.hidden, c.type = a.type, c.act = a.act;
+    c.x = x.p, c.ldx = x.ld, c.dh = dh.p, c.lddh = dh.ld;
+    c.w_gate = wg.p, c.ldwg = wg.ld, c.w_up = wu.p, c.ldwu = wu.ld;
+    c.dx = a.dx, c.lddx = a.lddx, c.pitch = pitch;
+    if (a.dw_gate) c.dw_gate = (float*)(base + at_g), c.dw_up = (float*)(base + at_u);
+    s = glu_narrow_grad(c, st);
+    if (s != GS_OK || !a.dw_gate) return s;
+    JoinJobs joins;
+    s = joins.add(c.dw_gate, blocks, a.hidden, a.in_features, pitch, a.dw_gate, a.lddwg, a.dw_type);
+    if (s == GS_OK) s = joins.add(c.dw_up, blocks, a.hidden, a.in_features, pitch, a.dw_up, a.lddwu, a.dw_type);
+    return s != GS_OK ? s : joins.run(st);
+}
+
 extern "C" gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* ws_bytes, void* stream)
 {
     GS_NVTX_RANGE("gs_glu_bwd");
@@ -580,6 +598,7 @@ extern "C" gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* w
         if ((a.dw_gate || !a.g) && !mat_ok(a.x, a.ldx, k, a.type)) return GS_ERR_INVALID_ARG;
     }
     const bool again = !a.g;   // the projections are computed again
+    if (again && m > 0 && (a.dx || a.dw_gate) && glu_narrow_fits(k, f)) return narrow_glu_bwd(a, ws, ws_bytes, (cudaStream_t)stream);
     const int64_t ldd = round_up(f, 8);
     Scratch sc;
     const size_t at_dg = sc.take((size_t)m * ldd * 2), at_du = sc.take((size_t)m * ldd * 2);

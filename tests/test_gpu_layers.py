@@ -359,6 +359,54 @@ def test_glu_gradients_again(layers, m, k, f, dt, act):
         check(got, dd.t() @ x64, ee.t() @ x64.abs() + (m + 4) * 2.0 ** -23 * (dd.abs().t() @ x64.abs()), name)
 
 
+@pytest.mark.parametrize("m,k,f", [(1, 64, 128), (127, 64, 128), (128, 16, 64), (129, 33, 65), (257, 64, 64), (5000, 1, 1),
+                                   (20000, 57, 100), (70001, 64, 128), (70001, 40, 24)])
+@pytest.mark.parametrize("dt,act", [(BF, "silu"), (HF, "gelu"), (BF, "relu"), (HF, "none")])
+def test_glu_gradients_narrow(layers, m, k, f, dt, act):
+    """The one-pass gradients of a narrow layer: tiles of 128 rows, several a multiprocessor, halves of 64 hidden columns."""
+    x = rnd((m, k), 0, dt)
+    wg, wu = rnd((f, k), 1, dt, k ** -0.5), rnd((f, k), 2, dt, k ** -0.5)
+    g, mg = pre64(x, wg)
+    u, mu = pre64(x, wu)
+    dh = rnd((m, f), 7, dt)
+    gr = layers.glu_backward(dh, x, wg, wu, act=act)
+    d, s, a, ut = dh.double(), slope64(g, act), act64(g, act), U[dt]
+    dg, du = d * u * s, d * a
+    jump = (g.abs() <= mg).double() if act == "relu" else 0.0
+    eg = ut * dg.abs() + 2.0 ** -18 * (d * u).abs() + LEAST[dt] + d.abs() * (1.13 * mu + (0.8 * mg + jump) * (u.abs() + mu))
+    eu = ut * du.abs() + 2.0 ** -18 * (d * g).abs() + LEAST[dt] + 1.13 * d.abs() * mg
+    x64, wg64, wu64 = x.double(), wg.double(), wu.double()
+    mag = dg.abs() @ wg64.abs() + du.abs() @ wu64.abs()
+    check(gr.dx, dg @ wg64 + du @ wu64, eg @ wg64.abs() + eu @ wu64.abs() + (2 * f + 4) * 2.0 ** -23 * mag, "dx")
+    for got, dd, ee, name in ((gr.dw_gate, dg, eg, "dw_gate"), (gr.dw_up, du, eu, "dw_up")):
+        check(got, dd.t() @ x64, ee.t() @ x64.abs() + (m + 4) * 2.0 ** -23 * (dd.abs().t() @ x64.abs()), name)
+    twice = layers.glu_backward(dh, x, wg, wu, act=act)
+    assert all(torch.equal(p, q) for p, q in ((gr.dx, twice.dx), (gr.dw_gate, twice.dw_gate), (gr.dw_up, twice.dw_up)))
+    f32 = layers.glu_backward(dh, x, wg, wu, act=act, need_dx=False, dw_dtype=F32)
+    assert f32.dx is None and torch.equal(f32.dw_gate.to(dt), gr.dw_gate) and torch.equal(f32.dw_up.to(dt), gr.dw_up)
+    only = layers.glu_backward(dh, x, wg, wu, act=act, need_dw=False)
+    assert only.dw_up is None and torch.equal(only.dx, gr.dx)
+    # rows of other pitches and bases, the same values
+    def wide(t, off):
+        w = torch.full((t.shape[0], t.shape[1] + 11), float("nan"), dtype=dt, device="cuda")[:, off:off + t.shape[1]]
+        w.copy_(t)
+        return w
+    odd = layers.glu_backward(wide(dh, 3), wide(x, 5), wide(wg, 1), wide(wu, 8), act=act)
+    assert torch.equal(odd.dx, gr.dx) and torch.equal(odd.dw_gate, gr.dw_gate) and torch.equal(odd.dw_up, gr.dw_up)
+
+
+def test_glu_gradients_narrow_bad_rows(layers):
+    """A row with an infinity or a NaN spoils its own dx and no other row's."""
+    m, k, f = 400, 40, 100
+    x, wg, wu, dh = rnd((m, k), 0, BF), rnd((f, k), 1, BF), rnd((f, k), 2, BF), rnd((m, f), 3, BF)
+    want = layers.glu_backward(dh, x, wg, wu).dx
+    x[130, 7], dh[250, 99] = float("inf"), float("nan")
+    got = layers.glu_backward(dh, x, wg, wu).dx
+    same = torch.ones(m, dtype=torch.bool, device="cuda")
+    same[[130, 250]] = False
+    assert torch.equal(got[same], want[same]) and not got[130].isfinite().any() and got[250].isnan().all()
+
+
 def test_glu_saves_for_wide_inputs_only(layers):
     for k, saved in ((512, False), (520, True)):
         o = layers.glu(rnd((3, k), 0, BF), rnd((16, k), 1, BF), rnd((16, k), 2, BF), need_backward=True)
