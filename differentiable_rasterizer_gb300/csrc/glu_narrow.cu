@@ -29,15 +29,36 @@ using namespace tc;
 constexpr int kWarps = 18, kThreads = kWarps * 32, kEpiWarps = 16;
 constexpr int kTileRows = 128, kHalf = 64;             // rows of a tile; hidden columns of a half
 constexpr uint32_t kBox = kTileRows * 128;             // bytes of 128 rows of 64 columns
-constexpr uint32_t kWeights = 2 * kBox;                // per half: 64 rows of Wg, 64 of Wu
-constexpr uint32_t kAtDg = kBox, kAtDu = 3 * kBox;     // in a stage: x, dh (then dg) of both halves, du of both
-constexpr uint32_t kStage = 5 * kBox;
-constexpr int kStages = 2;
 constexpr uint32_t kTmemDx = 256, kTmemDw = 320, kTmemCols = 512;   // columns: dx; dWg, dWu
+constexpr int kMostStages = 4;
 
-enum Bar { kWFull = 0, kFull = 1, kEmpty = 3, kGuFull = 5, kGuFree = 7, kGradFull = 9, kDxFull = 11, kDxFree, kDone, kDrain, kBars };
-constexpr int kSmem = kWeights + kStages * kStage + ((kBars * 8 + 15) & ~15) + 16;
-static_assert(kSmem <= 232448, "shared memory of an SM");
+enum Bar {
+    kWFull = 0,
+    kFull = 1,                            // a stage's x and dh have landed
+    kEmpty = kFull + kMostStages,         // its products are done
+    kGradFull = kEmpty + kMostStages,     // its dg and du are written
+    kGuFull = kGradFull + kMostStages,    // a buffer's g and u are there
+    kGuFree = kGuFull + 2,                // and read
+    kDxFull = kGuFree + 2,
+    kDxFree,
+    kDone,
+    kDrain,
+    kBars
+};
+
+// HALVES: of the hidden columns, 64 each.
+template <int HALVES>
+struct Shape {
+    static constexpr int kStages = HALVES == 1 ? 4 : 2;
+    static constexpr uint32_t kWeights = HALVES * kBox;     // per half: 64 rows of Wg, 64 of Wu
+    // a stage: dh (then dg), du, x.  The last half's dg and du have a box behind them, which
+    // the MMA's M side of 128 hidden columns reads (and whose rows nothing keeps).
+    static constexpr uint32_t kAtDu = HALVES * kBox, kAtX = 2 * HALVES * kBox, kStage = kAtX + kBox;
+    static constexpr int kSmem = kWeights + kStages * kStage + ((kBars * 8 + 15) & ~15) + 16;
+    static_assert(kSmem <= 232448, "shared memory of an SM");
+    static __device__ __forceinline__ uint32_t stage(uint32_t i) { return i % kStages; }
+    static __device__ __forceinline__ uint32_t phase(uint32_t i) { return i / kStages & 1; }
+};
 
 struct Params {
     CUtensorMap x, dh, wg, wu;
@@ -55,95 +76,109 @@ __device__ __forceinline__ void prefetch_2d(const CUtensorMap* map, int x, int y
     asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
 }
 
-// Stage addresses and phases of the CTA's i-th tile.
-__device__ __forceinline__ uint32_t stage_at(uint32_t stages, uint32_t i) { return stages + (i & 1) * kStage; }
-
+template <int HALVES>
 __device__ __forceinline__ void load_rows(const Params& p, uint32_t weights, uint32_t stages, uint32_t bars, volatile int* gave_up)
 {
-    const int halves = p.hidden > kHalf ? 2 : 1;
-    mbar_expect(bars + 8 * kWFull, halves * kBox);
-    for (int h = 0; h < halves; ++h) {
+    using S = Shape<HALVES>;
+    mbar_expect(bars + 8 * kWFull, S::kWeights);
+#pragma unroll
+    for (int h = 0; h < HALVES; ++h) {
         tma_load_2d<false>(weights + h * kBox, &p.wg, 0, h * kHalf, bars + 8 * kWFull);
         tma_load_2d<false>(weights + h * kBox + kBox / 2, &p.wu, 0, h * kHalf, bars + 8 * kWFull);
     }
     uint32_t i = 0;
     for (uint32_t t = blockIdx.x; t < p.tiles; t += gridDim.x, ++i) {
-        if (!mbar_wait(bars + 8 * (kEmpty + (i & 1)), ((i >> 1) & 1) ^ 1, gave_up)) break;
-        const uint32_t full = bars + 8 * (kFull + (i & 1)), at = stage_at(stages, i);
-        mbar_expect(full, (1 + halves) * kBox);
-        tma_load_2d<false>(at, &p.x, 0, (int)(t * kTileRows), full);
-        for (int h = 0; h < halves; ++h) tma_load_2d<false>(at + kAtDg + h * kBox, &p.dh, h * kHalf, (int)(t * kTileRows), full);
-        // a stage is empty for a short time only: the tile after the next is on its way into L2 by then
-        const uint64_t ahead = (uint64_t)t + 2ull * gridDim.x;
+        if (!mbar_wait(bars + 8 * (kEmpty + S::stage(i)), S::phase(i) ^ 1, gave_up)) break;
+        const uint32_t full = bars + 8 * (kFull + S::stage(i)), at = stages + S::stage(i) * S::kStage;
+        const int row = (int)(t * kTileRows);
+        mbar_expect(full, (1 + HALVES) * kBox);
+        tma_load_2d<false>(at + S::kAtX, &p.x, 0, row, full);
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h) tma_load_2d<false>(at + h * kBox, &p.dh, h * kHalf, row, full);
+        // a stage is empty for a short time only: its next tile is on its way into L2 by then
+        const uint64_t ahead = (uint64_t)t + (uint64_t)S::kStages * gridDim.x;
         if (ahead < p.tiles) {
             prefetch_2d(&p.x, 0, (int)(ahead * kTileRows));
-            for (int h = 0; h < halves; ++h) prefetch_2d(&p.dh, h * kHalf, (int)(ahead * kTileRows));
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h) prefetch_2d(&p.dh, h * kHalf, (int)(ahead * kTileRows));
         }
     }
     // the block does not leave before its copies have landed
     volatile int still = 0;
     mbar_wait(bars + 8 * kWFull, 0, &still);
-    for (uint32_t j = i > kStages ? i - kStages : 0; j < i; ++j) mbar_wait(bars + 8 * (kFull + (j & 1)), (j >> 1) & 1, &still);
+    for (uint32_t j = i > S::kStages ? i - S::kStages : 0; j < i; ++j)
+        mbar_wait(bars + 8 * (kFull + S::stage(j)), S::phase(j), &still);
 }
 
+// Two kinds of work in the order in which they become ready: a half's g and u, when its rows
+// have landed and its buffer is read; a tile's dx, dWg and dWu, when its dg and du are
+// written.  (In a fixed order, the next tile's g and u first, a late copy held the products
+// back that free the stage of the copy after it: 160 us the million rows.)
+template <int HALVES>
 __device__ __forceinline__ void issue_products(const Params& p, uint32_t weights, uint32_t stages, uint32_t bars, uint32_t tmem,
                                                volatile int* gave_up)
 {
-    const uint32_t halves = p.hidden > kHalf ? 2 : 1, steps_x = (uint32_t)(p.features + 15) / 16;
-    uint32_t unit = 0;
-    const auto gate_up = [&](uint32_t i, uint32_t h) -> bool {
-        const uint32_t b = unit & 1;
-        if (!mbar_wait(bars + 8 * (kGuFree + b), ((unit >> 1) & 1) ^ 1, gave_up)) return false;
-        tc_fence_after();
-        const uint32_t x = desc_lo(stage_at(stages, i), true), w = desc_lo(weights + h * kBox, true);
-        for (uint32_t j = 0; j < steps_x; ++j)
-            mma<false, false>(tmem + b * 128, x + j * k_step(true), kDescHi, w + j * k_step(true), kDescHi, p.idesc_gu, j > 0);
-        mma_commit<false>(bars + 8 * (kGuFull + b));
-        ++unit;
-        return true;
-    };
-    if (!mbar_wait(bars + 8 * kWFull, 0, gave_up) || !mbar_wait(bars + 8 * kFull, 0, gave_up)) return;
-    tc_fence_after();
-    for (uint32_t h = 0; h < halves; ++h)
-        if (!gate_up(0, h)) return;
-    uint32_t i = 0;
-    for (uint32_t t = blockIdx.x; t < p.tiles; t += gridDim.x, ++i) {
-        if ((uint64_t)t + gridDim.x < p.tiles) {   // the next tile's g and u, as their buffers are read
-            if (!mbar_wait(bars + 8 * (kFull + ((i + 1) & 1)), ((i + 1) >> 1) & 1, gave_up)) return;
+    using S = Shape<HALVES>;
+    const uint32_t steps_x = (uint32_t)(p.features + 15) / 16, tiles = (p.tiles - blockIdx.x + gridDim.x - 1) / gridDim.x;
+    if (!mbar_wait(bars + 8 * kWFull, 0, gave_up)) return;
+    uint32_t unit = 0, i = 0, idle = 0;
+    long long since = 0;
+    while (i < tiles) {
+        bool did = false;
+        const uint32_t next = unit / HALVES, h = unit % HALVES, b = unit & 1;
+        if (next < tiles && (h > 0 || mbar_test(bars + 8 * (kFull + S::stage(next)), S::phase(next))) &&
+            mbar_test(bars + 8 * (kGuFree + b), (unit >> 1 & 1) ^ 1)) {
             tc_fence_after();
-            for (uint32_t h = 0; h < halves; ++h)
-                if (!gate_up(i + 1, h)) return;
+            const uint32_t x = desc_lo(stages + S::stage(next) * S::kStage + S::kAtX, true);
+            const uint32_t w = desc_lo(weights + h * kBox, true);
+            for (uint32_t j = 0; j < steps_x; ++j)
+                mma<false, false>(tmem + b * 128, x + j * k_step(true), kDescHi, w + j * k_step(true), kDescHi, p.idesc_gu, j > 0);
+            mma_commit<false>(bars + 8 * (kGuFull + b));
+            ++unit;
+            did = true;
         }
-        if (!mbar_wait(bars + 8 * (kGradFull + (i & 1)), (i >> 1) & 1, gave_up)) return;
-        tc_fence_after();
-        const uint32_t at = stage_at(stages, i);
-        if (p.dx) {
-            if (!mbar_wait(bars + 8 * kDxFree, (i & 1) ^ 1, gave_up)) return;
+        if (i < next && mbar_test(bars + 8 * (kGradFull + S::stage(i)), S::phase(i)) &&
+            (!p.dx || mbar_test(bars + 8 * kDxFree, (i & 1) ^ 1))) {
             tc_fence_after();
-            uint32_t add = 0;
-            for (uint32_t h = 0; h < halves; ++h)
-                for (uint32_t w = 0; w < 2; ++w) {   // dg Wg, du Wu
-                    const uint32_t a = desc_lo(at + (w ? kAtDu : kAtDg) + h * kBox, true);
-                    const uint32_t b = desc_lo(weights + h * kBox + w * (kBox / 2), false);
+            const uint32_t at = stages + S::stage(i) * S::kStage;
+            if (p.dx) {
 #pragma unroll
-                    for (uint32_t j = 0; j < 4; ++j, add = 1)
-                        mma<false, false>(tmem + kTmemDx, a + j * k_step(true), kDescHi, b + j * k_step(false), kDescHi,
-                                          p.idesc_dx, add);
+                for (uint32_t s = 0; s < 2 * HALVES; ++s) {   // dg Wg, du Wu of a half
+                    const uint32_t a = desc_lo(at + s * kBox, true);
+                    const uint32_t w = desc_lo(weights + s % HALVES * kBox + s / HALVES * (kBox / 2), false);
+#pragma unroll
+                    for (uint32_t j = 0; j < 4; ++j)
+                        mma<false, false>(tmem + kTmemDx, a + j * k_step(true), kDescHi, w + j * k_step(false), kDescHi, p.idesc_dx,
+                                          s > 0 || j > 0);
                 }
-            mma_commit<false>(bars + 8 * kDxFull);
-        }
-        if (p.dw[0]) {
-            const uint32_t b = desc_lo(at, false);
-            for (uint32_t w = 0; w < 2; ++w) {
-                // k is the row: 64 columns a group, the next group a box on
-                const uint32_t a = ((at + (w ? kAtDu : kAtDg)) >> 4) | ((kBox >> 4) << 16);
+                mma_commit<false>(bars + 8 * kDxFull);
+            }
+            if (p.dw[0]) {
+                const uint32_t x = desc_lo(at + S::kAtX, false);
 #pragma unroll
-                for (uint32_t j = 0; j < kTileRows / 16; ++j)
-                    mma<false, false>(tmem + kTmemDw + w * 64, a + j * k_step(false), kDescHi, b + j * k_step(false), kDescHi,
-                                      p.idesc_dw, i > 0 || j > 0);
+                for (uint32_t w = 0; w < 2; ++w) {
+                    // k is the row: 64 columns a group, the next group a box on
+                    const uint32_t a = ((at + w * S::kAtDu) >> 4) | ((kBox >> 4) << 16);
+#pragma unroll
+                    for (uint32_t j = 0; j < kTileRows / 16; ++j)
+                        mma<false, false>(tmem + kTmemDw + w * 64, a + j * k_step(false), kDescHi, x + j * k_step(false), kDescHi,
+                                          p.idesc_dw, i > 0 || j > 0);
+                }
+            }
+            mma_commit<false>(bars + 8 * (kEmpty + S::stage(i)));
+            ++i;
+            did = true;
+        }
+        if (did) idle = 0;
+        else if (++idle % 256 == 0) {   // bounded as every wait is
+            const long long now = clock64();
+            if (idle == 256) since = now;
+            if (*gave_up) return;
+            if (now - since > kWaitCycles) {
+                *gave_up = 1;
+                return;
             }
         }
-        mma_commit<false>(bars + 8 * (kEmpty + (i & 1)));
     }
     mma_commit<false>(bars + 8 * kDone);
 }
@@ -177,16 +212,17 @@ __device__ __forceinline__ bool store_dx(const Params& p, uint32_t i, uint32_t r
     return true;
 }
 
-template <int T, int ACT>
+template <int T, int ACT, int HALVES>
 __global__ void __launch_bounds__(kThreads, 1) glu_narrow_kernel(const __grid_constant__ Params p)
 {
+    using S = Shape<HALVES>;
     extern __shared__ __align__(1024) char smem_raw[];
     const uint32_t weights = smem_addr(smem_raw);
     if (weights & 1023u) {   // every thread sees the same address; there is no padding to move within
         g_narrow_wait_expired = 1;
         return;
     }
-    const uint32_t stages = weights + kWeights, bars = stages + kStages * kStage;
+    const uint32_t stages = weights + S::kWeights, bars = stages + S::kStages * S::kStage;
     char* tail = smem_raw + (bars - weights) + ((kBars * 8 + 15) & ~15);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail);
     volatile int* gave_up = reinterpret_cast<volatile int*>(tail + 4);
@@ -194,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) glu_narrow_kernel(const __grid_co
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kBars; ++i) {
-            const bool warps = i == kGuFree || i == kGuFree + 1 || i == kGradFull || i == kGradFull + 1 || i == kDxFree;
+            const bool warps = (i >= kGradFull && i < kGuFull) || (i >= kGuFree && i < kDxFull) || i == kDxFree;
             mbar_init(bars + 8 * i, warps ? kEpiWarps : 1);
         }
         *gave_up = 0;
@@ -208,10 +244,10 @@ __global__ void __launch_bounds__(kThreads, 1) glu_narrow_kernel(const __grid_co
     wait_for_predecessor();
 
     if (warp == 0) {
-        if (elect_one()) load_rows(p, weights, stages, bars, gave_up);
+        if (elect_one()) load_rows<HALVES>(p, weights, stages, bars, gave_up);
     } else if (warp == 1) {
         if (elect_one()) {
-            issue_products(p, weights, stages, bars, tmem, gave_up);
+            issue_products<HALVES>(p, weights, stages, bars, tmem, gave_up);
             if (*gave_up) {
                 volatile int still = 0;
                 mma_commit<false>(bars + 8 * kDrain);
@@ -222,14 +258,13 @@ __global__ void __launch_bounds__(kThreads, 1) glu_narrow_kernel(const __grid_co
         const int quarter = warp & 3, col = ((warp - 2) >> 2) * 16;   // 32 rows, 16 columns of a half
         const uint32_t row = quarter * 32 + lane, mine = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t piece = row * 128 + (((uint32_t)(col >> 3) ^ (row & 7)) << 4);   // its columns' first 16 bytes in a box
-        const int halves = p.hidden > kHalf ? 2 : 1;
         uint32_t unit = 0, i = 0;
         bool ok = true;
         for (uint32_t t = blockIdx.x; ok && t < p.tiles; t += gridDim.x, ++i) {
-            const uint32_t at = stage_at(stages, i) + kAtDg + piece;
-            ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (kFull + (i & 1)), (i >> 1) & 1, gave_up));
+            const uint32_t at = stages + S::stage(i) * S::kStage + piece;
+            ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (kFull + S::stage(i)), S::phase(i), gave_up));
 #pragma unroll 1
-            for (int h = 0; ok && h < halves; ++h, ++unit) {
+            for (int h = 0; ok && h < HALVES; ++h, ++unit) {
                 const uint32_t b = unit & 1;
                 ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (kGuFull + b), (unit >> 1) & 1, gave_up));
                 if (!ok) break;
@@ -264,14 +299,14 @@ __global__ void __launch_bounds__(kThreads, 1) glu_narrow_kernel(const __grid_co
                 for (int e = 0; e < 2; ++e) {
                     st_shared16(a ^ (e << 4), make_uint4(pack_half2(g[8 * e], g[8 * e + 1], T), pack_half2(g[8 * e + 2], g[8 * e + 3], T),
                                                          pack_half2(g[8 * e + 4], g[8 * e + 5], T), pack_half2(g[8 * e + 6], g[8 * e + 7], T)));
-                    st_shared16((a ^ (e << 4)) + (kAtDu - kAtDg),
+                    st_shared16((a ^ (e << 4)) + S::kAtDu,
                                 make_uint4(pack_half2(u[8 * e], u[8 * e + 1], T), pack_half2(u[8 * e + 2], u[8 * e + 3], T),
                                            pack_half2(u[8 * e + 4], u[8 * e + 5], T), pack_half2(u[8 * e + 6], u[8 * e + 7], T)));
                 }
-                if (h == halves - 1) {
+                if (h == HALVES - 1) {
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the products read what was just written
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bars + 8 * (kGradFull + (i & 1)));
+                    if (lane == 0) mbar_arrive(bars + 8 * (kGradFull + S::stage(i)));
                 }
                 // the dx of the tile before is ready by now
                 if (h == 0 && i > 0 && p.dx) ok = store_dx<T>(p, i - 1, (t - gridDim.x) * kTileRows + row, col, mine, bars, lane, gave_up);
@@ -302,13 +337,13 @@ __global__ void __launch_bounds__(kThreads, 1) glu_narrow_kernel(const __grid_co
     }
 }
 
-template <int T, int ACT>
+template <int T, int ACT, int HALVES>
 gs_status launch(const Params& p, unsigned grid, cudaStream_t st)
 {
     static std::atomic<uint64_t> done{0};
-    const gs_status s = allow_smem(glu_narrow_kernel<T, ACT>, kSmem, done);
+    const gs_status s = allow_smem(glu_narrow_kernel<T, ACT, HALVES>, Shape<HALVES>::kSmem, done);
     if (s != GS_OK) return s;
-    return launch_after(glu_narrow_kernel<T, ACT>, dim3(grid), kThreads, kSmem, 1, st, p);
+    return launch_after(glu_narrow_kernel<T, ACT, HALVES>, dim3(grid), kThreads, Shape<HALVES>::kSmem, 1, st, p);
 }
 
 }  // namespace
@@ -338,7 +373,10 @@ gs_status glu_narrow_grad(const GluNarrowCall& c, cudaStream_t st)
     p.idesc_dx = instr_desc(c.type, true, false, 64, kTileRows);
     p.idesc_dw = instr_desc(c.type, false, false, 64, 2 * kHalf);
     const unsigned grid = (unsigned)glu_narrow_blocks(c.rows);
-    return for_type_act(c.type, c.act, [&](auto t, auto act) { return launch<decltype(t)::value, decltype(act)::value>(p, grid, st); });
+    return for_type_act(c.type, c.act, [&](auto t, auto act) {
+        constexpr int T = decltype(t)::value, ACT = decltype(act)::value;
+        return c.hidden <= kHalf ? launch<T, ACT, 1>(p, grid, st) : launch<T, ACT, 2>(p, grid, st);
+    });
 }
 
 gs_status glu_narrow_wait_report(int* expired)
