@@ -26,10 +26,11 @@ namespace {
 
 using namespace tc;
 
-constexpr int kWarps = 18, kThreads = kWarps * 32, kEpiWarps = 16;
+constexpr int kWarps = 18, kThreads = kWarps * 32;
 constexpr int kTileRows = 128, kHalf = 64;             // rows of a tile; hidden columns of a half
 constexpr uint32_t kBox = kTileRows * 128;             // bytes of 128 rows of 64 columns
-constexpr uint32_t kTmemDx = 256, kTmemDw = 320, kTmemCols = 512;   // columns: dx; dWg, dWu
+constexpr uint32_t kTmemDw = 320, kTmemCols = 512;     // columns: two of g and u, dx, dWg, dWu, dx
+__device__ __forceinline__ uint32_t dx_buffer(uint32_t b) { return b ? 448 : 256; }
 constexpr int kMostStages = 4;
 
 enum Bar {
@@ -39,9 +40,9 @@ enum Bar {
     kGradFull = kEmpty + kMostStages,     // its dg and du are written
     kGuFull = kGradFull + kMostStages,    // a buffer's g and u are there
     kGuFree = kGuFull + 2,                // and read
-    kDxFull = kGuFree + 2,
-    kDxFree,
-    kDone,
+    kDxFull = kGuFree + 2,                // a buffer's dx is there
+    kDxFree = kDxFull + 2,
+    kDone = kDxFree + 2,
     kDrain,
     kBars
 };
@@ -56,6 +57,8 @@ struct Shape {
     static constexpr uint32_t kAtDu = HALVES * kBox, kAtX = 2 * HALVES * kBox, kStage = kAtX + kBox;
     static constexpr int kSmem = kWeights + kStages * kStage + ((kBars * 8 + 15) & ~15) + 16;
     static_assert(kSmem <= 232448, "shared memory of an SM");
+    // Eight epilogue warps a buffer of g and u: both halves of a tile at a time, or two tiles.
+    static constexpr int kDxCols = HALVES == 1 ? 32 : 16, kTileWarps = HALVES * 8;
     static __device__ __forceinline__ uint32_t stage(uint32_t i) { return i % kStages; }
     static __device__ __forceinline__ uint32_t phase(uint32_t i) { return i / kStages & 1; }
 };
@@ -138,7 +141,7 @@ __device__ __forceinline__ void issue_products(const Params& p, uint32_t weights
             did = true;
         }
         if (i < next && mbar_test(bars + 8 * (kGradFull + S::stage(i)), S::phase(i)) &&
-            (!p.dx || mbar_test(bars + 8 * kDxFree, (i & 1) ^ 1))) {
+            (!p.dx || mbar_test(bars + 8 * (kDxFree + (i & 1)), (i >> 1 & 1) ^ 1))) {
             tc_fence_after();
             const uint32_t at = stages + S::stage(i) * S::kStage;
             if (p.dx) {
@@ -148,10 +151,10 @@ __device__ __forceinline__ void issue_products(const Params& p, uint32_t weights
                     const uint32_t w = desc_lo(weights + s % HALVES * kBox + s / HALVES * (kBox / 2), false);
 #pragma unroll
                     for (uint32_t j = 0; j < 4; ++j)
-                        mma<false, false>(tmem + kTmemDx, a + j * k_step(true), kDescHi, w + j * k_step(false), kDescHi, p.idesc_dx,
+                        mma<false, false>(tmem + dx_buffer(i & 1), a + j * k_step(true), kDescHi, w + j * k_step(false), kDescHi, p.idesc_dx,
                                           s > 0 || j > 0);
                 }
-                mma_commit<false>(bars + 8 * kDxFull);
+                mma_commit<false>(bars + 8 * (kDxFull + (i & 1)));
             }
             if (p.dw[0]) {
                 const uint32_t x = desc_lo(at + S::kAtX, false);
@@ -183,24 +186,36 @@ __device__ __forceinline__ void issue_products(const Params& p, uint32_t weights
     mma_commit<false>(bars + 8 * kDone);
 }
 
-// 16 columns of dx of the CTA's i-th tile to memory: a thread has its row's 32 bytes.
-template <int T>
+// kDxCols columns of dx of the CTA's i-th tile to memory: a thread has its row's.
+template <int T, int HALVES>
 __device__ __forceinline__ bool store_dx(const Params& p, uint32_t i, uint32_t row, int col, uint32_t tmem, uint32_t bars, int lane,
                                          volatile int* gave_up)
 {
-    if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * kDxFull, i & 1, gave_up))) return false;
+    constexpr int kCols = Shape<HALVES>::kDxCols;
+    const uint32_t b = i & 1;
+    if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * (kDxFull + b), i >> 1 & 1, gave_up))) return false;
     tc_fence_after();
+#pragma unroll 1
+    for (int c = 0; c < kCols; c += 16, col += 16) {
     uint32_t v[16];
-    tmem_ld16(tmem + kTmemDx + col, v);
+    tmem_ld16(tmem + dx_buffer(b) + col, v);
     tmem_ld_wait(v);
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bars + 8 * kDxFree);
+    if (c + 16 == kCols) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + 8 * (kDxFree + b));
+    }
     const int left = row < p.m ? p.features - col : 0;
     uint16_t* to = (uint16_t*)p.dx + (int64_t)row * p.lddx + col;
     uint32_t w[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[j] = pack_half2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]), T);
+    if (p.dx_vec == 2 && left >= 16) {   // whole sectors
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+        continue;
+    }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         if (p.dx_vec && left >= 8 * e + 8) *reinterpret_cast<uint4*>(to + 8 * e) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
@@ -208,6 +223,7 @@ __device__ __forceinline__ bool store_dx(const Params& p, uint32_t i, uint32_t r
 #pragma unroll
             for (int j = 8 * e; j < 8 * e + 8; ++j)
                 if (j < left) to[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+    }
     }
     return true;
 }
@@ -230,8 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1) glu_narrow_kernel(const __grid_co
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kBars; ++i) {
-            const bool warps = (i >= kGradFull && i < kGuFull) || (i >= kGuFree && i < kDxFull) || i == kDxFree;
-            mbar_init(bars + 8 * i, warps ? kEpiWarps : 1);
+            const bool gu = i >= kGuFree && i < kDxFull, tile = (i >= kGradFull && i < kGuFull) || (i >= kDxFree && i < kDone);
+            mbar_init(bars + 8 * i, gu ? 8 : (tile ? S::kTileWarps : 1));
         }
         *gave_up = 0;
         mbar_init_fence();
@@ -255,30 +271,43 @@ __global__ void __launch_bounds__(kThreads, 1) glu_narrow_kernel(const __grid_co
             }
         }
     } else {
-        const int quarter = warp & 3, col = ((warp - 2) >> 2) * 16;   // 32 rows, 16 columns of a half
+        // 32 rows, 32 columns of a buffer; the group's half or every other tile
+        const int quarter = warp & 3, col = ((warp - 2) >> 2 & 1) * 32;
+        const uint32_t group = (uint32_t)(warp - 2) >> 3;
         const uint32_t row = quarter * 32 + lane, mine = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t piece = row * 128 + (((uint32_t)(col >> 3) ^ (row & 7)) << 4);   // its columns' first 16 bytes in a box
-        uint32_t unit = 0, i = 0;
+        const int dx_col = HALVES == 1 ? col : (int)group * 32 + col / 2;
+        constexpr uint32_t kTurn = 2 / HALVES;
+        const uint32_t tiles = (p.tiles - blockIdx.x + gridDim.x - 1) / gridDim.x;
+        const auto row_of = [&](uint32_t i) { return (blockIdx.x + i * gridDim.x) * kTileRows + row; };
+        const int live = p.hidden - (HALVES == 1 ? 0 : (int)group * kHalf) - col;   // columns of the layer from col on
         bool ok = true;
-        for (uint32_t t = blockIdx.x; ok && t < p.tiles; t += gridDim.x, ++i) {
-            const uint32_t at = stages + S::stage(i) * S::kStage + piece;
-            ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (kFull + S::stage(i)), S::phase(i), gave_up));
-#pragma unroll 1
-            for (int h = 0; ok && h < HALVES; ++h, ++unit) {
-                const uint32_t b = unit & 1;
-                ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (kGuFull + b), (unit >> 1) & 1, gave_up));
-                if (!ok) break;
-                tc_fence_after();
-                uint32_t raw[16], up[16];
-                tmem_ld16(mine + b * 128 + col, raw);
-                tmem_ld16(mine + b * 128 + 64 + col, up);
-                const uint32_t a = at + h * kBox;
+        uint32_t i = HALVES == 1 ? group : 0;
+        for (; i < tiles; i += kTurn) {
+            const uint32_t at = stages + S::stage(i) * S::kStage + (HALVES == 1 ? 0 : group * kBox) + piece;
+            const uint32_t nth = HALVES == 1 ? i >> 1 : i;
+            ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (kFull + S::stage(i)), S::phase(i), gave_up) &&
+                                             mbar_wait(bars + 8 * (kGuFull + group), nth & 1, gave_up));
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t raw[2][16], up[2][16];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                tmem_ld16(mine + group * 128 + col + 16 * c, raw[c]);
+                tmem_ld16(mine + group * 128 + 64 + col + 16 * c, up[c]);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                tmem_ld_wait(raw[c]);
+                tmem_ld_wait(up[c]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars + 8 * (kGuFree + group));
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const uint32_t a = at ^ (c << 5);
                 const uint4 d0 = ld_shared16(a), d1 = ld_shared16(a ^ 16);
-                tmem_ld_wait(raw);
-                tmem_ld_wait(up);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bars + 8 * (kGuFree + b));
                 const uint32_t dh[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
                 float g[16], u[16], d[16];
 #pragma unroll
@@ -287,13 +316,12 @@ __global__ void __launch_bounds__(kThreads, 1) glu_narrow_kernel(const __grid_co
                     d[2 * e] = f.x, d[2 * e + 1] = f.y;
                 }
 #pragma unroll
-                for (int e = 0; e < 16; ++e) g[e] = __uint_as_float(raw[e]), u[e] = __uint_as_float(up[e]);
+                for (int e = 0; e < 16; ++e) g[e] = __uint_as_float(raw[c][e]), u[e] = __uint_as_float(up[c][e]);
                 glu_gradient<ACT>(g, u, d);
-                const int left = p.hidden - h * kHalf - col;
-                if (left < 16) {   // beyond the layer: zeros, though an infinite x times no weight were none
+                if (live < 32) {   // beyond the layer: zeros, though an infinite x times no weight were none
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
-                        if (e >= left) g[e] = u[e] = 0.0f;
+                        if (e + 16 * c >= live) g[e] = u[e] = 0.0f;
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -303,27 +331,27 @@ __global__ void __launch_bounds__(kThreads, 1) glu_narrow_kernel(const __grid_co
                                 make_uint4(pack_half2(u[8 * e], u[8 * e + 1], T), pack_half2(u[8 * e + 2], u[8 * e + 3], T),
                                            pack_half2(u[8 * e + 4], u[8 * e + 5], T), pack_half2(u[8 * e + 6], u[8 * e + 7], T)));
                 }
-                if (h == HALVES - 1) {
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the products read what was just written
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bars + 8 * (kGradFull + S::stage(i)));
-                }
-                // the dx of the tile before is ready by now
-                if (h == 0 && i > 0 && p.dx) ok = store_dx<T>(p, i - 1, (t - gridDim.x) * kTileRows + row, col, mine, bars, lane, gave_up);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the products read what was just written
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars + 8 * (kGradFull + S::stage(i)));
+            if (i >= kTurn && p.dx) {   // the dx of the tile before is ready by now
+                ok = store_dx<T, HALVES>(p, i - kTurn, row_of(i - kTurn), dx_col, mine, bars, lane, gave_up);
+                if (!ok) break;
             }
         }
-        if (ok && p.dx) ok = store_dx<T>(p, i - 1, (blockIdx.x + (i - 1) * gridDim.x) * kTileRows + row, col, mine, bars, lane, gave_up);
+        if (ok && p.dx && i >= kTurn) ok = store_dx<T, HALVES>(p, i - kTurn, row_of(i - kTurn), dx_col, mine, bars, lane, gave_up);
         if (ok && p.dw[0] && __all_sync(0xffffffffu, mbar_wait(bars + 8 * kDone, 0, gave_up))) {
             tc_fence_after();
 #pragma unroll 1
-            for (int w = 0; w < 2; ++w) {
+            for (int c = col; c < col + 32; c += 16) {
                 uint32_t v[16];
-                tmem_ld16(mine + kTmemDw + w * 64 + col, v);
+                tmem_ld16(mine + kTmemDw + group * 64 + c, v);
                 tmem_ld_wait(v);
-                float* to = p.dw[w] + ((int64_t)blockIdx.x * p.hidden + row) * p.pitch + col;
+                float* to = p.dw[group] + ((int64_t)blockIdx.x * p.hidden + row) * p.pitch + c;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if ((int)row < p.hidden && col + 4 * e < p.pitch)
+                    if ((int)row < p.hidden && c + 4 * e < p.pitch)
                         *reinterpret_cast<uint4*>(to + 4 * e) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
             }
             tc_fence_before();
@@ -365,7 +393,8 @@ gs_status glu_narrow_grad(const GluNarrowCall& c, cudaStream_t st)
     if (s == GS_OK) s = make_map(&p.wg, c.w_gate, c.type, c.hidden, c.features, c.ldwg, kHalf, kHalf);
     if (s == GS_OK) s = make_map(&p.wu, c.w_up, c.type, c.hidden, c.features, c.ldwu, kHalf, kHalf);
     if (s != GS_OK) return s;
-    p.dx = c.dx, p.lddx = c.lddx, p.dx_vec = c.dx && rows16(c.dx, c.lddx, c.type);
+    p.dx = c.dx, p.lddx = c.lddx, 
+    p.dx_vec = c.dx && rows16(c.dx, c.lddx, c.type) ? (((uintptr_t)c.dx | (uintptr_t)(c.lddx * 2)) % 32 == 0 ? 2 : 1) : 0;
     p.dw[0] = c.dw_gate, p.dw[1] = c.dw_up, p.pitch = (int)c.pitch;
     p.m = (uint32_t)c.rows, p.tiles = (uint32_t)((c.rows + kTileRows - 1) / kTileRows);
     p.features = (int)c.features, p.hidden = (int)c.hidden;
