@@ -7,13 +7,17 @@
 // for at most 64 features and 128 hidden columns (a per-Gaussian decoder's layer), where
 // both weights, a tile of 128 rows with its dg and du, and all accumulators fit on one SM:
 // only x and dh are read and dx is written, 2 (2 features + hidden) bytes a row.  As three
-// products dg and du cross HBM three times (1,000,000 x 64 -> 128: 1.5 GB of 2.0): 160 us
-// against 411 there, 26 against 56 for 100,000 rows, 10 against 15.5 for one.
+// products dg and du cross HBM three times (1,000,000 x 64 -> 128: 1.5 GB of 2.0): 122 us
+// against 411 there, 24 against 56 for 100,000 rows, 10 against 15.5 for one.  What bounds
+// it at 128 hidden columns is the turn of a stage, at 4.2 TB/s (copy, TMEM reads and
+// arithmetic, products whose factors shared memory delivers at 48 cycles each; without
+// most products 109 us before the stages were halves, without the activation 119); at 64
+// HBM at 5.1 TB/s (75 us).
 //
 // A persistent CTA an SM, 18 warps: a TMA producer, an MMA issuer, 16 epilogue warps.
 // TMEM, fp32: two buffers of 64 gate and 64 up columns (a half of the hidden columns
-// each, refilled while the other is read), dx, and dWg and dWu, which stay for all of the
-// CTA's rows and end as its partial sum.  dg takes dh's place in shared memory; the same
+// each), two of dx, and dWg and dWu, which stay for all of the CTA's rows and end as its
+// partial sum.  dg takes dh's place in shared memory; the same
 // tiles are k-fast factors of dx and k-slow factors of the weights' gradients, and the
 // weights are k-fast for g and u and k-slow for dx.
 #include <atomic>
@@ -29,38 +33,37 @@ using namespace tc;
 constexpr int kWarps = 18, kThreads = kWarps * 32;
 constexpr int kTileRows = 128, kHalf = 64;             // rows of a tile; hidden columns of a half
 constexpr uint32_t kBox = kTileRows * 128;             // bytes of 128 rows of 64 columns
-constexpr uint32_t kTmemDw = 320, kTmemCols = 512;     // columns: two of g and u, dx, dWg, dWu, dx
+constexpr uint32_t kTmemDw = 320, kTmemCols = 512;     // columns: two of g and u, dx, the weights' gradients, dx
 __device__ __forceinline__ uint32_t dx_buffer(uint32_t b) { return b ? 448 : 256; }
-constexpr int kMostStages = 4;
+constexpr int kStages = 4, kMostX = 4;
 
 enum Bar {
     kWFull = 0,
-    kFull = 1,                            // a stage's x and dh have landed
-    kEmpty = kFull + kMostStages,         // its products are done
-    kGradFull = kEmpty + kMostStages,     // its dg and du are written
-    kGuFull = kGradFull + kMostStages,    // a buffer's g and u are there
-    kGuFree = kGuFull + 2,                // and read
-    kDxFull = kGuFree + 2,                // a buffer's dx is there
+    kXFull = 1,                    // x of a tile has landed
+    kXEmpty = kXFull + kMostX,     // its products are done
+    kFull = kXEmpty + kMostX,      // dh of a unit has landed
+    kEmpty = kFull + kStages,      // its products are done
+    kGradFull = kEmpty + kStages,  // its dg and du are written
+    kGuFull = kGradFull + kStages, // a buffer's g and u are there
+    kGuFree = kGuFull + 2,         // and read
+    kDxFull = kGuFree + 2,         // a buffer's dx is there
     kDxFree = kDxFull + 2,
     kDone = kDxFree + 2,
     kDrain,
     kBars
 };
 
-// HALVES: of the hidden columns, 64 each.
+// HALVES: of the hidden columns, 64 each.  A unit is a half of a tile; unit u's buffer of
+// g and u and its eight epilogue warps are number u % 2, its stage u % 4.
 template <int HALVES>
 struct Shape {
-    static constexpr int kStages = HALVES == 1 ? 4 : 2;
+    static constexpr int kStagesX = HALVES == 1 ? 4 : 3;
     static constexpr uint32_t kWeights = HALVES * kBox;     // per half: 64 rows of Wg, 64 of Wu
-    // a stage: dh (then dg), du, x.  The last half's dg and du have a box behind them, which
-    // the MMA's M side of 128 hidden columns reads (and whose rows nothing keeps).
-    static constexpr uint32_t kAtDu = HALVES * kBox, kAtX = 2 * HALVES * kBox, kStage = kAtX + kBox;
-    static constexpr int kSmem = kWeights + kStages * kStage + ((kBars * 8 + 15) & ~15) + 16;
+    static constexpr uint32_t kStage = 2 * kBox;            // dh, then dg in its place; du
+    static constexpr uint32_t kAtX = kWeights + kStages * kStage, kAtBars = kAtX + kStagesX * kBox;
+    static constexpr int kSmem = kAtBars + ((kBars * 8 + 15) & ~15) + 16;
     static_assert(kSmem <= 232448, "shared memory of an SM");
-    // Eight epilogue warps a buffer of g and u: both halves of a tile at a time, or two tiles.
-    static constexpr int kDxCols = HALVES == 1 ? 32 : 16, kTileWarps = HALVES * 8;
-    static __device__ __forceinline__ uint32_t stage(uint32_t i) { return i % kStages; }
-    static __device__ __forceinline__ uint32_t phase(uint32_t i) { return i / kStages & 1; }
+    static constexpr int kDxCols = HALVES == 1 ? 32 : 16;   // of an epilogue warp
 };
 
 struct Params {
@@ -72,6 +75,9 @@ struct Params {
     int features, hidden, pitch, dx_vec;
 };
 
+// The CTA's tiles: blockIdx.x, blockIdx.x + gridDim.x, ...
+__device__ __forceinline__ uint32_t own_tiles(const Params& p) { return (p.tiles - blockIdx.x + gridDim.x - 1) / gridDim.x; }
+
 __device__ int g_narrow_wait_expired;
 
 __device__ __forceinline__ void prefetch_2d(const CUtensorMap* map, int x, int y)
@@ -80,96 +86,108 @@ __device__ __forceinline__ void prefetch_2d(const CUtensorMap* map, int x, int y
 }
 
 template <int HALVES>
-__device__ __forceinline__ void load_rows(const Params& p, uint32_t weights, uint32_t stages, uint32_t bars, volatile int* gave_up)
+__device__ __forceinline__ void load_rows(const Params& p, uint32_t smem, uint32_t bars, volatile int* gave_up)
 {
     using S = Shape<HALVES>;
     mbar_expect(bars + 8 * kWFull, S::kWeights);
 #pragma unroll
     for (int h = 0; h < HALVES; ++h) {
-        tma_load_2d<false>(weights + h * kBox, &p.wg, 0, h * kHalf, bars + 8 * kWFull);
-        tma_load_2d<false>(weights + h * kBox + kBox / 2, &p.wu, 0, h * kHalf, bars + 8 * kWFull);
+        tma_load_2d<false>(smem + h * kBox, &p.wg, 0, h * kHalf, bars + 8 * kWFull);
+        tma_load_2d<false>(smem + h * kBox + kBox / 2, &p.wu, 0, h * kHalf, bars + 8 * kWFull);
     }
-    uint32_t i = 0;
-    for (uint32_t t = blockIdx.x; t < p.tiles; t += gridDim.x, ++i) {
-        if (!mbar_wait(bars + 8 * (kEmpty + S::stage(i)), S::phase(i) ^ 1, gave_up)) break;
-        const uint32_t full = bars + 8 * (kFull + S::stage(i)), at = stages + S::stage(i) * S::kStage;
+    Ring<S::kStagesX> rx;
+    Ring<kStages> ru;
+    uint32_t xs = 0, units = 0;
+    bool ok = true;
+    for (uint32_t t = blockIdx.x; ok && t < p.tiles; t += gridDim.x) {
         const int row = (int)(t * kTileRows);
-        mbar_expect(full, (1 + HALVES) * kBox);
-        tma_load_2d<false>(at + S::kAtX, &p.x, 0, row, full);
-#pragma unroll
-        for (int h = 0; h < HALVES; ++h) tma_load_2d<false>(at + h * kBox, &p.dh, h * kHalf, row, full);
         // a stage is empty for a short time only: its next tile is on its way into L2 by then
-        const uint64_t ahead = (uint64_t)t + (uint64_t)S::kStages * gridDim.x;
-        if (ahead < p.tiles) {
-            prefetch_2d(&p.x, 0, (int)(ahead * kTileRows));
+        const uint64_t ahead = (uint64_t)t + (uint64_t)S::kStagesX * gridDim.x;
+        const bool more = ahead < p.tiles;
+        const int row_ahead = (int)(ahead * kTileRows);
+        if (!mbar_wait(bars + 8 * (kXEmpty + rx.s), rx.parity ^ 1, gave_up)) break;
+        mbar_expect(bars + 8 * (kXFull + rx.s), kBox);
+        tma_load_2d<false>(smem + S::kAtX + rx.s * kBox, &p.x, 0, row, bars + 8 * (kXFull + rx.s));
+        if (more) prefetch_2d(&p.x, 0, row_ahead);
+        rx.next();
+        ++xs;
 #pragma unroll
-            for (int h = 0; h < HALVES; ++h) prefetch_2d(&p.dh, h * kHalf, (int)(ahead * kTileRows));
+        for (int h = 0; h < HALVES; ++h) {
+            ok = ok && mbar_wait(bars + 8 * (kEmpty + ru.s), ru.parity ^ 1, gave_up);
+            if (!ok) break;
+            mbar_expect(bars + 8 * (kFull + ru.s), kBox);
+            tma_load_2d<false>(smem + S::kWeights + ru.s * S::kStage, &p.dh, h * kHalf, row, bars + 8 * (kFull + ru.s));
+            if (more) prefetch_2d(&p.dh, h * kHalf, row_ahead);
+            ru.next();
+            ++units;
         }
     }
     // the block does not leave before its copies have landed
     volatile int still = 0;
     mbar_wait(bars + 8 * kWFull, 0, &still);
-    for (uint32_t j = i > S::kStages ? i - S::kStages : 0; j < i; ++j)
-        mbar_wait(bars + 8 * (kFull + S::stage(j)), S::phase(j), &still);
+    for (uint32_t j = xs > S::kStagesX ? xs - S::kStagesX : 0; j < xs; ++j)
+        mbar_wait(bars + 8 * (kXFull + j % S::kStagesX), j / S::kStagesX & 1, &still);
+    for (uint32_t j = units > kStages ? units - kStages : 0; j < units; ++j)
+        mbar_wait(bars + 8 * (kFull + j % kStages), j / kStages & 1, &still);
 }
 
-// Two kinds of work in the order in which they become ready: a half's g and u, when its rows
-// have landed and its buffer is read; a tile's dx, dWg and dWu, when its dg and du are
-// written.  (In a fixed order, the next tile's g and u first, a late copy held the products
-// back that free the stage of the copy after it: 160 us the million rows.)
+// Two kinds of work in the order in which they become ready: a unit's g and u, when its x
+// has landed and its buffer is read; its part of dx and of the weights' gradients, when its
+// dg and du are written.  (In a fixed order, the next tile's g and u first, a late copy
+// held the products back that free the stage of the copy after it: 160 us the million rows.)
 template <int HALVES>
-__device__ __forceinline__ void issue_products(const Params& p, uint32_t weights, uint32_t stages, uint32_t bars, uint32_t tmem,
-                                               volatile int* gave_up)
+__device__ __forceinline__ void issue_products(const Params& p, uint32_t smem, uint32_t bars, uint32_t tmem, volatile int* gave_up)
 {
     using S = Shape<HALVES>;
-    const uint32_t steps_x = (uint32_t)(p.features + 15) / 16, tiles = (p.tiles - blockIdx.x + gridDim.x - 1) / gridDim.x;
+    const uint32_t steps_x = (uint32_t)(p.features + 15) / 16, units = own_tiles(p) * HALVES;
     if (!mbar_wait(bars + 8 * kWFull, 0, gave_up)) return;
-    uint32_t unit = 0, i = 0, idle = 0;
+    Ring<S::kStagesX> xg, xd;   // x of the next unit of either kind
+    uint32_t next = 0, v = 0, idle = 0;
     long long since = 0;
-    while (i < tiles) {
+    while (v < units) {
         bool did = false;
-        const uint32_t next = unit / HALVES, h = unit % HALVES, b = unit & 1;
-        if (next < tiles && (h > 0 || mbar_test(bars + 8 * (kFull + S::stage(next)), S::phase(next))) &&
-            mbar_test(bars + 8 * (kGuFree + b), (unit >> 1 & 1) ^ 1)) {
+        const uint32_t b = next & 1;
+        if (next < units && mbar_test(bars + 8 * (kXFull + xg.s), xg.parity) &&
+            mbar_test(bars + 8 * (kGuFree + b), (next >> 1 & 1) ^ 1)) {
             tc_fence_after();
-            const uint32_t x = desc_lo(stages + S::stage(next) * S::kStage + S::kAtX, true);
-            const uint32_t w = desc_lo(weights + h * kBox, true);
+            const uint32_t x = desc_lo(smem + S::kAtX + xg.s * kBox, true), w = desc_lo(smem + next % HALVES * kBox, true);
             for (uint32_t j = 0; j < steps_x; ++j)
                 mma<false, false>(tmem + b * 128, x + j * k_step(true), kDescHi, w + j * k_step(true), kDescHi, p.idesc_gu, j > 0);
             mma_commit<false>(bars + 8 * (kGuFull + b));
-            ++unit;
+            ++next;
+            if (next % HALVES == 0) xg.next();
             did = true;
         }
-        if (i < next && mbar_test(bars + 8 * (kGradFull + S::stage(i)), S::phase(i)) &&
-            (!p.dx || mbar_test(bars + 8 * (kDxFree + (i & 1)), (i >> 1 & 1) ^ 1))) {
+        const uint32_t i = v / HALVES, h = v % HALVES, s = v % kStages;
+        if (v < next && mbar_test(bars + 8 * (kGradFull + s), v / kStages & 1) &&
+            (!p.dx || h > 0 || mbar_test(bars + 8 * (kDxFree + (i & 1)), (i >> 1 & 1) ^ 1))) {
             tc_fence_after();
-            const uint32_t at = stages + S::stage(i) * S::kStage;
+            const uint32_t at = smem + S::kWeights + s * S::kStage;
             if (p.dx) {
 #pragma unroll
-                for (uint32_t s = 0; s < 2 * HALVES; ++s) {   // dg Wg, du Wu of a half
-                    const uint32_t a = desc_lo(at + s * kBox, true);
-                    const uint32_t w = desc_lo(weights + s % HALVES * kBox + s / HALVES * (kBox / 2), false);
+                for (uint32_t w = 0; w < 2; ++w) {   // dg Wg, du Wu
+                    const uint32_t a = desc_lo(at + w * kBox, true), c = desc_lo(smem + h * kBox + w * (kBox / 2), false);
 #pragma unroll
                     for (uint32_t j = 0; j < 4; ++j)
-                        mma<false, false>(tmem + dx_buffer(i & 1), a + j * k_step(true), kDescHi, w + j * k_step(false), kDescHi, p.idesc_dx,
-                                          s > 0 || j > 0);
+                        mma<false, false>(tmem + dx_buffer(i & 1), a + j * k_step(true), kDescHi, c + j * k_step(false), kDescHi,
+                                          p.idesc_dx, h > 0 || w > 0 || j > 0);
                 }
-                mma_commit<false>(bars + 8 * (kDxFull + (i & 1)));
+                if (h == HALVES - 1) mma_commit<false>(bars + 8 * (kDxFull + (i & 1)));
             }
             if (p.dw[0]) {
-                const uint32_t x = desc_lo(at + S::kAtX, false);
+                // k is the row, M the half's 64 columns of dg and, a box on, of du
+                const uint32_t a = (at >> 4) | ((kBox >> 4) << 16), c = desc_lo(smem + S::kAtX + xd.s * kBox, false);
 #pragma unroll
-                for (uint32_t w = 0; w < 2; ++w) {
-                    // k is the row: 64 columns a group, the next group a box on
-                    const uint32_t a = ((at + w * S::kAtDu) >> 4) | ((kBox >> 4) << 16);
-#pragma unroll
-                    for (uint32_t j = 0; j < kTileRows / 16; ++j)
-                        mma<false, false>(tmem + kTmemDw + w * 64, a + j * k_step(false), kDescHi, x + j * k_step(false), kDescHi,
-                                          p.idesc_dw, i > 0 || j > 0);
-                }
+                for (uint32_t j = 0; j < kTileRows / 16; ++j)
+                    mma<false, false>(tmem + kTmemDw + h * 64, a + j * k_step(false), kDescHi, c + j * k_step(false), kDescHi,
+                                      p.idesc_dw, i > 0 || j > 0);
             }
-            mma_commit<false>(bars + 8 * (kEmpty + S::stage(i)));
-            ++i;
+            mma_commit<false>(bars + 8 * (kEmpty + s));
+            if (h == HALVES - 1) {
+                mma_commit<false>(bars + 8 * (kXEmpty + xd.s));
+                xd.next();
+            }
+            ++v;
             did = true;
         }
         if (did) idle = 0;
@@ -197,33 +215,34 @@ __device__ __forceinline__ bool store_dx(const Params& p, uint32_t i, uint32_t r
     tc_fence_after();
 #pragma unroll 1
     for (int c = 0; c < kCols; c += 16, col += 16) {
-    uint32_t v[16];
-    tmem_ld16(tmem + dx_buffer(b) + col, v);
-    tmem_ld_wait(v);
-    if (c + 16 == kCols) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars + 8 * (kDxFree + b));
-    }
-    const int left = row < p.m ? p.features - col : 0;
-    uint16_t* to = (uint16_t*)p.dx + (int64_t)row * p.lddx + col;
-    uint32_t w[8];
+        uint32_t v[16];
+        tmem_ld16(tmem + dx_buffer(b) + col, v);
+        tmem_ld_wait(v);
+        if (c + 16 == kCols) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars + 8 * (kDxFree + b));
+        }
+        const int left = row < p.m ? p.features - col : 0;
+        uint16_t* to = (uint16_t*)p.dx + (int64_t)row * p.lddx + col;
+        uint32_t w[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = pack_half2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]), T);
-    if (p.dx_vec == 2 && left >= 16) {   // whole sectors
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                     : "memory");
-        continue;
-    }
+        for (int j = 0; j < 8; ++j) w[j] = pack_half2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]), T);
+        if (p.dx_vec == 2 && left >= 16) {   // whole sectors
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                         "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                         : "memory");
+            continue;
+        }
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        if (p.dx_vec && left >= 8 * e + 8) *reinterpret_cast<uint4*>(to + 8 * e) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-        else
+        for (int e = 0; e < 2; ++e) {
+            if (p.dx_vec && left >= 8 * e + 8)
+                *reinterpret_cast<uint4*>(to + 8 * e) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+            else
 #pragma unroll
-            for (int j = 8 * e; j < 8 * e + 8; ++j)
-                if (j < left) to[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
-    }
+                for (int j = 8 * e; j < 8 * e + 8; ++j)
+                    if (j < left) to[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+        }
     }
     return true;
 }
@@ -233,21 +252,21 @@ __global__ void __launch_bounds__(kThreads, 1) glu_narrow_kernel(const __grid_co
 {
     using S = Shape<HALVES>;
     extern __shared__ __align__(1024) char smem_raw[];
-    const uint32_t weights = smem_addr(smem_raw);
-    if (weights & 1023u) {   // every thread sees the same address; there is no padding to move within
+    const uint32_t smem = smem_addr(smem_raw);
+    if (smem & 1023u) {   // every thread sees the same address; there is no padding to move within
         g_narrow_wait_expired = 1;
         return;
     }
-    const uint32_t stages = weights + S::kWeights, bars = stages + S::kStages * S::kStage;
-    char* tail = smem_raw + (bars - weights) + ((kBars * 8 + 15) & ~15);
+    const uint32_t bars = smem + S::kAtBars;
+    char* tail = smem_raw + S::kAtBars + ((kBars * 8 + 15) & ~15);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail);
     volatile int* gave_up = reinterpret_cast<volatile int*>(tail + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kBars; ++i) {
-            const bool gu = i >= kGuFree && i < kDxFull, tile = (i >= kGradFull && i < kGuFull) || (i >= kDxFree && i < kDone);
-            mbar_init(bars + 8 * i, gu ? 8 : (tile ? S::kTileWarps : 1));
+            const bool group = (i >= kGradFull && i < kGuFull) || (i >= kGuFree && i < kDxFull), dx = i >= kDxFree && i < kDone;
+            mbar_init(bars + 8 * i, group ? 8 : (dx ? 8 * HALVES : 1));
         }
         *gave_up = 0;
         mbar_init_fence();
@@ -260,10 +279,10 @@ __global__ void __launch_bounds__(kThreads, 1) glu_narrow_kernel(const __grid_co
     wait_for_predecessor();
 
     if (warp == 0) {
-        if (elect_one()) load_rows<HALVES>(p, weights, stages, bars, gave_up);
+        if (elect_one()) load_rows<HALVES>(p, smem, bars, gave_up);
     } else if (warp == 1) {
         if (elect_one()) {
-            issue_products<HALVES>(p, weights, stages, bars, tmem, gave_up);
+            issue_products<HALVES>(p, smem, bars, tmem, gave_up);
             if (*gave_up) {
                 volatile int still = 0;
                 mma_commit<false>(bars + 8 * kDrain);
@@ -271,23 +290,22 @@ __global__ void __launch_bounds__(kThreads, 1) glu_narrow_kernel(const __grid_co
             }
         }
     } else {
-        // 32 rows, 32 columns of a buffer; the group's half or every other tile
-        const int quarter = warp & 3, col = ((warp - 2) >> 2 & 1) * 32;
+        // 32 rows and 32 columns of the units of a group: a half, or every other tile
+        const int quarter = warp & 3, part = (warp - 2) >> 2 & 1, col = part * 32;
         const uint32_t group = (uint32_t)(warp - 2) >> 3;
         const uint32_t row = quarter * 32 + lane, mine = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t piece = row * 128 + (((uint32_t)(col >> 3) ^ (row & 7)) << 4);   // its columns' first 16 bytes in a box
-        const int dx_col = HALVES == 1 ? col : (int)group * 32 + col / 2;
-        constexpr uint32_t kTurn = 2 / HALVES;
-        const uint32_t tiles = (p.tiles - blockIdx.x + gridDim.x - 1) / gridDim.x;
+        const int dx_col = HALVES == 1 ? col : (int)group * 32 + part * 16;
+        constexpr uint32_t kTurn = 2 / HALVES;   // tiles from one of a group's units to the next
+        const uint32_t tiles = own_tiles(p);
         const auto row_of = [&](uint32_t i) { return (blockIdx.x + i * gridDim.x) * kTileRows + row; };
         const int live = p.hidden - (HALVES == 1 ? 0 : (int)group * kHalf) - col;   // columns of the layer from col on
         bool ok = true;
-        uint32_t i = HALVES == 1 ? group : 0;
-        for (; i < tiles; i += kTurn) {
-            const uint32_t at = stages + S::stage(i) * S::kStage + (HALVES == 1 ? 0 : group * kBox) + piece;
-            const uint32_t nth = HALVES == 1 ? i >> 1 : i;
-            ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (kFull + S::stage(i)), S::phase(i), gave_up) &&
-                                             mbar_wait(bars + 8 * (kGuFull + group), nth & 1, gave_up));
+        uint32_t i = HALVES == 1 ? group : 0, u = group;
+        for (; i < tiles; i += kTurn, u += 2) {
+            const uint32_t at = smem + S::kWeights + u % kStages * S::kStage + piece;
+            ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (kFull + u % kStages), u / kStages & 1, gave_up) &&
+                                             mbar_wait(bars + 8 * (kGuFull + group), u >> 1 & 1, gave_up));
             if (!ok) break;
             tc_fence_after();
             uint32_t raw[2][16], up[2][16];
@@ -327,14 +345,14 @@ __global__ void __launch_bounds__(kThreads, 1) glu_narrow_kernel(const __grid_co
                 for (int e = 0; e < 2; ++e) {
                     st_shared16(a ^ (e << 4), make_uint4(pack_half2(g[8 * e], g[8 * e + 1], T), pack_half2(g[8 * e + 2], g[8 * e + 3], T),
                                                          pack_half2(g[8 * e + 4], g[8 * e + 5], T), pack_half2(g[8 * e + 6], g[8 * e + 7], T)));
-                    st_shared16((a ^ (e << 4)) + S::kAtDu,
+                    st_shared16((a ^ (e << 4)) + kBox,
                                 make_uint4(pack_half2(u[8 * e], u[8 * e + 1], T), pack_half2(u[8 * e + 2], u[8 * e + 3], T),
                                            pack_half2(u[8 * e + 4], u[8 * e + 5], T), pack_half2(u[8 * e + 6], u[8 * e + 7], T)));
                 }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the products read what was just written
             __syncwarp();
-            if (lane == 0) mbar_arrive(bars + 8 * (kGradFull + S::stage(i)));
+            if (lane == 0) mbar_arrive(bars + 8 * (kGradFull + u % kStages));
             if (i >= kTurn && p.dx) {   // the dx of the tile before is ready by now
                 ok = store_dx<T, HALVES>(p, i - kTurn, row_of(i - kTurn), dx_col, mine, bars, lane, gave_up);
                 if (!ok) break;
@@ -343,15 +361,18 @@ __global__ void __launch_bounds__(kThreads, 1) glu_narrow_kernel(const __grid_co
         if (ok && p.dx && i >= kTurn) ok = store_dx<T, HALVES>(p, i - kTurn, row_of(i - kTurn), dx_col, mine, bars, lane, gave_up);
         if (ok && p.dw[0] && __all_sync(0xffffffffu, mbar_wait(bars + 8 * kDone, 0, gave_up))) {
             tc_fence_after();
+            // lanes: a half's 64 rows of dWg, then of dWu
+            const uint32_t half = HALVES == 1 ? 0 : group, which = row >> 6;
+            const int hidden = (int)(half * kHalf + (row & 63)), from = HALVES == 1 ? (int)group * 32 + part * 16 : col;
 #pragma unroll 1
-            for (int c = col; c < col + 32; c += 16) {
+            for (int c = from; c < from + 16 * HALVES; c += 16) {
                 uint32_t v[16];
-                tmem_ld16(mine + kTmemDw + group * 64 + c, v);
+                tmem_ld16(mine + kTmemDw + half * 64 + c, v);
                 tmem_ld_wait(v);
-                float* to = p.dw[group] + ((int64_t)blockIdx.x * p.hidden + row) * p.pitch + c;
+                float* to = p.dw[which] + ((int64_t)blockIdx.x * p.hidden + hidden) * p.pitch + c;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if ((int)row < p.hidden && c + 4 * e < p.pitch)
+                    if (hidden < p.hidden && c + 4 * e < p.pitch)
                         *reinterpret_cast<uint4*>(to + 4 * e) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
             }
             tc_fence_before();
