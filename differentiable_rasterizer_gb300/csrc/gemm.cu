@@ -997,14 +997,16 @@ struct Tile {
     bool pair;
     double per_kb;   // cycles a k-block (128 bytes of k) takes
     double per_clk;  // bytes a cycle its epilogue moves
+    double values;   // its epilogue's arithmetic, relative: the wide pair's rows are staged in halves
 };
 // An SM takes in 64 bytes a cycle: 24, 32, 24 and 32 KB a k-block, against 128, 256,
 // 256 and 512 cycles of products.  So the wide pair alone keeps the tensor cores fed.
-// These rates and the cycles below are fitted to the times of all four shapes at 44
-// sizes (500 to 1,000,000 rows, k 64 to 4096, plain, with activation, gated, 8 bits,
-// gradients): the choice is within 6 % of the best shape, 20 % at 5 us (100,000 x 256 ->
-// 1024: 61 us with the narrow pair, 54 with the wide one).
-constexpr Tile kTiles[4] = {{64, false, 450, 22}, {128, false, 440, 21}, {128, true, 430, 19}, {256, true, 690, 21}};
+// These rates and the cycles below are fitted to the times of all four shapes at 62
+// sizes (500 to 1,000,000 rows, k 32 to 4096, plain, with activation, gated, 8 bits,
+// gradients): the choice is within 10 % of the best shape (100,000 x 256 -> 1024: 61 us
+// with the narrow pair, 54 with the wide one; gated 1,000,000 x 64 -> 128: 101 with the
+// wide pair, 84 with 128 x 128).
+constexpr Tile kTiles[4] = {{64, false, 450, 22, 0.8}, {128, false, 570, 22, 0.95}, {128, true, 550, 19, 0.9}, {256, true, 800, 20, 1.6}};
 
 // Cycles of a call with a tile shape: waves of tiles, each bound by its k-blocks or by
 // its epilogue's arithmetic and traffic, and a start-up.
@@ -1031,18 +1033,18 @@ double cost(const GemmCall& c, const Tile& t, int sms, GemmPlan* out)
     const double live = (double)(c.n < p.out_cols ? c.n : p.out_cols);
     // the weights' gradients: a plan, and so an order, that does not depend on the type they are rounded to
     const int bytes = (c.a[0].k_fast ? type_bytes(c.out_type) : 4) * (c.residual ? 2 : 1) + (c.z ? (glu ? 4 : 2) : 0);
-    const double per_value = glu ? 0.13 : (c.act != GS_ACT_NONE ? 0.17 : (c.type == GS_E4M3 ? 0.04 : 0.02));
+    const double per_value = t.values * (glu ? 0.055 : (c.act != GS_ACT_NONE ? 0.18 : (c.type == GS_E4M3 ? 0.04 : 0.0)));
     double best = 0;
     int64_t most = sum_only ? slots / tiles : 1;
     if (most > kb / 4) most = kb / 4;
     if (most < 1) most = 1;
     for (int64_t s = 1; s <= most; s = s == most ? most + 1 : (s + s / 2 + 1 < most ? s + s / 2 + 1 : most)) {
         const double main = t.per_kb * (double)((kb + s - 1) / s);
-        const double epi = 650 + 128.0 * live * (per_value + (s > 1 ? 4 : bytes) / t.per_clk);
+        const double epi = 460 + 128.0 * live * (per_value + (s > 1 ? 4 : bytes) / t.per_clk);
         const double waves = (double)((tiles * s + slots - 1) / slots);
         // the join: a launch, and every partial sum read once at about 20 bytes a cycle and SM
         const double join = s > 1 ? 4500 + (double)s * c.m * c.n * p.probs * 4 / (sms * 20.0) : 0;
-        const double v = 5700 + waves * (main > epi ? main : epi) + (main > epi ? epi : main) + join;
+        const double v = 6300 + waves * (main > epi ? main : epi) + (main > epi ? epi : main) + join;
         if (s == 1 || v < best) {
             best = v;
             p.splits = (int)s;
