@@ -999,8 +999,9 @@ struct Tile {
     double per_clk;  // bytes a cycle its epilogue moves
     double values;   // its epilogue's arithmetic, relative: the wide pair's rows are staged in halves
 };
-// An SM takes in 64 bytes a cycle: 24, 32, 24 and 32 KB a k-block, against 128, 256,
-// 256 and 512 cycles of products.  So the wide pair alone keeps the tensor cores fed.
+// A k-block of the three smaller tiles takes 350 to 420 cycles against 128, 256 and 256 of
+// products, whatever its bytes (one factor alone: the same), its MMAs (one of four: 330) or
+// the ring's depth; the wide pair's 520 against 512.  So that alone keeps the tensor cores fed.
 // These rates and the cycles below are fitted to the times of all four shapes at 62
 // sizes (500 to 1,000,000 rows, k 32 to 4096, plain, with activation, gated, 8 bits,
 // gradients): the choice is within 10 % of the best shape (100,000 x 256 -> 1024: 61 us
