@@ -343,6 +343,13 @@ __device__ __forceinline__ void store_chunk(uint32_t slot, Residual<ROW, OSZ>& r
     }
 }
 
+template <int T>
+__device__ __forceinline__ void pack_half16(uint32_t (&w)[8], const float (&v)[16])
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = pack_half2(v[2 * j], v[2 * j + 1], T);
+}
+
 template <int ACT>
 __device__ __forceinline__ void activate(float (&v)[16])
 {
@@ -723,6 +730,22 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     const int type = last ? p.out_type : p.z_type;
                     const int64_t ld = last ? p.ldy[q.prob] : (GLU && pass == 1 ? p.ldz2 : p.ldz);
                     uint16_t* to = (uint16_t*)(last ? p.yp[q.prob] : (GLU && pass == 1 ? p.z2p : p.zp)) + row0 * ld + col0;
+                    // The wide pair's slots hold half lines: where a thread's 32 bytes are a sector they go
+                    // straight out (1,000,000 x 64 -> 192 95 us staged, 81 so; gated 100,000 x 256 -> 512
+                    // 54, 45; in the other shapes up to 7 % slower).
+                    if (BN == 256 && cols >= kGroupCols && (((uintptr_t)to | (uintptr_t)(ld * 2)) & 31) == 0) {
+                        to += lane * ld;
+#pragma unroll 1
+                        for (int c = 0; c < kGroupCols; c += 16) {
+                            float v[16];
+                            columns16(c, pass, v);
+                            uint32_t w[8];
+                            if (type == GS_BF16) pack_half16<GS_BF16>(w, v);
+                            else pack_half16<GS_F16>(w, v);
+                            if (lane < rows) st_global32(to + c, w);
+                        }
+                        continue;
+                    }
 #pragma unroll 1
                     for (int c = 0; c < kGroupCols && c < cols; c += kCols, to += kCols) {
                         __syncwarp();   // the slot's last readers are done
@@ -997,7 +1020,7 @@ struct Tile {
     bool pair;
     double per_kb;   // cycles a k-block (128 bytes of k) takes
     double per_clk;  // bytes a cycle its epilogue moves
-    double values;   // its epilogue's arithmetic, relative: the wide pair's rows are staged in halves
+    double values;   // its epilogue's arithmetic, relative
 };
 // A k-block of the three smaller tiles takes 350 to 420 cycles against 128, 256 and 256 of
 // products, whatever its bytes (one factor alone: the same), its MMAs (one of four: 330) or
@@ -1005,9 +1028,8 @@ struct Tile {
 // These rates and the cycles below are fitted to the times of all four shapes at 62
 // sizes (500 to 1,000,000 rows, k 32 to 4096, plain, with activation, gated, 8 bits,
 // gradients): the choice is within 10 % of the best shape (100,000 x 256 -> 1024: 61 us
-// with the narrow pair, 54 with the wide one; gated 1,000,000 x 64 -> 128: 101 with the
-// wide pair, 84 with 128 x 128).
-constexpr Tile kTiles[4] = {{64, false, 450, 22, 0.8}, {128, false, 570, 22, 0.95}, {128, true, 550, 19, 0.9}, {256, true, 800, 20, 1.6}};
+// with the narrow pair, 55 with the wide one; gated 100,000 x 256 -> 512: 55, 47).
+constexpr Tile kTiles[4] = {{64, false, 480, 22.5, 0.92}, {128, false, 560, 22, 0.95}, {128, true, 550, 19, 0.89}, {256, true, 800, 19.3, 1.15}};
 
 // Cycles of a call with a tile shape: waves of tiles, each bound by its k-blocks or by
 // its epilogue's arithmetic and traffic, and a start-up.
@@ -1034,18 +1056,18 @@ double cost(const GemmCall& c, const Tile& t, int sms, GemmPlan* out)
     const double live = (double)(c.n < p.out_cols ? c.n : p.out_cols);
     // the weights' gradients: a plan, and so an order, that does not depend on the type they are rounded to
     const int bytes = (c.a[0].k_fast ? type_bytes(c.out_type) : 4) * (c.residual ? 2 : 1) + (c.z ? (glu ? 4 : 2) : 0);
-    const double per_value = t.values * (glu ? 0.055 : (c.act != GS_ACT_NONE ? 0.18 : (c.type == GS_E4M3 ? 0.04 : 0.0)));
+    const double per_value = t.values * (glu ? 0.048 : (c.act != GS_ACT_NONE ? 0.185 : (c.type == GS_E4M3 ? 0.048 : 0.0)));
     double best = 0;
     int64_t most = sum_only ? slots / tiles : 1;
     if (most > kb / 4) most = kb / 4;
     if (most < 1) most = 1;
     for (int64_t s = 1; s <= most; s = s == most ? most + 1 : (s + s / 2 + 1 < most ? s + s / 2 + 1 : most)) {
         const double main = t.per_kb * (double)((kb + s - 1) / s);
-        const double epi = 460 + 128.0 * live * (per_value + (s > 1 ? 4 : bytes) / t.per_clk);
+        const double epi = 390 + 128.0 * live * (per_value + (s > 1 ? 4 : bytes) / t.per_clk);
         const double waves = (double)((tiles * s + slots - 1) / slots);
         // the join: a launch, and every partial sum read once at about 20 bytes a cycle and SM
         const double join = s > 1 ? 4500 + (double)s * c.m * c.n * p.probs * 4 / (sms * 20.0) : 0;
-        const double v = 6300 + waves * (main > epi ? main : epi) + (main > epi ? epi : main) + join;
+        const double v = 6400 + waves * (main > epi ? main : epi) + (main > epi ? epi : main) + join;
         if (s == 1 || v < best) {
             best = v;
             p.splits = (int)s;

@@ -229,9 +229,7 @@ __device__ __forceinline__ bool store_dx(const Params& p, uint32_t i, uint32_t r
 #pragma unroll
         for (int j = 0; j < 8; ++j) w[j] = pack_half2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]), T);
         if (p.dx_vec == 2 && left >= 16) {   // whole sectors
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                         "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                         : "memory");
+            st_global32(to, w);
             continue;
         }
 #pragma unroll

@@ -57,6 +57,14 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t a)
     return v;
 }
 
+// A sector: 32 bytes, so aligned.
+__device__ __forceinline__ void st_global32(void* p, const uint32_t (&w)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 // ------------------------------------------------------------------ mbarriers
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
 {
