@@ -291,25 +291,40 @@ __device__ __forceinline__ float rcp_fast(float v)
     return r;
 }
 
-// sigma(v): relative error below 2^-20 (two roundings of |v| log2 e and the
-// instructions' 2 ulp), far inside the 16-bit results.  For v below about -88 the
-// exponential is infinite and the reciprocal 0, as it should be.
+// sigma(v): relative error below 2^-21 + |v| 2^-23 (the instructions' 2 and 1 ulp; two
+// roundings of |v| log2 e, which the exponential multiplies by |v|).  For v below about
+// -88 the exponential is infinite and the reciprocal 0, as it should be.
 __device__ __forceinline__ float sigmoid_fast(float v) { return rcp_fast(1.0f + exp2_fast(-1.4426950408889634f * v)); }
 
 // Phi(v), the normal distribution function, and e = exp(-v^2 / 2), which its slope
-// shares:  Phi(-|v|) = (a1 t + ... + a5 t^5) e / 2,  t = 1 / (1 + p |v| / sqrt 2)
-// (Abramowitz & Stegun, Handbook of Mathematical Functions, 7.1.26: |error| of erf
-// below 1.5e-7).  Taken on the negative side, so that small tails do not cancel.
+// shares:  Phi(-|v|) = (c1 t + ... + c8 t^8) e,  t = 1 / (1 + p |v|).
+// The form is that of Abramowitz & Stegun, Handbook of Mathematical Functions, 7.1.26;
+// the coefficients are a minimax fit of the relative error over 0 <= |v| <= 13.4 (1.3e-7;
+// beyond, e is below fp32's normal range).  Taken on the negative side and chosen by the
+// sign, so that the tail keeps its digits: with the instructions' errors Phi is within
+// 2^-20 + v^2 2^-23 of itself (the latter from rounding v^2, so 2^-16 at -10).  1/2 +
+// sign(v) (1/2 - Phi(-|v|)) would lose the tail in the subtraction, GELU below -5 with it.
 // An erff and a second exponential cost three times as many instructions, which
 // is what bounded the elementwise gradients and the epilogues.
+constexpr float kPhiP = 0.3f;
+__host__ __device__ constexpr float phi_coeff(int i)   // c[i + 1]
+{
+    return i == 0   ? 0.119625784f
+           : i == 1 ? 0.120807543f
+           : i == 2 ? 0.0995807424f
+           : i == 3 ? 0.129654914f
+           : i == 4 ? -0.0557424501f
+           : i == 5 ? 0.208583161f
+           : i == 6 ? -0.158493474f
+                    : 0.0359837115f;
+}
 __device__ __forceinline__ float normal_cdf(float v, float& e)
 {
-    const float t = rcp_fast(__fmaf_rn(fabsf(v), 0.3275911f * 0.70710678f, 1.0f));
+    const float t = rcp_fast(__fmaf_rn(fabsf(v), kPhiP, 1.0f));
     e = exp2_fast(v * v * (-0.5f * 1.4426950408889634f));
-    float q = __fmaf_rn(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
-    q = __fmaf_rn(t, q, 0.5f * 1.421413741f);
-    q = __fmaf_rn(t, q, 0.5f * -0.284496736f);
-    q = __fmaf_rn(t, q, 0.5f * 0.254829592f);
+    float q = phi_coeff(7);
+#pragma unroll
+    for (int i = 6; i >= 0; --i) q = __fmaf_rn(t, q, phi_coeff(i));
     q = q * t * e;
     return v < 0.0f ? q : 1.0f - q;
 }
@@ -358,24 +373,21 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
     return r;
 }
 
-// Phi of two values as normal_cdf computes it, but 1/2 + sign(v) (1/2 - q): in pairs that
-// is cheaper than a choice, and off by half a unit of 1/2 more.
+// Phi of two values, to the bit as normal_cdf computes it.
 __device__ __forceinline__ uint64_t normal_cdf2(uint64_t v, uint64_t& e)
 {
-    const float2 f = unpair(v);
-    const float2 d = unpair(fma2(pair(fabsf(f.x), fabsf(f.y)), pair(0.3275911f * 0.70710678f, 0.3275911f * 0.70710678f),
-                                 pair(1.0f, 1.0f)));
-    const uint64_t t = pair(rcp_fast(d.x), rcp_fast(d.y));
-    const float kE = -0.5f * 1.4426950408889634f;
-    const float2 x = unpair(mul2(mul2(v, v), pair(kE, kE)));
-    e = pair(exp2_fast(x.x), exp2_fast(x.y));
     const auto both = [](float c) { return pair(c, c); };
-    uint64_t q = fma2(t, both(0.5f * 1.061405429f), both(0.5f * -1.453152027f));
-    q = fma2(t, q, both(0.5f * 1.421413741f));
-    q = fma2(t, q, both(0.5f * -0.284496736f));
-    q = fma2(t, q, both(0.5f * 0.254829592f));
-    const float2 h = unpair(fma2(mul2(q, t), mul2(e, both(-1.0f)), both(0.5f)));
-    return add2(pair(copysignf(h.x, f.x), copysignf(h.y, f.y)), both(0.5f));
+    const float2 f = unpair(v);
+    const float2 d = unpair(fma2(pair(fabsf(f.x), fabsf(f.y)), both(kPhiP), both(1.0f)));
+    const uint64_t t = pair(rcp_fast(d.x), rcp_fast(d.y));
+    const float2 x = unpair(mul2(mul2(v, v), both(-0.5f * 1.4426950408889634f)));
+    e = pair(exp2_fast(x.x), exp2_fast(x.y));
+    uint64_t q = both(phi_coeff(7));
+#pragma unroll
+    for (int i = 6; i >= 0; --i) q = fma2(t, q, both(phi_coeff(i)));
+    q = mul2(mul2(q, t), e);
+    const float2 lo = unpair(q), hi = unpair(fma2(q, both(-1.0f), both(1.0f)));
+    return pair(f.x < 0.0f ? lo.x : hi.x, f.y < 0.0f ? lo.y : hi.y);
 }
 
 template <int ACT>

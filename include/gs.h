@@ -458,6 +458,10 @@ GS_API gs_status gs_check_report(uint64_t* report, int32_t* checked);
  *   - Sums, norms and products are accumulated in fp32; each output is rounded
  *     to its type once, to nearest even.  Results do not depend on the run:
  *     there are no atomics on values, split sums are joined in a fixed order.
+ *     fp32 outputs are as good as these: the tensor cores truncate as they add
+ *     (a product of K terms is within K 2^-23 of the sum of their magnitudes),
+ *     SILU's factor is within 2^-21 + |v| 2^-23 of itself, GELU's within
+ *     2^-20 + v^2 2^-23, tails included, down to fp32's normal range.
  *   - NULL marks an optional array that is absent.  Scale vectors are fp32.
  *   - ws / ws_bytes: scratch of 256-byte alignment; ws == NULL queries the size
  *     into *ws_bytes and does nothing else; where that size is 0, both may be
