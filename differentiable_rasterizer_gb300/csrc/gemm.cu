@@ -371,8 +371,12 @@ __device__ __forceinline__ void activate(float (&v)[16], int act)
 // the factors' orders are constants, the ring is stepped, addresses are added to
 // (with all of that in the loop a k-block took 500 cycles whatever its products:
 // 2048 x 4096 -> 1024 19 us).
+// load_tiles returns the stages it has filled.  It stops when its own wait has run out,
+// not when another role gives up: a stage is freed in both CTAs of a pair by one commit,
+// so both producers stop behind the same copies, and the first CTA's barriers, which count
+// both CTAs' bytes, tell when all of them have landed.
 template <int BN, bool PAIR, bool GLU, bool A_FAST, bool B_FAST>
-__device__ __forceinline__ void load_tiles(const Params& p, uint32_t first, uint32_t step, uint32_t rank, uint32_t stages,
+__device__ __forceinline__ uint32_t load_tiles(const Params& p, uint32_t first, uint32_t step, uint32_t rank, uint32_t stages,
                                            uint32_t bar_full, uint32_t bar_empty, volatile int* gave_up)
 {
     using S = Shape<BN, PAIR, GLU>;
@@ -392,14 +396,9 @@ __device__ __forceinline__ void load_tiles(const Params& p, uint32_t first, uint
             const CUtensorMap *a = &p.a[which], *b = &p.b[GLU && PAIR ? rank : which];
             int k = (int)(kb - term * k_blocks) * k_elems;
             for (; kb < end; ++kb, k += k_elems, ++issued) {
-                if (!mbar_wait(bar_empty + 8 * ring.s, ring.parity ^ 1, gave_up)) {
-                    // given up: let the copies in flight land before the block leaves
-                    volatile int still = 0;
-                    for (int i = 0; rank == 0 && i < S::kStages && (uint32_t)i < issued; ++i) {
-                        const uint32_t s = (ring.s + S::kStages - 1 - i) % S::kStages;
-                        mbar_wait(bar_full + 8 * s, s < ring.s ? ring.parity : ring.parity ^ 1, &still);
-                    }
-                    return;
+                if (!mbar_wait_alone(bar_empty + 8 * ring.s, ring.parity ^ 1)) {
+                    *gave_up = 1;
+                    return issued;
                 }
                 const uint32_t full = full0 + 8 * ring.s, sa = stages + ring.s * S::kStageBytes, sb = sa + S::kBytesA;
                 if (rank == 0) mbar_expect(bar_full + 8 * ring.s, S::kStageBytes * (PAIR ? 2 : 1));
@@ -418,6 +417,7 @@ __device__ __forceinline__ void load_tiles(const Params& p, uint32_t first, uint
             }
         }
     }
+    return issued;
 }
 
 template <int BN, bool PAIR, bool GLU, bool A_FAST, bool B_FAST, bool E4M3>
@@ -543,11 +543,16 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         if (elect_one()) {
             prefetch_map(&p.a[0]);
             prefetch_map(&p.b[0]);
-            if (p.b_fast) load_tiles<BN, PAIR, GLU, true, true>(p, first, step, rank, stages, bar_full, bar_empty, gave_up);
+            uint32_t issued = 0;
+            if (p.b_fast) issued = load_tiles<BN, PAIR, GLU, true, true>(p, first, step, rank, stages, bar_full, bar_empty, gave_up);
             else if constexpr (!GLU) {
-                if (p.a_fast) load_tiles<BN, PAIR, GLU, true, false>(p, first, step, rank, stages, bar_full, bar_empty, gave_up);
-                else load_tiles<BN, PAIR, GLU, false, false>(p, first, step, rank, stages, bar_full, bar_empty, gave_up);
+                if (p.a_fast) issued = load_tiles<BN, PAIR, GLU, true, false>(p, first, step, rank, stages, bar_full, bar_empty, gave_up);
+                else issued = load_tiles<BN, PAIR, GLU, false, false>(p, first, step, rank, stages, bar_full, bar_empty, gave_up);
             }
+            // the block does not leave before its copies have landed (the pair: at its last cluster barrier)
+            bool landed = true;
+            if (rank == 0)
+                last_copies<S::kStages>(issued, [&](uint32_t s, uint32_t parity) { landed = landed && mbar_wait_alone(bar_full + 8 * s, parity); });
         }
     } else if (warp == 1) {
         if (rank == 0 && elect_one()) {
@@ -564,9 +569,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 else issue(no, no, no);
             }
             if (*gave_up) {
-                volatile int still = 0;
                 mma_commit<PAIR>(bar_drain);
-                mbar_wait(bar_drain, 0, &still);
+                mbar_wait_alone(bar_drain, 0);
             }
         }
     } else {
@@ -894,16 +898,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
     if (warp == 0) {
         if (elect_one()) {
             Ring<S::kStages> ring;   // round 1 on: a stage is sent again once its products are done
-            for (uint32_t kb = kb_first; kb < kb1; ++kb) {
-                if (!mbar_wait(bar_empty + 8 * ring.s, ring.parity, gave_up)) {
-                    volatile int still = 0;   // given up: let the copies in flight land
-                    for (uint32_t s = 0; s < S::kStages; ++s)
-                        mbar_wait(bar_full + 8 * s, s < ring.s ? ring.parity ^ 1 : ring.parity, &still);
-                    break;
-                }
+            uint32_t sent = kb_first - kb0;
+            for (uint32_t kb = kb_first; kb < kb1; ++kb, ++sent) {
+                if (!mbar_wait(bar_empty + 8 * ring.s, ring.parity, gave_up)) break;
                 send(ring.s, kb);
                 ring.next();
             }
+            bool landed = true;   // the ring is not used again before the copies have landed
+            last_copies<S::kStages>(sent, [&](uint32_t s, uint32_t parity) { landed = landed && mbar_wait_alone(bar_full + 8 * s, parity); });
         }
     } else if (warp == 1) {
         if (elect_one()) {
@@ -924,11 +926,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
                 ring.next();
             }
             mma_commit<false>(bar_acc);   // every product so far, also after giving up
+            if (!mbar_wait_alone(bar_acc, 0)) *gave_up = 1;
         }
     }
     __syncwarp();
     mbar_wait(bar_acc, 0, gave_up);
-    __syncthreads();   // every wait of the block has ended; the ring is free for the partial sums
+    __syncthreads();   // copies and products are done; the ring is free for the partial sums
     tc_fence_after();
     // partial[row][feature]: 128 features a row
     if (warp < 4) {

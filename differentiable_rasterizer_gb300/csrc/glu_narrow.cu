@@ -123,12 +123,9 @@ __device__ __forceinline__ void load_rows(const Params& p, uint32_t smem, uint32
         }
     }
     // the block does not leave before its copies have landed
-    volatile int still = 0;
-    mbar_wait(bars + 8 * kWFull, 0, &still);
-    for (uint32_t j = xs > S::kStagesX ? xs - S::kStagesX : 0; j < xs; ++j)
-        mbar_wait(bars + 8 * (kXFull + j % S::kStagesX), j / S::kStagesX & 1, &still);
-    for (uint32_t j = units > kStages ? units - kStages : 0; j < units; ++j)
-        mbar_wait(bars + 8 * (kFull + j % kStages), j / kStages & 1, &still);
+    bool landed = mbar_wait_alone(bars + 8 * kWFull, 0);
+    last_copies<S::kStagesX>(xs, [&](uint32_t s, uint32_t parity) { landed = landed && mbar_wait_alone(bars + 8 * (kXFull + s), parity); });
+    last_copies<kStages>(units, [&](uint32_t s, uint32_t parity) { landed = landed && mbar_wait_alone(bars + 8 * (kFull + s), parity); });
 }
 
 // Two kinds of work in the order in which they become ready: a unit's g and u, when its x
@@ -282,9 +279,8 @@ __global__ void __launch_bounds__(kThreads, 1) glu_narrow_kernel(const __grid_co
         if (elect_one()) {
             issue_products<HALVES>(p, smem, bars, tmem, gave_up);
             if (*gave_up) {
-                volatile int still = 0;
                 mma_commit<false>(bars + 8 * kDrain);
-                mbar_wait(bars + 8 * kDrain, 0, &still);
+                mbar_wait_alone(bars + 8 * kDrain, 0);
             }
         }
     } else {

@@ -118,10 +118,13 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
 
 // Every wait is bounded: after kWaitCycles (about two seconds) without the phase,
 // or once another role of the block has given up, it sets the block's flag and
-// returns false; the caller leaves its loop, and the kernel drains and returns.
+// returns false; the caller leaves its loop.  Then the block drains: its copies and its
+// tensor-core work are waited for once more, each by a thread that does not look at the
+// flag (mbar_wait_alone), before shared memory is used again, TMEM freed or the kernel left.
 constexpr long long kWaitCycles = 4000000000ll;
 
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up)
+template <class Stop>
+__device__ __forceinline__ bool mbar_wait_until(uint32_t bar, uint32_t parity, Stop stop)
 {
     long long t0 = 0;
     while (true) {
@@ -130,12 +133,29 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
             if (mbar_try(bar, parity)) return true;
         const long long t = clock64();
         if (t0 == 0) t0 = t;
-        if (*gave_up) return false;
-        if (t - t0 > kWaitCycles) {
-            *gave_up = 1;
-            return false;
-        }
+        if (stop(t - t0 > kWaitCycles)) return false;
     }
+}
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up)
+{
+    return mbar_wait_until(bar, parity, [&](bool late) {
+        if (*gave_up) return true;
+        if (late) *gave_up = 1;
+        return late;
+    });
+}
+__device__ __forceinline__ bool mbar_wait_alone(uint32_t bar, uint32_t parity)
+{
+    return mbar_wait_until(bar, parity, [](bool late) { return late; });
+}
+
+// The stages and parities to wait for before a producer may leave: the last N of the
+// `issued` copies into a ring of N stages, copy j in stage j % N in that stage's round
+// j / N.  The earlier ones' stages were free, so they have landed.
+template <uint32_t N, class F>
+__host__ __device__ __forceinline__ void last_copies(uint32_t issued, F wait_for)
+{
+    for (uint32_t j = issued > N ? issued - N : 0; j < issued; ++j) wait_for(j % N, j / N & 1);
 }
 
 // ------------------------------------------------------------------ TMA
