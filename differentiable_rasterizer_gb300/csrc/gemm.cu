@@ -1184,6 +1184,16 @@ GemmPlan gemm_plan(const GemmCall& c)
     return p;
 }
 
+// The epilogue waits for a whole unit's contraction under kWaitCycles (4e9 cycles), and a
+// k-block takes at most about 1500 cycles (the wide pair's 64 KB with all SMs on HBM).
+constexpr int64_t kMostKBlocks = 1 << 21;
+
+bool gemm_fits(const GemmPlan& p)
+{
+    const int64_t parts = p.nb ? p.ranks : p.splits;
+    return p.k_blocks * p.terms <= kMostKBlocks * (parts > 0 ? parts : 1);
+}
+
 gs_status gemm_run(const GemmCall& c, const GemmPlan& plan, void* ws, JoinJobs* joins, cudaStream_t st)
 {
     if (plan.units > 0x7fffffffll || c.m > 0x7fffff00ll || c.n > 0x7fffff00ll || c.k > 0x7fffff00ll)

@@ -56,6 +56,9 @@ struct GemmPlan {
     size_t bytes;    // of the partial sums: the call's scratch
 };
 GemmPlan gemm_plan(const GemmCall& c);
+// Whether a CTA's part of the contraction ends well within the bound of a wait for it (a
+// default plan: no product, fits).
+bool gemm_fits(const GemmPlan& p);
 
 // Multiprocessors of the current device (0 if there is none).
 int device_sms();

@@ -390,6 +390,7 @@ extern "C" gs_status gs_linear(const gs_linear_args* args, void* ws, size_t* ws_
     size_t at = 0;
     if (a.rows > 0) {
         plan = gemm_plan(c);
+        if (!gemm_fits(plan)) return GS_ERR_INVALID_ARG;
         x = aligned_rows(sc, true, a.x, a.ldx, c.m, c.k, a.type);
         w = aligned_rows(sc, true, a.w, a.ldw, c.n, c.k, a.type);
         at = sc.take(plan.bytes);
@@ -444,6 +445,7 @@ extern "C" gs_status gs_linear_bwd(const gs_linear_bwd_args* args, void* ws, siz
     GemmPlan px = {}, pw = {};
     if (m > 0 && a.dx) px = gemm_plan(cx);
     if (m > 0 && a.dw) pw = gemm_plan(cw);
+    if (!gemm_fits(px) || !gemm_fits(pw)) return GS_ERR_INVALID_ARG;
     Rows dz = aligned_rows(sc, m > 0 && products && !make_dz, a.dy, a.lddy, m, n, a.type);
     Rows w = aligned_rows(sc, m > 0 && a.dx, a.w, a.ldw, n, k, a.type);
     Rows x = aligned_rows(sc, m > 0 && a.dw, a.x, a.ldx, m, k, a.type);
@@ -530,6 +532,7 @@ extern "C" gs_status gs_glu(const gs_glu_args* args, void* ws, size_t* ws_bytes,
     Rows x, wg, wu;
     if (a.rows > 0) {
         plan = gemm_plan(c);
+        if (!gemm_fits(plan)) return GS_ERR_INVALID_ARG;
         x = aligned_rows(sc, true, a.x, a.ldx, c.m, c.k, a.type);
         wg = aligned_rows(sc, true, a.w_gate, a.ldwg, c.n, c.k, a.type);
         wu = aligned_rows(sc, true, a.w_up, a.ldwu, c.n, c.k, a.type);
@@ -620,6 +623,7 @@ extern "C" gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* w
     if (m > 0 && a.dx) px = gemm_plan(cx);
     if (m > 0 && a.dw_gate) pw = gemm_plan(cw);
     if (m > 0 && again) pg = gemm_plan(cg);
+    if (!gemm_fits(px) || !gemm_fits(pw) || !gemm_fits(pg)) return GS_ERR_INVALID_ARG;
     Rows x = aligned_rows(sc, m > 0 && (again || a.dw_gate), a.x, a.ldx, m, k, a.type);
     Rows wg = aligned_rows(sc, m > 0 && (again || a.dx), a.w_gate, a.ldwg, f, k, a.type);
     Rows wu = aligned_rows(sc, m > 0 && (again || a.dx), a.w_up, a.ldwu, f, k, a.type);

@@ -455,6 +455,9 @@ GS_API gs_status gs_check_report(uint64_t* report, int32_t* checked);
  *     other operands are first copied to aligned rows in the workspace.
  *   - rows = 0 is valid (gradients of weights are then zero); features >= 1.
  *     Sizes are below 2^31; products of sizes and offsets are 64-bit.
+ *     A contraction that would keep one multiprocessor past the bound of its
+ *     waits (2^27 16-bit or 2^28 8-bit elements, where it is not split) is
+ *     refused: INVALID_ARG.
  *   - Sums, norms and products are accumulated in fp32; each output is rounded
  *     to its type once, to nearest even.  Results do not depend on the run:
  *     there are no atomics on values, split sums are joined in a fixed order.
