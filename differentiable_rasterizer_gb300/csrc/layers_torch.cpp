@@ -177,8 +177,25 @@ int type_arg(PyObject* o, const char* name, unsigned types, int fallback)
     return c;
 }
 
-bool flag(PyObject* o) { return o == Py_True || (o != Py_False && PyObject_IsTrue(o) == 1); }
-int code(PyObject* o) { return (int)PyLong_AsLong(o); }
+bool flag(PyObject* o, const char* name)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) {
+        PyErr_Clear();
+        refuse(std::string(name) + ": expected a truth value, got " + Py_TYPE(o)->tp_name);
+    }
+    return v == 1;
+}
+float number(PyObject* o, const char* name)
+{
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) {
+        PyErr_Clear();
+        refuse(std::string(name) + ": expected a number, got " + Py_TYPE(o)->tp_name);
+    }
+    return (float)v;
+}
+int code(PyObject* o) { return (int)PyLong_AsLong(o); }   // of layers.py's own table
 
 // ------------------------------------------------------------------ outputs
 // [*lead, cols] like `like`'s leading dimensions, rows padded to 16 bytes.
@@ -281,7 +298,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n)
         gs_rms_norm_args g = {};
         g.rows = rx.rows, g.cols = rx.cols, g.x = rx.p, g.ldx = rx.ld, g.type = rx.type;
         g.weight = required(vector_of(a[1], "weight", kFloat, dev, rx.cols, &g.weight_type), "weight", 1);
-        g.eps = (float)PyFloat_AsDouble(a[3]);
+        g.eps = number(a[3], "eps");
         g.y_type = type_arg(a[4], "out_dtype", kFloat | kE4m3, rx.type);
         Tensor s = x, scale, rstd;
         if (a[2] != Py_None) {
@@ -293,7 +310,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n)
         const Out y = output(x, rx.rows, rx.cols, g.y_type);
         g.y = y.r.p, g.ldy = y.r.ld;
         if (g.y_type == GS_E4M3) g.y_scale = (scale = row_values(x)).data_ptr<float>();
-        if (flag(a[5])) g.rstd = (rstd = row_values(x)).data_ptr<float>();
+        if (flag(a[5], "need_backward")) g.rstd = (rstd = row_values(x)).data_ptr<float>();
         if (rx.rows) check("gs_rms_norm", lib.rms_norm(&g, c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream()));
         return result(y.t, scale, s, rstd);
     });
@@ -380,7 +397,7 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n)
             y = o.t;
             g.y = o.r.p, g.ldy = o.r.ld;
         }
-        if (flag(a[9]) && g.act != GS_ACT_NONE) {
+        if (flag(a[9], "need_backward") && g.act != GS_ACT_NONE) {
             if (rx.type == GS_E4M3) refuse("need_backward: 8-bit operands have no gradients");
             const Out o = output(x, rx.rows, w.rows, rx.type);
             z = o.t;
@@ -414,16 +431,16 @@ PyObject* linear_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
         g.dw_type = type_arg(a[8], "dw_dtype", 1u << rx.type | kF32, rx.type);
         g.db_type = type_arg(a[9], "db_dtype", kFloat, rx.type);
         Tensor dx, dw, db;
-        if (flag(a[6])) {
+        if (flag(a[6], "need_dx")) {
             const Out o = output(x, rx.rows, rx.cols, rx.type);
             dx = o.t;
             g.dx = o.r.p, g.lddx = o.r.ld;
         }
-        if (flag(a[7])) {
+        if (flag(a[7], "need_dw")) {
             dw = plain(x, {w.rows, rx.cols}, g.dw_type);
             g.dw = dw.data_ptr(), g.lddw = rx.cols;
         }
-        if (flag(a[5])) g.db = (db = plain(x, {w.rows}, g.db_type)).data_ptr();
+        if (flag(a[5], "bias")) g.db = (db = plain(x, {w.rows}, g.db_type)).data_ptr();
         with_scratch("gs_linear_bwd", lib.linear_bwd, g, x, dev, false);
         return result(dx, dw, db);
     });
@@ -452,7 +469,7 @@ PyObject* glu(PyObject*, PyObject* const* a, Py_ssize_t n)
         const Out h = output(x, rx.rows, wg.rows, g.out_type);
         g.h = h.r.p, g.ldh = h.r.ld;
         Tensor gate, up;
-        if (flag(a[8])) {
+        if (flag(a[8], "save")) {
             if (rx.type == GS_E4M3) refuse("need_backward: 8-bit operands have no gradients");
             const Out og = output(x, rx.rows, wg.rows, g.out_type), ou = output(x, rx.rows, wg.rows, g.out_type);
             gate = og.t, up = ou.t;
@@ -487,12 +504,12 @@ PyObject* glu_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
         g.act = code(a[6]);
         g.dw_type = type_arg(a[9], "dw_dtype", type | kF32, rx.type);
         Tensor dx, dwg, dwu;
-        if (flag(a[7])) {
+        if (flag(a[7], "need_dx")) {
             const Out o = output(x, rx.rows, rx.cols, rx.type);
             dx = o.t;
             g.dx = o.r.p, g.lddx = o.r.ld;
         }
-        if (flag(a[8])) {
+        if (flag(a[8], "need_dw")) {
             dwg = plain(x, {wg.rows, rx.cols}, g.dw_type);
             dwu = plain(x, {wg.rows, rx.cols}, g.dw_type);
             g.dw_gate = dwg.data_ptr(), g.lddwg = rx.cols, g.dw_up = dwu.data_ptr(), g.lddwu = rx.cols;

@@ -88,7 +88,7 @@ _native = _Native()
 
 
 def _act(act):
-    code = _ACTS.get(act)
+    code = _ACTS.get(act) if act is None or isinstance(act, str) else None
     if code is None:
         raise ValueError(f"act: {act!r} is not one of {[a for a in _ACTS if a]}")
     return code
@@ -154,7 +154,7 @@ def glu(x, w_gate, w_up, *, x_scale=None, gate_scale=None, up_scale=None, act="s
     float32 scales per row.  h: x's type, or out_dtype (16 bits, default bfloat16) for
     8-bit x.  need_backward also returns the projections g and u where glu_backward is
     better off reading them (wide inputs; save=True or False decides instead), else None."""
-    if need_backward:
+    if need_backward and isinstance(x, torch.Tensor) and x.dim() > 0:   # else it is refused below
         if x.dtype == torch.float8_e4m3fn:
             raise ValueError("need_backward: 8-bit operands have no gradients")
         save = x.shape[-1] > _AGAIN_FEATURES if save is None else save
