@@ -13,6 +13,7 @@
 #include <string>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -89,7 +90,12 @@ std::string types_of(unsigned mask)
 const Tensor& tensor(PyObject* o, const char* name)
 {
     if (!THPVariable_Check(o)) refuse(std::string(name) + ": expected a tensor, got " + Py_TYPE(o)->tp_name);
-    return THPVariable_Unpack(o);
+    const Tensor& t = THPVariable_Unpack(o);
+    // results have no grad_fn: a gradient would be lost without a word
+    if (t.requires_grad() && at::GradMode::is_enabled())
+        refuse(std::string(name) + ": requires grad, which the layers do not record; call under torch.no_grad() or detach it, "
+                                   "and take the gradients from the *_backward functions");
+    return t;
 }
 
 // The device of a call: its first tensor's, made current while the call runs.

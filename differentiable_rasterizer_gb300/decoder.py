@@ -50,7 +50,7 @@ class GaussianDecoder:
 
     def refresh(self):
         """bfloat16 weights from the fp32 masters (after an optimizer step)."""
-        self.w = {k: v.to(torch.bfloat16) if k != "b_head" else v for k, v in self.masters.items()}
+        self.w = {k: v.detach().to(torch.bfloat16) if k != "b_head" else v.detach() for k, v in self.masters.items()}
         self._quantised = None
 
     # ------------------------------------------------------------------ forward
@@ -128,8 +128,7 @@ def main(argv=None):
         for k, v in masters.items():
             v.grad = g[k].float()
         opt.step()
-        with torch.no_grad():
-            dec.refresh()
+        dec.refresh()
         losses.append(trainer.loss.sum().clone())
     losses = torch.stack(losses).cpu().tolist()
     for step in range(0, a.steps, max(1, a.steps // 10)):

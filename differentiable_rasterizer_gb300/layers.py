@@ -17,6 +17,11 @@ tensor made on another stream needs the usual wait before the call.  Nothing is 
 between calls.  Arguments that a call cannot take raise ValueError, or ``abi.GsError``
 with the library's status; there is no fallback.
 
+The layers are outside autograd: their gradients are the *_backward functions, called
+explicitly.  A tensor that requires grad is refused while gradients are recorded (its
+gradient would be lost without a word); pass ``t.detach()`` or call under
+``torch.no_grad()``.
+
 The checks, the allocations and the calls are native (``csrc/layers_torch.cpp``).
 """
 from __future__ import annotations
