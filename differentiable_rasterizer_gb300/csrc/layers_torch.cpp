@@ -410,6 +410,8 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n)
             g.z = o.r.p, g.ldz = o.r.ld;
         }
         with_scratch("gs_linear", lib.linear, g, x, dev, true);
+        // written in place: autograd has to see it where y is saved for a backward
+        if (a[7] != Py_None && !y.is_inference()) y.unsafeGetTensorImpl()->bump_version();
         return result(y, z);
     });
 }

@@ -1,6 +1,6 @@
 """Arguments of the layers on torch tensors: what is of the wrong kind raises ValueError and
 names the argument, also with no rows, and leaves no error behind; a tensor whose gradient would be lost is
-refused."""
+refused; writes to a given output are seen by autograd."""
 import pytest
 import torch
 
@@ -89,3 +89,18 @@ def test_decoder_takes_its_own_masters(layers):
     params = torch.zeros((10, 16), device="cuda")
     saved = dec.decode(torch.randn((10, 16), device="cuda").to(BF), params)
     assert dec.backward(torch.ones_like(params), saved)["w_head"].shape == dec.masters["w_head"].shape
+
+
+def test_writes_to_out_are_seen(layers):
+    """A tensor that autograd has saved and a layer overwrites: its backward says so, as after any write in place."""
+    x, w = zeros(6, 16), zeros(8, 16)
+    y = torch.ones((6, 12), device="cuda")
+    leaf = torch.ones((6, 12), device="cuda", requires_grad=True)
+    loss = (leaf * y).sum()
+    before = y._version
+    layers.linear(x, w, out=y[:, 2:10], out_dtype=F32)
+    assert y._version == before + 1
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():
+        layers.linear(x, w, out=torch.ones((6, 8), dtype=BF, device="cuda"))
