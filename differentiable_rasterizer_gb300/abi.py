@@ -32,7 +32,7 @@ EXPORTS = ("gs_project", "gs_bin_sort", "gs_raster_fused_fwd_bwd", "gs_grad_comp
            "gs_raster_forward_state", "gs_dssim_loss_grad", "gs_raster_backward_state", "gs_grad_compact_static",
            "gs_prune_tiles", "gs_split_ranges", "gs_compose", "gs_raster_work_counts", "gs_check_report",
            "gs_rms_norm", "gs_rms_norm_bwd", "gs_quantize_rows", "gs_linear", "gs_linear_bwd", "gs_glu", "gs_glu_bwd",
-           "gs_wait_report",
+           "gs_wait_report", "gs_layer_tile",
            "gs_error_string", "gs_param_rows", "gs_param_stride", "gs_num_tiles", "gs_version")
 
 
@@ -112,6 +112,8 @@ def lib():
             getattr(L, name).restype = ctypes.c_int
         L.gs_wait_report.argtypes = [ctypes.POINTER(ctypes.c_int32)]
         L.gs_wait_report.restype = ctypes.c_int
+        L.gs_layer_tile.argtypes = [ctypes.c_int32]
+        L.gs_layer_tile.restype = ctypes.c_int
         L.gs_check_report.argtypes = [_P, ctypes.POINTER(ctypes.c_int32)]
         L.gs_check_report.restype = ctypes.c_int
         L.gs_error_string.argtypes = [ctypes.c_int]
@@ -434,3 +436,8 @@ def gs_wait_report() -> bool:
     if st not in (GS_OK, GS_ERR_TIMEOUT):
         _check("gs_wait_report", st)
     return bool(expired.value)
+
+
+def gs_layer_tile(tile: int):
+    """For tests and measurements: the tile shape (0..3; -1: chosen by size) of this thread's products."""
+    _check("gs_layer_tile", lib().gs_layer_tile(tile))

@@ -1156,15 +1156,19 @@ gs_status make_map(CUtensorMap* map, const void* p, int type, int64_t rows, int6
 
 }  // namespace tc
 
+static thread_local int t_tile = -1;   // gs_layer_tile
+
 GemmPlan gemm_plan(const GemmCall& c)
 {
     const int known = device_sms(), sms = known > 0 ? known : 152;
     GemmPlan best, p;
     double at = 0;
     const bool glu = c.kind == GemmKind::kGlu || c.kind == GemmKind::kGluGrad;
-    for (int i = glu ? 1 : 0; i < 4; ++i) {
+    const bool forced = t_tile >= (glu ? 1 : 0);
+    const int first = forced ? t_tile : (glu ? 1 : 0), last = forced ? t_tile : 3;
+    for (int i = first; i <= last; ++i) {
         const double v = cost(c, kTiles[i], sms, &p);
-        if (i == (glu ? 1 : 0) || v < at) {
+        if (i == first || v < at) {
             at = v;
             best = p;
         }
@@ -1172,7 +1176,7 @@ GemmPlan gemm_plan(const GemmCall& c)
     p = best;
     p.sms = sms;
     p.nb = 0;
-    if ((c.kind == GemmKind::kLinear || c.kind == GemmKind::kGlu) && c.a[0].k_fast && c.b[0].k_fast && c.m <= kFewRows) {
+    if (!forced && (c.kind == GemmKind::kLinear || c.kind == GemmKind::kGlu) && c.a[0].k_fast && c.b[0].k_fast && c.m <= kFewRows) {
         p.nb = c.m <= 16 ? 16 : (c.m <= 32 ? 32 : 64);
         const int64_t tiles = ((c.n + (glu ? 63 : 127)) / (glu ? 64 : 128)) * ((c.m + p.nb - 1) / p.nb);
         p.ranks = 1;
@@ -1302,6 +1306,14 @@ gs_status gemm_run(const GemmCall& c, const GemmPlan& plan, void* ws, JoinJobs* 
 }  // namespace gs
 
 using namespace gs;
+
+extern "C" gs_status gs_layer_tile(int32_t tile)
+{
+    GS_NVTX_RANGE("gs_layer_tile");
+    if (tile < -1 || tile > 3) return GS_ERR_INVALID_ARG;
+    t_tile = tile;
+    return GS_OK;
+}
 
 extern "C" gs_status gs_wait_report(int32_t* expired)
 {

@@ -674,6 +674,14 @@ GS_API gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* ws_by
  * Errors: INVALID_ARG for NULL; TIMEOUT when a wait ran out; CUDA. */
 GS_API gs_status gs_wait_report(int32_t* expired);
 
+/* For tests and measurements: the tile shape of the products that the calling host
+ * thread asks for from now on, whatever their sizes (few rows included):
+ *   0: 128 x 64   1: 128 x 128   2: 256 x 128 over a pair of SMs   3: 256 x 256 over a pair
+ * (0 leaves a gated layer its choice, it has the other three); -1: chosen by size,
+ * as at the start.  Workspace sizes change with it.  No device work.
+ * Errors: INVALID_ARG outside -1..3. */
+GS_API gs_status gs_layer_tile(int32_t tile);
+
 /* Static helpers (no device work). */
 GS_API const char* gs_error_string(gs_status s);
 GS_API int32_t gs_param_rows(int32_t sh_degree);                     /* P: 14, 59, or -1 */
