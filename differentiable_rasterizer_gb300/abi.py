@@ -341,15 +341,6 @@ def layer_run(name, packed, ws, ws_bytes, stream):
         _check(name, st)
 
 
-def layer_call(name, args, stream) -> bool:
-    """The named layer call without scratch; False if it needs some or refuses its arguments
-    (layer_ws_bytes tells which)."""
-    st = getattr(_lib or lib(), name)(args, None, None, stream)
-    if st not in (GS_OK, GS_ERR_INVALID_ARG):
-        _check(name, st)
-    return st == GS_OK
-
-
 def _ws_query(name, packed) -> int:
     sz = ctypes.c_size_t(0)
     st = getattr(_lib or lib(), name)(packed, None, ctypes.byref(sz), None)

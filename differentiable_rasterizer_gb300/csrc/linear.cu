@@ -10,8 +10,8 @@ namespace {
 
 // Gradient in front of the products: dz = dy * act'(z) rounded to the operands'
 // type, and (DB) its column sums unrounded.  HBM bound: every value is read and
-// written once.  A block owns kCols columns and every gridDim.y-th slab of
-// kRows rows; a thread keeps its columns' sums in registers over all its rows,
+// written once.  A block owns tx VEC columns and takes 256 / tx rows at
+// a time, gridDim.y blocks in turn; a thread keeps its columns' sums in registers over all its rows,
 // the block joins them in row order and writes one partial row.
 constexpr int kElemThreads = 256;
 constexpr int kElemRows = 2;   // rows of a thread in flight (100,000 x 256, relu: 2 rows 22 us, 4 rows 28 us)
@@ -22,7 +22,7 @@ struct DzParams {
     void* dz;         // NULL: column sums only
     float* partial;   // [gridDim.y][n] or NULL
     int64_t m, n, lddy, ldz, lddz;
-    int dy_type, type, act;
+    int dy_type;
 };
 
 template <int T, int TDY, int VEC, int ACT>
@@ -89,7 +89,6 @@ struct GluGradParams {
     const void *dh, *g, *u;
     void *dg, *du;
     int64_t m, n, lddh, ldg, ldu, ldd;
-    int type, act;
 };
 
 // dg = dh * u * act'(g), du = dh * act(g).  HBM bound: three reads, two writes.
@@ -466,7 +465,7 @@ extern "C" gs_status gs_linear_bwd(const gs_linear_bwd_args* args, void* ws, siz
         p.dy = a.dy, p.z = a.z, p.dz = make_dz ? base + at_dz : nullptr;
         p.partial = a.db ? (float*)(base + at_db) : nullptr;
         p.m = m, p.n = n, p.lddy = a.lddy, p.ldz = a.ldz, p.lddz = lddz;
-        p.dy_type = a.dy_type, p.type = a.type, p.act = a.act;
+        p.dy_type = a.dy_type;
         const int v = vec ? 8 : 1, tx = thread_cols(n, v);
         const int64_t slabs = slabs_for(m, n, v);
         const dim3 grid((unsigned)((n + (int64_t)tx * v - 1) / ((int64_t)tx * v)), (unsigned)slabs);
@@ -654,7 +653,6 @@ extern "C" gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* w
     GluGradParams p = {};
     p.dh = a.dh, p.g = a.g, p.u = a.u, p.dg = base + at_dg, p.du = base + at_du;
     p.m = m, p.n = f, p.lddh = a.lddh, p.ldg = a.ldg, p.ldu = a.ldu, p.ldd = ldd;
-    p.type = a.type, p.act = a.act;
     const bool vec = f % 8 == 0 && rows16(a.dh, a.lddh, a.type) && rows16(a.g, a.ldg, a.type) &&
                      rows16(a.u, a.ldu, a.type);
     const int v = vec ? 8 : 1, tx = thread_cols(f, v), ty = kElemThreads / tx;
