@@ -215,13 +215,14 @@ int thread_cols(int64_t n, int vec)
     return tx;
 }
 
-constexpr int64_t kSlabs = 608;   // about four blocks an SM over the column blocks
+// Multiprocessors, also where a size is asked for without a device.
+int64_t sms_or_default() { return device_sms() > 0 ? device_sms() : 152; }
 
 int64_t slabs_for(int64_t m, int64_t n, int vec)
 {
     const int tx = thread_cols(n, vec), ty = kElemThreads / tx;
     const int64_t cb = (n + (int64_t)tx * vec - 1) / ((int64_t)tx * vec);
-    int64_t s = (kSlabs + cb - 1) / cb;
+    int64_t s = (4 * sms_or_default() + cb - 1) / cb;   // about four blocks an SM over the column blocks
     const int64_t most = (m + ty - 1) / ty;
     return s < most ? s : (most > 0 ? most : 1);
 }
@@ -310,7 +311,7 @@ gs_status pack_all(Rows* const* list, int n, char* base, int type, cudaStream_t 
 {
     PackJobs jobs;
     unsigned blocks = 0;
-    const int64_t esz = type_bytes(type), most = 16ll * (device_sms() > 0 ? device_sms() : 152);
+    const int64_t esz = type_bytes(type), most = 16 * sms_or_default();
     for (int i = 0; i < n; ++i) {
         Rows& r = *list[i];
         if (!r.src) continue;
@@ -337,7 +338,7 @@ gs_status JoinJobs::add(const float* partial, int64_t parts, int64_t rows, int64
     const int64_t threads = rows * (q.vec ? (cols + 3) / 4 : cols);
     // one thread a result where they fill the SMs; else so many that they do, eight parts each at least
     q.slices = 1;
-    while (q.slices < 64 && threads * q.slices < 152 * 512 && parts >= 8 * q.slices) q.slices *= 2;
+    while (q.slices < 64 && threads * q.slices < sms_or_default() * 512 && parts >= 8 * q.slices) q.slices *= 2;
     const int64_t wide = 256 / q.slices, n = (threads + wide - 1) / wide;
     if (n + blocks > 0x7fffffll || threads > 0x7fffffffll) return GS_ERR_INVALID_ARG;
     q.partial = partial, q.out = out, q.count = rows * pitch, q.ld = ld;
