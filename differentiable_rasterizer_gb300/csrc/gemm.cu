@@ -350,20 +350,21 @@ __device__ __forceinline__ void pack_half16(uint32_t (&w)[8], const float (&v)[1
     for (int j = 0; j < 8; ++j) w[j] = pack_half2(v[2 * j], v[2 * j + 1], T);
 }
 
-template <int ACT>
+template <int ACT, bool FINE>
 __device__ __forceinline__ void activate(float (&v)[16])
 {
 #pragma unroll
     for (int j = 0; j < 16; j += 2) {
-        const float2 f = unpair(act_value2<ACT>(pair(v[j], v[j + 1])));
+        const float2 f = unpair(act_value2<ACT, FINE>(pair(v[j], v[j + 1])));
         v[j] = f.x, v[j + 1] = f.y;
     }
 }
+template <bool FINE>
 __device__ __forceinline__ void activate(float (&v)[16], int act)
 {
-    if (act == GS_ACT_SILU) activate<GS_ACT_SILU>(v);
-    else if (act == GS_ACT_GELU) activate<GS_ACT_GELU>(v);
-    else if (act == GS_ACT_RELU) activate<GS_ACT_RELU>(v);
+    if (act == GS_ACT_SILU) activate<GS_ACT_SILU, FINE>(v);
+    else if (act == GS_ACT_GELU) activate<GS_ACT_GELU, FINE>(v);
+    else if (act == GS_ACT_RELU) activate<GS_ACT_RELU, FINE>(v);
 }
 
 // The loops of the producer's and the MMA warp's elected lanes.  One thread's
@@ -642,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                                 up[j] = __float_as_uint(__uint_as_float(up[j]) * (xs * factors[16 + j]));
                             }
                         }
-                        activate(v, p.act);
+                        activate<OSZ == 4>(v, p.act);
 #pragma unroll
                         for (int j = 0; j < 16; ++j) v[j] *= __uint_as_float(up[j]);
                         return;
@@ -669,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                             v[j] = f.x, v[j + 1] = f.y;
                         }
                     }
-                    if (last) activate(v, p.act);
+                    if (last) activate<OSZ == 4>(v, p.act);
                 }
             };
 
@@ -993,7 +994,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
                 store_elem(p.z, row * p.ldz + col, p.z_type, o);
                 if constexpr (GLU) store_elem(p.z2, row * p.ldz2 + col, p.z_type, u[e]);
             }
-            o = act_value(o, p.act);
+            o = act_value(o, p.act, p.out_type == GS_F32);
             if constexpr (GLU) o *= u[e];
             else if (p.residual) o += load_elem(p.residual, row * p.ldr + col, p.out_type);
             v[e] = o;

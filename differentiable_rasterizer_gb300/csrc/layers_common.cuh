@@ -297,45 +297,51 @@ __device__ __forceinline__ float rcp_fast(float v)
 __device__ __forceinline__ float sigmoid_fast(float v) { return rcp_fast(1.0f + exp2_fast(-1.4426950408889634f * v)); }
 
 // Phi(v), the normal distribution function, and e = exp(-v^2 / 2), which its slope
-// shares:  Phi(-|v|) = (c1 t + ... + c8 t^8) e,  t = 1 / (1 + p |v|).
+// shares:  Phi(-|v|) = (c1 t + ... + cN t^N) e,  t = 1 / (1 + p |v|).
 // The form is that of Abramowitz & Stegun, Handbook of Mathematical Functions, 7.1.26;
-// the coefficients are a minimax fit of the relative error over 0 <= |v| <= 13.4 (1.3e-7;
-// beyond, e is below fp32's normal range).  Taken on the negative side and chosen by the
-// sign, so that the tail keeps its digits: with the instructions' errors Phi is within
-// 2^-20 + v^2 2^-23 of itself (the latter from rounding v^2, so 2^-16 at -10).  1/2 +
-// sign(v) (1/2 - Phi(-|v|)) would lose the tail in the subtraction, GELU below -5 with it.
+// the coefficients are minimax fits of the relative error over 0 <= |v| <= 13.4 (beyond, e
+// is below fp32's normal range): eight terms 1.3e-7, for what stays in fp32; six 4.7e-6,
+// for what is rounded to 16 bits, where that is a 50th of f16's half unit (1,000,000 x 64
+// -> 128: six 107 us, eight 117; all the epilogue's issue slots are taken).
+// Taken on the negative side and chosen by the sign, so that the tail keeps its digits: with
+// the instructions' errors Phi is within 2^-20 (2^-17 of six terms) + v^2 2^-23 of itself,
+// the latter from rounding v^2.  1/2 + sign(v) (1/2 - Phi(-|v|)) would lose the tail in the
+// subtraction, GELU below -5 with it.
 // An erff and a second exponential cost three times as many instructions, which
 // is what bounded the elementwise gradients and the epilogues.
-constexpr float kPhiP = 0.3f;
-__host__ __device__ constexpr float phi_coeff(int i)   // c[i + 1]
-{
-    return i == 0   ? 0.119625784f
-           : i == 1 ? 0.120807543f
-           : i == 2 ? 0.0995807424f
-           : i == 3 ? 0.129654914f
-           : i == 4 ? -0.0557424501f
-           : i == 5 ? 0.208583161f
-           : i == 6 ? -0.158493474f
-                    : 0.0359837115f;
-}
+template <bool FINE>
+struct Phi {
+    static constexpr int kTerms = FINE ? 8 : 6;
+    static constexpr float kP = FINE ? 0.3f : 0.31f;
+    __host__ __device__ static constexpr float c(int i)   // of t^(i + 1)
+    {
+        constexpr float fine[8] = {0.119625784f,   0.120807543f, 0.0995807424f, 0.129654914f,
+                                   -0.0557424501f, 0.208583161f, -0.158493474f, 0.0359837115f};
+        constexpr float coarse[6] = {0.123860702f, 0.12044128f, 0.133429766f, 0.0157447252f, 0.180450335f, -0.0739291385f};
+        return FINE ? fine[i] : coarse[i];
+    }
+};
+template <bool FINE>
 __device__ __forceinline__ float normal_cdf(float v, float& e)
 {
-    const float t = rcp_fast(__fmaf_rn(fabsf(v), kPhiP, 1.0f));
+    using F = Phi<FINE>;
+    const float t = rcp_fast(__fmaf_rn(fabsf(v), F::kP, 1.0f));
     e = exp2_fast(v * v * (-0.5f * 1.4426950408889634f));
-    float q = phi_coeff(7);
+    float q = F::c(F::kTerms - 1);
 #pragma unroll
-    for (int i = 6; i >= 0; --i) q = __fmaf_rn(t, q, phi_coeff(i));
+    for (int i = F::kTerms - 2; i >= 0; --i) q = __fmaf_rn(t, q, F::c(i));
     q = q * t * e;
-    return v < 0.0f ? q : 1.0f - q;
+    return __float_as_int(v) < 0 ? q : 1.0f - q;
 }
 
-__device__ __forceinline__ float act_value(float v, int act)
+// fine: the value is not rounded to 16 bits.
+__device__ __forceinline__ float act_value(float v, int act, bool fine)
 {
     if (act == GS_ACT_RELU) return v < 0.0f ? 0.0f : v;   // NaN stays NaN
     if (act == GS_ACT_SILU) return v * sigmoid_fast(v);
     if (act == GS_ACT_GELU) {
         float e;
-        return v * normal_cdf(v, e);
+        return v * (fine ? normal_cdf<true>(v, e) : normal_cdf<false>(v, e));
     }
     return v;
 }
@@ -373,24 +379,35 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
     return r;
 }
 
-// Phi of two values, to the bit as normal_cdf computes it.
+// Phi of two values, to the bit as normal_cdf computes it.  Its last step is a choice where
+// the value alone is wanted; beside the slope, which keeps more registers alive, (1 or 0)
+// minus the tail with its sign set, without predicates (1,000,000 x 64 x 128 GELU gradients
+// 149 us, 162 with choices, which spill).
+template <bool FINE, bool SLOPE>
 __device__ __forceinline__ uint64_t normal_cdf2(uint64_t v, uint64_t& e)
 {
+    using F = Phi<FINE>;
     const auto both = [](float c) { return pair(c, c); };
     const float2 f = unpair(v);
-    const float2 d = unpair(fma2(pair(fabsf(f.x), fabsf(f.y)), both(kPhiP), both(1.0f)));
+    const float2 d = unpair(fma2(pair(fabsf(f.x), fabsf(f.y)), both(F::kP), both(1.0f)));
     const uint64_t t = pair(rcp_fast(d.x), rcp_fast(d.y));
     const float2 x = unpair(mul2(mul2(v, v), both(-0.5f * 1.4426950408889634f)));
     e = pair(exp2_fast(x.x), exp2_fast(x.y));
-    uint64_t q = both(phi_coeff(7));
+    uint64_t q = both(F::c(F::kTerms - 1));
 #pragma unroll
-    for (int i = 6; i >= 0; --i) q = fma2(t, q, both(phi_coeff(i)));
+    for (int i = F::kTerms - 2; i >= 0; --i) q = fma2(t, q, both(F::c(i)));
     q = mul2(mul2(q, t), e);
-    const float2 lo = unpair(q), hi = unpair(fma2(q, both(-1.0f), both(1.0f)));
-    return pair(f.x < 0.0f ? lo.x : hi.x, f.y < 0.0f ? lo.y : hi.y);
+    const float2 p = unpair(q);
+    if constexpr (SLOPE) {
+        float hx, hy;   // 0 below zero (-0 too), else 1
+        asm("set.ge.f32.s32 %0, %1, 0;" : "=f"(hx) : "r"(__float_as_int(f.x)));
+        asm("set.ge.f32.s32 %0, %1, 0;" : "=f"(hy) : "r"(__float_as_int(f.y)));
+        return add2(pair(hx, hy), pair(copysignf(p.x, -f.x), copysignf(p.y, -f.y)));
+    } else
+        return pair(__float_as_int(f.x) < 0 ? p.x : 1.0f - p.x, __float_as_int(f.y) < 0 ? p.y : 1.0f - p.y);
 }
 
-template <int ACT>
+template <int ACT, bool FINE>
 __device__ __forceinline__ uint64_t act_value2(uint64_t v)
 {
     if constexpr (ACT == GS_ACT_SILU) {
@@ -399,14 +416,15 @@ __device__ __forceinline__ uint64_t act_value2(uint64_t v)
         return mul2(v, pair(rcp_fast(d.x), rcp_fast(d.y)));
     } else if constexpr (ACT == GS_ACT_GELU) {
         uint64_t e;
-        return mul2(v, normal_cdf2(v, e));
+        return mul2(v, normal_cdf2<FINE, false>(v, e));
     } else {
         const float2 f = unpair(v);
-        return pair(act_value(f.x, ACT), act_value(f.y, ACT));
+        return pair(act_value(f.x, ACT, FINE), act_value(f.y, ACT, FINE));
     }
 }
 
 // act(v) and act'(v), from one sigma or one Phi.
+template <bool FINE>
 __device__ __forceinline__ void act_both(float v, int act, float& value, float& slope)
 {
     if (act == GS_ACT_SILU) {
@@ -415,7 +433,7 @@ __device__ __forceinline__ void act_both(float v, int act, float& value, float& 
         slope = p * __fmaf_rn(v, 1.0f - p, 1.0f);
     } else if (act == GS_ACT_GELU) {
         float e;
-        const float c = normal_cdf(v, e);
+        const float c = normal_cdf<FINE>(v, e);
         value = v * c;
         slope = __fmaf_rn(v * 0.39894228040143268f, e, c);
     } else if (act == GS_ACT_RELU) {
@@ -427,7 +445,7 @@ __device__ __forceinline__ void act_both(float v, int act, float& value, float& 
     }
 }
 
-template <int ACT>
+template <int ACT, bool FINE>
 __device__ __forceinline__ void act_both2(uint64_t v, uint64_t& value, uint64_t& slope)
 {
     const auto both = [](float c) { return pair(c, c); };
@@ -439,14 +457,14 @@ __device__ __forceinline__ void act_both2(uint64_t v, uint64_t& value, uint64_t&
         slope = mul2(p, fma2(v, fma2(p, both(-1.0f), both(1.0f)), both(1.0f)));
     } else if constexpr (ACT == GS_ACT_GELU) {
         uint64_t e;
-        const uint64_t c = normal_cdf2(v, e);
+        const uint64_t c = normal_cdf2<FINE, true>(v, e);
         value = mul2(v, c);
         slope = fma2(mul2(v, both(0.39894228040143268f)), e, c);
     } else {
         const float2 f = unpair(v);
         float2 a, b;
-        act_both(f.x, ACT, a.x, b.x);
-        act_both(f.y, ACT, a.y, b.y);
+        act_both<FINE>(f.x, ACT, a.x, b.x);
+        act_both<FINE>(f.y, ACT, a.y, b.y);
         value = pair(a.x, a.y);
         slope = pair(b.x, b.y);
     }
@@ -455,7 +473,7 @@ __device__ __forceinline__ void act_both2(uint64_t v, uint64_t& value, uint64_t&
 __device__ __forceinline__ float act_slope(float v, int act)
 {
     float value, slope;
-    act_both(v, act, value, slope);
+    act_both<true>(v, act, value, slope);
     return slope;
 }
 
@@ -466,7 +484,7 @@ __device__ __forceinline__ void glu_gradient(float (&g)[16], float (&u)[16], con
 #pragma unroll
     for (int j = 0; j < 16; j += 2) {
         uint64_t value, slope;
-        act_both2<ACT>(pair(g[j], g[j + 1]), value, slope);
+        act_both2<ACT, false>(pair(g[j], g[j + 1]), value, slope);
         const uint64_t d = pair(dh[j], dh[j + 1]);
         const float2 a = unpair(mul2(mul2(d, pair(u[j], u[j + 1])), slope)), b = unpair(mul2(d, value));
         g[j] = a.x, g[j + 1] = a.y;

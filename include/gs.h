@@ -464,7 +464,8 @@ GS_API gs_status gs_check_report(uint64_t* report, int32_t* checked);
  *     fp32 outputs are as good as these: the tensor cores truncate as they add
  *     (a product of K terms is within K 2^-23 of the sum of their magnitudes),
  *     SILU's factor is within 2^-21 + |v| 2^-23 of itself, GELU's within
- *     2^-20 + v^2 2^-23, tails included, down to fp32's normal range.
+ *     2^-20 + v^2 2^-23 (2^-17 in place of 2^-20 where the result is rounded to
+ *     16 bits), tails included, down to fp32's normal range.
  *   - NULL marks an optional array that is absent.  Scale vectors are fp32.
  *   - ws / ws_bytes: scratch of 256-byte alignment; ws == NULL queries the size
  *     into *ws_bytes and does nothing else; where that size is 0, both may be
