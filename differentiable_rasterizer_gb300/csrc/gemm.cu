@@ -350,21 +350,21 @@ __device__ __forceinline__ void pack_half16(uint32_t (&w)[8], const float (&v)[1
     for (int j = 0; j < 8; ++j) w[j] = pack_half2(v[2 * j], v[2 * j + 1], T);
 }
 
-template <int ACT, bool FINE>
+template <int ACT, bool FINE, bool GLU>
 __device__ __forceinline__ void activate(float (&v)[16])
 {
 #pragma unroll
     for (int j = 0; j < 16; j += 2) {
-        const float2 f = unpair(act_value2<ACT, FINE>(pair(v[j], v[j + 1])));
+        const float2 f = unpair(act_value2<ACT, FINE, GLU>(pair(v[j], v[j + 1])));
         v[j] = f.x, v[j + 1] = f.y;
     }
 }
-template <bool FINE>
+template <bool FINE, bool GLU>
 __device__ __forceinline__ void activate(float (&v)[16], int act)
 {
-    if (act == GS_ACT_SILU) activate<GS_ACT_SILU, FINE>(v);
-    else if (act == GS_ACT_GELU) activate<GS_ACT_GELU, FINE>(v);
-    else if (act == GS_ACT_RELU) activate<GS_ACT_RELU, FINE>(v);
+    if (act == GS_ACT_SILU) activate<GS_ACT_SILU, FINE, GLU>(v);
+    else if (act == GS_ACT_GELU) activate<GS_ACT_GELU, FINE, GLU>(v);
+    else if (act == GS_ACT_RELU) activate<GS_ACT_RELU, FINE, GLU>(v);
 }
 
 // The loops of the producer's and the MMA warp's elected lanes.  One thread's
@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                                 up[j] = __float_as_uint(__uint_as_float(up[j]) * (xs * factors[16 + j]));
                             }
                         }
-                        activate<OSZ == 4>(v, p.act);
+                        activate<OSZ == 4, GLU>(v, p.act);
 #pragma unroll
                         for (int j = 0; j < 16; ++j) v[j] *= __uint_as_float(up[j]);
                         return;
@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                             v[j] = f.x, v[j + 1] = f.y;
                         }
                     }
-                    if (last) activate<OSZ == 4>(v, p.act);
+                    if (last) activate<OSZ == 4, GLU>(v, p.act);
                 }
             };
 

@@ -302,7 +302,7 @@ __device__ __forceinline__ float sigmoid_fast(float v) { return rcp_fast(1.0f + 
 // the coefficients are minimax fits of the relative error over 0 <= |v| <= 13.4 (beyond, e
 // is below fp32's normal range): eight terms 1.3e-7, for what stays in fp32; six 4.7e-6,
 // for what is rounded to 16 bits, where that is a 50th of f16's half unit (1,000,000 x 64
-// -> 128: six 107 us, eight 117; all the epilogue's issue slots are taken).
+// -> 128: six 107 us, eight 117 in one coding; the epilogue is bound by issue slots).
 // Taken on the negative side and chosen by the sign, so that the tail keeps its digits: with
 // the instructions' errors Phi is within 2^-20 (2^-17 of six terms) + v^2 2^-23 of itself,
 // the latter from rounding v^2.  1/2 + sign(v) (1/2 - Phi(-|v|)) would lose the tail in the
@@ -379,17 +379,22 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
     return r;
 }
 
-// Phi of two values, to the bit as normal_cdf computes it.  Its last step is a choice where
-// the value alone is wanted; beside the slope, which keeps more registers alive, (1 or 0)
-// minus the tail with its sign set, without predicates (1,000,000 x 64 x 128 GELU gradients
-// 149 us, 162 with choices, which spill).
-template <bool FINE, bool SLOPE>
+// Phi of two values, to the bit as normal_cdf computes it, in codings that the callers'
+// registers suit best (all measured, the others being spilled or issued worse): CHOICE, the
+// last step as a choice by sign, or (1 or 0) minus the tail with its sign set, without
+// predicates; FOLD, t's divisor one value at a time, which takes |v| along.
+//   gated layer's value          choice           1,000,000 x 64 -> 128 111 us, signed 118
+//   product's value              signed, folded   100,000 x 256 -> 256 56 us, choice 60
+//   gated layer's gradients      signed           1,000,000 x 64 x 128 149 us, choice 162
+//   elementwise gradient         choice           100,000 x 256 37.5 us, signed 39.5
+template <bool FINE, bool CHOICE, bool FOLD>
 __device__ __forceinline__ uint64_t normal_cdf2(uint64_t v, uint64_t& e)
 {
     using F = Phi<FINE>;
     const auto both = [](float c) { return pair(c, c); };
     const float2 f = unpair(v);
-    const float2 d = unpair(fma2(pair(fabsf(f.x), fabsf(f.y)), both(F::kP), both(1.0f)));
+    const float2 d = FOLD ? make_float2(__fmaf_rn(fabsf(f.x), F::kP, 1.0f), __fmaf_rn(fabsf(f.y), F::kP, 1.0f))
+                          : unpair(fma2(pair(fabsf(f.x), fabsf(f.y)), both(F::kP), both(1.0f)));
     const uint64_t t = pair(rcp_fast(d.x), rcp_fast(d.y));
     const float2 x = unpair(mul2(mul2(v, v), both(-0.5f * 1.4426950408889634f)));
     e = pair(exp2_fast(x.x), exp2_fast(x.y));
@@ -398,7 +403,7 @@ __device__ __forceinline__ uint64_t normal_cdf2(uint64_t v, uint64_t& e)
     for (int i = F::kTerms - 2; i >= 0; --i) q = fma2(t, q, both(F::c(i)));
     q = mul2(mul2(q, t), e);
     const float2 p = unpair(q);
-    if constexpr (SLOPE) {
+    if constexpr (!CHOICE) {
         float hx, hy;   // 0 below zero (-0 too), else 1
         asm("set.ge.f32.s32 %0, %1, 0;" : "=f"(hx) : "r"(__float_as_int(f.x)));
         asm("set.ge.f32.s32 %0, %1, 0;" : "=f"(hy) : "r"(__float_as_int(f.y)));
@@ -407,7 +412,7 @@ __device__ __forceinline__ uint64_t normal_cdf2(uint64_t v, uint64_t& e)
         return pair(__float_as_int(f.x) < 0 ? p.x : 1.0f - p.x, __float_as_int(f.y) < 0 ? p.y : 1.0f - p.y);
 }
 
-template <int ACT, bool FINE>
+template <int ACT, bool FINE, bool GLU>
 __device__ __forceinline__ uint64_t act_value2(uint64_t v)
 {
     if constexpr (ACT == GS_ACT_SILU) {
@@ -416,7 +421,7 @@ __device__ __forceinline__ uint64_t act_value2(uint64_t v)
         return mul2(v, pair(rcp_fast(d.x), rcp_fast(d.y)));
     } else if constexpr (ACT == GS_ACT_GELU) {
         uint64_t e;
-        return mul2(v, normal_cdf2<FINE, false>(v, e));
+        return mul2(v, normal_cdf2<FINE, GLU, !GLU>(v, e));
     } else {
         const float2 f = unpair(v);
         return pair(act_value(f.x, ACT, FINE), act_value(f.y, ACT, FINE));
@@ -445,7 +450,7 @@ __device__ __forceinline__ void act_both(float v, int act, float& value, float& 
     }
 }
 
-template <int ACT, bool FINE>
+template <int ACT, bool FINE, bool CHOICE>
 __device__ __forceinline__ void act_both2(uint64_t v, uint64_t& value, uint64_t& slope)
 {
     const auto both = [](float c) { return pair(c, c); };
@@ -457,7 +462,7 @@ __device__ __forceinline__ void act_both2(uint64_t v, uint64_t& value, uint64_t&
         slope = mul2(p, fma2(v, fma2(p, both(-1.0f), both(1.0f)), both(1.0f)));
     } else if constexpr (ACT == GS_ACT_GELU) {
         uint64_t e;
-        const uint64_t c = normal_cdf2<FINE, true>(v, e);
+        const uint64_t c = normal_cdf2<FINE, CHOICE, false>(v, e);
         value = mul2(v, c);
         slope = fma2(mul2(v, both(0.39894228040143268f)), e, c);
     } else {
@@ -484,7 +489,7 @@ __device__ __forceinline__ void glu_gradient(float (&g)[16], float (&u)[16], con
 #pragma unroll
     for (int j = 0; j < 16; j += 2) {
         uint64_t value, slope;
-        act_both2<ACT, false>(pair(g[j], g[j + 1]), value, slope);
+        act_both2<ACT, false, false>(pair(g[j], g[j + 1]), value, slope);
         const uint64_t d = pair(dh[j], dh[j + 1]);
         const float2 a = unpair(mul2(mul2(d, pair(u[j], u[j + 1])), slope)), b = unpair(mul2(d, value));
         g[j] = a.x, g[j + 1] = a.y;

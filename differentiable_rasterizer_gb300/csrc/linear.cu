@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kElemThreads) dz_kernel(const __grid_constant_
 #pragma unroll
                         for (int e = 0; e < 8; e += 2) {
                             uint64_t value, slope;
-                            act_both2<ACT, true>(pair(z[e], z[e + 1]), value, slope);
+                            act_both2<ACT, true, true>(pair(z[e], z[e + 1]), value, slope);
                             const float2 f = unpair(mul2(pair(g[e], g[e + 1]), slope));
                             g[e] = f.x, g[e + 1] = f.y;
                         }
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kElemThreads) glu_grad_kernel(const __grid_con
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
                     uint64_t value, slope;
-                    act_both2<ACT, false>(pair(g[e], g[e + 1]), value, slope);
+                    act_both2<ACT, false, false>(pair(g[e], g[e + 1]), value, slope);
                     const uint64_t q = pair(d[e], d[e + 1]);
                     const float2 a = unpair(mul2(mul2(q, pair(u[e], u[e + 1])), slope)), b = unpair(mul2(q, value));
                     g[e] = a.x, g[e + 1] = a.y;
