@@ -420,8 +420,8 @@ def layer_ws_bytes(name: str, args: bytes) -> int:
 
 
 def gs_wait_report() -> bool:
-    """True if a layer kernel's bounded wait ran out since the last report (then cleared);
-    synchronises the device."""
+    """True if a layer kernel's bounded wait ran out on the current device since the last report
+    (then cleared); synchronises the device."""
     expired = ctypes.c_int32(0)
     st = lib().gs_wait_report(ctypes.byref(expired))
     if st not in (GS_OK, GS_ERR_TIMEOUT):

@@ -17,6 +17,10 @@ tensor made on another stream needs the usual wait before the call.  Nothing is 
 between calls.  Arguments that a call cannot take raise ValueError, or ``abi.GsError``
 with the library's status; there is no fallback.
 
+Kernels wait for their own copies and products within a bound of about two seconds; one that
+runs out of it (a device fault, or a process stopped for that long) leaves its outputs
+undefined, which ``abi.gs_wait_report()`` tells.
+
 The layers are outside autograd: their gradients are the *_backward functions, called
 explicitly.  A tensor that requires grad is refused while gradients are recorded (its
 gradient would be lost without a word); pass ``t.detach()`` or call under
@@ -145,9 +149,11 @@ def linear_backward(dy, x, w, *, z=None, act=None, bias=False, need_dx=True, nee
 
 # ------------------------------------------------------------------ gated feed-forward
 # Up to this many input features glu's gradients compute the projections again rather than
-# read them: two more products of that depth against 8 bytes a value written and read
-# (a step of 1,000,000 x 64 x 128: again 690 us, saved 766; of 32768 x 1024 x 4096: saved
-# 1.73 ms, again about 1.8).
+# read them: two more products of that depth against 8 bytes a value written and read.
+# Layer and gradients, saved and again: 1,000,000 x 64 x 128 566 and 219 us (one pass),
+# 100,000 x 256 x 1024 487 and 408, 32768 x 512 x 2048 426 and 403, 32768 x 640 x 2560 610 and
+# 604, 32768 x 1024 x 4096 1161 and 1224.  (Of few rows they are close: 4096 x 512 x 2048 80
+# and 84.)
 _AGAIN_FEATURES = 512
 
 

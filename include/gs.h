@@ -486,6 +486,8 @@ typedef enum gs_act { GS_ACT_NONE = 0, GS_ACT_RELU = 1, GS_ACT_SILU = 2, GS_ACT_
  *   the norm: rstd cancels out of the 8-bit values.  A NaN in a row makes its
  *   y and y_scale NaN.
  * The norm is taken of the fp32 sum; `sum` receives it rounded to `type`.
+ * Its mean square is an fp32 number: rows of more than about 1.8e19 / sqrt(cols)
+ * (which bf16 and fp32 can hold) give an infinite one, rstd 0 and y 0.
  * x, residual, sum: [rows][cols] of `type` (F32, BF16, F16).  weight: [cols] of
  * weight_type (F32, BF16, F16).  y: y_type (F32, BF16, F16, E4M3).  y_scale:
  * [rows], with E4M3 only.  rstd: [rows] or NULL.
@@ -554,7 +556,8 @@ GS_API gs_status gs_quantize_rows(const gs_quantize_rows_args* args, void* strea
  * [rows] and w_scale [out]: with E4M3 only (NULL: 1).  bias: [out] of bias_type
  * (F32, BF16, F16) or NULL.  residual (or NULL), y: [rows][out] of out_type
  * (F32, BF16, F16).  z: NULL, or [rows][out] of `type` (16 bits): the
- * pre-activations rounded to 16 bits, which gs_linear_bwd takes.
+ * pre-activations rounded to 16 bits, which gs_linear_bwd takes (beyond F16's
+ * 65504 infinite, and a SILU's or GELU's gradient of them NaN).
  * act: gs_act; GELU is the exact one, v * Phi(v).
  * Errors: INVALID_ARG for bad pointers, sizes, types or a too small workspace;
  * CUDA on launch failure. */
@@ -668,9 +671,11 @@ typedef struct gs_glu_bwd_args {
 GS_API gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* ws_bytes, void* stream);
 
 /* The layers' products wait on their own copies and tensor-core work, each wait
- * bounded to about two seconds; a kernel whose wait runs out (a device fault; it
- * cannot happen otherwise) drains, returns with its outputs undefined, and
- * leaves a mark that this call reports and clears.  Synchronises the device.
+ * bounded to about two seconds of the multiprocessor's clock; a kernel whose wait
+ * runs out (a device fault, or a process preempted or stopped in a debugger for as
+ * long) drains, returns with its outputs undefined, and leaves a mark on its device.
+ * The call that queued it has returned OK by then; this one reports and clears the
+ * current device's mark.  Synchronises the device.
  * expired: HOST int32 out, 1 if a wait ran out since the last report.
  * Errors: INVALID_ARG for NULL; TIMEOUT when a wait ran out; CUDA. */
 GS_API gs_status gs_wait_report(int32_t* expired);
