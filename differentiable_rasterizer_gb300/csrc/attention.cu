@@ -1,0 +1,589 @@
+// attention.cu -- attention over packed sequences, forward.
+//
+//   t = scale q k^T,  p = exp(t - m),  o = (p v) / sum p,   m the rows' running maximum
+//
+// One pass over the keys, 128 at a time, for two tiles of 128 packed rows a CTA.  10 warps
+// with fixed roles:
+//   warps 0-3, 4-7  softmax of the first and of the second tile, a row a thread: scores
+//                   TMEM -> registers -> p in 16 bits back over the scores, the sum in fp32
+//   warp 8          TMA producer: the two tiles of q, then keys and values in a ring
+//   warp 9          issues tcgen05.mma: scores from shared memory, p v with p from TMEM
+// The tiles take turns: while one tile's softmax works, the tensor cores compute the
+// other's products.  TMEM, fp32: scores of both tiles (p in their first 64 columns), o of
+// both.  The products of a tile's p with v and of its next scores, which overwrite p, are
+// issued in that order by one thread and run in it.
+//
+// The maximum that a row's terms are taken to is raised only when a tile of keys exceeds
+// it by more than 2^8: o and the sum are then rescaled (rare after the first tiles), and
+// terms stay within 2^8 in between, which neither 16-bit type nor the fp32 sums mind.
+//
+// Few rows against many keys (single tokens) leave most SMs idle: the keys of a tile are
+// then split over several CTAs, whose sums and maxima join_kernel puts together in a
+// fixed order.
+#include <atomic>
+
+#include "attention.cuh"
+
+namespace gs {
+namespace attn {
+namespace {
+
+constexpr int kWarps = 10, kThreads = kWarps * 32;
+constexpr int kTmemCols = 512, kTmemO = 256;
+constexpr float kRaise = 8.0f;   // log2
+
+template <int DP>
+struct Shape {
+    static constexpr int kChunks = DP / 64;
+    static constexpr uint32_t kTile = kChunks * kBox;
+    static constexpr int kStages = DP == 128 ? 5 : 8;
+    static constexpr uint32_t kAtRing = 2 * kTile, kAtBars = kAtRing + kStages * kTile;
+    static constexpr int kQFull = 0, kFull = 2, kEmpty = kFull + kStages, kScores = kEmpty + kStages, kTerms = kScores + 2,
+                         kSums = kTerms + 2, kDone = kSums + 2, kBars = kDone + 1;
+    static constexpr int kSmem = kAtBars + ((kBars * 8 + 15) & ~15) + 16;
+    static_assert(kSmem <= 232448, "shared memory of an SM");
+};
+
+struct Params {
+    CUtensorMap q, k, v;
+    Sequences seqs;
+    Fill fill;
+    uint16_t* o;
+    int64_t o_row, o_head;
+    float* lse;
+    float* part;          // splits > 1: [item][rows of a tile][DP] sums of p v, then their (maximum, sum of p)
+    float2* part_stats;
+    float scale2;         // scale log2(e)
+    uint32_t splits, kv_heads;
+    int tiles;            // of a unit: 1 or 2
+    int group, tokens;    // query heads of a key head, tokens of a tile
+    int dim, o_vec, causal, zero;
+    uint32_t idesc_s, idesc_o;
+};
+
+__device__ int g_attention_wait_expired;
+
+// A CTA's work: a unit of one or two tiles of a key head, and its part of the keys' tiles.
+struct Work {
+    Sequence seq;
+    uint32_t item, head;
+    int t0;            // the first token of the unit
+    int from;          // the first tile of keys
+    int n[2];          // tiles of keys from there for either tile of the unit
+};
+
+// Keys that the tokens up to `last` of a sequence see.
+__device__ __forceinline__ int keys_seen(const Sequence& s, int last, bool causal)
+{
+    const int e = causal ? last + 1 + s.lk - s.lq : s.lk;
+    return e < 0 ? 0 : (e < s.lk ? e : s.lk);
+}
+
+__device__ __forceinline__ bool find_work(const Params& p, Work& w)
+{
+    const uint32_t split = blockIdx.x % p.splits, rest = blockIdx.x / p.splits;
+    w.head = rest % p.kv_heads;
+    uint32_t unit, units;
+    const int tokens = p.tokens * p.tiles;
+    if (!find_unit<false>(p.seqs, rest / p.kv_heads, tokens, w.seq, unit, units)) return false;
+    w.item = blockIdx.x;
+    if (p.causal) unit = units - 1 - unit;   // the longest first
+    w.t0 = (int)unit * tokens;
+    int tiles[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int t = w.t0 + i * p.tokens;
+        int last = t + p.tokens - 1;
+        last = last < w.seq.lq ? last : w.seq.lq - 1;
+        tiles[i] = i < p.tiles && t < w.seq.lq ? (keys_seen(w.seq, last, p.causal) + kRows - 1) / kRows : 0;
+    }
+    const int most = tiles[0] > tiles[1] ? tiles[0] : tiles[1];
+    const int each = (most + (int)p.splits - 1) / (int)p.splits;
+    w.from = (int)split * each;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        int n = tiles[i] - w.from;
+        n = n < 0 ? 0 : n;
+        w.n[i] = n < each ? n : each;
+    }
+    return true;
+}
+
+template <int DP>
+__device__ __forceinline__ void load(const Params& p, const Work& w, int n, uint32_t smem, uint32_t bars, volatile int* gave_up)
+{
+    using S = Shape<DP>;
+    const uint32_t q_bytes = (uint32_t)(S::kChunks * p.tokens * p.group) * 128;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (w.n[i] > 0) {
+            mbar_expect(bars + 8 * (S::kQFull + i), q_bytes);
+            load_tile<S::kChunks>(smem + i * S::kTile, &p.q, w.head * p.group, w.seq.q0 + w.t0 + i * p.tokens, bars + 8 * (S::kQFull + i));
+        }
+    Ring<S::kStages> ring;
+    uint32_t issued = 0;
+    int row = w.seq.k0 + w.from * kRows;
+    for (int j = 0; j < 2 * n; ++j, ++issued, ring.next()) {
+        if (!mbar_wait(bars + 8 * (S::kEmpty + ring.s), ring.parity ^ 1, gave_up)) break;
+        mbar_expect(bars + 8 * (S::kFull + ring.s), S::kTile);
+        load_tile<S::kChunks>(smem + S::kAtRing + ring.s * S::kTile, j & 1 ? &p.v : &p.k, w.head, row, bars + 8 * (S::kFull + ring.s));
+        if (j & 1) row += kRows;
+    }
+    // the block does not leave before its copies have landed
+    bool landed = true;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) landed = landed && (w.n[i] == 0 || mbar_wait_alone(bars + 8 * (S::kQFull + i), 0));
+    last_copies<S::kStages>(issued, [&](uint32_t s, uint32_t parity) { landed = landed && mbar_wait_alone(bars + 8 * (S::kFull + s), parity); });
+}
+
+// The issuing warp: a whole warp waits and clears rows, its elected lane issues.
+template <int DP>
+__device__ __forceinline__ void issue(const Params& p, const Work& w, int n, uint32_t smem, uint32_t bars, uint32_t tmem, int lane,
+                                      volatile int* gave_up)
+{
+    using S = Shape<DP>;
+    const bool one = elect_one();
+    const int steps = (p.dim + 15) / 16;
+    const auto scores = [&](int i, uint32_t tile) {   // of tile i with the keys there
+        const uint32_t a = desc_lo(smem + i * S::kTile, true), b = desc_lo(tile, true);
+        for (int s = 0; s < steps; ++s) {
+            const uint32_t at = (uint32_t)(s >> 2) * (kBox >> 4) + (uint32_t)(s & 3) * k_step(true);
+            mma<false, false>(tmem + i * 128, a + at, kDescHi, b + at, kDescHi, p.idesc_s, s > 0);
+        }
+        mma_commit<false>(bars + 8 * (S::kScores + i));
+    };
+    Ring<S::kStages> ring;   // at the next stage to be waited for
+    uint32_t keys = ring.s;
+    bool ok = mbar_wait(bars + 8 * (S::kFull + ring.s), ring.parity, gave_up);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (ok && w.n[i] > 0) {
+            ok = mbar_wait(bars + 8 * (S::kQFull + i), 0, gave_up);
+            if (ok && one) scores(i, smem + S::kAtRing + keys * S::kTile);
+        }
+    if (ok && one) mma_commit<false>(bars + 8 * (S::kEmpty + keys));
+    ring.next();
+    for (int j = 0; ok && j < n; ++j) {
+        const uint32_t values = ring.s, at = smem + S::kAtRing + values * S::kTile;
+        ok = mbar_wait(bars + 8 * (S::kFull + ring.s), ring.parity, gave_up);
+        if (!ok) break;
+        ring.next();
+        const int live = w.seq.lk - (w.from + j) * kRows;   // the rows behind are other sequences'
+        if (live < kRows) zero_rows<S::kChunks>(at, live, lane);
+        bool more = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (!ok || j >= w.n[i]) continue;
+            ok = mbar_wait(bars + 8 * (S::kTerms + i), j & 1, gave_up);
+            if (!ok) continue;
+            tc_fence_after();
+            if (one) {
+                const uint32_t b = desc_rows(at);
+#pragma unroll
+                for (int s = 0; s < kRows / 16; ++s)
+                    mma_tmem(tmem + kTmemO + i * DP, tmem + i * 128 + s * 8, b + s * k_step(false), kDescHi, p.idesc_o, j > 0 || s > 0);
+                mma_commit<false>(bars + 8 * (S::kSums + i));
+            }
+            if (j + 1 < w.n[i]) {
+                if (!more) {
+                    keys = ring.s;
+                    ok = mbar_wait(bars + 8 * (S::kFull + keys), ring.parity, gave_up);
+                    more = true;
+                }
+                if (ok && one) scores(i, smem + S::kAtRing + keys * S::kTile);
+            }
+        }
+        if (ok && one) {
+            mma_commit<false>(bars + 8 * (S::kEmpty + values));
+            if (more) mma_commit<false>(bars + 8 * (S::kEmpty + keys));
+        }
+        if (more) ring.next();
+    }
+    if (one) {
+        mma_commit<false>(bars + 8 * S::kDone);
+        if (!mbar_wait_alone(bars + 8 * S::kDone, 0)) *gave_up = 1;
+    }
+    __syncwarp();
+}
+
+// A row a thread: i the tile, r the row.
+template <int T, int DP>
+__device__ __forceinline__ void softmax(const Params& p, const Work& w, int i, int r, uint32_t bars, uint32_t tmem, volatile int* gave_up)
+{
+    using S = Shape<DP>;
+    const int n = w.n[i], t0 = w.t0 + i * p.tokens;
+    const int token = t0 + r / p.group, head = (int)w.head * p.group + r % p.group;
+    const bool live = r < p.tokens * p.group && token < w.seq.lq;
+    const int seen = keys_seen(w.seq, token, p.causal);                 // this row's keys
+    const int all = keys_seen(w.seq, t0, p.causal);                     // every row's
+    const uint32_t scores = tmem + i * 128, sums = tmem + kTmemO + i * DP;
+    float m = -INFINITY;
+    uint64_t l2[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (S::kScores + i), j & 1, gave_up));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[128];
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) tmem_ld32(scores + c, s + c);
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) tmem_ld32_wait(s + c);
+        const int first = (w.from + j) * kRows;
+        if (first + kRows > all) {
+            const int left = seen - first;
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+                if (c >= left) s[c] = 0xff800000u;   // -infinity, whatever the hidden key gave
+        }
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 128; c += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top[e] = fmaxf(fmaxf(top[e], __uint_as_float(s[c + e])), __uint_as_float(s[c + 4 + e]));
+        const float new_m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale2;
+        const bool raise = new_m > m + kRaise;   // from -infinity: by any score
+        if (j == 0) m = new_m;
+        else if (__any_sync(0xffffffffu, raise)) {
+            // the sums so far, to the new maximum: the product that last added to them is done
+            const float to = raise ? new_m : m, by = m == to ? 1.0f : exp2_fast(m - to);
+            ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (S::kSums + i), (j - 1) & 1, gave_up));
+            if (!ok) break;
+            tc_fence_after();
+            m = to;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) l2[e] = mul2(l2[e], pair(by, by));
+#pragma unroll 1
+            for (int c = 0; c < DP; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(sums + c, o);
+                tmem_ld32_wait(o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
+                tmem_st32(sums + c, o);
+            }
+        }
+        const float less = m == -INFINITY ? 0.0f : -m;   // no key yet: every term 0
+        const uint64_t scale = pair(p.scale2, p.scale2), minus = pair(less, less);
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+            uint32_t h[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float2 x = unpair(fma2(pair(__uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1])), scale, minus));
+                const float a = exp2_fast(x.x), b = exp2_fast(x.y);
+                l2[e & 1] = add2(l2[e & 1], pair(a, b));
+                h[e] = pack_half2(a, b, T);
+            }
+            tmem_st16(scores + c / 2, h);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(bars + 8 * (S::kTerms + i));
+    }
+    if (n > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (S::kSums + i), (n - 1) & 1, gave_up));
+    if (!ok) return;
+    tc_fence_after();
+    const float2 la = unpair(l2[0]), lb = unpair(l2[1]);
+    const float l = (la.x + la.y) + (lb.x + lb.y);
+    const int64_t row = w.seq.q0 + token;
+    if (p.splits > 1) {
+        const int64_t at = (int64_t)w.item * (p.tokens * p.group) + r;
+        if (live) p.part_stats[at] = make_float2(m, l);
+        if (n == 0) return;
+        float* to = p.part + at * DP;
+#pragma unroll 1
+        for (int c = 0; c < DP; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(sums + c, o);
+            tmem_ld32_wait(o);
+            if (live)
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<uint4*>(to + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+    } else {
+        const bool none = l == 0.0f;
+        if (live && p.lse) p.lse[row * (p.group * p.kv_heads) + head] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+        const float by = none ? 0.0f : 1.0f / l;
+        uint16_t* to = p.o + row * p.o_row + head * p.o_head;
+#pragma unroll 1
+        for (int c = 0; c < DP; c += 32) {
+            float v[32];
+            uint32_t o[32];
+            if (n > 0) {
+                tmem_ld32(sums + c, o);
+                tmem_ld32_wait(o);
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = n > 0 && !none ? __uint_as_float(o[e]) * by : 0.0f;
+            if (live && c < p.dim) store_row32<T>(to, c, p.dim, p.o_vec, v);
+        }
+    }
+    tc_fence_before();
+}
+
+template <int T, int DP>
+__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ Params p)
+{
+    using S = Shape<DP>;
+    extern __shared__ __align__(1024) char smem_raw[];
+    const uint32_t smem = smem_addr(smem_raw);
+    if (smem & 1023u) {   // every thread sees the same address; there is no padding to move within
+        g_attention_wait_expired = 1;
+        return;
+    }
+    const uint32_t bars = smem + S::kAtBars;
+    char* tail = smem_raw + S::kAtBars + ((S::kBars * 8 + 15) & ~15);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail);
+    volatile int* gave_up = reinterpret_cast<volatile int*>(tail + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kBars; ++i) mbar_init(bars + 8 * i, i >= S::kTerms && i < S::kSums ? 4 : 1);
+        *gave_up = 0;
+        mbar_init_fence();
+    }
+    wait_for_predecessor();
+    if (p.zero) fill_rows(p.fill, p.seqs.q_starts, p.seqs.count, p.seqs.q_rows);
+    Work w;
+    if (!find_work(p, w)) return;   // the same for every warp
+    if (warp == 9) tmem_alloc<false>(smem_addr(tmem_slot), kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int n = w.n[0] > w.n[1] ? w.n[0] : w.n[1];
+
+    if (warp == 8) {
+        if (n > 0 && elect_one()) load<DP>(p, w, n, smem, bars, gave_up);
+        __syncwarp();
+    } else if (warp == 9) {
+        if (n > 0) issue<DP>(p, w, n, smem, bars, tmem, lane, gave_up);
+    } else {
+        const int i = warp >> 2, r = threadIdx.x & 127;
+        if (i < p.tiles && w.t0 + i * p.tokens < w.seq.lq)
+            softmax<T, DP>(p, w, i, r, bars, tmem + ((uint32_t)((warp & 3) * 32) << 16), gave_up);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && *gave_up) atomicExch(&g_attention_wait_expired, 1);
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_free<false>(tmem, kTmemCols);
+    }
+}
+
+// The parts of a row's keys: o = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s.  A warp a row.
+template <int T, int DP>
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Params p)
+{
+    wait_for_predecessor();
+    Sequence seq;
+    uint32_t unit, units;
+    const uint32_t head = blockIdx.x % p.kv_heads;
+    if (!find_unit<false>(p.seqs, blockIdx.x / p.kv_heads, p.tokens, seq, unit, units)) return;
+    if (p.causal) unit = units - 1 - unit;
+    const int r = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31, used = p.tokens * p.group;
+    const int token = (int)unit * p.tokens + r / p.group;
+    if (r >= used || token >= seq.lq) return;
+    const int64_t first = (int64_t)blockIdx.x * p.splits * used + r;
+    float m = -INFINITY;
+    for (uint32_t s = lane; s < p.splits; s += 32) m = fmaxf(m, p.part_stats[first + (int64_t)s * used].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    constexpr int kPer = DP / 32;
+    float l = 0.0f, v[kPer] = {};
+    for (uint32_t s = 0; s < p.splits; ++s) {
+        const float2 st = p.part_stats[first + (int64_t)s * used];
+        if (st.y == 0.0f) continue;   // no key of this part is seen; of no keys at all there is nothing to read
+        const float by = exp2_fast(st.x - m);
+        const float* from = p.part + (first + (int64_t)s * used) * DP + lane * kPer;
+        l = __fmaf_rn(by, st.y, l);
+        float t[kPer];
+        if constexpr (kPer == 4) *reinterpret_cast<float4*>(t) = *reinterpret_cast<const float4*>(from);
+        else *reinterpret_cast<float2*>(t) = *reinterpret_cast<const float2*>(from);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) v[e] = __fmaf_rn(by, t[e], v[e]);
+    }
+    const int64_t row = seq.q0 + token;
+    const int h = (int)head * p.group + r % p.group;
+    const bool none = l == 0.0f;
+    if (lane == 0 && p.lse) p.lse[row * (p.group * p.kv_heads) + h] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+    const float by = none ? 0.0f : 1.0f / l;
+    uint16_t* to = p.o + row * p.o_row + h * p.o_head + lane * kPer;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e)
+        if (lane * kPer + e < p.dim) store_elem(to, e, T, v[e] * by);
+}
+
+__global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackList p)
+{
+    wait_for_predecessor();
+    int j = 0;
+    while (j + 1 < p.jobs && blockIdx.x >= p.job[j + 1].first) ++j;
+    const auto& q = p.job[j];
+    const unsigned blocks = (j + 1 < p.jobs ? p.job[j + 1].first : p.blocks) - q.first;
+    const int64_t lines = q.rows * q.heads;   // a warp a line
+    for (int64_t i = (int64_t)(blockIdx.x - q.first) * 8 + (threadIdx.x >> 5); i < lines; i += (int64_t)blocks * 8) {
+        const int64_t r = i / q.heads, h = i - r * q.heads;
+        for (int c = threadIdx.x & 31; c < p.dim; c += 32) q.to[i * p.pitch + c] = q.from[r * q.row + h * q.head + c];
+    }
+}
+
+}  // namespace
+
+bool tensor_ok(const void* p, int64_t row, int64_t head, int64_t rows, int64_t heads, int64_t dim, bool out)
+{
+    constexpr int64_t most = 1ll << 38;   // the tensor copies take strides below 2^40 bytes
+    if (!p || ((uintptr_t)p & 1u)) return false;
+    if (rows > 1 && (row < dim || row > most)) return false;
+    if (heads > 1 && (head < dim || head > most)) return false;
+    if (!out || rows <= 1 || heads <= 1) return true;
+    return row >= (heads - 1) * head + dim || (__int128)head >= (__int128)(rows - 1) * row + dim;
+}
+bool tensor_tma(const void* p, int64_t row, int64_t head, int64_t rows, int64_t heads)
+{
+    return aligned16(p) && (rows <= 1 || row % 8 == 0) && (heads <= 1 || head % 8 == 0);
+}
+int tensor_vec(const void* p, int64_t row, int64_t head, int64_t rows, int64_t heads)
+{
+    const uint64_t bits = (uint64_t)(uintptr_t)p | (rows > 1 ? (uint64_t)row * 2 : 0) | (heads > 1 ? (uint64_t)head * 2 : 0);
+    return bits % 32 == 0 ? 2 : (bits % 16 == 0 ? 1 : 0);
+}
+
+Tensor3 PackList::add(const Tensor3& t, int64_t rows, int64_t heads, int64_t d, char*& to)
+{
+    if (tensor_tma(t.p, t.row, t.head, rows, heads)) return t;
+    dim = (int)d, pitch = (int)round_up(d, 8);
+    const int64_t want = (rows * heads + 63) / 64;   // eight lines a warp
+    job[jobs++] = {(const uint16_t*)t.p, (uint16_t*)to, t.row, t.head, rows, (int)heads, blocks};
+    blocks += (unsigned)(want < 1216 ? want : 1216);
+    const Tensor3 r = {to, pitch * heads, pitch};
+    to += packed_bytes(rows, heads, d);
+    return r;
+}
+gs_status PackList::run(cudaStream_t st) const
+{
+    return blocks ? launch_after(pack_kernel, dim3(blocks), 256, 0, 1, st, *this) : GS_OK;
+}
+
+gs_status forward_wait_report(int* expired)
+{
+    const int zero = 0;
+    GS_CUDA_TRY(cudaMemcpyFromSymbol(expired, g_attention_wait_expired, sizeof *expired));
+    if (*expired) GS_CUDA_TRY(cudaMemcpyToSymbol(g_attention_wait_expired, &zero, sizeof zero));
+    return GS_OK;
+}
+
+namespace {
+
+// How a call is cut: tiles of a unit, and parts of the keys.
+struct Plan {
+    int group, tokens, tiles, dp;
+    uint32_t splits;
+    int64_t units, items;   // units at most; times key heads and splits
+    size_t part, stats;     // bytes of the parts' sums and of their maxima
+    size_t packs, bytes;
+};
+
+Plan plan_for(const gs_attention_args& a)
+{
+    Plan r = {};
+    r.group = a.heads / a.kv_heads;
+    r.tokens = kRows / r.group;
+    r.dp = a.dim <= 64 ? 64 : 128;
+    const int known = device_sms();
+    const int64_t sms = known > 0 ? known : 152;
+    const bool starts = a.q_starts != nullptr;
+    const int64_t one = units_at_most(a.q_rows, a.sequences, starts, r.tokens);
+    const int64_t two = units_at_most(a.q_rows, a.sequences, starts, 2 * (int64_t)r.tokens);
+    // two tiles a CTA where there are CTAs enough all the same, and tokens for both
+    r.tiles = two * a.kv_heads >= sms && a.q_rows > a.sequences * r.tokens ? 2 : 1;
+    r.units = r.tiles == 2 ? two : one;
+    r.splits = 1;
+    const int64_t ctas = r.units * a.kv_heads, key_tiles = (a.k_rows / (a.sequences ? a.sequences : 1) + kRows - 1) / kRows;
+    if (r.tiles == 1 && ctas < 2 * sms && key_tiles > 1) {
+        int64_t s = ctas < sms ? sms / ctas : 4 * sms / ctas;
+        if (s > key_tiles) s = key_tiles;
+        r.splits = (uint32_t)s;
+    }
+    r.items = ctas * r.splits;
+    if (r.splits > 1) {
+        r.part = (size_t)round_up(r.items * r.tokens * r.group * r.dp * 4, 256);
+        r.stats = (size_t)round_up(r.items * r.tokens * r.group * 8, 256);
+    }
+    if (!tensor_tma(a.q, a.q_row, a.q_head, a.q_rows, a.heads)) r.packs += packed_bytes(a.q_rows, a.heads, a.dim);
+    if (!tensor_tma(a.k, a.k_row, a.k_head, a.k_rows, a.kv_heads)) r.packs += packed_bytes(a.k_rows, a.kv_heads, a.dim);
+    if (!tensor_tma(a.v, a.v_row, a.v_head, a.k_rows, a.kv_heads)) r.packs += packed_bytes(a.k_rows, a.kv_heads, a.dim);
+    r.bytes = r.part + r.stats + r.packs;
+    return r;
+}
+
+template <int T, int DP>
+gs_status launch(const Params& p, const Plan& plan, int64_t q_rows, cudaStream_t st)
+{
+    static std::atomic<uint64_t> done{0};
+    gs_status s = allow_smem(attention_kernel<T, DP>, Shape<DP>::kSmem, done);
+    if (s != GS_OK) return s;
+    s = launch_after(attention_kernel<T, DP>, dim3((unsigned)plan.items), kThreads, Shape<DP>::kSmem, 1, st, p);
+    if (s != GS_OK || plan.splits == 1) return s;
+    const int64_t rows = (q_rows < plan.tokens ? q_rows : plan.tokens) * plan.group;   // of a tile, at most
+    return launch_after(join_kernel<T, DP>, dim3((unsigned)(plan.items / plan.splits), (unsigned)((rows + 3) / 4)), 128, 0, 1, st, p);
+}
+
+}  // namespace
+}  // namespace attn
+}  // namespace gs
+
+using namespace gs;
+using namespace gs::attn;
+
+extern "C" gs_status gs_attention(const gs_attention_args* args, void* ws, size_t* ws_bytes, void* stream)
+{
+    GS_NVTX_RANGE("gs_attention");
+    if (!args) return GS_ERR_INVALID_ARG;
+    const gs_attention_args& a = *args;
+    if (!sizes_ok(a.q_rows, a.k_rows, a.sequences, a.heads, a.kv_heads, a.dim, a.type, a.scale, a.q_starts, a.k_starts))
+        return GS_ERR_INVALID_ARG;
+    if (((uintptr_t)a.k_lengths & 3u) || ((uintptr_t)a.lse & 3u)) return GS_ERR_INVALID_ARG;
+    if (a.q_rows > 0 && (!tensor_ok(a.q, a.q_row, a.q_head, a.q_rows, a.heads, a.dim, false) ||
+                         !tensor_ok(a.o, a.o_row, a.o_head, a.q_rows, a.heads, a.dim, true)))
+        return GS_ERR_INVALID_ARG;
+    if (a.k_rows > 0 && (!tensor_ok(a.k, a.k_row, a.k_head, a.k_rows, a.kv_heads, a.dim, false) ||
+                         !tensor_ok(a.v, a.v_row, a.v_head, a.k_rows, a.kv_heads, a.dim, false)))
+        return GS_ERR_INVALID_ARG;
+    const Plan plan = plan_for(a);
+    if (plan.items > 0x7fffffffll) return GS_ERR_INVALID_ARG;
+    const WsCheck wc = ws_check(ws, ws_bytes, plan.bytes);
+    if (wc == WsCheck::kBad) return GS_ERR_INVALID_ARG;
+    if (wc == WsCheck::kQuery) return GS_OK;
+    if (a.q_rows == 0) return GS_OK;
+    cudaStream_t st = (cudaStream_t)stream;
+    Params p = {};
+    char* to = (char*)ws + plan.part + plan.stats;
+    PackList packs;
+    const Tensor3 q = packs.add({a.q, a.q_row, a.q_head}, a.q_rows, a.heads, a.dim, to);
+    gs_status s = tile_map(&p.q, q, a.type, a.q_rows, a.heads, a.dim, plan.group, plan.tokens);
+    if (s == GS_OK && a.k_rows > 0) {   // without keys nothing is read from them
+        const Tensor3 k = packs.add({a.k, a.k_row, a.k_head}, a.k_rows, a.kv_heads, a.dim, to);
+        const Tensor3 v = packs.add({a.v, a.v_row, a.v_head}, a.k_rows, a.kv_heads, a.dim, to);
+        s = tile_map(&p.k, k, a.type, a.k_rows, a.kv_heads, a.dim, 1, kRows);
+        if (s == GS_OK) s = tile_map(&p.v, v, a.type, a.k_rows, a.kv_heads, a.dim, 1, kRows);
+    }
+    if (s == GS_OK) s = packs.run(st);
+    if (s != GS_OK) return s;
+    p.seqs = {a.q_starts, a.k_starts, a.k_lengths, a.q_rows, a.k_rows, (uint32_t)a.sequences};
+    p.fill = {(uint16_t*)a.o, a.o_row, a.o_head, a.lse, a.heads, a.dim};
+    p.zero = a.fill && a.q_starts;
+    p.o = (uint16_t*)a.o, p.o_row = a.o_row, p.o_head = a.o_head, p.lse = a.lse;
+    p.part = (float*)ws, p.part_stats = (float2*)((char*)ws + plan.part);
+    p.scale2 = a.scale * kLog2e;
+    p.splits = plan.splits, p.kv_heads = (uint32_t)a.kv_heads, p.tiles = plan.tiles, p.group = plan.group, p.tokens = plan.tokens;
+    p.dim = a.dim, p.causal = a.causal != 0;
+    p.o_vec = tensor_vec(a.o, a.o_row, a.o_head, a.q_rows, a.heads);
+    p.idesc_s = instr_desc(a.type, true, true, kRows, kRows);
+    p.idesc_o = instr_desc(a.type, true, false, (int)round_up(a.dim, 16), kRows);
+    if (a.type == GS_BF16) return plan.dp == 64 ? launch<GS_BF16, 64>(p, plan, a.q_rows, st) : launch<GS_BF16, 128>(p, plan, a.q_rows, st);
+    return plan.dp == 64 ? launch<GS_F16, 64>(p, plan, a.q_rows, st) : launch<GS_F16, 128>(p, plan, a.q_rows, st);
+}

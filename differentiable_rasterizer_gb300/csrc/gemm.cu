@@ -22,6 +22,7 @@
 #include <atomic>
 #include <type_traits>
 
+#include "attention.cuh"
 #include "gemm.cuh"
 #include "tc_common.cuh"
 
@@ -1124,8 +1125,8 @@ int device_sms()
 
 namespace tc {
 
-gs_status make_map(CUtensorMap* map, const void* p, int type, int64_t rows, int64_t cols, int64_t ld, int box_rows,
-                   int box_cols)
+static gs_status encode_map(CUtensorMap* map, const void* p, int type, int dims, const cuuint64_t* size, const cuuint64_t* pitch,
+                            const cuuint32_t* box)
 {
     using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -1140,19 +1141,34 @@ gs_status make_map(CUtensorMap* map, const void* p, int type, int64_t rows, int6
         return (Encode)f;
     }();
     if (!encode) return GS_ERR_CUDA;
-    const int esz = type_bytes(type);
     const CUtensorMapDataType dt = type == GS_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : type == GS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                    : type == GS_F16  ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                      : CU_TENSOR_MAP_DATA_TYPE_UINT8;
-    const cuuint64_t size[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t pitch[1] = {(cuuint64_t)(ld * esz)};
-    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
-    const cuuint32_t unit[2] = {1, 1};
-    const CUresult r = encode(map, dt, 2, const_cast<void*>(p), size, pitch, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+    const cuuint32_t unit[3] = {1, 1, 1};
+    const CUresult r = encode(map, dt, (cuuint32_t)dims, const_cast<void*>(p), size, pitch, box, unit,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? GS_OK : GS_ERR_CUDA;
+}
+
+gs_status make_map(CUtensorMap* map, const void* p, int type, int64_t rows, int64_t cols, int64_t ld, int box_rows,
+                   int box_cols)
+{
+    const cuuint64_t size[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t pitch[1] = {(cuuint64_t)(ld * type_bytes(type))};
+    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+    return encode_map(map, p, type, 2, size, pitch, box);
+}
+
+gs_status make_map3(CUtensorMap* map, const void* p, int type, const int64_t (&size)[3], const int64_t (&pitch)[2],
+                    const int (&box)[3])
+{
+    const int64_t e = type_bytes(type);
+    const cuuint64_t sizes[3] = {(cuuint64_t)size[0], (cuuint64_t)size[1], (cuuint64_t)size[2]};
+    const cuuint64_t pitches[2] = {(cuuint64_t)(pitch[0] * e), (cuuint64_t)(pitch[1] * e)};
+    const cuuint32_t boxes[3] = {(cuuint32_t)box[0], (cuuint32_t)box[1], (cuuint32_t)box[2]};
+    return encode_map(map, p, type, 3, sizes, pitches, boxes);
 }
 
 }  // namespace tc
@@ -1321,14 +1337,17 @@ extern "C" gs_status gs_wait_report(int32_t* expired)
     GS_NVTX_RANGE("gs_wait_report");
     if (!expired) return GS_ERR_INVALID_ARG;
     *expired = 0;
-    int v = 0, narrow = 0;
+    int v = 0;
     const int zero = 0;
     GS_CUDA_TRY(cudaDeviceSynchronize());
     GS_CUDA_TRY(cudaMemcpyFromSymbol(&v, g_wait_expired, sizeof v));
     if (v) GS_CUDA_TRY(cudaMemcpyToSymbol(g_wait_expired, &zero, sizeof zero));
-    const gs_status s = glu_narrow_wait_report(&narrow);
-    if (s != GS_OK) return s;
-    v |= narrow;
+    for (gs_status (*report)(int*) : {glu_narrow_wait_report, attn::forward_wait_report}) {
+        int other = 0;
+        const gs_status s = report(&other);
+        if (s != GS_OK) return s;
+        v |= other;
+    }
     *expired = v;
     return v ? GS_ERR_TIMEOUT : GS_OK;
 }

@@ -10,6 +10,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <cmath>
 #include <string>
 
 #include <ATen/core/Tensor.h>
@@ -36,6 +37,7 @@ struct Library {
     decltype(&gs_linear_bwd) linear_bwd;
     decltype(&gs_glu) glu;
     decltype(&gs_glu_bwd) glu_bwd;
+    decltype(&gs_attention) attention;
 };
 Library lib = {};
 PyObject* gs_error = nullptr;   // abi.GsError
@@ -527,15 +529,117 @@ PyObject* glu_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
-// bind(GsError, address of gs_rms_norm, ..._bwd, quantize_rows, linear, linear_bwd, glu, glu_bwd)
+// ------------------------------------------------------------------ attention
+// [rows][heads][dim], the last dimension contiguous.
+struct Heads {
+    void* p = nullptr;
+    int64_t row = 0, head = 0, rows = 0;
+    int heads = 0, dim = 0, type = 0;
+};
+Heads heads_of(const Tensor& t, const char* name, unsigned types, int dev, int64_t rows = -1, int64_t heads = -1, int64_t dim = -1)
+{
+    check_kind(t, name, types, dev);
+    if (t.dim() != 3) refuse(std::string(name) + ": expected [rows, heads, dim], got " + shape_of(t));
+    if ((rows >= 0 && t.size(0) != rows) || (heads >= 0 && t.size(1) != heads) || (dim >= 0 && t.size(2) != dim))
+        refuse(std::string(name) + ": expected [" + (rows >= 0 ? std::to_string(rows) : "rows") + ", " +
+               (heads >= 0 ? std::to_string(heads) : "heads") + ", " + (dim >= 0 ? std::to_string(dim) : "dim") + "], got " + shape_of(t));
+    if (t.size(1) < 1 || t.size(1) > 65536) refuse(std::string(name) + ": 1 to 65536 heads, got " + shape_of(t));
+    if (t.size(2) < 1 || t.size(2) > GS_ATTENTION_MAX_DIM)
+        refuse(std::string(name) + ": 1 to " + std::to_string(GS_ATTENTION_MAX_DIM) + " columns a head, got " + shape_of(t));
+    if (t.size(2) > 1 && t.stride(2) != 1) refuse(std::string(name) + ": the last dimension is not contiguous, " + shape_of(t));
+    Heads h;
+    h.rows = t.size(0), h.heads = (int)t.size(1), h.dim = (int)t.size(2);
+    h.row = t.stride(0), h.head = t.stride(1);
+    if ((h.rows > 1 && h.row < h.dim) || (h.heads > 1 && h.head < h.dim)) refuse(std::string(name) + ": rows overlap, " + shape_of(t));
+    h.type = type_code(t.scalar_type());
+    h.p = t.data_ptr();
+    return h;
+}
+const int32_t* indices(PyObject* o, const char* name, int dev, int64_t size)   // None: NULL
+{
+    if (o == Py_None) return nullptr;
+    const Tensor& t = tensor(o, name);
+    if (t.scalar_type() != ScalarType::Int) refuse(std::string(name) + ": expected int32, got " + c10::toString(t.scalar_type()));
+    if (!t.is_cuda() || t.get_device() != dev)
+        refuse(std::string(name) + ": on " + t.device().str() + ", expected cuda:" + std::to_string(dev));
+    if (t.dim() != 1 || !t.is_contiguous() || (size >= 0 && t.numel() != size))
+        refuse(std::string(name) + ": expected " + (size >= 0 ? std::to_string(size) : "a vector of") + " contiguous values, got " + shape_of(t));
+    return t.data_ptr<int32_t>();
+}
+// q_starts and k_starts (None: q_starts), the number of sequences.
+template <class Args>
+void sequences_of(Args& g, PyObject* q_starts, PyObject* k_starts, int dev)
+{
+    g.sequences = 1;
+    if (q_starts == Py_None) {
+        if (k_starts != Py_None) refuse("q_starts: required with k_starts");
+        return;
+    }
+    g.q_starts = indices(q_starts, "q_starts", dev, -1);
+    const int64_t n = THPVariable_Unpack(q_starts).numel();
+    if (n < 1) refuse("q_starts: expected the sequences' starts and the end of the last, got no value");
+    g.sequences = n - 1;
+    g.k_starts = k_starts == Py_None ? g.q_starts : indices(k_starts, "k_starts", dev, n);
+}
+float scale_of(PyObject* o, int dim)
+{
+    return o == Py_None ? (float)(1.0 / std::sqrt((double)dim)) : number(o, "scale");
+}
+
+// (q, k, v, q_starts, k_starts, k_lengths, causal, scale, out, need_backward) -> (o, lse)
+PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded(n, 10, [&] {
+        const Tensor& q = tensor(a[0], "q");
+        const int dev = cuda_device(q, "q");
+        const c10::cuda::OptionalCUDAGuard guard(q.device());
+        const Heads hq = heads_of(q, "q", kHalf, dev);
+        const Heads hk = heads_of(tensor(a[1], "k"), "k", 1u << hq.type, dev, -1, -1, hq.dim);
+        const Heads hv = heads_of(tensor(a[2], "v"), "v", 1u << hq.type, dev, hk.rows, hk.heads, hq.dim);
+        if (hq.heads % hk.heads || hq.heads / hk.heads > GS_ATTENTION_MAX_GROUP)
+            refuse("k: " + std::to_string(hk.heads) + " heads do not divide q's " + std::to_string(hq.heads) + " into groups of at most " +
+                   std::to_string(GS_ATTENTION_MAX_GROUP));
+        gs_attention_args g = {};
+        g.q_rows = hq.rows, g.k_rows = hk.rows;
+        g.q = hq.p, g.q_row = hq.row, g.q_head = hq.head, g.k = hk.p, g.k_row = hk.row, g.k_head = hk.head;
+        g.v = hv.p, g.v_row = hv.row, g.v_head = hv.head;
+        g.heads = hq.heads, g.kv_heads = hk.heads, g.dim = hq.dim, g.type = hq.type;
+        sequences_of(g, a[3], a[4], dev);
+        g.k_lengths = indices(a[5], "k_lengths", dev, g.sequences);
+        g.causal = flag(a[6], "causal");
+        g.scale = scale_of(a[7], hq.dim);
+        const bool backward = flag(a[9], "need_backward");
+        if (backward && g.k_lengths) refuse("need_backward: the gradients take no k_lengths; pack the keys");
+        Tensor o, lse;
+        if (a[8] != Py_None) {
+            o = tensor(a[8], "out");
+            const Heads ho = heads_of(o, "out", 1u << hq.type, dev, hq.rows, hq.heads, hq.dim);
+            g.o = ho.p, g.o_row = ho.row, g.o_head = ho.head;
+        } else {
+            o = at::empty({hq.rows, hq.heads, hq.dim}, q.options());
+            g.o = o.data_ptr(), g.o_row = (int64_t)hq.heads * hq.dim, g.o_head = hq.dim;
+            g.fill = 1;
+        }
+        if (backward) {
+            lse = at::empty({hq.rows, hq.heads}, q.options().dtype(ScalarType::Float));
+            g.lse = lse.data_ptr<float>();
+        }
+        with_scratch("gs_attention", lib.attention, g, q, dev, true);
+        if (a[8] != Py_None && !o.is_inference()) o.unsafeGetTensorImpl()->bump_version();
+        return result(o, lse);
+    });
+}
+
+// bind(GsError, addresses of the library's functions in the order of Library)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    if (n != 8) {
-        PyErr_SetString(PyExc_TypeError, "bind: 8 arguments");
+    constexpr int kFunctions = sizeof(Library) / sizeof(void*);
+    if (n != kFunctions + 1) {
+        PyErr_Format(PyExc_TypeError, "bind: %d arguments", kFunctions + 1);
         return nullptr;
     }
-    void* f[7];
-    for (int i = 0; i < 7; ++i) {
+    void* f[kFunctions];
+    for (int i = 0; i < kFunctions; ++i) {
         f[i] = PyLong_AsVoidPtr(a[i + 1]);
         if (!f[i]) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind: null function");
@@ -549,6 +653,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
     lib.linear_bwd = reinterpret_cast<decltype(lib.linear_bwd)>(f[4]);
     lib.glu = reinterpret_cast<decltype(lib.glu)>(f[5]);
     lib.glu_bwd = reinterpret_cast<decltype(lib.glu_bwd)>(f[6]);
+    lib.attention = reinterpret_cast<decltype(lib.attention)>(f[7]);
     Py_INCREF(a[0]);
     Py_XDECREF(gs_error);
     gs_error = a[0];
@@ -558,7 +663,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 #define GS_FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {GS_FAST(bind),          GS_FAST(rms_norm), GS_FAST(rms_norm_backward), GS_FAST(quantize_rows),
                          GS_FAST(linear),        GS_FAST(linear_backward), GS_FAST(glu),       GS_FAST(glu_backward),
-                         {nullptr, nullptr, 0, nullptr}};
+                         GS_FAST(attention),     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layers_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

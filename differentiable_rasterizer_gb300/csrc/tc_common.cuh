@@ -301,6 +301,9 @@ __host__ __device__ constexpr uint32_t instr_desc(int type, bool a_k_fast, bool 
 // (box_cols elements) under the 128-byte swizzle.
 gs_status make_map(CUtensorMap* map, const void* p, int type, int64_t rows, int64_t cols, int64_t ld, int box_rows,
                    int box_cols);
+// Three dimensions, the fastest first, the two slower ones at `pitch` elements each.
+gs_status make_map3(CUtensorMap* map, const void* p, int type, const int64_t (&size)[3], const int64_t (&pitch)[2],
+                    const int (&box)[3]);
 
 }  // namespace tc
 }  // namespace gs

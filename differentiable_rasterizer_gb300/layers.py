@@ -1,6 +1,6 @@
 """Decoder layers on torch tensors: the norm, the matrix product with its epilogue, the
 gated feed-forward and their gradients, through the C ABI (``gs_rms_norm``,
-``gs_linear``, ``gs_glu`` ... in ``include/gs.h``, which states the formulas).
+``gs_linear``, ``gs_glu``, ``gs_attention`` ... in ``include/gs.h``, which states the formulas).
 
     o = rms_norm(x, weight, residual=r)                      # o.y, o.s = x + r
     q = rms_norm(x, weight, residual=r, out_dtype=torch.float8_e4m3fn)   # q.y, q.scale
@@ -62,6 +62,11 @@ class GluOut(NamedTuple):
     u: Optional[torch.Tensor]
 
 
+class AttentionOut(NamedTuple):
+    o: torch.Tensor
+    lse: Optional[torch.Tensor]     # [rows, heads], for the gradients
+
+
 class LinearGrads(NamedTuple):
     dx: Optional[torch.Tensor]
     dw: Optional[torch.Tensor]
@@ -87,8 +92,10 @@ class _Native:
         loader.exec_module(module)
         L = abi.lib()
         module.bind(abi.GsError, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
-            "gs_rms_norm", "gs_rms_norm_bwd", "gs_quantize_rows", "gs_linear", "gs_linear_bwd", "gs_glu", "gs_glu_bwd")))
-        for f in ("rms_norm", "rms_norm_backward", "quantize_rows", "linear", "linear_backward", "glu", "glu_backward"):
+            "gs_rms_norm", "gs_rms_norm_bwd", "gs_quantize_rows", "gs_linear", "gs_linear_bwd", "gs_glu", "gs_glu_bwd",
+            "gs_attention")))
+        for f in ("rms_norm", "rms_norm_backward", "quantize_rows", "linear", "linear_backward", "glu", "glu_backward",
+                  "attention"):
             setattr(self, f, getattr(module, f))
         return self.__dict__[name]
 
@@ -178,3 +185,19 @@ def glu_backward(dh, x, w_gate, w_up, g=None, u=None, *, act="silu", need_dx=Tru
     """Gradients of glu from dh; g, u: glu's with need_backward (None: computed again).  dx has
     x's type, dw_gate and dw_up dw_dtype (default x's; float32 also)."""
     return GluGrads(*_native.glu_backward(dh, x, w_gate, w_up, g, u, _act(act), need_dx, need_dw, dw_dtype))
+
+
+# ------------------------------------------------------------------ attention
+def attention(q, k, v, *, q_starts=None, k_starts=None, k_lengths=None, causal=False, scale=None, out=None,
+              need_backward=False) -> AttentionOut:
+    """o = softmax(scale q k^T) v, for each head and each of the sequences packed in the rows.
+
+    q [rows, heads, dim], k, v [key rows, key heads, dim]: bfloat16 or float16, dim at most
+    128; key heads divide heads (head h uses key head h // (heads // key heads)).  Rows and
+    heads may have any strides (slices of one projection's output are fine).  scale: dim^-1/2.
+    q_starts, k_starts: int32, sequence s has the rows starts[s] to starts[s + 1] (k_starts:
+    default q_starts; without either, one sequence of all rows).  k_lengths: int32, how many
+    of a sequence's keys are in use (a cache's slots), without gradients.  causal: the last
+    query sees every key, the one before all but one, ...  A query that sees none gives 0.
+    out: like q, rows of no sequence are left as they are; else o is allocated, those rows 0."""
+    return AttentionOut(*_native.attention(q, k, v, q_starts, k_starts, k_lengths, causal, scale, out, need_backward))

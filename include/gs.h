@@ -443,10 +443,11 @@ GS_API gs_status gs_check_report(uint64_t* report, int32_t* checked);
 /* ---- Decoder layers: the network in front of the rasterizer ----
  * Rows are Gaussians (or tokens of a reconstruction model), features are
  * columns; the last layer may write the [n][stride] parameter buffer itself.
- * Three operators and their gradients:
+ * Operators and their gradients:
  *   gs_rms_norm   s = x + residual, y = s / rms(s) * weight, also in e4m3 with scales
  *   gs_linear     y = act(x w^T + bias) + residual
  *   gs_glu        h = act(x Wg^T) * (x Wu^T)   (gs_linear is the down projection)
+ *   gs_attention  o = softmax(scale q k^T) v over packed sequences
  * Conventions, besides those at the top of this file:
  *   - Matrices are row-major: element (r, c) of a matrix with leading dimension
  *     ld (in elements, >= its columns) is p[r * ld + c].  Any ld and any
@@ -669,6 +670,52 @@ typedef struct gs_glu_bwd_args {
     int32_t type, dw_type, act, reserved;
 } gs_glu_bwd_args;
 GS_API gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* ws_bytes, void* stream);
+
+/* Attention over packed sequences.
+ *   t_ij = scale q_i . k_j  for the keys j < Lk that query i sees: all, or with
+ *          causal j <= i + Lk - Lq (the last query sees every key)
+ *   lse_i = ln(sum_j exp t_ij),  o_i = sum_j exp(t_ij - lse_i) v_j
+ * A query that sees no key has o = 0 and lse = -infinity.
+ * q, o: [q_rows][heads][dim], k, v: [k_rows][kv_heads][dim], all of `type` (BF16
+ * or F16); element (r, h, c) of q is q[r * q_row + h * q_head + c], any row and
+ * head strides that keep heads apart (o, dq, dk, dv: and rows apart).  kv_heads
+ * divides heads, at most GS_ATTENTION_MAX_GROUP query heads share one (head h
+ * uses key head h / (heads / kv_heads)).  dim: 1..GS_ATTENTION_MAX_DIM.  lse:
+ * [q_rows][heads] or NULL; the gradients need it.  scale: finite, positive.
+ * Sequences: q_starts, k_starts: [sequences + 1] device arrays, sequence s has the
+ * rows q_starts[s] .. q_starts[s + 1] - 1 of q and those of k_starts of k and v;
+ * both NULL: one sequence of all rows (sequences = 1).  k_lengths: NULL, or
+ * [sequences]: keys in use, the first of each sequence's rows.  The starts must
+ * not decrease; they and the lengths are held within the arrays when read, so that
+ * bad ones give wrong values but no access outside.  Rows of o and lse that belong
+ * to no sequence are left as they are (fill = 0) or set to zero (fill = 1).
+ * Rows of other sequences have no influence, whatever they hold.  A NaN or an infinity
+ * among a sequence's own values reaches queries that it is hidden from, if they are
+ * less than 256 rows of the group before the first that sees it.
+ * Scores, maxima, sums and outputs are fp32 until o's rounding; exp(t - m), m a
+ * running maximum, is rounded to `type` as a factor of its product with v.
+ * Errors: INVALID_ARG for bad pointers, sizes, types or a too small workspace;
+ * CUDA on launch failure. */
+#define GS_ATTENTION_MAX_DIM 128
+#define GS_ATTENTION_MAX_GROUP 128
+typedef struct gs_attention_args {
+    int64_t q_rows, k_rows, sequences;
+    const void* q;
+    int64_t q_row, q_head;
+    const void* k;
+    int64_t k_row, k_head;
+    const void* v;
+    int64_t v_row, v_head;
+    const int32_t* q_starts;
+    const int32_t* k_starts;
+    const int32_t* k_lengths;
+    void* o;
+    int64_t o_row, o_head;
+    float* lse;
+    float scale;
+    int32_t heads, kv_heads, dim, type, causal, fill, reserved;
+} gs_attention_args;
+GS_API gs_status gs_attention(const gs_attention_args* args, void* ws, size_t* ws_bytes, void* stream);
 
 /* The layers' products wait on their own copies and tensor-core work, each wait
  * bounded to about two seconds of the multiprocessor's clock; a kernel whose wait
