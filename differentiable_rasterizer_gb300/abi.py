@@ -32,7 +32,7 @@ EXPORTS = ("gs_project", "gs_bin_sort", "gs_raster_fused_fwd_bwd", "gs_grad_comp
            "gs_raster_forward_state", "gs_dssim_loss_grad", "gs_raster_backward_state", "gs_grad_compact_static",
            "gs_prune_tiles", "gs_split_ranges", "gs_compose", "gs_raster_work_counts", "gs_check_report",
            "gs_rms_norm", "gs_rms_norm_bwd", "gs_quantize_rows", "gs_linear", "gs_linear_bwd", "gs_glu", "gs_glu_bwd",
-           "gs_attention", "gs_wait_report", "gs_layer_tile",
+           "gs_attention", "gs_attention_bwd", "gs_wait_report", "gs_layer_tile",
            "gs_error_string", "gs_param_rows", "gs_param_stride", "gs_num_tiles", "gs_version")
 
 
@@ -107,7 +107,8 @@ def lib():
         for name in ("gs_rms_norm", "gs_quantize_rows"):
             getattr(L, name).argtypes = [ctypes.c_char_p, _P]
             getattr(L, name).restype = ctypes.c_int
-        for name in ("gs_rms_norm_bwd", "gs_linear", "gs_linear_bwd", "gs_glu", "gs_glu_bwd", "gs_attention"):
+        for name in ("gs_rms_norm_bwd", "gs_linear", "gs_linear_bwd", "gs_glu", "gs_glu_bwd", "gs_attention",
+                     "gs_attention_bwd"):
             getattr(L, name).argtypes = [ctypes.c_char_p, _P, ctypes.POINTER(ctypes.c_size_t), _P]
             getattr(L, name).restype = ctypes.c_int
         L.gs_wait_report.argtypes = [ctypes.POINTER(ctypes.c_int32)]
@@ -331,6 +332,7 @@ _LINEAR = struct.Struct("=qqq Qq Qq QQ Q Qq Qq Qq iiii")
 _LINEAR_BWD = struct.Struct("=qqq Qq Qq Qq Qq Qq Qq Q iiii ii")
 _GLU = struct.Struct("=qqq Qq Qq Qq QQQ Qq Qq Qq iiii")
 _ATTENTION = struct.Struct("=qqq Qqq Qqq Qqq QQQ Qqq Q f iiiiiii")
+_ATTENTION_BWD = struct.Struct("=qqq Qqq Qqq Qqq Qqq Qqq Q QQ Qqq Qqq Qqq f iiiiiii")
 _GLU_BWD = struct.Struct("=qqq Qq Qq Qq Qq Qq Qq Qq Qq Qq iiii")
 
 
@@ -400,6 +402,14 @@ def attention_args(q_rows, k_rows, sequences, q, q_row, q_head, k, k_row, k_head
                            k_starts, k_lengths, o, o_row, o_head, lse, scale, heads, kv_heads, dim, type_, causal, fill, 0)
 
 
+def attention_bwd_args(q_rows, k_rows, sequences, q, q_row, q_head, k, k_row, k_head, v, v_row, v_head, o, o_row, o_head,
+                       d_o, do_row, do_head, lse, q_starts, k_starts, dq, dq_row, dq_head, dk, dk_row, dk_head, dv, dv_row,
+                       dv_head, scale, heads, kv_heads, dim, type_, causal, fill) -> bytes:
+    return _ATTENTION_BWD.pack(q_rows, k_rows, sequences, q, q_row, q_head, k, k_row, k_head, v, v_row, v_head, o, o_row,
+                               o_head, d_o, do_row, do_head, lse, q_starts, k_starts, dq, dq_row, dq_head, dk, dk_row,
+                               dk_head, dv, dv_row, dv_head, scale, heads, kv_heads, dim, type_, causal, fill, 0)
+
+
 def gs_rms_norm_bwd(args: bytes, ws, ws_bytes, stream):
     """args: rms_norm_bwd_args(...); ws: device pointer of ws_bytes, or None and None where none is needed."""
     layer_run("gs_rms_norm_bwd", args, ws, ws_bytes, stream)
@@ -423,6 +433,10 @@ def gs_glu_bwd(args: bytes, ws, ws_bytes, stream):
 
 def gs_attention(args: bytes, ws, ws_bytes, stream):
     layer_run("gs_attention", args, ws, ws_bytes, stream)
+
+
+def gs_attention_bwd(args: bytes, ws, ws_bytes, stream):
+    layer_run("gs_attention_bwd", args, ws, ws_bytes, stream)
 
 
 def layer_ws_bytes(name: str, args: bytes) -> int:

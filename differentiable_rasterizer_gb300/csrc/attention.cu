@@ -72,13 +72,6 @@ struct Work {
     int n[2];          // tiles of keys from there for either tile of the unit
 };
 
-// Keys that the tokens up to `last` of a sequence see.
-__device__ __forceinline__ int keys_seen(const Sequence& s, int last, bool causal)
-{
-    const int e = causal ? last + 1 + s.lk - s.lq : s.lk;
-    return e < 0 ? 0 : (e < s.lk ? e : s.lk);
-}
-
 __device__ __forceinline__ bool find_work(const Params& p, Work& w)
 {
     const uint32_t split = blockIdx.x % p.splits, rest = blockIdx.x / p.splits;

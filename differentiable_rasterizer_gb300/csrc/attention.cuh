@@ -86,6 +86,13 @@ __device__ __forceinline__ bool find_unit(const Sequences& p, uint32_t u, int to
     }
     return false;
 }
+// Keys that the tokens up to `last` of a sequence see.
+__device__ __forceinline__ int keys_seen(const Sequence& s, int last, bool causal)
+{
+    const int e = causal ? last + 1 + s.lk - s.lq : s.lk;
+    return e < 0 ? 0 : (e < s.lk ? e : s.lk);
+}
+
 // The units' number at most, known without the starts.
 inline int64_t units_at_most(int64_t rows, int64_t sequences, bool starts, int64_t tokens)
 {

@@ -1,0 +1,895 @@
+// attention_bwd.cu -- the gradients of attention over packed sequences.
+//
+//   delta = do . o (a row),  p = exp(scale q k^T - lse),  ds = p (do v^T - delta)
+//   dv = p^T do,  dk = scale ds^T q,  dq = scale ds k
+//
+// Scores and do v^T are computed again from the tiles, so that nothing of the size of
+// queries times keys is stored.  Three launches: delta with the row statistics; dk and dv,
+// a tile of keys a CTA against all its queries; dq, two tiles of queries a CTA against
+// their keys.  dq could come out of the second's products, but its sum runs over the CTAs
+// there: atomics would make its bits depend on the run, so dq's kernel computes scores and
+// do v^T a second time (seven products of a pair in place of five).
+//
+// Both product kernels keep p and ds out of shared memory: a tile's scores are computed
+// with the rows that stay (keys, or queries) as TMEM lanes, p and ds take their place in
+// TMEM as 16 bits, and are the first factor of the next products from there.
+//
+// f16 holds neither small p nor small ds among its normal numbers: p is taken times 2^12
+// (at most 1 times that), ds times the power of two that brings its bound, 2 dim max|do|
+// max|v|, to 2^15; the sums are scaled back at the end.
+#include <atomic>
+
+#include "attention.cuh"
+
+namespace gs {
+namespace attn {
+namespace {
+
+constexpr int kWarps = 10, kThreads = kWarps * 32;
+constexpr int kTmemCols = 512;
+constexpr int kStatRows = kRows + 2;   // of a copy of row statistics, which starts on 16 bytes
+
+__device__ int g_attention_bwd_wait_expired;
+
+struct Params {
+    CUtensorMap q, k, v, d_o;
+    Sequences seqs;
+    Fill fill_dq, fill_dk, fill_dv;
+    const float2* stats;     // [key head][token][head of the group]: lse log2(e) (infinite for a row that sees no key), delta
+    const float* most;       // F16: the blocks' largest |do| and |v|
+    int most_count;
+    uint16_t *dq, *dk, *dv;
+    int64_t dq_row, dq_head, dk_row, dk_head, dv_row, dv_head;
+    int64_t stat_pitch;      // of a key head
+    float scale, scale2;     // scale2: scale log2(e)
+    uint32_t kv_heads;
+    int tiles, group, tokens, dim, causal, zero, dq_vec, dk_vec, dv_vec;
+    uint32_t idesc_s, idesc_d;
+};
+
+// ------------------------------------------------------------------ row statistics
+struct StatParams {
+    const uint16_t *o, *d_o, *v;
+    int64_t o_row, o_head, do_row, do_head, v_row, v_head;
+    const float* lse;
+    float2* stats;
+    float* most;
+    int64_t q_rows, k_rows, stat_pitch;
+    int heads, kv_heads, group, dim, vec;
+};
+
+// A warp a row and head, 8 elements a lane.
+template <int T>
+__global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ StatParams p)
+{
+    __shared__ float most[2][8];
+    wait_for_predecessor();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t step = (int64_t)gridDim.x * 8, lines = p.q_rows * p.heads;
+    float most_do = 0.0f, most_v = 0.0f;
+    for (int64_t i = (int64_t)blockIdx.x * 8 + warp; i < lines; i += step) {
+        const int64_t r = i / p.heads;
+        const int h = (int)(i - r * p.heads);
+        const uint16_t *o = p.o + r * p.o_row + h * p.o_head, *d = p.d_o + r * p.do_row + h * p.do_head;
+        float sum = 0.0f;
+        if (lane * 8 < p.dim) {   // the same sum in either case
+            float a[8], b[8];
+            if (p.vec) {
+                load8(o, lane * 8, T, a);
+                load8(d, lane * 8, T, b);
+            } else
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const bool there = lane * 8 + e < p.dim;
+                    a[e] = there ? load_elem(o, lane * 8 + e, T) : 0.0f;
+                    b[e] = there ? load_elem(d, lane * 8 + e, T) : 0.0f;
+                }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                sum = __fmaf_rn(a[e], b[e], sum);
+                most_do = fmaxf(most_do, fabsf(b[e]));
+            }
+        }
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+        if (lane == 0) {
+            const float lse = p.lse[i];
+            // a row that sees no key: every p is 2^-infinity
+            p.stats[(h / p.group) * p.stat_pitch + r * p.group + h % p.group] =
+                make_float2(lse == -INFINITY ? INFINITY : lse * kLog2e, lse == -INFINITY ? 0.0f : sum);
+        }
+    }
+    if (!p.most) return;
+    for (int64_t i = (int64_t)blockIdx.x * 8 + warp; i < p.k_rows * p.kv_heads; i += step) {
+        const int64_t r = i / p.kv_heads;
+        const uint16_t* v = p.v + r * p.v_row + (i - r * p.kv_heads) * p.v_head;
+        for (int c = lane; c < p.dim; c += 32) most_v = fmaxf(most_v, fabsf(load_elem(v, c, T)));
+    }
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) {
+        most_do = fmaxf(most_do, __shfl_xor_sync(0xffffffffu, most_do, s));
+        most_v = fmaxf(most_v, __shfl_xor_sync(0xffffffffu, most_v, s));
+    }
+    if (lane == 0) most[0][warp] = most_do, most[1][warp] = most_v;
+    __syncthreads();
+    if (threadIdx.x < 2) {
+        float m = 0.0f;
+        for (int w = 0; w < 8; ++w) m = fmaxf(m, most[threadIdx.x][w]);
+        p.most[2 * blockIdx.x + threadIdx.x] = m;
+    }
+}
+
+// The power of two that ds is held times, from the largest |do| and |v|; by a whole warp.
+template <int T>
+__device__ __forceinline__ int ds_exponent(const Params& p)
+{
+    if constexpr (T != GS_F16) return 0;
+    float a = 0.0f, b = 0.0f;
+    for (int i = threadIdx.x & 31; i < p.most_count; i += 32) a = fmaxf(a, p.most[2 * i]), b = fmaxf(b, p.most[2 * i + 1]);
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) {
+        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, s));
+        b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, s));
+    }
+    // finite 16-bit numbers: 2^-24 to 2^16; an infinity or zeros: any power does
+    const float bound = 2.0f * (float)p.dim * a * b;
+    if (!(bound > 0.0f && bound < 3.0e38f)) return 0;
+    return 15 - (((__float_as_int(bound) >> 23) & 255) - 126);   // bound <= 2^(exponent - 126)
+}
+__device__ __forceinline__ float power2(int e) { return __int_as_float((e + 127) << 23); }   // -126..127
+
+// Queries that see a key come from this token of the sequence on.
+__device__ __forceinline__ int first_query(const Sequence& s, int key, bool causal)
+{
+    const int t = causal ? key - (s.lk - s.lq) : 0;
+    return t < 0 ? 0 : t;
+}
+
+// ------------------------------------------------------------------ dk, dv
+// A CTA a tile of 128 keys of a key head.  TMEM lanes are keys:
+//   S = K Q^T, R = V dO^T (columns are packed query rows), dV += P dO, dK += dS Q
+// Warps 0-3 take the first 64 columns of S and R, warps 4-7 the others; P and dS take
+// the first half of their own columns' place.  The products of a tile of queries are issued as
+//   dV(i), S(i + 1), dK(i), R(i + 1)
+// so that P and dS are made while the other two run.
+template <int DP>
+struct KeyShape {
+    static constexpr int kChunks = DP / 64;
+    static constexpr uint32_t kTile = kChunks * kBox;
+    static constexpr int kStagesQ = 3, kStagesO = DP == 128 ? 2 : 3;
+    static constexpr uint32_t kAtQ = 2 * kTile, kAtO = kAtQ + kStagesQ * kTile, kAtStats = kAtO + kStagesO * kTile;
+    static constexpr uint32_t kStatBytes = kStatRows * 8;
+    static constexpr uint32_t kAtBars = kAtStats + 2 * kStatBytes;
+    static constexpr int kKV = 0, kQFull = 1, kQEmpty = kQFull + kStagesQ, kOFull = kQEmpty + kStagesQ, kOEmpty = kOFull + kStagesO,
+                         kStatFull = kOEmpty + kStagesO, kStatEmpty = kStatFull + 2, kS = kStatEmpty + 2, kR = kS + 1, kP = kR + 1,
+                         kDs = kP + 1, kDone = kDs + 1, kBars = kDone + 1;
+    static constexpr int kSmem = kAtBars + ((kBars * 8 + 15) & ~15) + 16;
+    static_assert(kSmem <= 232448 && kStatBytes % 16 == 0, "shared memory of an SM");
+};
+constexpr uint32_t kTmemR = 128, kTmemDv = 256;   // S at 0, R, dV, dK at kTmemDv + DP
+
+struct KeyWork {
+    Sequence seq;
+    uint32_t head;
+    int key0, first, n;   // first key; first token of the first tile of queries; tiles
+};
+__device__ __forceinline__ bool find_keys(const Params& p, KeyWork& w)
+{
+    uint32_t unit, units;
+    w.head = blockIdx.x % p.kv_heads;
+    if (!find_unit<true>(p.seqs, blockIdx.x / p.kv_heads, kRows, w.seq, unit, units)) return false;
+    w.key0 = (int)unit * kRows;          // the first keys are seen by the most queries
+    w.first = first_query(w.seq, w.key0, p.causal);
+    const int left = w.seq.lq - w.first;
+    w.n = left <= 0 ? 0 : (left + p.tokens - 1) / p.tokens;
+    return true;
+}
+
+template <int DP>
+__device__ __forceinline__ void load_queries(const Params& p, const KeyWork& w, uint32_t smem, uint32_t bars, volatile int* gave_up)
+{
+    using S = KeyShape<DP>;
+    mbar_expect(bars + 8 * S::kKV, 2 * S::kTile);
+    load_tile<S::kChunks>(smem, &p.k, w.head, w.seq.k0 + w.key0, bars + 8 * S::kKV);
+    load_tile<S::kChunks>(smem + S::kTile, &p.v, w.head, w.seq.k0 + w.key0, bars + 8 * S::kKV);
+    const uint32_t bytes = (uint32_t)(S::kChunks * p.tokens * p.group) * 128;
+    const float2* stats = p.stats + w.head * p.stat_pitch;
+    Ring<S::kStagesQ> rq;
+    Ring<S::kStagesO> ro;
+    Ring<2> rs;
+    uint32_t nq = 0, no = 0, ns = 0;
+    bool ok = true;
+    for (int i = 0; i < w.n; ++i) {
+        const int row = w.seq.q0 + w.first + i * p.tokens, head = w.head * p.group;
+        ok = mbar_wait(bars + 8 * (S::kQEmpty + rq.s), rq.parity ^ 1, gave_up);
+        if (!ok) break;
+        mbar_expect(bars + 8 * (S::kQFull + rq.s), bytes);
+        load_tile<S::kChunks>(smem + S::kAtQ + rq.s * S::kTile, &p.q, head, row, bars + 8 * (S::kQFull + rq.s));
+        rq.next(), ++nq;
+        ok = mbar_wait(bars + 8 * (S::kStatEmpty + rs.s), rs.parity ^ 1, gave_up);
+        if (!ok) break;
+        mbar_expect(bars + 8 * (S::kStatFull + rs.s), S::kStatBytes);
+        const int64_t at = (int64_t)row * p.group & ~1ll;   // two statistics are 16 bytes
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                         smem + S::kAtStats + rs.s * S::kStatBytes),
+                     "l"(stats + at), "r"(S::kStatBytes), "r"(bars + 8 * (S::kStatFull + rs.s))
+                     : "memory");
+        rs.next(), ++ns;
+        ok = mbar_wait(bars + 8 * (S::kOEmpty + ro.s), ro.parity ^ 1, gave_up);
+        if (!ok) break;
+        mbar_expect(bars + 8 * (S::kOFull + ro.s), bytes);
+        load_tile<S::kChunks>(smem + S::kAtO + ro.s * S::kTile, &p.d_o, head, row, bars + 8 * (S::kOFull + ro.s));
+        ro.next(), ++no;
+    }
+    // the block does not leave before its copies have landed
+    bool landed = mbar_wait_alone(bars + 8 * S::kKV, 0);
+    last_copies<S::kStagesQ>(nq, [&](uint32_t s, uint32_t parity) { landed = landed && mbar_wait_alone(bars + 8 * (S::kQFull + s), parity); });
+    last_copies<2>(ns, [&](uint32_t s, uint32_t parity) { landed = landed && mbar_wait_alone(bars + 8 * (S::kStatFull + s), parity); });
+    last_copies<S::kStagesO>(no, [&](uint32_t s, uint32_t parity) { landed = landed && mbar_wait_alone(bars + 8 * (S::kOFull + s), parity); });
+}
+
+template <int DP>
+__device__ __forceinline__ void issue_keys(const Params& p, const KeyWork& w, uint32_t smem, uint32_t bars, uint32_t tmem, int lane,
+                                           volatile int* gave_up)
+{
+    using S = KeyShape<DP>;
+    const bool one = elect_one();
+    const int steps = (p.dim + 15) / 16;
+    // rows that hold no query of the sequence: contracted over, so they have to be zero
+    const auto live = [&](int i) {
+        const int rows = (w.seq.lq - w.first - i * p.tokens) * p.group, full = p.tokens * p.group;
+        return rows < full ? rows : full;
+    };
+    const auto rows_product = [&](uint32_t d, uint32_t a, uint32_t b) {   // [keys] x [queries]
+        for (int s = 0; s < steps; ++s) {
+            const uint32_t at = (uint32_t)(s >> 2) * (kBox >> 4) + (uint32_t)(s & 3) * k_step(true);
+            mma<false, false>(d, desc_lo(a, true) + at, kDescHi, desc_lo(b, true) + at, kDescHi, p.idesc_s, s > 0);
+        }
+    };
+    const auto sum_product = [&](uint32_t d, uint32_t a, uint32_t b, bool add) {   // halves of 64 queries, 32 columns each, 64 apart
+#pragma unroll
+        for (int s = 0; s < kRows / 16; ++s)
+            mma_tmem(d, a + (s >> 2) * 64 + (s & 3) * 8, desc_rows(b) + s * k_step(false), kDescHi, p.idesc_d, add || s > 0);
+    };
+    Ring<S::kStagesQ> q, q_sum;   // tiles for S, and for dK
+    Ring<S::kStagesO> o, o_sum;   // for R, and for dV
+    bool ok = mbar_wait(bars + 8 * S::kKV, 0, gave_up);
+    const auto scores = [&](int i) {
+        ok = mbar_wait(bars + 8 * (S::kQFull + q.s), q.parity, gave_up);
+        if (!ok) return;
+        const uint32_t at = smem + S::kAtQ + q.s * S::kTile;
+        if (live(i) < kRows) zero_rows<S::kChunks>(at, live(i), lane);
+        if (one) {
+            rows_product(tmem, smem, at);
+            mma_commit<false>(bars + 8 * S::kS);
+        }
+        q.next();
+    };
+    const auto reach = [&](int i) {
+        ok = mbar_wait(bars + 8 * (S::kOFull + o.s), o.parity, gave_up);
+        if (!ok) return;
+        const uint32_t at = smem + S::kAtO + o.s * S::kTile;
+        if (live(i) < kRows) zero_rows<S::kChunks>(at, live(i), lane);
+        if (one) {
+            rows_product(tmem + kTmemR, smem + S::kTile, at);
+            mma_commit<false>(bars + 8 * S::kR);
+        }
+        o.next();
+    };
+    if (ok) scores(0);
+    if (ok) reach(0);
+    for (int i = 0; ok && i < w.n; ++i) {
+        ok = mbar_wait(bars + 8 * S::kP, i & 1, gave_up);
+        if (!ok) break;
+        tc_fence_after();
+        if (one) {
+            sum_product(tmem + kTmemDv, tmem, smem + S::kAtO + o_sum.s * S::kTile, i > 0);
+            mma_commit<false>(bars + 8 * (S::kOEmpty + o_sum.s));
+        }
+        o_sum.next();
+        if (i + 1 < w.n) scores(i + 1);
+        if (!ok) break;
+        ok = mbar_wait(bars + 8 * S::kDs, i & 1, gave_up);
+        if (!ok) break;
+        tc_fence_after();
+        if (one) {
+            sum_product(tmem + kTmemDv + DP, tmem + kTmemR, smem + S::kAtQ + q_sum.s * S::kTile, i > 0);
+            mma_commit<false>(bars + 8 * (S::kQEmpty + q_sum.s));
+        }
+        q_sum.next();
+        if (i + 1 < w.n) reach(i + 1);
+    }
+    if (one) {
+        mma_commit<false>(bars + 8 * S::kDone);
+        if (!mbar_wait_alone(bars + 8 * S::kDone, 0)) *gave_up = 1;
+    }
+    __syncwarp();
+}
+
+__device__ __forceinline__ float2 ld_shared_f2(uint32_t a)
+{
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+    return v;
+}
+
+// A key a thread (row r of the tile), 64 columns: half 0 or 1.
+template <int T, int DP>
+__device__ __forceinline__ void key_terms(const Params& p, const KeyWork& w, int half, int r, uint32_t smem, uint32_t bars, uint32_t tmem,
+                                          int exponent, volatile int* gave_up)
+{
+    using S = KeyShape<DP>;
+    constexpr float kUp = T == GS_F16 ? 12.0f : 0.0f;   // p times 2^12
+    const float by_ds = power2(exponent) * (T == GS_F16 ? 0x1p-12f : 1.0f);
+    const int key = w.key0 + r;
+    bool ok = true;
+    Ring<2> rs;
+    for (int i = 0; i < w.n; ++i, rs.next()) {
+        const int t0 = w.first + i * p.tokens;
+        // columns of this tile that count for this key: from the first query that sees it to the last of the sequence
+        const int rows = (w.seq.lq - t0) * p.group, full = p.tokens * p.group, to = (rows < full ? rows : full) - half * 64;
+        int from = (first_query(w.seq, key, p.causal) - t0) * p.group - half * 64;
+        const bool cut = to < 64 || __any_sync(0xffffffffu, from > 0);
+        const int odd = (int)(((int64_t)(w.seq.q0 + t0) * p.group) & 1);
+        const uint32_t stats = smem + S::kAtStats + rs.s * S::kStatBytes + (uint32_t)(odd + half * 64) * 8;
+        ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (S::kStatFull + rs.s), rs.parity, gave_up) &&
+                                         mbar_wait(bars + 8 * S::kS, i & 1, gave_up));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[64];
+        tmem_ld32(tmem + half * 64, s);
+        tmem_ld32(tmem + half * 64 + 32, s + 32);
+        tmem_ld32_wait(s);
+        tmem_ld32_wait(s + 32);
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+            uint32_t h[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+                const float l0 = ld_shared_f2(stats + (c + e) * 8).x, l1 = ld_shared_f2(stats + (c + e + 1) * 8).x;
+                float a = exp2_fast(__fmaf_rn(__uint_as_float(s[c + e]), p.scale2, kUp - l0));
+                float b = exp2_fast(__fmaf_rn(__uint_as_float(s[c + e + 1]), p.scale2, kUp - l1));
+                if (cut) {
+                    if (c + e < from || c + e >= to) a = 0.0f;
+                    if (c + e + 1 < from || c + e + 1 >= to) b = 0.0f;
+                }
+                s[c + e] = __float_as_uint(a), s[c + e + 1] = __float_as_uint(b);
+                h[e / 2] = pack_half2(a, b, T);
+            }
+            tmem_st16(tmem + half * 64 + c / 2, h);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(bars + 8 * S::kP);
+        ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * S::kR, i & 1, gave_up));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t h[32];
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+            uint32_t d[32];
+            tmem_ld32(tmem + kTmemR + half * 64 + c, d);
+            tmem_ld32_wait(d);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+                const float d0 = ld_shared_f2(stats + (c + e) * 8).y, d1 = ld_shared_f2(stats + (c + e + 1) * 8).y;
+                float a = __uint_as_float(s[c + e]) * ((__uint_as_float(d[e]) - d0) * by_ds);
+                float b = __uint_as_float(s[c + e + 1]) * ((__uint_as_float(d[e + 1]) - d1) * by_ds);
+                if (cut) {   // 0 times whatever the hidden rows give
+                    if (c + e < from || c + e >= to) a = 0.0f;
+                    if (c + e + 1 < from || c + e + 1 >= to) b = 0.0f;
+                }
+                h[(c + e) / 2] = pack_half2(a, b, T);
+            }
+        }
+        tmem_st32(tmem + kTmemR + half * 64, h);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) {
+            mbar_arrive(bars + 8 * S::kDs);
+            mbar_arrive(bars + 8 * (S::kStatEmpty + rs.s));
+        }
+    }
+    if (w.n > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * S::kDone, 0, gave_up));
+    if (!ok) return;
+    tc_fence_after();
+    // the first warps write dV, the others dK
+    const bool live = key < w.seq.lk;
+    const int64_t row = w.seq.k0 + key;
+    const float by = half == 0 ? (T == GS_F16 ? 0x1p-12f : 1.0f) : p.scale * power2(-exponent);
+    uint16_t* to = half == 0 ? p.dv + row * p.dv_row + w.head * p.dv_head : p.dk + row * p.dk_row + w.head * p.dk_head;
+#pragma unroll 1
+    for (int c = 0; c < DP; c += 32) {
+        float f[32];
+        uint32_t v[32];
+        if (w.n > 0) {
+            tmem_ld32(tmem + kTmemDv + half * DP + c, v);
+            tmem_ld32_wait(v);
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) f[e] = w.n > 0 ? __uint_as_float(v[e]) * by : 0.0f;
+        if (live && c < p.dim) store_row32<T>(to, c, p.dim, half == 0 ? p.dv_vec : p.dk_vec, f);
+    }
+    tc_fence_before();
+}
+
+template <int T, int DP>
+__global__ void __launch_bounds__(kThreads, 1) keys_kernel(const __grid_constant__ Params p)
+{
+    using S = KeyShape<DP>;
+    extern __shared__ __align__(1024) char smem_raw[];
+    const uint32_t smem = smem_addr(smem_raw);
+    if (smem & 1023u) {   // every thread sees the same address; there is no padding to move within
+        g_attention_bwd_wait_expired = 1;
+        return;
+    }
+    const uint32_t bars = smem + S::kAtBars;
+    char* tail = smem_raw + S::kAtBars + ((S::kBars * 8 + 15) & ~15);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail);
+    volatile int* gave_up = reinterpret_cast<volatile int*>(tail + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kBars; ++i)
+            mbar_init(bars + 8 * i, i == S::kP || i == S::kDs || (i >= S::kStatEmpty && i < S::kS) ? 8 : 1);
+        *gave_up = 0;
+        mbar_init_fence();
+    }
+    wait_for_predecessor();
+    if (p.zero) {
+        fill_rows(p.fill_dk, p.seqs.k_starts, p.seqs.count, p.seqs.k_rows);
+        fill_rows(p.fill_dv, p.seqs.k_starts, p.seqs.count, p.seqs.k_rows);
+    }
+    KeyWork w;
+    if (!find_keys(p, w)) return;   // the same for every warp
+    if (warp == 9) tmem_alloc<false>(smem_addr(tmem_slot), kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    if (warp == 8) {
+        if (w.n > 0 && elect_one()) load_queries<DP>(p, w, smem, bars, gave_up);
+        __syncwarp();
+    } else if (warp == 9) {
+        if (w.n > 0) issue_keys<DP>(p, w, smem, bars, tmem, lane, gave_up);
+    } else {
+        const int exponent = ds_exponent<T>(p);
+        key_terms<T, DP>(p, w, warp >> 2, threadIdx.x & 127, smem, bars, tmem + ((uint32_t)((warp & 3) * 32) << 16), exponent, gave_up);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && *gave_up) atomicExch(&g_attention_bwd_wait_expired, 1);
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_free<false>(tmem, kTmemCols);
+    }
+}
+
+// ------------------------------------------------------------------ dq
+// A CTA two tiles of packed query rows, which take turns as in the forward.  TMEM lanes
+// are query rows: S = Q K^T; P in registers; R = dO V^T in S's place; dS in 16 bits in
+// its place; dQ += dS K.
+template <int DP>
+struct QueryShape {
+    static constexpr int kChunks = DP / 64;
+    static constexpr uint32_t kTile = kChunks * kBox;
+    static constexpr int kStages = DP == 128 ? 3 : 6;   // keys and values in turn
+    static constexpr uint32_t kAtRing = 4 * kTile, kAtBars = kAtRing + kStages * kTile;
+    static constexpr int kQFull = 0, kFull = 2, kEmpty = kFull + kStages, kS = kEmpty + kStages, kP = kS + 2, kR = kP + 2, kDs = kR + 2,
+                         kDone = kDs + 2, kBars = kDone + 1;
+    static constexpr int kSmem = kAtBars + ((kBars * 8 + 15) & ~15) + 16;
+    static_assert(kSmem <= 232448, "shared memory of an SM");
+};
+constexpr uint32_t kTmemDq = 256;
+
+struct QueryWork {
+    Sequence seq;
+    uint32_t head;
+    int t0, n[2];
+};
+__device__ __forceinline__ bool find_queries(const Params& p, QueryWork& w)
+{
+    uint32_t unit, units;
+    w.head = blockIdx.x % p.kv_heads;
+    const int tokens = p.tokens * p.tiles;
+    if (!find_unit<false>(p.seqs, blockIdx.x / p.kv_heads, tokens, w.seq, unit, units)) return false;
+    if (p.causal) unit = units - 1 - unit;   // the longest first
+    w.t0 = (int)unit * tokens;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int t = w.t0 + i * p.tokens;
+        int last = t + p.tokens - 1;
+        last = last < w.seq.lq ? last : w.seq.lq - 1;
+        w.n[i] = i < p.tiles && t < w.seq.lq ? (keys_seen(w.seq, last, p.causal) + kRows - 1) / kRows : 0;
+    }
+    return true;
+}
+
+// The order of the ring: K(0), V(0), K(1), V(1), ...
+template <int DP>
+__device__ __forceinline__ void load_keys(const Params& p, const QueryWork& w, int n, uint32_t smem, uint32_t bars, volatile int* gave_up)
+{
+    using S = QueryShape<DP>;
+    const uint32_t bytes = (uint32_t)(S::kChunks * p.tokens * p.group) * 128;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (w.n[i] > 0) {
+            const int row = w.seq.q0 + w.t0 + i * p.tokens, head = w.head * p.group;
+            mbar_expect(bars + 8 * (S::kQFull + i), 2 * bytes);
+            load_tile<S::kChunks>(smem + 2 * i * S::kTile, &p.q, head, row, bars + 8 * (S::kQFull + i));
+            load_tile<S::kChunks>(smem + (2 * i + 1) * S::kTile, &p.d_o, head, row, bars + 8 * (S::kQFull + i));
+        }
+    Ring<S::kStages> ring;
+    uint32_t issued = 0;
+    int row = w.seq.k0;
+    for (int j = 0; j < 2 * n; ++j, ++issued, ring.next()) {
+        if (!mbar_wait(bars + 8 * (S::kEmpty + ring.s), ring.parity ^ 1, gave_up)) break;
+        mbar_expect(bars + 8 * (S::kFull + ring.s), S::kTile);
+        load_tile<S::kChunks>(smem + S::kAtRing + ring.s * S::kTile, j & 1 ? &p.v : &p.k, w.head, row, bars + 8 * (S::kFull + ring.s));
+        if (j & 1) row += kRows;
+    }
+    // the block does not leave before its copies have landed
+    bool landed = true;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) landed = landed && (w.n[i] == 0 || mbar_wait_alone(bars + 8 * (S::kQFull + i), 0));
+    last_copies<S::kStages>(issued, [&](uint32_t s, uint32_t parity) { landed = landed && mbar_wait_alone(bars + 8 * (S::kFull + s), parity); });
+}
+
+// Tile of keys j: R of both tiles of queries once their P is in registers, then dQ of each
+// once its dS is written, and right after it the next scores in dS's place.
+template <int DP>
+__device__ __forceinline__ void issue_queries(const Params& p, const QueryWork& w, int n, uint32_t smem, uint32_t bars, uint32_t tmem,
+                                              int lane, volatile int* gave_up)
+{
+    using S = QueryShape<DP>;
+    const bool one = elect_one();
+    const int steps = (p.dim + 15) / 16;
+    const auto rows_product = [&](uint32_t d, uint32_t a, uint32_t b) {
+        for (int s = 0; s < steps; ++s) {
+            const uint32_t at = (uint32_t)(s >> 2) * (kBox >> 4) + (uint32_t)(s & 3) * k_step(true);
+            mma<false, false>(d, desc_lo(a, true) + at, kDescHi, desc_lo(b, true) + at, kDescHi, p.idesc_s, s > 0);
+        }
+    };
+    Ring<S::kStages> ring;
+    bool ok = mbar_wait(bars + 8 * (S::kFull + ring.s), ring.parity, gave_up);
+    uint32_t keys = ring.s;
+    ring.next();
+    const auto clear = [&](int j) {   // keys behind the sequence are contracted over in dQ: zero
+        const int live = w.seq.lk - j * kRows;
+        if (live < kRows) zero_rows<S::kChunks>(smem + S::kAtRing + keys * S::kTile, live, lane);
+    };
+    if (ok) clear(0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (ok && w.n[i] > 0) {
+            ok = mbar_wait(bars + 8 * (S::kQFull + i), 0, gave_up);
+            if (ok && one) {
+                rows_product(tmem + i * 128, smem + 2 * i * S::kTile, smem + S::kAtRing + keys * S::kTile);
+                mma_commit<false>(bars + 8 * (S::kS + i));
+            }
+        }
+    for (int j = 0; ok && j < n; ++j) {
+        const uint32_t values = ring.s, k_at = smem + S::kAtRing + keys * S::kTile;
+        ok = mbar_wait(bars + 8 * (S::kFull + ring.s), ring.parity, gave_up);
+        ring.next();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (!ok || j >= w.n[i]) continue;
+            ok = mbar_wait(bars + 8 * (S::kP + i), j & 1, gave_up);
+            if (!ok) continue;
+            tc_fence_after();
+            if (one) {
+                rows_product(tmem + i * 128, smem + (2 * i + 1) * S::kTile, smem + S::kAtRing + values * S::kTile);
+                mma_commit<false>(bars + 8 * (S::kR + i));
+            }
+        }
+        if (!ok) break;
+        if (one) mma_commit<false>(bars + 8 * (S::kEmpty + values));
+        const uint32_t old = keys;
+        bool more = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (!ok || j >= w.n[i]) continue;
+            ok = mbar_wait(bars + 8 * (S::kDs + i), j & 1, gave_up);
+            if (!ok) continue;
+            tc_fence_after();
+            if (one)
+#pragma unroll
+                for (int s = 0; s < kRows / 16; ++s)
+                    mma_tmem(tmem + kTmemDq + i * DP, tmem + i * 128 + s * 8, desc_rows(k_at) + s * k_step(false), kDescHi, p.idesc_d,
+                             j > 0 || s > 0);
+            if (j + 1 < w.n[i]) {
+                if (!more) {
+                    more = true;
+                    keys = ring.s;
+                    ok = mbar_wait(bars + 8 * (S::kFull + ring.s), ring.parity, gave_up);
+                    ring.next();
+                    if (ok) clear(j + 1);
+                }
+                if (ok && one) {
+                    rows_product(tmem + i * 128, smem + 2 * i * S::kTile, smem + S::kAtRing + keys * S::kTile);
+                    mma_commit<false>(bars + 8 * (S::kS + i));
+                }
+            }
+        }
+        if (ok && one) mma_commit<false>(bars + 8 * (S::kEmpty + old));
+    }
+    if (one) {
+        mma_commit<false>(bars + 8 * S::kDone);
+        if (!mbar_wait_alone(bars + 8 * S::kDone, 0)) *gave_up = 1;
+    }
+    __syncwarp();
+}
+
+// A row a thread: i the tile, r the row.
+template <int T, int DP>
+__device__ __forceinline__ void query_terms(const Params& p, const QueryWork& w, int i, int r, uint32_t bars, uint32_t tmem, int exponent,
+                                            volatile int* gave_up)
+{
+    using S = QueryShape<DP>;
+    const int n = w.n[i], t0 = w.t0 + i * p.tokens;
+    const int token = t0 + r / p.group;
+    const bool live = r < p.tokens * p.group && token < w.seq.lq;
+    const int64_t row = w.seq.q0 + token;
+    const float2 st = live ? p.stats[w.head * p.stat_pitch + row * p.group + r % p.group] : make_float2(INFINITY, 0.0f);
+    const int seen = live ? keys_seen(w.seq, token, p.causal) : 0;
+    const int all = keys_seen(w.seq, t0, p.causal);
+    const float by_ds = power2(exponent);
+    const uint32_t here = tmem + i * 128;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (S::kS + i), j & 1, gave_up));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[128];
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) tmem_ld32(here + c, s + c);
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) tmem_ld32_wait(s + c);
+        tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(bars + 8 * (S::kP + i));   // read: R takes its place
+#pragma unroll
+        for (int c = 0; c < 128; ++c) s[c] = __float_as_uint(exp2_fast(__fmaf_rn(__uint_as_float(s[c]), p.scale2, -st.x)));
+        const int left = seen - j * kRows;
+        const bool cut = (j + 1) * kRows > all;
+        ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (S::kR + i), j & 1, gave_up));
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+            uint32_t d[32], h[16];
+            tmem_ld32(here + c, d);
+            tmem_ld32_wait(d);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+                float a = __uint_as_float(s[c + e]) * ((__uint_as_float(d[e]) - st.y) * by_ds);
+                float b = __uint_as_float(s[c + e + 1]) * ((__uint_as_float(d[e + 1]) - st.y) * by_ds);
+                if (cut) {   // 0 whatever the hidden keys give
+                    if (c + e >= left) a = 0.0f;
+                    if (c + e + 1 >= left) b = 0.0f;
+                }
+                h[e / 2] = pack_half2(a, b, T);
+            }
+            tmem_st16(here + c / 2, h);   // behind what has been read
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(bars + 8 * (S::kDs + i));
+    }
+    if (n > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * S::kDone, 0, gave_up));
+    if (!ok) return;
+    tc_fence_after();
+    const float by = p.scale * power2(-exponent);
+    uint16_t* to = p.dq + row * p.dq_row + ((int)w.head * p.group + r % p.group) * p.dq_head;
+#pragma unroll 1
+    for (int c = 0; c < DP; c += 32) {
+        float f[32];
+        uint32_t v[32];
+        if (n > 0) {
+            tmem_ld32(tmem + kTmemDq + i * DP + c, v);
+            tmem_ld32_wait(v);
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) f[e] = n > 0 ? __uint_as_float(v[e]) * by : 0.0f;
+        if (live && c < p.dim) store_row32<T>(to, c, p.dim, p.dq_vec, f);
+    }
+    tc_fence_before();
+}
+
+template <int T, int DP>
+__global__ void __launch_bounds__(kThreads, 1) queries_kernel(const __grid_constant__ Params p)
+{
+    using S = QueryShape<DP>;
+    extern __shared__ __align__(1024) char smem_raw[];
+    const uint32_t smem = smem_addr(smem_raw);
+    if (smem & 1023u) {
+        g_attention_bwd_wait_expired = 1;
+        return;
+    }
+    const uint32_t bars = smem + S::kAtBars;
+    char* tail = smem_raw + S::kAtBars + ((S::kBars * 8 + 15) & ~15);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail);
+    volatile int* gave_up = reinterpret_cast<volatile int*>(tail + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kBars; ++i) {
+            const bool warps = (i >= S::kP && i < S::kR) || (i >= S::kDs && i < S::kDone);
+            mbar_init(bars + 8 * i, warps ? 4 : 1);
+        }
+        *gave_up = 0;
+        mbar_init_fence();
+    }
+    wait_for_predecessor();
+    if (p.zero) fill_rows(p.fill_dq, p.seqs.q_starts, p.seqs.count, p.seqs.q_rows);
+    QueryWork w;
+    if (!find_queries(p, w)) return;   // the same for every warp
+    if (warp == 9) tmem_alloc<false>(smem_addr(tmem_slot), kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int n = w.n[0] > w.n[1] ? w.n[0] : w.n[1];
+    if (warp == 8) {
+        if (n > 0 && elect_one()) load_keys<DP>(p, w, n, smem, bars, gave_up);
+        __syncwarp();
+    } else if (warp == 9) {
+        if (n > 0) issue_queries<DP>(p, w, n, smem, bars, tmem, lane, gave_up);
+    } else {
+        const int i = warp >> 2, exponent = ds_exponent<T>(p);
+        if (i < p.tiles && w.t0 + i * p.tokens < w.seq.lq)
+            query_terms<T, DP>(p, w, i, threadIdx.x & 127, bars, tmem + ((uint32_t)((warp & 3) * 32) << 16), exponent, gave_up);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && *gave_up) atomicExch(&g_attention_bwd_wait_expired, 1);
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_free<false>(tmem, kTmemCols);
+    }
+}
+
+struct Plan {
+    int group, tokens, tiles, dp, blocks;
+    int64_t query_items, key_items, stat_pitch;
+    size_t stats, most, packs, bytes;
+};
+Plan plan_for(const gs_attention_bwd_args& a)
+{
+    Plan r = {};
+    r.group = a.heads / a.kv_heads;
+    r.tokens = kRows / r.group;
+    r.dp = a.dim <= 64 ? 64 : 128;
+    const int known = device_sms();
+    const int64_t sms = known > 0 ? known : 152;
+    const bool starts = a.q_starts != nullptr;
+    const int64_t two = units_at_most(a.q_rows, a.sequences, starts, 2 * (int64_t)r.tokens);
+    r.tiles = two * a.kv_heads >= sms && a.q_rows > a.sequences * r.tokens ? 2 : 1;
+    r.query_items = (r.tiles == 2 ? two : units_at_most(a.q_rows, a.sequences, starts, r.tokens)) * a.kv_heads;
+    r.key_items = units_at_most(a.k_rows, a.sequences, starts, kRows) * a.kv_heads;
+    r.stat_pitch = round_up(a.q_rows * r.group, 2);
+    // the last copy of statistics reads up to a tile past the last row
+    r.stats = (size_t)round_up((a.kv_heads * r.stat_pitch + kStatRows) * 8, 256);
+    const int64_t want = (a.q_rows * a.heads + 7) / 8, most = sms * (a.type == GS_F16 ? 2 : 8);
+    r.blocks = (int)(want < 1 ? 1 : (want < most ? want : most));
+    r.most = a.type == GS_F16 ? (size_t)round_up(r.blocks * 8, 256) : 0;
+    if (!tensor_tma(a.q, a.q_row, a.q_head, a.q_rows, a.heads)) r.packs += packed_bytes(a.q_rows, a.heads, a.dim);
+    if (!tensor_tma(a.d_o, a.do_row, a.do_head, a.q_rows, a.heads)) r.packs += packed_bytes(a.q_rows, a.heads, a.dim);
+    if (!tensor_tma(a.k, a.k_row, a.k_head, a.k_rows, a.kv_heads)) r.packs += packed_bytes(a.k_rows, a.kv_heads, a.dim);
+    if (!tensor_tma(a.v, a.v_row, a.v_head, a.k_rows, a.kv_heads)) r.packs += packed_bytes(a.k_rows, a.kv_heads, a.dim);
+    r.bytes = r.stats + r.most + r.packs;
+    return r;
+}
+
+template <class K>
+gs_status launch_one(K* kernel, int smem, std::atomic<uint64_t>& done, int64_t items, const Params& p, cudaStream_t st)
+{
+    const gs_status s = allow_smem(kernel, smem, done);
+    return s != GS_OK ? s : launch_after(kernel, dim3((unsigned)items), kThreads, (size_t)smem, 1, st, p);
+}
+template <int T, int DP>
+gs_status launch(const Params& p, const Plan& plan, cudaStream_t st)
+{
+    static std::atomic<uint64_t> keys_done{0}, queries_done{0};
+    gs_status s = GS_OK;
+    if (p.dk) s = launch_one(keys_kernel<T, DP>, KeyShape<DP>::kSmem, keys_done, plan.key_items, p, st);
+    if (s == GS_OK && p.dq) s = launch_one(queries_kernel<T, DP>, QueryShape<DP>::kSmem, queries_done, plan.query_items, p, st);
+    return s;
+}
+
+}  // namespace
+
+gs_status backward_wait_report(int* expired)
+{
+    const int zero = 0;
+    GS_CUDA_TRY(cudaMemcpyFromSymbol(expired, g_attention_bwd_wait_expired, sizeof *expired));
+    if (*expired) GS_CUDA_TRY(cudaMemcpyToSymbol(g_attention_bwd_wait_expired, &zero, sizeof zero));
+    return GS_OK;
+}
+
+}  // namespace attn
+}  // namespace gs
+
+using namespace gs;
+using namespace gs::attn;
+
+extern "C" gs_status gs_attention_bwd(const gs_attention_bwd_args* args, void* ws, size_t* ws_bytes, void* stream)
+{
+    GS_NVTX_RANGE("gs_attention_bwd");
+    if (!args) return GS_ERR_INVALID_ARG;
+    const gs_attention_bwd_args& a = *args;
+    if (!sizes_ok(a.q_rows, a.k_rows, a.sequences, a.heads, a.kv_heads, a.dim, a.type, a.scale, a.q_starts, a.k_starts))
+        return GS_ERR_INVALID_ARG;
+    if (!a.dk != !a.dv && a.k_rows > 0) return GS_ERR_INVALID_ARG;
+    if (a.q_rows > 0) {
+        if (!tensor_ok(a.q, a.q_row, a.q_head, a.q_rows, a.heads, a.dim, false) ||
+            !tensor_ok(a.o, a.o_row, a.o_head, a.q_rows, a.heads, a.dim, false) ||
+            !tensor_ok(a.d_o, a.do_row, a.do_head, a.q_rows, a.heads, a.dim, false) || !a.lse || ((uintptr_t)a.lse & 3u))
+            return GS_ERR_INVALID_ARG;
+        if (a.dq && !tensor_ok(a.dq, a.dq_row, a.dq_head, a.q_rows, a.heads, a.dim, true)) return GS_ERR_INVALID_ARG;
+    }
+    if (a.k_rows > 0) {
+        if (!tensor_ok(a.k, a.k_row, a.k_head, a.k_rows, a.kv_heads, a.dim, false) ||
+            !tensor_ok(a.v, a.v_row, a.v_head, a.k_rows, a.kv_heads, a.dim, false))
+            return GS_ERR_INVALID_ARG;
+        if (a.dk && (!tensor_ok(a.dk, a.dk_row, a.dk_head, a.k_rows, a.kv_heads, a.dim, true) ||
+                     !tensor_ok(a.dv, a.dv_row, a.dv_head, a.k_rows, a.kv_heads, a.dim, true)))
+            return GS_ERR_INVALID_ARG;
+    }
+    const Plan plan = plan_for(a);
+    if (plan.query_items > 0x7fffffffll || plan.key_items > 0x7fffffffll) return GS_ERR_INVALID_ARG;
+    const WsCheck wc = ws_check(ws, ws_bytes, plan.bytes);
+    if (wc == WsCheck::kBad) return GS_ERR_INVALID_ARG;
+    if (wc == WsCheck::kQuery) return GS_OK;
+    cudaStream_t st = (cudaStream_t)stream;
+    const bool dq = a.dq && a.q_rows > 0, dk = a.dk && a.k_rows > 0;
+    if (!dq && !dk) return GS_OK;
+    float2* stats = (float2*)ws;
+    float* most = plan.most ? (float*)((char*)ws + plan.stats) : nullptr;
+    char* to = (char*)ws + plan.stats + plan.most;
+    PackList packs;
+    Params p = {};
+    gs_status s = GS_OK;
+    if (a.q_rows > 0 && a.k_rows > 0) {   // without a pair of query and key the kernels read nothing and write zeros
+        const Tensor3 q = packs.add({a.q, a.q_row, a.q_head}, a.q_rows, a.heads, a.dim, to);
+        const Tensor3 d = packs.add({a.d_o, a.do_row, a.do_head}, a.q_rows, a.heads, a.dim, to);
+        const Tensor3 k = packs.add({a.k, a.k_row, a.k_head}, a.k_rows, a.kv_heads, a.dim, to);
+        const Tensor3 v = packs.add({a.v, a.v_row, a.v_head}, a.k_rows, a.kv_heads, a.dim, to);
+        s = tile_map(&p.q, q, a.type, a.q_rows, a.heads, a.dim, plan.group, plan.tokens);
+        if (s == GS_OK) s = tile_map(&p.d_o, d, a.type, a.q_rows, a.heads, a.dim, plan.group, plan.tokens);
+        if (s == GS_OK) s = tile_map(&p.k, k, a.type, a.k_rows, a.kv_heads, a.dim, 1, kRows);
+        if (s == GS_OK) s = tile_map(&p.v, v, a.type, a.k_rows, a.kv_heads, a.dim, 1, kRows);
+        if (s == GS_OK) s = packs.run(st);
+        if (s != GS_OK) return s;
+        StatParams t = {};
+        t.o = (const uint16_t*)a.o, t.o_row = a.o_row, t.o_head = a.o_head;
+        t.d_o = (const uint16_t*)a.d_o, t.do_row = a.do_row, t.do_head = a.do_head;
+        t.v = (const uint16_t*)a.v, t.v_row = a.v_row, t.v_head = a.v_head;
+        t.lse = a.lse, t.stats = stats, t.most = most, t.q_rows = a.q_rows, t.k_rows = a.k_rows, t.stat_pitch = plan.stat_pitch;
+        t.heads = a.heads, t.kv_heads = a.kv_heads, t.group = plan.group, t.dim = a.dim;
+        t.vec = a.dim % 8 == 0 && tensor_tma(a.o, a.o_row, a.o_head, a.q_rows, a.heads) &&
+                tensor_tma(a.d_o, a.do_row, a.do_head, a.q_rows, a.heads);
+        s = a.type == GS_BF16 ? launch_after(stats_kernel<GS_BF16>, dim3((unsigned)plan.blocks), 256, 0, 1, st, t)
+                              : launch_after(stats_kernel<GS_F16>, dim3((unsigned)plan.blocks), 256, 0, 1, st, t);
+        if (s != GS_OK) return s;
+    }
+    p.seqs = {a.q_starts, a.k_starts, nullptr, a.q_rows, a.k_rows, (uint32_t)a.sequences};
+    p.zero = a.fill && a.q_starts;
+    p.fill_dq = {(uint16_t*)a.dq, a.dq_row, a.dq_head, nullptr, a.heads, a.dim};
+    p.fill_dk = {(uint16_t*)a.dk, a.dk_row, a.dk_head, nullptr, a.kv_heads, a.dim};
+    p.fill_dv = {(uint16_t*)a.dv, a.dv_row, a.dv_head, nullptr, a.kv_heads, a.dim};
+    p.stats = stats, p.most = most, p.most_count = plan.blocks, p.stat_pitch = plan.stat_pitch;
+    p.dq = dq ? (uint16_t*)a.dq : nullptr, p.dq_row = a.dq_row, p.dq_head = a.dq_head;
+    p.dk = dk ? (uint16_t*)a.dk : nullptr, p.dk_row = a.dk_row, p.dk_head = a.dk_head;
+    p.dv = (uint16_t*)a.dv, p.dv_row = a.dv_row, p.dv_head = a.dv_head;
+    p.scale = a.scale, p.scale2 = a.scale * kLog2e;
+    p.kv_heads = (uint32_t)a.kv_heads, p.tiles = plan.tiles, p.group = plan.group, p.tokens = plan.tokens, p.dim = a.dim;
+    p.causal = a.causal != 0;
+    p.dq_vec = tensor_vec(a.dq, a.dq_row, a.dq_head, a.q_rows, a.heads);
+    p.dk_vec = tensor_vec(a.dk, a.dk_row, a.dk_head, a.k_rows, a.kv_heads);
+    p.dv_vec = tensor_vec(a.dv, a.dv_row, a.dv_head, a.k_rows, a.kv_heads);
+    p.idesc_s = instr_desc(a.type, true, true, kRows, kRows);
+    p.idesc_d = instr_desc(a.type, true, false, (int)round_up(a.dim, 16), kRows);
+    if (a.type == GS_BF16) return plan.dp == 64 ? launch<GS_BF16, 64>(p, plan, st) : launch<GS_BF16, 128>(p, plan, st);
+    return plan.dp == 64 ? launch<GS_F16, 64>(p, plan, st) : launch<GS_F16, 128>(p, plan, st);
+}

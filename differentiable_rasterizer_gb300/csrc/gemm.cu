@@ -1342,7 +1342,7 @@ extern "C" gs_status gs_wait_report(int32_t* expired)
     GS_CUDA_TRY(cudaDeviceSynchronize());
     GS_CUDA_TRY(cudaMemcpyFromSymbol(&v, g_wait_expired, sizeof v));
     if (v) GS_CUDA_TRY(cudaMemcpyToSymbol(g_wait_expired, &zero, sizeof zero));
-    for (gs_status (*report)(int*) : {glu_narrow_wait_report, attn::forward_wait_report}) {
+    for (gs_status (*report)(int*) : {glu_narrow_wait_report, attn::forward_wait_report, attn::backward_wait_report}) {
         int other = 0;
         const gs_status s = report(&other);
         if (s != GS_OK) return s;

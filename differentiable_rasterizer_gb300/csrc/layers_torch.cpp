@@ -38,6 +38,7 @@ struct Library {
     decltype(&gs_glu) glu;
     decltype(&gs_glu_bwd) glu_bwd;
     decltype(&gs_attention) attention;
+    decltype(&gs_attention_bwd) attention_bwd;
 };
 Library lib = {};
 PyObject* gs_error = nullptr;   // abi.GsError
@@ -555,6 +556,12 @@ Heads heads_of(const Tensor& t, const char* name, unsigned types, int dev, int64
     h.p = t.data_ptr();
     return h;
 }
+void groups(const Heads& q, const Heads& k)
+{
+    if (q.heads % k.heads || q.heads / k.heads > GS_ATTENTION_MAX_GROUP)
+        refuse("k: " + std::to_string(k.heads) + " heads do not divide q's " + std::to_string(q.heads) + " into groups of at most " +
+               std::to_string(GS_ATTENTION_MAX_GROUP));
+}
 const int32_t* indices(PyObject* o, const char* name, int dev, int64_t size)   // None: NULL
 {
     if (o == Py_None) return nullptr;
@@ -596,9 +603,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n)
         const Heads hq = heads_of(q, "q", kHalf, dev);
         const Heads hk = heads_of(tensor(a[1], "k"), "k", 1u << hq.type, dev, -1, -1, hq.dim);
         const Heads hv = heads_of(tensor(a[2], "v"), "v", 1u << hq.type, dev, hk.rows, hk.heads, hq.dim);
-        if (hq.heads % hk.heads || hq.heads / hk.heads > GS_ATTENTION_MAX_GROUP)
-            refuse("k: " + std::to_string(hk.heads) + " heads do not divide q's " + std::to_string(hq.heads) + " into groups of at most " +
-                   std::to_string(GS_ATTENTION_MAX_GROUP));
+        groups(hq, hk);
         gs_attention_args g = {};
         g.q_rows = hq.rows, g.k_rows = hk.rows;
         g.q = hq.p, g.q_row = hq.row, g.q_head = hq.head, g.k = hk.p, g.k_row = hk.row, g.k_head = hk.head;
@@ -630,6 +635,55 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
+// (do, q, k, v, o, lse, q_starts, k_starts, causal, scale, dq, dk, dv) -> (dq, dk, dv); the
+// last three: where to, or None
+PyObject* attention_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded(n, 13, [&] {
+        const Tensor& q = tensor(a[1], "q");
+        const int dev = cuda_device(q, "q");
+        const c10::cuda::OptionalCUDAGuard guard(q.device());
+        const Heads hq = heads_of(q, "q", kHalf, dev);
+        const unsigned type = 1u << hq.type;
+        const Tensor &k = tensor(a[2], "k"), &v = tensor(a[3], "v");
+        const Heads hk = heads_of(k, "k", type, dev, -1, -1, hq.dim);
+        const Heads hv = heads_of(v, "v", type, dev, hk.rows, hk.heads, hq.dim);
+        const Heads hd = heads_of(tensor(a[0], "do"), "do", type, dev, hq.rows, hq.heads, hq.dim);
+        const Heads ho = heads_of(tensor(a[4], "o"), "o", type, dev, hq.rows, hq.heads, hq.dim);
+        groups(hq, hk);
+        gs_attention_bwd_args g = {};
+        g.q_rows = hq.rows, g.k_rows = hk.rows;
+        g.q = hq.p, g.q_row = hq.row, g.q_head = hq.head, g.k = hk.p, g.k_row = hk.row, g.k_head = hk.head;
+        g.v = hv.p, g.v_row = hv.row, g.v_head = hv.head, g.o = ho.p, g.o_row = ho.row, g.o_head = ho.head;
+        g.d_o = hd.p, g.do_row = hd.row, g.do_head = hd.head;
+        g.lse = (const float*)required(vector_of(a[5], "lse", kF32, dev, hq.rows * hq.heads), "lse (attention's with need_backward)",
+                                       hq.rows * hq.heads);
+        g.heads = hq.heads, g.kv_heads = hk.heads, g.dim = hq.dim, g.type = hq.type;
+        sequences_of(g, a[6], a[7], dev);
+        g.causal = flag(a[8], "causal");
+        g.scale = scale_of(a[9], hq.dim);
+        const bool given = a[10] != Py_None;
+        Tensor t[3];
+        Heads h[3];
+        for (int i = 0; i < 3; ++i) {
+            static const char* const names[3] = {"dq", "dk", "dv"};
+            const Heads& like = i == 0 ? hq : hk;
+            if (given != (a[10 + i] != Py_None)) refuse("out: expected dq, dk and dv");
+            t[i] = given ? tensor(a[10 + i], names[i]) : at::empty({like.rows, like.heads, like.dim}, q.options());
+            h[i] = heads_of(t[i], names[i], type, dev, like.rows, like.heads, like.dim);
+        }
+        g.fill = !given;
+        g.dq = h[0].p, g.dq_row = h[0].row, g.dq_head = h[0].head;
+        g.dk = h[1].p, g.dk_row = h[1].row, g.dk_head = h[1].head;
+        g.dv = h[2].p, g.dv_row = h[2].row, g.dv_head = h[2].head;
+        with_scratch("gs_attention_bwd", lib.attention_bwd, g, q, dev, false);
+        if (given)
+            for (const Tensor& x : t)
+                if (!x.is_inference()) x.unsafeGetTensorImpl()->bump_version();
+        return result(t[0], t[1], t[2]);
+    });
+}
+
 // bind(GsError, addresses of the library's functions in the order of Library)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
@@ -654,6 +708,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
     lib.glu = reinterpret_cast<decltype(lib.glu)>(f[5]);
     lib.glu_bwd = reinterpret_cast<decltype(lib.glu_bwd)>(f[6]);
     lib.attention = reinterpret_cast<decltype(lib.attention)>(f[7]);
+    lib.attention_bwd = reinterpret_cast<decltype(lib.attention_bwd)>(f[8]);
     Py_INCREF(a[0]);
     Py_XDECREF(gs_error);
     gs_error = a[0];
@@ -663,7 +718,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 #define GS_FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {GS_FAST(bind),          GS_FAST(rms_norm), GS_FAST(rms_norm_backward), GS_FAST(quantize_rows),
                          GS_FAST(linear),        GS_FAST(linear_backward), GS_FAST(glu),       GS_FAST(glu_backward),
-                         GS_FAST(attention),     {nullptr, nullptr, 0, nullptr}};
+                         GS_FAST(attention),     GS_FAST(attention_backward), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layers_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -67,6 +67,12 @@ class AttentionOut(NamedTuple):
     lse: Optional[torch.Tensor]     # [rows, heads], for the gradients
 
 
+class AttentionGrads(NamedTuple):
+    dq: torch.Tensor
+    dk: torch.Tensor
+    dv: torch.Tensor
+
+
 class LinearGrads(NamedTuple):
     dx: Optional[torch.Tensor]
     dw: Optional[torch.Tensor]
@@ -93,9 +99,9 @@ class _Native:
         L = abi.lib()
         module.bind(abi.GsError, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
             "gs_rms_norm", "gs_rms_norm_bwd", "gs_quantize_rows", "gs_linear", "gs_linear_bwd", "gs_glu", "gs_glu_bwd",
-            "gs_attention")))
+            "gs_attention", "gs_attention_bwd")))
         for f in ("rms_norm", "rms_norm_backward", "quantize_rows", "linear", "linear_backward", "glu", "glu_backward",
-                  "attention"):
+                  "attention", "attention_backward"):
             setattr(self, f, getattr(module, f))
         return self.__dict__[name]
 
@@ -201,3 +207,12 @@ def attention(q, k, v, *, q_starts=None, k_starts=None, k_lengths=None, causal=F
     query sees every key, the one before all but one, ...  A query that sees none gives 0.
     out: like q, rows of no sequence are left as they are; else o is allocated, those rows 0."""
     return AttentionOut(*_native.attention(q, k, v, q_starts, k_starts, k_lengths, causal, scale, out, need_backward))
+
+
+def attention_backward(do, q, k, v, o, lse, *, q_starts=None, k_starts=None, causal=False, scale=None,
+                       out=None) -> AttentionGrads:
+    """Gradients of attention from do, in q's type; o, lse: attention's with need_backward, the
+    other arguments as they were given to it.  out: (dq, dk, dv) to write to (column ranges of
+    the projection's gradient, say), rows of no sequence are left as they are; else 0."""
+    dq, dk, dv = (None, None, None) if out is None else out
+    return AttentionGrads(*_native.attention_backward(do, q, k, v, o, lse, q_starts, k_starts, causal, scale, dq, dk, dv))
