@@ -32,7 +32,8 @@ EXPORTS = ("gs_project", "gs_bin_sort", "gs_raster_fused_fwd_bwd", "gs_grad_comp
            "gs_raster_forward_state", "gs_dssim_loss_grad", "gs_raster_backward_state", "gs_grad_compact_static",
            "gs_prune_tiles", "gs_split_ranges", "gs_compose", "gs_raster_work_counts", "gs_check_report",
            "gs_rms_norm", "gs_rms_norm_bwd", "gs_quantize_rows", "gs_linear", "gs_linear_bwd", "gs_glu", "gs_glu_bwd",
-           "gs_attention", "gs_attention_bwd", "gs_wait_report", "gs_layer_tile",
+           "gs_attention", "gs_attention_bwd", "gs_block_norm", "gs_block_norm_bwd", "gs_clip_norm",
+           "gs_wait_report", "gs_layer_tile",
            "gs_error_string", "gs_param_rows", "gs_param_stride", "gs_num_tiles", "gs_version")
 
 
@@ -104,11 +105,11 @@ def lib():
                      "gs_raster_forward_state", "gs_dssim_loss_grad", "gs_raster_backward_state", "gs_prune_tiles",
                      "gs_split_ranges", "gs_compose", "gs_raster_work_counts"):
             getattr(L, name).restype = ctypes.c_int
-        for name in ("gs_rms_norm", "gs_quantize_rows"):
+        for name in ("gs_rms_norm", "gs_quantize_rows", "gs_block_norm"):
             getattr(L, name).argtypes = [ctypes.c_char_p, _P]
             getattr(L, name).restype = ctypes.c_int
         for name in ("gs_rms_norm_bwd", "gs_linear", "gs_linear_bwd", "gs_glu", "gs_glu_bwd", "gs_attention",
-                     "gs_attention_bwd"):
+                     "gs_attention_bwd", "gs_block_norm_bwd", "gs_clip_norm"):
             getattr(L, name).argtypes = [ctypes.c_char_p, _P, ctypes.POINTER(ctypes.c_size_t), _P]
             getattr(L, name).restype = ctypes.c_int
         L.gs_wait_report.argtypes = [ctypes.POINTER(ctypes.c_int32)]
@@ -333,6 +334,10 @@ _LINEAR_BWD = struct.Struct("=qqq Qq Qq Qq Qq Qq Qq Q iiii ii")
 _GLU = struct.Struct("=qqq Qq Qq Qq QQQ Qq Qq Qq iiii")
 _ATTENTION = struct.Struct("=qqq Qqq Qqq Qqq QQQ Qqq Q f iiiiiii")
 _ATTENTION_BWD = struct.Struct("=qqq Qqq Qqq Qqq Qqq Qqq Q QQ Qqq Qqq Qqq f iiiiiii")
+_BLOCK_NORM = struct.Struct("=qq Qq Qq Q Qq Q Qq Qq QQQ ff iiiiii")
+_BLOCK_NORM_BWD = struct.Struct("=qq Qq Qq Qq Qq Q Qq Q QQ Qq Qq Qq QQ f iiiiiii")
+_CLIP_TENSOR = struct.Struct("=QQq ii")
+_CLIP_NORM = struct.Struct("=Qq Q f i")
 _GLU_BWD = struct.Struct("=qqq Qq Qq Qq Qq Qq Qq Qq Qq Qq iiii")
 
 
@@ -410,6 +415,28 @@ def attention_bwd_args(q_rows, k_rows, sequences, q, q_row, q_head, k, k_row, k_
                                dk_head, dv, dv_row, dv_head, scale, heads, kv_heads, dim, type_, causal, fill, 0)
 
 
+def gs_block_norm(rows, cols, h, ldh, x, ldx, post_weight, gate, ldg, weight, s, lds, y, ldy, y_scale, rstd_post, rstd,
+                  scale, eps, type_, post_type, gate_type, gate_rows, weight_type, y_type, stream):
+    _check("gs_block_norm", lib().gs_block_norm(
+        _BLOCK_NORM.pack(rows, cols, h, ldh, x, ldx, post_weight, gate, ldg, weight, s, lds, y, ldy, y_scale, rstd_post,
+                         rstd, scale, eps, type_, post_type, gate_type, gate_rows, weight_type, y_type), stream))
+
+
+def block_norm_bwd_args(rows, cols, dy, lddy, ds, ldds, h, ldh, s, lds, post_weight, gate, ldg, weight, rstd_post, rstd,
+                        dh, lddh, dx, lddx, dgate, lddg, dweight, dpost, scale, type_, dy_type, post_type, gate_type,
+                        gate_rows, weight_type) -> bytes:
+    return _BLOCK_NORM_BWD.pack(rows, cols, dy, lddy, ds, ldds, h, ldh, s, lds, post_weight, gate, ldg, weight, rstd_post,
+                                rstd, dh, lddh, dx, lddx, dgate, lddg, dweight, dpost, scale, type_, dy_type, post_type,
+                                gate_type, gate_rows, weight_type, 0)
+
+
+def clip_norm_args(tensors, norm, max_norm):
+    """tensors: (p, out, size, type, out_type) each.  Returns the packed arguments and the table that they
+    point to, which has to outlive the call."""
+    table = ctypes.create_string_buffer(b"".join(_CLIP_TENSOR.pack(*t) for t in tensors), len(tensors) * _CLIP_TENSOR.size or 1)
+    return _CLIP_NORM.pack(ctypes.addressof(table) if tensors else 0, len(tensors), norm, max_norm, 0), table
+
+
 def gs_rms_norm_bwd(args: bytes, ws, ws_bytes, stream):
     """args: rms_norm_bwd_args(...); ws: device pointer of ws_bytes, or None and None where none is needed."""
     layer_run("gs_rms_norm_bwd", args, ws, ws_bytes, stream)
@@ -437,6 +464,14 @@ def gs_attention(args: bytes, ws, ws_bytes, stream):
 
 def gs_attention_bwd(args: bytes, ws, ws_bytes, stream):
     layer_run("gs_attention_bwd", args, ws, ws_bytes, stream)
+
+
+def gs_block_norm_bwd(args: bytes, ws, ws_bytes, stream):
+    layer_run("gs_block_norm_bwd", args, ws, ws_bytes, stream)
+
+
+def gs_clip_norm(args: bytes, ws, ws_bytes, stream):
+    layer_run("gs_clip_norm", args, ws, ws_bytes, stream)
 
 
 def layer_ws_bytes(name: str, args: bytes) -> int:

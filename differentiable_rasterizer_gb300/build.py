@@ -30,8 +30,8 @@ CHECKED_LIB = os.path.join(OUT_DIR, "libgs_gb300_checked.so")
 VARIANTS = ((LIB, OUT_DIR, []), (CHECKED_LIB, os.path.join(OUT_DIR, "checked"), ["-DGS_CHECKED"]))
 SOURCES = ["abi.cu", "project.cu", "binsort.cu", "prune.cu", "raster.cu", "dssim.cu", "compose.cu", "compact.cu", "adam.cu",
            "norm.cu", "linear.cu", "gemm.cu", "glu_narrow.cu", "attention.cu",
-           "attention_bwd.cu"]
-HEADERS = ["gs_common.cuh", "project_math.cuh", "scan.cuh", "layers_common.cuh", "gemm.cuh", "tc_common.cuh", "attention.cuh"]
+           "attention_bwd.cu", "block_norm.cu", "clip.cu"]
+HEADERS = ["gs_common.cuh", "project_math.cuh", "scan.cuh", "layers_common.cuh", "gemm.cuh", "tc_common.cuh", "attention.cuh", "rows.cuh"]
 
 # The layers on torch tensors: a Python extension module against the installed torch's headers.
 TORCH_SRC = os.path.join(CSRC, "layers_torch.cpp")

@@ -11,7 +11,9 @@
 #include <Python.h>
 
 #include <cmath>
+#include <cstring>
 #include <string>
+#include <vector>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/core/grad_mode.h>
@@ -39,6 +41,9 @@ struct Library {
     decltype(&gs_glu_bwd) glu_bwd;
     decltype(&gs_attention) attention;
     decltype(&gs_attention_bwd) attention_bwd;
+    decltype(&gs_block_norm) block_norm;
+    decltype(&gs_block_norm_bwd) block_norm_bwd;
+    decltype(&gs_clip_norm) clip_norm;
 };
 Library lib = {};
 PyObject* gs_error = nullptr;   // abi.GsError
@@ -122,6 +127,7 @@ struct Rows {
     void* p = nullptr;
     int64_t ld = 0, rows = 0, cols = 0;
     int type = 0;
+    bool one_dim = false;   // a single row without a dimension of rows
 };
 
 Rows rows_of(const Tensor& t, const char* name, unsigned types, int dev, int64_t cols = -1, int64_t rows = -1)
@@ -133,6 +139,7 @@ Rows rows_of(const Tensor& t, const char* name, unsigned types, int dev, int64_t
     r.type = type_code(t.scalar_type());
     r.cols = t.size(d - 1);
     r.rows = 1;
+    r.one_dim = d == 1;
     for (int64_t i = 0; i + 1 < d; ++i) r.rows *= t.size(i);
     if (cols >= 0 && r.cols != cols)
         refuse(std::string(name) + ": " + std::to_string(r.cols) + " columns, expected " + std::to_string(cols));
@@ -684,6 +691,148 @@ PyObject* attention_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
+// ------------------------------------------------------------------ block norm
+// A gate: [cols], or rows of the rest's type.
+template <class Args>
+Tensor gate_of(Args& g, PyObject* o, int dev, const Rows& r)
+{
+    if (o == Py_None) return {};
+    const Tensor& t = tensor(o, "gate");
+    if (t.dim() == 1 && !(r.rows == 1 && r.one_dim)) {
+        g.gate = vector_of(o, "gate", kFloat, dev, r.cols, &g.gate_type);
+    } else {
+        const Rows rg = rows_of(t, "gate", 1u << r.type, dev, r.cols, r.rows);
+        g.gate = rg.p, g.ldg = rg.ld, g.gate_type = r.type, g.gate_rows = 1;
+    }
+    return t;
+}
+
+// (h, x, weight, post_weight, gate, scale, eps, out_dtype, need_backward) -> (y, y_scale, s, rstd_post, rstd)
+PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded(n, 9, [&] {
+        const Tensor& h = tensor(a[0], "h");
+        const int dev = cuda_device(h, "h");
+        const c10::cuda::OptionalCUDAGuard guard(h.device());
+        const Rows rh = rows_of(h, "h", kFloat, dev);
+        const Rows rx = rows_of(tensor(a[1], "x"), "x", 1u << rh.type, dev, rh.cols, rh.rows);
+        gs_block_norm_args g = {};
+        g.rows = rh.rows, g.cols = rh.cols, g.type = rh.type;
+        g.h = rh.p, g.ldh = rh.ld, g.x = rx.p, g.ldx = rx.ld;
+        g.weight = vector_of(a[2], "weight", kFloat, dev, rh.cols, &g.weight_type);
+        g.post_weight = vector_of(a[3], "post_weight", kFloat, dev, rh.cols, &g.post_type);
+        gate_of(g, a[4], dev, rh);
+        g.scale = number(a[5], "scale");
+        g.eps = number(a[6], "eps");
+        g.y_type = type_arg(a[7], "out_dtype", kFloat | kE4m3, rh.type);
+        if (!g.weight && a[7] != Py_None) refuse("out_dtype: there is no y without weight");
+        const bool backward = flag(a[8], "need_backward");
+        const Out s = output(h, rh.rows, rh.cols, rh.type);
+        g.s = s.r.p, g.lds = s.r.ld;
+        Tensor y, y_scale, rstd_post, rstd;
+        if (g.weight) {
+            const Out o = output(h, rh.rows, rh.cols, g.y_type);
+            y = o.t;
+            g.y = o.r.p, g.ldy = o.r.ld;
+            if (g.y_type == GS_E4M3) g.y_scale = (y_scale = row_values(h)).data_ptr<float>();
+            if (backward) g.rstd = (rstd = row_values(h)).data_ptr<float>();
+        }
+        if (backward && g.post_weight) g.rstd_post = (rstd_post = row_values(h)).data_ptr<float>();
+        check("gs_block_norm", lib.block_norm(&g, c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream()));
+        return result(y, y_scale, s.t, rstd_post, rstd);
+    });
+}
+
+// (dy, h, s, weight, rstd, post_weight, rstd_post, gate, scale, ds) -> (dh, dx, dweight, dpost_weight, dgate)
+PyObject* block_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded(n, 10, [&] {
+        const Tensor& h = tensor(a[1], "h");
+        const int dev = cuda_device(h, "h");
+        const c10::cuda::OptionalCUDAGuard guard(h.device());
+        const Rows rh = rows_of(h, "h", kFloat, dev);
+        gs_block_norm_bwd_args g = {};
+        g.rows = rh.rows, g.cols = rh.cols, g.type = rh.type, g.h = rh.p, g.ldh = rh.ld;
+        if (a[0] != Py_None) {
+            const Rows dy = rows_of(tensor(a[0], "dy"), "dy", kFloat, dev, rh.cols, rh.rows);
+            const Rows rs = rows_of(tensor(a[2], "s"), "s", 1u << rh.type, dev, rh.cols, rh.rows);
+            g.dy = dy.p, g.lddy = dy.ld, g.dy_type = dy.type, g.s = rs.p, g.lds = rs.ld;
+            g.weight = required(vector_of(a[3], "weight", kFloat, dev, rh.cols, &g.weight_type), "weight", 1);
+            g.rstd = (const float*)required(vector_of(a[4], "rstd", kF32, dev, rh.rows), "rstd (block_norm's with need_backward)", rh.rows);
+        } else if (a[3] != Py_None || a[9] == Py_None)
+            refuse(a[3] != Py_None ? "dy: required with weight" : "ds: required without dy");
+        if (a[9] != Py_None) {
+            const Rows ds = rows_of(tensor(a[9], "ds"), "ds", 1u << rh.type, dev, rh.cols, rh.rows);
+            g.ds = ds.p, g.ldds = ds.ld;
+        }
+        g.post_weight = vector_of(a[5], "post_weight", kFloat, dev, rh.cols, &g.post_type);
+        if (g.post_weight)
+            g.rstd_post = (const float*)required(vector_of(a[6], "rstd_post", kF32, dev, rh.rows), "rstd_post (block_norm's with need_backward)", rh.rows);
+        const Tensor gate = gate_of(g, a[7], dev, rh);
+        g.scale = number(a[8], "scale");
+        Tensor dweight, dpost, dgate;
+        const Out dh = output(h, rh.rows, rh.cols, rh.type), dx = output(h, rh.rows, rh.cols, rh.type);
+        g.dh = dh.r.p, g.lddh = dh.r.ld, g.dx = dx.r.p, g.lddx = dx.r.ld;
+        if (g.weight) g.dweight = (dweight = plain(h, THPVariable_Unpack(a[3]).sizes(), g.weight_type)).data_ptr();
+        if (g.post_weight) g.dpost = (dpost = plain(h, THPVariable_Unpack(a[5]).sizes(), g.post_type)).data_ptr();
+        if (g.gate_rows) {
+            const Out o = output(h, rh.rows, rh.cols, rh.type);
+            dgate = o.t;
+            g.dgate = o.r.p, g.lddg = o.r.ld;
+        } else if (g.gate) g.dgate = (dgate = plain(h, gate.sizes(), g.gate_type)).data_ptr();
+        with_scratch("gs_block_norm_bwd", lib.block_norm_bwd, g, h, dev, false);
+        return result(dh.t, dx.t, dweight, dpost, dgate);
+    });
+}
+
+// ------------------------------------------------------------------ clipping
+// (tensors, max_norm, out) -> norm
+PyObject* clip_norm(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded(n, 3, [&]() -> PyObject* {
+        const auto items = [](PyObject* o, const char* name) {
+            if (!PyList_Check(o) && !PyTuple_Check(o)) refuse(std::string(name) + ": expected a list of tensors, got " + Py_TYPE(o)->tp_name);
+            return PySequence_Fast_GET_SIZE(o);
+        };
+        const Py_ssize_t count = items(a[0], "tensors");
+        if (count < 1 || count > GS_CLIP_MAX_TENSORS)
+            refuse("tensors: 1 to " + std::to_string(GS_CLIP_MAX_TENSORS) + ", got " + std::to_string(count));
+        const bool given = a[2] != Py_None;
+        if (given && items(a[2], "out") != count) refuse("out: expected as many tensors as there are to clip");
+        const Tensor& first = tensor(PySequence_Fast_GET_ITEM(a[0], 0), "tensors[0]");
+        const int dev = cuda_device(first, "tensors[0]");
+        const c10::cuda::OptionalCUDAGuard guard(first.device());
+        std::vector<gs_clip_tensor> list((size_t)count);
+        const auto dense = [&](PyObject* o, const char* what, Py_ssize_t i, int64_t size, int32_t* type) {
+            const std::string name = std::string(what) + "[" + std::to_string(i) + "]";
+            const Tensor& t = tensor(o, name.c_str());
+            check_kind(t, name.c_str(), kFloat, dev);
+            if (!t.is_contiguous()) refuse(name + ": not contiguous, " + shape_of(t));
+            if (size >= 0 && t.numel() != size) refuse(name + ": expected " + std::to_string(size) + " values, got " + shape_of(t));
+            *type = type_code(t.scalar_type());
+            return t;
+        };
+        std::vector<Tensor> outs;
+        outs.reserve((size_t)count);
+        for (Py_ssize_t i = 0; i < count; ++i) {
+            gs_clip_tensor& c = list[(size_t)i];
+            const Tensor t = dense(PySequence_Fast_GET_ITEM(a[0], i), "tensors", i, -1, &c.type);
+            c.p = t.data_ptr(), c.size = t.numel();
+            outs.push_back(given ? dense(PySequence_Fast_GET_ITEM(a[2], i), "out", i, c.size, &c.out_type) : t);
+            if (!given) c.out_type = c.type;
+            c.out = outs.back().data_ptr();
+        }
+        const Tensor norm = at::empty({}, first.options().dtype(ScalarType::Float));
+        gs_clip_norm_args g = {};
+        g.tensors = list.data(), g.count = count, g.norm = norm.data_ptr<float>();
+        g.max_norm = number(a[1], "max_norm");
+        with_scratch("gs_clip_norm", lib.clip_norm, g, first, dev, false);
+        for (const Tensor& t : outs)
+            if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+        return wrap(norm);
+    });
+}
+
 // bind(GsError, addresses of the library's functions in the order of Library)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
@@ -700,15 +849,8 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
             return nullptr;
         }
     }
-    lib.rms_norm = reinterpret_cast<decltype(lib.rms_norm)>(f[0]);
-    lib.rms_norm_bwd = reinterpret_cast<decltype(lib.rms_norm_bwd)>(f[1]);
-    lib.quantize_rows = reinterpret_cast<decltype(lib.quantize_rows)>(f[2]);
-    lib.linear = reinterpret_cast<decltype(lib.linear)>(f[3]);
-    lib.linear_bwd = reinterpret_cast<decltype(lib.linear_bwd)>(f[4]);
-    lib.glu = reinterpret_cast<decltype(lib.glu)>(f[5]);
-    lib.glu_bwd = reinterpret_cast<decltype(lib.glu_bwd)>(f[6]);
-    lib.attention = reinterpret_cast<decltype(lib.attention)>(f[7]);
-    lib.attention_bwd = reinterpret_cast<decltype(lib.attention_bwd)>(f[8]);
+    static_assert(sizeof lib == sizeof f, "a function pointer each");
+    std::memcpy(&lib, f, sizeof f);
     Py_INCREF(a[0]);
     Py_XDECREF(gs_error);
     gs_error = a[0];
@@ -718,7 +860,8 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 #define GS_FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {GS_FAST(bind),          GS_FAST(rms_norm), GS_FAST(rms_norm_backward), GS_FAST(quantize_rows),
                          GS_FAST(linear),        GS_FAST(linear_backward), GS_FAST(glu),       GS_FAST(glu_backward),
-                         GS_FAST(attention),     GS_FAST(attention_backward), {nullptr, nullptr, 0, nullptr}};
+                         GS_FAST(attention),     GS_FAST(attention_backward),
+                         GS_FAST(block_norm),    GS_FAST(block_norm_backward), GS_FAST(clip_norm), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layers_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,45 @@
+// rows.cuh -- reductions over a row that a group of threads holds (norm.cu, block_norm.cu).
+#pragma once
+
+#include "layers_common.cuh"
+
+namespace gs {
+namespace rows {
+
+constexpr float kE4m3Max = 448.0f;
+constexpr float kTiny = 0x1p-100f;
+
+__device__ __forceinline__ float max_nan(float a, float b)   // NaN if either is
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+struct Sum {
+    __device__ static float join(float a, float b) { return a + b; }
+};
+struct Max {
+    __device__ static float join(float a, float b) { return max_nan(a, b); }
+};
+
+// Reduction over the `group` threads of a row: a warp's lanes by butterfly (all
+// lanes get the same bits, the joins being commutative), then the group's warps
+// through shared memory, in order.
+template <class Op>
+__device__ __forceinline__ float group_reduce(float v, int group, float* sm)
+{
+    const int in_warp = group < 32 ? group : 32;
+    for (int o = in_warp >> 1; o > 0; o >>= 1) v = Op::join(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if (group <= 32) return v;
+    const int warp = threadIdx.x >> 5, first = threadIdx.x / group * (group >> 5), last = first + (group >> 5);
+    __syncthreads();   // the previous row's readers are done
+    if ((threadIdx.x & 31) == 0) sm[warp] = v;
+    __syncthreads();
+    float r = sm[first];
+    for (int w = first + 1; w < last; ++w) r = Op::join(r, sm[w]);
+    return r;
+}
+
+}  // namespace rows
+}  // namespace gs

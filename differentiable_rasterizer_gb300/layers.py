@@ -73,6 +73,22 @@ class AttentionGrads(NamedTuple):
     dv: torch.Tensor
 
 
+class BlockNormOut(NamedTuple):
+    y: Optional[torch.Tensor]
+    y_scale: Optional[torch.Tensor]    # [rows], 8-bit y only
+    s: torch.Tensor
+    rstd_post: Optional[torch.Tensor]  # [rows], both for the gradients
+    rstd: Optional[torch.Tensor]
+
+
+class BlockNormGrads(NamedTuple):
+    dh: torch.Tensor
+    dx: torch.Tensor
+    dweight: Optional[torch.Tensor]
+    dpost_weight: Optional[torch.Tensor]
+    dgate: Optional[torch.Tensor]
+
+
 class LinearGrads(NamedTuple):
     dx: Optional[torch.Tensor]
     dw: Optional[torch.Tensor]
@@ -99,9 +115,9 @@ class _Native:
         L = abi.lib()
         module.bind(abi.GsError, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
             "gs_rms_norm", "gs_rms_norm_bwd", "gs_quantize_rows", "gs_linear", "gs_linear_bwd", "gs_glu", "gs_glu_bwd",
-            "gs_attention", "gs_attention_bwd")))
+            "gs_attention", "gs_attention_bwd", "gs_block_norm", "gs_block_norm_bwd", "gs_clip_norm")))
         for f in ("rms_norm", "rms_norm_backward", "quantize_rows", "linear", "linear_backward", "glu", "glu_backward",
-                  "attention", "attention_backward"):
+                  "attention", "attention_backward", "block_norm", "block_norm_backward", "clip_norm"):
             setattr(self, f, getattr(module, f))
         return self.__dict__[name]
 
@@ -216,3 +232,36 @@ def attention_backward(do, q, k, v, o, lse, *, q_starts=None, k_starts=None, cau
     the projection's gradient, say), rows of no sequence are left as they are; else 0."""
     dq, dk, dv = (None, None, None) if out is None else out
     return AttentionGrads(*_native.attention_backward(do, q, k, v, o, lse, q_starts, k_starts, causal, scale, dq, dk, dv))
+
+
+# ------------------------------------------------------------------ block norm
+def block_norm(h, x, weight=None, *, post_weight=None, gate=None, scale=1.0, eps=1e-6, out_dtype=None,
+               need_backward=False) -> BlockNormOut:
+    """What lies between a block's output h, on the residual stream x, and the next block:
+
+        a = h / sqrt(mean(h^2) + eps) * post_weight      (a = h without post_weight)
+        s = scale * x + gate * a                          (gate 1 without one)
+        y = s / sqrt(mean(s^2) + eps) * weight            (no y without weight)
+
+    over the last dimension.  h, x: float32, bfloat16 or float16 (one type); the weights any
+    of them; gate: [columns] of any of them, or like h, a gate a value.  s is rounded to h's
+    type; y has out_dtype as in rms_norm (float8_e4m3fn: y * y_scale is the norm)."""
+    return BlockNormOut(*_native.block_norm(h, x, weight, post_weight, gate, scale, eps, out_dtype, need_backward))
+
+
+def block_norm_backward(dy, h, s, weight, rstd, *, post_weight=None, rstd_post=None, gate=None, scale=1.0,
+                        ds=None) -> BlockNormGrads:
+    """Gradients of block_norm from those of y (dy) and, optionally, of s (ds); rstd, rstd_post:
+    block_norm's with need_backward.  Without weight: dy, s, weight and rstd are None, ds is
+    required.  dh, dx have h's type, the others that of what they are the gradients of."""
+    return BlockNormGrads(*_native.block_norm_backward(dy, h, s, weight, rstd, post_weight, rstd_post, gate, scale, ds))
+
+
+# ------------------------------------------------------------------ clipping
+def clip_norm(tensors, max_norm, *, out=None) -> torch.Tensor:
+    """The norm over all values of the tensors (a list; contiguous float32, bfloat16 or float16,
+    each of its own memory) as a float32 scalar on their device; the tensors times
+    min(1, max_norm / norm) are written to out (a list of as many values each, of any of the
+    types), or in place.  Nothing is scaled by a norm that is not finite: the caller sees it in
+    the result and can skip the step."""
+    return _native.clip_norm(tensors, max_norm, out)

@@ -448,6 +448,8 @@ GS_API gs_status gs_check_report(uint64_t* report, int32_t* checked);
  *   gs_linear     y = act(x w^T + bias) + residual
  *   gs_glu        h = act(x Wg^T) * (x Wu^T)   (gs_linear is the down projection)
  *   gs_attention  o = softmax(scale q k^T) v over packed sequences
+ *   gs_block_norm s = scale x + gate (h / rms(h) * post), y = s / rms(s) * weight
+ * and gs_clip_norm, which scales all gradients to a largest norm.
  * Conventions, besides those at the top of this file:
  *   - Matrices are row-major: element (r, c) of a matrix with leading dimension
  *     ld (in elements, >= its columns) is p[r * ld + c].  Any ld and any
@@ -751,6 +753,110 @@ typedef struct gs_attention_bwd_args {
     int32_t heads, kv_heads, dim, type, causal, fill, reserved;
 } gs_attention_bwd_args;
 GS_API gs_status gs_attention_bwd(const gs_attention_bwd_args* args, void* ws, size_t* ws_bytes, void* stream);
+
+/* The norm after a block, its gate and residual scale, and the norm before the next
+ * block, in one pass over the rows:
+ *   a = h * rstd_post * post_weight,  rstd_post = 1 / sqrt(mean(h^2) + eps)
+ *   s = scale * x + gate * a,         rstd = 1 / sqrt(mean(s^2) + eps)
+ *   y = s * rstd * weight             (E4M3: with y_scale, as gs_rms_norm's)
+ * post_weight NULL: a = h.  gate: NULL (1), [cols] of gate_type, or with gate_rows
+ * [rows][cols] of `type` at pitch ldg.  weight and y: both NULL, or both given.  The
+ * norm is taken of the fp32 sum; s receives it rounded to `type`.
+ * h, x, s: [rows][cols] of `type` (F32, BF16, F16); weight, post_weight, gate: F32,
+ * BF16 or F16 each; y: y_type.  rstd_post (with post_weight only), rstd (with weight
+ * only): [rows] or NULL.  s may be the same array as x or h.
+ * Errors: as gs_rms_norm; scale not finite. */
+typedef struct gs_block_norm_args {
+    int64_t rows, cols;
+    const void* h;
+    int64_t ldh;
+    const void* x;
+    int64_t ldx;
+    const void* post_weight;
+    const void* gate;
+    int64_t ldg;
+    const void* weight;
+    void* s;
+    int64_t lds;
+    void* y;
+    int64_t ldy;
+    float* y_scale;
+    float* rstd_post;
+    float* rstd;
+    float scale, eps;
+    int32_t type, post_type, gate_type, gate_rows, weight_type, y_type;
+} gs_block_norm_args;
+GS_API gs_status gs_block_norm(const gs_block_norm_args* args, void* stream);
+
+/* Gradients of gs_block_norm (16- or 32-bit y).
+ *   g = rstd * (dy * weight - s * rstd^2 * mean(dy * weight * s)) + ds   (of s)
+ *   dx = scale * g;  dgate = g * a, [cols]: summed over rows;  da = gate * g
+ *   dh = rstd_post * (da * post_weight - h * rstd_post^2 * mean(da * post_weight * h))
+ *   dpost = sum over rows of da * h * rstd_post;  dweight = sum over rows of dy * s * rstd
+ * dy, weight, rstd: all given or all NULL (g = ds then, which must be given).
+ * post_weight, rstd_post: both or neither (dh = da then).  ds may be NULL with dy.
+ * s: the forward's, read with dy only; h is read with post_weight or dgate only.  dy:
+ * dy_type; h, s, ds, dh, dx: `type`; dweight, dpost, dgate: the types of weight,
+ * post_weight and gate (gate_rows: [rows][cols] at pitch lddg).  Each output may be NULL.
+ * Errors: as gs_block_norm, and a too small workspace. */
+typedef struct gs_block_norm_bwd_args {
+    int64_t rows, cols;
+    const void* dy;
+    int64_t lddy;
+    const void* ds;
+    int64_t ldds;
+    const void* h;
+    int64_t ldh;
+    const void* s;
+    int64_t lds;
+    const void* post_weight;
+    const void* gate;
+    int64_t ldg;
+    const void* weight;
+    const float* rstd_post;
+    const float* rstd;
+    void* dh;
+    int64_t lddh;
+    void* dx;
+    int64_t lddx;
+    void* dgate;
+    int64_t lddg;
+    void* dweight;
+    void* dpost;
+    float scale;
+    int32_t type, dy_type, post_type, gate_type, gate_rows, weight_type, reserved;
+} gs_block_norm_bwd_args;
+GS_API gs_status gs_block_norm_bwd(const gs_block_norm_bwd_args* args, void* ws, size_t* ws_bytes, void* stream);
+
+/* The norm over many tensors, and the tensors scaled to a largest one (gradient clipping):
+ *   norm = sqrt(sum over all values of all tensors of v^2)
+ *   out = v * min(1, max_norm / norm)
+ * tensors: HOST array of `count`, at most GS_CLIP_MAX_TENSORS; each has `size` (0 is
+ * valid) consecutive values of `type` at `p` and as many of out_type at `out` (F32,
+ * BF16 or F16; out may be p with the same type: in place).  Nothing else may overlap:
+ * two tensors that share memory are refused.  The product is rounded once; with a factor
+ * of 1 values pass unchanged (in place: nothing is written).  norm: device fp32 out.
+ * Squares are summed in fp32 in parts and the parts in fp64, those of very large and
+ * very small values apart, so that no norm within fp32's range overflows or vanishes on
+ * the way; the sum is taken in a fixed order.  A norm that is not finite (a NaN or an infinity among the
+ * values) leaves the values unscaled (factor 1), so that the caller can tell by `norm`
+ * and skip the step.  max_norm: not NaN, >= 0.
+ * Errors: INVALID_ARG; CUDA on launch failure. */
+#define GS_CLIP_MAX_TENSORS 1024
+typedef struct gs_clip_tensor {
+    const void* p;
+    void* out;
+    int64_t size;
+    int32_t type, out_type;
+} gs_clip_tensor;
+typedef struct gs_clip_norm_args {
+    const gs_clip_tensor* tensors;
+    int64_t count;
+    float* norm;
+    float max_norm;
+    int32_t reserved;
+} gs_clip_norm_args;
+GS_API gs_status gs_clip_norm(const gs_clip_norm_args* args, void* ws, size_t* ws_bytes, void* stream);
 
 /* The layers' products wait on their own copies and tensor-core work, each wait
  * bounded to about two seconds of the multiprocessor's clock; a kernel whose wait
