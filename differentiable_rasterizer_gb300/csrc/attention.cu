@@ -2,16 +2,16 @@
 //
 //   t = scale q k^T,  p = exp(t - m),  o = (p v) / sum p,   m the rows' running maximum
 //
-// One pass over the keys, 128 at a time, for two tiles of 128 packed rows a CTA.  10 warps
-// with fixed roles:
+// One pass over the keys, 128 at a time, for two tiles of 128 packed rows a CTA.  Warps have
+// fixed roles:
 //   warps 0-3, 4-7  softmax of the first and of the second tile, a row a thread: scores
 //                   TMEM -> registers -> p in 16 bits back over the scores, the sum in fp32
 //   warp 8          TMA producer: the two tiles of q, then keys and values in a ring
-//   warp 9          issues tcgen05.mma: scores from shared memory, p v with p from TMEM
+//   warps 9, 10     issue a tile's tcgen05.mma: scores from shared memory, p v with p from TMEM
 // The tiles take turns: while one tile's softmax works, the tensor cores compute the
 // other's products.  TMEM, fp32: scores of both tiles (p in their first 64 columns), o of
 // both.  The products of a tile's p with v and of its next scores, which overwrite p, are
-// issued in that order by one thread and run in it.
+// issued in that order by one lane and run in it.
 //
 // The maximum that a row's terms are taken to is raised only when a tile of keys exceeds
 // it by more than 2^8: o and the sum are then rescaled (rare after the first tiles), and
@@ -28,7 +28,6 @@ namespace gs {
 namespace attn {
 namespace {
 
-constexpr int kWarps = 10, kThreads = kWarps * 32;
 constexpr int kTmemCols = 512, kTmemO = 256;
 constexpr float kRaise = 8.0f;   // log2
 
@@ -39,7 +38,7 @@ struct Shape {
     static constexpr int kStages = DP == 128 ? 5 : 8;
     static constexpr uint32_t kAtRing = 2 * kTile, kAtBars = kAtRing + kStages * kTile;
     static constexpr int kQFull = 0, kFull = 2, kEmpty = kFull + kStages, kScores = kEmpty + kStages, kTerms = kScores + 2,
-                         kSums = kTerms + 2, kDone = kSums + 2, kBars = kDone + 1;
+                         kSums = kTerms + 4, kClear = kSums + 2, kDone = kClear + 1, kBars = kDone + 2;
     static constexpr int kSmem = kAtBars + ((kBars * 8 + 15) & ~15) + 16;
     static_assert(kSmem <= 232448, "shared memory of an SM");
 };
@@ -129,74 +128,76 @@ __device__ __forceinline__ void load(const Params& p, const Work& w, int n, uint
     last_copies<S::kStages>(issued, [&](uint32_t s, uint32_t parity) { landed = landed && mbar_wait_alone(bars + 8 * (S::kFull + s), parity); });
 }
 
-// The issuing warp: a whole warp waits and clears rows, its elected lane issues.
+// A lane issues the products of tile i.  (Of both tiles in turn one lane is too slow: each
+// of its waits takes some 350 cycles beside products whose factors come from shared memory,
+// 900 TFLOP/s where two lanes reach 1,100.)
 template <int DP>
-__device__ __forceinline__ void issue(const Params& p, const Work& w, int n, uint32_t smem, uint32_t bars, uint32_t tmem, int lane,
-                                      volatile int* gave_up)
+__device__ __forceinline__ void issue(const Params& p, const Work& w, int i, int n, uint32_t smem, uint32_t bars, uint32_t tmem, volatile int* gave_up)
 {
     using S = Shape<DP>;
-    const bool one = elect_one();
-    const int steps = (p.dim + 15) / 16;
-    const auto scores = [&](int i, uint32_t tile) {   // of tile i with the keys there
+    const int mine = i ? w.n[1] : w.n[0];
+    const uint32_t steps = (uint32_t)(p.dim + 15) / 16, score = tmem + i * 128, sum = tmem + kTmemO + i * DP;
+    const bool ragged = w.seq.lk < (w.from + n) * kRows;
+    const auto scores = [&](uint32_t tile) {
         const uint32_t a = desc_lo(smem + i * S::kTile, true), b = desc_lo(tile, true);
-        for (int s = 0; s < steps; ++s) {
-            const uint32_t at = (uint32_t)(s >> 2) * (kBox >> 4) + (uint32_t)(s & 3) * k_step(true);
-            mma<false, false>(tmem + i * 128, a + at, kDescHi, b + at, kDescHi, p.idesc_s, s > 0);
+#pragma unroll
+        for (uint32_t s = 0; s < DP / 16; ++s) {
+            const uint32_t at = (s >> 2) * (kBox >> 4) + (s & 3) * k_step(true);
+            if (s < steps) mma<false, false>(score, a + at, kDescHi, b + at, kDescHi, p.idesc_s, s > 0);
         }
         mma_commit<false>(bars + 8 * (S::kScores + i));
     };
-    Ring<S::kStages> ring;   // at the next stage to be waited for
-    uint32_t keys = ring.s;
-    bool ok = mbar_wait(bars + 8 * (S::kFull + ring.s), ring.parity, gave_up);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (ok && w.n[i] > 0) {
-            ok = mbar_wait(bars + 8 * (S::kQFull + i), 0, gave_up);
-            if (ok && one) scores(i, smem + S::kAtRing + keys * S::kTile);
-        }
-    if (ok && one) mma_commit<false>(bars + 8 * (S::kEmpty + keys));
-    ring.next();
-    for (int j = 0; ok && j < n; ++j) {
-        const uint32_t values = ring.s, at = smem + S::kAtRing + values * S::kTile;
-        ok = mbar_wait(bars + 8 * (S::kFull + ring.s), ring.parity, gave_up);
-        if (!ok) break;
+    Ring<S::kStages> ring;   // copies in the order K(0), V(0), K(1), ...
+    if (mine > 0) {
+        if (!mbar_wait(bars + 8 * S::kFull, 0, gave_up) || !mbar_wait(bars + 8 * (S::kQFull + i), 0, gave_up)) return;
+        scores(smem + S::kAtRing);
+        mma_commit<false>(bars + 8 * S::kEmpty);
         ring.next();
-        const int live = w.seq.lk - (w.from + j) * kRows;   // the rows behind are other sequences'
-        if (live < kRows) zero_rows<S::kChunks>(at, live, lane);
-        bool more = false;
+    }
+    for (int j = 0; j < mine; ++j) {
+        const uint32_t values = ring.s, b = desc_rows(smem + S::kAtRing + values * S::kTile);
+        if (!mbar_wait(bars + 8 * (S::kFull + values), ring.parity, gave_up)) return;
+        ring.next();
+        const uint32_t keys = ring.s;
+        const bool more = j + 1 < mine;
+        if (more && !mbar_wait(bars + 8 * (S::kFull + keys), ring.parity, gave_up)) return;
+        if (ragged && j == n - 1 && !mbar_wait(bars + 8 * S::kClear, 0, gave_up)) return;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (!ok || j >= w.n[i]) continue;
-            ok = mbar_wait(bars + 8 * (S::kTerms + i), j & 1, gave_up);
-            if (!ok) continue;
+        for (int half = 0; half < 2; ++half) {
+            if (!mbar_wait(bars + 8 * (S::kTerms + 2 * i + half), j & 1, gave_up)) return;
             tc_fence_after();
-            if (one) {
-                const uint32_t b = desc_rows(at);
 #pragma unroll
-                for (int s = 0; s < kRows / 16; ++s)
-                    mma_tmem(tmem + kTmemO + i * DP, tmem + i * 128 + s * 8, b + s * k_step(false), kDescHi, p.idesc_o, j > 0 || s > 0);
-                mma_commit<false>(bars + 8 * (S::kSums + i));
-            }
-            if (j + 1 < w.n[i]) {
-                if (!more) {
-                    keys = ring.s;
-                    ok = mbar_wait(bars + 8 * (S::kFull + keys), ring.parity, gave_up);
-                    more = true;
-                }
-                if (ok && one) scores(i, smem + S::kAtRing + keys * S::kTile);
-            }
+            for (int s = 4 * half; s < 4 * half + 4; ++s)
+                mma_tmem(sum, score + s * 8, b + s * k_step(false), kDescHi, p.idesc_o, j > 0 || s > 0);
         }
-        if (ok && one) {
-            mma_commit<false>(bars + 8 * (S::kEmpty + values));
-            if (more) mma_commit<false>(bars + 8 * (S::kEmpty + keys));
+        if (more) scores(smem + S::kAtRing + keys * S::kTile);
+        mma_commit<false>(bars + 8 * (S::kSums + i));
+        mma_commit<false>(bars + 8 * (S::kEmpty + values));
+        if (more) {
+            mma_commit<false>(bars + 8 * (S::kEmpty + keys));
+            ring.next();
         }
-        if (more) ring.next();
     }
-    if (one) {
-        mma_commit<false>(bars + 8 * S::kDone);
-        if (!mbar_wait_alone(bars + 8 * S::kDone, 0)) *gave_up = 1;
+    // copies that only the other tile reads: both lanes free a stage
+    for (int c = 2 * mine; c < 2 * n; ++c, ring.next()) {
+        if (!mbar_wait(bars + 8 * (S::kFull + ring.s), ring.parity, gave_up)) return;
+        mbar_arrive(bars + 8 * (S::kEmpty + ring.s));
     }
-    __syncwarp();
+}
+
+// The rows of the last values that are behind the sequence, other sequences' perhaps: zero,
+// for the product contracts over them.  By the loading warp, once all copies are under way
+// (no stage is filled again, so the barrier's parity tells the last copy).
+template <int DP>
+__device__ __forceinline__ void clear_values(const Work& w, int n, uint32_t smem, uint32_t bars, int lane, volatile int* gave_up)
+{
+    using S = Shape<DP>;
+    const int live = w.seq.lk - (w.from + n - 1) * kRows;
+    if (live >= kRows || *gave_up) return;
+    const uint32_t copy = 2 * n - 1;
+    if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * (S::kFull + copy % S::kStages), copy / S::kStages & 1, gave_up))) return;
+    zero_rows<S::kChunks>(smem + S::kAtRing + copy % S::kStages * S::kTile, live, lane);
+    if (lane == 0) mbar_arrive(bars + 8 * S::kClear);
 }
 
 // A row a thread: i the tile, r the row.
@@ -204,7 +205,7 @@ template <int T, int DP>
 __device__ __forceinline__ void softmax(const Params& p, const Work& w, int i, int r, uint32_t bars, uint32_t tmem, volatile int* gave_up)
 {
     using S = Shape<DP>;
-    const int n = w.n[i], t0 = w.t0 + i * p.tokens;
+    const int n = i ? w.n[1] : w.n[0], t0 = w.t0 + i * p.tokens;
     const int token = t0 + r / p.group, head = (int)w.head * p.group + r % p.group;
     const bool live = r < p.tokens * p.group && token < w.seq.lq;
     const int seen = keys_seen(w.seq, token, p.causal);                 // this row's keys
@@ -218,23 +219,26 @@ __device__ __forceinline__ void softmax(const Params& p, const Work& w, int i, i
         if (!ok) break;
         tc_fence_after();
         uint32_t s[128];
-#pragma unroll
-        for (int c = 0; c < 128; c += 32) tmem_ld32(scores + c, s + c);
-#pragma unroll
-        for (int c = 0; c < 128; c += 32) tmem_ld32_wait(s + c);
-        const int first = (w.from + j) * kRows;
-        if (first + kRows > all) {
-            const int left = seen - first;
-#pragma unroll
-            for (int c = 0; c < 128; ++c)
-                if (c >= left) s[c] = 0xff800000u;   // -infinity, whatever the hidden key gave
-        }
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        const int first = (w.from + j) * kRows, left = seen - first;
+        const bool cut = first + kRows > all;
+        tmem_ld32(scores, s);
+        tmem_ld32_wait(s);
 #pragma unroll
-        for (int c = 0; c < 128; c += 8)
+        for (int c = 0; c < 128; c += 32) {
+            if (c < 96) tmem_ld32(scores + c + 32, s + c + 32);   // on its way while these are compared
+            if (cut) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) top[e] = fmaxf(fmaxf(top[e], __uint_as_float(s[c + e])), __uint_as_float(s[c + 4 + e]));
-        const float new_m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale2;
+                for (int e = c; e < c + 32; ++e)
+                    if (e >= left) s[e] = 0xff800000u;   // -infinity, whatever the hidden key gave
+            }
+#pragma unroll
+            for (int e = c; e < c + 32; e += 8)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top[k] = max3(top[k], __uint_as_float(s[e + k]), __uint_as_float(s[e + 4 + k]));
+            if (c < 96) tmem_ld32_wait(s + c + 32);
+        }
+        const float new_m = max3(fmaxf(top[0], top[1]), top[2], top[3]) * p.scale2;
         const bool raise = new_m > m + kRaise;   // from -infinity: by any score
         if (j == 0) m = new_m;
         else if (__any_sync(0xffffffffu, raise)) {
@@ -269,11 +273,13 @@ __device__ __forceinline__ void softmax(const Params& p, const Work& w, int i, i
                 h[e] = pack_half2(a, b, T);
             }
             tmem_st16(scores + c / 2, h);
+            if (c & 32) {   // a half of the terms, whose product starts with it
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if ((threadIdx.x & 31) == 0) mbar_arrive(bars + 8 * (S::kTerms + 2 * i + c / 64));
+            }
         }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) mbar_arrive(bars + 8 * (S::kTerms + i));
     }
     if (n > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (S::kSums + i), (n - 1) & 1, gave_up));
     if (!ok) return;
@@ -334,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < S::kBars; ++i) mbar_init(bars + 8 * i, i >= S::kTerms && i < S::kSums ? 4 : 1);
+        for (int i = 0; i < S::kBars; ++i) mbar_init(bars + 8 * i, i >= S::kTerms && i < S::kSums ? 4 : (i >= S::kEmpty && i < S::kScores ? 2 : 1));
         *gave_up = 0;
         mbar_init_fence();
     }
@@ -349,12 +355,24 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const uint32_t tmem = *tmem_slot;
     const int n = w.n[0] > w.n[1] ? w.n[0] : w.n[1];
 
-    if (warp == 8) {
-        if (n > 0 && elect_one()) load<DP>(p, w, n, smem, bars, gave_up);
-        __syncwarp();
-    } else if (warp == 9) {
-        if (n > 0) issue<DP>(p, w, n, smem, bars, tmem, lane, gave_up);
+    if (warp >= 8) {
+        few_registers();
+        if (warp == 8) {
+            if (n > 0) {
+                if (elect_one()) load<DP>(p, w, n, smem, bars, gave_up);
+                __syncwarp();
+                clear_values<DP>(w, n, smem, bars, lane, gave_up);
+            }
+        } else if (warp < 11) {
+            const int i = warp - 9;
+            if (elect_one()) {
+                issue<DP>(p, w, i, n, smem, bars, tmem, gave_up);
+                mma_commit<false>(bars + 8 * (S::kDone + i));   // the block does not leave before its products are done
+                if (!mbar_wait_alone(bars + 8 * (S::kDone + i), 0)) *gave_up = 1;
+            }
+        }
     } else {
+        many_registers();
         const int i = warp >> 2, r = threadIdx.x & 127;
         if (i < p.tiles && w.t0 + i * p.tokens < w.seq.lq)
             softmax<T, DP>(p, w, i, r, bars, tmem + ((uint32_t)((warp & 3) * 32) << 16), gave_up);

@@ -203,6 +203,20 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 // A tile's descriptor as the contracted rows of a product (k slow, 64 columns a box).
 __device__ __forceinline__ uint32_t desc_rows(uint32_t addr) { return (addr >> 4) | ((kBox >> 4) << 16); }
 
+// The greatest of three in one instruction.
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Three warpgroups start with 168 registers a thread, all that the SM has: the third, of
+// few registers, leaves the other two 224 (2 x 224 + 56 = 3 x 168).  Whole warpgroups call these.
+constexpr int kThreads = 384;
+__device__ __forceinline__ void many_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 224;"); }
+__device__ __forceinline__ void few_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 56;"); }
+
 // ------------------------------------------------------------------ rows out
 // 32 columns from col of a row of `cols` 16-bit elements; vec: 2 the row starts on 32
 // bytes, 1 on 16, 0 neither.

@@ -25,7 +25,6 @@ namespace gs {
 namespace attn {
 namespace {
 
-constexpr int kWarps = 10, kThreads = kWarps * 32;
 constexpr int kTmemCols = 512;
 constexpr int kStatRows = kRows + 2;   // of a copy of row statistics, which starts on 16 bytes
 
@@ -448,12 +447,15 @@ __global__ void __launch_bounds__(kThreads, 1) keys_kernel(const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    if (warp == 8) {
-        if (w.n > 0 && elect_one()) load_queries<DP>(p, w, smem, bars, gave_up);
-        __syncwarp();
-    } else if (warp == 9) {
-        if (w.n > 0) issue_keys<DP>(p, w, smem, bars, tmem, lane, gave_up);
+    if (warp >= 8) {
+        few_registers();
+        if (warp == 8) {
+            if (w.n > 0 && elect_one()) load_queries<DP>(p, w, smem, bars, gave_up);
+            __syncwarp();
+        } else if (warp == 9 && w.n > 0)
+            issue_keys<DP>(p, w, smem, bars, tmem, lane, gave_up);
     } else {
+        many_registers();
         const int exponent = ds_exponent<T>(p);
         key_terms<T, DP>(p, w, warp >> 2, threadIdx.x & 127, smem, bars, tmem + ((uint32_t)((warp & 3) * 32) << 16), exponent, gave_up);
     }
@@ -627,7 +629,7 @@ __device__ __forceinline__ void query_terms(const Params& p, const QueryWork& w,
                                             volatile int* gave_up)
 {
     using S = QueryShape<DP>;
-    const int n = w.n[i], t0 = w.t0 + i * p.tokens;
+    const int n = i ? w.n[1] : w.n[0], t0 = w.t0 + i * p.tokens;
     const int token = t0 + r / p.group;
     const bool live = r < p.tokens * p.group && token < w.seq.lq;
     const int64_t row = w.seq.q0 + token;
@@ -731,12 +733,15 @@ __global__ void __launch_bounds__(kThreads, 1) queries_kernel(const __grid_const
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int n = w.n[0] > w.n[1] ? w.n[0] : w.n[1];
-    if (warp == 8) {
-        if (n > 0 && elect_one()) load_keys<DP>(p, w, n, smem, bars, gave_up);
-        __syncwarp();
-    } else if (warp == 9) {
-        if (n > 0) issue_queries<DP>(p, w, n, smem, bars, tmem, lane, gave_up);
+    if (warp >= 8) {
+        few_registers();
+        if (warp == 8) {
+            if (n > 0 && elect_one()) load_keys<DP>(p, w, n, smem, bars, gave_up);
+            __syncwarp();
+        } else if (warp == 9 && n > 0)
+            issue_queries<DP>(p, w, n, smem, bars, tmem, lane, gave_up);
     } else {
+        many_registers();
         const int i = warp >> 2, exponent = ds_exponent<T>(p);
         if (i < p.tiles && w.t0 + i * p.tokens < w.seq.lq)
             query_terms<T, DP>(p, w, i, threadIdx.x & 127, bars, tmem + ((uint32_t)((warp & 3) * 32) << 16), exponent, gave_up);
