@@ -57,32 +57,34 @@ struct StatParams {
     int heads, kv_heads, group, dim, vec;
 };
 
-// A warp a row and head, 8 elements a lane.
-template <int T>
+// LANES lanes a row and head (a power of two that covers dim at 8 elements a lane).
+template <int T, int LANES>
 __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ StatParams p)
 {
     __shared__ float most[2][8];
+    constexpr int kLines = 256 / LANES;   // of a block's round
     wait_for_predecessor();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t step = (int64_t)gridDim.x * 8, lines = p.q_rows * p.heads;
-    float most_do = 0.0f, most_v = 0.0f;
-    for (int64_t i = (int64_t)blockIdx.x * 8 + warp; i < lines; i += step) {
-        const int64_t r = i / p.heads;
-        const int h = (int)(i - r * p.heads);
-        const uint16_t *o = p.o + r * p.o_row + h * p.o_head, *d = p.d_o + r * p.do_row + h * p.do_head;
-        float sum = 0.0f;
-        if (lane * 8 < p.dim) {   // the same sum in either case
-            float a[8], b[8];
-            if (p.vec) {
-                load8(o, lane * 8, T, a);
-                load8(d, lane * 8, T, b);
-            } else
+    const int lane = threadIdx.x % LANES, col = lane * 8;
+    const int64_t step = (int64_t)gridDim.x * kLines, first = (int64_t)blockIdx.x * kLines + threadIdx.x / LANES;
+    const auto load = [&](const uint16_t* from, float (&v)[8]) {
+        if (p.vec) {
+            load8(from, col, T, v);
+            return;
+        }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const bool there = lane * 8 + e < p.dim;
-                    a[e] = there ? load_elem(o, lane * 8 + e, T) : 0.0f;
-                    b[e] = there ? load_elem(d, lane * 8 + e, T) : 0.0f;
-                }
+        for (int e = 0; e < 8; ++e) v[e] = col + e < p.dim ? load_elem(from, col + e, T) : 0.0f;
+    };
+    float most_do = 0.0f, most_v = 0.0f;
+    // every thread of a warp runs the same number of rounds (the sums use whole warps)
+    const int64_t lines = p.q_rows * p.heads;
+    for (int64_t i0 = (int64_t)blockIdx.x * kLines; i0 < lines; i0 += step) {
+        const int64_t i = i0 + threadIdx.x / LANES, r = i / p.heads;
+        const int h = (int)(i - r * p.heads);
+        float sum = 0.0f;
+        if (i < lines && col < p.dim) {
+            float a[8], b[8];
+            load(p.o + r * p.o_row + h * p.o_head, a);
+            load(p.d_o + r * p.do_row + h * p.do_head, b);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 sum = __fmaf_rn(a[e], b[e], sum);
@@ -90,8 +92,8 @@ __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ Stat
             }
         }
 #pragma unroll
-        for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-        if (lane == 0) {
+        for (int s = LANES / 2; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+        if (lane == 0 && i < lines) {
             const float lse = p.lse[i];
             // a row that sees no key: every p is 2^-infinity
             p.stats[(h / p.group) * p.stat_pitch + r * p.group + h % p.group] =
@@ -99,17 +101,20 @@ __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ Stat
         }
     }
     if (!p.most) return;
-    for (int64_t i = (int64_t)blockIdx.x * 8 + warp; i < p.k_rows * p.kv_heads; i += step) {
+    for (int64_t i = first; i < p.k_rows * p.kv_heads; i += step) {
+        if (col >= p.dim) break;
         const int64_t r = i / p.kv_heads;
-        const uint16_t* v = p.v + r * p.v_row + (i - r * p.kv_heads) * p.v_head;
-        for (int c = lane; c < p.dim; c += 32) most_v = fmaxf(most_v, fabsf(load_elem(v, c, T)));
+        float v[8];
+        load(p.v + r * p.v_row + (i - r * p.kv_heads) * p.v_head, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) most_v = fmaxf(most_v, fabsf(v[e]));
     }
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) {
         most_do = fmaxf(most_do, __shfl_xor_sync(0xffffffffu, most_do, s));
         most_v = fmaxf(most_v, __shfl_xor_sync(0xffffffffu, most_v, s));
     }
-    if (lane == 0) most[0][warp] = most_do, most[1][warp] = most_v;
+    if ((threadIdx.x & 31) == 0) most[0][threadIdx.x >> 5] = most_do, most[1][threadIdx.x >> 5] = most_v;
     __syncthreads();
     if (threadIdx.x < 2) {
         float m = 0.0f;
@@ -161,7 +166,7 @@ struct KeyShape {
     static constexpr uint32_t kAtBars = kAtStats + 2 * kStatBytes;
     static constexpr int kKV = 0, kQFull = 1, kQEmpty = kQFull + kStagesQ, kOFull = kQEmpty + kStagesQ, kOEmpty = kOFull + kStagesO,
                          kStatFull = kOEmpty + kStagesO, kStatEmpty = kStatFull + 2, kS = kStatEmpty + 2, kR = kS + 1, kP = kR + 1,
-                         kDs = kP + 1, kDone = kDs + 1, kBars = kDone + 1;
+                         kDs = kP + 1, kClearQ = kDs + 1, kClearO = kClearQ + 1, kDone = kClearO + 1, kBars = kDone + 2;
     static constexpr int kSmem = kAtBars + ((kBars * 8 + 15) & ~15) + 16;
     static_assert(kSmem <= 232448 && kStatBytes % 16 == 0, "shared memory of an SM");
 };
@@ -227,82 +232,71 @@ __device__ __forceinline__ void load_queries(const Params& p, const KeyWork& w, 
     last_copies<S::kStagesO>(no, [&](uint32_t s, uint32_t parity) { landed = landed && mbar_wait_alone(bars + 8 * (S::kOFull + s), parity); });
 }
 
+// Rows of the last tiles that hold no query of the sequence are other sequences': zero, for
+// they are contracted over.  (Rows behind the packed ones are zeroed once, at the start.)
+// By the loading warp, once all copies are under way.
 template <int DP>
-__device__ __forceinline__ void issue_keys(const Params& p, const KeyWork& w, uint32_t smem, uint32_t bars, uint32_t tmem, int lane,
+__device__ __forceinline__ void clear_queries(const Params& p, const KeyWork& w, uint32_t smem, uint32_t bars, int lane, volatile int* gave_up)
+{
+    using S = KeyShape<DP>;
+    const int live = (w.seq.lq - w.first - (w.n - 1) * p.tokens) * p.group;
+    if (live >= p.tokens * p.group || *gave_up) return;
+    const uint32_t copy = w.n - 1, q = copy % S::kStagesQ, o = copy % S::kStagesO;
+    if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * (S::kQFull + q), copy / S::kStagesQ & 1, gave_up))) return;
+    zero_rows<S::kChunks>(smem + S::kAtQ + q * S::kTile, live, lane);
+    if (lane == 0) mbar_arrive(bars + 8 * S::kClearQ);
+    if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * (S::kOFull + o), copy / S::kStagesO & 1, gave_up))) return;
+    zero_rows<S::kChunks>(smem + S::kAtO + o * S::kTile, live, lane);
+    if (lane == 0) mbar_arrive(bars + 8 * S::kClearO);
+}
+
+// Two lanes issue, each the products around what it waits for: S and dV (P's), R and dK
+// (dS's).  S(i + 1) takes P(i)'s place after dV(i), R(i + 1) dS(i)'s after dK(i).
+template <int DP>
+__device__ __forceinline__ void issue_keys(const Params& p, const KeyWork& w, bool second, uint32_t smem, uint32_t bars, uint32_t tmem,
                                            volatile int* gave_up)
 {
     using S = KeyShape<DP>;
-    const bool one = elect_one();
-    const int steps = (p.dim + 15) / 16;
-    // rows that hold no query of the sequence: contracted over, so they have to be zero
-    const auto live = [&](int i) {
-        const int rows = (w.seq.lq - w.first - i * p.tokens) * p.group, full = p.tokens * p.group;
-        return rows < full ? rows : full;
-    };
-    const auto rows_product = [&](uint32_t d, uint32_t a, uint32_t b) {   // [keys] x [queries]
-        for (int s = 0; s < steps; ++s) {
-            const uint32_t at = (uint32_t)(s >> 2) * (kBox >> 4) + (uint32_t)(s & 3) * k_step(true);
-            mma<false, false>(d, desc_lo(a, true) + at, kDescHi, desc_lo(b, true) + at, kDescHi, p.idesc_s, s > 0);
-        }
-    };
-    const auto sum_product = [&](uint32_t d, uint32_t a, uint32_t b, bool add) {   // halves of 64 queries, 32 columns each, 64 apart
+    const uint32_t steps = (uint32_t)(p.dim + 15) / 16;
+    const bool ragged = (w.seq.lq - w.first - (w.n - 1) * p.tokens) * p.group < p.tokens * p.group;
+    // first lane: a is K, the rows Q, the sum's rows dO; second: V, dO, Q
+    const uint32_t at_rows = smem + (second ? S::kAtO : S::kAtQ), at_sum = smem + (second ? S::kAtQ : S::kAtO);
+    const uint32_t rows_full = bars + 8 * (second ? S::kOFull : S::kQFull), sum_full = bars + 8 * (second ? S::kQFull : S::kOFull);
+    const uint32_t rows_empty = bars + 8 * (second ? S::kOEmpty : S::kQEmpty), sum_empty = bars + 8 * (second ? S::kQEmpty : S::kOEmpty);
+    const uint32_t rows_stages = second ? S::kStagesO : S::kStagesQ, sum_stages = second ? S::kStagesQ : S::kStagesO;
+    const uint32_t terms = tmem + (second ? kTmemR : 0), sum = tmem + kTmemDv + (second ? DP : 0);
+    const uint32_t a = desc_lo(smem + (second ? S::kTile : 0), true), done = bars + 8 * (second ? S::kR : S::kS);
+    const uint32_t ready = bars + 8 * (second ? S::kDs : S::kP);
+    const uint32_t rows_clear = bars + 8 * (second ? S::kClearO : S::kClearQ), sum_clear = bars + 8 * (second ? S::kClearQ : S::kClearO);
+    uint32_t rs = 0, rp = 0, ss = 0, sp = 0;   // stage and parity of the next tile of rows, and of the sum's
+    const auto rows_product = [&](int i) {      // [keys] x [queries]
+        if (!mbar_wait(rows_full + 8 * rs, rp, gave_up) || (ragged && i == w.n - 1 && !mbar_wait(rows_clear, 0, gave_up))) return false;
+        const uint32_t b = desc_lo(at_rows + rs * S::kTile, true);
 #pragma unroll
-        for (int s = 0; s < kRows / 16; ++s)
-            mma_tmem(d, a + (s >> 2) * 64 + (s & 3) * 8, desc_rows(b) + s * k_step(false), kDescHi, p.idesc_d, add || s > 0);
-    };
-    Ring<S::kStagesQ> q, q_sum;   // tiles for S, and for dK
-    Ring<S::kStagesO> o, o_sum;   // for R, and for dV
-    bool ok = mbar_wait(bars + 8 * S::kKV, 0, gave_up);
-    const auto scores = [&](int i) {
-        ok = mbar_wait(bars + 8 * (S::kQFull + q.s), q.parity, gave_up);
-        if (!ok) return;
-        const uint32_t at = smem + S::kAtQ + q.s * S::kTile;
-        if (live(i) < kRows) zero_rows<S::kChunks>(at, live(i), lane);
-        if (one) {
-            rows_product(tmem, smem, at);
-            mma_commit<false>(bars + 8 * S::kS);
+        for (uint32_t s = 0; s < DP / 16; ++s) {
+            const uint32_t at = (s >> 2) * (kBox >> 4) + (s & 3) * k_step(true);
+            if (s < steps) mma<false, false>(terms, a + at, kDescHi, b + at, kDescHi, p.idesc_s, s > 0);
         }
-        q.next();
+        mma_commit<false>(done);
+        mma_commit<false>(rows_empty + 8 * rs);
+        if (++rs == rows_stages) rs = 0, rp ^= 1;
+        return true;
     };
-    const auto reach = [&](int i) {
-        ok = mbar_wait(bars + 8 * (S::kOFull + o.s), o.parity, gave_up);
-        if (!ok) return;
-        const uint32_t at = smem + S::kAtO + o.s * S::kTile;
-        if (live(i) < kRows) zero_rows<S::kChunks>(at, live(i), lane);
-        if (one) {
-            rows_product(tmem + kTmemR, smem + S::kTile, at);
-            mma_commit<false>(bars + 8 * S::kR);
-        }
-        o.next();
-    };
-    if (ok) scores(0);
-    if (ok) reach(0);
-    for (int i = 0; ok && i < w.n; ++i) {
-        ok = mbar_wait(bars + 8 * S::kP, i & 1, gave_up);
-        if (!ok) break;
+    if (!mbar_wait(bars + 8 * S::kKV, 0, gave_up) || !rows_product(0)) return;
+    for (int i = 0; i < w.n; ++i) {
+        if (!mbar_wait(sum_full + 8 * ss, sp, gave_up) || (ragged && i == w.n - 1 && !mbar_wait(sum_clear, 0, gave_up))) return;
+        if (!mbar_wait(ready, i & 1, gave_up)) return;
         tc_fence_after();
-        if (one) {
-            sum_product(tmem + kTmemDv, tmem, smem + S::kAtO + o_sum.s * S::kTile, i > 0);
-            mma_commit<false>(bars + 8 * (S::kOEmpty + o_sum.s));
+        const uint32_t b = desc_rows(at_sum + ss * S::kTile);
+#pragma unroll
+        for (int s = 0; s < kRows / 16; ++s)   // halves of 64 queries, 32 columns each, 64 apart
+            mma_tmem(sum, terms + (s >> 2) * 64 + (s & 3) * 8, b + s * k_step(false), kDescHi, p.idesc_d, i > 0 || s > 0);
+        if (i + 1 < w.n) {
+            mma_commit<false>(sum_empty + 8 * ss);
+            if (!rows_product(i + 1)) return;
         }
-        o_sum.next();
-        if (i + 1 < w.n) scores(i + 1);
-        if (!ok) break;
-        ok = mbar_wait(bars + 8 * S::kDs, i & 1, gave_up);
-        if (!ok) break;
-        tc_fence_after();
-        if (one) {
-            sum_product(tmem + kTmemDv + DP, tmem + kTmemR, smem + S::kAtQ + q_sum.s * S::kTile, i > 0);
-            mma_commit<false>(bars + 8 * (S::kQEmpty + q_sum.s));
-        }
-        q_sum.next();
-        if (i + 1 < w.n) reach(i + 1);
+        if (++ss == sum_stages) ss = 0, sp ^= 1;
     }
-    if (one) {
-        mma_commit<false>(bars + 8 * S::kDone);
-        if (!mbar_wait_alone(bars + 8 * S::kDone, 0)) *gave_up = 1;
-    }
-    __syncwarp();
 }
 
 __device__ __forceinline__ float2 ld_shared_f2(uint32_t a)
@@ -391,7 +385,7 @@ __device__ __forceinline__ void key_terms(const Params& p, const KeyWork& w, int
             mbar_arrive(bars + 8 * (S::kStatEmpty + rs.s));
         }
     }
-    if (w.n > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * S::kDone, 0, gave_up));
+    if (w.n > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (S::kDone + half), 0, gave_up));
     if (!ok) return;
     tc_fence_after();
     // the first warps write dV, the others dK
@@ -431,7 +425,9 @@ __global__ void __launch_bounds__(kThreads, 1) keys_kernel(const __grid_constant
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kBars; ++i)
-            mbar_init(bars + 8 * i, i == S::kP || i == S::kDs || (i >= S::kStatEmpty && i < S::kS) ? 8 : 1);
+            mbar_init(bars + 8 * i, i == S::kP || i == S::kDs || (i >= S::kStatEmpty && i < S::kS)                ? 8
+                                    : (i >= S::kQEmpty && i < S::kOFull) || (i >= S::kOEmpty && i < S::kStatFull) ? 2
+                                                                                                                  : 1);
         *gave_up = 0;
         mbar_init_fence();
     }
@@ -443,6 +439,9 @@ __global__ void __launch_bounds__(kThreads, 1) keys_kernel(const __grid_constant
     KeyWork w;
     if (!find_keys(p, w)) return;   // the same for every warp
     if (warp == 9) tmem_alloc<false>(smem_addr(tmem_slot), kTmemCols);
+    const int packed = p.tokens * p.group;
+    if (packed < kRows && w.n > 0)   // rows that no copy writes
+        for (int t = warp; t < S::kStagesQ + S::kStagesO; t += kThreads / 32) zero_rows<S::kChunks>(smem + S::kAtQ + t * S::kTile, packed, lane);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -450,10 +449,16 @@ __global__ void __launch_bounds__(kThreads, 1) keys_kernel(const __grid_constant
     if (warp >= 8) {
         few_registers();
         if (warp == 8) {
-            if (w.n > 0 && elect_one()) load_queries<DP>(p, w, smem, bars, gave_up);
-            __syncwarp();
-        } else if (warp == 9 && w.n > 0)
-            issue_keys<DP>(p, w, smem, bars, tmem, lane, gave_up);
+            if (w.n > 0) {
+                if (elect_one()) load_queries<DP>(p, w, smem, bars, gave_up);
+                __syncwarp();
+                clear_queries<DP>(p, w, smem, bars, lane, gave_up);
+            }
+        } else if (warp < 11 && elect_one()) {
+            if (w.n > 0) issue_keys<DP>(p, w, warp == 10, smem, bars, tmem, gave_up);
+            mma_commit<false>(bars + 8 * (S::kDone + warp - 9));   // the block does not leave before its products are done
+            if (!mbar_wait_alone(bars + 8 * (S::kDone + warp - 9), 0)) *gave_up = 1;
+        }
     } else {
         many_registers();
         const int exponent = ds_exponent<T>(p);
@@ -478,7 +483,7 @@ struct QueryShape {
     static constexpr int kStages = DP == 128 ? 3 : 6;   // keys and values in turn
     static constexpr uint32_t kAtRing = 4 * kTile, kAtBars = kAtRing + kStages * kTile;
     static constexpr int kQFull = 0, kFull = 2, kEmpty = kFull + kStages, kS = kEmpty + kStages, kP = kS + 2, kR = kP + 2, kDs = kR + 2,
-                         kDone = kDs + 2, kBars = kDone + 1;
+                         kClear = kDs + 2, kDone = kClear + 1, kBars = kDone + 2;
     static constexpr int kSmem = kAtBars + ((kBars * 8 + 15) & ~15) + 16;
     static_assert(kSmem <= 232448, "shared memory of an SM");
 };
@@ -537,90 +542,80 @@ __device__ __forceinline__ void load_keys(const Params& p, const QueryWork& w, i
     last_copies<S::kStages>(issued, [&](uint32_t s, uint32_t parity) { landed = landed && mbar_wait_alone(bars + 8 * (S::kFull + s), parity); });
 }
 
-// Tile of keys j: R of both tiles of queries once their P is in registers, then dQ of each
-// once its dS is written, and right after it the next scores in dS's place.
+// Keys behind the sequence are contracted over in dQ: zero, by the loading warp, once all
+// copies are under way.
 template <int DP>
-__device__ __forceinline__ void issue_queries(const Params& p, const QueryWork& w, int n, uint32_t smem, uint32_t bars, uint32_t tmem,
-                                              int lane, volatile int* gave_up)
+__device__ __forceinline__ void clear_keys(const QueryWork& w, int n, uint32_t smem, uint32_t bars, int lane, volatile int* gave_up)
 {
     using S = QueryShape<DP>;
-    const bool one = elect_one();
-    const int steps = (p.dim + 15) / 16;
-    const auto rows_product = [&](uint32_t d, uint32_t a, uint32_t b) {
-        for (int s = 0; s < steps; ++s) {
-            const uint32_t at = (uint32_t)(s >> 2) * (kBox >> 4) + (uint32_t)(s & 3) * k_step(true);
-            mma<false, false>(d, desc_lo(a, true) + at, kDescHi, desc_lo(b, true) + at, kDescHi, p.idesc_s, s > 0);
+    const int live = w.seq.lk - (n - 1) * kRows;
+    if (live >= kRows || *gave_up) return;
+    const uint32_t copy = 2 * n - 2;
+    if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * (S::kFull + copy % S::kStages), copy / S::kStages & 1, gave_up))) return;
+    zero_rows<S::kChunks>(smem + S::kAtRing + copy % S::kStages * S::kTile, live, lane);
+    if (lane == 0) mbar_arrive(bars + 8 * S::kClear);
+}
+
+// A lane issues the products of tile i: R(j) once P(j) is in registers, dQ(j) once dS(j) is
+// written and, right behind it, S(j + 1) in dS's place.
+template <int DP>
+__device__ __forceinline__ void issue_queries(const Params& p, const QueryWork& w, int i, int n, uint32_t smem, uint32_t bars, uint32_t tmem,
+                                              volatile int* gave_up)
+{
+    using S = QueryShape<DP>;
+    const int mine = i ? w.n[1] : w.n[0];
+    const uint32_t steps = (uint32_t)(p.dim + 15) / 16, here = tmem + i * 128;
+    const bool ragged = w.seq.lk < n * kRows;
+    const auto rows_product = [&](uint32_t at_a, uint32_t at_b) {
+        const uint32_t a = desc_lo(at_a, true), b = desc_lo(at_b, true);
+#pragma unroll
+        for (uint32_t s = 0; s < DP / 16; ++s) {
+            const uint32_t at = (s >> 2) * (kBox >> 4) + (s & 3) * k_step(true);
+            if (s < steps) mma<false, false>(here, a + at, kDescHi, b + at, kDescHi, p.idesc_s, s > 0);
         }
     };
+    const auto landed = [&](const Ring<S::kStages>& r) { return mbar_wait(bars + 8 * (S::kFull + r.s), r.parity, gave_up); };
     Ring<S::kStages> ring;
-    bool ok = mbar_wait(bars + 8 * (S::kFull + ring.s), ring.parity, gave_up);
-    uint32_t keys = ring.s;
-    ring.next();
-    const auto clear = [&](int j) {   // keys behind the sequence are contracted over in dQ: zero
-        const int live = w.seq.lk - j * kRows;
-        if (live < kRows) zero_rows<S::kChunks>(smem + S::kAtRing + keys * S::kTile, live, lane);
-    };
-    if (ok) clear(0);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (ok && w.n[i] > 0) {
-            ok = mbar_wait(bars + 8 * (S::kQFull + i), 0, gave_up);
-            if (ok && one) {
-                rows_product(tmem + i * 128, smem + 2 * i * S::kTile, smem + S::kAtRing + keys * S::kTile);
-                mma_commit<false>(bars + 8 * (S::kS + i));
-            }
-        }
-    for (int j = 0; ok && j < n; ++j) {
-        const uint32_t values = ring.s, k_at = smem + S::kAtRing + keys * S::kTile;
-        ok = mbar_wait(bars + 8 * (S::kFull + ring.s), ring.parity, gave_up);
+    uint32_t keys = 0;
+    if (mine > 0) {
+        if (!mbar_wait(bars + 8 * (S::kQFull + i), 0, gave_up) || !landed(ring)) return;
+        if (ragged && n == 1 && !mbar_wait(bars + 8 * S::kClear, 0, gave_up)) return;
+        rows_product(smem + 2 * i * S::kTile, smem + S::kAtRing);
+        mma_commit<false>(bars + 8 * (S::kS + i));
         ring.next();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (!ok || j >= w.n[i]) continue;
-            ok = mbar_wait(bars + 8 * (S::kP + i), j & 1, gave_up);
-            if (!ok) continue;
-            tc_fence_after();
-            if (one) {
-                rows_product(tmem + i * 128, smem + (2 * i + 1) * S::kTile, smem + S::kAtRing + values * S::kTile);
-                mma_commit<false>(bars + 8 * (S::kR + i));
-            }
-        }
-        if (!ok) break;
-        if (one) mma_commit<false>(bars + 8 * (S::kEmpty + values));
-        const uint32_t old = keys;
-        bool more = false;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (!ok || j >= w.n[i]) continue;
-            ok = mbar_wait(bars + 8 * (S::kDs + i), j & 1, gave_up);
-            if (!ok) continue;
-            tc_fence_after();
-            if (one)
-#pragma unroll
-                for (int s = 0; s < kRows / 16; ++s)
-                    mma_tmem(tmem + kTmemDq + i * DP, tmem + i * 128 + s * 8, desc_rows(k_at) + s * k_step(false), kDescHi, p.idesc_d,
-                             j > 0 || s > 0);
-            if (j + 1 < w.n[i]) {
-                if (!more) {
-                    more = true;
-                    keys = ring.s;
-                    ok = mbar_wait(bars + 8 * (S::kFull + ring.s), ring.parity, gave_up);
-                    ring.next();
-                    if (ok) clear(j + 1);
-                }
-                if (ok && one) {
-                    rows_product(tmem + i * 128, smem + 2 * i * S::kTile, smem + S::kAtRing + keys * S::kTile);
-                    mma_commit<false>(bars + 8 * (S::kS + i));
-                }
-            }
-        }
-        if (ok && one) mma_commit<false>(bars + 8 * (S::kEmpty + old));
     }
-    if (one) {
-        mma_commit<false>(bars + 8 * S::kDone);
-        if (!mbar_wait_alone(bars + 8 * S::kDone, 0)) *gave_up = 1;
+    for (int j = 0; j < mine; ++j) {
+        const uint32_t values = ring.s;
+        if (!landed(ring) || !mbar_wait(bars + 8 * (S::kP + i), j & 1, gave_up)) return;
+        tc_fence_after();
+        rows_product(smem + (2 * i + 1) * S::kTile, smem + S::kAtRing + values * S::kTile);
+        mma_commit<false>(bars + 8 * (S::kR + i));
+        mma_commit<false>(bars + 8 * (S::kEmpty + values));
+        ring.next();
+        const bool more = j + 1 < mine;
+        const uint32_t next = ring.s;
+        if (more && !landed(ring)) return;
+        if (!mbar_wait(bars + 8 * (S::kDs + i), j & 1, gave_up)) return;
+        tc_fence_after();
+        const uint32_t b = desc_rows(smem + S::kAtRing + keys * S::kTile);
+#pragma unroll
+        for (int s = 0; s < kRows / 16; ++s)
+            mma_tmem(tmem + kTmemDq + i * DP, here + s * 8, b + s * k_step(false), kDescHi, p.idesc_d, j > 0 || s > 0);
+        mma_commit<false>(bars + 8 * (S::kEmpty + keys));
+        if (more) {
+            // not before: the rows are cleared behind the last copy, which may want these keys' stage
+            if (ragged && j + 2 == n && !mbar_wait(bars + 8 * S::kClear, 0, gave_up)) return;
+            rows_product(smem + 2 * i * S::kTile, smem + S::kAtRing + next * S::kTile);
+            mma_commit<false>(bars + 8 * (S::kS + i));
+            ring.next();
+        }
+        keys = next;
     }
-    __syncwarp();
+    // copies that only the other tile reads: both lanes free a stage
+    for (int c = 2 * mine; c < 2 * n; ++c, ring.next()) {
+        if (!landed(ring)) return;
+        mbar_arrive(bars + 8 * (S::kEmpty + ring.s));
+    }
 }
 
 // A row a thread: i the tile, r the row.
@@ -680,7 +675,7 @@ __device__ __forceinline__ void query_terms(const Params& p, const QueryWork& w,
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(bars + 8 * (S::kDs + i));
     }
-    if (n > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * S::kDone, 0, gave_up));
+    if (n > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (S::kDone + i), 0, gave_up));
     if (!ok) return;
     tc_fence_after();
     const float by = p.scale * power2(-exponent);
@@ -717,8 +712,8 @@ __global__ void __launch_bounds__(kThreads, 1) queries_kernel(const __grid_const
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kBars; ++i) {
-            const bool warps = (i >= S::kP && i < S::kR) || (i >= S::kDs && i < S::kDone);
-            mbar_init(bars + 8 * i, warps ? 4 : 1);
+            const bool warps = (i >= S::kP && i < S::kR) || (i >= S::kDs && i < S::kClear);
+            mbar_init(bars + 8 * i, warps ? 4 : (i >= S::kEmpty && i < S::kS ? 2 : 1));
         }
         *gave_up = 0;
         mbar_init_fence();
@@ -736,10 +731,16 @@ __global__ void __launch_bounds__(kThreads, 1) queries_kernel(const __grid_const
     if (warp >= 8) {
         few_registers();
         if (warp == 8) {
-            if (n > 0 && elect_one()) load_keys<DP>(p, w, n, smem, bars, gave_up);
-            __syncwarp();
-        } else if (warp == 9 && n > 0)
-            issue_queries<DP>(p, w, n, smem, bars, tmem, lane, gave_up);
+            if (n > 0) {
+                if (elect_one()) load_keys<DP>(p, w, n, smem, bars, gave_up);
+                __syncwarp();
+                clear_keys<DP>(w, n, smem, bars, lane, gave_up);
+            }
+        } else if (warp < 11 && elect_one()) {
+            issue_queries<DP>(p, w, warp - 9, n, smem, bars, tmem, gave_up);
+            mma_commit<false>(bars + 8 * (S::kDone + warp - 9));   // the block does not leave before its products are done
+            if (!mbar_wait_alone(bars + 8 * (S::kDone + warp - 9), 0)) *gave_up = 1;
+        }
     } else {
         many_registers();
         const int i = warp >> 2, exponent = ds_exponent<T>(p);
@@ -775,7 +776,7 @@ Plan plan_for(const gs_attention_bwd_args& a)
     r.stat_pitch = round_up(a.q_rows * r.group, 2);
     // the last copy of statistics reads up to a tile past the last row
     r.stats = (size_t)round_up((a.kv_heads * r.stat_pitch + kStatRows) * 8, 256);
-    const int64_t want = (a.q_rows * a.heads + 7) / 8, most = sms * (a.type == GS_F16 ? 2 : 8);
+    const int64_t want = (a.q_rows * a.heads + 31) / 32, most = sms * (a.type == GS_F16 ? 2 : 8);
     r.blocks = (int)(want < 1 ? 1 : (want < most ? want : most));
     r.most = a.type == GS_F16 ? (size_t)round_up(r.blocks * 8, 256) : 0;
     if (!tensor_tma(a.q, a.q_row, a.q_head, a.q_rows, a.heads)) r.packs += packed_bytes(a.q_rows, a.heads, a.dim);
@@ -873,9 +874,12 @@ extern "C" gs_status gs_attention_bwd(const gs_attention_bwd_args* args, void* w
         t.lse = a.lse, t.stats = stats, t.most = most, t.q_rows = a.q_rows, t.k_rows = a.k_rows, t.stat_pitch = plan.stat_pitch;
         t.heads = a.heads, t.kv_heads = a.kv_heads, t.group = plan.group, t.dim = a.dim;
         t.vec = a.dim % 8 == 0 && tensor_tma(a.o, a.o_row, a.o_head, a.q_rows, a.heads) &&
-                tensor_tma(a.d_o, a.do_row, a.do_head, a.q_rows, a.heads);
-        s = a.type == GS_BF16 ? launch_after(stats_kernel<GS_BF16>, dim3((unsigned)plan.blocks), 256, 0, 1, st, t)
-                              : launch_after(stats_kernel<GS_F16>, dim3((unsigned)plan.blocks), 256, 0, 1, st, t);
+                tensor_tma(a.d_o, a.do_row, a.do_head, a.q_rows, a.heads) &&
+                (!most || tensor_tma(a.v, a.v_row, a.v_head, a.k_rows, a.kv_heads));
+        const auto run = [&](auto kernel) { return launch_after(kernel, dim3((unsigned)plan.blocks), 256, 0, 1, st, t); };
+        if (a.type == GS_BF16)
+            s = a.dim > 64 ? run(stats_kernel<GS_BF16, 16>) : a.dim > 32 ? run(stats_kernel<GS_BF16, 8>) : run(stats_kernel<GS_BF16, 4>);
+        else s = a.dim > 64 ? run(stats_kernel<GS_F16, 16>) : a.dim > 32 ? run(stats_kernel<GS_F16, 8>) : run(stats_kernel<GS_F16, 4>);
         if (s != GS_OK) return s;
     }
     p.seqs = {a.q_starts, a.k_starts, nullptr, a.q_rows, a.k_rows, (uint32_t)a.sequences};
