@@ -21,6 +21,7 @@
 // then split over several CTAs, whose sums and maxima join_kernel puts together in a
 // fixed order.
 #include <atomic>
+#include <cmath>
 
 #include "attention.cuh"
 
@@ -28,19 +29,21 @@ namespace gs {
 namespace attn {
 namespace {
 
-constexpr int kTmemCols = 512, kTmemO = 256;
 constexpr float kRaise = 8.0f;   // log2
 
-template <int DP>
+// TILES: of a CTA.  With one, two CTAs share an SM.
+template <int DP, int TILES>
 struct Shape {
     static constexpr int kChunks = DP / 64;
     static constexpr uint32_t kTile = kChunks * kBox;
-    static constexpr int kStages = DP == 128 ? 5 : 8;
-    static constexpr uint32_t kAtRing = 2 * kTile, kAtBars = kAtRing + kStages * kTile;
+    static constexpr int kStages = TILES == 1 ? (DP == 128 ? 2 : 5) : (DP == 128 ? 5 : 8);
+    static constexpr int kSoftmaxWarps = 4 * TILES, kThreads = (kSoftmaxWarps + 4) * 32;
+    static constexpr uint32_t kTmemCols = 256 * TILES, kTmemO = 128 * TILES;
+    static constexpr uint32_t kAtRing = TILES * kTile, kAtBars = kAtRing + kStages * kTile;
     static constexpr int kQFull = 0, kFull = 2, kEmpty = kFull + kStages, kScores = kEmpty + kStages, kTerms = kScores + 2,
                          kSums = kTerms + 4, kClear = kSums + 2, kDone = kClear + 1, kBars = kDone + 2;
     static constexpr int kSmem = kAtBars + ((kBars * 8 + 15) & ~15) + 16;
-    static_assert(kSmem <= 232448, "shared memory of an SM");
+    static_assert(kSmem <= 232448 / (3 - TILES) - (2 - TILES) * 1024, "shared memory of an SM");
 };
 
 struct Params {
@@ -50,11 +53,10 @@ struct Params {
     uint16_t* o;
     int64_t o_row, o_head;
     float* lse;
-    float* part;          // splits > 1: [item][rows of a tile][DP] sums of p v, then their (maximum, sum of p)
-    float2* part_stats;
+    float* part;          // splits > 1: [split][q row][head][DP] sums of p v
+    float2* part_stats;   // [split][q row][head] their maxima and sums of p
     float scale2;         // scale log2(e)
     uint32_t splits, kv_heads;
-    int tiles;            // of a unit: 1 or 2
     int group, tokens;    // query heads of a key head, tokens of a tile
     int dim, o_vec, causal, zero;
     uint32_t idesc_s, idesc_o;
@@ -65,20 +67,21 @@ __device__ int g_attention_wait_expired;
 // A CTA's work: a unit of one or two tiles of a key head, and its part of the keys' tiles.
 struct Work {
     Sequence seq;
-    uint32_t item, head;
+    uint32_t split, head;
     int t0;            // the first token of the unit
     int from;          // the first tile of keys
     int n[2];          // tiles of keys from there for either tile of the unit
 };
 
+template <int TILES>
 __device__ __forceinline__ bool find_work(const Params& p, Work& w)
 {
-    const uint32_t split = blockIdx.x % p.splits, rest = blockIdx.x / p.splits;
+    const uint32_t rest = blockIdx.x / p.splits;
+    w.split = blockIdx.x % p.splits;
     w.head = rest % p.kv_heads;
     uint32_t unit, units;
-    const int tokens = p.tokens * p.tiles;
+    const int tokens = p.tokens * TILES;
     if (!find_unit<false>(p.seqs, rest / p.kv_heads, tokens, w.seq, unit, units)) return false;
-    w.item = blockIdx.x;
     if (p.causal) unit = units - 1 - unit;   // the longest first
     w.t0 = (int)unit * tokens;
     int tiles[2];
@@ -87,11 +90,11 @@ __device__ __forceinline__ bool find_work(const Params& p, Work& w)
         const int t = w.t0 + i * p.tokens;
         int last = t + p.tokens - 1;
         last = last < w.seq.lq ? last : w.seq.lq - 1;
-        tiles[i] = i < p.tiles && t < w.seq.lq ? (keys_seen(w.seq, last, p.causal) + kRows - 1) / kRows : 0;
+        tiles[i] = i < TILES && t < w.seq.lq ? (keys_seen(w.seq, last, p.causal) + kRows - 1) / kRows : 0;
     }
     const int most = tiles[0] > tiles[1] ? tiles[0] : tiles[1];
     const int each = (most + (int)p.splits - 1) / (int)p.splits;
-    w.from = (int)split * each;
+    w.from = (int)w.split * each;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         int n = tiles[i] - w.from;
@@ -101,13 +104,13 @@ __device__ __forceinline__ bool find_work(const Params& p, Work& w)
     return true;
 }
 
-template <int DP>
+template <int DP, int TILES>
 __device__ __forceinline__ void load(const Params& p, const Work& w, int n, uint32_t smem, uint32_t bars, volatile int* gave_up)
 {
-    using S = Shape<DP>;
+    using S = Shape<DP, TILES>;
     const uint32_t q_bytes = (uint32_t)(S::kChunks * p.tokens * p.group) * 128;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < TILES; ++i)
         if (w.n[i] > 0) {
             mbar_expect(bars + 8 * (S::kQFull + i), q_bytes);
             load_tile<S::kChunks>(smem + i * S::kTile, &p.q, w.head * p.group, w.seq.q0 + w.t0 + i * p.tokens, bars + 8 * (S::kQFull + i));
@@ -124,19 +127,19 @@ __device__ __forceinline__ void load(const Params& p, const Work& w, int n, uint
     // the block does not leave before its copies have landed
     bool landed = true;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) landed = landed && (w.n[i] == 0 || mbar_wait_alone(bars + 8 * (S::kQFull + i), 0));
+    for (int i = 0; i < TILES; ++i) landed = landed && (w.n[i] == 0 || mbar_wait_alone(bars + 8 * (S::kQFull + i), 0));
     last_copies<S::kStages>(issued, [&](uint32_t s, uint32_t parity) { landed = landed && mbar_wait_alone(bars + 8 * (S::kFull + s), parity); });
 }
 
 // A lane issues the products of tile i.  (Of both tiles in turn one lane is too slow: each
 // of its waits takes some 350 cycles beside products whose factors come from shared memory,
 // 900 TFLOP/s where two lanes reach 1,100.)
-template <int DP>
+template <int DP, int TILES>
 __device__ __forceinline__ void issue(const Params& p, const Work& w, int i, int n, uint32_t smem, uint32_t bars, uint32_t tmem, volatile int* gave_up)
 {
-    using S = Shape<DP>;
+    using S = Shape<DP, TILES>;
     const int mine = i ? w.n[1] : w.n[0];
-    const uint32_t steps = (uint32_t)(p.dim + 15) / 16, score = tmem + i * 128, sum = tmem + kTmemO + i * DP;
+    const uint32_t steps = (uint32_t)(p.dim + 15) / 16, score = tmem + i * 128, sum = tmem + S::kTmemO + i * DP;
     const bool ragged = w.seq.lk < (w.from + n) * kRows;
     const auto scores = [&](uint32_t tile) {
         const uint32_t a = desc_lo(smem + i * S::kTile, true), b = desc_lo(tile, true);
@@ -188,10 +191,10 @@ __device__ __forceinline__ void issue(const Params& p, const Work& w, int i, int
 // The rows of the last values that are behind the sequence, other sequences' perhaps: zero,
 // for the product contracts over them.  By the loading warp, once all copies are under way
 // (no stage is filled again, so the barrier's parity tells the last copy).
-template <int DP>
+template <int DP, int TILES>
 __device__ __forceinline__ void clear_values(const Work& w, int n, uint32_t smem, uint32_t bars, int lane, volatile int* gave_up)
 {
-    using S = Shape<DP>;
+    using S = Shape<DP, TILES>;
     const int live = w.seq.lk - (w.from + n - 1) * kRows;
     if (live >= kRows || *gave_up) return;
     const uint32_t copy = 2 * n - 1;
@@ -201,16 +204,16 @@ __device__ __forceinline__ void clear_values(const Work& w, int n, uint32_t smem
 }
 
 // A row a thread: i the tile, r the row.
-template <int T, int DP>
+template <int T, int DP, int TILES>
 __device__ __forceinline__ void softmax(const Params& p, const Work& w, int i, int r, uint32_t bars, uint32_t tmem, volatile int* gave_up)
 {
-    using S = Shape<DP>;
+    using S = Shape<DP, TILES>;
     const int n = i ? w.n[1] : w.n[0], t0 = w.t0 + i * p.tokens;
     const int token = t0 + r / p.group, head = (int)w.head * p.group + r % p.group;
     const bool live = r < p.tokens * p.group && token < w.seq.lq;
     const int seen = keys_seen(w.seq, token, p.causal);                 // this row's keys
     const int all = keys_seen(w.seq, t0, p.causal);                     // every row's
-    const uint32_t scores = tmem + i * 128, sums = tmem + kTmemO + i * DP;
+    const uint32_t scores = tmem + i * 128, sums = tmem + S::kTmemO + i * DP;
     float m = -INFINITY;
     uint64_t l2[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
     bool ok = true;
@@ -288,7 +291,7 @@ __device__ __forceinline__ void softmax(const Params& p, const Work& w, int i, i
     const float l = (la.x + la.y) + (lb.x + lb.y);
     const int64_t row = w.seq.q0 + token;
     if (p.splits > 1) {
-        const int64_t at = (int64_t)w.item * (p.tokens * p.group) + r;
+        const int64_t at = ((int64_t)w.split * p.seqs.q_rows + row) * (p.group * p.kv_heads) + head;
         if (live) p.part_stats[at] = make_float2(m, l);
         if (n == 0) return;
         float* to = p.part + at * DP;
@@ -323,10 +326,10 @@ __device__ __forceinline__ void softmax(const Params& p, const Work& w, int i, i
     tc_fence_before();
 }
 
-template <int T, int DP>
-__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ Params p)
+template <int T, int DP, int TILES>
+__global__ void __launch_bounds__(Shape<DP, TILES>::kThreads, 3 - TILES) attention_kernel(const __grid_constant__ Params p)
 {
-    using S = Shape<DP>;
+    using S = Shape<DP, TILES>;
     extern __shared__ __align__(1024) char smem_raw[];
     const uint32_t smem = smem_addr(smem_raw);
     if (smem & 1023u) {   // every thread sees the same address; there is no padding to move within
@@ -340,76 +343,76 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < S::kBars; ++i) mbar_init(bars + 8 * i, i >= S::kTerms && i < S::kSums ? 4 : (i >= S::kEmpty && i < S::kScores ? 2 : 1));
+        for (int i = 0; i < S::kBars; ++i)
+            mbar_init(bars + 8 * i, i >= S::kTerms && i < S::kSums ? 4 : (i >= S::kEmpty && i < S::kScores ? TILES : 1));
         *gave_up = 0;
         mbar_init_fence();
     }
     wait_for_predecessor();
     if (p.zero) fill_rows(p.fill, p.seqs.q_starts, p.seqs.count, p.seqs.q_rows);
     Work w;
-    if (!find_work(p, w)) return;   // the same for every warp
-    if (warp == 9) tmem_alloc<false>(smem_addr(tmem_slot), kTmemCols);
+    if (!find_work<TILES>(p, w)) return;   // the same for every warp
+    if (warp == S::kSoftmaxWarps) tmem_alloc<false>(smem_addr(tmem_slot), S::kTmemCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int n = w.n[0] > w.n[1] ? w.n[0] : w.n[1];
 
-    if (warp >= 8) {
+    if (warp >= S::kSoftmaxWarps) {
         few_registers();
-        if (warp == 8) {
+        const int i = warp - S::kSoftmaxWarps - 1;
+        if (i < 0) {
             if (n > 0) {
-                if (elect_one()) load<DP>(p, w, n, smem, bars, gave_up);
+                if (elect_one()) load<DP, TILES>(p, w, n, smem, bars, gave_up);
                 __syncwarp();
-                clear_values<DP>(w, n, smem, bars, lane, gave_up);
+                clear_values<DP, TILES>(w, n, smem, bars, lane, gave_up);
             }
-        } else if (warp < 11) {
-            const int i = warp - 9;
-            if (elect_one()) {
-                issue<DP>(p, w, i, n, smem, bars, tmem, gave_up);
-                mma_commit<false>(bars + 8 * (S::kDone + i));   // the block does not leave before its products are done
-                if (!mbar_wait_alone(bars + 8 * (S::kDone + i), 0)) *gave_up = 1;
-            }
+        } else if (i < TILES && elect_one()) {
+            issue<DP, TILES>(p, w, i, n, smem, bars, tmem, gave_up);
+            mma_commit<false>(bars + 8 * (S::kDone + i));   // the block does not leave before its products are done
+            if (!mbar_wait_alone(bars + 8 * (S::kDone + i), 0)) *gave_up = 1;
         }
     } else {
-        many_registers();
+        many_registers<TILES == 2 ? 224 : 200>();
         const int i = warp >> 2, r = threadIdx.x & 127;
-        if (i < p.tiles && w.t0 + i * p.tokens < w.seq.lq)
-            softmax<T, DP>(p, w, i, r, bars, tmem + ((uint32_t)((warp & 3) * 32) << 16), gave_up);
+        if (w.t0 + i * p.tokens < w.seq.lq)
+            softmax<T, DP, TILES>(p, w, i, r, bars, tmem + ((uint32_t)((warp & 3) * 32) << 16), gave_up);
     }
     __syncthreads();
     if (threadIdx.x == 0 && *gave_up) atomicExch(&g_attention_wait_expired, 1);
-    if (warp == 9) {
+    if (warp == S::kSoftmaxWarps) {
         tc_fence_after();
-        tmem_free<false>(tmem, kTmemCols);
+        tmem_free<false>(tmem, S::kTmemCols);
     }
 }
 
-// The parts of a row's keys: o = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s.  A warp a row.
+// The parts of a row's keys: o = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s.  A block a
+// row: its warps take the parts in turn, their sums are added in order.  (A warp a row waited
+// for one part after the other: 20 us for 33 of them, 4 so.)
+constexpr int kJoinWarps = 8;
 template <int T, int DP>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ Params p)
 {
+    __shared__ float sums[kJoinWarps][DP + 1];
     wait_for_predecessor();
-    Sequence seq;
-    uint32_t unit, units;
-    const uint32_t head = blockIdx.x % p.kv_heads;
-    if (!find_unit<false>(p.seqs, blockIdx.x / p.kv_heads, p.tokens, seq, unit, units)) return;
-    if (p.causal) unit = units - 1 - unit;
-    const int r = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31, used = p.tokens * p.group;
-    const int token = (int)unit * p.tokens + r / p.group;
-    if (r >= used || token >= seq.lq) return;
-    const int64_t first = (int64_t)blockIdx.x * p.splits * used + r;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t heads = p.group * p.kv_heads, all = p.seqs.q_rows * heads, row = blockIdx.x / heads;
+    if (p.seqs.q_starts && (row < p.seqs.q_starts[0] || row >= p.seqs.q_starts[p.seqs.count])) return;   // of no sequence
+    const float2* stats = p.part_stats + blockIdx.x;
+    const float* part = p.part + (int64_t)blockIdx.x * DP;
     float m = -INFINITY;
-    for (uint32_t s = lane; s < p.splits; s += 32) m = fmaxf(m, p.part_stats[first + (int64_t)s * used].x);
+    for (uint32_t s = lane; s < p.splits; s += 32) m = fmaxf(m, stats[s * all].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     constexpr int kPer = DP / 32;
     float l = 0.0f, v[kPer] = {};
-    for (uint32_t s = 0; s < p.splits; ++s) {
-        const float2 st = p.part_stats[first + (int64_t)s * used];
+#pragma unroll 4
+    for (uint32_t s = warp; s < p.splits; s += kJoinWarps) {
+        const float2 st = stats[s * all];
         if (st.y == 0.0f) continue;   // no key of this part is seen; of no keys at all there is nothing to read
         const float by = exp2_fast(st.x - m);
-        const float* from = p.part + (first + (int64_t)s * used) * DP + lane * kPer;
+        const float* from = part + s * all * DP + lane * kPer;
         l = __fmaf_rn(by, st.y, l);
         float t[kPer];
         if constexpr (kPer == 4) *reinterpret_cast<float4*>(t) = *reinterpret_cast<const float4*>(from);
@@ -417,15 +420,18 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Param
 #pragma unroll
         for (int e = 0; e < kPer; ++e) v[e] = __fmaf_rn(by, t[e], v[e]);
     }
-    const int64_t row = seq.q0 + token;
-    const int h = (int)head * p.group + r % p.group;
-    const bool none = l == 0.0f;
-    if (lane == 0 && p.lse) p.lse[row * (p.group * p.kv_heads) + h] = none ? -INFINITY : (m + log2f(l)) * kLn2;
-    const float by = none ? 0.0f : 1.0f / l;
-    uint16_t* to = p.o + row * p.o_row + h * p.o_head + lane * kPer;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e)
-        if (lane * kPer + e < p.dim) store_elem(to, e, T, v[e] * by);
+    for (int e = 0; e < kPer; ++e) sums[warp][lane * kPer + e] = v[e];
+    if (lane == 0) sums[warp][DP] = l;
+    __syncthreads();
+    const int c = threadIdx.x;
+    if (c > DP) return;
+    float total = 0.0f, mine = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) total += sums[w][DP], mine += sums[w][c];
+    const bool none = total == 0.0f;
+    if (c == DP && p.lse) p.lse[blockIdx.x] = none ? -INFINITY : (m + log2f(total)) * kLn2;
+    if (c < p.dim) store_elem(p.o + row * p.o_row + (blockIdx.x - row * heads) * p.o_head, c, T, none ? 0.0f : mine / total);
 }
 
 __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackList p)
@@ -509,20 +515,39 @@ Plan plan_for(const gs_attention_args& a)
     const bool starts = a.q_starts != nullptr;
     const int64_t one = units_at_most(a.q_rows, a.sequences, starts, r.tokens);
     const int64_t two = units_at_most(a.q_rows, a.sequences, starts, 2 * (int64_t)r.tokens);
-    // two tiles a CTA where there are CTAs enough all the same, and tokens for both
-    r.tiles = two * a.kv_heads >= sms && a.q_rows > a.sequences * r.tokens ? 2 : 1;
+    const int64_t sequences = a.sequences > 0 ? a.sequences : 1, keys = a.k_rows / sequences;
+    // Two tiles a CTA read their keys once; two CTAs an SM hide each other's first and last
+    // steps, and for 64 columns and fewer, where the softmax bounds both, each other's
+    // barriers.  us with one and two: 8192 tokens of 64 causal 162, 185; 24 sequences of up to
+    // 1024 56, 66; of 128: 64 x 512 151, 163; 16 x 2048 293, 310; 4099 69, 69; 16384 463, 416.
+    r.tiles = r.dp == 128 && keys >= 4096 && a.q_rows > sequences * r.tokens && two * a.kv_heads >= sms ? 2 : 1;
     r.units = r.tiles == 2 ? two : one;
     r.splits = 1;
-    const int64_t ctas = r.units * a.kv_heads, key_tiles = (a.k_rows / (a.sequences ? a.sequences : 1) + kRows - 1) / kRows;
-    if (r.tiles == 1 && ctas < 2 * sms && key_tiles > 1) {
-        int64_t s = ctas < sms ? sms / ctas : 4 * sms / ctas;
-        if (s > key_tiles) s = key_tiles;
-        r.splits = (uint32_t)s;
+    const int64_t ctas = r.units * a.kv_heads, key_tiles = (keys + kRows - 1) / kRows;
+    const int64_t rows = ((a.q_rows + sequences - 1) / sequences < r.tokens ? (a.q_rows + sequences - 1) / sequences : r.tokens) * r.group;
+    if (r.tiles == 1 && key_tiles > 1 && (ctas < sms || rows <= 32) && a.q_rows * a.heads <= 0x7fffffffll) {
+        // Parts of the keys: what they save in waiting, of a CTA alone (1.4 us a tile of keys) or
+        // for the last one (a third of its share of HBM's time), against a wave's start and end
+        // and the parts' sums.  us by parts: 1 token against 4097 keys 39 (1), 13 (8), 11 (32), 65536
+        // keys 765 (1), 22 (64); 32 tokens against up to 16384 keys 306 (1), 251 (4), 244 (8),
+        // 264 (24); 64 against up to 2000 82 (1), 88 (2).
+        const double slots = 2.0 * sms, tile_bytes = 512.0 * r.dp, byte_us = 1.0 / 6.5e6;
+        double best = 0;
+        for (int64_t s = 1; s <= key_tiles && s <= 256; ++s) {
+            const int64_t each = (key_tiles + s - 1) / s;
+            if (s > 1 && (key_tiles + s - 2) / (s - 1) == each) continue;   // fewer parts are as long
+            const double waves = std::ceil((double)(ctas * s) / slots), busy = (double)(ctas * s) < slots ? (double)(ctas * s) : slots;
+            const double tile_us = 1.4 > tile_bytes * busy * byte_us ? 1.4 : tile_bytes * busy * byte_us;
+            const double work = (double)(ctas * key_tiles) * tile_bytes * byte_us, alone = waves * (double)each * 1.4;
+            const double us = (work > alone ? work : alone) + waves + 0.3 * (double)each * tile_us +
+                              (s > 1 ? 2.5 + 0.05 * (double)s + (double)(a.q_rows * a.heads * s) * r.dp * 8 / 4e6 : 0.0);
+            if (s == 1 || us < best) best = us, r.splits = (uint32_t)s;
+        }
     }
     r.items = ctas * r.splits;
     if (r.splits > 1) {
-        r.part = (size_t)round_up(r.items * r.tokens * r.group * r.dp * 4, 256);
-        r.stats = (size_t)round_up(r.items * r.tokens * r.group * 8, 256);
+        r.part = (size_t)(r.splits * a.q_rows * a.heads * r.dp * 4);   // a multiple of 256
+        r.stats = (size_t)round_up(r.splits * a.q_rows * a.heads * 8, 256);
     }
     if (!tensor_tma(a.q, a.q_row, a.q_head, a.q_rows, a.heads)) r.packs += packed_bytes(a.q_rows, a.heads, a.dim);
     if (!tensor_tma(a.k, a.k_row, a.k_head, a.k_rows, a.kv_heads)) r.packs += packed_bytes(a.k_rows, a.kv_heads, a.dim);
@@ -531,16 +556,16 @@ Plan plan_for(const gs_attention_args& a)
     return r;
 }
 
-template <int T, int DP>
-gs_status launch(const Params& p, const Plan& plan, int64_t q_rows, cudaStream_t st)
+template <int T, int DP, int TILES>
+gs_status launch(const Params& p, const Plan& plan, cudaStream_t st)
 {
+    using S = Shape<DP, TILES>;
     static std::atomic<uint64_t> done{0};
-    gs_status s = allow_smem(attention_kernel<T, DP>, Shape<DP>::kSmem, done);
+    gs_status s = allow_smem(attention_kernel<T, DP, TILES>, S::kSmem, done);
     if (s != GS_OK) return s;
-    s = launch_after(attention_kernel<T, DP>, dim3((unsigned)plan.items), kThreads, Shape<DP>::kSmem, 1, st, p);
+    s = launch_after(attention_kernel<T, DP, TILES>, dim3((unsigned)plan.items), S::kThreads, S::kSmem, 1, st, p);
     if (s != GS_OK || plan.splits == 1) return s;
-    const int64_t rows = (q_rows < plan.tokens ? q_rows : plan.tokens) * plan.group;   // of a tile, at most
-    return launch_after(join_kernel<T, DP>, dim3((unsigned)(plan.items / plan.splits), (unsigned)((rows + 3) / 4)), 128, 0, 1, st, p);
+    return launch_after(join_kernel<T, DP>, dim3((unsigned)(p.seqs.q_rows * plan.group * p.kv_heads)), kJoinWarps * 32, 0, 1, st, p);
 }
 
 }  // namespace
@@ -590,11 +615,15 @@ extern "C" gs_status gs_attention(const gs_attention_args* args, void* ws, size_
     p.o = (uint16_t*)a.o, p.o_row = a.o_row, p.o_head = a.o_head, p.lse = a.lse;
     p.part = (float*)ws, p.part_stats = (float2*)((char*)ws + plan.part);
     p.scale2 = a.scale * kLog2e;
-    p.splits = plan.splits, p.kv_heads = (uint32_t)a.kv_heads, p.tiles = plan.tiles, p.group = plan.group, p.tokens = plan.tokens;
+    p.splits = plan.splits, p.kv_heads = (uint32_t)a.kv_heads, p.group = plan.group, p.tokens = plan.tokens;
     p.dim = a.dim, p.causal = a.causal != 0;
     p.o_vec = tensor_vec(a.o, a.o_row, a.o_head, a.q_rows, a.heads);
     p.idesc_s = instr_desc(a.type, true, true, kRows, kRows);
     p.idesc_o = instr_desc(a.type, true, false, (int)round_up(a.dim, 16), kRows);
-    if (a.type == GS_BF16) return plan.dp == 64 ? launch<GS_BF16, 64>(p, plan, a.q_rows, st) : launch<GS_BF16, 128>(p, plan, a.q_rows, st);
-    return plan.dp == 64 ? launch<GS_F16, 64>(p, plan, a.q_rows, st) : launch<GS_F16, 128>(p, plan, a.q_rows, st);
+    const auto run = [&](auto type) {
+        constexpr int T = decltype(type)::value;
+        if (plan.dp == 64) return plan.tiles == 1 ? launch<T, 64, 1>(p, plan, st) : launch<T, 64, 2>(p, plan, st);
+        return plan.tiles == 1 ? launch<T, 128, 1>(p, plan, st) : launch<T, 128, 2>(p, plan, st);
+    };
+    return a.type == GS_BF16 ? run(std::integral_constant<int, GS_BF16>()) : run(std::integral_constant<int, GS_F16>());
 }

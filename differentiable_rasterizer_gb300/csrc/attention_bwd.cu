@@ -25,7 +25,7 @@ namespace gs {
 namespace attn {
 namespace {
 
-constexpr int kTmemCols = 512;
+constexpr int kThreads = 384, kTmemCols = 512;
 constexpr int kStatRows = kRows + 2;   // of a copy of row statistics, which starts on 16 bytes
 
 __device__ int g_attention_bwd_wait_expired;
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) keys_kernel(const __grid_constant
             if (!mbar_wait_alone(bars + 8 * (S::kDone + warp - 9), 0)) *gave_up = 1;
         }
     } else {
-        many_registers();
+        many_registers<224>();
         const int exponent = ds_exponent<T>(p);
         key_terms<T, DP>(p, w, warp >> 2, threadIdx.x & 127, smem, bars, tmem + ((uint32_t)((warp & 3) * 32) << 16), exponent, gave_up);
     }
@@ -742,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) queries_kernel(const __grid_const
             if (!mbar_wait_alone(bars + 8 * (S::kDone + warp - 9), 0)) *gave_up = 1;
         }
     } else {
-        many_registers();
+        many_registers<224>();
         const int i = warp >> 2, exponent = ds_exponent<T>(p);
         if (i < p.tiles && w.t0 + i * p.tokens < w.seq.lq)
             query_terms<T, DP>(p, w, i, threadIdx.x & 127, bars, tmem + ((uint32_t)((warp & 3) * 32) << 16), exponent, gave_up);

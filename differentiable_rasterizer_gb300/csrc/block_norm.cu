@@ -5,10 +5,13 @@
 //
 // One pass over the rows: a group of threads holds a row in registers from h and x to s
 // and y (backward: from dy, ds, s and h to dx and dh), with two reductions in between.
-// HBM bounds both; the group is the smallest power of two of threads that covers the row
-// at VEC elements a thread, as in norm.cu, so narrow rows share a warp and wide ones take
-// a block.  As separate norm, product, sum and norm a row would cross HBM nine times in
+// HBM bounds both.  The group is the smallest power of two of threads that covers the row
+// at NV vectors of VEC elements a thread: eight (16-byte accesses) where every row allows
+// them, else two, so that narrow rows share a warp and rows of up to 512 columns need no
+// barrier.  As separate norm, product, sum and norm a row would cross HBM nine times in
 // place of four.
+//   1,000,000 x 256 bf16  303 us at HBM's rate; 500 with weights fetched for each row
+//   20,011 x 331 f16      single elements and barriers: 138 us, gradients 362
 #include <type_traits>
 
 #include "gemm.cuh"
@@ -19,104 +22,213 @@ namespace {
 
 using namespace rows;
 
-// A vector that may be absent, in fp32.
+// VEC consecutive elements of a row as they lie in memory.  Of two, in 16 bits one access
+// where they start on 4 bytes.
+template <int T, int VEC>
+struct Cells {
+    Raw<T, 8> raw;
+    __device__ __forceinline__ void zero() { raw_zero(raw); }
+    __device__ __forceinline__ void load(const void* p, int64_t i, int, int type) { raw_load(raw, p, i, type); }
+    __device__ __forceinline__ void values(int type, float (&v)[8]) const { raw_values(raw, type, v); }
+};
+template <>
+struct Cells<GS_F32, 2> {
+    float a, b;
+    __device__ __forceinline__ void zero() { a = b = 0.0f; }
+    __device__ __forceinline__ void load(const void* p, int64_t i, int n, int)
+    {
+        a = ((const float*)p)[i];
+        if (n > 1) b = ((const float*)p)[i + 1];
+    }
+    __device__ __forceinline__ void values(int, float (&v)[2]) const { v[0] = a, v[1] = b; }
+};
+template <>
+struct Cells<kAnyType, 2> : Cells<GS_F32, 2> {
+    __device__ __forceinline__ void load(const void* p, int64_t i, int n, int type)
+    {
+        a = load_elem(p, i, type);
+        if (n > 1) b = load_elem(p, i + 1, type);
+    }
+};
+template <int T>
+struct CellsHalf {
+    uint32_t w;
+    __device__ __forceinline__ void zero() { w = 0; }
+    __device__ __forceinline__ void load(const void* p, int64_t i, int n, int)
+    {
+        const uint16_t* at = (const uint16_t*)p + i;
+        if (n > 1 && ((uintptr_t)at & 3u) == 0) w = *reinterpret_cast<const uint32_t*>(at);
+        else w = at[0] | (n > 1 ? (uint32_t)at[1] << 16 : 0u);
+    }
+    __device__ __forceinline__ void values(int, float (&v)[2]) const
+    {
+        const float2 f = unpack_half2(w, T);
+        v[0] = f.x, v[1] = f.y;
+    }
+};
+template <>
+struct Cells<GS_BF16, 2> : CellsHalf<GS_BF16> {};
+template <>
+struct Cells<GS_F16, 2> : CellsHalf<GS_F16> {};
+
 template <int VEC>
-__device__ __forceinline__ void load_or_one(const void* p, int64_t i, int type, bool there, float (&v)[VEC])
+__device__ __forceinline__ void store_cells(void* p, int64_t i, int n, int type, const float (&v)[VEC])
 {
+    if constexpr (VEC == 8) store8(p, i, type, v);
+    else if (n > 1 && type != GS_F32 && type != GS_E4M3 && ((uintptr_t)((uint16_t*)p + i) & 3u) == 0)
+        *reinterpret_cast<uint32_t*>((uint16_t*)p + i) = pack_half2(v[0], v[1], type);
+    else
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) v[e] = 1.0f;
-    if (p && there) load_vec<VEC>(p, i, type, v);
+        for (int e = 0; e < VEC; ++e)
+            if (e < n) store_elem(p, i + e, type, v[e]);
 }
 
-template <int T, int VEC, int NV>
+// The thread's columns of a vector over them; 1 where there is none, 0 beyond the row.
+template <int VEC>
+__device__ __forceinline__ void load_weight(const void* p, int64_t i, int n, int type, float (&v)[VEC])
+{
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] = e < n ? 1.0f : 0.0f;
+    if (!p || n <= 0) return;
+    if constexpr (VEC == 8) load8(p, i, type, v);
+    else
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            if (e < n) v[e] = load_elem(p, i + e, type);
+}
+
+// Weights of up to KEEP columns a thread stay in registers, of more they are fetched from
+// the first-level cache for every row.
+template <int VEC, int NV, int KEEP>
+struct Weight {
+    static constexpr bool kKeep = VEC * NV <= KEEP;
+    float v[kKeep ? NV : 1][VEC];
+    const void* p;
+    int type, lane, group, cols;
+    __device__ __forceinline__ void init(const void* p_, int type_, int lane_, int group_, int cols_)
+    {
+        p = p_, type = type_, lane = lane_, group = group_, cols = cols_;
+        if constexpr (kKeep)
+#pragma unroll
+            for (int j = 0; j < NV; ++j) load_weight<VEC>(p, col(j), cols - col(j), type, v[j]);
+    }
+    __device__ __forceinline__ int col(int j) const { return (lane + j * group) * VEC; }
+    __device__ __forceinline__ void get(int j, float (&w)[VEC]) const
+    {
+        if constexpr (kKeep)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) w[e] = v[j][e];
+        else load_weight<VEC>(p, col(j), cols - col(j), type, w);
+    }
+};
+
+// R rows a group at a time, their loads in flight together.
+template <int T, int VEC, int NV, int R>
 __global__ void __launch_bounds__(512) block_norm_kernel(const __grid_constant__ gs_block_norm_args a, int group)
 {
     __shared__ float sm[32];
     wait_for_predecessor();
-    const int lane = threadIdx.x % group, rows_per_block = blockDim.x / group;
-    const int nvec = (int)((a.cols + VEC - 1) / VEC);
+    const int lane = threadIdx.x % group, cols = (int)a.cols;
+    const int64_t rows_per_block = (int64_t)(blockDim.x / group) * R;
     const float inv_cols = 1.0f / (float)a.cols;
     const bool q8 = a.y_type == GS_E4M3 && a.y;
+    Weight<VEC, NV, 16> weight, post, gate;
+    weight.init(a.weight, a.weight_type, lane, group, cols);
+    post.init(a.post_weight, a.post_type, lane, group, cols);
+    gate.init(a.gate_rows ? nullptr : a.gate, a.gate_type, lane, group, cols);
     // every thread of a warp runs the same number of rounds (the reductions use whole warps)
     for (int64_t row0 = (int64_t)blockIdx.x * rows_per_block; row0 < a.rows; row0 += (int64_t)gridDim.x * rows_per_block) {
-        const int64_t row = row0 + threadIdx.x / group;
-        const bool here = row < a.rows;
-        Raw<T, VEC> hr[NV], xr[NV], gr[NV];
+        const int64_t row = row0 + (int64_t)(threadIdx.x / group) * R;
+        Cells<T, VEC> hr[R][NV], xr[R][NV], gr[R][NV];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = lane + j * group;
-            raw_zero(hr[j]);
-            raw_zero(xr[j]);
-            raw_zero(gr[j]);
-            if (here && c < nvec) {
-                raw_load(hr[j], a.h, row * a.ldh + (int64_t)c * VEC, T);
-                raw_load(xr[j], a.x, row * a.ldx + (int64_t)c * VEC, T);
-                if (a.gate_rows) raw_load(gr[j], a.gate, row * a.ldg + (int64_t)c * VEC, T);
-            }
-        }
-        float s[NV][VEC], rstd_post = 1.0f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) raw_values(hr[j], T, s[j]);
-        if (a.post_weight) {
-            float ss = 0.0f;
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) ss = __fmaf_rn(s[j][e], s[j][e], ss);
-            rstd_post = 1.0f / sqrtf(group_reduce<Sum>(ss, group, sm) * inv_cols + a.eps);
-            if (a.rstd_post && here && lane == 0) a.rstd_post[row] = rstd_post;
-        }
-        float ss = 0.0f, top = 0.0f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = lane + j * group;
-            float x[VEC], g[VEC], w[VEC];
-            raw_values(xr[j], T, x);
-            load_or_one<VEC>(a.post_weight, (int64_t)c * VEC, a.post_type, c < nvec, w);
-            if (a.gate_rows) raw_values(gr[j], T, g);
-            else load_or_one<VEC>(a.gate, (int64_t)c * VEC, a.gate_type, c < nvec, g);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float n = a.post_weight ? (s[j][e] * rstd_post) * w[e] : s[j][e];
-                s[j][e] = __fmaf_rn(a.scale, x[e], g[e] * n);
-                if (VEC == 8 || c < nvec) ss = __fmaf_rn(s[j][e], s[j][e], ss);
-            }
-            if (here && c < nvec) store_vec<VEC>(a.s, row * a.lds + (int64_t)c * VEC, T, s[j]);
-        }
-        if (!a.y) continue;
-        ss = group_reduce<Sum>(ss, group, sm);
-        const float rstd = 1.0f / sqrtf(ss * inv_cols + a.eps);
-        if (a.rstd && here && lane == 0) a.rstd[row] = rstd;
-        float factor = rstd;
-        if (q8) {
+        for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int c = lane + j * group;
-                float w[VEC];
-                load_or_one<VEC>(a.weight, (int64_t)c * VEC, a.weight_type, c < nvec, w);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    s[j][e] *= w[e];
-                    top = max_nan(top, fabsf(s[j][e]));
+                const int c = weight.col(j), n = cols - c;
+                hr[i][j].zero(), xr[i][j].zero(), gr[i][j].zero();
+                if (row + i < a.rows && n > 0) {
+                    hr[i][j].load(a.h, (row + i) * a.ldh + c, n, T);
+                    xr[i][j].load(a.x, (row + i) * a.ldx + c, n, T);
+                    if (a.gate_rows) gr[i][j].load(a.gate, (row + i) * a.ldg + c, n, T);
                 }
             }
-            top = max_nan(group_reduce<Max>(top, group, sm), kTiny);
-            factor = kE4m3Max / top;
-            if (here && lane == 0) a.y_scale[row] = (top / kE4m3Max) * rstd;
+        float s[R][NV][VEC], rstd_post[R], ss[R], top[R], factor[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            ss[i] = top[i] = 0.0f;
+            rstd_post[i] = 1.0f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                hr[i][j].values(T, s[i][j]);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) ss[i] = __fmaf_rn(s[i][j][e], s[i][j][e], ss[i]);
+            }
+        }
+        if (a.post_weight) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) ss[i] = group_reduce<Sum>(ss[i], group, sm);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                rstd_post[i] = 1.0f / sqrtf(ss[i] * inv_cols + a.eps);
+                if (a.rstd_post && row + i < a.rows && lane == 0) a.rstd_post[row + i] = rstd_post[i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) ss[i] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = weight.col(j), n = cols - c;
+            float w[VEC], p[VEC], g0[VEC];
+            post.get(j, p);
+            gate.get(j, g0);
+            if (q8) weight.get(j, w);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                float x[VEC], g[VEC];
+                xr[i][j].values(T, x);
+                gr[i][j].values(T, g);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float unit = a.post_weight ? (s[i][j][e] * rstd_post[i]) * p[e] : s[i][j][e];
+                    s[i][j][e] = __fmaf_rn(a.scale, x[e], (a.gate_rows ? g[e] : g0[e]) * unit);
+                    ss[i] = __fmaf_rn(s[i][j][e], s[i][j][e], ss[i]);
+                }
+                if (row + i < a.rows && n > 0) store_cells<VEC>(a.s, (row + i) * a.lds + c, n, T, s[i][j]);
+                if (q8)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        s[i][j][e] *= w[e];
+                        top[i] = max_nan(top[i], fabsf(s[i][j][e]));
+                    }
+            }
+        }
+        if (!a.y) continue;
+#pragma unroll
+        for (int i = 0; i < R; ++i) ss[i] = group_reduce<Sum>(ss[i], group, sm);
+        if (q8) {   // e4m3 keeps 4 significant bits; the row's largest magnitude goes to 448
+#pragma unroll
+            for (int i = 0; i < R; ++i) top[i] = max_nan(group_reduce<Max>(top[i], group, sm), kTiny);
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const float rstd = 1.0f / sqrtf(ss[i] * inv_cols + a.eps);
+            factor[i] = q8 ? kE4m3Max / top[i] : rstd;
+            if (row + i < a.rows && lane == 0) {
+                if (a.rstd) a.rstd[row + i] = rstd;
+                if (q8) a.y_scale[row + i] = (top[i] / kE4m3Max) * rstd;
+            }
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = lane + j * group;
-            if (q8) {
+            const int c = weight.col(j), n = cols - c;
+            float w[VEC];
+            if (!q8) weight.get(j, w);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) s[j][e] *= factor;
-            } else {
-                float w[VEC];
-                load_or_one<VEC>(a.weight, (int64_t)c * VEC, a.weight_type, c < nvec, w);
+            for (int i = 0; i < R; ++i) {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) s[j][e] = (s[j][e] * factor) * w[e];
+                for (int e = 0; e < VEC; ++e) s[i][j][e] = q8 ? s[i][j][e] * factor[i] : (s[i][j][e] * factor[i]) * w[e];
+                if (row + i < a.rows && n > 0) store_cells<VEC>(a.y, (row + i) * a.ldy + c, n, a.y_type, s[i][j]);
             }
-            if (here && c < nvec) store_vec<VEC>(a.y, row * a.ldy + (int64_t)c * VEC, a.y_type, s[j]);
         }
     }
 }
@@ -124,17 +236,19 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const __grid_constant__
 // Sums over rows: every thread keeps its columns' over the rows it visits, a block joins
 // its groups' in order into partial rows, and JoinJobs adds the blocks' in order.
 // partial: [3][blocks][cols]: dweight, dpost, dgate.
-template <int T, int TDY, int VEC, int NV>
-__global__ void __launch_bounds__(512) block_norm_bwd_kernel(const __grid_constant__ gs_block_norm_bwd_args a,
-                                                                                     int group, float* partial)
+template <int T, int TDY, int VEC, int NV, int R>
+__global__ void __launch_bounds__(512) block_norm_bwd_kernel(const __grid_constant__ gs_block_norm_bwd_args a, int group, float* partial)
 {
     extern __shared__ float part[];   // [groups][columns rounded up] when a block holds several groups
     __shared__ float sm[32];
     wait_for_predecessor();
-    const int lane = threadIdx.x % group, groups = blockDim.x / group;
-    const int nvec = (int)((a.cols + VEC - 1) / VEC);
+    const int lane = threadIdx.x % group, groups = blockDim.x / group, cols = (int)a.cols;
     const float inv_cols = 1.0f / (float)a.cols;
     const bool post = a.post_weight != nullptr, gate_sum = a.dgate && !a.gate_rows;
+    Weight<VEC, NV, 8> weight, post_weight, gate;   // beside the sums
+    weight.init(a.weight, a.weight_type, lane, group, cols);
+    post_weight.init(a.post_weight, a.post_type, lane, group, cols);
+    gate.init(a.gate_rows ? nullptr : a.gate, a.gate_type, lane, group, cols);
     float acc[3][NV][VEC];
 #pragma unroll
     for (int k = 0; k < 3; ++k)
@@ -142,92 +256,113 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(const __grid_consta
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) acc[k][j][e] = 0.0f;
-    for (int64_t row0 = (int64_t)blockIdx.x * groups; row0 < a.rows; row0 += (int64_t)gridDim.x * groups) {
-        const int64_t row = row0 + threadIdx.x / group;
-        const bool here = row < a.rows;
-        Raw<T, VEC> hr[NV], sr[NV], dr[NV], gr[NV];
-        Raw<TDY, VEC> yr[NV];
-        const float rstd = a.dy && here ? a.rstd[row] : 0.0f, rstd_post = post && here ? a.rstd_post[row] : 1.0f;
+    const int64_t step = (int64_t)gridDim.x * groups * R;
+    for (int64_t row0 = (int64_t)blockIdx.x * groups * R; row0 < a.rows; row0 += step) {
+        const int64_t row = row0 + (int64_t)(threadIdx.x / group) * R;
+        Cells<T, VEC> hr[R][NV], sr[R][NV], dr[R][NV], gr[R][NV];
+        Cells<TDY, VEC> yr[R][NV];
+        float rstd[R], rstd_post[R];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = lane + j * group;
-            raw_zero(hr[j]);
-            raw_zero(sr[j]);
-            raw_zero(dr[j]);
-            raw_zero(gr[j]);
-            raw_zero(yr[j]);
-            if (here && c < nvec) {
-                const int64_t at = (int64_t)c * VEC;
-                if (a.dy) {
-                    raw_load(yr[j], a.dy, row * a.lddy + at, a.dy_type);
-                    raw_load(sr[j], a.s, row * a.lds + at, T);
-                }
-                if (a.ds) raw_load(dr[j], a.ds, row * a.ldds + at, T);
-                if (post || a.dgate) raw_load(hr[j], a.h, row * a.ldh + at, T);
-                if (a.gate_rows) raw_load(gr[j], a.gate, row * a.ldg + at, T);
-            }
-        }
-        float g[NV][VEC];   // the gradient of s, then of a times post
-#pragma unroll
-        for (int j = 0; j < NV; ++j) raw_values(dr[j], T, g[j]);
-        if (a.dy) {
-            float dot = 0.0f;
-            float s[NV][VEC], w[NV][VEC];
+        for (int i = 0; i < R; ++i) {
+            const bool here = row + i < a.rows;
+            rstd[i] = a.dy && here ? a.rstd[row + i] : 0.0f;
+            rstd_post[i] = post && here ? a.rstd_post[row + i] : 1.0f;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int c = lane + j * group;
-                float dy[VEC];
-                raw_values(sr[j], T, s[j]);
-                raw_values(yr[j], a.dy_type, dy);
-                load_or_one<VEC>(a.weight, (int64_t)c * VEC, a.weight_type, c < nvec, w[j]);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    acc[0][j][e] = __fmaf_rn(dy[e], s[j][e] * rstd, acc[0][j][e]);
-                    w[j][e] *= dy[e];
-                    dot = __fmaf_rn(w[j][e], s[j][e], dot);
+                const int c = weight.col(j), n = cols - c;
+                hr[i][j].zero(), sr[i][j].zero(), dr[i][j].zero(), gr[i][j].zero(), yr[i][j].zero();
+                if (here && n > 0) {
+                    if (a.dy) {
+                        yr[i][j].load(a.dy, (row + i) * a.lddy + c, n, a.dy_type);
+                        sr[i][j].load(a.s, (row + i) * a.lds + c, n, T);
+                    }
+                    if (a.ds) dr[i][j].load(a.ds, (row + i) * a.ldds + c, n, T);
+                    if (post || a.dgate) hr[i][j].load(a.h, (row + i) * a.ldh + c, n, T);
+                    if (a.gate_rows) gr[i][j].load(a.gate, (row + i) * a.ldg + c, n, T);
                 }
             }
-            const float c2 = group_reduce<Sum>(dot, group, sm) * inv_cols * rstd * rstd;
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) g[j][e] = __fmaf_rn(rstd, __fmaf_rn(-s[j][e], c2, w[j][e]), g[j][e]);
         }
-        float h[NV][VEC], dot = 0.0f;
+        float g[R][NV][VEC], dot[R], c2[R];   // g: dy * weight, the gradient of s, that of a times post
+#pragma unroll
+        for (int i = 0; i < R; ++i) dot[i] = c2[i] = 0.0f;
+        if (a.dy) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                float w[VEC];
+                weight.get(j, w);
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    float s[VEC], dy[VEC];
+                    sr[i][j].values(T, s);
+                    yr[i][j].values(a.dy_type, dy);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        acc[0][j][e] = __fmaf_rn(dy[e], s[e] * rstd[i], acc[0][j][e]);
+                        g[i][j][e] = dy[e] * w[e];
+                        dot[i] = __fmaf_rn(g[i][j][e], s[e], dot[i]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i) dot[i] = group_reduce<Sum>(dot[i], group, sm);
+#pragma unroll
+            for (int i = 0; i < R; ++i) c2[i] = dot[i] * inv_cols * rstd[i] * rstd[i], dot[i] = 0.0f;
+        }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = lane + j * group;
-            const int64_t at = (int64_t)c * VEC;
-            float w[VEC], gate[VEC], v[VEC];
-            raw_values(hr[j], T, h[j]);
-            load_or_one<VEC>(a.post_weight, at, a.post_type, c < nvec, w);
-            if (a.gate_rows) raw_values(gr[j], T, gate);
-            else load_or_one<VEC>(a.gate, at, a.gate_type, c < nvec, gate);
+            const int c = weight.col(j), n = cols - c;
+            float w[VEC], g0[VEC];
+            post_weight.get(j, w);
+            gate.get(j, g0);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) v[e] = a.scale * g[j][e];
-            if (a.dx && here && c < nvec) store_vec<VEC>(a.dx, row * a.lddx + at, T, v);
+            for (int i = 0; i < R; ++i) {
+                float h[VEC], v[VEC], gates[VEC];
+                hr[i][j].values(T, h);
+                dr[i][j].values(T, v);
+                gr[i][j].values(T, gates);
+                if (a.dy) {
+                    float s[VEC];
+                    sr[i][j].values(T, s);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float unit = h[j][e] * rstd_post;
-                v[e] = g[j][e] * (post ? unit * w[e] : h[j][e]);   // the gate's gradient
-                acc[2][j][e] += v[e];
-                g[j][e] *= gate[e];
-                acc[1][j][e] = __fmaf_rn(g[j][e], unit, acc[1][j][e]);
-                if (post) g[j][e] *= w[e];
-                dot = __fmaf_rn(g[j][e], h[j][e], dot);
+                    for (int e = 0; e < VEC; ++e) g[i][j][e] = __fmaf_rn(rstd[i], __fmaf_rn(-s[e], c2[i], g[i][j][e]), v[e]);
+                } else
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) g[i][j][e] = v[e];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) v[e] = a.scale * g[i][j][e];
+                const bool there = row + i < a.rows && n > 0;
+                if (a.dx && there) store_cells<VEC>(a.dx, (row + i) * a.lddx + c, n, T, v);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float unit = h[e] * rstd_post[i];
+                    v[e] = g[i][j][e] * (post ? unit * w[e] : h[e]);   // the gate's gradient
+                    acc[2][j][e] += v[e];
+                    g[i][j][e] *= a.gate_rows ? gates[e] : g0[e];
+                    acc[1][j][e] = __fmaf_rn(g[i][j][e], unit, acc[1][j][e]);
+                    if (post) g[i][j][e] *= w[e];
+                    dot[i] = __fmaf_rn(g[i][j][e], h[e], dot[i]);
+                }
+                if (a.dgate && a.gate_rows && there) store_cells<VEC>(a.dgate, (row + i) * a.lddg + c, n, T, v);
             }
-            if (a.dgate && a.gate_rows && here && c < nvec) store_vec<VEC>(a.dgate, row * a.lddg + at, T, v);
         }
         if (!a.dh) continue;
-        const float c2 = post ? group_reduce<Sum>(dot, group, sm) * inv_cols * rstd_post * rstd_post : 0.0f;
+        if (post) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = lane + j * group;
-            if (post) {
+            for (int i = 0; i < R; ++i) dot[i] = group_reduce<Sum>(dot[i], group, sm);
+        }
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) g[j][e] = rstd_post * __fmaf_rn(-h[j][e], c2, g[j][e]);
+        for (int i = 0; i < R; ++i) {
+            c2[i] = dot[i] * inv_cols * rstd_post[i] * rstd_post[i];
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = weight.col(j), n = cols - c;
+                float h[VEC];
+                hr[i][j].values(T, h);
+                if (post)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) g[i][j][e] = rstd_post[i] * __fmaf_rn(-h[e], c2[i], g[i][j][e]);
+                if (row + i < a.rows && n > 0) store_cells<VEC>(a.dh, (row + i) * a.lddh + c, n, T, g[i][j]);
             }
-            if (here && c < nvec) store_vec<VEC>(a.dh, row * a.lddh + (int64_t)c * VEC, T, g[j]);
         }
     }
     const bool wanted[3] = {a.dweight != nullptr, a.dpost != nullptr, gate_sum};
@@ -239,10 +374,8 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(const __grid_consta
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const int c = (lane + j * group) * VEC + e;
-                    if (c < a.cols) out[c] = acc[k][j][e];
-                }
+                for (int e = 0; e < VEC; ++e)
+                    if (weight.col(j) + e < cols) out[weight.col(j) + e] = acc[k][j][e];
             continue;
         }
         const int width = NV * group * VEC;
@@ -251,9 +384,9 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(const __grid_consta
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) mine[(lane + j * group) * VEC + e] = acc[k][j][e];
+            for (int e = 0; e < VEC; ++e) mine[weight.col(j) + e] = acc[k][j][e];
         __syncthreads();
-        for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+        for (int c = threadIdx.x; c < cols; c += blockDim.x) {
             float t = 0.0f;
             for (int r = 0; r < groups; ++r) t += part[r * width + c];
             out[c] = t;
@@ -264,21 +397,19 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(const __grid_consta
 template <int V>
 using Type = std::integral_constant<int, V>;
 
-// The group: the smallest power of two of threads that covers the row with one vector
-// each, at most 512; then as many vectors a thread as that leaves.
 struct Shape {
     int nv, group, threads;
 };
-Shape shape_for(int64_t cols, int vec)
+// Vectors of eight: one a thread within a warp, two where that keeps a row within it, then as
+// many as 512 threads need.  Pairs: two a thread for rows within a warp, else eight, or sixteen.
+Shape shape_for(int64_t cols, bool vec)
 {
-    const int64_t nvec = (cols + vec - 1) / vec, widest = 512;
+    const int64_t n = vec ? (cols + 7) / 8 : (cols + 1) / 2;
     Shape s;
+    if (vec) s.nv = n <= 32 ? 1 : (n <= 1024 ? 2 : 4);
+    else s.nv = n <= 64 ? 2 : (n <= 4096 ? 8 : 16);
     s.group = 1;
-    while (s.group < nvec && s.group < (vec == 8 ? widest : 32)) s.group *= 2;
-    if (vec == 1)
-        while (s.group < widest && nvec > 8 * (int64_t)s.group) s.group *= 2;
-    s.nv = 1;
-    while ((int64_t)s.nv * s.group < nvec) s.nv *= vec == 8 ? 2 : 4;
+    while ((int64_t)s.group * s.nv < n) s.group *= 2;
     s.threads = s.group < 256 ? 256 : s.group;
     return s;
 }
@@ -319,21 +450,23 @@ extern "C" gs_status gs_block_norm(const gs_block_norm_args* args, void* stream)
     const bool vec = a.cols % 8 == 0 && rows16(a.h, a.ldh, a.type) && rows16(a.x, a.ldx, a.type) && rows16(a.s, a.lds, a.type) &&
                      weight16(a.post_weight) && weight16(a.weight) && (a.gate_rows ? rows16(a.gate, a.ldg, a.type) : weight16(a.gate)) &&
                      (!a.weight || (a.y_type == GS_E4M3 ? ((uintptr_t)a.y & 7u) == 0 && a.ldy % 8 == 0 : rows16(a.y, a.ldy, a.y_type)));
-    const Shape s = shape_for(a.cols, vec ? 8 : 1);
-    const int64_t rpb = s.threads / s.group, want = (a.rows + rpb - 1) / rpb, most = (int64_t)sms * (2048 / s.threads);
+    const Shape s = shape_for(a.cols, vec);
+    // two rows a group where there are rows enough to fill the SMs all the same
+    const bool two = vec && s.nv == 1 && a.rows >= (int64_t)sms * 4 * (s.threads / s.group) * 2;
+    const int64_t rpb = s.threads / s.group * (two ? 2 : 1), want = (a.rows + rpb - 1) / rpb, most = (int64_t)sms * (two ? 4 : 2048 / s.threads);
     const int grid = (int)(want < most ? want : most);
     cudaStream_t st = (cudaStream_t)stream;
     const auto run = [&](auto t) -> gs_status {
         constexpr int T = decltype(t)::value;
-#define GS_FWD(V, N) return launch_after(block_norm_kernel<T, V, N>, dim3(grid), s.threads, 0, 1, st, a, s.group)
+#define GS_FWD(V, N, R) return launch_after(block_norm_kernel<T, V, N, R>, dim3(grid), s.threads, 0, 1, st, a, s.group)
         if (vec) {
-            if (s.nv == 1) GS_FWD(8, 1);
-            else if (s.nv == 2) GS_FWD(8, 2);
-            else GS_FWD(8, 4);
-        } else if (s.nv <= 1) GS_FWD(1, 1);
-        else if (s.nv <= 4) GS_FWD(1, 4);
-        else if (s.nv <= 16) GS_FWD(1, 16);
-        else GS_FWD(1, 32);
+            if (two) GS_FWD(8, 1, 2);
+            else if (s.nv == 1) GS_FWD(8, 1, 1);
+            else if (s.nv == 2) GS_FWD(8, 2, 1);
+            else GS_FWD(8, 4, 1);
+        } else if (s.nv == 2) GS_FWD(2, 2, 1);
+        else if (s.nv == 8) GS_FWD(2, 8, 1);
+        else GS_FWD(2, 16, 1);
 #undef GS_FWD
     };
     if (a.type == GS_F32) return run(Type<GS_F32>());
@@ -379,32 +512,36 @@ extern "C" gs_status gs_block_norm_bwd(const gs_block_norm_bwd_args* args, void*
     if (!a.dx && !a.dh && !a.dweight && !a.dpost && !a.dgate) return GS_OK;
     if (sms <= 0) return GS_ERR_CUDA;
     const auto wide = [&](const void* p, int64_t ld, bool used, int type) { return !used || rows16(p, ld, type); };
-    const bool vec = a.cols % 8 == 0 && wide(a.dy, a.lddy, a.dy, a.dy_type) && wide(a.s, a.lds, a.dy, a.type) &&
+    const bool same = !a.dy || a.dy_type == a.type;   // dy of another type goes by pairs
+    const bool vec = same && a.cols % 8 == 0 && wide(a.dy, a.lddy, a.dy, a.dy_type) && wide(a.s, a.lds, a.dy, a.type) &&
                      wide(a.ds, a.ldds, a.ds, a.type) && wide(a.h, a.ldh, reads_h, a.type) && wide(a.gate, a.ldg, row_gate, a.type) &&
                      wide(a.dgate, a.lddg, row_dgate, a.type) && wide(a.dx, a.lddx, a.dx, a.type) && wide(a.dh, a.lddh, a.dh, a.type) &&
                      weight16(a.weight) && weight16(a.post_weight) && (row_gate || weight16(a.gate));
-    const int v = vec ? 8 : 1;
-    const Shape s = shape_for(a.cols, v);
+    const int v = vec ? 8 : 2;
+    const Shape s = shape_for(a.cols, vec);
     const int groups = s.threads / s.group;
-    const int64_t want = (a.rows + groups - 1) / groups;
+    const bool two = vec && s.nv == 1 && a.rows >= blocks * groups * 2;   // rows enough to fill the SMs
+    const int64_t rpb = groups * (two ? 2 : 1), want = (a.rows + rpb - 1) / rpb;
     const int grid = (int)(want < blocks ? want : blocks);
     const size_t smem = groups > 1 && need ? (size_t)groups * s.nv * s.group * v * 4 : 0;   // at most 16 KB
     float* part = (float*)ws;
     const auto run = [&](auto t, auto tdy) -> gs_status {
         constexpr int T = decltype(t)::value, TDY = decltype(tdy)::value;
-#define GS_BWD(V, N) return launch_after(block_norm_bwd_kernel<T, TDY, V, N>, dim3(grid), s.threads, smem, 1, st, a, s.group, part)
-        if (vec) {
-            if (s.nv == 1) GS_BWD(8, 1);
-            else if (s.nv == 2) GS_BWD(8, 2);
-            else GS_BWD(8, 4);
-        } else if (s.nv <= 1) GS_BWD(1, 1);
-        else if (s.nv <= 4) GS_BWD(1, 4);
-        else if (s.nv <= 16) GS_BWD(1, 16);
-        else GS_BWD(1, 32);
+#define GS_BWD(V, N, R) return launch_after(block_norm_bwd_kernel<T, TDY, V, N, R>, dim3(grid), s.threads, smem, 1, st, a, s.group, part)
+        if constexpr (T == TDY)
+            if (vec) {
+                if (two) GS_BWD(8, 1, 2);
+                else if (s.nv == 1) GS_BWD(8, 1, 1);
+                else if (s.nv == 2) GS_BWD(8, 2, 1);
+                else GS_BWD(8, 4, 1);
+            }
+        if (s.nv == 2) GS_BWD(2, 2, 1);
+        else if (s.nv == 8) GS_BWD(2, 8, 1);
+        else GS_BWD(2, 16, 1);
 #undef GS_BWD
     };
     const auto pick = [&](auto t) -> gs_status {
-        if (!a.dy || a.dy_type == a.type) return run(t, t);
+        if (same) return run(t, t);
         return run(t, Type<kAnyType>());
     };
     gs_status status = a.type == GS_F32 ? pick(Type<GS_F32>()) : (a.type == GS_BF16 ? pick(Type<GS_BF16>()) : pick(Type<GS_F16>()));
