@@ -11,7 +11,6 @@
 // barrier.  As separate norm, product, sum and norm a row would cross HBM nine times in
 // place of four.
 //   1,000,000 x 256 bf16  303 us at HBM's rate; 500 with weights fetched for each row
-//   20,011 x 331 f16      single elements and barriers: 138 us, gradients 362
 #include <type_traits>
 
 #include "gemm.cuh"
@@ -22,376 +21,384 @@ namespace {
 
 using namespace rows;
 
-// VEC consecutive elements of a row as they lie in memory.  Of two, in 16 bits one access
-// where they start on 4 bytes.
+// VEC consecutive elements of a row as they lie in memory, and as pairs in fp32.  Two elements
+// are fetched one by one, whatever their alignment: a branch on it between loads would make
+// each wait for the one before.
 template <int T, int VEC>
 struct Cells {
     Raw<T, 8> raw;
     __device__ __forceinline__ void zero() { raw_zero(raw); }
     __device__ __forceinline__ void load(const void* p, int64_t i, int, int type) { raw_load(raw, p, i, type); }
-    __device__ __forceinline__ void values(int type, float (&v)[8]) const { raw_values(raw, type, v); }
-};
-template <>
-struct Cells<GS_F32, 2> {
-    float a, b;
-    __device__ __forceinline__ void zero() { a = b = 0.0f; }
-    __device__ __forceinline__ void load(const void* p, int64_t i, int n, int)
+    __device__ __forceinline__ void values(int type, uint64_t (&v)[4]) const
     {
-        a = ((const float*)p)[i];
-        if (n > 1) b = ((const float*)p)[i + 1];
-    }
-    __device__ __forceinline__ void values(int, float (&v)[2]) const { v[0] = a, v[1] = b; }
-};
-template <>
-struct Cells<kAnyType, 2> : Cells<GS_F32, 2> {
-    __device__ __forceinline__ void load(const void* p, int64_t i, int n, int type)
-    {
-        a = load_elem(p, i, type);
-        if (n > 1) b = load_elem(p, i + 1, type);
+        float f[8];
+        raw_values(raw, type, f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = pair(f[2 * e], f[2 * e + 1]);
     }
 };
 template <int T>
-struct CellsHalf {
-    uint32_t w;
-    __device__ __forceinline__ void zero() { w = 0; }
-    __device__ __forceinline__ void load(const void* p, int64_t i, int n, int)
+struct Cells<T, 2> {
+    Raw<T, 1> a, b;
+    __device__ __forceinline__ void zero() { raw_zero(a), raw_zero(b); }
+    __device__ __forceinline__ void load(const void* p, int64_t i, int n, int type)
     {
-        const uint16_t* at = (const uint16_t*)p + i;
-        if (n > 1 && ((uintptr_t)at & 3u) == 0) w = *reinterpret_cast<const uint32_t*>(at);
-        else w = at[0] | (n > 1 ? (uint32_t)at[1] << 16 : 0u);
+        raw_load(a, p, i, type);
+        if (n > 1) raw_load(b, p, i + 1, type);
     }
-    __device__ __forceinline__ void values(int, float (&v)[2]) const
+    __device__ __forceinline__ void values(int type, uint64_t (&v)[1]) const
     {
-        const float2 f = unpack_half2(w, T);
-        v[0] = f.x, v[1] = f.y;
+        float x[1], y[1];
+        raw_values(a, type, x);
+        raw_values(b, type, y);
+        v[0] = pair(x[0], y[0]);
     }
 };
-template <>
-struct Cells<GS_BF16, 2> : CellsHalf<GS_BF16> {};
-template <>
-struct Cells<GS_F16, 2> : CellsHalf<GS_F16> {};
 
 template <int VEC>
-__device__ __forceinline__ void store_cells(void* p, int64_t i, int n, int type, const float (&v)[VEC])
+__device__ __forceinline__ void store_cells(void* p, int64_t i, int n, int type, const uint64_t (&v)[VEC / 2])
 {
-    if constexpr (VEC == 8) store8(p, i, type, v);
-    else if (n > 1 && type != GS_F32 && type != GS_E4M3 && ((uintptr_t)((uint16_t*)p + i) & 3u) == 0)
-        *reinterpret_cast<uint32_t*>((uint16_t*)p + i) = pack_half2(v[0], v[1], type);
+    float f[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC / 2; ++e) {
+        const float2 t = unpair(v[e]);
+        f[2 * e] = t.x, f[2 * e + 1] = t.y;
+    }
+    if constexpr (VEC == 8) store8(p, i, type, f);
+    else if (n > 1 && (type == GS_BF16 || type == GS_F16) && ((uintptr_t)((uint16_t*)p + i) & 3u) == 0)
+        *reinterpret_cast<uint32_t*>((uint16_t*)p + i) = pack_half2(f[0], f[1], type);
     else
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
-            if (e < n) store_elem(p, i + e, type, v[e]);
+            if (e < n) store_elem(p, i + e, type, f[e]);
 }
 
 // The thread's columns of a vector over them; 1 where there is none, 0 beyond the row.
 template <int VEC>
-__device__ __forceinline__ void load_weight(const void* p, int64_t i, int n, int type, float (&v)[VEC])
+__device__ __forceinline__ void load_weight(const void* p, int64_t i, int n, int type, uint64_t (&v)[VEC / 2])
 {
+    float f[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) v[e] = e < n ? 1.0f : 0.0f;
-    if (!p || n <= 0) return;
-    if constexpr (VEC == 8) load8(p, i, type, v);
-    else
+    for (int e = 0; e < VEC; ++e) f[e] = e < n ? 1.0f : 0.0f;
+    if (p && n > 0) {
+        if constexpr (VEC == 8) load8(p, i, type, f);
+        else
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
-            if (e < n) v[e] = load_elem(p, i + e, type);
+            for (int e = 0; e < VEC; ++e)
+                if (e < n) f[e] = load_elem(p, i + e, type);
+    }
+#pragma unroll
+    for (int e = 0; e < VEC / 2; ++e) v[e] = pair(f[2 * e], f[2 * e + 1]);
 }
 
-// Weights of up to KEEP columns a thread stay in registers, of more they are fetched from
-// the first-level cache for every row.
-template <int VEC, int NV, int KEEP>
+// The product of one or two vectors over the columns.  Of up to 16 columns a thread they stay
+// in registers, of more they are fetched from the first-level cache for every row.
+template <int VEC, int NV>
 struct Weight {
-    static constexpr bool kKeep = VEC * NV <= KEEP;
-    float v[kKeep ? NV : 1][VEC];
-    const void* p;
-    int type, lane, group, cols;
-    __device__ __forceinline__ void init(const void* p_, int type_, int lane_, int group_, int cols_)
+    static constexpr bool kKeep = VEC * NV <= 16;
+    uint64_t v[kKeep ? NV : 1][VEC / 2];
+    const void *p, *q;
+    int p_type, q_type, lane, group, cols;
+    __device__ __forceinline__ Weight(const void* p_, int p_type_, const void* q_, int q_type_, int lane_, int group_, int cols_)
+        : p(p_), q(q_), p_type(p_type_), q_type(q_type_), lane(lane_), group(group_), cols(cols_)
     {
-        p = p_, type = type_, lane = lane_, group = group_, cols = cols_;
         if constexpr (kKeep)
 #pragma unroll
-            for (int j = 0; j < NV; ++j) load_weight<VEC>(p, col(j), cols - col(j), type, v[j]);
+            for (int j = 0; j < NV; ++j) fetch(j, v[j]);
     }
     __device__ __forceinline__ int col(int j) const { return (lane + j * group) * VEC; }
-    __device__ __forceinline__ void get(int j, float (&w)[VEC]) const
+    __device__ __forceinline__ void fetch(int j, uint64_t (&w)[VEC / 2]) const
+    {
+        load_weight<VEC>(p, col(j), cols - col(j), p_type, w);
+        if (q) {
+            uint64_t t[VEC / 2];
+            load_weight<VEC>(q, col(j), cols - col(j), q_type, t);
+#pragma unroll
+            for (int e = 0; e < VEC / 2; ++e) w[e] = mul2(w[e], t[e]);
+        }
+    }
+    __device__ __forceinline__ void get(int j, uint64_t (&w)[VEC / 2]) const
     {
         if constexpr (kKeep)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) w[e] = v[j][e];
-        else load_weight<VEC>(p, col(j), cols - col(j), type, w);
+            for (int e = 0; e < VEC / 2; ++e) w[e] = v[j][e];
+        else fetch(j, w);
     }
 };
 
-// R rows a group at a time, their loads in flight together.
-template <int T, int VEC, int NV, int R>
-__global__ void __launch_bounds__(512) block_norm_kernel(const __grid_constant__ gs_block_norm_args a, int group)
+__device__ __forceinline__ uint64_t both(float v) { return pair(v, v); }
+__device__ __forceinline__ float sum_of(uint64_t v)
 {
+    const float2 f = unpair(v);
+    return f.x + f.y;
+}
+
+// Threads of a block at most, and blocks an SM: one vector of eight a thread wants many warps
+// of few registers; eight pairs a thread, each element in a register, need more than 128.
+template <int VEC, int NV>
+constexpr int kThreads = (VEC == 2 && NV == 8) || (VEC == 8 && NV == 1) ? 256 : 512;
+template <int T, int VEC, int NV>
+constexpr int kForwardBlocks = VEC == 8 && NV == 1 ? (T == GS_F32 ? 3 : 4) : 1;
+template <int T, int VEC, int NV>
+constexpr int kBackwardBlocks = VEC == 8 && NV == 1 ? (T == GS_F32 ? 2 : 3) : 1;
+
+template <int T, int VEC, int NV>
+__global__ void __launch_bounds__(kThreads<VEC, NV>, kForwardBlocks<T, VEC, NV>) block_norm_kernel(const __grid_constant__ gs_block_norm_args a, int group)
+{
+    constexpr int P = VEC / 2;
+    constexpr bool kAhead = VEC * NV == 8;   // the next row's loads before this one's work
     __shared__ float sm[32];
     wait_for_predecessor();
     const int lane = threadIdx.x % group, cols = (int)a.cols;
-    const int64_t rows_per_block = (int64_t)(blockDim.x / group) * R;
+    const int64_t step = (int64_t)gridDim.x * (blockDim.x / group);
     const float inv_cols = 1.0f / (float)a.cols;
     const bool q8 = a.y_type == GS_E4M3 && a.y;
-    Weight<VEC, NV, 16> weight, post, gate;
-    weight.init(a.weight, a.weight_type, lane, group, cols);
-    post.init(a.post_weight, a.post_type, lane, group, cols);
-    gate.init(a.gate_rows ? nullptr : a.gate, a.gate_type, lane, group, cols);
-    // every thread of a warp runs the same number of rounds (the reductions use whole warps)
-    for (int64_t row0 = (int64_t)blockIdx.x * rows_per_block; row0 < a.rows; row0 += (int64_t)gridDim.x * rows_per_block) {
-        const int64_t row = row0 + (int64_t)(threadIdx.x / group) * R;
-        Cells<T, VEC> hr[R][NV], xr[R][NV], gr[R][NV];
+    const Weight<VEC, NV> weight(a.weight, a.weight_type, nullptr, 0, lane, group, cols);
+    const Weight<VEC, NV> post(a.post_weight, a.post_type, a.gate_rows ? nullptr : a.gate, a.gate_type, lane, group, cols);
+    const uint64_t scale = both(a.scale);
+    Cells<T, VEC> hr[NV], xr[NV], gr[NV];
+    const auto load = [&](int64_t row) {
 #pragma unroll
-        for (int i = 0; i < R; ++i)
+        for (int j = 0; j < NV; ++j) {
+            const int c = weight.col(j), n = cols - c;
+            hr[j].zero(), xr[j].zero();
+            if (row < a.rows && n > 0) {
+                hr[j].load(a.h, row * a.ldh + c, n, T);
+                xr[j].load(a.x, row * a.ldx + c, n, T);
+            }
+        }
+    };
+    int64_t row = (int64_t)blockIdx.x * (blockDim.x / group) + threadIdx.x / group;
+    if (kAhead) load(row);
+    // every thread of a warp runs the same number of rounds (the reductions use whole warps)
+    for (int64_t row0 = row - threadIdx.x / group; row0 < a.rows; row0 += step, row += step) {
+        const bool here = row < a.rows;
+        if (!kAhead) load(row);
+        if (a.gate_rows)
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int c = weight.col(j), n = cols - c;
-                hr[i][j].zero(), xr[i][j].zero(), gr[i][j].zero();
-                if (row + i < a.rows && n > 0) {
-                    hr[i][j].load(a.h, (row + i) * a.ldh + c, n, T);
-                    xr[i][j].load(a.x, (row + i) * a.ldx + c, n, T);
-                    if (a.gate_rows) gr[i][j].load(a.gate, (row + i) * a.ldg + c, n, T);
-                }
+                gr[j].zero();
+                if (here && n > 0) gr[j].load(a.gate, row * a.ldg + c, n, T);
             }
-        float s[R][NV][VEC], rstd_post[R], ss[R], top[R], factor[R];
+        uint64_t s[NV][P], x[NV][P], q = both(0.0f);
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            ss[i] = top[i] = 0.0f;
-            rstd_post[i] = 1.0f;
+        for (int j = 0; j < NV; ++j) {
+            hr[j].values(T, s[j]);
+            xr[j].values(T, x[j]);
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                hr[i][j].values(T, s[i][j]);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) ss[i] = __fmaf_rn(s[i][j][e], s[i][j][e], ss[i]);
-            }
+            for (int e = 0; e < P; ++e) q = fma2(s[j][e], s[j][e], q);
         }
+        if (kAhead) load(row + step);
+        float rstd_post = 1.0f;
         if (a.post_weight) {
-#pragma unroll
-            for (int i = 0; i < R; ++i) ss[i] = group_reduce<Sum>(ss[i], group, sm);
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-                rstd_post[i] = 1.0f / sqrtf(ss[i] * inv_cols + a.eps);
-                if (a.rstd_post && row + i < a.rows && lane == 0) a.rstd_post[row + i] = rstd_post[i];
-            }
+            rstd_post = rsqrtf(group_reduce<Sum>(sum_of(q), group, sm) * inv_cols + a.eps);
+            if (a.rstd_post && here && lane == 0) a.rstd_post[row] = rstd_post;
         }
-#pragma unroll
-        for (int i = 0; i < R; ++i) ss[i] = 0.0f;
+        float top = 0.0f;
+        q = both(0.0f);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = weight.col(j), n = cols - c;
-            float w[VEC], p[VEC], g0[VEC];
-            post.get(j, p);
-            gate.get(j, g0);
-            if (q8) weight.get(j, w);
+            uint64_t p[P];
+            post.get(j, p);   // with the gate's vector
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                float x[VEC], g[VEC];
-                xr[i][j].values(T, x);
-                gr[i][j].values(T, g);
+            for (int e = 0; e < P; ++e) s[j][e] = mul2(mul2(s[j][e], both(rstd_post)), p[e]);
+            if (a.gate_rows) {
+                uint64_t g[P];
+                gr[j].values(T, g);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float unit = a.post_weight ? (s[i][j][e] * rstd_post[i]) * p[e] : s[i][j][e];
-                    s[i][j][e] = __fmaf_rn(a.scale, x[e], (a.gate_rows ? g[e] : g0[e]) * unit);
-                    ss[i] = __fmaf_rn(s[i][j][e], s[i][j][e], ss[i]);
+                for (int e = 0; e < P; ++e) s[j][e] = mul2(s[j][e], g[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+                s[j][e] = fma2(scale, x[j][e], s[j][e]);
+                q = fma2(s[j][e], s[j][e], q);
+            }
+            if (here && n > 0) store_cells<VEC>(a.s, row * a.lds + c, n, T, s[j]);
+            if (q8) {
+                uint64_t w[P];
+                weight.get(j, w);
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    s[j][e] = mul2(s[j][e], w[e]);
+                    const float2 f = unpair(s[j][e]);
+                    top = max_nan(top, max_nan(fabsf(f.x), fabsf(f.y)));
                 }
-                if (row + i < a.rows && n > 0) store_cells<VEC>(a.s, (row + i) * a.lds + c, n, T, s[i][j]);
-                if (q8)
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        s[i][j][e] *= w[e];
-                        top[i] = max_nan(top[i], fabsf(s[i][j][e]));
-                    }
             }
         }
         if (!a.y) continue;
-#pragma unroll
-        for (int i = 0; i < R; ++i) ss[i] = group_reduce<Sum>(ss[i], group, sm);
+        const float rstd = rsqrtf(group_reduce<Sum>(sum_of(q), group, sm) * inv_cols + a.eps);
+        float factor = rstd;
         if (q8) {   // e4m3 keeps 4 significant bits; the row's largest magnitude goes to 448
-#pragma unroll
-            for (int i = 0; i < R; ++i) top[i] = max_nan(group_reduce<Max>(top[i], group, sm), kTiny);
+            top = max_nan(group_reduce<Max>(top, group, sm), kTiny);
+            factor = kE4m3Max / top;
+            if (here && lane == 0) a.y_scale[row] = (top / kE4m3Max) * rstd;
         }
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const float rstd = 1.0f / sqrtf(ss[i] * inv_cols + a.eps);
-            factor[i] = q8 ? kE4m3Max / top[i] : rstd;
-            if (row + i < a.rows && lane == 0) {
-                if (a.rstd) a.rstd[row + i] = rstd;
-                if (q8) a.y_scale[row + i] = (top[i] / kE4m3Max) * rstd;
-            }
-        }
+        if (a.rstd && here && lane == 0) a.rstd[row] = rstd;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = weight.col(j), n = cols - c;
-            float w[VEC];
-            if (!q8) weight.get(j, w);
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
+            for (int e = 0; e < P; ++e) s[j][e] = mul2(s[j][e], both(factor));
+            if (!q8) {
+                uint64_t w[P];
+                weight.get(j, w);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) s[i][j][e] = q8 ? s[i][j][e] * factor[i] : (s[i][j][e] * factor[i]) * w[e];
-                if (row + i < a.rows && n > 0) store_cells<VEC>(a.y, (row + i) * a.ldy + c, n, a.y_type, s[i][j]);
+                for (int e = 0; e < P; ++e) s[j][e] = mul2(s[j][e], w[e]);
             }
+            if (here && n > 0) store_cells<VEC>(a.y, row * a.ldy + c, n, a.y_type, s[j]);
         }
     }
 }
 
 // Sums over rows: every thread keeps its columns' over the rows it visits, a block joins
 // its groups' in order into partial rows, and JoinJobs adds the blocks' in order.
+//   A = sum of g h rstd_post gives two of them where the gate is a vector: dgate = post A,
+//   dpost = gate A; where it is rows, dpost sums g h rstd_post gate.
 // partial: [3][blocks][cols]: dweight, dpost, dgate.
-template <int T, int TDY, int VEC, int NV, int R>
-__global__ void __launch_bounds__(512) block_norm_bwd_kernel(const __grid_constant__ gs_block_norm_bwd_args a, int group, float* partial)
+template <int T, int TDY, int VEC, int NV>
+__global__ void __launch_bounds__(kThreads<VEC, NV>, kBackwardBlocks<T, VEC, NV>) block_norm_bwd_kernel(const __grid_constant__ gs_block_norm_bwd_args a,
+                                                                                                   int group, float* partial)
 {
+    constexpr int P = VEC / 2;
     extern __shared__ float part[];   // [groups][columns rounded up] when a block holds several groups
     __shared__ float sm[32];
     wait_for_predecessor();
     const int lane = threadIdx.x % group, groups = blockDim.x / group, cols = (int)a.cols;
     const float inv_cols = 1.0f / (float)a.cols;
-    const bool post = a.post_weight != nullptr, gate_sum = a.dgate && !a.gate_rows;
-    Weight<VEC, NV, 8> weight, post_weight, gate;   // beside the sums
-    weight.init(a.weight, a.weight_type, lane, group, cols);
-    post_weight.init(a.post_weight, a.post_type, lane, group, cols);
-    gate.init(a.gate_rows ? nullptr : a.gate, a.gate_type, lane, group, cols);
-    float acc[3][NV][VEC];
+    const bool post = a.post_weight != nullptr;
+    const void* gate = a.gate_rows ? nullptr : a.gate;
+    const Weight<VEC, NV> weight(a.weight, a.weight_type, nullptr, 0, lane, group, cols);
+    const Weight<VEC, NV> post_weight(a.post_weight, a.post_type, gate, a.gate_type, lane, group, cols);
+    const uint64_t scale = both(a.scale);
+    uint64_t acc[2][NV][P];
 #pragma unroll
-    for (int k = 0; k < 3; ++k)
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) acc[k][j][e] = 0.0f;
-    const int64_t step = (int64_t)gridDim.x * groups * R;
-    for (int64_t row0 = (int64_t)blockIdx.x * groups * R; row0 < a.rows; row0 += step) {
-        const int64_t row = row0 + (int64_t)(threadIdx.x / group) * R;
-        Cells<T, VEC> hr[R][NV], sr[R][NV], dr[R][NV], gr[R][NV];
-        Cells<TDY, VEC> yr[R][NV];
-        float rstd[R], rstd_post[R];
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const bool here = row + i < a.rows;
-            rstd[i] = a.dy && here ? a.rstd[row + i] : 0.0f;
-            rstd_post[i] = post && here ? a.rstd_post[row + i] : 1.0f;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int c = weight.col(j), n = cols - c;
-                hr[i][j].zero(), sr[i][j].zero(), dr[i][j].zero(), gr[i][j].zero(), yr[i][j].zero();
-                if (here && n > 0) {
-                    if (a.dy) {
-                        yr[i][j].load(a.dy, (row + i) * a.lddy + c, n, a.dy_type);
-                        sr[i][j].load(a.s, (row + i) * a.lds + c, n, T);
-                    }
-                    if (a.ds) dr[i][j].load(a.ds, (row + i) * a.ldds + c, n, T);
-                    if (post || a.dgate) hr[i][j].load(a.h, (row + i) * a.ldh + c, n, T);
-                    if (a.gate_rows) gr[i][j].load(a.gate, (row + i) * a.ldg + c, n, T);
-                }
-            }
-        }
-        float g[R][NV][VEC], dot[R], c2[R];   // g: dy * weight, the gradient of s, that of a times post
-#pragma unroll
-        for (int i = 0; i < R; ++i) dot[i] = c2[i] = 0.0f;
-        if (a.dy) {
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                float w[VEC];
-                weight.get(j, w);
-#pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    float s[VEC], dy[VEC];
-                    sr[i][j].values(T, s);
-                    yr[i][j].values(a.dy_type, dy);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        acc[0][j][e] = __fmaf_rn(dy[e], s[e] * rstd[i], acc[0][j][e]);
-                        g[i][j][e] = dy[e] * w[e];
-                        dot[i] = __fmaf_rn(g[i][j][e], s[e], dot[i]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < R; ++i) dot[i] = group_reduce<Sum>(dot[i], group, sm);
-#pragma unroll
-            for (int i = 0; i < R; ++i) c2[i] = dot[i] * inv_cols * rstd[i] * rstd[i], dot[i] = 0.0f;
-        }
+            for (int e = 0; e < P; ++e) acc[k][j][e] = both(0.0f);
+    for (int64_t row0 = (int64_t)blockIdx.x * groups; row0 < a.rows; row0 += (int64_t)gridDim.x * groups) {
+        const int64_t row = row0 + threadIdx.x / group;
+        const bool here = row < a.rows;
+        Cells<T, VEC> hr[NV], sr[NV], dr[NV], gr[NV];
+        Cells<TDY, VEC> yr[NV];
+        const float rstd = a.dy && here ? a.rstd[row] : 0.0f, rstd_post = post && here ? a.rstd_post[row] : 1.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = weight.col(j), n = cols - c;
-            float w[VEC], g0[VEC];
-            post_weight.get(j, w);
-            gate.get(j, g0);
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-                float h[VEC], v[VEC], gates[VEC];
-                hr[i][j].values(T, h);
-                dr[i][j].values(T, v);
-                gr[i][j].values(T, gates);
+            hr[j].zero(), sr[j].zero(), dr[j].zero(), gr[j].zero(), yr[j].zero();
+            if (here && n > 0) {
                 if (a.dy) {
-                    float s[VEC];
-                    sr[i][j].values(T, s);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) g[i][j][e] = __fmaf_rn(rstd[i], __fmaf_rn(-s[e], c2[i], g[i][j][e]), v[e]);
-                } else
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) g[i][j][e] = v[e];
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) v[e] = a.scale * g[i][j][e];
-                const bool there = row + i < a.rows && n > 0;
-                if (a.dx && there) store_cells<VEC>(a.dx, (row + i) * a.lddx + c, n, T, v);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float unit = h[e] * rstd_post[i];
-                    v[e] = g[i][j][e] * (post ? unit * w[e] : h[e]);   // the gate's gradient
-                    acc[2][j][e] += v[e];
-                    g[i][j][e] *= a.gate_rows ? gates[e] : g0[e];
-                    acc[1][j][e] = __fmaf_rn(g[i][j][e], unit, acc[1][j][e]);
-                    if (post) g[i][j][e] *= w[e];
-                    dot[i] = __fmaf_rn(g[i][j][e], h[e], dot[i]);
+                    yr[j].load(a.dy, row * a.lddy + c, n, a.dy_type);
+                    sr[j].load(a.s, row * a.lds + c, n, T);
                 }
-                if (a.dgate && a.gate_rows && there) store_cells<VEC>(a.dgate, (row + i) * a.lddg + c, n, T, v);
+                if (a.ds) dr[j].load(a.ds, row * a.ldds + c, n, T);
+                if (post || a.dgate) hr[j].load(a.h, row * a.ldh + c, n, T);
+                if (a.gate_rows) gr[j].load(a.gate, row * a.ldg + c, n, T);
+            }
+        }
+        uint64_t g[NV][P], q = both(0.0f);   // g: dy * weight, the gradient of s, that of h / rms(h)
+        float c2 = 0.0f;
+        if (a.dy) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                uint64_t s[P], dy[P], w[P];
+                weight.get(j, w);
+                sr[j].values(T, s);
+                yr[j].values(a.dy_type, dy);
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    acc[0][j][e] = fma2(dy[e], mul2(s[e], both(rstd)), acc[0][j][e]);
+                    g[j][e] = mul2(dy[e], w[e]);
+                    q = fma2(g[j][e], s[e], q);
+                }
+            }
+            c2 = -group_reduce<Sum>(sum_of(q), group, sm) * inv_cols * rstd * rstd;
+        }
+        q = both(0.0f);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = weight.col(j), n = cols - c;
+            const bool there = here && n > 0;
+            uint64_t h[P], v[P], w[P];
+            post_weight.get(j, w);   // with the gate's vector
+            hr[j].values(T, h);
+            dr[j].values(T, v);
+            if (a.dy) {
+                uint64_t s[P];
+                sr[j].values(T, s);
+#pragma unroll
+                for (int e = 0; e < P; ++e) g[j][e] = fma2(both(rstd), fma2(s[e], both(c2), g[j][e]), v[e]);
+            } else
+#pragma unroll
+                for (int e = 0; e < P; ++e) g[j][e] = v[e];
+            if (a.dx && there) {
+#pragma unroll
+                for (int e = 0; e < P; ++e) v[e] = mul2(scale, g[j][e]);
+                store_cells<VEC>(a.dx, row * a.lddx + c, n, T, v);
+            }
+            if (a.gate_rows) {
+                uint64_t gates[P];
+                gr[j].values(T, gates);
+                if (a.dgate && there) {
+#pragma unroll
+                    for (int e = 0; e < P; ++e) v[e] = mul2(g[j][e], mul2(mul2(h[e], both(rstd_post)), w[e]));
+                    store_cells<VEC>(a.dgate, row * a.lddg + c, n, T, v);
+                }
+#pragma unroll
+                for (int e = 0; e < P; ++e) g[j][e] = mul2(g[j][e], gates[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+                acc[1][j][e] = fma2(g[j][e], mul2(h[e], both(rstd_post)), acc[1][j][e]);
+                g[j][e] = mul2(g[j][e], w[e]);
+                q = fma2(g[j][e], h[e], q);
             }
         }
         if (!a.dh) continue;
-        if (post) {
+        if (post) c2 = -group_reduce<Sum>(sum_of(q), group, sm) * inv_cols * rstd_post * rstd_post;
 #pragma unroll
-            for (int i = 0; i < R; ++i) dot[i] = group_reduce<Sum>(dot[i], group, sm);
-        }
+        for (int j = 0; j < NV; ++j) {
+            const int c = weight.col(j), n = cols - c;
+            if (post) {
+                uint64_t h[P];
+                hr[j].values(T, h);
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            c2[i] = dot[i] * inv_cols * rstd_post[i] * rstd_post[i];
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int c = weight.col(j), n = cols - c;
-                float h[VEC];
-                hr[i][j].values(T, h);
-                if (post)
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) g[i][j][e] = rstd_post[i] * __fmaf_rn(-h[e], c2[i], g[i][j][e]);
-                if (row + i < a.rows && n > 0) store_cells<VEC>(a.dh, (row + i) * a.lddh + c, n, T, g[i][j]);
+                for (int e = 0; e < P; ++e) g[j][e] = mul2(both(rstd_post), fma2(h[e], both(c2), g[j][e]));
             }
+            if (here && n > 0) store_cells<VEC>(a.dh, row * a.lddh + c, n, T, g[j]);
         }
     }
-    const bool wanted[3] = {a.dweight != nullptr, a.dpost != nullptr, gate_sum};
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        if (!wanted[k]) continue;
-        float* out = partial + ((int64_t)k * gridDim.x + blockIdx.x) * a.cols;
-        if (groups == 1) {
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    if (weight.col(j) + e < cols) out[weight.col(j) + e] = acc[k][j][e];
-            continue;
-        }
+    const auto write = [&](int which, const uint64_t (&v)[NV][P], const void* by, int by_type) {
+        float* out = partial + ((int64_t)which * gridDim.x + blockIdx.x) * a.cols;
         const int width = NV * group * VEC;
-        float* mine = part + (threadIdx.x / group) * width;
+        float* mine = groups == 1 ? out : part + (threadIdx.x / group) * width;
         __syncthreads();   // the sums before have been read
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j) {
+            const int c = weight.col(j);
+            uint64_t w[P];
+            load_weight<VEC>(by, c, cols - c, by_type, w);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) mine[weight.col(j) + e] = acc[k][j][e];
+            for (int e = 0; e < P; ++e) {
+                const float2 f = unpair(mul2(v[j][e], w[e]));
+                if (groups > 1 || c + 2 * e < cols) mine[c + 2 * e] = f.x;
+                if (groups > 1 || c + 2 * e + 1 < cols) mine[c + 2 * e + 1] = f.y;
+            }
+        }
+        if (groups == 1) return;
         __syncthreads();
         for (int c = threadIdx.x; c < cols; c += blockDim.x) {
             float t = 0.0f;
             for (int r = 0; r < groups; ++r) t += part[r * width + c];
             out[c] = t;
         }
-    }
+    };
+    if (a.dweight) write(0, acc[0], nullptr, 0);
+    if (a.dpost) write(1, acc[1], gate, a.gate_type);
+    if (a.dgate && !a.gate_rows) write(2, acc[1], a.post_weight, a.post_type);
 }
 
 template <int V>
@@ -401,16 +408,17 @@ struct Shape {
     int nv, group, threads;
 };
 // Vectors of eight: one a thread within a warp, two where that keeps a row within it, then as
-// many as 512 threads need.  Pairs: two a thread for rows within a warp, else eight, or sixteen.
-Shape shape_for(int64_t cols, bool vec)
+// many as 512 threads need.  Pairs: two a thread for rows within a warp, else eight (256
+// threads at most), or sixteen.
+Shape shape_for(int64_t cols, bool vec, bool forward)
 {
     const int64_t n = vec ? (cols + 7) / 8 : (cols + 1) / 2;
     Shape s;
     if (vec) s.nv = n <= 32 ? 1 : (n <= 1024 ? 2 : 4);
-    else s.nv = n <= 64 ? 2 : (n <= 4096 ? 8 : 16);
+    else s.nv = n <= 64 ? 2 : (n <= 2048 ? 8 : 16);
     s.group = 1;
     while ((int64_t)s.group * s.nv < n) s.group *= 2;
-    s.threads = s.group < 256 ? 256 : s.group;
+    s.threads = s.group > (forward ? 32 : 256) ? s.group : 256;
     return s;
 }
 
@@ -450,23 +458,20 @@ extern "C" gs_status gs_block_norm(const gs_block_norm_args* args, void* stream)
     const bool vec = a.cols % 8 == 0 && rows16(a.h, a.ldh, a.type) && rows16(a.x, a.ldx, a.type) && rows16(a.s, a.lds, a.type) &&
                      weight16(a.post_weight) && weight16(a.weight) && (a.gate_rows ? rows16(a.gate, a.ldg, a.type) : weight16(a.gate)) &&
                      (!a.weight || (a.y_type == GS_E4M3 ? ((uintptr_t)a.y & 7u) == 0 && a.ldy % 8 == 0 : rows16(a.y, a.ldy, a.y_type)));
-    const Shape s = shape_for(a.cols, vec);
-    // two rows a group where there are rows enough to fill the SMs all the same
-    const bool two = vec && s.nv == 1 && a.rows >= (int64_t)sms * 4 * (s.threads / s.group) * 2;
-    const int64_t rpb = s.threads / s.group * (two ? 2 : 1), want = (a.rows + rpb - 1) / rpb, most = (int64_t)sms * (two ? 4 : 2048 / s.threads);
+    const Shape s = shape_for(a.cols, vec, true);
+    const int64_t rpb = s.threads / s.group, want = (a.rows + rpb - 1) / rpb, most = (int64_t)sms * (1024 / s.threads);
     const int grid = (int)(want < most ? want : most);
     cudaStream_t st = (cudaStream_t)stream;
     const auto run = [&](auto t) -> gs_status {
         constexpr int T = decltype(t)::value;
-#define GS_FWD(V, N, R) return launch_after(block_norm_kernel<T, V, N, R>, dim3(grid), s.threads, 0, 1, st, a, s.group)
+#define GS_FWD(V, N) return launch_after(block_norm_kernel<T, V, N>, dim3(grid), s.threads, 0, 1, st, a, s.group)
         if (vec) {
-            if (two) GS_FWD(8, 1, 2);
-            else if (s.nv == 1) GS_FWD(8, 1, 1);
-            else if (s.nv == 2) GS_FWD(8, 2, 1);
-            else GS_FWD(8, 4, 1);
-        } else if (s.nv == 2) GS_FWD(2, 2, 1);
-        else if (s.nv == 8) GS_FWD(2, 8, 1);
-        else GS_FWD(2, 16, 1);
+            if (s.nv == 1) GS_FWD(8, 1);
+            else if (s.nv == 2) GS_FWD(8, 2);
+            else GS_FWD(8, 4);
+        } else if (s.nv == 2) GS_FWD(2, 2);
+        else if (s.nv == 8) GS_FWD(2, 8);
+        else GS_FWD(2, 16);
 #undef GS_FWD
     };
     if (a.type == GS_F32) return run(Type<GS_F32>());
@@ -518,26 +523,24 @@ extern "C" gs_status gs_block_norm_bwd(const gs_block_norm_bwd_args* args, void*
                      wide(a.dgate, a.lddg, row_dgate, a.type) && wide(a.dx, a.lddx, a.dx, a.type) && wide(a.dh, a.lddh, a.dh, a.type) &&
                      weight16(a.weight) && weight16(a.post_weight) && (row_gate || weight16(a.gate));
     const int v = vec ? 8 : 2;
-    const Shape s = shape_for(a.cols, vec);
+    const Shape s = shape_for(a.cols, vec, false);
     const int groups = s.threads / s.group;
-    const bool two = vec && s.nv == 1 && a.rows >= blocks * groups * 2;   // rows enough to fill the SMs
-    const int64_t rpb = groups * (two ? 2 : 1), want = (a.rows + rpb - 1) / rpb;
+    const int64_t want = (a.rows + groups - 1) / groups;
     const int grid = (int)(want < blocks ? want : blocks);
     const size_t smem = groups > 1 && need ? (size_t)groups * s.nv * s.group * v * 4 : 0;   // at most 16 KB
     float* part = (float*)ws;
     const auto run = [&](auto t, auto tdy) -> gs_status {
         constexpr int T = decltype(t)::value, TDY = decltype(tdy)::value;
-#define GS_BWD(V, N, R) return launch_after(block_norm_bwd_kernel<T, TDY, V, N, R>, dim3(grid), s.threads, smem, 1, st, a, s.group, part)
+#define GS_BWD(V, N) return launch_after(block_norm_bwd_kernel<T, TDY, V, N>, dim3(grid), s.threads, smem, 1, st, a, s.group, part)
         if constexpr (T == TDY)
             if (vec) {
-                if (two) GS_BWD(8, 1, 2);
-                else if (s.nv == 1) GS_BWD(8, 1, 1);
-                else if (s.nv == 2) GS_BWD(8, 2, 1);
-                else GS_BWD(8, 4, 1);
+                if (s.nv == 1) GS_BWD(8, 1);
+                else if (s.nv == 2) GS_BWD(8, 2);
+                else GS_BWD(8, 4);
             }
-        if (s.nv == 2) GS_BWD(2, 2, 1);
-        else if (s.nv == 8) GS_BWD(2, 8, 1);
-        else GS_BWD(2, 16, 1);
+        if (s.nv == 2) GS_BWD(2, 2);
+        else if (s.nv == 8) GS_BWD(2, 8);
+        else GS_BWD(2, 16);
 #undef GS_BWD
     };
     const auto pick = [&](auto t) -> gs_status {

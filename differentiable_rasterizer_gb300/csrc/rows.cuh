@@ -29,8 +29,11 @@ struct Max {
 template <class Op>
 __device__ __forceinline__ float group_reduce(float v, int group, float* sm)
 {
-    const int in_warp = group < 32 ? group : 32;
-    for (int o = in_warp >> 1; o > 0; o >>= 1) v = Op::join(v, __shfl_xor_sync(0xffffffffu, v, o));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {   // unrolled: a step that the group has not leaves v as it is
+        const float other = __shfl_xor_sync(0xffffffffu, v, o);
+        v = o < group ? Op::join(v, other) : v;
+    }
     if (group <= 32) return v;
     const int warp = threadIdx.x >> 5, first = threadIdx.x / group * (group >> 5), last = first + (group >> 5);
     __syncthreads();   // the previous row's readers are done
