@@ -6,9 +6,8 @@
 // One pass over the rows: a group of threads holds a row in registers from h and x to s
 // and y (backward: from dy, ds, s and h to dx and dh), with two reductions in between.
 // HBM bounds both.  The group is the smallest power of two of threads that covers the row
-// at NV vectors of VEC elements a thread: eight (16-byte accesses) where every row allows
-// them, else two, so that narrow rows share a warp and rows of up to 512 columns need no
-// barrier.  As separate norm, product, sum and norm a row would cross HBM nine times in
+// at eight columns a thread, so that narrow rows share a warp and rows of up to 256 columns
+// need no barrier.  As separate norm, product, sum and norm a row would cross HBM nine times in
 // place of four.
 //   1,000,000 x 256 bf16  303 us at HBM's rate; 500 with weights fetched for each row
 #include <type_traits>
@@ -21,82 +20,144 @@ namespace {
 
 using namespace rows;
 
-// VEC consecutive elements of a row as they lie in memory, and as pairs in fp32.  Two elements
-// are fetched one by one, whatever their alignment: a branch on it between loads would make
-// each wait for the one before.
-template <int T, int VEC>
-struct Cells {
-    Raw<T, 8> raw;
-    __device__ __forceinline__ void zero() { raw_zero(raw); }
-    __device__ __forceinline__ void load(const void* p, int64_t i, int, int type) { raw_load(raw, p, i, type); }
-    __device__ __forceinline__ void values(int type, uint64_t (&v)[4]) const
-    {
-        float f[8];
-        raw_values(raw, type, f);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = pair(f[2 * e], f[2 * e + 1]);
-    }
-};
-template <int T>
-struct Cells<T, 2> {
-    Raw<T, 1> a, b;
-    __device__ __forceinline__ void zero() { raw_zero(a), raw_zero(b); }
-    __device__ __forceinline__ void load(const void* p, int64_t i, int n, int type)
-    {
-        raw_load(a, p, i, type);
-        if (n > 1) raw_load(b, p, i + 1, type);
-    }
-    __device__ __forceinline__ void values(int type, uint64_t (&v)[1]) const
-    {
-        float x[1], y[1];
-        raw_values(a, type, x);
-        raw_values(b, type, y);
-        v[0] = pair(x[0], y[0]);
-    }
+// A matrix's rows as a thread reads them, eight columns at a time.  Rows of 16-byte base and
+// pitch: whole pieces, of which a row's last may lie in its padding.  Others of 16-bit
+// elements: the two aligned pieces that the eight columns lie in, shifted together; single
+// elements in the first and the last row, whose pieces may reach beyond the matrix, and in fp32.
+struct Source {
+    const void* p;
+    int64_t ld;
+    int type;
+    bool aligned;
+    __device__ __forceinline__ Source(const void* p_, int64_t ld_, int type_)
+        : p(p_), ld(ld_), type(type_), aligned(((uintptr_t)p_ & 15u) == 0 && ld_ * (type_ == GS_F32 ? 4 : 2) % 16 == 0) {}
 };
 
-template <int VEC>
-__device__ __forceinline__ void store_cells(void* p, int64_t i, int n, int type, const uint64_t (&v)[VEC / 2])
-{
-    float f[VEC];
+// WHOLE: every matrix's rows are whole pieces.
+template <int T, bool WHOLE>
+constexpr bool kShifts = !WHOLE && (T == GS_BF16 || T == GS_F16);
+template <int T, bool WHOLE>
+struct Cells {
+    Raw<T, 8> raw;
+    uint32_t high[kShifts<T, WHOLE> ? 4 : 1];   // the second piece of unaligned rows
+    __device__ __forceinline__ void zero()
+    {
+        raw_zero(raw);
 #pragma unroll
-    for (int e = 0; e < VEC / 2; ++e) {
+        for (int e = 0; e < (int)(sizeof high / 4); ++e) high[e] = 0;
+    }
+};
+// Elements from one to the other, of the eight at p.
+__device__ __forceinline__ uint32_t element_bits(const void* p, int64_t i, int type)
+{
+    return type == GS_F32 ? ((const uint32_t*)p)[i] : ((const uint16_t*)p)[i];
+}
+
+template <int T, bool WHOLE>
+__device__ __forceinline__ void fetch(Cells<T, WHOLE>& to, const Source& m, int64_t row, int64_t rows, int col, int cols)
+{
+    const int n = cols - col, type = T == kAnyType ? m.type : T;
+    const int64_t at = row * m.ld + col;
+    if constexpr (WHOLE) {
+        raw_load(to.raw, m.p, at, type);
+        return;
+    }
+    const bool inside = row > 0 && row + 1 < rows;
+    if (m.aligned && (inside || (cols & 7) == 0)) {
+        raw_load(to.raw, m.p, at, type);
+    } else if (kShifts<T, WHOLE> && inside) {
+        const uintptr_t a = (uintptr_t)((const uint16_t*)m.p + at);
+        const uint4* piece = reinterpret_cast<const uint4*>(a & ~(uintptr_t)15);
+        to.raw.q[0] = *piece;
+        if (n > 8 - (int)(a >> 1 & 7)) {
+            const uint4 h = piece[1];
+            to.high[0] = h.x;
+            if constexpr (kShifts<T, WHOLE>) to.high[1] = h.y, to.high[2] = h.z, to.high[3] = h.w;
+        }
+    } else {
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = e < n ? element_bits(m.p, at + e, type) : 0;
+        if (type == GS_F32) {
+            to.raw.q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            if constexpr (T == GS_F32 || T == kAnyType) to.raw.q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        } else
+            to.raw.q[0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+    }
+}
+
+// The values, in pairs; 0 beyond the row.
+template <int T, bool WHOLE>
+__device__ __forceinline__ void values(const Cells<T, WHOLE>& c, const Source& m, int64_t row, int64_t rows, int col, int cols, uint64_t (&v)[4])
+{
+    const int n = cols - col, type = T == kAnyType ? m.type : T;
+    Raw<T, 8> raw = c.raw;
+    if constexpr (kShifts<T, WHOLE>) {
+        if (!m.aligned && row > 0 && row + 1 < rows) {
+            const uint32_t shift = (uint32_t)((uintptr_t)((const uint16_t*)m.p + row * m.ld + col) >> 1) & 7;   // elements
+            uint32_t w[8] = {raw.q[0].x, raw.q[0].y, raw.q[0].z, raw.q[0].w, c.high[0], c.high[1], c.high[2], c.high[3]};
+#pragma unroll
+            for (int e = 0; e < 6; ++e) w[e] = shift & 4 ? w[e + 2] : w[e];
+#pragma unroll
+            for (int e = 0; e < 5; ++e) w[e] = shift & 2 ? w[e + 1] : w[e];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = __funnelshift_r(w[e], w[e + 1], shift & 1 ? 16 : 0);
+            raw.q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    float f[8];
+    raw_values(raw, type, f);
+    if (!WHOLE && n < 8) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e >= n) f[e] = 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = pair(f[2 * e], f[2 * e + 1]);
+}
+
+// Eight columns to a row, whole where the row's place (aligned) and its end allow it.
+__device__ __forceinline__ void store(void* p, int64_t at, int n, int type, bool aligned, const uint64_t (&v)[4])
+{
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
         const float2 t = unpair(v[e]);
         f[2 * e] = t.x, f[2 * e + 1] = t.y;
     }
-    if constexpr (VEC == 8) store8(p, i, type, f);
-    else if (n > 1 && (type == GS_BF16 || type == GS_F16) && ((uintptr_t)((uint16_t*)p + i) & 3u) == 0)
-        *reinterpret_cast<uint32_t*>((uint16_t*)p + i) = pack_half2(f[0], f[1], type);
+    if (aligned && n >= 8) store8(p, at, type, f);
     else
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
-            if (e < n) store_elem(p, i + e, type, f[e]);
+        for (int e = 0; e < 8; ++e)
+            if (e < n) store_elem(p, at + e, type, f[e]);
+}
+__device__ __forceinline__ bool rows_aligned(const void* p, int64_t ld, int type)
+{
+    const int e = type_bytes(type), piece = type == GS_E4M3 ? 8 : 16;
+    return ((uintptr_t)p & (uintptr_t)(piece - 1)) == 0 && ld * e % piece == 0;
 }
 
 // The thread's columns of a vector over them; 1 where there is none, 0 beyond the row.
-template <int VEC>
-__device__ __forceinline__ void load_weight(const void* p, int64_t i, int n, int type, uint64_t (&v)[VEC / 2])
+__device__ __forceinline__ void load_weight(const void* p, int col, int n, int type, uint64_t (&v)[4])
 {
-    float f[VEC];
+    float f[8];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) f[e] = e < n ? 1.0f : 0.0f;
-    if (p && n > 0) {
-        if constexpr (VEC == 8) load8(p, i, type, f);
-        else
+    for (int e = 0; e < 8; ++e) f[e] = e < n ? 1.0f : 0.0f;
+    if (p && n >= 8 && ((uintptr_t)p & 15u) == 0) load8(p, col, type, f);
+    else if (p)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                if (e < n) f[e] = load_elem(p, i + e, type);
-    }
+        for (int e = 0; e < 8; ++e)
+            if (e < n) f[e] = load_elem(p, col + e, type);
 #pragma unroll
-    for (int e = 0; e < VEC / 2; ++e) v[e] = pair(f[2 * e], f[2 * e + 1]);
+    for (int e = 0; e < 4; ++e) v[e] = pair(f[2 * e], f[2 * e + 1]);
 }
 
 // The product of one or two vectors over the columns.  Of up to 16 columns a thread they stay
 // in registers, of more they are fetched from the first-level cache for every row.
-template <int VEC, int NV>
+template <int NV>
 struct Weight {
-    static constexpr bool kKeep = VEC * NV <= 16;
-    uint64_t v[kKeep ? NV : 1][VEC / 2];
+    static constexpr bool kKeep = NV <= 2;
+    uint64_t v[kKeep ? NV : 1][4];
     const void *p, *q;
     int p_type, q_type, lane, group, cols;
     __device__ __forceinline__ Weight(const void* p_, int p_type_, const void* q_, int q_type_, int lane_, int group_, int cols_)
@@ -104,25 +165,25 @@ struct Weight {
     {
         if constexpr (kKeep)
 #pragma unroll
-            for (int j = 0; j < NV; ++j) fetch(j, v[j]);
+            for (int j = 0; j < NV; ++j) product(j, v[j]);
     }
-    __device__ __forceinline__ int col(int j) const { return (lane + j * group) * VEC; }
-    __device__ __forceinline__ void fetch(int j, uint64_t (&w)[VEC / 2]) const
+    __device__ __forceinline__ int col(int j) const { return (lane + j * group) * 8; }
+    __device__ __forceinline__ void product(int j, uint64_t (&w)[4]) const
     {
-        load_weight<VEC>(p, col(j), cols - col(j), p_type, w);
+        load_weight(p, col(j), cols - col(j), p_type, w);
         if (q) {
-            uint64_t t[VEC / 2];
-            load_weight<VEC>(q, col(j), cols - col(j), q_type, t);
+            uint64_t t[4];
+            load_weight(q, col(j), cols - col(j), q_type, t);
 #pragma unroll
-            for (int e = 0; e < VEC / 2; ++e) w[e] = mul2(w[e], t[e]);
+            for (int e = 0; e < 4; ++e) w[e] = mul2(w[e], t[e]);
         }
     }
-    __device__ __forceinline__ void get(int j, uint64_t (&w)[VEC / 2]) const
+    __device__ __forceinline__ void get(int j, uint64_t (&w)[4]) const
     {
         if constexpr (kKeep)
 #pragma unroll
-            for (int e = 0; e < VEC / 2; ++e) w[e] = v[j][e];
-        else fetch(j, w);
+            for (int e = 0; e < 4; ++e) w[e] = v[j][e];
+        else product(j, w);
     }
 };
 
@@ -133,38 +194,40 @@ __device__ __forceinline__ float sum_of(uint64_t v)
     return f.x + f.y;
 }
 
-// Threads of a block at most, and blocks an SM: one vector of eight a thread wants many warps
-// of few registers; eight pairs a thread, each element in a register, need more than 128.
-template <int VEC, int NV>
-constexpr int kThreads = (VEC == 2 && NV == 8) || (VEC == 8 && NV == 1) ? 256 : 512;
-template <int T, int VEC, int NV>
-constexpr int kForwardBlocks = VEC == 8 && NV == 1 ? (T == GS_F32 ? 3 : 4) : 1;
-template <int T, int VEC, int NV>
-constexpr int kBackwardBlocks = VEC == 8 && NV == 1 ? (T == GS_F32 ? 2 : 3) : 1;
+// Threads of a block at most, and blocks an SM, which set the registers: one vector a thread
+// wants many warps of few.
+template <int T, int NV, bool WHOLE>
+constexpr int kForwardThreads = NV == 1 && T != GS_F32 && WHOLE ? 1024 : 512;
+template <int NV>
+constexpr int kBackwardThreads = NV == 1 ? 256 : 512;
+template <int T, int NV, bool WHOLE>
+constexpr int kBackwardBlocks = NV == 1 ? (T != GS_F32 && WHOLE ? 3 : 2) : 1;
 
-template <int T, int VEC, int NV>
-__global__ void __launch_bounds__(kThreads<VEC, NV>, kForwardBlocks<T, VEC, NV>) block_norm_kernel(const __grid_constant__ gs_block_norm_args a, int group)
+template <int T, int NV, bool WHOLE>
+__global__ void __launch_bounds__(kForwardThreads<T, NV, WHOLE>) block_norm_kernel(const __grid_constant__ gs_block_norm_args a, int group)
 {
-    constexpr int P = VEC / 2;
-    constexpr bool kAhead = VEC * NV == 8;   // the next row's loads before this one's work
+    constexpr int P = 4;
+    constexpr bool kAhead = NV == 1;   // the next row's loads before this one's work
     __shared__ float sm[32];
     wait_for_predecessor();
     const int lane = threadIdx.x % group, cols = (int)a.cols;
     const int64_t step = (int64_t)gridDim.x * (blockDim.x / group);
     const float inv_cols = 1.0f / (float)a.cols;
     const bool q8 = a.y_type == GS_E4M3 && a.y;
-    const Weight<VEC, NV> weight(a.weight, a.weight_type, nullptr, 0, lane, group, cols);
-    const Weight<VEC, NV> post(a.post_weight, a.post_type, a.gate_rows ? nullptr : a.gate, a.gate_type, lane, group, cols);
+    const Weight<NV> weight(a.weight, a.weight_type, nullptr, 0, lane, group, cols);
+    const Weight<NV> post(a.post_weight, a.post_type, a.gate_rows ? nullptr : a.gate, a.gate_type, lane, group, cols);
     const uint64_t scale = both(a.scale);
-    Cells<T, VEC> hr[NV], xr[NV], gr[NV];
+    const Source sh(a.h, a.ldh, T), sx(a.x, a.ldx, T), sg(a.gate, a.ldg, T);
+    const bool s_aligned = rows_aligned(a.s, a.lds, T), y_aligned = rows_aligned(a.y, a.ldy, a.y_type);
+    Cells<T, WHOLE> hr[NV], xr[NV], gr[NV];
     const auto load = [&](int64_t row) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = weight.col(j), n = cols - c;
             hr[j].zero(), xr[j].zero();
             if (row < a.rows && n > 0) {
-                hr[j].load(a.h, row * a.ldh + c, n, T);
-                xr[j].load(a.x, row * a.ldx + c, n, T);
+                fetch(hr[j], sh, row, a.rows, c, cols);
+                fetch(xr[j], sx, row, a.rows, c, cols);
             }
         }
     };
@@ -179,13 +242,13 @@ __global__ void __launch_bounds__(kThreads<VEC, NV>, kForwardBlocks<T, VEC, NV>)
             for (int j = 0; j < NV; ++j) {
                 const int c = weight.col(j), n = cols - c;
                 gr[j].zero();
-                if (here && n > 0) gr[j].load(a.gate, row * a.ldg + c, n, T);
+                if (here && n > 0) fetch(gr[j], sg, row, a.rows, c, cols);
             }
         uint64_t s[NV][P], x[NV][P], q = both(0.0f);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            hr[j].values(T, s[j]);
-            xr[j].values(T, x[j]);
+            values(hr[j], sh, row, a.rows, weight.col(j), cols, s[j]);
+            values(xr[j], sx, row, a.rows, weight.col(j), cols, x[j]);
 #pragma unroll
             for (int e = 0; e < P; ++e) q = fma2(s[j][e], s[j][e], q);
         }
@@ -206,7 +269,7 @@ __global__ void __launch_bounds__(kThreads<VEC, NV>, kForwardBlocks<T, VEC, NV>)
             for (int e = 0; e < P; ++e) s[j][e] = mul2(mul2(s[j][e], both(rstd_post)), p[e]);
             if (a.gate_rows) {
                 uint64_t g[P];
-                gr[j].values(T, g);
+                values(gr[j], sg, row, a.rows, c, cols, g);
 #pragma unroll
                 for (int e = 0; e < P; ++e) s[j][e] = mul2(s[j][e], g[e]);
             }
@@ -215,7 +278,7 @@ __global__ void __launch_bounds__(kThreads<VEC, NV>, kForwardBlocks<T, VEC, NV>)
                 s[j][e] = fma2(scale, x[j][e], s[j][e]);
                 q = fma2(s[j][e], s[j][e], q);
             }
-            if (here && n > 0) store_cells<VEC>(a.s, row * a.lds + c, n, T, s[j]);
+            if (here && n > 0) store(a.s, row * a.lds + c, n, T, s_aligned, s[j]);
             if (q8) {
                 uint64_t w[P];
                 weight.get(j, w);
@@ -247,7 +310,7 @@ __global__ void __launch_bounds__(kThreads<VEC, NV>, kForwardBlocks<T, VEC, NV>)
 #pragma unroll
                 for (int e = 0; e < P; ++e) s[j][e] = mul2(s[j][e], w[e]);
             }
-            if (here && n > 0) store_cells<VEC>(a.y, row * a.ldy + c, n, a.y_type, s[j]);
+            if (here && n > 0) store(a.y, row * a.ldy + c, n, a.y_type, y_aligned, s[j]);
         }
     }
 }
@@ -257,11 +320,11 @@ __global__ void __launch_bounds__(kThreads<VEC, NV>, kForwardBlocks<T, VEC, NV>)
 //   A = sum of g h rstd_post gives two of them where the gate is a vector: dgate = post A,
 //   dpost = gate A; where it is rows, dpost sums g h rstd_post gate.
 // partial: [3][blocks][cols]: dweight, dpost, dgate.
-template <int T, int TDY, int VEC, int NV>
-__global__ void __launch_bounds__(kThreads<VEC, NV>, kBackwardBlocks<T, VEC, NV>) block_norm_bwd_kernel(const __grid_constant__ gs_block_norm_bwd_args a,
-                                                                                                   int group, float* partial)
+template <int T, int TDY, int NV, bool WHOLE>
+__global__ void __launch_bounds__(kBackwardThreads<NV>, kBackwardBlocks<T, NV, WHOLE>) block_norm_bwd_kernel(const __grid_constant__ gs_block_norm_bwd_args a,
+                                                                                               int group, float* partial)
 {
-    constexpr int P = VEC / 2;
+    constexpr int P = 4;
     extern __shared__ float part[];   // [groups][columns rounded up] when a block holds several groups
     __shared__ float sm[32];
     wait_for_predecessor();
@@ -269,9 +332,11 @@ __global__ void __launch_bounds__(kThreads<VEC, NV>, kBackwardBlocks<T, VEC, NV>
     const float inv_cols = 1.0f / (float)a.cols;
     const bool post = a.post_weight != nullptr;
     const void* gate = a.gate_rows ? nullptr : a.gate;
-    const Weight<VEC, NV> weight(a.weight, a.weight_type, nullptr, 0, lane, group, cols);
-    const Weight<VEC, NV> post_weight(a.post_weight, a.post_type, gate, a.gate_type, lane, group, cols);
+    const Weight<NV> weight(a.weight, a.weight_type, nullptr, 0, lane, group, cols);
+    const Weight<NV> post_weight(a.post_weight, a.post_type, gate, a.gate_type, lane, group, cols);
     const uint64_t scale = both(a.scale);
+    const Source sy(a.dy, a.lddy, a.dy_type), ss(a.s, a.lds, T), sd(a.ds, a.ldds, T), sh(a.h, a.ldh, T), sg(a.gate, a.ldg, T);
+    const bool dx_aligned = rows_aligned(a.dx, a.lddx, T), dh_aligned = rows_aligned(a.dh, a.lddh, T), dg_aligned = rows_aligned(a.dgate, a.lddg, T);
     uint64_t acc[2][NV][P];
 #pragma unroll
     for (int k = 0; k < 2; ++k)
@@ -282,8 +347,8 @@ __global__ void __launch_bounds__(kThreads<VEC, NV>, kBackwardBlocks<T, VEC, NV>
     for (int64_t row0 = (int64_t)blockIdx.x * groups; row0 < a.rows; row0 += (int64_t)gridDim.x * groups) {
         const int64_t row = row0 + threadIdx.x / group;
         const bool here = row < a.rows;
-        Cells<T, VEC> hr[NV], sr[NV], dr[NV], gr[NV];
-        Cells<TDY, VEC> yr[NV];
+        Cells<T, WHOLE> hr[NV], sr[NV], dr[NV], gr[NV];
+        Cells<TDY, WHOLE> yr[NV];
         const float rstd = a.dy && here ? a.rstd[row] : 0.0f, rstd_post = post && here ? a.rstd_post[row] : 1.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -291,12 +356,12 @@ __global__ void __launch_bounds__(kThreads<VEC, NV>, kBackwardBlocks<T, VEC, NV>
             hr[j].zero(), sr[j].zero(), dr[j].zero(), gr[j].zero(), yr[j].zero();
             if (here && n > 0) {
                 if (a.dy) {
-                    yr[j].load(a.dy, row * a.lddy + c, n, a.dy_type);
-                    sr[j].load(a.s, row * a.lds + c, n, T);
+                    fetch(yr[j], sy, row, a.rows, c, cols);
+                    fetch(sr[j], ss, row, a.rows, c, cols);
                 }
-                if (a.ds) dr[j].load(a.ds, row * a.ldds + c, n, T);
-                if (post || a.dgate) hr[j].load(a.h, row * a.ldh + c, n, T);
-                if (a.gate_rows) gr[j].load(a.gate, row * a.ldg + c, n, T);
+                if (a.ds) fetch(dr[j], sd, row, a.rows, c, cols);
+                if (post || a.dgate) fetch(hr[j], sh, row, a.rows, c, cols);
+                if (a.gate_rows) fetch(gr[j], sg, row, a.rows, c, cols);
             }
         }
         uint64_t g[NV][P], q = both(0.0f);   // g: dy * weight, the gradient of s, that of h / rms(h)
@@ -306,8 +371,8 @@ __global__ void __launch_bounds__(kThreads<VEC, NV>, kBackwardBlocks<T, VEC, NV>
             for (int j = 0; j < NV; ++j) {
                 uint64_t s[P], dy[P], w[P];
                 weight.get(j, w);
-                sr[j].values(T, s);
-                yr[j].values(a.dy_type, dy);
+                values(sr[j], ss, row, a.rows, weight.col(j), cols, s);
+                values(yr[j], sy, row, a.rows, weight.col(j), cols, dy);
 #pragma unroll
                 for (int e = 0; e < P; ++e) {
                     acc[0][j][e] = fma2(dy[e], mul2(s[e], both(rstd)), acc[0][j][e]);
@@ -324,11 +389,11 @@ __global__ void __launch_bounds__(kThreads<VEC, NV>, kBackwardBlocks<T, VEC, NV>
             const bool there = here && n > 0;
             uint64_t h[P], v[P], w[P];
             post_weight.get(j, w);   // with the gate's vector
-            hr[j].values(T, h);
-            dr[j].values(T, v);
+            values(hr[j], sh, row, a.rows, c, cols, h);
+            values(dr[j], sd, row, a.rows, c, cols, v);
             if (a.dy) {
                 uint64_t s[P];
-                sr[j].values(T, s);
+                values(sr[j], ss, row, a.rows, c, cols, s);
 #pragma unroll
                 for (int e = 0; e < P; ++e) g[j][e] = fma2(both(rstd), fma2(s[e], both(c2), g[j][e]), v[e]);
             } else
@@ -337,15 +402,15 @@ __global__ void __launch_bounds__(kThreads<VEC, NV>, kBackwardBlocks<T, VEC, NV>
             if (a.dx && there) {
 #pragma unroll
                 for (int e = 0; e < P; ++e) v[e] = mul2(scale, g[j][e]);
-                store_cells<VEC>(a.dx, row * a.lddx + c, n, T, v);
+                store(a.dx, row * a.lddx + c, n, T, dx_aligned, v);
             }
             if (a.gate_rows) {
                 uint64_t gates[P];
-                gr[j].values(T, gates);
+                values(gr[j], sg, row, a.rows, c, cols, gates);
                 if (a.dgate && there) {
 #pragma unroll
                     for (int e = 0; e < P; ++e) v[e] = mul2(g[j][e], mul2(mul2(h[e], both(rstd_post)), w[e]));
-                    store_cells<VEC>(a.dgate, row * a.lddg + c, n, T, v);
+                    store(a.dgate, row * a.lddg + c, n, T, dg_aligned, v);
                 }
 #pragma unroll
                 for (int e = 0; e < P; ++e) g[j][e] = mul2(g[j][e], gates[e]);
@@ -364,23 +429,23 @@ __global__ void __launch_bounds__(kThreads<VEC, NV>, kBackwardBlocks<T, VEC, NV>
             const int c = weight.col(j), n = cols - c;
             if (post) {
                 uint64_t h[P];
-                hr[j].values(T, h);
+                values(hr[j], sh, row, a.rows, c, cols, h);
 #pragma unroll
                 for (int e = 0; e < P; ++e) g[j][e] = mul2(both(rstd_post), fma2(h[e], both(c2), g[j][e]));
             }
-            if (here && n > 0) store_cells<VEC>(a.dh, row * a.lddh + c, n, T, g[j]);
+            if (here && n > 0) store(a.dh, row * a.lddh + c, n, T, dh_aligned, g[j]);
         }
     }
     const auto write = [&](int which, const uint64_t (&v)[NV][P], const void* by, int by_type) {
         float* out = partial + ((int64_t)which * gridDim.x + blockIdx.x) * a.cols;
-        const int width = NV * group * VEC;
+        const int width = NV * group * 8;
         float* mine = groups == 1 ? out : part + (threadIdx.x / group) * width;
         __syncthreads();   // the sums before have been read
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = weight.col(j);
             uint64_t w[P];
-            load_weight<VEC>(by, c, cols - c, by_type, w);
+            load_weight(by, c, cols - c, by_type, w);
 #pragma unroll
             for (int e = 0; e < P; ++e) {
                 const float2 f = unpair(mul2(v[j][e], w[e]));
@@ -407,26 +472,21 @@ using Type = std::integral_constant<int, V>;
 struct Shape {
     int nv, group, threads;
 };
-// Vectors of eight: one a thread within a warp, two where that keeps a row within it, then as
-// many as 512 threads need.  Pairs: two a thread for rows within a warp, else eight (256
-// threads at most), or sixteen.
-Shape shape_for(int64_t cols, bool vec, bool forward)
+// One vector a thread up to `widest` threads, then two or four.
+Shape shape_for(int64_t cols, int widest)
 {
-    const int64_t n = vec ? (cols + 7) / 8 : (cols + 1) / 2;
+    const int64_t n = (cols + 7) / 8;
     Shape s;
-    if (vec) s.nv = n <= 32 ? 1 : (n <= 1024 ? 2 : 4);
-    else s.nv = n <= 64 ? 2 : (n <= 2048 ? 8 : 16);
+    s.nv = n <= widest ? 1 : (n <= 1024 ? 2 : 4);
     s.group = 1;
     while ((int64_t)s.group * s.nv < n) s.group *= 2;
-    s.threads = s.group > (forward ? 32 : 256) ? s.group : 256;
+    s.threads = s.group < 256 ? 256 : s.group;
     return s;
 }
 
 bool norm_sizes_ok(int64_t rows, int64_t cols, int type) { return size_ok(rows, 0) && size_ok(cols, 1) && cols <= GS_NORM_MAX_COLS && type_float(type); }
 
 bool weight_ok(const void* p, int type) { return !p || (type_float(type) && vec_ok(p, type)); }
-
-bool weight16(const void* p) { return !p || aligned16(p); }
 
 }  // namespace
 }  // namespace gs
@@ -455,23 +515,21 @@ extern "C" gs_status gs_block_norm(const gs_block_norm_args* args, void* stream)
     if (a.weight && !mat_ok(a.y, a.ldy, a.cols, a.y_type)) return GS_ERR_INVALID_ARG;
     const int sms = device_sms();
     if (sms <= 0) return GS_ERR_CUDA;
-    const bool vec = a.cols % 8 == 0 && rows16(a.h, a.ldh, a.type) && rows16(a.x, a.ldx, a.type) && rows16(a.s, a.lds, a.type) &&
-                     weight16(a.post_weight) && weight16(a.weight) && (a.gate_rows ? rows16(a.gate, a.ldg, a.type) : weight16(a.gate)) &&
-                     (!a.weight || (a.y_type == GS_E4M3 ? ((uintptr_t)a.y & 7u) == 0 && a.ldy % 8 == 0 : rows16(a.y, a.ldy, a.y_type)));
-    const Shape s = shape_for(a.cols, vec, true);
+    const bool whole = a.cols % 8 == 0 && a.cols <= 8192 && rows16(a.h, a.ldh, a.type) && rows16(a.x, a.ldx, a.type) &&
+                       (!a.gate_rows || rows16(a.gate, a.ldg, a.type));
+    const Shape s = shape_for(a.cols, a.type == GS_F32 || !whole ? 512 : 1024);
     const int64_t rpb = s.threads / s.group, want = (a.rows + rpb - 1) / rpb, most = (int64_t)sms * (1024 / s.threads);
     const int grid = (int)(want < most ? want : most);
     cudaStream_t st = (cudaStream_t)stream;
     const auto run = [&](auto t) -> gs_status {
         constexpr int T = decltype(t)::value;
-#define GS_FWD(V, N) return launch_after(block_norm_kernel<T, V, N>, dim3(grid), s.threads, 0, 1, st, a, s.group)
-        if (vec) {
-            if (s.nv == 1) GS_FWD(8, 1);
-            else if (s.nv == 2) GS_FWD(8, 2);
-            else GS_FWD(8, 4);
-        } else if (s.nv == 2) GS_FWD(2, 2);
-        else if (s.nv == 8) GS_FWD(2, 8);
-        else GS_FWD(2, 16);
+#define GS_FWD(N, W) return launch_after(block_norm_kernel<T, N, W>, dim3(grid), s.threads, 0, 1, st, a, s.group)
+        if (whole) {
+            if (s.nv == 1) GS_FWD(1, true);
+            else GS_FWD(2, true);
+        } else if (s.nv == 1) GS_FWD(1, false);
+        else if (s.nv == 2) GS_FWD(2, false);
+        else GS_FWD(4, false);
 #undef GS_FWD
     };
     if (a.type == GS_F32) return run(Type<GS_F32>());
@@ -516,31 +574,27 @@ extern "C" gs_status gs_block_norm_bwd(const gs_block_norm_bwd_args* args, void*
         return GS_ERR_INVALID_ARG;
     if (!a.dx && !a.dh && !a.dweight && !a.dpost && !a.dgate) return GS_OK;
     if (sms <= 0) return GS_ERR_CUDA;
-    const auto wide = [&](const void* p, int64_t ld, bool used, int type) { return !used || rows16(p, ld, type); };
-    const bool same = !a.dy || a.dy_type == a.type;   // dy of another type goes by pairs
-    const bool vec = same && a.cols % 8 == 0 && wide(a.dy, a.lddy, a.dy, a.dy_type) && wide(a.s, a.lds, a.dy, a.type) &&
-                     wide(a.ds, a.ldds, a.ds, a.type) && wide(a.h, a.ldh, reads_h, a.type) && wide(a.gate, a.ldg, row_gate, a.type) &&
-                     wide(a.dgate, a.lddg, row_dgate, a.type) && wide(a.dx, a.lddx, a.dx, a.type) && wide(a.dh, a.lddh, a.dh, a.type) &&
-                     weight16(a.weight) && weight16(a.post_weight) && (row_gate || weight16(a.gate));
-    const int v = vec ? 8 : 2;
-    const Shape s = shape_for(a.cols, vec, false);
+    const auto wide = [&](const void* p, int64_t ld, bool used) { return !used || rows16(p, ld, a.type); };
+    const bool same = !a.dy || a.dy_type == a.type;
+    const bool whole = same && a.cols % 8 == 0 && a.cols <= 8192 && wide(a.dy, a.lddy, a.dy) && wide(a.s, a.lds, a.dy) &&
+                       wide(a.ds, a.ldds, a.ds) && wide(a.h, a.ldh, reads_h) && wide(a.gate, a.ldg, row_gate);
+    const Shape s = shape_for(a.cols, 256);
     const int groups = s.threads / s.group;
     const int64_t want = (a.rows + groups - 1) / groups;
     const int grid = (int)(want < blocks ? want : blocks);
-    const size_t smem = groups > 1 && need ? (size_t)groups * s.nv * s.group * v * 4 : 0;   // at most 16 KB
+    const size_t smem = groups > 1 && need ? (size_t)groups * s.nv * s.group * 32 : 0;   // at most 16 KB
     float* part = (float*)ws;
     const auto run = [&](auto t, auto tdy) -> gs_status {
         constexpr int T = decltype(t)::value, TDY = decltype(tdy)::value;
-#define GS_BWD(V, N) return launch_after(block_norm_bwd_kernel<T, TDY, V, N>, dim3(grid), s.threads, smem, 1, st, a, s.group, part)
+#define GS_BWD(N, W) return launch_after(block_norm_bwd_kernel<T, TDY, N, W>, dim3(grid), s.threads, smem, 1, st, a, s.group, part)
         if constexpr (T == TDY)
-            if (vec) {
-                if (s.nv == 1) GS_BWD(8, 1);
-                else if (s.nv == 2) GS_BWD(8, 2);
-                else GS_BWD(8, 4);
+            if (whole) {
+                if (s.nv == 1) GS_BWD(1, true);
+                else GS_BWD(2, true);
             }
-        if (s.nv == 2) GS_BWD(2, 2);
-        else if (s.nv == 8) GS_BWD(2, 8);
-        else GS_BWD(2, 16);
+        if (s.nv == 1) GS_BWD(1, false);
+        else if (s.nv == 2) GS_BWD(2, false);
+        else GS_BWD(4, false);
 #undef GS_BWD
     };
     const auto pick = [&](auto t) -> gs_status {

@@ -35,10 +35,12 @@ __device__ __forceinline__ float group_reduce(float v, int group, float* sm)
         v = o < group ? Op::join(v, other) : v;
     }
     if (group <= 32) return v;
+    // the group's own barrier: other rows of the block go their way
     const int warp = threadIdx.x >> 5, first = threadIdx.x / group * (group >> 5), last = first + (group >> 5);
-    __syncthreads();   // the previous row's readers are done
+    const int barrier = 1 + threadIdx.x / group;   // at most 8 groups of 64 in a block
+    asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(group) : "memory");   // the previous row's readers are done
     if ((threadIdx.x & 31) == 0) sm[warp] = v;
-    __syncthreads();
+    asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(group) : "memory");
     float r = sm[first];
     for (int w = first + 1; w < last; ++w) r = Op::join(r, sm[w]);
     return r;
