@@ -26,7 +26,7 @@ namespace attn {
 namespace {
 
 constexpr int kThreads = 384, kTmemCols = 512;
-constexpr int kStatRows = kRows + 2;   // of a copy of row statistics, which starts on 16 bytes
+constexpr int kStatRows = kRows + 4;   // of a copy of row statistics, which starts on 16 bytes
 
 __device__ int g_attention_bwd_wait_expired;
 
@@ -34,26 +34,32 @@ struct Params {
     CUtensorMap q, k, v, d_o;
     Sequences seqs;
     Fill fill_dq, fill_dk, fill_dv;
-    const float2* stats;     // [key head][token][head of the group]: lse log2(e) (infinite for a row that sees no key), delta
+    const float* stats;      // [key head][token][head of the group], twice: kUp - lse log2(e) (-infinite for a row that sees no key), -delta
     const float* most;       // F16: the blocks' largest |do| and |v|
     int most_count;
     uint16_t *dq, *dk, *dv;
     int64_t dq_row, dq_head, dk_row, dk_head, dv_row, dv_head;
-    int64_t stat_pitch;      // of a key head
+    int64_t stat_pitch, stat_plane;   // of a key head; to the second plane
     float scale, scale2;     // scale2: scale log2(e)
     uint32_t kv_heads;
-    int tiles, group, tokens, dim, causal, zero, dq_vec, dk_vec, dv_vec;
+    int group, tokens, dim, causal, zero, dq_vec, dk_vec, dv_vec;
     uint32_t idesc_s, idesc_d;
 };
+
+// log2 of what p is held times.
+template <int T>
+constexpr float kUp = T == GS_F16 ? 12.0f : 0.0f;
+template <int T>
+constexpr float kDown = T == GS_F16 ? 0x1p-12f : 1.0f;
 
 // ------------------------------------------------------------------ row statistics
 struct StatParams {
     const uint16_t *o, *d_o, *v;
     int64_t o_row, o_head, do_row, do_head, v_row, v_head;
     const float* lse;
-    float2* stats;
+    float* stats;
     float* most;
-    int64_t q_rows, k_rows, stat_pitch;
+    int64_t q_rows, k_rows, stat_pitch, stat_plane;
     int heads, kv_heads, group, dim, vec;
 };
 
@@ -96,8 +102,9 @@ __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ Stat
         if (lane == 0 && i < lines) {
             const float lse = p.lse[i];
             // a row that sees no key: every p is 2^-infinity
-            p.stats[(h / p.group) * p.stat_pitch + r * p.group + h % p.group] =
-                make_float2(lse == -INFINITY ? INFINITY : lse * kLog2e, lse == -INFINITY ? 0.0f : sum);
+            float* to = p.stats + (h / p.group) * p.stat_pitch + r * p.group + h % p.group;
+            to[0] = lse == -INFINITY ? -INFINITY : __fmaf_rn(lse, -kLog2e, kUp<T>);
+            to[p.stat_plane] = lse == -INFINITY ? 0.0f : -sum;
         }
     }
     if (!p.most) return;
@@ -162,8 +169,8 @@ struct KeyShape {
     static constexpr uint32_t kTile = kChunks * kBox;
     static constexpr int kStagesQ = 3, kStagesO = DP == 128 ? 2 : 3;
     static constexpr uint32_t kAtQ = 2 * kTile, kAtO = kAtQ + kStagesQ * kTile, kAtStats = kAtO + kStagesO * kTile;
-    static constexpr uint32_t kStatBytes = kStatRows * 8;
-    static constexpr uint32_t kAtBars = kAtStats + 2 * kStatBytes;
+    static constexpr uint32_t kStatBytes = kStatRows * 4;   // of a plane
+    static constexpr uint32_t kAtBars = kAtStats + 4 * kStatBytes;
     static constexpr int kKV = 0, kQFull = 1, kQEmpty = kQFull + kStagesQ, kOFull = kQEmpty + kStagesQ, kOEmpty = kOFull + kStagesO,
                          kStatFull = kOEmpty + kStagesO, kStatEmpty = kStatFull + 2, kS = kStatEmpty + 2, kR = kS + 1, kP = kR + 1,
                          kDs = kP + 1, kClearQ = kDs + 1, kClearO = kClearQ + 1, kDone = kClearO + 1, kBars = kDone + 2;
@@ -197,7 +204,7 @@ __device__ __forceinline__ void load_queries(const Params& p, const KeyWork& w, 
     load_tile<S::kChunks>(smem, &p.k, w.head, w.seq.k0 + w.key0, bars + 8 * S::kKV);
     load_tile<S::kChunks>(smem + S::kTile, &p.v, w.head, w.seq.k0 + w.key0, bars + 8 * S::kKV);
     const uint32_t bytes = (uint32_t)(S::kChunks * p.tokens * p.group) * 128;
-    const float2* stats = p.stats + w.head * p.stat_pitch;
+    const float* stats = p.stats + w.head * p.stat_pitch;
     Ring<S::kStagesQ> rq;
     Ring<S::kStagesO> ro;
     Ring<2> rs;
@@ -212,12 +219,14 @@ __device__ __forceinline__ void load_queries(const Params& p, const KeyWork& w, 
         rq.next(), ++nq;
         ok = mbar_wait(bars + 8 * (S::kStatEmpty + rs.s), rs.parity ^ 1, gave_up);
         if (!ok) break;
-        mbar_expect(bars + 8 * (S::kStatFull + rs.s), S::kStatBytes);
-        const int64_t at = (int64_t)row * p.group & ~1ll;   // two statistics are 16 bytes
-        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                         smem + S::kAtStats + rs.s * S::kStatBytes),
-                     "l"(stats + at), "r"(S::kStatBytes), "r"(bars + 8 * (S::kStatFull + rs.s))
-                     : "memory");
+        mbar_expect(bars + 8 * (S::kStatFull + rs.s), 2 * S::kStatBytes);
+        const int64_t at = (int64_t)row * p.group & ~3ll;   // four are 16 bytes
+#pragma unroll
+        for (int plane = 0; plane < 2; ++plane)
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             smem + S::kAtStats + (2 * rs.s + plane) * S::kStatBytes),
+                         "l"(stats + plane * p.stat_plane + at), "r"(S::kStatBytes), "r"(bars + 8 * (S::kStatFull + rs.s))
+                         : "memory");
         rs.next(), ++ns;
         ok = mbar_wait(bars + 8 * (S::kOEmpty + ro.s), ro.parity ^ 1, gave_up);
         if (!ok) break;
@@ -299,12 +308,27 @@ __device__ __forceinline__ void issue_keys(const Params& p, const KeyWork& w, bo
     }
 }
 
-__device__ __forceinline__ float2 ld_shared_f2(uint32_t a)
+__device__ __forceinline__ float ld_shared_f1(uint32_t a)
 {
-    float2 v;
-    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
     return v;
 }
+
+// Four consecutive statistics from the one at `at`, which lies `odd` after a multiple of
+// four: a copy starts on 16 bytes, the tile's rows where they start.
+struct Stats4 {
+    uint64_t v[2];
+    __device__ __forceinline__ void load(uint32_t at, bool even)
+    {
+        if (even) {
+            const uint4 q = ld_shared16(at);
+            v[0] = pair(__uint_as_float(q.x), __uint_as_float(q.y)), v[1] = pair(__uint_as_float(q.z), __uint_as_float(q.w));
+        } else
+            v[0] = pair(ld_shared_f1(at), ld_shared_f1(at + 4)), v[1] = pair(ld_shared_f1(at + 8), ld_shared_f1(at + 12));
+    }
+};
+__device__ __forceinline__ uint64_t both(float v) { return pair(v, v); }
 
 // A key a thread (row r of the tile), 64 columns: half 0 or 1.
 template <int T, int DP>
@@ -312,8 +336,7 @@ __device__ __forceinline__ void key_terms(const Params& p, const KeyWork& w, int
                                           int exponent, volatile int* gave_up)
 {
     using S = KeyShape<DP>;
-    constexpr float kUp = T == GS_F16 ? 12.0f : 0.0f;   // p times 2^12
-    const float by_ds = power2(exponent) * (T == GS_F16 ? 0x1p-12f : 1.0f);
+    const uint64_t by_ds = both(power2(exponent) * kDown<T>), scale2 = both(p.scale2);
     const int key = w.key0 + r;
     bool ok = true;
     Ring<2> rs;
@@ -321,34 +344,39 @@ __device__ __forceinline__ void key_terms(const Params& p, const KeyWork& w, int
         const int t0 = w.first + i * p.tokens;
         // columns of this tile that count for this key: from the first query that sees it to the last of the sequence
         const int rows = (w.seq.lq - t0) * p.group, full = p.tokens * p.group, to = (rows < full ? rows : full) - half * 64;
-        int from = (first_query(w.seq, key, p.causal) - t0) * p.group - half * 64;
+        const int from = (first_query(w.seq, key, p.causal) - t0) * p.group - half * 64;
         const bool cut = to < 64 || __any_sync(0xffffffffu, from > 0);
-        const int odd = (int)(((int64_t)(w.seq.q0 + t0) * p.group) & 1);
-        const uint32_t stats = smem + S::kAtStats + rs.s * S::kStatBytes + (uint32_t)(odd + half * 64) * 8;
+        const uint32_t odd = (uint32_t)((int64_t)(w.seq.q0 + t0) * p.group) & 3;
+        const uint32_t stats = smem + S::kAtStats + 2 * rs.s * S::kStatBytes + (odd + (uint32_t)half * 64) * 4;
         ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (S::kStatFull + rs.s), rs.parity, gave_up) &&
                                          mbar_wait(bars + 8 * S::kS, i & 1, gave_up));
         if (!ok) break;
         tc_fence_after();
         uint32_t s[64];
         tmem_ld32(tmem + half * 64, s);
-        tmem_ld32(tmem + half * 64 + 32, s + 32);
         tmem_ld32_wait(s);
-        tmem_ld32_wait(s + 32);
 #pragma unroll
         for (int c = 0; c < 64; c += 32) {
+            if (c == 0) tmem_ld32(tmem + half * 64 + 32, s + 32);   // on its way during the first terms
+#pragma unroll
+            for (int e = c; e < c + 32; e += 4) {
+                Stats4 l;
+                l.load(stats + e * 4, odd == 0);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float2 x = unpair(fma2(pair(__uint_as_float(s[e + 2 * k]), __uint_as_float(s[e + 2 * k + 1])), scale2, l.v[k]));
+                    s[e + 2 * k] = __float_as_uint(exp2_fast(x.x)), s[e + 2 * k + 1] = __float_as_uint(exp2_fast(x.y));
+                }
+            }
+            if (cut) {
+#pragma unroll
+                for (int e = c; e < c + 32; ++e)
+                    if (e < from || e >= to) s[e] = 0;
+            }
             uint32_t h[16];
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-                const float l0 = ld_shared_f2(stats + (c + e) * 8).x, l1 = ld_shared_f2(stats + (c + e + 1) * 8).x;
-                float a = exp2_fast(__fmaf_rn(__uint_as_float(s[c + e]), p.scale2, kUp - l0));
-                float b = exp2_fast(__fmaf_rn(__uint_as_float(s[c + e + 1]), p.scale2, kUp - l1));
-                if (cut) {
-                    if (c + e < from || c + e >= to) a = 0.0f;
-                    if (c + e + 1 < from || c + e + 1 >= to) b = 0.0f;
-                }
-                s[c + e] = __float_as_uint(a), s[c + e + 1] = __float_as_uint(b);
-                h[e / 2] = pack_half2(a, b, T);
-            }
+            for (int e = 0; e < 16; ++e) h[e] = pack_half2(__uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1]), T);
+            if (c == 0) tmem_ld32_wait(s + 32);   // before the terms take columns' place
             tmem_st16(tmem + half * 64 + c / 2, h);
         }
         tmem_st_wait();
@@ -358,23 +386,32 @@ __device__ __forceinline__ void key_terms(const Params& p, const KeyWork& w, int
         ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * S::kR, i & 1, gave_up));
         if (!ok) break;
         tc_fence_after();
-        uint32_t h[32];
+        uint32_t h[32], d[64];
+        tmem_ld32(tmem + kTmemR + half * 64, d);
+        tmem_ld32_wait(d);
 #pragma unroll
         for (int c = 0; c < 64; c += 32) {
-            uint32_t d[32];
-            tmem_ld32(tmem + kTmemR + half * 64 + c, d);
-            tmem_ld32_wait(d);
+            if (c == 0) tmem_ld32(tmem + kTmemR + half * 64 + 32, d + 32);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-                const float d0 = ld_shared_f2(stats + (c + e) * 8).y, d1 = ld_shared_f2(stats + (c + e + 1) * 8).y;
-                float a = __uint_as_float(s[c + e]) * ((__uint_as_float(d[e]) - d0) * by_ds);
-                float b = __uint_as_float(s[c + e + 1]) * ((__uint_as_float(d[e + 1]) - d1) * by_ds);
-                if (cut) {   // 0 times whatever the hidden rows give
-                    if (c + e < from || c + e >= to) a = 0.0f;
-                    if (c + e + 1 < from || c + e + 1 >= to) b = 0.0f;
+            for (int e = c; e < c + 32; e += 4) {
+                Stats4 l;
+                l.load(stats + S::kStatBytes + e * 4, odd == 0);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint64_t x = add2(pair(__uint_as_float(d[e + 2 * k]), __uint_as_float(d[e + 2 * k + 1])), l.v[k]);
+                    if constexpr (T == GS_F16) x = mul2(x, by_ds);
+                    const float2 f = unpair(mul2(x, pair(__uint_as_float(s[e + 2 * k]), __uint_as_float(s[e + 2 * k + 1]))));
+                    d[e + 2 * k] = __float_as_uint(f.x), d[e + 2 * k + 1] = __float_as_uint(f.y);
                 }
-                h[(c + e) / 2] = pack_half2(a, b, T);
             }
+            if (cut) {   // 0 times whatever the hidden rows give
+#pragma unroll
+                for (int e = c; e < c + 32; ++e)
+                    if (e < from || e >= to) d[e] = 0;
+            }
+#pragma unroll
+            for (int e = c; e < c + 32; e += 2) h[e / 2] = pack_half2(__uint_as_float(d[e]), __uint_as_float(d[e + 1]), T);
+            if (c == 0) tmem_ld32_wait(d + 32);
         }
         tmem_st32(tmem + kTmemR + half * 64, h);
         tmem_st_wait();
@@ -391,7 +428,7 @@ __device__ __forceinline__ void key_terms(const Params& p, const KeyWork& w, int
     // the first warps write dV, the others dK
     const bool live = key < w.seq.lk;
     const int64_t row = w.seq.k0 + key;
-    const float by = half == 0 ? (T == GS_F16 ? 0x1p-12f : 1.0f) : p.scale * power2(-exponent);
+    const float by = half == 0 ? kDown<T> : p.scale * power2(-exponent);
     uint16_t* to = half == 0 ? p.dv + row * p.dv_row + w.head * p.dv_head : p.dk + row * p.dk_row + w.head * p.dk_head;
 #pragma unroll 1
     for (int c = 0; c < DP; c += 32) {
@@ -473,32 +510,35 @@ __global__ void __launch_bounds__(kThreads, 1) keys_kernel(const __grid_constant
 }
 
 // ------------------------------------------------------------------ dq
-// A CTA two tiles of packed query rows, which take turns as in the forward.  TMEM lanes
+// A CTA one or two tiles of packed query rows; two take turns as in the forward.  TMEM lanes
 // are query rows: S = Q K^T; P in registers; R = dO V^T in S's place; dS in 16 bits in
-// its place; dQ += dS K.
-template <int DP>
+// its place; dQ += dS K.  Values are done with early, keys late: rings of their own.
+template <int DP, int TILES>
 struct QueryShape {
     static constexpr int kChunks = DP / 64;
     static constexpr uint32_t kTile = kChunks * kBox;
-    static constexpr int kStages = DP == 128 ? 3 : 6;   // keys and values in turn
-    static constexpr uint32_t kAtRing = 4 * kTile, kAtBars = kAtRing + kStages * kTile;
-    static constexpr int kQFull = 0, kFull = 2, kEmpty = kFull + kStages, kS = kEmpty + kStages, kP = kS + 2, kR = kP + 2, kDs = kR + 2,
-                         kClear = kDs + 2, kDone = kClear + 1, kBars = kDone + 2;
+    static constexpr int kStagesK = DP == 128 ? 2 : 3, kStagesV = DP == 128 ? 1 : 2;
+    static constexpr int kTermWarps = 4 * TILES, kThreads = (kTermWarps + 4) * 32;
+    static constexpr uint32_t kTmemCols = 256 * TILES, kTmemDq = 128 * TILES;
+    static constexpr uint32_t kAtK = 2 * TILES * kTile, kAtV = kAtK + kStagesK * kTile, kAtBars = kAtV + kStagesV * kTile;
+    static constexpr int kQFull = 0, kKFull = 2, kKEmpty = kKFull + kStagesK, kVFull = kKEmpty + kStagesK, kVEmpty = kVFull + kStagesV,
+                         kS = kVEmpty + kStagesV, kP = kS + 2, kR = kP + 2, kDs = kR + 2, kClear = kDs + 2, kDone = kClear + 1,
+                         kBars = kDone + 2;
     static constexpr int kSmem = kAtBars + ((kBars * 8 + 15) & ~15) + 16;
     static_assert(kSmem <= 232448, "shared memory of an SM");
 };
-constexpr uint32_t kTmemDq = 256;
 
 struct QueryWork {
     Sequence seq;
     uint32_t head;
     int t0, n[2];
 };
+template <int TILES>
 __device__ __forceinline__ bool find_queries(const Params& p, QueryWork& w)
 {
     uint32_t unit, units;
     w.head = blockIdx.x % p.kv_heads;
-    const int tokens = p.tokens * p.tiles;
+    const int tokens = p.tokens * TILES;
     if (!find_unit<false>(p.seqs, blockIdx.x / p.kv_heads, tokens, w.seq, unit, units)) return false;
     if (p.causal) unit = units - 1 - unit;   // the longest first
     w.t0 = (int)unit * tokens;
@@ -507,62 +547,67 @@ __device__ __forceinline__ bool find_queries(const Params& p, QueryWork& w)
         const int t = w.t0 + i * p.tokens;
         int last = t + p.tokens - 1;
         last = last < w.seq.lq ? last : w.seq.lq - 1;
-        w.n[i] = i < p.tiles && t < w.seq.lq ? (keys_seen(w.seq, last, p.causal) + kRows - 1) / kRows : 0;
+        w.n[i] = i < TILES && t < w.seq.lq ? (keys_seen(w.seq, last, p.causal) + kRows - 1) / kRows : 0;
     }
     return true;
 }
 
-// The order of the ring: K(0), V(0), K(1), V(1), ...
-template <int DP>
+template <int DP, int TILES>
 __device__ __forceinline__ void load_keys(const Params& p, const QueryWork& w, int n, uint32_t smem, uint32_t bars, volatile int* gave_up)
 {
-    using S = QueryShape<DP>;
+    using S = QueryShape<DP, TILES>;
     const uint32_t bytes = (uint32_t)(S::kChunks * p.tokens * p.group) * 128;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < TILES; ++i)
         if (w.n[i] > 0) {
             const int row = w.seq.q0 + w.t0 + i * p.tokens, head = w.head * p.group;
             mbar_expect(bars + 8 * (S::kQFull + i), 2 * bytes);
             load_tile<S::kChunks>(smem + 2 * i * S::kTile, &p.q, head, row, bars + 8 * (S::kQFull + i));
             load_tile<S::kChunks>(smem + (2 * i + 1) * S::kTile, &p.d_o, head, row, bars + 8 * (S::kQFull + i));
         }
-    Ring<S::kStages> ring;
-    uint32_t issued = 0;
+    Ring<S::kStagesK> rk;
+    Ring<S::kStagesV> rv;
+    uint32_t nk = 0, nv = 0;
     int row = w.seq.k0;
-    for (int j = 0; j < 2 * n; ++j, ++issued, ring.next()) {
-        if (!mbar_wait(bars + 8 * (S::kEmpty + ring.s), ring.parity ^ 1, gave_up)) break;
-        mbar_expect(bars + 8 * (S::kFull + ring.s), S::kTile);
-        load_tile<S::kChunks>(smem + S::kAtRing + ring.s * S::kTile, j & 1 ? &p.v : &p.k, w.head, row, bars + 8 * (S::kFull + ring.s));
-        if (j & 1) row += kRows;
+    for (int j = 0; j < n; ++j, row += kRows) {
+        if (!mbar_wait(bars + 8 * (S::kKEmpty + rk.s), rk.parity ^ 1, gave_up)) break;
+        mbar_expect(bars + 8 * (S::kKFull + rk.s), S::kTile);
+        load_tile<S::kChunks>(smem + S::kAtK + rk.s * S::kTile, &p.k, w.head, row, bars + 8 * (S::kKFull + rk.s));
+        rk.next(), ++nk;
+        if (!mbar_wait(bars + 8 * (S::kVEmpty + rv.s), rv.parity ^ 1, gave_up)) break;
+        mbar_expect(bars + 8 * (S::kVFull + rv.s), S::kTile);
+        load_tile<S::kChunks>(smem + S::kAtV + rv.s * S::kTile, &p.v, w.head, row, bars + 8 * (S::kVFull + rv.s));
+        rv.next(), ++nv;
     }
     // the block does not leave before its copies have landed
     bool landed = true;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) landed = landed && (w.n[i] == 0 || mbar_wait_alone(bars + 8 * (S::kQFull + i), 0));
-    last_copies<S::kStages>(issued, [&](uint32_t s, uint32_t parity) { landed = landed && mbar_wait_alone(bars + 8 * (S::kFull + s), parity); });
+    for (int i = 0; i < TILES; ++i) landed = landed && (w.n[i] == 0 || mbar_wait_alone(bars + 8 * (S::kQFull + i), 0));
+    last_copies<S::kStagesK>(nk, [&](uint32_t s, uint32_t parity) { landed = landed && mbar_wait_alone(bars + 8 * (S::kKFull + s), parity); });
+    last_copies<S::kStagesV>(nv, [&](uint32_t s, uint32_t parity) { landed = landed && mbar_wait_alone(bars + 8 * (S::kVFull + s), parity); });
 }
 
 // Keys behind the sequence are contracted over in dQ: zero, by the loading warp, once all
 // copies are under way.
-template <int DP>
+template <int DP, int TILES>
 __device__ __forceinline__ void clear_keys(const QueryWork& w, int n, uint32_t smem, uint32_t bars, int lane, volatile int* gave_up)
 {
-    using S = QueryShape<DP>;
+    using S = QueryShape<DP, TILES>;
     const int live = w.seq.lk - (n - 1) * kRows;
     if (live >= kRows || *gave_up) return;
-    const uint32_t copy = 2 * n - 2;
-    if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * (S::kFull + copy % S::kStages), copy / S::kStages & 1, gave_up))) return;
-    zero_rows<S::kChunks>(smem + S::kAtRing + copy % S::kStages * S::kTile, live, lane);
+    const uint32_t copy = n - 1, s = copy % S::kStagesK;
+    if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * (S::kKFull + s), copy / S::kStagesK & 1, gave_up))) return;
+    zero_rows<S::kChunks>(smem + S::kAtK + s * S::kTile, live, lane);
     if (lane == 0) mbar_arrive(bars + 8 * S::kClear);
 }
 
 // A lane issues the products of tile i: R(j) once P(j) is in registers, dQ(j) once dS(j) is
 // written and, right behind it, S(j + 1) in dS's place.
-template <int DP>
+template <int DP, int TILES>
 __device__ __forceinline__ void issue_queries(const Params& p, const QueryWork& w, int i, int n, uint32_t smem, uint32_t bars, uint32_t tmem,
                                               volatile int* gave_up)
 {
-    using S = QueryShape<DP>;
+    using S = QueryShape<DP, TILES>;
     const int mine = i ? w.n[1] : w.n[0];
     const uint32_t steps = (uint32_t)(p.dim + 15) / 16, here = tmem + i * 128;
     const bool ragged = w.seq.lk < n * kRows;
@@ -574,64 +619,63 @@ __device__ __forceinline__ void issue_queries(const Params& p, const QueryWork& 
             if (s < steps) mma<false, false>(here, a + at, kDescHi, b + at, kDescHi, p.idesc_s, s > 0);
         }
     };
-    const auto landed = [&](const Ring<S::kStages>& r) { return mbar_wait(bars + 8 * (S::kFull + r.s), r.parity, gave_up); };
-    Ring<S::kStages> ring;
-    uint32_t keys = 0;
-    if (mine > 0) {
-        if (!mbar_wait(bars + 8 * (S::kQFull + i), 0, gave_up) || !landed(ring)) return;
-        if (ragged && n == 1 && !mbar_wait(bars + 8 * S::kClear, 0, gave_up)) return;
-        rows_product(smem + 2 * i * S::kTile, smem + S::kAtRing);
+    const auto keys_landed = [&](const Ring<S::kStagesK>& r) { return mbar_wait(bars + 8 * (S::kKFull + r.s), r.parity, gave_up); };
+    const auto values_landed = [&](const Ring<S::kStagesV>& r) { return mbar_wait(bars + 8 * (S::kVFull + r.s), r.parity, gave_up); };
+    // the rows are cleared behind the last copies, which wait for products before these
+    const auto cleared = [&](int j) { return !ragged || j + 1 < n || mbar_wait(bars + 8 * S::kClear, 0, gave_up); };
+    Ring<S::kStagesK> rk;
+    Ring<S::kStagesV> rv;
+    const auto scores = [&](int j) {
+        if (!cleared(j)) return false;
+        rows_product(smem + 2 * i * S::kTile, smem + S::kAtK + rk.s * S::kTile);
         mma_commit<false>(bars + 8 * (S::kS + i));
-        ring.next();
-    }
+        return true;
+    };
+    if (mine > 0 && (!mbar_wait(bars + 8 * (S::kQFull + i), 0, gave_up) || !keys_landed(rk) || !scores(0))) return;
     for (int j = 0; j < mine; ++j) {
-        const uint32_t values = ring.s;
-        if (!landed(ring) || !mbar_wait(bars + 8 * (S::kP + i), j & 1, gave_up)) return;
+        if (!values_landed(rv) || !mbar_wait(bars + 8 * (S::kP + i), j & 1, gave_up)) return;
         tc_fence_after();
-        rows_product(smem + (2 * i + 1) * S::kTile, smem + S::kAtRing + values * S::kTile);
+        rows_product(smem + (2 * i + 1) * S::kTile, smem + S::kAtV + rv.s * S::kTile);
         mma_commit<false>(bars + 8 * (S::kR + i));
-        mma_commit<false>(bars + 8 * (S::kEmpty + values));
-        ring.next();
+        mma_commit<false>(bars + 8 * (S::kVEmpty + rv.s));
+        rv.next();
+        const uint32_t keys = rk.s;
+        rk.next();
         const bool more = j + 1 < mine;
-        const uint32_t next = ring.s;
-        if (more && !landed(ring)) return;
+        if (more && !keys_landed(rk)) return;
         if (!mbar_wait(bars + 8 * (S::kDs + i), j & 1, gave_up)) return;
         tc_fence_after();
-        const uint32_t b = desc_rows(smem + S::kAtRing + keys * S::kTile);
+        const uint32_t b = desc_rows(smem + S::kAtK + keys * S::kTile);
 #pragma unroll
         for (int s = 0; s < kRows / 16; ++s)
-            mma_tmem(tmem + kTmemDq + i * DP, here + s * 8, b + s * k_step(false), kDescHi, p.idesc_d, j > 0 || s > 0);
-        mma_commit<false>(bars + 8 * (S::kEmpty + keys));
-        if (more) {
-            // not before: the rows are cleared behind the last copy, which may want these keys' stage
-            if (ragged && j + 2 == n && !mbar_wait(bars + 8 * S::kClear, 0, gave_up)) return;
-            rows_product(smem + 2 * i * S::kTile, smem + S::kAtRing + next * S::kTile);
-            mma_commit<false>(bars + 8 * (S::kS + i));
-            ring.next();
-        }
-        keys = next;
+            mma_tmem(tmem + S::kTmemDq + i * DP, here + s * 8, b + s * k_step(false), kDescHi, p.idesc_d, j > 0 || s > 0);
+        if (more && !scores(j + 1)) return;
+        mma_commit<false>(bars + 8 * (S::kKEmpty + keys));
     }
     // copies that only the other tile reads: both lanes free a stage
-    for (int c = 2 * mine; c < 2 * n; ++c, ring.next()) {
-        if (!landed(ring)) return;
-        mbar_arrive(bars + 8 * (S::kEmpty + ring.s));
+    for (int j = mine; j < n; ++j, rk.next(), rv.next()) {
+        if (!keys_landed(rk)) return;
+        mbar_arrive(bars + 8 * (S::kKEmpty + rk.s));
+        if (!values_landed(rv)) return;
+        mbar_arrive(bars + 8 * (S::kVEmpty + rv.s));
     }
 }
 
 // A row a thread: i the tile, r the row.
-template <int T, int DP>
+template <int T, int DP, int TILES>
 __device__ __forceinline__ void query_terms(const Params& p, const QueryWork& w, int i, int r, uint32_t bars, uint32_t tmem, int exponent,
                                             volatile int* gave_up)
 {
-    using S = QueryShape<DP>;
+    using S = QueryShape<DP, TILES>;
     const int n = i ? w.n[1] : w.n[0], t0 = w.t0 + i * p.tokens;
     const int token = t0 + r / p.group;
     const bool live = r < p.tokens * p.group && token < w.seq.lq;
     const int64_t row = w.seq.q0 + token;
-    const float2 st = live ? p.stats[w.head * p.stat_pitch + row * p.group + r % p.group] : make_float2(INFINITY, 0.0f);
+    const float* st = p.stats + w.head * p.stat_pitch + row * p.group + r % p.group;
+    const uint64_t less = both(live ? st[0] - kUp<T> : -INFINITY), minus = both(live ? st[p.stat_plane] : 0.0f);   // p is no factor here
     const int seen = live ? keys_seen(w.seq, token, p.causal) : 0;
     const int all = keys_seen(w.seq, t0, p.causal);
-    const float by_ds = power2(exponent);
+    const uint64_t by_ds = both(power2(exponent)), scale2 = both(p.scale2);
     const uint32_t here = tmem + i * 128;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
@@ -647,27 +691,38 @@ __device__ __forceinline__ void query_terms(const Params& p, const QueryWork& w,
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(bars + 8 * (S::kP + i));   // read: R takes its place
 #pragma unroll
-        for (int c = 0; c < 128; ++c) s[c] = __float_as_uint(exp2_fast(__fmaf_rn(__uint_as_float(s[c]), p.scale2, -st.x)));
+        for (int c = 0; c < 128; c += 2) {
+            const float2 x = unpair(fma2(pair(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale2, less));
+            s[c] = __float_as_uint(exp2_fast(x.x)), s[c + 1] = __float_as_uint(exp2_fast(x.y));
+        }
         const int left = seen - j * kRows;
         const bool cut = (j + 1) * kRows > all;
         ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (S::kR + i), j & 1, gave_up));
         if (!ok) break;
         tc_fence_after();
+        uint32_t d[2][32];
+        tmem_ld32(here, d[0]);
+        tmem_ld32_wait(d[0]);
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
-            uint32_t d[32], h[16];
-            tmem_ld32(here + c, d);
-            tmem_ld32_wait(d);
+            uint32_t(&v)[32] = d[c / 32 & 1];
+            if (c < 96) tmem_ld32(here + c + 32, d[c / 32 + 1 & 1]);   // on its way during this part
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-                float a = __uint_as_float(s[c + e]) * ((__uint_as_float(d[e]) - st.y) * by_ds);
-                float b = __uint_as_float(s[c + e + 1]) * ((__uint_as_float(d[e + 1]) - st.y) * by_ds);
-                if (cut) {   // 0 whatever the hidden keys give
-                    if (c + e >= left) a = 0.0f;
-                    if (c + e + 1 >= left) b = 0.0f;
-                }
-                h[e / 2] = pack_half2(a, b, T);
+                uint64_t x = add2(pair(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), minus);
+                if constexpr (T == GS_F16) x = mul2(x, by_ds);
+                const float2 f = unpair(mul2(x, pair(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 1]))));
+                v[e] = __float_as_uint(f.x), v[e + 1] = __float_as_uint(f.y);
             }
+            if (cut) {   // 0 whatever the hidden keys give
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (c + e >= left) v[e] = 0;
+            }
+            uint32_t h[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) h[e] = pack_half2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]), T);
+            if (c < 96) tmem_ld32_wait(d[c / 32 + 1 & 1]);
             tmem_st16(here + c / 2, h);   // behind what has been read
         }
         tmem_st_wait();
@@ -685,7 +740,7 @@ __device__ __forceinline__ void query_terms(const Params& p, const QueryWork& w,
         float f[32];
         uint32_t v[32];
         if (n > 0) {
-            tmem_ld32(tmem + kTmemDq + i * DP + c, v);
+            tmem_ld32(tmem + S::kTmemDq + i * DP + c, v);
             tmem_ld32_wait(v);
         }
 #pragma unroll
@@ -695,10 +750,10 @@ __device__ __forceinline__ void query_terms(const Params& p, const QueryWork& w,
     tc_fence_before();
 }
 
-template <int T, int DP>
-__global__ void __launch_bounds__(kThreads, 1) queries_kernel(const __grid_constant__ Params p)
+template <int T, int DP, int TILES>
+__global__ void __launch_bounds__(QueryShape<DP, TILES>::kThreads, 3 - TILES) queries_kernel(const __grid_constant__ Params p)
 {
-    using S = QueryShape<DP>;
+    using S = QueryShape<DP, TILES>;
     extern __shared__ __align__(1024) char smem_raw[];
     const uint32_t smem = smem_addr(smem_raw);
     if (smem & 1023u) {
@@ -713,7 +768,8 @@ __global__ void __launch_bounds__(kThreads, 1) queries_kernel(const __grid_const
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kBars; ++i) {
             const bool warps = (i >= S::kP && i < S::kR) || (i >= S::kDs && i < S::kClear);
-            mbar_init(bars + 8 * i, warps ? 4 : (i >= S::kEmpty && i < S::kS ? 2 : 1));
+            const bool lanes = (i >= S::kKEmpty && i < S::kVFull) || (i >= S::kVEmpty && i < S::kS);
+            mbar_init(bars + 8 * i, warps ? 4 : (lanes ? TILES : 1));
         }
         *gave_up = 0;
         mbar_init_fence();
@@ -721,43 +777,44 @@ __global__ void __launch_bounds__(kThreads, 1) queries_kernel(const __grid_const
     wait_for_predecessor();
     if (p.zero) fill_rows(p.fill_dq, p.seqs.q_starts, p.seqs.count, p.seqs.q_rows);
     QueryWork w;
-    if (!find_queries(p, w)) return;   // the same for every warp
-    if (warp == 9) tmem_alloc<false>(smem_addr(tmem_slot), kTmemCols);
+    if (!find_queries<TILES>(p, w)) return;   // the same for every warp
+    if (warp == S::kTermWarps) tmem_alloc<false>(smem_addr(tmem_slot), S::kTmemCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int n = w.n[0] > w.n[1] ? w.n[0] : w.n[1];
-    if (warp >= 8) {
+    if (warp >= S::kTermWarps) {
         few_registers();
-        if (warp == 8) {
+        const int i = warp - S::kTermWarps - 1;
+        if (i < 0) {
             if (n > 0) {
-                if (elect_one()) load_keys<DP>(p, w, n, smem, bars, gave_up);
+                if (elect_one()) load_keys<DP, TILES>(p, w, n, smem, bars, gave_up);
                 __syncwarp();
-                clear_keys<DP>(w, n, smem, bars, lane, gave_up);
+                clear_keys<DP, TILES>(w, n, smem, bars, lane, gave_up);
             }
-        } else if (warp < 11 && elect_one()) {
-            issue_queries<DP>(p, w, warp - 9, n, smem, bars, tmem, gave_up);
-            mma_commit<false>(bars + 8 * (S::kDone + warp - 9));   // the block does not leave before its products are done
-            if (!mbar_wait_alone(bars + 8 * (S::kDone + warp - 9), 0)) *gave_up = 1;
+        } else if (i < TILES && elect_one()) {
+            issue_queries<DP, TILES>(p, w, i, n, smem, bars, tmem, gave_up);
+            mma_commit<false>(bars + 8 * (S::kDone + i));   // the block does not leave before its products are done
+            if (!mbar_wait_alone(bars + 8 * (S::kDone + i), 0)) *gave_up = 1;
         }
     } else {
-        many_registers<224>();
+        many_registers<TILES == 2 ? 224 : 200>();
         const int i = warp >> 2, exponent = ds_exponent<T>(p);
-        if (i < p.tiles && w.t0 + i * p.tokens < w.seq.lq)
-            query_terms<T, DP>(p, w, i, threadIdx.x & 127, bars, tmem + ((uint32_t)((warp & 3) * 32) << 16), exponent, gave_up);
+        if (w.t0 + i * p.tokens < w.seq.lq)
+            query_terms<T, DP, TILES>(p, w, i, threadIdx.x & 127, bars, tmem + ((uint32_t)((warp & 3) * 32) << 16), exponent, gave_up);
     }
     __syncthreads();
     if (threadIdx.x == 0 && *gave_up) atomicExch(&g_attention_bwd_wait_expired, 1);
-    if (warp == 9) {
+    if (warp == S::kTermWarps) {
         tc_fence_after();
-        tmem_free<false>(tmem, kTmemCols);
+        tmem_free<false>(tmem, S::kTmemCols);
     }
 }
 
 struct Plan {
     int group, tokens, tiles, dp, blocks;
-    int64_t query_items, key_items, stat_pitch;
+    int64_t query_items, key_items, stat_pitch, stat_plane;
     size_t stats, most, packs, bytes;
 };
 Plan plan_for(const gs_attention_bwd_args& a)
@@ -770,12 +827,15 @@ Plan plan_for(const gs_attention_bwd_args& a)
     const int64_t sms = known > 0 ? known : 152;
     const bool starts = a.q_starts != nullptr;
     const int64_t two = units_at_most(a.q_rows, a.sequences, starts, 2 * (int64_t)r.tokens);
-    r.tiles = two * a.kv_heads >= sms && a.q_rows > a.sequences * r.tokens ? 2 : 1;
+    // as in the forward: two CTAs an SM of 64 columns and fewer, whose shared memory allows it; of
+    // more, two tiles a CTA where there are CTAs enough all the same, and tokens for both
+    r.tiles = r.dp == 128 && two * a.kv_heads >= sms && a.q_rows > a.sequences * r.tokens ? 2 : 1;
     r.query_items = (r.tiles == 2 ? two : units_at_most(a.q_rows, a.sequences, starts, r.tokens)) * a.kv_heads;
     r.key_items = units_at_most(a.k_rows, a.sequences, starts, kRows) * a.kv_heads;
-    r.stat_pitch = round_up(a.q_rows * r.group, 2);
-    // the last copy of statistics reads up to a tile past the last row
-    r.stats = (size_t)round_up((a.kv_heads * r.stat_pitch + kStatRows) * 8, 256);
+    r.stat_pitch = round_up(a.q_rows * r.group, 4);
+    // the last copy of a plane's statistics reads up to a tile past the last row
+    r.stat_plane = round_up(a.kv_heads * r.stat_pitch + kStatRows, 64);
+    r.stats = (size_t)r.stat_plane * 8;
     const int64_t want = (a.q_rows * a.heads + 31) / 32, most = sms * (a.type == GS_F16 ? 2 : 8);
     r.blocks = (int)(want < 1 ? 1 : (want < most ? want : most));
     r.most = a.type == GS_F16 ? (size_t)round_up(r.blocks * 8, 256) : 0;
@@ -788,19 +848,22 @@ Plan plan_for(const gs_attention_bwd_args& a)
 }
 
 template <class K>
-gs_status launch_one(K* kernel, int smem, std::atomic<uint64_t>& done, int64_t items, const Params& p, cudaStream_t st)
+gs_status launch_one(K* kernel, int smem, int threads, std::atomic<uint64_t>& done, int64_t items, const Params& p, cudaStream_t st)
 {
     const gs_status s = allow_smem(kernel, smem, done);
-    return s != GS_OK ? s : launch_after(kernel, dim3((unsigned)items), kThreads, (size_t)smem, 1, st, p);
+    return s != GS_OK ? s : launch_after(kernel, dim3((unsigned)items), (unsigned)threads, (size_t)smem, 1, st, p);
 }
 template <int T, int DP>
 gs_status launch(const Params& p, const Plan& plan, cudaStream_t st)
 {
-    static std::atomic<uint64_t> keys_done{0}, queries_done{0};
+    static std::atomic<uint64_t> keys_done{0}, one_done{0}, two_done{0};
     gs_status s = GS_OK;
-    if (p.dk) s = launch_one(keys_kernel<T, DP>, KeyShape<DP>::kSmem, keys_done, plan.key_items, p, st);
-    if (s == GS_OK && p.dq) s = launch_one(queries_kernel<T, DP>, QueryShape<DP>::kSmem, queries_done, plan.query_items, p, st);
-    return s;
+    if (p.dk) s = launch_one(keys_kernel<T, DP>, KeyShape<DP>::kSmem, kThreads, keys_done, plan.key_items, p, st);
+    if (s != GS_OK || !p.dq) return s;
+    if constexpr (DP == 128)
+        if (plan.tiles == 2)
+            return launch_one(queries_kernel<T, DP, 2>, QueryShape<DP, 2>::kSmem, QueryShape<DP, 2>::kThreads, two_done, plan.query_items, p, st);
+    return launch_one(queries_kernel<T, DP, 1>, QueryShape<DP, 1>::kSmem, QueryShape<DP, 1>::kThreads, one_done, plan.query_items, p, st);
 }
 
 }  // namespace
@@ -850,7 +913,7 @@ extern "C" gs_status gs_attention_bwd(const gs_attention_bwd_args* args, void* w
     cudaStream_t st = (cudaStream_t)stream;
     const bool dq = a.dq && a.q_rows > 0, dk = a.dk && a.k_rows > 0;
     if (!dq && !dk) return GS_OK;
-    float2* stats = (float2*)ws;
+    float* stats = (float*)ws;
     float* most = plan.most ? (float*)((char*)ws + plan.stats) : nullptr;
     char* to = (char*)ws + plan.stats + plan.most;
     PackList packs;
@@ -871,7 +934,7 @@ extern "C" gs_status gs_attention_bwd(const gs_attention_bwd_args* args, void* w
         t.o = (const uint16_t*)a.o, t.o_row = a.o_row, t.o_head = a.o_head;
         t.d_o = (const uint16_t*)a.d_o, t.do_row = a.do_row, t.do_head = a.do_head;
         t.v = (const uint16_t*)a.v, t.v_row = a.v_row, t.v_head = a.v_head;
-        t.lse = a.lse, t.stats = stats, t.most = most, t.q_rows = a.q_rows, t.k_rows = a.k_rows, t.stat_pitch = plan.stat_pitch;
+        t.lse = a.lse, t.stats = stats, t.most = most, t.q_rows = a.q_rows, t.k_rows = a.k_rows, t.stat_pitch = plan.stat_pitch, t.stat_plane = plan.stat_plane;
         t.heads = a.heads, t.kv_heads = a.kv_heads, t.group = plan.group, t.dim = a.dim;
         t.vec = a.dim % 8 == 0 && tensor_tma(a.o, a.o_row, a.o_head, a.q_rows, a.heads) &&
                 tensor_tma(a.d_o, a.do_row, a.do_head, a.q_rows, a.heads) &&
@@ -887,12 +950,12 @@ extern "C" gs_status gs_attention_bwd(const gs_attention_bwd_args* args, void* w
     p.fill_dq = {(uint16_t*)a.dq, a.dq_row, a.dq_head, nullptr, a.heads, a.dim};
     p.fill_dk = {(uint16_t*)a.dk, a.dk_row, a.dk_head, nullptr, a.kv_heads, a.dim};
     p.fill_dv = {(uint16_t*)a.dv, a.dv_row, a.dv_head, nullptr, a.kv_heads, a.dim};
-    p.stats = stats, p.most = most, p.most_count = plan.blocks, p.stat_pitch = plan.stat_pitch;
+    p.stats = stats, p.most = most, p.most_count = plan.blocks, p.stat_pitch = plan.stat_pitch, p.stat_plane = plan.stat_plane;
     p.dq = dq ? (uint16_t*)a.dq : nullptr, p.dq_row = a.dq_row, p.dq_head = a.dq_head;
     p.dk = dk ? (uint16_t*)a.dk : nullptr, p.dk_row = a.dk_row, p.dk_head = a.dk_head;
     p.dv = (uint16_t*)a.dv, p.dv_row = a.dv_row, p.dv_head = a.dv_head;
     p.scale = a.scale, p.scale2 = a.scale * kLog2e;
-    p.kv_heads = (uint32_t)a.kv_heads, p.tiles = plan.tiles, p.group = plan.group, p.tokens = plan.tokens, p.dim = a.dim;
+    p.kv_heads = (uint32_t)a.kv_heads, p.group = plan.group, p.tokens = plan.tokens, p.dim = a.dim;
     p.causal = a.causal != 0;
     p.dq_vec = tensor_vec(a.dq, a.dq_row, a.dq_head, a.q_rows, a.heads);
     p.dk_vec = tensor_vec(a.dk, a.dk_row, a.dk_head, a.k_rows, a.kv_heads);
