@@ -213,11 +213,12 @@ __device__ __forceinline__ float max3(float a, float b, float c)
 
 // Three warpgroups start with 168 registers a thread, all that the SM has: the third, of
 // few registers, leaves the other two 224 (2 x 224 + 56 = 3 x 168); two that start with 128
-// (two blocks an SM) 200 and 56.  Whole warpgroups call these.
+// (two blocks an SM) 200 and 56; five that start with 96, 104 four times and 56.  Whole
+// warpgroups call these.
 template <int N>
 __device__ __forceinline__ void many_registers()
 {
-    static_assert(N == 224 || N == 200, "of three warpgroups, or of two");
+    static_assert(N == 224 || N == 200 || N == 104, "of three warpgroups, of two, of five");
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 __device__ __forceinline__ void few_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 56;"); }

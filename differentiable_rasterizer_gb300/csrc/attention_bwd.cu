@@ -25,7 +25,7 @@ namespace gs {
 namespace attn {
 namespace {
 
-constexpr int kThreads = 384, kTmemCols = 512;
+constexpr int kKeyWarps = 16, kKeyThreads = (kKeyWarps + 4) * 32, kTmemCols = 512;
 constexpr int kStatRows = kRows + 4;   // of a copy of row statistics, which starts on 16 bytes
 
 __device__ int g_attention_bwd_wait_expired;
@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ Stat
         for (int e = 0; e < 8; ++e) v[e] = col + e < p.dim ? load_elem(from, col + e, T) : 0.0f;
     };
     float most_do = 0.0f, most_v = 0.0f;
-    // every thread of a warp runs the same number of rounds (the sums use whole warps)
+    // every thread of a warp runs the same number of rounds (the sums use whole warps).  (Four
+    // rounds' loads at a time took more registers than they hid: 590 -> 620 us with the products.)
     const int64_t lines = p.q_rows * p.heads;
     for (int64_t i0 = (int64_t)blockIdx.x * kLines; i0 < lines; i0 += step) {
         const int64_t i = i0 + threadIdx.x / LANES, r = i / p.heads;
@@ -159,8 +160,9 @@ __device__ __forceinline__ int first_query(const Sequence& s, int key, bool caus
 // ------------------------------------------------------------------ dk, dv
 // A CTA a tile of 128 keys of a key head.  TMEM lanes are keys:
 //   S = K Q^T, R = V dO^T (columns are packed query rows), dV += P dO, dK += dS Q
-// Warps 0-3 take the first 64 columns of S and R, warps 4-7 the others; P and dS take
-// the first half of their own columns' place.  The products of a tile of queries are issued as
+// Sixteen warps, four of them 32 columns of S and R each; P and dS take the first half of
+// their own columns' place.  (Eight warps of 64 columns waited for TMEM and shared memory most
+// of their time: 3,440 cycles a tile, where the products take 2,050.)  The products of a tile of queries are issued as
 //   dV(i), S(i + 1), dK(i), R(i + 1)
 // so that P and dS are made while the other two run.
 template <int DP>
@@ -298,8 +300,8 @@ __device__ __forceinline__ void issue_keys(const Params& p, const KeyWork& w, bo
         tc_fence_after();
         const uint32_t b = desc_rows(at_sum + ss * S::kTile);
 #pragma unroll
-        for (int s = 0; s < kRows / 16; ++s)   // halves of 64 queries, 32 columns each, 64 apart
-            mma_tmem(sum, terms + (s >> 2) * 64 + (s & 3) * 8, b + s * k_step(false), kDescHi, p.idesc_d, i > 0 || s > 0);
+        for (int s = 0; s < kRows / 16; ++s)   // quarters of 32 queries, 16 columns each, 32 apart
+            mma_tmem(sum, terms + (s >> 1) * 32 + (s & 1) * 8, b + s * k_step(false), kDescHi, p.idesc_d, i > 0 || s > 0);
         if (i + 1 < w.n) {
             mma_commit<false>(sum_empty + 8 * ss);
             if (!rows_product(i + 1)) return;
@@ -330,90 +332,79 @@ struct Stats4 {
 };
 __device__ __forceinline__ uint64_t both(float v) { return pair(v, v); }
 
-// A key a thread (row r of the tile), 64 columns: half 0 or 1.
+// A key a thread (row r of the tile), 32 columns: those of `quarter`.
 template <int T, int DP>
-__device__ __forceinline__ void key_terms(const Params& p, const KeyWork& w, int half, int r, uint32_t smem, uint32_t bars, uint32_t tmem,
+__device__ __forceinline__ void key_terms(const Params& p, const KeyWork& w, int quarter, int r, uint32_t smem, uint32_t bars, uint32_t tmem,
                                           int exponent, volatile int* gave_up)
 {
     using S = KeyShape<DP>;
     const uint64_t by_ds = both(power2(exponent) * kDown<T>), scale2 = both(p.scale2);
     const int key = w.key0 + r;
+    const uint32_t mine = tmem + quarter * 32;
     bool ok = true;
     Ring<2> rs;
     for (int i = 0; i < w.n; ++i, rs.next()) {
         const int t0 = w.first + i * p.tokens;
         // columns of this tile that count for this key: from the first query that sees it to the last of the sequence
-        const int rows = (w.seq.lq - t0) * p.group, full = p.tokens * p.group, to = (rows < full ? rows : full) - half * 64;
-        const int from = (first_query(w.seq, key, p.causal) - t0) * p.group - half * 64;
-        const bool cut = to < 64 || __any_sync(0xffffffffu, from > 0);
+        const int rows = (w.seq.lq - t0) * p.group, full = p.tokens * p.group, to = (rows < full ? rows : full) - quarter * 32;
+        const int from = (first_query(w.seq, key, p.causal) - t0) * p.group - quarter * 32;
+        const bool cut = to < 32 || __any_sync(0xffffffffu, from > 0);
         const uint32_t odd = (uint32_t)((int64_t)(w.seq.q0 + t0) * p.group) & 3;
-        const uint32_t stats = smem + S::kAtStats + 2 * rs.s * S::kStatBytes + (odd + (uint32_t)half * 64) * 4;
+        const uint32_t stats = smem + S::kAtStats + 2 * rs.s * S::kStatBytes + (odd + (uint32_t)quarter * 32) * 4;
         ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (S::kStatFull + rs.s), rs.parity, gave_up) &&
                                          mbar_wait(bars + 8 * S::kS, i & 1, gave_up));
         if (!ok) break;
         tc_fence_after();
-        uint32_t s[64];
-        tmem_ld32(tmem + half * 64, s);
+        uint32_t s[32], h[16];
+        tmem_ld32(mine, s);
+        Stats4 l[4];   // half of them at a time
+#pragma unroll
+        for (int e = 0; e < 4; ++e) l[e].load(stats + e * 16, odd == 0);
         tmem_ld32_wait(s);
 #pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-            if (c == 0) tmem_ld32(tmem + half * 64 + 32, s + 32);   // on its way during the first terms
-#pragma unroll
-            for (int e = c; e < c + 32; e += 4) {
-                Stats4 l;
-                l.load(stats + e * 4, odd == 0);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float2 x = unpair(fma2(pair(__uint_as_float(s[e + 2 * k]), __uint_as_float(s[e + 2 * k + 1])), scale2, l.v[k]));
-                    s[e + 2 * k] = __float_as_uint(exp2_fast(x.x)), s[e + 2 * k + 1] = __float_as_uint(exp2_fast(x.y));
-                }
-            }
-            if (cut) {
-#pragma unroll
-                for (int e = c; e < c + 32; ++e)
-                    if (e < from || e >= to) s[e] = 0;
-            }
-            uint32_t h[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) h[e] = pack_half2(__uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1]), T);
-            if (c == 0) tmem_ld32_wait(s + 32);   // before the terms take columns' place
-            tmem_st16(tmem + half * 64 + c / 2, h);
+        for (int e = 0; e < 16; ++e) {
+            Stats4& q = l[e / 2 & 3];
+            const float2 x = unpair(fma2(pair(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), scale2, q.v[e & 1]));
+            s[2 * e] = __float_as_uint(exp2_fast(x.x)), s[2 * e + 1] = __float_as_uint(exp2_fast(x.y));
+            if (e < 8 && (e & 1)) q.load(stats + (e / 2 + 4) * 16, odd == 0);
         }
+        if (cut) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if (e < from || e >= to) s[e] = 0;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) h[e] = pack_half2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]), T);
+        tmem_st16(mine, h);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(bars + 8 * S::kP);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) l[e].load(stats + S::kStatBytes + e * 16, odd == 0);
         ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * S::kR, i & 1, gave_up));
         if (!ok) break;
         tc_fence_after();
-        uint32_t h[32], d[64];
-        tmem_ld32(tmem + kTmemR + half * 64, d);
+        uint32_t d[32];
+        tmem_ld32(mine + kTmemR, d);
         tmem_ld32_wait(d);
 #pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-            if (c == 0) tmem_ld32(tmem + kTmemR + half * 64 + 32, d + 32);
-#pragma unroll
-            for (int e = c; e < c + 32; e += 4) {
-                Stats4 l;
-                l.load(stats + S::kStatBytes + e * 4, odd == 0);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    uint64_t x = add2(pair(__uint_as_float(d[e + 2 * k]), __uint_as_float(d[e + 2 * k + 1])), l.v[k]);
-                    if constexpr (T == GS_F16) x = mul2(x, by_ds);
-                    const float2 f = unpair(mul2(x, pair(__uint_as_float(s[e + 2 * k]), __uint_as_float(s[e + 2 * k + 1]))));
-                    d[e + 2 * k] = __float_as_uint(f.x), d[e + 2 * k + 1] = __float_as_uint(f.y);
-                }
-            }
-            if (cut) {   // 0 times whatever the hidden rows give
-#pragma unroll
-                for (int e = c; e < c + 32; ++e)
-                    if (e < from || e >= to) d[e] = 0;
-            }
-#pragma unroll
-            for (int e = c; e < c + 32; e += 2) h[e / 2] = pack_half2(__uint_as_float(d[e]), __uint_as_float(d[e + 1]), T);
-            if (c == 0) tmem_ld32_wait(d + 32);
+        for (int e = 0; e < 16; ++e) {
+            Stats4& q = l[e / 2 & 3];
+            uint64_t x = add2(pair(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])), q.v[e & 1]);
+            if (e < 8 && (e & 1)) q.load(stats + S::kStatBytes + (e / 2 + 4) * 16, odd == 0);
+            if constexpr (T == GS_F16) x = mul2(x, by_ds);
+            const float2 f = unpair(mul2(x, pair(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]))));
+            d[2 * e] = __float_as_uint(f.x), d[2 * e + 1] = __float_as_uint(f.y);
         }
-        tmem_st32(tmem + kTmemR + half * 64, h);
+        if (cut) {   // 0 times whatever the hidden rows give
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if (e < from || e >= to) d[e] = 0;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) h[e] = pack_half2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1]), T);
+        tmem_st16(mine + kTmemR, h);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -422,16 +413,17 @@ __device__ __forceinline__ void key_terms(const Params& p, const KeyWork& w, int
             mbar_arrive(bars + 8 * (S::kStatEmpty + rs.s));
         }
     }
+    // the first eight warps write dV, the others dK, half of the columns each
+    const int half = quarter >> 1;
     if (w.n > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (S::kDone + half), 0, gave_up));
     if (!ok) return;
     tc_fence_after();
-    // the first warps write dV, the others dK
     const bool live = key < w.seq.lk;
     const int64_t row = w.seq.k0 + key;
     const float by = half == 0 ? kDown<T> : p.scale * power2(-exponent);
     uint16_t* to = half == 0 ? p.dv + row * p.dv_row + w.head * p.dv_head : p.dk + row * p.dk_row + w.head * p.dk_head;
 #pragma unroll 1
-    for (int c = 0; c < DP; c += 32) {
+    for (int c = (quarter & 1) * (DP / 2); c < (quarter & 1) * (DP / 2) + DP / 2; c += 32) {
         float f[32];
         uint32_t v[32];
         if (w.n > 0) {
@@ -446,7 +438,7 @@ __device__ __forceinline__ void key_terms(const Params& p, const KeyWork& w, int
 }
 
 template <int T, int DP>
-__global__ void __launch_bounds__(kThreads, 1) keys_kernel(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(kKeyThreads, 1) keys_kernel(const __grid_constant__ Params p)
 {
     using S = KeyShape<DP>;
     extern __shared__ __align__(1024) char smem_raw[];
@@ -462,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) keys_kernel(const __grid_constant
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kBars; ++i)
-            mbar_init(bars + 8 * i, i == S::kP || i == S::kDs || (i >= S::kStatEmpty && i < S::kS)                ? 8
+            mbar_init(bars + 8 * i, i == S::kP || i == S::kDs || (i >= S::kStatEmpty && i < S::kS)                ? kKeyWarps
                                     : (i >= S::kQEmpty && i < S::kOFull) || (i >= S::kOEmpty && i < S::kStatFull) ? 2
                                                                                                                   : 1);
         *gave_up = 0;
@@ -475,35 +467,36 @@ __global__ void __launch_bounds__(kThreads, 1) keys_kernel(const __grid_constant
     }
     KeyWork w;
     if (!find_keys(p, w)) return;   // the same for every warp
-    if (warp == 9) tmem_alloc<false>(smem_addr(tmem_slot), kTmemCols);
+    if (warp == kKeyWarps) tmem_alloc<false>(smem_addr(tmem_slot), kTmemCols);
     const int packed = p.tokens * p.group;
     if (packed < kRows && w.n > 0)   // rows that no copy writes
-        for (int t = warp; t < S::kStagesQ + S::kStagesO; t += kThreads / 32) zero_rows<S::kChunks>(smem + S::kAtQ + t * S::kTile, packed, lane);
+        for (int t = warp; t < S::kStagesQ + S::kStagesO; t += kKeyThreads / 32) zero_rows<S::kChunks>(smem + S::kAtQ + t * S::kTile, packed, lane);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    if (warp >= 8) {
+    if (warp < kKeyWarps) {
+        many_registers<104>();
+        const int exponent = ds_exponent<T>(p);
+        key_terms<T, DP>(p, w, warp >> 2, threadIdx.x & 127, smem, bars, tmem + ((uint32_t)((warp & 3) * 32) << 16), exponent, gave_up);
+    } else {
         few_registers();
-        if (warp == 8) {
+        if (warp == kKeyWarps) {
             if (w.n > 0) {
                 if (elect_one()) load_queries<DP>(p, w, smem, bars, gave_up);
                 __syncwarp();
                 clear_queries<DP>(p, w, smem, bars, lane, gave_up);
             }
-        } else if (warp < 11 && elect_one()) {
-            if (w.n > 0) issue_keys<DP>(p, w, warp == 10, smem, bars, tmem, gave_up);
-            mma_commit<false>(bars + 8 * (S::kDone + warp - 9));   // the block does not leave before its products are done
-            if (!mbar_wait_alone(bars + 8 * (S::kDone + warp - 9), 0)) *gave_up = 1;
+        } else if (warp < kKeyWarps + 3 && elect_one()) {
+            const int second = warp - kKeyWarps - 1;
+            if (w.n > 0) issue_keys<DP>(p, w, second, smem, bars, tmem, gave_up);
+            mma_commit<false>(bars + 8 * (S::kDone + second));   // the block does not leave before its products are done
+            if (!mbar_wait_alone(bars + 8 * (S::kDone + second), 0)) *gave_up = 1;
         }
-    } else {
-        many_registers<224>();
-        const int exponent = ds_exponent<T>(p);
-        key_terms<T, DP>(p, w, warp >> 2, threadIdx.x & 127, smem, bars, tmem + ((uint32_t)((warp & 3) * 32) << 16), exponent, gave_up);
     }
     __syncthreads();
     if (threadIdx.x == 0 && *gave_up) atomicExch(&g_attention_bwd_wait_expired, 1);
-    if (warp == 9) {
+    if (warp == kKeyWarps) {
         tc_fence_after();
         tmem_free<false>(tmem, kTmemCols);
     }
@@ -858,7 +851,7 @@ gs_status launch(const Params& p, const Plan& plan, cudaStream_t st)
 {
     static std::atomic<uint64_t> keys_done{0}, one_done{0}, two_done{0};
     gs_status s = GS_OK;
-    if (p.dk) s = launch_one(keys_kernel<T, DP>, KeyShape<DP>::kSmem, kThreads, keys_done, plan.key_items, p, st);
+    if (p.dk) s = launch_one(keys_kernel<T, DP>, KeyShape<DP>::kSmem, kKeyThreads, keys_done, plan.key_items, p, st);
     if (s != GS_OK || !p.dq) return s;
     if constexpr (DP == 128)
         if (plan.tiles == 2)
