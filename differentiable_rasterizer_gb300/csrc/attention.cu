@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(Shape<DP, TILES>::kThreads, 3 - TILES) attenti
         *gave_up = 0;
         mbar_init_fence();
     }
-    wait_for_predecessor();
+    wait_for_predecessor_alone();
     if (p.zero) fill_rows(p.fill, p.seqs.q_starts, p.seqs.count, p.seqs.q_rows);
     Work w;
     if (!find_work<TILES>(p, w)) return;   // the same for every warp
@@ -357,6 +357,7 @@ __global__ void __launch_bounds__(Shape<DP, TILES>::kThreads, 3 - TILES) attenti
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    let_successor_start();
     const int n = w.n[0] > w.n[1] ? w.n[0] : w.n[1];
 
     if (warp >= S::kSoftmaxWarps) {

@@ -87,7 +87,7 @@ __device__ __forceinline__ bool find_unit(const Sequences& p, uint32_t u, int to
     return false;
 }
 // Keys that the tokens up to `last` of a sequence see.
-__device__ __forceinline__ int keys_seen(const Sequence& s, int last, bool causal)
+__host__ __device__ __forceinline__ int keys_seen(const Sequence& s, int last, bool causal)
 {
     const int e = causal ? last + 1 + s.lk - s.lq : s.lk;
     return e < 0 ? 0 : (e < s.lk ? e : s.lk);
@@ -299,7 +299,8 @@ inline gs_status tile_map(CUtensorMap* map, const Tensor3& t, int type, int64_t 
 inline bool sizes_ok(int64_t q_rows, int64_t k_rows, int64_t sequences, int heads, int kv_heads, int dim, int type, float scale,
                      const void* q_starts, const void* k_starts)
 {
-    if (!size_ok(q_rows, 0) || !size_ok(k_rows, 0) || !size_ok(sequences, 0)) return false;
+    constexpr int64_t most = 0x7fffffffll - 1024;   // a tile past the last row still has a number
+    if (!size_ok(q_rows, 0) || !size_ok(k_rows, 0) || !size_ok(sequences, 0) || q_rows > most || k_rows > most) return false;
     if (!q_starts != !k_starts || (!q_starts && sequences != 1)) return false;
     if (((uintptr_t)q_starts & 3u) || ((uintptr_t)k_starts & 3u)) return false;
     if (kv_heads < 1 || heads < kv_heads || heads % kv_heads || heads / kv_heads > GS_ATTENTION_MAX_GROUP || heads > 65536) return false;

@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kKeyThreads, 1) keys_kernel(const __grid_const
         *gave_up = 0;
         mbar_init_fence();
     }
-    wait_for_predecessor();
+    wait_for_predecessor_alone();
     if (p.zero) {
         fill_rows(p.fill_dk, p.seqs.k_starts, p.seqs.count, p.seqs.k_rows);
         fill_rows(p.fill_dv, p.seqs.k_starts, p.seqs.count, p.seqs.k_rows);
@@ -475,6 +475,7 @@ __global__ void __launch_bounds__(kKeyThreads, 1) keys_kernel(const __grid_const
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    let_successor_start();
     if (warp < kKeyWarps) {
         many_registers<104>();
         const int exponent = ds_exponent<T>(p);
@@ -767,7 +768,7 @@ __global__ void __launch_bounds__(QueryShape<DP, TILES>::kThreads, 3 - TILES) qu
         *gave_up = 0;
         mbar_init_fence();
     }
-    wait_for_predecessor();
+    wait_for_predecessor_alone();
     if (p.zero) fill_rows(p.fill_dq, p.seqs.q_starts, p.seqs.count, p.seqs.q_rows);
     QueryWork w;
     if (!find_queries<TILES>(p, w)) return;   // the same for every warp
@@ -776,6 +777,7 @@ __global__ void __launch_bounds__(QueryShape<DP, TILES>::kThreads, 3 - TILES) qu
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    let_successor_start();
     const int n = w.n[0] > w.n[1] ? w.n[0] : w.n[1];
     if (warp >= S::kTermWarps) {
         few_registers();

@@ -59,6 +59,11 @@ __device__ __forceinline__ void wait_for_predecessor()
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
 }
+// The two apart, for a block that takes TMEM only once it has read what it works on: blocks
+// of the next kernel, which may take theirs before they wait, have to come after that, or
+// they would hold the columns that this one needs to end.
+__device__ __forceinline__ void wait_for_predecessor_alone() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_successor_start() { asm volatile("griddepcontrol.launch_dependents;"); }
 
 template <class... P, class... A>
 gs_status launch_after(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, unsigned cluster, cudaStream_t st,

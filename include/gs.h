@@ -692,8 +692,8 @@ GS_API gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* ws_by
  * bad ones give wrong values but no access outside.  Rows of o and lse that belong
  * to no sequence are left as they are (fill = 0) or set to zero (fill = 1).
  * Rows of other sequences have no influence, whatever they hold.  A NaN or an infinity
- * among a sequence's own values reaches queries that it is hidden from, if they are
- * less than 256 rows of the group before the first that sees it.
+ * among a sequence's own values (v) reaches queries that it is hidden from, if they are
+ * less than 256 tokens before the first that sees it.  Rows: below 2^31 - 1024.
  * Scores, maxima, sums and outputs are fp32 until o's rounding; exp(t - m), m a
  * running maximum, is rounded to `type` as a factor of its product with v.
  * Errors: INVALID_ARG for bad pointers, sizes, types or a too small workspace;
@@ -726,7 +726,8 @@ GS_API gs_status gs_attention(const gs_attention_args* args, void* ws, size_t* w
  * `type` as factors of these products (F16: times powers of two that keep them among
  * its normal numbers, ds by the largest magnitudes in all of d_o and v).  q, k, v, o, lse: the forward's.  do, dq: like q;
  * dk, dv: like k.  dq may be NULL, and so may dk and dv together (not computed).
- * Rows that belong to no sequence: as gs_attention, in dq, dk and dv.
+ * Rows that belong to no sequence: as gs_attention, in dq, dk and dv.  A NaN or an
+ * infinity in d_o or q reaches keys that are hidden from its query within 256 tokens.
  * Errors: as gs_attention. */
 typedef struct gs_attention_bwd_args {
     int64_t q_rows, k_rows, sequences;

@@ -221,6 +221,20 @@ def test_offsets_past_32_bits(layers):
     assert (out.dx[:5] == 0).all() and out.dx[-2:].abs().sum() > 0
 
 
+@pytest.mark.parametrize("cols,ld", [(256, 256), (77, 80), (77, 77)])
+@pytest.mark.parametrize("over", ["x", "h"])
+def test_sum_in_place(layers, over, cols, ld):
+    """s may be the array of x or of h (through the C ABI; the torch layer allocates s)."""
+    from differentiable_rasterizer_gb300 import abi
+    rows = 3001
+    h, x, w, p, g = inputs(rows, cols, BF, "vector", True, pitch=ld)
+    want = layers.block_norm(h, x, w, post_weight=p, gate=g, scale=0.75)
+    s, y = (x if over == "x" else h), torch.empty((rows, cols), dtype=BF, device="cuda")
+    abi.gs_block_norm(rows, cols, h.data_ptr(), ld, x.data_ptr(), ld, p.data_ptr(), g.data_ptr(), 0, w.data_ptr(), s.data_ptr(), ld,
+                      y.data_ptr(), cols, 0, 0, 0, 0.75, EPS, 1, 1, 1, 0, 1, 1, torch.cuda.current_stream().cuda_stream)
+    assert torch.equal(y, want.y) and torch.equal(s, want.s)
+
+
 def test_no_rows(layers):
     e, w = torch.empty((0, 32), dtype=BF, device="cuda"), rnd((32,), 0, BF)
     b = layers.block_norm(e, e, w, post_weight=w, gate=w, need_backward=True)
