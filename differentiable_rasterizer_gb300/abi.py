@@ -333,7 +333,7 @@ _LINEAR = struct.Struct("=qqq Qq Qq QQ Q Qq Qq Qq iiii")
 _LINEAR_BWD = struct.Struct("=qqq Qq Qq Qq Qq Qq Qq Q iiii ii")
 _GLU = struct.Struct("=qqq Qq Qq Qq QQQ Qq Qq Qq iiii")
 _ATTENTION = struct.Struct("=qqq Qqq Qqq Qqq QQQ Qqq Q f iiiiiii")
-_ATTENTION_BWD = struct.Struct("=qqq Qqq Qqq Qqq Qqq Qqq Q QQ Qqq Qqq Qqq f iiiiiii")
+_ATTENTION_BWD = struct.Struct("=qqq Qqq Qqq Qqq Qqq Q QQ Qqq Qqq Qqq f iiiiiii")
 _BLOCK_NORM = struct.Struct("=qq Qq Qq Q Qq Q Qq Qq QQQ ff iiiiii")
 _BLOCK_NORM_BWD = struct.Struct("=qq Qq Qq Qq Qq Q Qq Q QQ Qq Qq Qq QQ f iiiiiii")
 _CLIP_TENSOR = struct.Struct("=QQq ii")
@@ -407,11 +407,10 @@ def attention_args(q_rows, k_rows, sequences, q, q_row, q_head, k, k_row, k_head
                            k_starts, k_lengths, o, o_row, o_head, lse, scale, heads, kv_heads, dim, type_, causal, fill, 0)
 
 
-def attention_bwd_args(q_rows, k_rows, sequences, q, q_row, q_head, k, k_row, k_head, v, v_row, v_head, o, o_row, o_head,
-                       d_o, do_row, do_head, lse, q_starts, k_starts, dq, dq_row, dq_head, dk, dk_row, dk_head, dv, dv_row,
+def attention_bwd_args(q_rows, k_rows, sequences, q, q_row, q_head, k, k_row, k_head, v, v_row, v_head, d_o, do_row,
+                       do_head, lse, q_starts, k_starts, dq, dq_row, dq_head, dk, dk_row, dk_head, dv, dv_row,
                        dv_head, scale, heads, kv_heads, dim, type_, causal, fill) -> bytes:
-    return _ATTENTION_BWD.pack(q_rows, k_rows, sequences, q, q_row, q_head, k, k_row, k_head, v, v_row, v_head, o, o_row,
-                               o_head, d_o, do_row, do_head, lse, q_starts, k_starts, dq, dq_row, dq_head, dk, dk_row,
+    return _ATTENTION_BWD.pack(q_rows, k_rows, sequences, q, q_row, q_head, k, k_row, k_head, v, v_row, v_head, d_o, do_row, do_head, lse, q_starts, k_starts, dq, dq_row, dq_head, dk, dk_row,
                                dk_head, dv, dv_row, dv_head, scale, heads, kv_heads, dim, type_, causal, fill, 0)
 
 

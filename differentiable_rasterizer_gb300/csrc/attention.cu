@@ -14,8 +14,8 @@
 // issued in that order by one lane and run in it.
 //
 // The maximum that a row's terms are taken to is raised only when a tile of keys exceeds
-// it by more than 2^8: o and the sum are then rescaled (rare after the first tiles), and
-// terms stay within 2^8 in between, which neither 16-bit type nor the fp32 sums mind.
+// it by more than 2^15: o and the sum are then rescaled (rare after the first tiles), and
+// terms stay within 2^15 in between, which f16 holds and the fp32 sums do not mind.
 //
 // Few rows against many keys (single tokens) leave most SMs idle: the keys of a tile are
 // then split over several CTAs, whose sums and maxima join_kernel puts together in a
@@ -29,7 +29,7 @@ namespace gs {
 namespace attn {
 namespace {
 
-constexpr float kRaise = 8.0f;   // log2
+constexpr float kRaise = 15.0f;   // log2
 
 // TILES: of a CTA.  With one, two CTAs share an SM.
 template <int DP, int TILES>

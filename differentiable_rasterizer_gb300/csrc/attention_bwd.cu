@@ -1,18 +1,20 @@
 // attention_bwd.cu -- the gradients of attention over packed sequences.
 //
-//   delta = do . o (a row),  p = exp(scale q k^T - lse),  ds = p (do v^T - delta)
+//   p = exp(scale q k^T - lse),  r = do v^T,  delta = sum of p r (a row),  ds = p (r - delta)
 //   dv = p^T do,  dk = scale ds^T q,  dq = scale ds k
 //
-// Scores and do v^T are computed again from the tiles, so that nothing of the size of
-// queries times keys is stored.  Three launches: delta with the row statistics; dk and dv,
-// a tile of keys a CTA against all its queries; dq, two tiles of queries a CTA against
-// their keys.  dq could come out of the second's products, but its sum runs over the CTAs
-// there: atomics would make its bits depend on the run, so dq's kernel computes scores and
-// do v^T a second time (seven products of a pair in place of five).
+// Scores and r are computed again from the tiles, so that nothing of the size of queries
+// times keys is stored.  Three launches: delta, two tiles of queries a CTA against their
+// keys; dk and dv, a tile of keys a CTA against all its queries; dq, tiles of queries again.
+// dq could come out of the second's products, but its sum runs over the CTAs there: atomics
+// would make its bits depend on the run.  delta is do . o, but o has been rounded: in bf16
+// that alone puts 4e-3 of dq's norm (where few keys carry the weight, 1e-2) beside the 2e-3 of
+// the factors' and results' roundings, for delta multiplies the keys' mean, and dq is what
+// remains of the keys beside it.  So nine products of a pair of tiles in place of five.
 //
-// Both product kernels keep p and ds out of shared memory: a tile's scores are computed
-// with the rows that stay (keys, or queries) as TMEM lanes, p and ds take their place in
-// TMEM as 16 bits, and are the first factor of the next products from there.
+// The kernels keep p and ds out of shared memory: a tile's scores are computed with the
+// rows that stay (keys, or queries) as TMEM lanes, p and ds take their place in TMEM as 16
+// bits, and are the first factor of the next products from there.
 //
 // f16 holds neither small p nor small ds among its normal numbers: p is taken times 2^12
 // (at most 1 times that), ds times the power of two that brings its bound, 2 dim max|do|
@@ -30,11 +32,18 @@ constexpr int kStatRows = kRows + 4;   // of a copy of row statistics, which sta
 
 __device__ int g_attention_bwd_wait_expired;
 
+// log2 of what p is held times as a factor.
+template <int T>
+constexpr float kUp = T == GS_F16 ? 12.0f : 0.0f;
+template <int T>
+constexpr float kDown = T == GS_F16 ? 0x1p-12f : 1.0f;
+
 struct Params {
     CUtensorMap q, k, v, d_o;
     Sequences seqs;
     Fill fill_dq, fill_dk, fill_dv;
-    const float* stats;      // [key head][token][head of the group], twice: kUp - lse log2(e) (-infinite for a row that sees no key), -delta
+    float* stats;            // [key head][token][head of the group], twice: kUp - lse log2(e) (-infinite for a row that sees no key), -delta
+    const float* lse;
     const float* most;       // F16: the blocks' largest |do| and |v|
     int most_count;
     uint16_t *dq, *dk, *dv;
@@ -46,88 +55,51 @@ struct Params {
     uint32_t idesc_s, idesc_d;
 };
 
-// log2 of what p is held times.
-template <int T>
-constexpr float kUp = T == GS_F16 ? 12.0f : 0.0f;
-template <int T>
-constexpr float kDown = T == GS_F16 ? 0x1p-12f : 1.0f;
-
-// ------------------------------------------------------------------ row statistics
-struct StatParams {
-    const uint16_t *o, *d_o, *v;
-    int64_t o_row, o_head, do_row, do_head, v_row, v_head;
-    const float* lse;
-    float* stats;
-    float* most;
-    int64_t q_rows, k_rows, stat_pitch, stat_plane;
-    int heads, kv_heads, group, dim, vec;
+// ------------------------------------------------------------------ F16's largest values
+struct MostParams {
+    const uint16_t *d_o, *v;
+    int64_t do_row, do_head, v_row, v_head;
+    float* most;   // a block's largest |do| and |v|
+    int64_t q_rows, k_rows;
+    int heads, kv_heads, dim, vec;
 };
 
-// LANES lanes a row and head (a power of two that covers dim at 8 elements a lane).
-template <int T, int LANES>
-__global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ StatParams p)
+// Sixteen lanes a row and head, eight elements a lane.
+__global__ void __launch_bounds__(256) most_kernel(const __grid_constant__ MostParams p)
 {
     __shared__ float most[2][8];
-    constexpr int kLines = 256 / LANES;   // of a block's round
     wait_for_predecessor();
-    const int lane = threadIdx.x % LANES, col = lane * 8;
-    const int64_t step = (int64_t)gridDim.x * kLines, first = (int64_t)blockIdx.x * kLines + threadIdx.x / LANES;
-    const auto load = [&](const uint16_t* from, float (&v)[8]) {
-        if (p.vec) {
-            load8(from, col, T, v);
-            return;
-        }
+    const int col = threadIdx.x % 16 * 8;
+    const int64_t step = (int64_t)gridDim.x * 16, first = (int64_t)blockIdx.x * 16 + threadIdx.x / 16;
+    float m[2] = {0.0f, 0.0f};
+    const auto over = [&](float& m, const uint16_t* t, int64_t row, int64_t head, int64_t lines, int heads) {
+#pragma unroll 4
+        for (int64_t i = first; i < lines; i += step) {
+            const int64_t r = i / heads;
+            const uint16_t* at = t + r * row + (i - r * heads) * head;
+            float v[8];
+            if (col >= p.dim) continue;
+            if (p.vec) load8(at, col, GS_F16, v);
+            else
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = col + e < p.dim ? load_elem(from, col + e, T) : 0.0f;
+                for (int e = 0; e < 8; ++e) v[e] = col + e < p.dim ? load_elem(at, col + e, GS_F16) : 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
+        }
     };
-    float most_do = 0.0f, most_v = 0.0f;
-    // every thread of a warp runs the same number of rounds (the sums use whole warps).  (Four
-    // rounds' loads at a time took more registers than they hid: 590 -> 620 us with the products.)
-    const int64_t lines = p.q_rows * p.heads;
-    for (int64_t i0 = (int64_t)blockIdx.x * kLines; i0 < lines; i0 += step) {
-        const int64_t i = i0 + threadIdx.x / LANES, r = i / p.heads;
-        const int h = (int)(i - r * p.heads);
-        float sum = 0.0f;
-        if (i < lines && col < p.dim) {
-            float a[8], b[8];
-            load(p.o + r * p.o_row + h * p.o_head, a);
-            load(p.d_o + r * p.do_row + h * p.do_head, b);
+    over(m[0], p.d_o, p.do_row, p.do_head, p.q_rows * p.heads, p.heads);
+    over(m[1], p.v, p.v_row, p.v_head, p.k_rows * p.kv_heads, p.kv_heads);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                sum = __fmaf_rn(a[e], b[e], sum);
-                most_do = fmaxf(most_do, fabsf(b[e]));
-            }
-        }
+    for (int k = 0; k < 2; ++k) {
 #pragma unroll
-        for (int s = LANES / 2; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-        if (lane == 0 && i < lines) {
-            const float lse = p.lse[i];
-            // a row that sees no key: every p is 2^-infinity
-            float* to = p.stats + (h / p.group) * p.stat_pitch + r * p.group + h % p.group;
-            to[0] = lse == -INFINITY ? -INFINITY : __fmaf_rn(lse, -kLog2e, kUp<T>);
-            to[p.stat_plane] = lse == -INFINITY ? 0.0f : -sum;
-        }
+        for (int s = 16; s > 0; s >>= 1) m[k] = fmaxf(m[k], __shfl_xor_sync(0xffffffffu, m[k], s));
+        if ((threadIdx.x & 31) == 0) most[k][threadIdx.x >> 5] = m[k];
     }
-    if (!p.most) return;
-    for (int64_t i = first; i < p.k_rows * p.kv_heads; i += step) {
-        if (col >= p.dim) break;
-        const int64_t r = i / p.kv_heads;
-        float v[8];
-        load(p.v + r * p.v_row + (i - r * p.kv_heads) * p.v_head, v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) most_v = fmaxf(most_v, fabsf(v[e]));
-    }
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) {
-        most_do = fmaxf(most_do, __shfl_xor_sync(0xffffffffu, most_do, s));
-        most_v = fmaxf(most_v, __shfl_xor_sync(0xffffffffu, most_v, s));
-    }
-    if ((threadIdx.x & 31) == 0) most[0][threadIdx.x >> 5] = most_do, most[1][threadIdx.x >> 5] = most_v;
     __syncthreads();
     if (threadIdx.x < 2) {
-        float m = 0.0f;
-        for (int w = 0; w < 8; ++w) m = fmaxf(m, most[threadIdx.x][w]);
-        p.most[2 * blockIdx.x + threadIdx.x] = m;
+        float all = 0.0f;
+        for (int w = 0; w < 8; ++w) all = fmaxf(all, most[threadIdx.x][w]);
+        p.most[2 * blockIdx.x + threadIdx.x] = all;
     }
 }
 
@@ -744,7 +716,112 @@ __device__ __forceinline__ void query_terms(const Params& p, const QueryWork& w,
     tc_fence_before();
 }
 
+// ------------------------------------------------------------------ delta
+// The queries' blocks once more: S and R in places of their own, read as they come, the
+// rows' sums of p r in registers.  Nothing waits for a term, so that the products run ahead.
+template <int DP, int TILES>
+__device__ __forceinline__ void issue_delta(const Params& p, const QueryWork& w, int i, int n, uint32_t smem, uint32_t bars, uint32_t tmem,
+                                            volatile int* gave_up)
+{
+    using S = QueryShape<DP, TILES>;
+    const int mine = i ? w.n[1] : w.n[0];
+    const uint32_t steps = (uint32_t)(p.dim + 15) / 16;
+    const auto rows_product = [&](uint32_t d, uint32_t at_a, uint32_t at_b) {
+        const uint32_t a = desc_lo(at_a, true), b = desc_lo(at_b, true);
+#pragma unroll
+        for (uint32_t s = 0; s < DP / 16; ++s) {
+            const uint32_t at = (s >> 2) * (kBox >> 4) + (s & 3) * k_step(true);
+            if (s < steps) mma<false, false>(d, a + at, kDescHi, b + at, kDescHi, p.idesc_s, s > 0);
+        }
+    };
+    Ring<S::kStagesK> rk;
+    Ring<S::kStagesV> rv;
+    if (mine > 0 && !mbar_wait(bars + 8 * (S::kQFull + i), 0, gave_up)) return;
+    for (int j = 0; j < n; ++j, rk.next(), rv.next()) {
+        if (!mbar_wait(bars + 8 * (S::kKFull + rk.s), rk.parity, gave_up)) return;
+        if (j < mine) {
+            if (j > 0 && !mbar_wait(bars + 8 * (S::kP + i), (j - 1) & 1, gave_up)) return;   // S has been read
+            tc_fence_after();
+            rows_product(tmem + i * 128, smem + 2 * i * S::kTile, smem + S::kAtK + rk.s * S::kTile);
+            mma_commit<false>(bars + 8 * (S::kS + i));
+            mma_commit<false>(bars + 8 * (S::kKEmpty + rk.s));
+        } else mbar_arrive(bars + 8 * (S::kKEmpty + rk.s));
+        if (!mbar_wait(bars + 8 * (S::kVFull + rv.s), rv.parity, gave_up)) return;
+        if (j < mine) {
+            if (j > 0 && !mbar_wait(bars + 8 * (S::kDs + i), (j - 1) & 1, gave_up)) return;   // R has been read
+            tc_fence_after();
+            rows_product(tmem + (TILES + i) * 128, smem + (2 * i + 1) * S::kTile, smem + S::kAtV + rv.s * S::kTile);
+            mma_commit<false>(bars + 8 * (S::kR + i));
+            mma_commit<false>(bars + 8 * (S::kVEmpty + rv.s));
+        } else mbar_arrive(bars + 8 * (S::kVEmpty + rv.s));
+    }
+}
+
+// A row a thread: i the tile, r the row.
 template <int T, int DP, int TILES>
+__device__ __forceinline__ void delta_terms(const Params& p, const QueryWork& w, int i, int r, uint32_t bars, uint32_t tmem, volatile int* gave_up)
+{
+    using S = QueryShape<DP, TILES>;
+    const int n = i ? w.n[1] : w.n[0], t0 = w.t0 + i * p.tokens;
+    const int token = t0 + r / p.group;
+    const bool live = r < p.tokens * p.group && token < w.seq.lq;
+    const int64_t row = w.seq.q0 + token;
+    const float lse = live ? p.lse[row * (p.group * p.kv_heads) + (int)w.head * p.group + r % p.group] : -INFINITY;
+    const uint64_t less = both(lse == -INFINITY ? -INFINITY : lse * -kLog2e), scale2 = both(p.scale2);
+    const int seen = live ? keys_seen(w.seq, token, p.causal) : 0;
+    const int all = keys_seen(w.seq, t0, p.causal);
+    uint64_t sum[2] = {both(0.0f), both(0.0f)};
+    for (int j = 0; j < n; ++j) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * (S::kS + i), j & 1, gave_up))) return;
+        tc_fence_after();
+        uint32_t s[128];
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) tmem_ld32(tmem + i * 128 + c, s + c);
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) tmem_ld32_wait(s + c);
+        tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(bars + 8 * (S::kP + i));
+#pragma unroll
+        for (int c = 0; c < 128; c += 2) {
+            const float2 x = unpair(fma2(pair(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale2, less));
+            s[c] = __float_as_uint(exp2_fast(x.x)), s[c + 1] = __float_as_uint(exp2_fast(x.y));
+        }
+        const int left = seen - j * kRows;
+        const bool cut = (j + 1) * kRows > all;
+        if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * (S::kR + i), j & 1, gave_up))) return;
+        tc_fence_after();
+        uint32_t d[2][32];
+        tmem_ld32(tmem + (TILES + i) * 128, d[0]);
+        tmem_ld32_wait(d[0]);
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+            uint32_t(&v)[32] = d[c / 32 & 1];
+            if (c < 96) tmem_ld32(tmem + (TILES + i) * 128 + c + 32, d[c / 32 + 1 & 1]);   // on its way during this part
+            if (cut) {   // 0 times whatever the hidden keys give
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (c + e >= left) s[c + e] = v[e] = 0;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+                sum[e / 2 & 1] = fma2(pair(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 1])),
+                                      pair(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sum[e / 2 & 1]);
+            if (c < 96) tmem_ld32_wait(d[c / 32 + 1 & 1]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(bars + 8 * (S::kDs + i));
+    }
+    if (!live) return;
+    const float2 a = unpair(sum[0]), b = unpair(sum[1]);
+    float* to = p.stats + w.head * p.stat_pitch + row * p.group + r % p.group;
+    // a row that sees no key: every p is 2^-infinity
+    to[0] = lse == -INFINITY ? -INFINITY : __fmaf_rn(lse, -kLog2e, kUp<T>);
+    to[p.stat_plane] = lse == -INFINITY ? 0.0f : -((a.x + a.y) + (b.x + b.y));
+}
+
+template <int T, int DP, int TILES, bool DELTA>
 __global__ void __launch_bounds__(QueryShape<DP, TILES>::kThreads, 3 - TILES) queries_kernel(const __grid_constant__ Params p)
 {
     using S = QueryShape<DP, TILES>;
@@ -769,7 +846,7 @@ __global__ void __launch_bounds__(QueryShape<DP, TILES>::kThreads, 3 - TILES) qu
         mbar_init_fence();
     }
     wait_for_predecessor_alone();
-    if (p.zero) fill_rows(p.fill_dq, p.seqs.q_starts, p.seqs.count, p.seqs.q_rows);
+    if (!DELTA && p.zero) fill_rows(p.fill_dq, p.seqs.q_starts, p.seqs.count, p.seqs.q_rows);
     QueryWork w;
     if (!find_queries<TILES>(p, w)) return;   // the same for every warp
     if (warp == S::kTermWarps) tmem_alloc<false>(smem_addr(tmem_slot), S::kTmemCols);
@@ -786,18 +863,22 @@ __global__ void __launch_bounds__(QueryShape<DP, TILES>::kThreads, 3 - TILES) qu
             if (n > 0) {
                 if (elect_one()) load_keys<DP, TILES>(p, w, n, smem, bars, gave_up);
                 __syncwarp();
-                clear_keys<DP, TILES>(w, n, smem, bars, lane, gave_up);
+                if constexpr (!DELTA) clear_keys<DP, TILES>(w, n, smem, bars, lane, gave_up);
             }
         } else if (i < TILES && elect_one()) {
-            issue_queries<DP, TILES>(p, w, i, n, smem, bars, tmem, gave_up);
+            if constexpr (DELTA) issue_delta<DP, TILES>(p, w, i, n, smem, bars, tmem, gave_up);
+            else issue_queries<DP, TILES>(p, w, i, n, smem, bars, tmem, gave_up);
             mma_commit<false>(bars + 8 * (S::kDone + i));   // the block does not leave before its products are done
             if (!mbar_wait_alone(bars + 8 * (S::kDone + i), 0)) *gave_up = 1;
         }
     } else {
         many_registers<TILES == 2 ? 224 : 200>();
-        const int i = warp >> 2, exponent = ds_exponent<T>(p);
-        if (w.t0 + i * p.tokens < w.seq.lq)
-            query_terms<T, DP, TILES>(p, w, i, threadIdx.x & 127, bars, tmem + ((uint32_t)((warp & 3) * 32) << 16), exponent, gave_up);
+        const int i = warp >> 2;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        if (w.t0 + i * p.tokens < w.seq.lq) {
+            if constexpr (DELTA) delta_terms<T, DP, TILES>(p, w, i, threadIdx.x & 127, bars, lanes, gave_up);
+            else query_terms<T, DP, TILES>(p, w, i, threadIdx.x & 127, bars, lanes, ds_exponent<T>(p), gave_up);
+        }
     }
     __syncthreads();
     if (threadIdx.x == 0 && *gave_up) atomicExch(&g_attention_bwd_wait_expired, 1);
@@ -831,7 +912,7 @@ Plan plan_for(const gs_attention_bwd_args& a)
     // the last copy of a plane's statistics reads up to a tile past the last row
     r.stat_plane = round_up(a.kv_heads * r.stat_pitch + kStatRows, 64);
     r.stats = (size_t)r.stat_plane * 8;
-    const int64_t want = (a.q_rows * a.heads + 31) / 32, most = sms * (a.type == GS_F16 ? 2 : 8);
+    const int64_t want = (a.q_rows * a.heads + a.k_rows * a.kv_heads + 63) / 64, most = sms * 2;
     r.blocks = (int)(want < 1 ? 1 : (want < most ? want : most));
     r.most = a.type == GS_F16 ? (size_t)round_up(r.blocks * 8, 256) : 0;
     if (!tensor_tma(a.q, a.q_row, a.q_head, a.q_rows, a.heads)) r.packs += packed_bytes(a.q_rows, a.heads, a.dim);
@@ -848,17 +929,22 @@ gs_status launch_one(K* kernel, int smem, int threads, std::atomic<uint64_t>& do
     const gs_status s = allow_smem(kernel, smem, done);
     return s != GS_OK ? s : launch_after(kernel, dim3((unsigned)items), (unsigned)threads, (size_t)smem, 1, st, p);
 }
-template <int T, int DP>
-gs_status launch(const Params& p, const Plan& plan, cudaStream_t st)
+template <int T, int DP, bool DELTA>
+gs_status launch_queries(const Params& p, const Plan& plan, cudaStream_t st)
 {
-    static std::atomic<uint64_t> keys_done{0}, one_done{0}, two_done{0};
-    gs_status s = GS_OK;
-    if (p.dk) s = launch_one(keys_kernel<T, DP>, KeyShape<DP>::kSmem, kKeyThreads, keys_done, plan.key_items, p, st);
-    if (s != GS_OK || !p.dq) return s;
+    static std::atomic<uint64_t> one_done{0}, two_done{0};
     if constexpr (DP == 128)
         if (plan.tiles == 2)
-            return launch_one(queries_kernel<T, DP, 2>, QueryShape<DP, 2>::kSmem, QueryShape<DP, 2>::kThreads, two_done, plan.query_items, p, st);
-    return launch_one(queries_kernel<T, DP, 1>, QueryShape<DP, 1>::kSmem, QueryShape<DP, 1>::kThreads, one_done, plan.query_items, p, st);
+            return launch_one(queries_kernel<T, DP, 2, DELTA>, QueryShape<DP, 2>::kSmem, QueryShape<DP, 2>::kThreads, two_done, plan.query_items, p, st);
+    return launch_one(queries_kernel<T, DP, 1, DELTA>, QueryShape<DP, 1>::kSmem, QueryShape<DP, 1>::kThreads, one_done, plan.query_items, p, st);
+}
+template <int T, int DP>
+gs_status launch(const Params& p, const Plan& plan, bool pairs, cudaStream_t st)
+{
+    static std::atomic<uint64_t> done{0};
+    gs_status s = pairs ? launch_queries<T, DP, true>(p, plan, st) : GS_OK;
+    if (s == GS_OK && p.dk) s = launch_one(keys_kernel<T, DP>, KeyShape<DP>::kSmem, kKeyThreads, done, plan.key_items, p, st);
+    return s == GS_OK && p.dq ? launch_queries<T, DP, false>(p, plan, st) : s;
 }
 
 }  // namespace
@@ -887,7 +973,6 @@ extern "C" gs_status gs_attention_bwd(const gs_attention_bwd_args* args, void* w
     if (!a.dk != !a.dv && a.k_rows > 0) return GS_ERR_INVALID_ARG;
     if (a.q_rows > 0) {
         if (!tensor_ok(a.q, a.q_row, a.q_head, a.q_rows, a.heads, a.dim, false) ||
-            !tensor_ok(a.o, a.o_row, a.o_head, a.q_rows, a.heads, a.dim, false) ||
             !tensor_ok(a.d_o, a.do_row, a.do_head, a.q_rows, a.heads, a.dim, false) || !a.lse || ((uintptr_t)a.lse & 3u))
             return GS_ERR_INVALID_ARG;
         if (a.dq && !tensor_ok(a.dq, a.dq_row, a.dq_head, a.q_rows, a.heads, a.dim, true)) return GS_ERR_INVALID_ARG;
@@ -925,27 +1010,23 @@ extern "C" gs_status gs_attention_bwd(const gs_attention_bwd_args* args, void* w
         if (s == GS_OK) s = tile_map(&p.v, v, a.type, a.k_rows, a.kv_heads, a.dim, 1, kRows);
         if (s == GS_OK) s = packs.run(st);
         if (s != GS_OK) return s;
-        StatParams t = {};
-        t.o = (const uint16_t*)a.o, t.o_row = a.o_row, t.o_head = a.o_head;
-        t.d_o = (const uint16_t*)a.d_o, t.do_row = a.do_row, t.do_head = a.do_head;
-        t.v = (const uint16_t*)a.v, t.v_row = a.v_row, t.v_head = a.v_head;
-        t.lse = a.lse, t.stats = stats, t.most = most, t.q_rows = a.q_rows, t.k_rows = a.k_rows, t.stat_pitch = plan.stat_pitch, t.stat_plane = plan.stat_plane;
-        t.heads = a.heads, t.kv_heads = a.kv_heads, t.group = plan.group, t.dim = a.dim;
-        t.vec = a.dim % 8 == 0 && tensor_tma(a.o, a.o_row, a.o_head, a.q_rows, a.heads) &&
-                tensor_tma(a.d_o, a.do_row, a.do_head, a.q_rows, a.heads) &&
-                (!most || tensor_tma(a.v, a.v_row, a.v_head, a.k_rows, a.kv_heads));
-        const auto run = [&](auto kernel) { return launch_after(kernel, dim3((unsigned)plan.blocks), 256, 0, 1, st, t); };
-        if (a.type == GS_BF16)
-            s = a.dim > 64 ? run(stats_kernel<GS_BF16, 16>) : a.dim > 32 ? run(stats_kernel<GS_BF16, 8>) : run(stats_kernel<GS_BF16, 4>);
-        else s = a.dim > 64 ? run(stats_kernel<GS_F16, 16>) : a.dim > 32 ? run(stats_kernel<GS_F16, 8>) : run(stats_kernel<GS_F16, 4>);
-        if (s != GS_OK) return s;
+        if (most) {
+            MostParams t = {};
+            t.d_o = (const uint16_t*)a.d_o, t.do_row = a.do_row, t.do_head = a.do_head;
+            t.v = (const uint16_t*)a.v, t.v_row = a.v_row, t.v_head = a.v_head;
+            t.most = most, t.q_rows = a.q_rows, t.k_rows = a.k_rows, t.heads = a.heads, t.kv_heads = a.kv_heads, t.dim = a.dim;
+            t.vec = a.dim % 8 == 0 && tensor_tma(a.d_o, a.do_row, a.do_head, a.q_rows, a.heads) &&
+                    tensor_tma(a.v, a.v_row, a.v_head, a.k_rows, a.kv_heads);
+            s = launch_after(most_kernel, dim3((unsigned)plan.blocks), 256, 0, 1, st, t);
+            if (s != GS_OK) return s;
+        }
     }
     p.seqs = {a.q_starts, a.k_starts, nullptr, a.q_rows, a.k_rows, (uint32_t)a.sequences};
     p.zero = a.fill && a.q_starts;
     p.fill_dq = {(uint16_t*)a.dq, a.dq_row, a.dq_head, nullptr, a.heads, a.dim};
     p.fill_dk = {(uint16_t*)a.dk, a.dk_row, a.dk_head, nullptr, a.kv_heads, a.dim};
     p.fill_dv = {(uint16_t*)a.dv, a.dv_row, a.dv_head, nullptr, a.kv_heads, a.dim};
-    p.stats = stats, p.most = most, p.most_count = plan.blocks, p.stat_pitch = plan.stat_pitch, p.stat_plane = plan.stat_plane;
+    p.stats = stats, p.lse = a.lse, p.most = most, p.most_count = plan.blocks, p.stat_pitch = plan.stat_pitch, p.stat_plane = plan.stat_plane;
     p.dq = dq ? (uint16_t*)a.dq : nullptr, p.dq_row = a.dq_row, p.dq_head = a.dq_head;
     p.dk = dk ? (uint16_t*)a.dk : nullptr, p.dk_row = a.dk_row, p.dk_head = a.dk_head;
     p.dv = (uint16_t*)a.dv, p.dv_row = a.dv_row, p.dv_head = a.dv_head;
@@ -957,6 +1038,7 @@ extern "C" gs_status gs_attention_bwd(const gs_attention_bwd_args* args, void* w
     p.dv_vec = tensor_vec(a.dv, a.dv_row, a.dv_head, a.k_rows, a.kv_heads);
     p.idesc_s = instr_desc(a.type, true, true, kRows, kRows);
     p.idesc_d = instr_desc(a.type, true, false, (int)round_up(a.dim, 16), kRows);
-    if (a.type == GS_BF16) return plan.dp == 64 ? launch<GS_BF16, 64>(p, plan, st) : launch<GS_BF16, 128>(p, plan, st);
-    return plan.dp == 64 ? launch<GS_F16, 64>(p, plan, st) : launch<GS_F16, 128>(p, plan, st);
+    const bool pairs = a.q_rows > 0 && a.k_rows > 0;
+    if (a.type == GS_BF16) return plan.dp == 64 ? launch<GS_BF16, 64>(p, plan, pairs, st) : launch<GS_BF16, 128>(p, plan, pairs, st);
+    return plan.dp == 64 ? launch<GS_F16, 64>(p, plan, pairs, st) : launch<GS_F16, 128>(p, plan, pairs, st);
 }

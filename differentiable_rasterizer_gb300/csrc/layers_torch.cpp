@@ -656,12 +656,12 @@ PyObject* attention_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
         const Heads hk = heads_of(k, "k", type, dev, -1, -1, hq.dim);
         const Heads hv = heads_of(v, "v", type, dev, hk.rows, hk.heads, hq.dim);
         const Heads hd = heads_of(tensor(a[0], "do"), "do", type, dev, hq.rows, hq.heads, hq.dim);
-        const Heads ho = heads_of(tensor(a[4], "o"), "o", type, dev, hq.rows, hq.heads, hq.dim);
+        if (a[4] != Py_None) heads_of(tensor(a[4], "o"), "o", type, dev, hq.rows, hq.heads, hq.dim);
         groups(hq, hk);
         gs_attention_bwd_args g = {};
         g.q_rows = hq.rows, g.k_rows = hk.rows;
         g.q = hq.p, g.q_row = hq.row, g.q_head = hq.head, g.k = hk.p, g.k_row = hk.row, g.k_head = hk.head;
-        g.v = hv.p, g.v_row = hv.row, g.v_head = hv.head, g.o = ho.p, g.o_row = ho.row, g.o_head = ho.head;
+        g.v = hv.p, g.v_row = hv.row, g.v_head = hv.head;
         g.d_o = hd.p, g.do_row = hd.row, g.do_head = hd.head;
         g.lse = (const float*)required(vector_of(a[5], "lse", kF32, dev, hq.rows * hq.heads), "lse (attention's with need_backward)",
                                        hq.rows * hq.heads);

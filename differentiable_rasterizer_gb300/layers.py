@@ -228,7 +228,8 @@ def attention(q, k, v, *, q_starts=None, k_starts=None, k_lengths=None, causal=F
 def attention_backward(do, q, k, v, o, lse, *, q_starts=None, k_starts=None, causal=False, scale=None,
                        out=None) -> AttentionGrads:
     """Gradients of attention from do, in q's type; o, lse: attention's with need_backward, the
-    other arguments as they were given to it.  out: (dq, dk, dv) to write to (column ranges of
+    other arguments as they were given to it.  (o, already rounded, is checked but not computed
+    with, and may be None: the rows' sums of do . o are taken from the terms again.)  out: (dq, dk, dv) to write to (column ranges of
     the projection's gradient, say), rows of no sequence are left as they are; else 0."""
     dq, dk, dv = (None, None, None) if out is None else out
     return AttentionGrads(*_native.attention_backward(do, q, k, v, o, lse, q_starts, k_starts, causal, scale, dq, dk, dv))

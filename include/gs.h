@@ -720,12 +720,12 @@ typedef struct gs_attention_args {
 GS_API gs_status gs_attention(const gs_attention_args* args, void* ws, size_t* ws_bytes, void* stream);
 
 /* Gradients of gs_attention (without k_lengths).  p_ij = exp(t_ij - lse_i):
- *   delta_i = do_i . o_i,  ds_ij = p_ij (do_i . v_j - delta_i)
+ *   r_ij = do_i . v_j,  delta_i = sum_j p_ij r_ij,  ds_ij = p_ij (r_ij - delta_i)
  *   dq_i = scale sum_j ds_ij k_j;  dk_j = scale sum_i ds_ij q_i;  dv_j = sum_i p_ij do_i
  * dk and dv sum over the query heads that share a key head.  p and ds are rounded to
  * `type` as factors of these products (F16: times powers of two that keep them among
- * its normal numbers, ds by the largest magnitudes in all of d_o and v).  q, k, v, o, lse: the forward's.  do, dq: like q;
- * dk, dv: like k.  dq may be NULL, and so may dk and dv together (not computed).
+ * its normal numbers, ds by the largest magnitudes in all of d_o and v).  q, k, v, lse:
+ * the forward's.  d_o, dq: like q; dk, dv: like k.  dq may be NULL, and so may dk and dv together (not computed).
  * Rows that belong to no sequence: as gs_attention, in dq, dk and dv.  A NaN or an
  * infinity in d_o or q reaches keys that are hidden from its query within 256 tokens.
  * Errors: as gs_attention. */
@@ -737,8 +737,6 @@ typedef struct gs_attention_bwd_args {
     int64_t k_row, k_head;
     const void* v;
     int64_t v_row, v_head;
-    const void* o;
-    int64_t o_row, o_head;
     const void* d_o;
     int64_t do_row, do_head;
     const float* lse;

@@ -24,7 +24,7 @@ def abi():
 ATTENTION = dict(q_rows=40, k_rows=50, sequences=1, q=4096, q_row=256, q_head=64, k=4096, k_row=128, k_head=64, v=4096, v_row=128,
                  v_head=64, q_starts=0, k_starts=0, k_lengths=0, o=4096, o_row=256, o_head=64, lse=0, scale=0.125, heads=4, kv_heads=2,
                  dim=64, type_=1, causal=0, fill=0)
-ATTENTION_BWD = dict({k: v for k, v in ATTENTION.items() if k not in ("k_lengths",)}, d_o=4096, do_row=256, do_head=64, lse=4096, dq=4096,
+ATTENTION_BWD = dict({k: v for k, v in ATTENTION.items() if k not in ("k_lengths", "o", "o_row", "o_head")}, d_o=4096, do_row=256, do_head=64, lse=4096, dq=4096,
                      dq_row=256, dq_head=64, dk=4096, dk_row=128, dk_head=64, dv=4096, dv_row=128, dv_head=64)
 BLOCK_NORM = dict(rows=4, cols=32, h=4096, ldh=32, x=4096, ldx=32, post_weight=4096, gate=4096, ldg=0, weight=4096, s=4096, lds=32, y=4096,
                   ldy=32, y_scale=0, rstd_post=4096, rstd=4096, scale=1.0, eps=1e-6, type_=1, post_type=1, gate_type=1, gate_rows=0,
@@ -37,10 +37,10 @@ SIZES = [dict(q_rows=-1), dict(k_rows=-1), dict(q_rows=2 ** 31), dict(sequences=
          dict(k_starts=4096), dict(q_starts=4098, k_starts=4096), dict(heads=0), dict(kv_heads=0), dict(kv_heads=3), dict(heads=258, kv_heads=2),
          dict(dim=0), dict(dim=129), dict(type_=0), dict(type_=3), dict(type_=7), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
          dict(scale=float("inf")), dict(q=0), dict(q=4097), dict(q_row=63), dict(q_head=63), dict(k=0), dict(k_row=63), dict(v=0), dict(v_head=63),
-         dict(q_row=2 ** 39), dict(o=0), dict(o_row=128)]
+         dict(q_row=2 ** 39)]
 BAD = {
-    "gs_attention": SIZES + [dict(o_row=64, o_head=64), dict(lse=4098), dict(k_lengths=4098), dict(o=4097)],
-    "gs_attention_bwd": SIZES[:-1] + [dict(lse=0), dict(lse=4098), dict(d_o=0), dict(do_row=63), dict(dq_row=128), dict(dk=0), dict(dv=0),
+    "gs_attention": SIZES + [dict(o=0), dict(o_row=128), dict(o_row=64, o_head=64), dict(lse=4098), dict(k_lengths=4098), dict(o=4097)],
+    "gs_attention_bwd": SIZES + [dict(lse=0), dict(lse=4098), dict(d_o=0), dict(do_row=63), dict(dq_row=128), dict(dk=0), dict(dv=0),
                                       dict(dk_row=64, dk_head=64), dict(dv_head=63), dict(dq=4097)],
     "gs_block_norm_bwd": [dict(rows=-1), dict(cols=0), dict(cols=16385), dict(type_=3), dict(dy_type=3), dict(dy=0), dict(rstd=0), dict(rstd=4098),
                           dict(weight=0), dict(weight=4097), dict(s=0), dict(lds=31), dict(h=0), dict(ldh=31), dict(rstd_post=0),
@@ -117,7 +117,7 @@ def test_workspaces(abi):
 
 def test_calls_that_need_no_device(abi):
     assert abi.gs_attention(pack(abi, "gs_attention", dict(ATTENTION, q_rows=0, q=0, o=0)), None, None, None) is None
-    nothing = dict(ATTENTION_BWD, q_rows=0, k_rows=0, q=0, k=0, v=0, o=0, d_o=0, lse=0)
+    nothing = dict(ATTENTION_BWD, q_rows=0, k_rows=0, q=0, k=0, v=0, d_o=0, lse=0)
     need = abi.layer_ws_bytes("gs_attention_bwd", pack(abi, "gs_attention_bwd", nothing))
     assert abi.gs_attention_bwd(pack(abi, "gs_attention_bwd", nothing), 4096, need, None) is None
     abi.gs_block_norm(**dict(BLOCK_NORM, rows=0, h=0, x=0, s=0, y=0), stream=None)

@@ -8,9 +8,10 @@ run; no case has its own).  With u(T) half a step of type T relative to the valu
   o       (u + 2.2 dt + 2^-20 + keys 2^-23) sum p |v|, u |o| for o's own rounding: the sum
           of p is off by dt as well, and p v adds in fp32, truncating
   lse     dt + 2^-20 + 2^-22 |lse| + keys 2^-23
-The gradients are compared with the formulas at the forward's stored o and lse:
+The gradients are compared with the formulas at the forward's stored lse:
   p       1.1 dt + 2^-20 + 2^-22 |lse| relative (the difference t - lse in fp32)
-  r       dim 2^-23 sum |do| |v|, delta: dim 2^-23 sum |do| |o|
+  r       dr = dim 2^-23 sum |do| |v|
+  delta   sum of p (dp |r| + dr), keys 2^-23 sum p |r|
   ds      dds = p (dp |r - delta| + dr + ddelta) + u |ds|
   dv      (u + dp + rows 2^-23) sum p |do|;  dq: scale (sum dds |k| + keys 2^-23 sum |ds| |k|);
   dk      the same over the rows, with q
@@ -121,17 +122,19 @@ def check_backward(g, do, a, q, k, v, q_lens, k_lens, causal, scale, q_first=0, 
     for s, (lq, lk) in enumerate(zip(q_lens, k_lens)):
         for h in range(kv):
             hs, rows, keys = slice(h * n, h * n + n), slice(q0, q0 + lq), slice(k0, k0 + lk)
-            qq, dd, oo = (t[rows, hs].double().transpose(0, 1) for t in (q, do, a.o))
+            qq, dd = (t[rows, hs].double().transpose(0, 1) for t in (q, do))
             kk, vv = k[keys, h].double(), v[keys, h].double()
             x = Sequence64(qq, kk, vv, causal, scale)
             lse = a.lse[rows, hs].double().t()
             t = ((qq @ kk.t()) * scale).masked_fill(~x.see, float("-inf"))
             p = torch.exp(t - lse.clamp_min(-1e300)[..., None])
             dp = (1.1 * x.dt + 2.0 ** -20 + 2.0 ** -22 * lse.abs().nan_to_num(posinf=0.0))[..., None]
-            r, delta = dd @ vv.t(), (dd * oo).sum(-1, keepdim=True)
+            r = dd @ vv.t()
+            delta = (p * r).sum(-1, keepdim=True)
             ds = p * (r - delta)
-            dr = dim * 2.0 ** -23 * (dd.abs() @ vv.abs().t() + (dd.abs() * oo.abs()).sum(-1, keepdim=True))
-            dds = p * (dp * (r - delta).abs() + dr) + u * ds.abs() + floor_ds * x.see
+            dr = dim * 2.0 ** -23 * (dd.abs() @ vv.abs().t())
+            ddelta = (p * ((dp + lk * 2.0 ** -23) * r.abs() + dr)).sum(-1, keepdim=True)
+            dds = p * (dp * (r - delta).abs() + dr + ddelta) + u * ds.abs() + floor_ds * x.see
             total = n * lq
             close(g.dv[keys, h], (p.transpose(1, 2) @ dd).sum(0),
                   (((u + dp + total * 2.0 ** -23) * p + floor_p * x.see).transpose(1, 2) @ dd.abs()).sum(0), f"dv of sequence {s}, key head {h}")
