@@ -20,6 +20,7 @@
 // (at most 1 times that), ds times the power of two that brings its bound, 2 dim max|do|
 // max|v|, to 2^15; the sums are scaled back at the end.
 #include <atomic>
+#include <cmath>
 
 #include "attention.cuh"
 
@@ -49,8 +50,9 @@ struct Params {
     uint16_t *dq, *dk, *dv;
     int64_t dq_row, dq_head, dk_row, dk_head, dv_row, dv_head;
     int64_t stat_pitch, stat_plane;   // of a key head; to the second plane
+    float* part;             // parts > 1: [part][key row][key head][dv, dk][DP] sums
     float scale, scale2;     // scale2: scale log2(e)
-    uint32_t kv_heads;
+    uint32_t kv_heads, parts;
     int group, tokens, dim, causal, zero, dq_vec, dk_vec, dv_vec;
     uint32_t idesc_s, idesc_d;
 };
@@ -157,17 +159,27 @@ struct KeyWork {
     Sequence seq;
     uint32_t head;
     int key0, first, n;   // first key; first token of the first tile of queries; tiles
+    int each;             // tiles of a part
 };
-__device__ __forceinline__ bool find_keys(const Params& p, KeyWork& w)
+// Work number i: a tile of keys of a head, all of its queries.
+__device__ __forceinline__ bool find_keys(const Params& p, uint32_t i, KeyWork& w)
 {
     uint32_t unit, units;
-    w.head = blockIdx.x % p.kv_heads;
-    if (!find_unit<true>(p.seqs, blockIdx.x / p.kv_heads, kRows, w.seq, unit, units)) return false;
+    w.head = i % p.kv_heads;
+    if (!find_unit<true>(p.seqs, i / p.kv_heads, kRows, w.seq, unit, units)) return false;
     w.key0 = (int)unit * kRows;          // the first keys are seen by the most queries
     w.first = first_query(w.seq, w.key0, p.causal);
     const int left = w.seq.lq - w.first;
     w.n = left <= 0 ? 0 : (left + p.tokens - 1) / p.tokens;
+    w.each = (w.n + (int)p.parts - 1) / (int)p.parts;
     return true;
+}
+// A part of them.
+__device__ __forceinline__ void take_part(const Params& p, uint32_t part, KeyWork& w)
+{
+    const int from = (int)part * w.each, n = w.n - from;
+    w.first += from * p.tokens;
+    w.n = n < 0 ? 0 : (n < w.each ? n : w.each);
 }
 
 template <int DP>
@@ -404,7 +416,12 @@ __device__ __forceinline__ void key_terms(const Params& p, const KeyWork& w, int
         }
 #pragma unroll
         for (int e = 0; e < 32; ++e) f[e] = w.n > 0 ? __uint_as_float(v[e]) * by : 0.0f;
-        if (live && c < p.dim) store_row32<T>(to, c, p.dim, half == 0 ? p.dv_vec : p.dk_vec, f);
+        if (p.parts > 1) {
+            float* part = p.part + ((((int64_t)(blockIdx.x % p.parts) * p.seqs.k_rows + row) * p.kv_heads + w.head) * 2 + half) * DP + c;
+            if (live)
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(part + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+        } else if (live && c < p.dim) store_row32<T>(to, c, p.dim, half == 0 ? p.dv_vec : p.dk_vec, f);
     }
     tc_fence_before();
 }
@@ -438,7 +455,11 @@ __global__ void __launch_bounds__(kKeyThreads, 1) keys_kernel(const __grid_const
         fill_rows(p.fill_dv, p.seqs.k_starts, p.seqs.count, p.seqs.k_rows);
     }
     KeyWork w;
-    if (!find_keys(p, w)) return;   // the same for every warp
+    if (!find_keys(p, blockIdx.x / p.parts, w)) return;   // the same for every warp
+    if (p.parts > 1) {
+        take_part(p, blockIdx.x % p.parts, w);
+        if (w.n == 0) return;   // the join knows
+    }
     if (warp == kKeyWarps) tmem_alloc<false>(smem_addr(tmem_slot), kTmemCols);
     const int packed = p.tokens * p.group;
     if (packed < kRows && w.n > 0)   // rows that no copy writes
@@ -472,6 +493,35 @@ __global__ void __launch_bounds__(kKeyThreads, 1) keys_kernel(const __grid_const
     if (warp == kKeyWarps) {
         tc_fence_after();
         tmem_free<false>(tmem, kTmemCols);
+    }
+}
+
+// The parts' sums of a tile of keys, added in order.  A thread 32 columns of a row.
+template <int T, int DP>
+__global__ void __launch_bounds__(256) keys_join_kernel(const __grid_constant__ Params p)
+{
+    wait_for_predecessor();
+    KeyWork w;
+    if (!find_keys(p, blockIdx.x, w)) return;
+    const int parts = w.each ? (w.n + w.each - 1) / w.each : 0;
+    int rows = w.seq.lk - w.key0;
+    rows = rows < kRows ? rows : kRows;
+    constexpr int kSteps = 2 * DP / 32;   // of a row: dv, then dk
+    for (int i = threadIdx.x; i < rows * kSteps; i += 256) {
+        const int64_t row = w.seq.k0 + w.key0 + i / kSteps;
+        const int half = i % kSteps / (kSteps / 2), c = i % (kSteps / 2) * 32;
+        const float* from = p.part + ((row * p.kv_heads + w.head) * 2 + half) * DP + c;
+        float f[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) f[e] = 0.0f;
+        for (int k = 0; k < parts; ++k, from += p.seqs.k_rows * p.kv_heads * 2 * DP)
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(from + e);
+                f[e] += v.x, f[e + 1] += v.y, f[e + 2] += v.z, f[e + 3] += v.w;
+            }
+        uint16_t* to = half == 0 ? p.dv + row * p.dv_row + w.head * p.dv_head : p.dk + row * p.dk_row + w.head * p.dk_head;
+        if (c < p.dim) store_row32<T>(to, c, p.dim, half == 0 ? p.dv_vec : p.dk_vec, f);
     }
 }
 
@@ -890,8 +940,9 @@ __global__ void __launch_bounds__(QueryShape<DP, TILES>::kThreads, 3 - TILES) qu
 
 struct Plan {
     int group, tokens, tiles, dp, blocks;
+    uint32_t parts;
     int64_t query_items, key_items, stat_pitch, stat_plane;
-    size_t stats, most, packs, bytes;
+    size_t stats, most, part, packs, bytes;
 };
 Plan plan_for(const gs_attention_bwd_args& a)
 {
@@ -908,6 +959,22 @@ Plan plan_for(const gs_attention_bwd_args& a)
     r.tiles = r.dp == 128 && two * a.kv_heads >= sms && a.q_rows > a.sequences * r.tokens ? 2 : 1;
     r.query_items = (r.tiles == 2 ? two : units_at_most(a.q_rows, a.sequences, starts, r.tokens)) * a.kv_heads;
     r.key_items = units_at_most(a.k_rows, a.sequences, starts, kRows) * a.kv_heads;
+    // Parts of a tile of keys' queries: what the longest takes (1.6 us a tile of queries) or the
+    // SMs' share of all, against the blocks' starts and the parts' sums.  us by parts, all
+    // gradients: 2048 tokens, 1 key head of 64 236 (1), 126 (3), 97 (8), 104 (16); 16384, 1 of
+    // 128 1248 (1), 911 (3), 991 (6); 4096, 4 of 64 297 (1), 228 (2), 239 (3); 4096, 16 of 128
+    // without a mask 465 (1), 555 (2).
+    r.parts = 1;
+    const int64_t sequences = a.sequences > 0 ? a.sequences : 1, query_tiles = (a.q_rows / sequences + r.tokens - 1) / r.tokens;
+    double best = 0;
+    for (int64_t n = 1; n <= 32 && (n == 1 || 2 * n <= query_tiles); ++n) {
+        const double longest = std::ceil((double)query_tiles / (double)n) * 1.6;
+        const double work = (double)(r.key_items * query_tiles) * (a.causal ? 0.8 : 1.6) / (double)sms;
+        const double us = (work > longest ? work : longest) + 0.15 * longest + 4.0 * (double)(r.key_items * n) / (double)sms +
+                          (n > 1 ? 6 + 0.4 * (double)n + (double)(n * a.k_rows * a.kv_heads) * r.dp * 16 / 2e6 : 0.0);
+        if (n == 1 || us < best) best = us, r.parts = (uint32_t)n;
+    }
+    if (r.parts > 1) r.part = (size_t)round_up(r.parts * a.k_rows * a.kv_heads * r.dp * 8, 256);
     r.stat_pitch = round_up(a.q_rows * r.group, 4);
     // the last copy of a plane's statistics reads up to a tile past the last row
     r.stat_plane = round_up(a.kv_heads * r.stat_pitch + kStatRows, 64);
@@ -919,7 +986,7 @@ Plan plan_for(const gs_attention_bwd_args& a)
     if (!tensor_tma(a.d_o, a.do_row, a.do_head, a.q_rows, a.heads)) r.packs += packed_bytes(a.q_rows, a.heads, a.dim);
     if (!tensor_tma(a.k, a.k_row, a.k_head, a.k_rows, a.kv_heads)) r.packs += packed_bytes(a.k_rows, a.kv_heads, a.dim);
     if (!tensor_tma(a.v, a.v_row, a.v_head, a.k_rows, a.kv_heads)) r.packs += packed_bytes(a.k_rows, a.kv_heads, a.dim);
-    r.bytes = r.stats + r.most + r.packs;
+    r.bytes = r.part + r.stats + r.most + r.packs;
     return r;
 }
 
@@ -943,7 +1010,8 @@ gs_status launch(const Params& p, const Plan& plan, bool pairs, cudaStream_t st)
 {
     static std::atomic<uint64_t> done{0};
     gs_status s = pairs ? launch_queries<T, DP, true>(p, plan, st) : GS_OK;
-    if (s == GS_OK && p.dk) s = launch_one(keys_kernel<T, DP>, KeyShape<DP>::kSmem, kKeyThreads, done, plan.key_items, p, st);
+    if (s == GS_OK && p.dk) s = launch_one(keys_kernel<T, DP>, KeyShape<DP>::kSmem, kKeyThreads, done, plan.key_items * plan.parts, p, st);
+    if (s == GS_OK && p.dk && plan.parts > 1) s = launch_after(keys_join_kernel<T, DP>, dim3((unsigned)plan.key_items), 256, 0, 1, st, p);
     return s == GS_OK && p.dq ? launch_queries<T, DP, false>(p, plan, st) : s;
 }
 
@@ -986,16 +1054,16 @@ extern "C" gs_status gs_attention_bwd(const gs_attention_bwd_args* args, void* w
             return GS_ERR_INVALID_ARG;
     }
     const Plan plan = plan_for(a);
-    if (plan.query_items > 0x7fffffffll || plan.key_items > 0x7fffffffll) return GS_ERR_INVALID_ARG;
+    if (plan.query_items > 0x7fffffffll || plan.key_items * plan.parts > 0x7fffffffll) return GS_ERR_INVALID_ARG;
     const WsCheck wc = ws_check(ws, ws_bytes, plan.bytes);
     if (wc == WsCheck::kBad) return GS_ERR_INVALID_ARG;
     if (wc == WsCheck::kQuery) return GS_OK;
     cudaStream_t st = (cudaStream_t)stream;
     const bool dq = a.dq && a.q_rows > 0, dk = a.dk && a.k_rows > 0;
     if (!dq && !dk) return GS_OK;
-    float* stats = (float*)ws;
-    float* most = plan.most ? (float*)((char*)ws + plan.stats) : nullptr;
-    char* to = (char*)ws + plan.stats + plan.most;
+    float* stats = (float*)((char*)ws + plan.part);
+    float* most = plan.most ? (float*)((char*)ws + plan.part + plan.stats) : nullptr;
+    char* to = (char*)ws + plan.part + plan.stats + plan.most;
     PackList packs;
     Params p = {};
     gs_status s = GS_OK;
@@ -1031,6 +1099,7 @@ extern "C" gs_status gs_attention_bwd(const gs_attention_bwd_args* args, void* w
     p.dk = dk ? (uint16_t*)a.dk : nullptr, p.dk_row = a.dk_row, p.dk_head = a.dk_head;
     p.dv = (uint16_t*)a.dv, p.dv_row = a.dv_row, p.dv_head = a.dv_head;
     p.scale = a.scale, p.scale2 = a.scale * kLog2e;
+    p.part = (float*)ws, p.parts = plan.parts;
     p.kv_heads = (uint32_t)a.kv_heads, p.group = plan.group, p.tokens = plan.tokens, p.dim = a.dim;
     p.causal = a.causal != 0;
     p.dq_vec = tensor_vec(a.dq, a.dq_row, a.dq_head, a.q_rows, a.heads);
