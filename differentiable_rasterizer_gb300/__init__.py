@@ -5,7 +5,8 @@ The compute path is a CUDA library for sm_103a behind a C ABI (``include/gs.h``)
 and ``gs_adam_deferred``.  ``differentiable_rasterizer_gb300.abi`` is the thin
 ctypes binding of those calls; ``differentiable_rasterizer_gb300.pipeline`` drives
 one training step with torch tensors as device memory.  ``layers`` calls the decoder
-layers (norm, linear, gated feed-forward and their gradients) on torch tensors, and
+layers (norm, linear, gated feed-forward, attention, block norm, their gradients, and
+clipping) on torch tensors, and
 ``decoder`` joins them into a network that produces a scene's Gaussians and trains
 through the rasterizer.  ``scenes`` draws the seeded synthetic inputs.
 

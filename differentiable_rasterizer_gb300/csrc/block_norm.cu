@@ -9,7 +9,10 @@
 // at eight columns a thread, so that narrow rows share a warp and rows of up to 256 columns
 // need no barrier.  As separate norm, product, sum and norm a row would cross HBM nine times in
 // place of four.
-//   1,000,000 x 256 bf16  303 us at HBM's rate; 500 with weights fetched for each row
+//   1,000,000 x 256 bf16 334 us, 6.1 TB/s (302 at the copy's rate; without the next row's loads
+//   ahead 449, with weights fetched for each row 500), its gradients 520 us, 5.9 TB/s
+//   20,011 x 331 f16, a gate a value: 35 and 78 us, bound by instructions and barriers (single
+//   elements 138 and 364)
 #include <type_traits>
 
 #include "gemm.cuh"

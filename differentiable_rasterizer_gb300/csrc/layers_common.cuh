@@ -1,5 +1,6 @@
 // layers_common.cuh -- element types, conversions and activations shared by the
-// decoder layers (norm.cu, linear.cu, gemm.cu, glu_narrow.cu).
+// decoder layers (norm.cu, block_norm.cu, linear.cu, gemm.cu, glu_narrow.cu, attention*.cu,
+// clip.cu).
 #pragma once
 
 #include <atomic>

@@ -7,6 +7,9 @@ gated feed-forward and their gradients, through the C ABI (``gs_rms_norm``,
     y = linear(x, w, bias, act="gelu", residual=r).y         # act(x w^T + b) + r
     h = glu(x, w_gate, w_up, act="silu").h                   # act(x Wg^T) * (x Wu^T)
     y = linear(h, w_down, residual=r).y                      # ... and its down projection
+    a = attention(q, k, v, q_starts=starts, causal=True).o   # over packed sequences
+    b = block_norm(h, x, w, post_weight=p, gate=g, scale=c)  # b.s = c x + g norm(h), b.y = norm(b.s)
+    n = clip_norm(grads, 1.0, out=grads_fp32)                # the norm over all, and all scaled to 1
 
 Tensors are CUDA tensors whose last dimension is contiguous; leading dimensions are
 rows and must merge into one stride (a slice of wider rows is fine).  Rows whose base
