@@ -11,8 +11,9 @@
 // place of four.
 //   1,000,000 x 256 bf16 334 us, 6.1 TB/s (302 at the copy's rate; without the next row's loads
 //   ahead 449, with weights fetched for each row 500), its gradients 520 us, 5.9 TB/s
-//   20,011 x 331 f16, a gate a value: 35 and 78 us, bound by instructions and barriers (single
-//   elements 138 and 364)
+//   20,011 x 331 f16, a gate a value: 35 and 78 us, bound by instructions (single elements 138
+//   and 364; the next row's pieces ahead in shared memory 36 and 83; whole pieces written with
+//   the neighbour's columns 37 and 79)
 #include <type_traits>
 
 #include "gemm.cuh"
@@ -26,7 +27,8 @@ using namespace rows;
 // A matrix's rows as a thread reads them, eight columns at a time.  Rows of 16-byte base and
 // pitch: whole pieces, of which a row's last may lie in its padding.  Others of 16-bit
 // elements: the two aligned pieces that the eight columns lie in, shifted together; single
-// elements in the first and the last row, whose pieces may reach beyond the matrix, and in fp32.
+// elements in the first and the last row and where the pitch is below eight, whose pieces may
+// reach beyond the matrix, and in fp32.
 struct Source {
     const void* p;
     int64_t ld;
@@ -34,6 +36,8 @@ struct Source {
     bool aligned;
     __device__ __forceinline__ Source(const void* p_, int64_t ld_, int type_)
         : p(p_), ld(ld_), type(type_), aligned(((uintptr_t)p_ & 15u) == 0 && ld_ * (type_ == GS_F32 ? 4 : 2) % 16 == 0) {}
+    // Pieces that hold columns of this row lie in the matrix.
+    __device__ __forceinline__ bool inside(int64_t row, int64_t rows) const { return row > 0 && row + 1 < rows && ld >= 8; }
 };
 
 // WHOLE: every matrix's rows are whole pieces.
@@ -65,7 +69,7 @@ __device__ __forceinline__ void fetch(Cells<T, WHOLE>& to, const Source& m, int6
         raw_load(to.raw, m.p, at, type);
         return;
     }
-    const bool inside = row > 0 && row + 1 < rows;
+    const bool inside = m.inside(row, rows);
     if (m.aligned && (inside || (cols & 7) == 0)) {
         raw_load(to.raw, m.p, at, type);
     } else if (kShifts<T, WHOLE> && inside) {
@@ -96,7 +100,7 @@ __device__ __forceinline__ void values(const Cells<T, WHOLE>& c, const Source& m
     const int n = cols - col, type = T == kAnyType ? m.type : T;
     Raw<T, 8> raw = c.raw;
     if constexpr (kShifts<T, WHOLE>) {
-        if (!m.aligned && row > 0 && row + 1 < rows) {
+        if (!m.aligned && m.inside(row, rows)) {
             const uint32_t shift = (uint32_t)((uintptr_t)((const uint16_t*)m.p + row * m.ld + col) >> 1) & 7;   // elements
             uint32_t w[8] = {raw.q[0].x, raw.q[0].y, raw.q[0].z, raw.q[0].w, c.high[0], c.high[1], c.high[2], c.high[3]};
 #pragma unroll

@@ -835,11 +835,12 @@ GS_API gs_status gs_block_norm_bwd(const gs_block_norm_bwd_args* args, void* ws,
  * BF16 or F16; out may be p with the same type: in place).  Nothing else may overlap:
  * two tensors that share memory are refused.  The product is rounded once; with a factor
  * of 1 values pass unchanged (in place: nothing is written).  norm: device fp32 out.
- * Squares are summed in fp32 in parts and the parts in fp64, those of very large and
- * very small values apart, so that no norm within fp32's range overflows or vanishes on
- * the way; the sum is taken in a fixed order.  A norm that is not finite (a NaN or an infinity among the
- * values) leaves the values unscaled (factor 1), so that the caller can tell by `norm`
- * and skip the step.  max_norm: not NaN, >= 0.
+ * A thread sums its squares in fp32, a second fp32 number keeping what its additions of a
+ * piece's sum round off; the threads' sums are added in fp64, those of very large and very
+ * small values apart, so that no norm within fp32's range overflows or vanishes on the
+ * way; the sum is taken in a fixed order.  A norm that is not finite (a NaN or an infinity
+ * among the values) leaves the values unscaled (factor 1), so that the caller can tell by
+ * `norm` and skip the step.  max_norm: not NaN, >= 0.
  * Errors: INVALID_ARG; CUDA on launch failure. */
 #define GS_CLIP_MAX_TENSORS 1024
 typedef struct gs_clip_tensor {
