@@ -26,9 +26,10 @@ using namespace rows;
 
 // A matrix's rows as a thread reads them, eight columns at a time.  Rows of 16-byte base and
 // pitch: whole pieces, of which a row's last may lie in its padding.  Others of 16-bit
-// elements: the two aligned pieces that the eight columns lie in, shifted together; single
-// elements in the first and the last row and where the pitch is below eight, whose pieces may
-// reach beyond the matrix, and in fp32.
+// elements: the four or five 32-bit words that the eight columns lie in, shifted by an element
+// where the row starts within a word (two pieces of 16 bytes shifted together took 15
+// instructions more a matrix: 20,011 x 331 OLDF and OLDB us, 250,000 x 197 268 and 410); single
+// elements in the first and the last row, whose words may reach beyond the matrix, and in fp32.
 struct Source {
     const void* p;
     int64_t ld;
@@ -36,8 +37,10 @@ struct Source {
     bool aligned;
     __device__ __forceinline__ Source(const void* p_, int64_t ld_, int type_)
         : p(p_), ld(ld_), type(type_), aligned(((uintptr_t)p_ & 15u) == 0 && ld_ * (type_ == GS_F32 ? 4 : 2) % 16 == 0) {}
-    // Pieces that hold columns of this row lie in the matrix.
-    __device__ __forceinline__ bool inside(int64_t row, int64_t rows) const { return row > 0 && row + 1 < rows && ld >= 8; }
+    // Words that hold columns of this row lie in the matrix.
+    __device__ __forceinline__ bool inside(int64_t row, int64_t rows) const { return row > 0 && row + 1 < rows; }
+    // Whether a row of 16-bit elements, and with it every eighth column, starts within a word.
+    __device__ __forceinline__ uint32_t odd(int64_t row) const { return ((uint32_t)((uintptr_t)p >> 1) + ((uint32_t)row & (uint32_t)ld)) & 1u; }
 };
 
 // WHOLE: every matrix's rows are whole pieces.
@@ -46,12 +49,11 @@ constexpr bool kShifts = !WHOLE && (T == GS_BF16 || T == GS_F16);
 template <int T, bool WHOLE>
 struct Cells {
     Raw<T, 8> raw;
-    uint32_t high[kShifts<T, WHOLE> ? 4 : 1];   // the second piece of unaligned rows
+    uint32_t last;   // a fifth word
     __device__ __forceinline__ void zero()
     {
         raw_zero(raw);
-#pragma unroll
-        for (int e = 0; e < (int)(sizeof high / 4); ++e) high[e] = 0;
+        last = 0;
     }
 };
 // Elements from one to the other, of the eight at p.
@@ -73,14 +75,13 @@ __device__ __forceinline__ void fetch(Cells<T, WHOLE>& to, const Source& m, int6
     if (m.aligned && (inside || (cols & 7) == 0)) {
         raw_load(to.raw, m.p, at, type);
     } else if (kShifts<T, WHOLE> && inside) {
-        const uintptr_t a = (uintptr_t)((const uint16_t*)m.p + at);
-        const uint4* piece = reinterpret_cast<const uint4*>(a & ~(uintptr_t)15);
-        to.raw.q[0] = *piece;
-        if (n > 8 - (int)(a >> 1 & 7)) {
-            const uint4 h = piece[1];
-            to.high[0] = h.x;
-            if constexpr (kShifts<T, WHOLE>) to.high[1] = h.y, to.high[2] = h.z, to.high[3] = h.w;
-        }
+        const int odd = (int)m.odd(row), end = odd + (n < 8 ? n : 8);
+        const uint32_t* word = reinterpret_cast<const uint32_t*>((const uint16_t*)m.p + (at - odd));
+        uint32_t w[5];
+#pragma unroll
+        for (int e = 0; e < 5; ++e) w[e] = 2 * e < end ? word[e] : 0;
+        to.raw.q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        to.last = w[4];
     } else {
         uint32_t w[8];
 #pragma unroll
@@ -100,17 +101,9 @@ __device__ __forceinline__ void values(const Cells<T, WHOLE>& c, const Source& m
     const int n = cols - col, type = T == kAnyType ? m.type : T;
     Raw<T, 8> raw = c.raw;
     if constexpr (kShifts<T, WHOLE>) {
-        if (!m.aligned && m.inside(row, rows)) {
-            const uint32_t shift = (uint32_t)((uintptr_t)((const uint16_t*)m.p + row * m.ld + col) >> 1) & 7;   // elements
-            uint32_t w[8] = {raw.q[0].x, raw.q[0].y, raw.q[0].z, raw.q[0].w, c.high[0], c.high[1], c.high[2], c.high[3]};
-#pragma unroll
-            for (int e = 0; e < 6; ++e) w[e] = shift & 4 ? w[e + 2] : w[e];
-#pragma unroll
-            for (int e = 0; e < 5; ++e) w[e] = shift & 2 ? w[e + 1] : w[e];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = __funnelshift_r(w[e], w[e + 1], shift & 1 ? 16 : 0);
-            raw.q[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        const uint32_t by = m.inside(row, rows) ? m.odd(row) * 16 : 0;
+        const uint4 w = raw.q[0];
+        raw.q[0] = make_uint4(__funnelshift_r(w.x, w.y, by), __funnelshift_r(w.y, w.z, by), __funnelshift_r(w.z, w.w, by), __funnelshift_r(w.w, c.last, by));
     }
     float f[8];
     raw_values(raw, type, f);
@@ -123,7 +116,8 @@ __device__ __forceinline__ void values(const Cells<T, WHOLE>& c, const Source& m
     for (int e = 0; e < 4; ++e) v[e] = pair(f[2 * e], f[2 * e + 1]);
 }
 
-// Eight columns to a row, whole where the row's place (aligned) and its end allow it.
+// Eight columns to a row, whole where the row's place (aligned) and its end allow it; 16-bit
+// ones of other rows in words.
 __device__ __forceinline__ void store(void* p, int64_t at, int n, int type, bool aligned, const uint64_t (&v)[4])
 {
     float f[8];
@@ -133,7 +127,25 @@ __device__ __forceinline__ void store(void* p, int64_t at, int n, int type, bool
         f[2 * e] = t.x, f[2 * e + 1] = t.y;
     }
     if (aligned && n >= 8) store8(p, at, type, f);
-    else
+    else if (type == GS_BF16 || type == GS_F16) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = pack_half2(f[2 * e], f[2 * e + 1], type);
+        uint16_t* to = (uint16_t*)p + at;
+        if (n < 8) {
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+                if (e < n) to[e] = (uint16_t)(w[e >> 1] >> (e & 1) * 16);
+        } else if (((uintptr_t)to & 3u) == 0) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) reinterpret_cast<uint32_t*>(to)[e] = w[e];
+        } else {
+            to[0] = (uint16_t)w[0];
+#pragma unroll
+            for (int e = 0; e < 3; ++e) reinterpret_cast<uint32_t*>(to + 1)[e] = __funnelshift_r(w[e], w[e + 1], 16);
+            to[7] = (uint16_t)(w[3] >> 16);
+        }
+    } else
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             if (e < n) store_elem(p, at + e, type, f[e]);
