@@ -5,15 +5,18 @@
 //
 // One pass over the rows: a group of threads holds a row in registers from h and x to s
 // and y (backward: from dy, ds, s and h to dx and dh), with two reductions in between.
-// HBM bounds both.  The group is the smallest power of two of threads that covers the row
-// at eight columns a thread, so that narrow rows share a warp and rows of up to 256 columns
-// need no barrier.  As separate norm, product, sum and norm a row would cross HBM nine times in
-// place of four.
+// HBM bounds both.  The group is the least number of threads that covers the row at eight
+// columns a thread: a power of two within a warp (narrow rows share one and rows of up to 256
+// columns need no barrier), whole warps beyond it.  As separate norm, product, sum and norm a row would
+// cross HBM nine times in place of four.
 //   1,000,000 x 256 bf16 334 us, 6.1 TB/s (302 at the copy's rate; without the next row's loads
 //   ahead 449, with weights fetched for each row 500), its gradients 520 us, 5.9 TB/s
-//   20,011 x 331 f16, a gate a value: 35 and 78 us, bound by instructions (single elements 138
-//   and 364; the next row's pieces ahead in shared memory 36 and 83; whole pieces written with
-//   the neighbour's columns 37 and 79)
+//   20,011 x 331 f16, a gate a value: 33 and 59 us, 250,000 x 197 172 and 300 (floors 72 and
+//   116), bound by the instructions that shift and write unaligned rows, half of the issue slots
+//   (single elements 20,011 x 331 138 and 364; the next row's pieces ahead in shared memory, or
+//   whole pieces written with the neighbour's columns, no faster)
+//   8,000 x 5928 bf16 132 and 203 us (floors 56 and 84): one row an SM at a time, whose two
+//   reductions nothing covers
 #include <type_traits>
 
 #include "gemm.cuh"
@@ -28,7 +31,7 @@ using namespace rows;
 // pitch: whole pieces, of which a row's last may lie in its padding.  Others of 16-bit
 // elements: the four or five 32-bit words that the eight columns lie in, shifted by an element
 // where the row starts within a word (two pieces of 16 bytes shifted together took 15
-// instructions more a matrix: 20,011 x 331 OLDF and OLDB us, 250,000 x 197 268 and 410); single
+// instructions more a matrix: 250,000 x 197 268 and 410 us against 230 and 367); single
 // elements in the first and the last row, whose words may reach beyond the matrix, and in fp32.
 struct Source {
     const void* p;
@@ -214,19 +217,20 @@ __device__ __forceinline__ float sum_of(uint64_t v)
 }
 
 // Threads of a block at most, and blocks an SM, which set the registers: one vector a thread
-// wants many warps of few.
+// wants many warps of few.  Of unaligned rows 64 without the next row's loads ahead: 250,000 x 197
+// 172 us; 80 with them 184, 97 with them 230; gradients with 80 300 us, with 117 309.
 template <int T, int NV, bool WHOLE>
-constexpr int kForwardThreads = NV == 1 && T != GS_F32 && WHOLE ? 1024 : 512;
+constexpr int kForwardThreads = NV == 1 && !(T == GS_F32 && WHOLE) ? 1024 : 512;
 template <int NV>
 constexpr int kBackwardThreads = NV == 1 ? 256 : 512;
 template <int T, int NV, bool WHOLE>
-constexpr int kBackwardBlocks = NV == 1 ? (T != GS_F32 && WHOLE ? 3 : 2) : 1;
+constexpr int kBackwardBlocks = NV == 1 ? (T != GS_F32 ? 3 : 2) : 1;
 
 template <int T, int NV, bool WHOLE>
 __global__ void __launch_bounds__(kForwardThreads<T, NV, WHOLE>) block_norm_kernel(const __grid_constant__ gs_block_norm_args a, int group)
 {
     constexpr int P = 4;
-    constexpr bool kAhead = NV == 1;   // the next row's loads before this one's work
+    constexpr bool kAhead = NV == 1 && WHOLE;   // the next row's loads before this one's work
     __shared__ float sm[32];
     wait_for_predecessor();
     const int lane = threadIdx.x % group, cols = (int)a.cols;
@@ -492,18 +496,24 @@ struct Shape {
     int nv, group, threads;
 };
 // One vector a thread up to `widest` threads, then two or four; in_warp: two for rows that a
-// warp holds so (forward of unaligned rows and of fp32: 20,011 x 331 50 -> 35 us, 20,000 x 512
-// fp32 39 -> 35; of aligned 16-bit rows 44 -> 49, gradients 78 -> 93).
+// warp holds so (forward of fp32 pieces: 20,000 x 512 39 -> 35 us).  Up to a warp a power of two of
+// threads, beyond it whole warps (of 2049 columns, 257 vectors, 288 threads in place
+// of 512: 16,000 rows 183 -> 111 us).
 Shape shape_for(int64_t cols, int widest, bool in_warp)
 {
     const int64_t n = (cols + 7) / 8;
     Shape s;
     s.nv = n <= widest && !(in_warp && n > 32 && n <= 64) ? 1 : (n <= 1024 ? 2 : 4);
+    const int lanes = (int)((n + s.nv - 1) / s.nv);
     s.group = 1;
-    while ((int64_t)s.group * s.nv < n) s.group *= 2;
-    s.threads = s.group < 256 ? 256 : s.group;
+    while (s.group < 32 && s.group < lanes) s.group *= 2;
+    if (lanes > 32) s.group = (lanes + 31) / 32 * 32;
+    s.threads = s.group < 256 ? 256 / s.group * s.group : s.group;
     return s;
 }
+// Blocks of the grid: those that the SMs hold at a time, whose threads take `threads` in all of
+// one SM (what is beyond would wait for a second turn: 20,011 x 331 gradients 73 -> 60 us).
+int64_t grid_for(int64_t sms, const Shape& s, int threads) { return sms * (s.threads < threads ? threads / s.threads : 1); }
 
 bool norm_sizes_ok(int64_t rows, int64_t cols, int type) { return size_ok(rows, 0) && size_ok(cols, 1) && cols <= GS_NORM_MAX_COLS && type_float(type); }
 
@@ -538,8 +548,10 @@ extern "C" gs_status gs_block_norm(const gs_block_norm_args* args, void* stream)
     if (sms <= 0) return GS_ERR_CUDA;
     const bool whole = a.cols % 8 == 0 && a.cols <= 8192 && rows16(a.h, a.ldh, a.type) && rows16(a.x, a.ldx, a.type) &&
                        (!a.gate_rows || rows16(a.gate, a.ldg, a.type));
-    const Shape s = shape_for(a.cols, a.type == GS_F32 || !whole ? 512 : 1024, a.type == GS_F32 || !whole);
-    const int64_t rpb = s.threads / s.group, want = (a.rows + rpb - 1) / rpb, most = (int64_t)sms * (1024 / s.threads);
+    // one vector a thread up to 1024 threads where pieces are whole (8,000 x 5928 147 -> 132 us), else
+    // up to 512 (unaligned 5925 columns 163 us, with 1024 175)
+    const Shape s = shape_for(a.cols, whole && a.type != GS_F32 ? 1024 : 512, a.type == GS_F32 && whole);
+    const int64_t rpb = s.threads / s.group, want = (a.rows + rpb - 1) / rpb, most = grid_for(sms, s, s.nv == 1 && !(a.type == GS_F32 && whole) ? 1024 : 512);
     const int grid = (int)(want < most ? want : most);
     cudaStream_t st = (cudaStream_t)stream;
     const auto run = [&](auto t) -> gs_status {
@@ -572,7 +584,8 @@ extern "C" gs_status gs_block_norm_bwd(const gs_block_norm_bwd_args* args, void*
         return GS_ERR_INVALID_ARG;
     if (a.weight && !type_float(a.dy_type)) return GS_ERR_INVALID_ARG;
     const int sms = device_sms();
-    const int64_t blocks = 3 * (sms > 0 ? sms : 152);   // the size is the same whatever the alignment of the arrays
+    const Shape s = shape_for(a.cols, 256, false);
+    const int64_t blocks = grid_for(sms > 0 ? sms : 152, s, s.nv == 1 && a.type != GS_F32 ? 768 : 512);   // whatever the arrays' alignment
     const bool gate_sum = a.dgate && !a.gate_rows;
     const size_t need = a.dweight || a.dpost || gate_sum ? (size_t)round_up(3 * blocks * a.cols * 4, 256) : 0;
     const WsCheck wc = ws_check(ws, ws_bytes, need);
@@ -599,7 +612,6 @@ extern "C" gs_status gs_block_norm_bwd(const gs_block_norm_bwd_args* args, void*
     const bool same = !a.dy || a.dy_type == a.type;
     const bool whole = same && a.cols % 8 == 0 && a.cols <= 8192 && wide(a.dy, a.lddy, a.dy) && wide(a.s, a.lds, a.dy) &&
                        wide(a.ds, a.ldds, a.ds) && wide(a.h, a.ldh, reads_h) && wide(a.gate, a.ldg, row_gate);
-    const Shape s = shape_for(a.cols, 256, false);
     const int groups = s.threads / s.group;
     const int64_t want = (a.rows + groups - 1) / groups;
     const int grid = (int)(want < blocks ? want : blocks);
