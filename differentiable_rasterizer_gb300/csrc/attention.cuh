@@ -30,6 +30,7 @@ struct Sequences {
 };
 struct Sequence {
     int q0, lq, k0, lk;   // first rows and lengths
+    uint32_t number;
 };
 
 // Starts and lengths as they are held within the arrays.
@@ -38,6 +39,7 @@ __host__ __device__ __forceinline__ int held(int64_t v, int64_t lo, int64_t hi) 
 __device__ __forceinline__ Sequence sequence_at(const Sequences& p, uint32_t s)
 {
     Sequence r;
+    r.number = s;
     if (!p.q_starts) {
         r.q0 = r.k0 = 0;
         r.lq = (int)p.q_rows;
@@ -61,7 +63,7 @@ __device__ __forceinline__ bool find_unit(const Sequences& p, uint32_t u, int to
     const uint32_t lane = threadIdx.x & 31;
     for (uint32_t base = 0; base < p.count; base += 32) {
         const uint32_t s = base + lane;
-        Sequence mine = {0, 0, 0, 0};
+        Sequence mine = {0, 0, 0, 0, 0};
         if (s < p.count) mine = sequence_at(p, s);
         const int length = KEYS ? mine.lk : mine.lq;
         const uint32_t n = ((uint32_t)length + (uint32_t)tokens - 1) / (uint32_t)tokens;
@@ -78,6 +80,7 @@ __device__ __forceinline__ bool find_unit(const Sequences& p, uint32_t u, int to
             seq.lq = __shfl_sync(0xffffffffu, mine.lq, l);
             seq.k0 = __shfl_sync(0xffffffffu, mine.k0, l);
             seq.lk = __shfl_sync(0xffffffffu, mine.lk, l);
+            seq.number = base + (uint32_t)l;
             units = __shfl_sync(0xffffffffu, n, l);
             unit = u - (__shfl_sync(0xffffffffu, end, l) - units);
             return true;
@@ -85,6 +88,18 @@ __device__ __forceinline__ bool find_unit(const Sequences& p, uint32_t u, int to
         u -= __shfl_sync(0xffffffffu, end, 31);
     }
     return false;
+}
+// The sequence that a row belongs to, from the starts: count if to none.
+__host__ __device__ __forceinline__ uint32_t sequence_of(const int32_t* starts, uint32_t count, int64_t row)
+{
+    if (!starts) return 0;
+    uint32_t lo = 0, hi = count;   // the first that ends behind the row
+    while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        if (starts[mid + 1] > row) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo < count && starts[lo] <= row ? lo : count;
 }
 // Keys that the tokens up to `last` of a sequence see.
 __host__ __device__ __forceinline__ int keys_seen(const Sequence& s, int last, bool causal)

@@ -29,7 +29,10 @@
 //
 // f16 holds neither small p nor small ds among its normal numbers: p is taken times 2^12
 // (at most 1 times that), ds times the power of two that brings its bound, 2 dim max|do|
-// max|v|, to 2^15; the sums are scaled back at the end.
+// max|v|, to 2^15; the sums are scaled back at the end.  v's maximum is that of the sequence and
+// key head, do's that of the row for dq, whose rows are TMEM lanes, and of the sequence's
+// rows and the key head for dk, which sums over them: rows of no sequence and other
+// sequences change nothing.
 #include <atomic>
 #include <cmath>
 
@@ -54,10 +57,9 @@ struct Params {
     CUtensorMap q, k, v, d_o;
     Sequences seqs;
     Fill fill_dq, fill_dk, fill_dv;
-    float* stats;            // [key head][token][head of the group], twice: kUp - lse log2(e) (-infinite for a row that sees no key), -delta
+    float* stats;            // planes of [key head][token][head of the group]: kUp - lse log2(e) (-infinite for a row that sees no key), -delta
     const float* lse;
-    const float* most;       // F16: the blocks' largest |do| and |v|
-    int most_count;
+    float* most;             // F16: a sequence's and key head's largest finite |do|; behind them |v|; a row's |do| in a third plane of stats
     uint16_t *dq, *dk, *dv;
     int64_t dq_row, dq_head, dk_row, dk_head, dv_row, dv_head;
     int64_t stat_pitch, stat_plane;   // of a key head; to the second plane
@@ -69,70 +71,119 @@ struct Params {
 };
 
 // ------------------------------------------------------------------ F16's largest values
+// Infinities and NaN are left out: what they reach is not finite whatever the power, and the
+// rest keeps its digits.
 struct MostParams {
     const uint16_t *d_o, *v;
     int64_t do_row, do_head, v_row, v_head;
-    float* most;   // a block's largest |do| and |v|
-    int64_t q_rows, k_rows;
-    int heads, kv_heads, dim, vec;
+    Sequences seqs;
+    float* row_most;         // of do's rows, laid out as stats
+    uint32_t* most;          // [2][sequences][key heads] bits of |do| and |v|, cleared by delta's launch
+    int64_t stat_pitch, q_each, k_each;   // rows of a block, multiples of kMostRows
+    uint32_t q_blocks, q_chunks, k_chunks;   // blocks of do; of a key head, do's and v's
+    uint32_t kv_heads;
+    int group, dim, do_vec, v_vec;
 };
+constexpr int kMostRows = 16;   // at a time, sixteen lanes each
 
-// Sixteen lanes a row and head, eight elements a lane.
+// A block some rows of a key head: of do (all heads of the group) or of v.  Sixteen lanes a
+// row, eight elements a lane.  Magnitudes are compared as bits, so that the order of the
+// atomics does not matter; one a block for each sequence that its last rows are of (with one
+// for each sixteen lanes all gradients of 5 x 1111 queries on 2049 keys, six heads of 72, took
+// 10 us more: they wait for one another at a long sequence's place).
 __global__ void __launch_bounds__(256) most_kernel(const __grid_constant__ MostParams p)
 {
-    __shared__ float most[2][8];
+    __shared__ uint32_t at_end[2][kMostRows];
     wait_for_predecessor();
-    const int col = threadIdx.x % 16 * 8;
-    const int64_t step = (int64_t)gridDim.x * 16, first = (int64_t)blockIdx.x * 16 + threadIdx.x / 16;
-    float m[2] = {0.0f, 0.0f};
-    const auto over = [&](float& m, const uint16_t* t, int64_t row, int64_t head, int64_t lines, int heads) {
-#pragma unroll 4
-        for (int64_t i = first; i < lines; i += step) {
-            const int64_t r = i / heads;
-            const uint16_t* at = t + r * row + (i - r * heads) * head;
-            float v[8];
-            if (col >= p.dim) continue;
-            if (p.vec) load8(at, col, GS_F16, v);
-            else
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = col + e < p.dim ? load_elem(at, col + e, GS_F16) : 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
+    const bool is_do = blockIdx.x < p.q_blocks;
+    const uint32_t i = is_do ? blockIdx.x : blockIdx.x - p.q_blocks, chunks = is_do ? p.q_chunks : p.k_chunks;
+    const uint32_t head = i / chunks;
+    const int64_t rows = is_do ? p.seqs.q_rows : p.seqs.k_rows, each = is_do ? p.q_each : p.k_each, start = (int64_t)(i % chunks) * each;
+    const int64_t end = start + each < rows ? start + each : rows;
+    const int32_t* starts = is_do ? p.seqs.q_starts : p.seqs.k_starts;
+    const int heads = is_do ? p.group : 1, vec = is_do ? p.do_vec : p.v_vec;
+    const int64_t pitch = is_do ? p.do_row : p.v_row, head_pitch = is_do ? p.do_head : p.v_head;
+    const uint16_t* from = (is_do ? p.d_o : p.v) + (int64_t)head * heads * head_pitch;
+    uint32_t* most = p.most + (is_do ? 0 : (int64_t)p.seqs.count * p.kv_heads) + head;
+    const int sub = threadIdx.x % 16, col = sub * 8;
+    uint32_t s = p.seqs.count, top = 0;   // the sequence so far and its largest
+    int64_t first = 0, last = 0;          // its rows
+    const auto flush = [&] {
+        if (sub == 0 && s < p.seqs.count && top > 0) {
+            uint32_t* to = most + (int64_t)s * p.kv_heads;
+            if (*(volatile uint32_t*)to < top) atomicMax(to, top);
         }
     };
-    over(m[0], p.d_o, p.do_row, p.do_head, p.q_rows * p.heads, p.heads);
-    over(m[1], p.v, p.v_row, p.v_head, p.k_rows * p.kv_heads, p.kv_heads);
+    // whole warps run the same number of rounds: each is two rows
+    for (int64_t row0 = start; row0 < end; row0 += kMostRows) {
+        const int64_t row = row0 + threadIdx.x / 16;
+        uint32_t mine = 0;
+#pragma unroll 4
+        for (int h = 0; h < heads; ++h) {
+            uint32_t m = 0;
+            if (row < end && col < p.dim) {
+                const uint16_t* at = from + row * pitch + h * head_pitch + col;
+                uint32_t w[4];
+                if (vec) {
+                    const uint4 q = *reinterpret_cast<const uint4*>(at);
+                    w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+                } else
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = (col + 2 * e < p.dim ? at[2 * e] : 0u) | (col + 2 * e + 1 < p.dim ? (uint32_t)at[2 * e + 1] : 0u) << 16;
 #pragma unroll
-        for (int s = 16; s > 0; s >>= 1) m[k] = fmaxf(m[k], __shfl_xor_sync(0xffffffffu, m[k], s));
-        if ((threadIdx.x & 31) == 0) most[k][threadIdx.x >> 5] = m[k];
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t lo = w[e] & 0x7fffu, hi = w[e] >> 16 & 0x7fffu;
+                    if (lo < 0x7c00u && lo > m) m = lo;
+                    if (hi < 0x7c00u && hi > m) m = hi;
+                }
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) {
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, m, o);
+                m = other > m ? other : m;
+            }
+            mine = m > mine ? m : mine;
+            if (is_do && sub == 0 && row < end)
+                p.row_most[head * p.stat_pitch + row * heads + h] = __half2float(__ushort_as_half((unsigned short)m));
+        }
+        if (row >= end) continue;
+        if (row < first || row >= last) {
+            flush();
+            s = sequence_of(starts, p.seqs.count, row), top = 0;
+            first = !starts ? 0 : (s < p.seqs.count ? starts[s] : row), last = !starts ? rows : (s < p.seqs.count ? starts[s + 1] : row + 1);
+        }
+        const uint32_t value = __float_as_uint(__half2float(__ushort_as_half((unsigned short)mine)));
+        top = value > top ? value : top;
     }
+    if (sub == 0) at_end[0][threadIdx.x / 16] = s, at_end[1][threadIdx.x / 16] = top;
     __syncthreads();
-    if (threadIdx.x < 2) {
-        float all = 0.0f;
-        for (int w = 0; w < 8; ++w) all = fmaxf(all, most[threadIdx.x][w]);
-        p.most[2 * blockIdx.x + threadIdx.x] = all;
-    }
+    bool mine = true;
+#pragma unroll
+    for (int i = 0; i < kMostRows; ++i)
+        if (at_end[0][i] == s) {
+            mine = mine && i >= (int)threadIdx.x / 16;   // the first with this sequence takes all
+            top = at_end[1][i] > top ? at_end[1][i] : top;
+        }
+    if (mine) flush();
 }
 
-// The power of two that ds is held times, from the largest |do| and |v|; by a whole warp.
+// The power of two that ds is held times, from the largest |do| and |v|.
 template <int T>
-__device__ __forceinline__ int ds_exponent(const Params& p)
+__device__ __forceinline__ int ds_exponent(int dim, float a, float b)
 {
     if constexpr (T != GS_F16) return 0;
-    float a = 0.0f, b = 0.0f;
-    for (int i = threadIdx.x & 31; i < p.most_count; i += 32) a = fmaxf(a, p.most[2 * i]), b = fmaxf(b, p.most[2 * i + 1]);
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) {
-        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, s));
-        b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, s));
-    }
-    // finite 16-bit numbers: 2^-24 to 2^16; an infinity or zeros: any power does
-    const float bound = 2.0f * (float)p.dim * a * b;
-    if (!(bound > 0.0f && bound < 3.0e38f)) return 0;
+    // finite 16-bit numbers, 2^-24 to 2^16; zeros: any power does
+    const float bound = 2.0f * (float)dim * a * b;
+    if (!(bound > 0.0f)) return 0;
     return 15 - (((__float_as_int(bound) >> 23) & 255) - 126);   // bound <= 2^(exponent - 126)
 }
+// Of v's and, for dk, of do's magnitudes in a sequence.
+__device__ __forceinline__ float most_v(const Params& p, const Sequence& s, uint32_t head)
+{
+    return p.most[((int64_t)p.seqs.count + s.number) * p.kv_heads + head];
+}
+__device__ __forceinline__ float most_do(const Params& p, const Sequence& s, uint32_t head) { return p.most[(int64_t)s.number * p.kv_heads + head]; }
 __device__ __forceinline__ float power2(int e) { return __int_as_float((e + 127) << 23); }   // -126..127
 
 // Queries that see a key come from this token of the sequence on.
@@ -482,7 +533,7 @@ __global__ void __launch_bounds__(kKeyThreads, 1) keys_kernel(const __grid_const
     let_successor_start();
     if (warp < kKeyWarps) {
         many_registers<104>();
-        const int exponent = ds_exponent<T>(p);
+        const int exponent = T == GS_F16 && w.n > 0 ? ds_exponent<T>(p.dim, most_do(p, w.seq, w.head), most_v(p, w.seq, w.head)) : 0;
         key_terms<T, DP>(p, w, warp >> 2, threadIdx.x & 127, smem, bars, tmem + ((uint32_t)((warp & 3) * 32) << 16), exponent, gave_up);
     } else {
         few_registers();
@@ -690,8 +741,7 @@ __device__ __forceinline__ void issue_queries(const Params& p, const QueryWork& 
 
 // A row a thread: i the tile, r the row.
 template <int T, int DP, int TILES>
-__device__ __forceinline__ void query_terms(const Params& p, const QueryWork& w, int i, int r, uint32_t bars, uint32_t tmem, int exponent,
-                                            volatile int* gave_up)
+__device__ __forceinline__ void query_terms(const Params& p, const QueryWork& w, int i, int r, uint32_t bars, uint32_t tmem, volatile int* gave_up)
 {
     using S = QueryShape<DP, TILES>;
     const int n = i ? w.n[1] : w.n[0], t0 = w.t0 + i * p.tokens;
@@ -702,6 +752,7 @@ __device__ __forceinline__ void query_terms(const Params& p, const QueryWork& w,
     const uint64_t less = both(live ? st[0] - kUp<T> : -INFINITY), minus = both(live ? st[p.stat_plane] : 0.0f);   // p is no factor here
     const int seen = live ? keys_seen(w.seq, token, p.causal) : 0;
     const int all = keys_seen(w.seq, t0, p.causal);
+    const int exponent = T == GS_F16 && live && n > 0 ? ds_exponent<T>(p.dim, st[2 * p.stat_plane], most_v(p, w.seq, w.head)) : 0;
     const uint64_t by_ds = both(power2(exponent)), scale2 = both(p.scale2);
     const uint32_t here = tmem + i * 128;
     bool ok = true;
@@ -907,6 +958,9 @@ __global__ void __launch_bounds__(QueryShape<DP, TILES>::kThreads, 3 - TILES) qu
         mbar_init_fence();
     }
     wait_for_predecessor_alone();
+    if (DELTA && T == GS_F16)
+        for (int64_t i = (int64_t)blockIdx.x * S::kThreads + threadIdx.x; i < 2 * (int64_t)p.seqs.count * p.kv_heads; i += (int64_t)gridDim.x * S::kThreads)
+            p.most[i] = 0.0f;
     if (!DELTA && p.zero) fill_rows(p.fill_dq, p.seqs.q_starts, p.seqs.count, p.seqs.q_rows);
     QueryWork w;
     if (!find_queries<TILES>(p, w)) return;   // the same for every warp
@@ -938,7 +992,7 @@ __global__ void __launch_bounds__(QueryShape<DP, TILES>::kThreads, 3 - TILES) qu
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         if (w.t0 + i * p.tokens < w.seq.lq) {
             if constexpr (DELTA) delta_terms<T, DP, TILES>(p, w, i, threadIdx.x & 127, bars, lanes, gave_up);
-            else query_terms<T, DP, TILES>(p, w, i, threadIdx.x & 127, bars, lanes, ds_exponent<T>(p), gave_up);
+            else query_terms<T, DP, TILES>(p, w, i, threadIdx.x & 127, bars, lanes, gave_up);
         }
     }
     __syncthreads();
@@ -950,7 +1004,7 @@ __global__ void __launch_bounds__(QueryShape<DP, TILES>::kThreads, 3 - TILES) qu
 }
 
 struct Plan {
-    int group, tokens, tiles, dp, blocks;
+    int group, tokens, tiles, dp;
     uint32_t parts;
     int64_t query_items, key_items, stat_pitch, stat_plane;
     size_t stats, most, part, packs, bytes;
@@ -989,10 +1043,9 @@ Plan plan_for(const gs_attention_bwd_args& a)
     r.stat_pitch = round_up(a.q_rows * r.group, 4);
     // the last copy of a plane's statistics reads up to a tile past the last row
     r.stat_plane = round_up(a.kv_heads * r.stat_pitch + kStatRows, 64);
-    r.stats = (size_t)r.stat_plane * 8;
-    const int64_t want = (a.q_rows * a.heads + a.k_rows * a.kv_heads + 63) / 64, most = sms * 2;
-    r.blocks = (int)(want < 1 ? 1 : (want < most ? want : most));
-    r.most = a.type == GS_F16 ? (size_t)round_up(r.blocks * 8, 256) : 0;
+    const bool f16 = a.type == GS_F16;
+    r.stats = (size_t)r.stat_plane * (f16 ? 12 : 8);
+    r.most = f16 ? (size_t)round_up(a.sequences * a.kv_heads * 8, 256) : 0;
     if (!tensor_tma(a.q, a.q_row, a.q_head, a.q_rows, a.heads)) r.packs += packed_bytes(a.q_rows, a.heads, a.dim);
     if (!tensor_tma(a.d_o, a.do_row, a.do_head, a.q_rows, a.heads)) r.packs += packed_bytes(a.q_rows, a.heads, a.dim);
     if (!tensor_tma(a.k, a.k_row, a.k_head, a.k_rows, a.kv_heads)) r.packs += packed_bytes(a.k_rows, a.kv_heads, a.dim);
@@ -1016,11 +1069,32 @@ gs_status launch_queries(const Params& p, const Plan& plan, cudaStream_t st)
             return launch_one(queries_kernel<T, DP, 2, DELTA>, QueryShape<DP, 2>::kSmem, QueryShape<DP, 2>::kThreads, two_done, plan.query_items, p, st);
     return launch_one(queries_kernel<T, DP, 1, DELTA>, QueryShape<DP, 1>::kSmem, QueryShape<DP, 1>::kThreads, one_done, plan.query_items, p, st);
 }
+// F16's largest magnitudes, after delta's launch.
+gs_status largest_values(const gs_attention_bwd_args& a, const Params& p, cudaStream_t st)
+{
+    const int known = device_sms();
+    const int64_t sms = known > 0 ? known : 152;
+    MostParams t = {};
+    t.d_o = (const uint16_t*)a.d_o, t.do_row = a.do_row, t.do_head = a.do_head;
+    t.v = (const uint16_t*)a.v, t.v_row = a.v_row, t.v_head = a.v_head;
+    t.seqs = p.seqs, t.row_most = p.stats + 2 * p.stat_plane, t.most = (uint32_t*)p.most, t.stat_pitch = p.stat_pitch;
+    t.kv_heads = p.kv_heads, t.group = p.group, t.dim = p.dim;
+    t.do_vec = a.dim % 8 == 0 && tensor_tma(a.d_o, a.do_row, a.do_head, a.q_rows, a.heads);
+    t.v_vec = a.dim % 8 == 0 && tensor_tma(a.v, a.v_row, a.v_head, a.k_rows, a.kv_heads);
+    // some four blocks an SM for either
+    t.q_each = round_up((a.q_rows * a.kv_heads + 4 * sms - 1) / (4 * sms), kMostRows);
+    t.k_each = round_up((a.k_rows * a.kv_heads + 4 * sms - 1) / (4 * sms), kMostRows);
+    t.q_chunks = (uint32_t)((a.q_rows + t.q_each - 1) / t.q_each), t.k_chunks = (uint32_t)((a.k_rows + t.k_each - 1) / t.k_each);
+    t.q_blocks = t.q_chunks * t.kv_heads;
+    return launch_after(most_kernel, dim3(t.q_blocks + t.k_chunks * t.kv_heads), 256, 0, 1, st, t);
+}
+
 template <int T, int DP>
-gs_status launch(const Params& p, const Plan& plan, bool pairs, cudaStream_t st)
+gs_status launch(const gs_attention_bwd_args& a, const Params& p, const Plan& plan, bool pairs, cudaStream_t st)
 {
     static std::atomic<uint64_t> done{0};
     gs_status s = pairs ? launch_queries<T, DP, true>(p, plan, st) : GS_OK;
+    if (T == GS_F16 && s == GS_OK && pairs) s = largest_values(a, p, st);
     if (s == GS_OK && p.dk) s = launch_one(keys_kernel<T, DP>, KeyShape<DP>::kSmem, kKeyThreads, done, plan.key_items * plan.parts, p, st);
     if (s == GS_OK && p.dk && plan.parts > 1) s = launch_after(keys_join_kernel<T, DP>, dim3((unsigned)plan.key_items), 256, 0, 1, st, p);
     return s == GS_OK && p.dq ? launch_queries<T, DP, false>(p, plan, st) : s;
@@ -1089,23 +1163,13 @@ extern "C" gs_status gs_attention_bwd(const gs_attention_bwd_args* args, void* w
         if (s == GS_OK) s = tile_map(&p.v, v, a.type, a.k_rows, a.kv_heads, a.dim, 1, kRows);
         if (s == GS_OK) s = packs.run(st);
         if (s != GS_OK) return s;
-        if (most) {
-            MostParams t = {};
-            t.d_o = (const uint16_t*)a.d_o, t.do_row = a.do_row, t.do_head = a.do_head;
-            t.v = (const uint16_t*)a.v, t.v_row = a.v_row, t.v_head = a.v_head;
-            t.most = most, t.q_rows = a.q_rows, t.k_rows = a.k_rows, t.heads = a.heads, t.kv_heads = a.kv_heads, t.dim = a.dim;
-            t.vec = a.dim % 8 == 0 && tensor_tma(a.d_o, a.do_row, a.do_head, a.q_rows, a.heads) &&
-                    tensor_tma(a.v, a.v_row, a.v_head, a.k_rows, a.kv_heads);
-            s = launch_after(most_kernel, dim3((unsigned)plan.blocks), 256, 0, 1, st, t);
-            if (s != GS_OK) return s;
-        }
     }
     p.seqs = {a.q_starts, a.k_starts, nullptr, a.q_rows, a.k_rows, (uint32_t)a.sequences};
     p.zero = a.fill && a.q_starts;
     p.fill_dq = {(uint16_t*)a.dq, a.dq_row, a.dq_head, nullptr, a.heads, a.dim};
     p.fill_dk = {(uint16_t*)a.dk, a.dk_row, a.dk_head, nullptr, a.kv_heads, a.dim};
     p.fill_dv = {(uint16_t*)a.dv, a.dv_row, a.dv_head, nullptr, a.kv_heads, a.dim};
-    p.stats = stats, p.lse = a.lse, p.most = most, p.most_count = plan.blocks, p.stat_pitch = plan.stat_pitch, p.stat_plane = plan.stat_plane;
+    p.stats = stats, p.lse = a.lse, p.most = most, p.stat_pitch = plan.stat_pitch, p.stat_plane = plan.stat_plane;
     p.dq = dq ? (uint16_t*)a.dq : nullptr, p.dq_row = a.dq_row, p.dq_head = a.dq_head;
     p.dk = dk ? (uint16_t*)a.dk : nullptr, p.dk_row = a.dk_row, p.dk_head = a.dk_head;
     p.dv = (uint16_t*)a.dv, p.dv_row = a.dv_row, p.dv_head = a.dv_head;
@@ -1119,6 +1183,6 @@ extern "C" gs_status gs_attention_bwd(const gs_attention_bwd_args* args, void* w
     p.idesc_s = instr_desc(a.type, true, true, kRows, kRows);
     p.idesc_d = instr_desc(a.type, true, false, (int)round_up(a.dim, 16), kRows);
     const bool pairs = a.q_rows > 0 && a.k_rows > 0;
-    if (a.type == GS_BF16) return plan.dp == 64 ? launch<GS_BF16, 64>(p, plan, pairs, st) : launch<GS_BF16, 128>(p, plan, pairs, st);
-    return plan.dp == 64 ? launch<GS_F16, 64>(p, plan, pairs, st) : launch<GS_F16, 128>(p, plan, pairs, st);
+    if (a.type == GS_BF16) return plan.dp == 64 ? launch<GS_BF16, 64>(a, p, plan, pairs, st) : launch<GS_BF16, 128>(a, p, plan, pairs, st);
+    return plan.dp == 64 ? launch<GS_F16, 64>(a, p, plan, pairs, st) : launch<GS_F16, 128>(a, p, plan, pairs, st);
 }
