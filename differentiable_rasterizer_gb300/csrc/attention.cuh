@@ -104,8 +104,24 @@ __host__ __device__ __forceinline__ uint32_t sequence_of(const int32_t* starts, 
 // Keys that the tokens up to `last` of a sequence see.
 __host__ __device__ __forceinline__ int keys_seen(const Sequence& s, int last, bool causal)
 {
-    const int e = causal ? last + 1 + s.lk - s.lq : s.lk;
+    const int e = causal ? last + 1 - s.lq + s.lk : s.lk;   // in this order within 32 bits
     return e < 0 ? 0 : (e < s.lk ? e : s.lk);
+}
+// Queries that see a key come from this token of the sequence on.
+__host__ __device__ __forceinline__ int first_query(const Sequence& s, int key, bool causal)
+{
+    const int t = causal ? key - (s.lk - s.lq) : 0;
+    return t < 0 ? 0 : t;
+}
+// Packed rows of the tile of `tokens` tokens from t0 on that a key counts for.  Cut in tokens:
+// a sequence's packed rows may be more than 2^31.
+struct Columns {
+    int from, to;
+};
+__host__ __device__ __forceinline__ Columns columns_of(const Sequence& s, int key, int t0, int tokens, int group, bool causal)
+{
+    const int left = s.lq - t0, hidden = first_query(s, key, causal) - t0;
+    return {(hidden < 0 ? 0 : (hidden < tokens ? hidden : tokens)) * group, (left < tokens ? left : tokens) * group};
 }
 
 // The units' number at most, known without the starts.

@@ -186,13 +186,6 @@ __device__ __forceinline__ float most_v(const Params& p, const Sequence& s, uint
 __device__ __forceinline__ float most_do(const Params& p, const Sequence& s, uint32_t head) { return p.most[(int64_t)s.number * p.kv_heads + head]; }
 __device__ __forceinline__ float power2(int e) { return __int_as_float((e + 127) << 23); }   // -126..127
 
-// Queries that see a key come from this token of the sequence on.
-__device__ __forceinline__ int first_query(const Sequence& s, int key, bool causal)
-{
-    const int t = causal ? key - (s.lk - s.lq) : 0;
-    return t < 0 ? 0 : t;
-}
-
 // ------------------------------------------------------------------ dk, dv
 // A CTA a tile of 128 keys of a key head.  TMEM lanes are keys:
 //   S = K Q^T, R = V dO^T (columns are packed query rows), dV += P dO, dK += dS Q
@@ -392,8 +385,8 @@ __device__ __forceinline__ void key_terms(const Params& p, const KeyWork& w, int
     for (int i = 0; i < w.n; ++i, rs.next()) {
         const int t0 = w.first + i * p.tokens;
         // columns of this tile that count for this key: from the first query that sees it to the last of the sequence
-        const int rows = (w.seq.lq - t0) * p.group, full = p.tokens * p.group, to = (rows < full ? rows : full) - quarter * 32;
-        const int from = (first_query(w.seq, key, p.causal) - t0) * p.group - quarter * 32;
+        const Columns all = columns_of(w.seq, key, t0, p.tokens, p.group, p.causal);
+        const int from = all.from - quarter * 32, to = all.to - quarter * 32;
         const bool cut = to < 32 || __any_sync(0xffffffffu, from > 0);
         const uint32_t odd = (uint32_t)((int64_t)(w.seq.q0 + t0) * p.group) & 3;
         const uint32_t stats = smem + S::kAtStats + 2 * rs.s * S::kStatBytes + (odd + (uint32_t)quarter * 32) * 4;

@@ -51,3 +51,49 @@ def run_on_host(program, tmp_path):
 
 def test_sequence_of_a_row(tmp_path):
     run_on_host(SEQUENCE_OF, tmp_path)
+
+
+COLUMNS = r"""
+#include <cstdio>
+#include <cstdlib>
+#include "attention.cuh"
+
+using namespace gs::attn;
+
+int main()
+{
+    int wrong = 0;
+    const int lengths[] = {1, 5, 127, 128, 1000, 1 << 24, (1 << 24) + 1000, 20000001, 0x7fffffff - 1024};
+    const int groups[] = {1, 2, 3, 7, 16, 71, 128};
+    std::srand(1);
+    for (int lq : lengths)
+        for (int lk : lengths)
+            for (int group : groups)
+                for (int trial = 0; trial < 300; ++trial) {
+                    const int tokens = 128 / group, key = trial % 3 ? std::rand() % lk : (lk - 1 < trial ? lk - 1 : trial);
+                    const Sequence s = {0, lq, 0, lk, 0};
+                    const bool causal = trial % 2;
+                    // a tile anywhere: the first, the last, around the first query that sees the key
+                    const int64_t tiles = ((int64_t)lq + tokens - 1) / tokens;
+                    int64_t tile = trial % 5 == 0 ? 0 : (trial % 5 == 1 ? tiles - 1 : std::rand() % tiles);
+                    if (trial % 5 == 2 && first_query(s, key, causal) < lq) tile = first_query(s, key, causal) / tokens;
+                    const int t0 = (int)(tile * tokens);
+                    const Columns c = columns_of(s, key, t0, tokens, group, causal);
+                    for (int e = 0; e < tokens * group; ++e) {
+                        const int64_t token = (int64_t)t0 + e / group;
+                        const bool counts = token < lq && (!causal || key <= token + lk - (int64_t)lq);
+                        wrong += counts != (e >= c.from && e < c.to);
+                    }
+                    wrong += c.to > 128;
+                    const int64_t seen = causal ? (int64_t)t0 + 1 + lk - lq : lk;
+                    wrong += keys_seen(s, t0, causal) != (seen < 0 ? 0 : (seen < lk ? seen : lk));
+                }
+    std::printf("%d\n", wrong);
+    return wrong != 0;
+}
+"""
+
+
+def test_rows_of_a_tile_that_count_for_a_key(tmp_path):
+    """Against the definition, up to the longest sequences and past 2^31 packed rows."""
+    run_on_host(COLUMNS, tmp_path)
