@@ -23,6 +23,9 @@
 // it by more than 2^15: o and the sum are then rescaled (rare after the first tiles), and
 // terms stay within 2^15 in between, which f16 holds and the fp32 sums do not mind.  p is
 // rounded to 16 bits because the tensor cores take 16-bit factors; the sum takes it unrounded.
+// f16's smallest step, 2^-24, would round away what the keys of a long context weigh together
+// (2^-25 of the row's largest for each): terms are held times a power of two that grows with the
+// keys, and the maximum is raised so much earlier (see held_up).
 //
 // Few rows against many keys (single tokens) leave most SMs idle: the keys of a tile are
 // then split over several CTAs, whose sums and maxima join_kernel puts together in a
@@ -36,7 +39,7 @@ namespace gs {
 namespace attn {
 namespace {
 
-constexpr float kRaise = 15.0f;   // log2
+constexpr float kMost = 15.0f;   // log2 of the largest term
 
 // TILES: of a CTA.  With one, two CTAs share an SM.
 template <int DP, int TILES>
@@ -61,7 +64,7 @@ struct Params {
     int64_t o_row, o_head;
     float* lse;
     float* part;          // splits > 1: [split][q row][head][DP] sums of p v
-    float2* part_stats;   // [split][q row][head] their maxima and sums of p
+    float2* part_stats;   // [split][q row][head] what their terms are taken to, and the sums of p
     float scale2;         // scale log2(e)
     uint32_t splits, kv_heads;
     int group, tokens;    // query heads of a key head, tokens of a tile
@@ -221,6 +224,7 @@ __device__ __forceinline__ void softmax(const Params& p, const Work& w, int i, i
     const int seen = keys_seen(w.seq, token, p.causal);                 // this row's keys
     const int all = keys_seen(w.seq, t0, p.causal);                     // every row's
     const uint32_t scores = tmem + i * 128, sums = tmem + S::kTmemO + i * DP;
+    const float up = T == GS_F16 ? (float)held_up(w.seq.lk) : 0.0f;
     float m = -INFINITY;
     uint64_t l2[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
     bool ok = true;
@@ -249,7 +253,7 @@ __device__ __forceinline__ void softmax(const Params& p, const Work& w, int i, i
             if (c < 96) tmem_ld32_wait(s + c + 32);
         }
         const float new_m = max3(fmaxf(top[0], top[1]), top[2], top[3]) * p.scale2;
-        const bool raise = new_m > m + kRaise;   // from -infinity: by any score
+        const bool raise = new_m > m + (kMost - up);   // from -infinity: by any score
         if (j == 0) m = new_m;
         else if (__any_sync(0xffffffffu, raise)) {
             // the sums so far, to the new maximum: the product that last added to them is done
@@ -270,7 +274,7 @@ __device__ __forceinline__ void softmax(const Params& p, const Work& w, int i, i
                 tmem_st32(sums + c, o);
             }
         }
-        const float less = m == -INFINITY ? 0.0f : -m;   // no key yet: every term 0
+        const float less = m == -INFINITY ? 0.0f : up - m;   // no key yet: every term 0
         const uint64_t scale = pair(p.scale2, p.scale2), minus = pair(less, less);
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
@@ -299,7 +303,7 @@ __device__ __forceinline__ void softmax(const Params& p, const Work& w, int i, i
     const int64_t row = w.seq.q0 + token;
     if (p.splits > 1) {
         const int64_t at = ((int64_t)w.split * p.seqs.q_rows + row) * (p.group * p.kv_heads) + head;
-        if (live) p.part_stats[at] = make_float2(m, l);
+        if (live) p.part_stats[at] = make_float2(m - up, l);
         if (n == 0) return;
         float* to = p.part + at * DP;
 #pragma unroll 1
@@ -314,7 +318,7 @@ __device__ __forceinline__ void softmax(const Params& p, const Work& w, int i, i
         }
     } else {
         const bool none = l == 0.0f;
-        if (live && p.lse) p.lse[row * (p.group * p.kv_heads) + head] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+        if (live && p.lse) p.lse[row * (p.group * p.kv_heads) + head] = none ? -INFINITY : (m - up + log2f(l)) * kLn2;
         const float by = none ? 0.0f : 1.0f / l;
         uint16_t* to = p.o + row * p.o_row + head * p.o_head;
 #pragma unroll 1

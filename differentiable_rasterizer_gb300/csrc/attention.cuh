@@ -107,6 +107,17 @@ __host__ __device__ __forceinline__ int keys_seen(const Sequence& s, int last, b
     const int e = causal ? last + 1 - s.lq + s.lk : s.lk;   // in this order within 32 bits
     return e < 0 ? 0 : (e < s.lk ? e : s.lk);
 }
+// log2 of what the forward's f16 terms are held times: a term below f16's normal numbers is off
+// by 2^-25, so that all keys of a row are off by 2^-13 of its largest together, a quarter of
+// f16's half unit.  12 at most, which leaves the maximum 2^3 to grow.  4099 tokens, 16 heads of
+// 128, causal, a few of whose keys draw far more weight than the first tile's: 65 us with 0 and 1, 67 with 4, 72 with
+// 10: every raise rescales o.
+__host__ __device__ __forceinline__ int held_up(int keys)
+{
+    int up = 0;
+    while (up < 12 && keys > 4096 << up) ++up;
+    return up;
+}
 // Queries that see a key come from this token of the sequence on.
 __host__ __device__ __forceinline__ int first_query(const Sequence& s, int key, bool causal)
 {

@@ -695,7 +695,9 @@ GS_API gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* ws_by
  * among a sequence's own values (v) reaches queries that it is hidden from, if they are
  * less than 256 tokens before the first that sees it.  Rows: below 2^31 - 1024.
  * Scores, maxima, sums and outputs are fp32 until o's rounding; exp(t - m), m a
- * running maximum, is rounded to `type` as a factor of its product with v.
+ * running maximum, is rounded to `type` as a factor of its product with v (F16: held times
+ * a power of two, so that what its smallest step loses of all keys together is below 2^-13
+ * of the row's largest).
  * Errors: INVALID_ARG for bad pointers, sizes, types or a too small workspace;
  * CUDA on launch failure. */
 #define GS_ATTENTION_MAX_DIM 128

@@ -88,6 +88,11 @@ int main()
                     const int64_t seen = causal ? (int64_t)t0 + 1 + lk - lq : lk;
                     wrong += keys_seen(s, t0, causal) != (seen < 0 ? 0 : (seen < lk ? seen : lk));
                 }
+    // what f16's terms lose, keys 2^-25 each, below 2^-13 up to 2^24 keys; no more than asks for
+    for (int keys : {0, 1, 4096, 4097, 8192, 8193, 1000000, 1 << 24, (1 << 24) + 1, 0x7fffffff - 1024}) {
+        const int up = held_up(keys);
+        wrong += up < 0 || up > 12 || (keys <= 1 << 24 && keys > 4096ll << up) || (up > 0 && keys <= 4096ll << (up - 1));
+    }
     std::printf("%d\n", wrong);
     return wrong != 0;
 }
