@@ -18,6 +18,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
+#include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -633,7 +634,9 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n)
             g.fill = 1;
         }
         if (backward) {
-            lse = at::empty({hq.rows, hq.heads}, q.options().dtype(ScalarType::Float));
+            // rows of no sequence: the call fills o's and lse's alike, but a given o is left as it is
+            const auto options = q.options().dtype(ScalarType::Float);
+            lse = g.fill || !g.q_starts ? at::empty({hq.rows, hq.heads}, options) : at::zeros({hq.rows, hq.heads}, options);
             g.lse = lse.data_ptr<float>();
         }
         with_scratch("gs_attention", lib.attention, g, q, dev, true);

@@ -224,7 +224,8 @@ def attention(q, k, v, *, q_starts=None, k_starts=None, k_lengths=None, causal=F
     default q_starts; without either, one sequence of all rows).  k_lengths: int32, how many
     of a sequence's keys are in use (a cache's slots), without gradients.  causal: the last
     query sees every key, the one before all but one, ...  A query that sees none gives 0.
-    out: like q, rows of no sequence are left as they are; else o is allocated, those rows 0."""
+    out: like q, rows of no sequence are left as they are; else o is allocated, those rows 0
+    (lse's are 0 in either case)."""
     return AttentionOut(*_native.attention(q, k, v, q_starts, k_starts, k_lengths, causal, scale, out, need_backward))
 
 
