@@ -695,13 +695,14 @@ PyObject* attention_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
 }
 
 // ------------------------------------------------------------------ block norm
-// A gate: [cols], or rows of the rest's type.
+// A gate: [cols], or rows of the rest's type.  For a single row without a dimension of rows both
+// are the same; one of its type is taken as rows.
 template <class Args>
 Tensor gate_of(Args& g, PyObject* o, int dev, const Rows& r)
 {
     if (o == Py_None) return {};
     const Tensor& t = tensor(o, "gate");
-    if (t.dim() == 1 && !(r.rows == 1 && r.one_dim)) {
+    if (t.dim() == 1 && !(r.one_dim && type_code(t.scalar_type()) == r.type)) {
         g.gate = vector_of(o, "gate", kFloat, dev, r.cols, &g.gate_type);
     } else {
         const Rows rg = rows_of(t, "gate", 1u << r.type, dev, r.cols, r.rows);
