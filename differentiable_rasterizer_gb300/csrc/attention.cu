@@ -41,12 +41,13 @@ namespace {
 
 constexpr float kMost = 15.0f;   // log2 of the largest term
 
-// TILES: of a CTA.  With one, two CTAs share an SM.
+// TILES: of a CTA.  With one, two CTAs share an SM; two only with 128 columns (see plan_for).
 template <int DP, int TILES>
 struct Shape {
+    static_assert(TILES == 1 || (TILES == 2 && DP == 128), "the shapes that plan_for chooses from");
     static constexpr int kChunks = DP / 64;
     static constexpr uint32_t kTile = kChunks * kBox;
-    static constexpr int kStages = TILES == 1 ? (DP == 128 ? 2 : 5) : (DP == 128 ? 5 : 8);
+    static constexpr int kStages = TILES == 1 && DP == 128 ? 2 : 5;
     static constexpr int kSoftmaxWarps = 4 * TILES, kThreads = (kSoftmaxWarps + 4) * 32;
     static constexpr uint32_t kTmemCols = 256 * TILES, kTmemO = 128 * TILES;
     static constexpr uint32_t kAtRing = TILES * kTile, kAtBars = kAtRing + kStages * kTile;
@@ -634,7 +635,7 @@ extern "C" gs_status gs_attention(const gs_attention_args* args, void* ws, size_
     p.idesc_o = instr_desc(a.type, true, false, (int)round_up(a.dim, 16), kRows);
     const auto run = [&](auto type) {
         constexpr int T = decltype(type)::value;
-        if (plan.dp == 64) return plan.tiles == 1 ? launch<T, 64, 1>(p, plan, st) : launch<T, 64, 2>(p, plan, st);
+        if (plan.dp == 64) return launch<T, 64, 1>(p, plan, st);
         return plan.tiles == 1 ? launch<T, 128, 1>(p, plan, st) : launch<T, 128, 2>(p, plan, st);
     };
     return a.type == GS_BF16 ? run(std::integral_constant<int, GS_BF16>()) : run(std::integral_constant<int, GS_F16>());

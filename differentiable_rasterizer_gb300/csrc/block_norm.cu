@@ -557,10 +557,10 @@ extern "C" gs_status gs_block_norm(const gs_block_norm_args* args, void* stream)
     const auto run = [&](auto t) -> gs_status {
         constexpr int T = decltype(t)::value;
 #define GS_FWD(N, W) return launch_after(block_norm_kernel<T, N, W>, dim3(grid), s.threads, 0, 1, st, a, s.group)
-        if (whole) {
-            if (s.nv == 1) GS_FWD(1, true);
-            else GS_FWD(2, true);
-        } else if (s.nv == 1) GS_FWD(1, false);
+        if constexpr (T == GS_F32)
+            if (whole && s.nv == 2) GS_FWD(2, true);
+        if (whole) GS_FWD(1, true);   // 16-bit: 1024 threads hold the widest of whole pieces
+        if (s.nv == 1) GS_FWD(1, false);
         else if (s.nv == 2) GS_FWD(2, false);
         else GS_FWD(4, false);
 #undef GS_FWD
