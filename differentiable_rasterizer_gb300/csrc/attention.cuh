@@ -346,7 +346,7 @@ inline bool sizes_ok(int64_t q_rows, int64_t k_rows, int64_t sequences, int head
     if (!q_starts != !k_starts || (!q_starts && sequences != 1)) return false;
     if (((uintptr_t)q_starts & 3u) || ((uintptr_t)k_starts & 3u)) return false;
     if (kv_heads < 1 || heads < kv_heads || heads % kv_heads || heads / kv_heads > GS_ATTENTION_MAX_GROUP || heads > 65536) return false;
-    return dim >= 1 && dim <= GS_ATTENTION_MAX_DIM && type_half(type) && scale > 0.0f && scale <= 3.4e38f;
+    return dim >= 1 && dim <= GS_ATTENTION_MAX_DIM && type_half(type) && scale > 0.0f && scale <= 0x1p127f;   // times log2(e) finite
 }
 
 // Whether a wait of the file's kernels ran out; clears the mark.  The device is idle.

@@ -683,7 +683,7 @@ GS_API gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* ws_by
  * head strides that keep heads apart (o, dq, dk, dv: and rows apart).  kv_heads
  * divides heads, at most GS_ATTENTION_MAX_GROUP query heads share one (head h
  * uses key head h / (heads / kv_heads)).  dim: 1..GS_ATTENTION_MAX_DIM.  lse:
- * [q_rows][heads] or NULL; the gradients need it.  scale: finite, positive.
+ * [q_rows][heads] or NULL; the gradients need it.  scale: positive, at most 2^127.
  * Sequences: q_starts, k_starts: [sequences + 1] device arrays, sequence s has the
  * rows q_starts[s] .. q_starts[s + 1] - 1 of q and those of k_starts of k and v;
  * both NULL: one sequence of all rows (sequences = 1).  k_lengths: NULL, or

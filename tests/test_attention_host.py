@@ -2,6 +2,8 @@
 import os
 import subprocess
 
+import pytest
+
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "differentiable_rasterizer_gb300", "csrc")
 
 SEQUENCE_OF = r"""
@@ -102,3 +104,21 @@ int main()
 def test_rows_of_a_tile_that_count_for_a_key(tmp_path):
     """Against the definition, up to the longest sequences and past 2^31 packed rows."""
     run_on_host(COLUMNS, tmp_path)
+
+
+@pytest.mark.parametrize("name", ["gs_attention", "gs_attention_bwd"])
+def test_scale_whose_product_is_infinite(name):
+    """The scores are taken times scale log2(e): finite for every scale that is taken."""
+    from differentiable_rasterizer_gb300 import abi, build
+    build.build()
+    tensors = dict(q=4096, q_row=256, q_head=64, k=4096, k_row=128, k_head=64, v=4096, v_row=128, v_head=64)
+    sizes = dict(q_rows=40, k_rows=50, sequences=1, q_starts=0, k_starts=0, heads=4, kv_heads=2, dim=64, type_=1, causal=0, fill=0)
+    more = dict(k_lengths=0, o=4096, o_row=256, o_head=64, lse=0) if name == "gs_attention" else dict(
+        d_o=4096, do_row=256, do_head=64, lse=4096, dq=4096, dq_row=256, dq_head=64, dk=4096, dk_row=128, dk_head=64, dv=4096, dv_row=128, dv_head=64)
+    for scale, good in ((2.0 ** 127, True), (2.0 ** 127 * 1.001, False), (3.4e38, False), (2.0 ** -149, True)):
+        args = getattr(abi, name[3:] + "_args")(**tensors, **sizes, **more, scale=scale)
+        if good:
+            assert abi.layer_ws_bytes(name, args) >= 0
+        else:
+            with pytest.raises(abi.GsError):
+                abi.layer_ws_bytes(name, args)
