@@ -570,6 +570,29 @@ void groups(const Heads& q, const Heads& k)
         refuse("k: " + std::to_string(k.heads) + " heads do not divide q's " + std::to_string(q.heads) + " into groups of at most " +
                std::to_string(GS_ATTENTION_MAX_GROUP));
 }
+// Whether two of them share elements, as far as their strides tell: both starting at one place, or
+// columns of one buffer's rows (heads one behind the other, or interleaved with others').
+bool share(const Heads& a, const Heads& b)
+{
+    if (!a.rows || !b.rows) return false;
+    if (a.p == b.p) return true;
+    const auto width = [](const Heads& h) { return (h.heads - 1) * (h.heads > 1 ? h.head : 0) + h.dim; };
+    const Heads &x = a.p < b.p ? a : b, &y = a.p < b.p ? b : a;
+    const int64_t off = ((const char*)y.p - (const char*)x.p) / 2;   // 16-bit elements
+    if (off >= (x.rows - 1) * (x.rows > 1 ? x.row : 0) + width(x)) return false;
+    if (x.rows > 1 && y.rows > 1 && x.row != y.row) return false;
+    const int64_t row = x.rows > 1 ? x.row : (y.rows > 1 ? y.row : 0), d = row ? off % row : off;
+    if (row && (width(x) > row || d + width(y) > row)) return false;
+    if (d >= width(x)) return false;
+    if (x.heads == 1 && y.heads == 1) return true;
+    if (x.heads > 1 && y.heads > 1 && x.head != y.head) return false;
+    const int64_t head = x.heads > 1 ? x.head : y.head;
+    return d % head < x.dim || d % head + y.dim > head;
+}
+void apart(const Heads& out, const char* name, const Heads& in, const char* other)
+{
+    if (share(out, in)) refuse(std::string(name) + ": shares memory with " + other);
+}
 const int32_t* indices(PyObject* o, const char* name, int dev, int64_t size)   // None: NULL
 {
     if (o == Py_None) return nullptr;
@@ -627,6 +650,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n)
         if (a[8] != Py_None) {
             o = tensor(a[8], "out");
             const Heads ho = heads_of(o, "out", 1u << hq.type, dev, hq.rows, hq.heads, hq.dim);
+            apart(ho, "out", hk, "k"), apart(ho, "out", hv, "v");
             g.o = ho.p, g.o_row = ho.row, g.o_head = ho.head;
         } else {
             o = at::empty({hq.rows, hq.heads, hq.dim}, q.options());
@@ -681,6 +705,14 @@ PyObject* attention_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
             if (given != (a[10 + i] != Py_None)) refuse("out: expected dq, dk and dv");
             t[i] = given ? tensor(a[10 + i], names[i]) : at::empty({like.rows, like.heads, like.dim}, q.options());
             h[i] = heads_of(t[i], names[i], type, dev, like.rows, like.heads, like.dim);
+        }
+        if (given) {
+            apart(h[0], "dq", hk, "k"), apart(h[0], "dq", hv, "v"), apart(h[0], "dq", h[1], "dk"), apart(h[0], "dq", h[2], "dv");
+            apart(h[1], "dk", h[2], "dv");
+            for (int i = 1; i < 3; ++i) {
+                const char* const name = i == 1 ? "dk" : "dv";
+                apart(h[i], name, hq, "q"), apart(h[i], name, hk, "k"), apart(h[i], name, hv, "v"), apart(h[i], name, hd, "do");
+            }
         }
         g.fill = !given;
         g.dq = h[0].p, g.dq_row = h[0].row, g.dq_head = h[0].head;

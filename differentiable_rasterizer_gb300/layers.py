@@ -225,7 +225,7 @@ def attention(q, k, v, *, q_starts=None, k_starts=None, k_lengths=None, causal=F
     of a sequence's keys are in use (a cache's slots), without gradients.  causal: the last
     query sees every key, the one before all but one, ...  A query that sees none gives 0.
     out: like q, rows of no sequence are left as they are; else o is allocated, those rows 0
-    (lse's are 0 in either case)."""
+    (lse's are 0 in either case).  It may be q, but shares no memory with k or v."""
     return AttentionOut(*_native.attention(q, k, v, q_starts, k_starts, k_lengths, causal, scale, out, need_backward))
 
 
@@ -234,7 +234,8 @@ def attention_backward(do, q, k, v, o, lse, *, q_starts=None, k_starts=None, cau
     """Gradients of attention from do, in q's type; o, lse: attention's with need_backward, the
     other arguments as they were given to it.  (o, already rounded, is checked but not computed
     with, and may be None: the rows' sums of do . o are taken from the terms again.)  out: (dq, dk, dv) to write to (column ranges of
-    the projection's gradient, say), rows of no sequence are left as they are; else 0."""
+    the projection's gradient, say), rows of no sequence are left as they are; else 0.  They share
+    no memory with one another or with the inputs, but that dq may be q or do."""
     dq, dk, dv = (None, None, None) if out is None else out
     return AttentionGrads(*_native.attention_backward(do, q, k, v, o, lse, q_starts, k_starts, causal, scale, dq, dk, dv))
 

@@ -474,7 +474,8 @@ GS_API gs_status gs_check_report(uint64_t* report, int32_t* checked);
  *     into *ws_bytes and does nothing else; where that size is 0, both may be
  *     NULL in the call.  Contents on entry are ignored.
  *   - y may be the same array as residual (same ld), sum the same as x or
- *     residual, dx the same as dsum; other outputs overlap nothing.
+ *     residual, dx the same as dsum, attention's o the same as q and dq the same
+ *     as q or d_o (same strides); other outputs overlap nothing.
  *   - Structs are read on the host during the call. */
 typedef enum gs_type { GS_F32 = 0, GS_BF16 = 1, GS_F16 = 2, GS_E4M3 = 3 } gs_type;
 typedef enum gs_act { GS_ACT_NONE = 0, GS_ACT_RELU = 1, GS_ACT_SILU = 2, GS_ACT_GELU = 3 } gs_act;
