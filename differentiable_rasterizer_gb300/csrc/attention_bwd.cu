@@ -11,7 +11,9 @@
 // would make its bits depend on the run.  delta is do . o, but o has been rounded: in bf16
 // that alone puts 4e-3 of dq's norm (where few keys carry the weight, 1e-2) beside the 2e-3 of
 // the factors' and results' roundings, for delta multiplies the keys' mean, and dq is what
-// remains of the keys beside it.  So nine products of a pair of tiles in place of five.
+// remains of the keys beside it.  So nine products of a pair of tiles in place of five.  (The
+// forward holds o in fp32 and could hand on what o's rounding leaves, in 16 bits more: an output
+// and an argument that the calls do not have.)
 //
 // The kernels keep p and ds out of shared memory: a tile's scores are computed with the
 // rows that stay (keys, or queries) as TMEM lanes, p and ds take their place in TMEM as 16
@@ -32,7 +34,7 @@
 // max|v|, to 2^15; the sums are scaled back at the end.  v's maximum is that of the sequence and
 // key head, do's that of the row for dq, whose rows are TMEM lanes, and of the sequence's
 // rows and the key head for dk, which sums over them: rows of no sequence and other
-// sequences change nothing.
+// sequences change nothing.  A launch behind delta's takes the maxima.
 #include <atomic>
 #include <cmath>
 

@@ -12,9 +12,11 @@
 //   1,000,000 x 256 bf16 334 us, 6.1 TB/s (302 at the copy's rate; without the next row's loads
 //   ahead 449, with weights fetched for each row 500), its gradients 520 us, 5.9 TB/s
 //   20,011 x 331 f16, a gate a value: 33 and 59 us, 250,000 x 197 172 and 300 (floors 72 and
-//   116), bound by the instructions that shift and write unaligned rows, half of the issue slots
-//   (single elements 20,011 x 331 138 and 364; the next row's pieces ahead in shared memory, or
-//   whole pieces written with the neighbour's columns, no faster)
+//   116).  Their instructions bound them: issue slots are 71 and 64 % busy with 7 and 6 warps a
+//   scheduler; of a warp's nine and eight cycles an instruction some two are the instructions' own
+//   latency, one and a half that another warp is chosen, one and a quarter loads, less than one the
+//   row's barriers (single elements 20,011 x 331 138 and 364 us; the next row's pieces ahead in
+//   shared memory, or whole pieces written with the neighbour's columns, no faster)
 //   8,000 x 5928 bf16 132 and 203 us (floors 56 and 84): one row an SM at a time, whose two
 //   reductions nothing covers
 #include <type_traits>

@@ -88,6 +88,9 @@ struct Squares {
 };
 // The sum over a thread's pieces: in fp32 with what each addition loses beside it (Knuth's
 // two-sum).  In fp64, of which an SM adds two a cycle, it took as long as the loads.
+// A piece's 32 squares of a thread pass twelve roundings at most (eight in a vector's sum, four
+// vectors), and a vector goes wholly by its largest value: 12 2^-24 of the sum, half of it in the
+// root; the two-sum's rest and the fp64 sums add next to nothing: the norm is within 2^-21.
 struct Total {
     float high = 0.0f, low = 0.0f;
     double rest = 0.0;

@@ -463,7 +463,7 @@ GS_API gs_status gs_check_report(uint64_t* report, int32_t* checked);
  *     refused: INVALID_ARG.
  *   - Sums, norms and products are accumulated in fp32; each output is rounded
  *     to its type once, to nearest even.  Results do not depend on the run:
- *     there are no atomics on values, split sums are joined in a fixed order.
+ *     there are no atomics whose order matters, split sums are joined in a fixed order.
  *     fp32 outputs are as good as these: the tensor cores truncate as they add
  *     (a product of K terms is within K 2^-23 of the sum of their magnitudes),
  *     SILU's factor is within 2^-21 + |v| 2^-23 of itself, GELU's within
@@ -695,6 +695,9 @@ GS_API gs_status gs_glu_bwd(const gs_glu_bwd_args* args, void* ws, size_t* ws_by
  * Rows of other sequences have no influence, whatever they hold.  A NaN or an infinity
  * among a sequence's own values (v) reaches queries that it is hidden from, if they are
  * less than 256 tokens before the first that sees it.  Rows: below 2^31 - 1024.
+ * Every block of a call, and of its gradients', looks its sequence up from the first start on, so
+ * that many short sequences cost with the square of their number: 1,000,000 rows in 15,625
+ * sequences, 4 heads of 16, take 55 ms, in 3,907 6.4 ms; 100,000 in 391 0.12 ms.
  * Scores, maxima, sums and outputs are fp32 until o's rounding; exp(t - m), m a
  * running maximum, is rounded to `type` as a factor of its product with v (F16: held times
  * a power of two, so that what its smallest step loses of all keys together is below 2^-13
