@@ -30,7 +30,7 @@ namespace {
 using namespace rows;
 
 // A matrix's rows as a thread reads them, eight columns at a time.  Rows of 16-byte base and
-// pitch: whole pieces, of which a row's last may lie in its padding.  Others of 16-bit
+// pitch: whole pieces, of which a row's last may lie in its padding (see piece_rows).  Others of 16-bit
 // elements: the four or five 32-bit words that the eight columns lie in, shifted by an element
 // where the row starts within a word (two pieces of 16 bytes shifted together took 15
 // instructions more a matrix: 250,000 x 197 268 and 410 us against 230 and 367); single
@@ -41,7 +41,7 @@ struct Source {
     int type;
     bool aligned;
     __device__ __forceinline__ Source(const void* p_, int64_t ld_, int type_)
-        : p(p_), ld(ld_), type(type_), aligned(((uintptr_t)p_ & 15u) == 0 && ld_ * (type_ == GS_F32 ? 4 : 2) % 16 == 0) {}
+        : p(p_), ld(ld_), type(type_), aligned(piece_rows(p_, ld_, type_)) {}
     // Words that hold columns of this row lie in the matrix.
     __device__ __forceinline__ bool inside(int64_t row, int64_t rows) const { return row > 0 && row + 1 < rows; }
     // Whether a row of 16-bit elements, and with it every eighth column, starts within a word.

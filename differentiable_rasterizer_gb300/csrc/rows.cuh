@@ -16,6 +16,15 @@ __device__ __forceinline__ float max_nan(float a, float b)   // NaN if either is
     return r;
 }
 
+// Rows that are read in pieces of eight columns from every eighth on, but for the last row's end:
+// of 16-byte base and pitch.  A piece may end in the row's padding, and of fp32 rows whose pitch is
+// not a multiple of eight in the next row's first four columns.  At a pitch of four a row of fewer
+// columns has not so many: its pieces would reach behind the matrix.
+__host__ __device__ __forceinline__ bool piece_rows(const void* p, int64_t ld, int type)
+{
+    return ((uintptr_t)p & 15u) == 0 && ld >= 8 && ld * type_bytes(type) % 16 == 0;
+}
+
 struct Sum {
     __device__ static float join(float a, float b) { return a + b; }
 };
