@@ -74,11 +74,12 @@ struct Params {
 
 // ------------------------------------------------------------------ F16's largest values
 // Infinities and NaN are left out: what they reach is not finite whatever the power, and the
-// rest keeps its digits.
+// rest keeps its digits.  So are, for dk, rows of do that see no key.
 struct MostParams {
     const uint16_t *d_o, *v;
     int64_t do_row, do_head, v_row, v_head;
     Sequences seqs;
+    const float* lse;        // of do's rows
     float* row_most;         // of do's rows, laid out as stats
     uint32_t* most;          // [2][sequences][key heads] bits of |do| and |v|, cleared by delta's launch
     int64_t stat_pitch, q_each, k_each;   // rows of a block, multiples of kMostRows
@@ -145,9 +146,12 @@ __global__ void __launch_bounds__(256) most_kernel(const __grid_constant__ MostP
                 const uint32_t other = __shfl_xor_sync(0xffffffffu, m, o);
                 m = other > m ? other : m;
             }
+            if (is_do && row < end) {
+                if (sub == 0) p.row_most[head * p.stat_pitch + row * heads + h] = __half2float(__ushort_as_half((unsigned short)m));
+                // of a row that sees no key every ds is 0
+                if (p.lse[row * (int64_t)(p.kv_heads * heads) + head * heads + h] == -INFINITY) m = 0;
+            }
             mine = m > mine ? m : mine;
-            if (is_do && sub == 0 && row < end)
-                p.row_most[head * p.stat_pitch + row * heads + h] = __half2float(__ushort_as_half((unsigned short)m));
         }
         if (row >= end) continue;
         if (row < first || row >= last) {
@@ -1072,7 +1076,7 @@ gs_status largest_values(const gs_attention_bwd_args& a, const Params& p, cudaSt
     MostParams t = {};
     t.d_o = (const uint16_t*)a.d_o, t.do_row = a.do_row, t.do_head = a.do_head;
     t.v = (const uint16_t*)a.v, t.v_row = a.v_row, t.v_head = a.v_head;
-    t.seqs = p.seqs, t.row_most = p.stats + 2 * p.stat_plane, t.most = (uint32_t*)p.most, t.stat_pitch = p.stat_pitch;
+    t.seqs = p.seqs, t.lse = p.lse, t.row_most = p.stats + 2 * p.stat_plane, t.most = (uint32_t*)p.most, t.stat_pitch = p.stat_pitch;
     t.kv_heads = p.kv_heads, t.group = p.group, t.dim = p.dim;
     t.do_vec = a.dim % 8 == 0 && tensor_tma(a.d_o, a.do_row, a.do_head, a.q_rows, a.heads);
     t.v_vec = a.dim % 8 == 0 && tensor_tma(a.v, a.v_row, a.v_head, a.k_rows, a.kv_heads);

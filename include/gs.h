@@ -731,8 +731,8 @@ GS_API gs_status gs_attention(const gs_attention_args* args, void* ws, size_t* w
  * dk and dv sum over the query heads that share a key head.  p and ds are rounded to
  * `type` as factors of these products (F16: times powers of two that keep them among
  * its normal numbers, ds by the largest finite magnitudes of the sequence's v and, for dq,
- * of the row's d_o, for dk of the sequence's, each within the key head; what lies 2^-40
- * below 2 dim max|d_o| max|v| is lost).  q, k, v, lse: the forward's.  d_o, dq: like q; dk, dv: like k.  dq may be NULL, and so may dk and dv together (not computed).
+ * of the row's d_o, for dk of the sequence's rows that see a key, each within the key head;
+ * what lies 2^-40 below 2 dim max|d_o| max|v| is lost).  q, k, v, lse: the forward's.  d_o, dq: like q; dk, dv: like k.  dq may be NULL, and so may dk and dv together (not computed).
  * Rows that belong to no sequence: as gs_attention, in dq, dk and dv.  A NaN or an
  * infinity in d_o or q reaches keys that are hidden from its query within 256 tokens.
  * Errors: as gs_attention. */

@@ -117,3 +117,22 @@ def test_a_captured_step(layers):
         torch.cuda.synchronize()
         for x, y in zip(out, want):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("big", [6e4, float("inf"), float("nan")])
+def test_rows_that_see_no_key(layers, big):
+    """More queries than keys under the causal mask: the first ones' do changes nothing, whatever it holds."""
+    q_lens, k_lens = [300, 50, 1], [130, 50, 40]
+    q, k, v, do = (rnd((sum(n), h, 64), i, HF, std) for i, (n, h, std) in enumerate([(q_lens, 6, 1), (k_lens, 2, 1), (k_lens, 2, 1), (q_lens, 6, 1e-5)]))
+    qs, ks = starts(q_lens), starts(k_lens)
+    do[:170] = 0
+    a, g = gradients(layers, q, k, v, do, qs, ks, causal=True)
+    assert (a.lse[:170] == -float("inf")).all() and g.dk[:130].abs().sum() > 0
+    check_backward(g, do, a, q, k, v, q_lens, k_lens, True, 0.125)
+    do[:44] = big      # whole tiles of queries: a NaN or an infinity reaches keys within 256 tokens of what sees them
+    if big == 6e4:
+        do[44:170] = big
+    _, h = gradients(layers, q, k, v, do, qs, ks, causal=True)
+    assert (h.dq[:170] == 0).all()
+    for x, y, name in zip(g, h, ("dq", "dk", "dv")):
+        assert torch.equal(x, y), name
